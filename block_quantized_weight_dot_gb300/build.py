@@ -2,7 +2,7 @@
 
 Each translation unit is compiled in parallel, then linked into one shared
 library next to this file.  No cmake, no torch extension machinery: the
-library is a plain C ABI (``include/lean_qmatmul.h``).
+library is a plain C ABI (``include/lean_qmatmul.h``, ``include/lean_step.h``).
 """
 from __future__ import annotations
 
@@ -32,9 +32,12 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
               "-Xcompiler", "-fno-gnu-unique", "--expt-relaxed-constexpr"] + ARCH
 SOURCES = ["lean_qmatmul.cu", "pack.cpp", "qmm_q4_0.cu", "qmm_q8_0.cu", "qmm_i8_b64.cu", "qmm_q6_k.cu",
            "qmm_fixed_ws.cu"]
+# the operators of a serving step around the product (include/lean_step.h)
+STEP = os.path.join(HERE, "step")
+STEP_SOURCES = ["norm.cu", "rope.cu", "kv_pages.cu", "attend.cu", "logprobs.cu"]
 # host-only helpers (no CUDA), compiled by the host C++ compiler
 HOST = os.path.join(HERE, "host")
-HOST_SOURCES = ["quant.cpp"]
+HOST_SOURCES = ["quant.cpp", "rope_table.cpp"]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-ffp-contract=off", "-pthread", "-fno-gnu-unique"]
 
 
@@ -47,6 +50,7 @@ def nvcc() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    files += [os.path.join(STEP, f) for f in os.listdir(STEP)]
     files += [os.path.join(HOST, f) for f in os.listdir(HOST)]
     inc = os.path.join(ROOT, "include")
     files += [os.path.join(inc, f) for f in os.listdir(inc)]
@@ -60,9 +64,9 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
-def _compile(src: str, extra, build_dir: str = BUILD) -> str:
+def _compile(src: str, extra, build_dir: str = BUILD, folder: str = CSRC) -> str:
     obj = os.path.join(build_dir, os.path.basename(src) + ".o")
-    cmd = [nvcc()] + NVCC_FLAGS + list(extra) + ["-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [nvcc()] + NVCC_FLAGS + list(extra) + ["-c", os.path.join(folder, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc failed for %s:\n%s\n%s" % (src, " ".join(cmd), r.stderr))
@@ -88,8 +92,9 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
     if not force and up_to_date(lib):
         return lib
     os.makedirs(build_dir, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + len(HOST_SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + len(STEP_SOURCES) + len(HOST_SOURCES)) as ex:
         dev = [ex.submit(_compile, s, extra, build_dir) for s in SOURCES]
+        dev += [ex.submit(_compile, s, extra, build_dir, STEP) for s in STEP_SOURCES]
         host = [ex.submit(_compile_host, s, build_dir) for s in HOST_SOURCES]
         objs = [f.result() for f in dev + host]
     tmp = lib + ".tmp.%d" % os.getpid()

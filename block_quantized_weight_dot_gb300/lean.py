@@ -1,5 +1,5 @@
-"""ctypes binding of ``liblean_qmatmul.so`` (C ABI in ``include/lean_qmatmul.h`` and
-``include/lean_quant.h``).
+"""ctypes binding of ``liblean_qmatmul.so`` (C ABI in ``include/lean_qmatmul.h``,
+``include/lean_quant.h`` and ``include/lean_step.h``).
 
 Argument marshalling only: every computation of the product runs in the CUDA
 library.  Functions keep the C names.  Buffers may be given as torch tensors
@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -28,7 +29,11 @@ LEAN_FLAG_X_PLANES = 2
 LEAN_FLAG_STREAM = 4
 LEAN_FLAG_X_INT8 = 8
 
-# every symbol the header declares, with (restype, argtypes)
+LEAN_F32, LEAN_BF16, LEAN_F16 = 0, 1, 2
+(LEAN_ROPE_PLAIN, LEAN_ROPE_LINEAR, LEAN_ROPE_BASE, LEAN_ROPE_RAMP, LEAN_ROPE_BANDS) = range(5)
+LEAN_MAX_TOP = 64
+
+# every symbol the headers declare, with (restype, argtypes)
 _i64, _int, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
 SIGNATURES = {
     "lean_block_elems": (_int, [_int]),
@@ -56,6 +61,15 @@ SIGNATURES = {
     "lean_qmatmul_fixed_ws": (_int, [_int, _vp, _vp, _vp, _i64, _i64, ctypes.c_uint, _vp]),
     "lean_fixed_workspace_bytes": (_i64, []),
     "lean_status_str": (ctypes.c_char_p, [_int]),
+    "lean_residual_norm": (_int, [_vp, _vp]),
+    "lean_rope_turns": (_int, [_vp, _i64, _vp]),
+    "lean_rope_frequencies": (_int, [_int, _i64] + [ctypes.c_double] * 5 + [_vp]),
+    "lean_rope_append": (_int, [_vp, _vp]),
+    "lean_kv_pages": (_int, [_vp, _vp]),
+    "lean_paged_attention": (_int, [_vp, _vp]),
+    "lean_paged_attention_workspace_bytes": (_i64, [_i64] * 4),
+    "lean_token_logprobs": (_int, [_vp, _vp]),
+    "lean_token_logprobs_workspace_bytes": (_i64, [_i64] * 3),
 }
 LEAN_MAX_BATCH = 256
 
@@ -299,6 +313,213 @@ def lean_wait_selftest(limit_us: int, stream=None) -> None:
     """Launch the bounded-wait self-test: a block waits on a barrier nothing
     completes, gives up after limit_us and sets bit 8 of the error word."""
     _check("lean_wait_selftest", _lib.lean_wait_selftest(limit_us, _stream(stream)))
+
+
+# ---- the operators of a serving step (include/lean_step.h) ----
+#
+# These take torch tensors on the GPU and read sizes, strides and element types
+# off them (a caller without torch fills the C structs); every output is the
+# caller's.  A tensor of a wrong shape, type or device is a ValueError, what the
+# library refuses a LeanError.
+
+_NORM = struct.Struct("<4qQqQqQqQQQqQq2dq")
+_ROPE = struct.Struct("<8q" + "Q2q" * 5 + "3Q2Q5qdq")
+_PAGES = struct.Struct("<3q3Q2qQqQ2Q5Qq")
+_ATTENTION = struct.Struct("<6qQ2q2Q5qQ2qQQ2qQdqQqq")
+_LOGPROBS = struct.Struct("<3qQqQdq5QQqq")
+_dtypes = {}
+
+
+def _dtype(t):
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.float32: LEAN_F32, torch.bfloat16: LEAN_BF16, torch.float16: LEAN_F16})
+    try:
+        return _dtypes[t.dtype]
+    except KeyError:
+        raise ValueError("element type %s: float32, bfloat16 or float16 is wanted" % t.dtype) from None
+
+
+def _array(t, shape, like, name):
+    """(address, stride of each dimension but the last) of a GPU tensor of that
+    shape and of the element type of `like` (a tensor), its last dimension
+    contiguous; zeros for None."""
+    if t is None:
+        return (0,) * len(shape)
+    if t.shape != shape or t.dtype != like.dtype or not t.is_cuda:
+        raise ValueError("%s is %s %s on %s: %s %s on the GPU is wanted"
+                         % (name, t.dtype, tuple(t.shape), t.device, like.dtype, tuple(shape)))
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError("%s: the last dimension is not contiguous" % name)
+    return (t.data_ptr(),) + st[:-1]
+
+
+def _plain(t, size, kind, name):
+    """Address of a contiguous GPU tensor of `size` elements of dtype `kind` (its
+    name: "int32" and so on); 0 for None."""
+    if t is None:
+        return 0
+    if t.numel() != size or str(t.dtype) != kind or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s is %s %s on %s: %d contiguous elements of %s on the GPU are wanted"
+                         % (name, t.dtype, tuple(t.shape), t.device, size, kind))
+    return t.data_ptr()
+
+
+def lean_residual_norm(x, h, w, h_out, y, eps: float = 1e-6, post_w=None, gate=None,
+                       res_scale: float = 1.0, flags: int = 0, stream=None) -> None:
+    """h_out = h + res_scale * gate * norm(x) and y = w * norm(h_out), rows of
+    [rows, width]: x a block's output (None: none), h the residual (None: none),
+    post_w the weights of the norm after the block (None: x as it is), gate
+    [rows, width] or [width] (None: 1), w of the norm before the next one.
+    h_out or y may be None."""
+    one = x if x is not None else h
+    if one is None or one.dim() != 2:
+        raise ValueError("x or h: [rows, width] is wanted")
+    act = x if x is not None else y if y is not None else h
+    res = h if h is not None else h_out if h_out is not None else act
+    shape = one.shape
+    rows, width = shape
+    if gate is None:
+        g = (0, 0)
+    elif gate.dim() == 1 or gate.shape[0] == 1:
+        g = _array(gate.reshape(1, -1), (1, width), act, "gate")[0], 0
+    else:
+        g = _array(gate, shape, act, "gate")
+    args = _NORM.pack(rows, width, _dtype(act), _dtype(res), *_array(x, shape, act, "x"), *_array(h, shape, res, "h"), *g,
+                      _plain(post_w, width, "torch.float32", "post_w"), _plain(w, width, "torch.float32", "w"),
+                      *_array(h_out, shape, res, "h_out"), *_array(y, shape, act, "y"), eps, res_scale, flags)
+    st = _lib.lean_residual_norm(args, _stream(stream))
+    if st:
+        raise LeanError("lean_residual_norm", st)
+
+
+def lean_rope_frequencies(kind: int, rot_dim: int, base: float, factor: float = 1.0, trained_len: float = 0.0,
+                          slow: float = 1.0, fast: float = 32.0) -> np.ndarray:
+    """Radians per position of each rotated pair (LEAN_ROPE_*), float64."""
+    freq = np.zeros(max(1, rot_dim // 2))
+    _check("lean_rope_frequencies", _lib.lean_rope_frequencies(kind, rot_dim, base, factor, trained_len, slow, fast,
+                                                               freq.ctypes.data))
+    return freq
+
+
+def lean_rope_turns(freq) -> np.ndarray:
+    """The whole-number form of frequencies that lean_rope_append takes: 2^-64
+    turns per position, as int64 (the bits of uint64)."""
+    freq = np.ascontiguousarray(freq, dtype=np.float64)
+    turns = np.zeros(freq.shape, dtype=np.int64)
+    _check("lean_rope_turns", _lib.lean_rope_turns(freq.ctypes.data, freq.size, turns.ctypes.data))
+    return turns
+
+
+def lean_rope_append(q, k, v, positions, slots, turns, q_out, k_cache, v_cache, rot_dim: int,
+                     interleaved: bool = False, rot_scale: float = 1.0, k_out=None, flags: int = 0,
+                     stream=None) -> None:
+    """Rotate the first rot_dim elements of each head of q and k ([tokens, heads,
+    dim]) to `positions`, into q_out (and k_out), and store k and v at `slots` of
+    the caches ([pages, page_size, kv_heads, dim], strides of their own)."""
+    one = q if q is not None else k
+    if one is None or one.dim() != 3:
+        raise ValueError("q or k: [tokens, heads, dim] is wanted")
+    n, _, dim = one.shape
+    hq = q.shape[1] if q is not None else 0
+    hkv = k.shape[1] if k is not None else 0
+    qs, ks = (n, hq, dim), (n, hkv, dim)
+    if k_cache is not None:
+        pages, page = k_cache.shape[:2]
+        kc = _array(k_cache, (pages, page, hkv, dim), k_cache, "k_cache")
+        if _array(v_cache, (pages, page, hkv, dim), k_cache, "v_cache")[1:] != kc[1:]:
+            raise ValueError("k_cache and v_cache have different strides")
+        cache, cdt, vc = (pages, page) + kc[1:], _dtype(k_cache), v_cache.data_ptr()
+    else:
+        cache, cdt, kc, vc = (0,) * 5, 0, (0,), 0
+    args = _ROPE.pack(n, hq, hkv, dim, rot_dim, 1 if interleaved else 0, _dtype(one), cdt, *_array(q, qs, one, "q"),
+                      *_array(k, ks, one, "k"), *_array(v, ks, one, "v"), *_array(q_out, qs, one, "q_out"),
+                      *_array(k_out, ks, one, "k_out"), _plain(positions, n, "torch.int32", "positions"),
+                      _plain(slots, n, "torch.int32", "slots"), _plain(turns, rot_dim // 2, "torch.int64", "turns"),
+                      kc[0], vc, *cache, rot_scale, flags)
+    st = _lib.lean_rope_append(args, _stream(stream))
+    if st:
+        raise LeanError("lean_rope_append", st)
+
+
+def lean_kv_pages(lens, targets, block_table, free_ring, ring_state, page_size: int, lens_out, ring_state_out,
+                  status, token_starts, slots=None, positions=None, token_seqs=None, flags: int = 0,
+                  stream=None) -> None:
+    """Sequences go from `lens` to `targets` tokens: pages are taken from and
+    given back to the free ring, block_table [seqs, width] follows, and the new
+    tokens' slots, positions and sequences are written as one packed batch
+    (int32 throughout)."""
+    n = lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError("block_table: [%d, width] is wanted" % n)
+    some = slots if slots is not None else positions if positions is not None else token_seqs
+    most = some.numel() if some is not None else 0
+    i32 = "torch.int32"
+    table, stride = _array(block_table, block_table.shape, lens, "block_table")
+    args = _PAGES.pack(n, page_size, most, _plain(lens, n, i32, "lens"), _plain(targets, n, i32, "targets"), table,
+                       block_table.shape[1], stride, _plain(free_ring, free_ring.numel(), i32, "free_ring"),
+                       free_ring.numel(), _plain(ring_state, 2, i32, "ring_state"), _plain(lens_out, n, i32, "lens_out"),
+                       _plain(ring_state_out, 2, i32, "ring_state_out"), _plain(status, n, i32, "status"),
+                       _plain(token_starts, n + 1, i32, "token_starts"), _plain(slots, most, i32, "slots"),
+                       _plain(positions, most, i32, "positions"), _plain(token_seqs, most, i32, "token_seqs"), flags)
+    st = _lib.lean_kv_pages(args, _stream(stream))
+    if st:
+        raise LeanError("lean_kv_pages", st)
+
+
+def lean_paged_attention_workspace_bytes(n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return _lib.lean_paged_attention_workspace_bytes(n_seqs, n_q_heads, n_kv_heads, head_dim)
+
+
+def lean_paged_attention(q, k_cache, v_cache, block_table, seq_lens, out, scale: float, window: int = 0, lse=None,
+                         workspace=None, flags: int = 0, stream=None) -> None:
+    """Attention of one new token per sequence: q and out [seqs, heads, dim], the
+    caches as for lean_rope_append, block_table [seqs, width], lse [seqs, heads]
+    (None: not wanted); workspace: a once-zeroed uint8 tensor of
+    lean_paged_attention_workspace_bytes."""
+    shape = q.shape
+    n, hq, dim = shape
+    pages, page, hkv = k_cache.shape[:3]
+    kc = _array(k_cache, (pages, page, hkv, dim), k_cache, "k_cache")
+    vc = _array(v_cache, (pages, page, hkv, dim), k_cache, "v_cache")
+    if vc[1:] != kc[1:]:
+        raise ValueError("k_cache and v_cache have different strides")
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError("block_table: [%d, width] is wanted" % n)
+    table = _array(block_table, block_table.shape, seq_lens, "block_table")
+    args = _ATTENTION.pack(n, hq, hkv, dim, _dtype(q), _dtype(k_cache), *_array(q, shape, q, "q"), kc[0], vc[0], pages,
+                           page, *kc[1:], table[0], block_table.shape[1], table[1],
+                           _plain(seq_lens, n, "torch.int32", "seq_lens"), *_array(out, shape, q, "out"),
+                           _plain(lse, n * hq, "torch.float32", "lse"), scale, window, _addr(workspace) or 0,
+                           0 if workspace is None else workspace.numel(), flags)
+    st = _lib.lean_paged_attention(args, _stream(stream))
+    if st:
+        raise LeanError("lean_paged_attention", st)
+
+
+def lean_token_logprobs_workspace_bytes(rows: int, vocab: int, top_k: int) -> int:
+    return _lib.lean_token_logprobs_workspace_bytes(rows, vocab, top_k)
+
+
+def lean_token_logprobs(logits, ids, logprobs, ranks=None, entropy=None, top_ids=None, top_logprobs=None,
+                        scale: float = 1.0, workspace=None, flags: int = 0, stream=None) -> None:
+    """Log probabilities of ids [rows] under softmax(scale * logits [rows, vocab]),
+    how many logits are larger, the entropy, and the top_ids.shape[1] most likely
+    ids with theirs.  Outputs that are None are left out; workspace: a once-zeroed
+    uint8 tensor of lean_token_logprobs_workspace_bytes."""
+    rows, vocab = logits.shape
+    k = 0 if top_ids is None else top_ids.numel() // rows
+    x = _array(logits, (rows, vocab), logits, "logits")
+    f32 = "torch.float32"
+    args = _LOGPROBS.pack(rows, vocab, _dtype(logits), *x, _plain(ids, rows, "torch.int32", "ids"), scale, k,
+                          _plain(logprobs, rows, f32, "logprobs"), _plain(ranks, rows, "torch.int32", "ranks"),
+                          _plain(entropy, rows, f32, "entropy"), _plain(top_ids, rows * k, "torch.int32", "top_ids"),
+                          _plain(top_logprobs, rows * k, f32, "top_logprobs"), _addr(workspace) or 0,
+                          0 if workspace is None else workspace.numel(), flags)
+    st = _lib.lean_token_logprobs(args, _stream(stream))
+    if st:
+        raise LeanError("lean_token_logprobs", st)
 
 
 # ---- torch conveniences (device memory via PyTorch; compute via the library) ----
