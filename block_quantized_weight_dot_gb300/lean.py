@@ -128,12 +128,23 @@ def _addr(buf):
     raise TypeError("unsupported buffer type %r" % type(buf))
 
 
+_raw_stream = None  # torch's current stream without the Stream object around it (0.2 us instead of 3.8)
+
+
 def _stream(stream):
+    global _raw_stream
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream()
         try:
             import torch
             if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
+                st = torch.cuda.current_stream().cuda_stream
+                c = torch._C
+                if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+                    get, dev = c._cuda_getCurrentRawStream, c._cuda_getDevice
+                    _raw_stream = lambda: get(dev())  # noqa: E731
+                return st
         except ImportError:
             pass
         return None
@@ -356,8 +367,8 @@ def _array(t, shape, like, name):
 
 
 def _plain(t, size, kind, name):
-    """Address of a contiguous GPU tensor of `size` elements of dtype `kind` (its
-    name: "int32" and so on); 0 for None."""
+    """Address of a contiguous GPU tensor of `size` elements of a dtype given by its
+    name ("torch.int32" and so on); 0 for None."""
     if t is None:
         return 0
     if t.numel() != size or str(t.dtype) != kind or not t.is_cuda or not t.is_contiguous():

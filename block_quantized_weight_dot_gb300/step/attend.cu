@@ -12,13 +12,12 @@
 //     query heads).  Every warp of the GPU takes an equal run of units, whatever
 //     the lengths are, and walks it alone: no barrier between its first load
 //     and its last.
-//   - A lane copies with cp.async exactly the 16-byte pieces that it will itself
-//     read, in the order in which the matrix instruction wants them: K as 8
-//     elements of one token (the contraction over the head dimension may take
-//     the elements in any order, as long as q has the same), V as 8 elements of
-//     four tokens (whose pairs are then interleaved in registers).  Shared memory
-//     is a queue of registers: no swizzle, no conflicts, and cp.async.wait_group
-//     is the only synchronisation.
+//   - A warp copies its units into a queue of its own with cp.async, consecutive
+//     lanes along a token's row (a copy in the order of the matrix fragments, 64
+//     bytes of eight rows at a time, needs no exchange between lanes but stops at
+//     5.2 TB/s; rows reach 6.6-7.0).  16-byte pieces are stored at their place XOR
+//     the row's number, where ldmatrix reads them without conflicts: K as it is,
+//     V transposed.
 //   - Scores and outputs come from mma.sync m16n8k16 with the query heads as
 //     rows: 16 tokens take dim / 4 of them for 64 * dim bytes, a fraction of the
 //     time the bytes take (tcgen05 wants 64 rows or more; a group has 1 to 16).
@@ -52,7 +51,7 @@ struct AttArgs {
     unsigned *counters;
     float *warp_parts, *cta_parts;
     int64_t qs, qhs, os, ohs, page_stride, place_stride, cache_hs, table_stride, n_pages;
-    int n_seqs, hq, hkv, group, tiles, dim, page, width, window;
+    int n_seqs, hq, hkv, group, tiles, dim, page, paged, width, window;
     int act;
     float scale_log2;
     int64_t cache_extent, q_extent, out_extent;  // elements, for the checked build
@@ -67,23 +66,31 @@ struct AttShape {
     static constexpr int kStages = DP == 64 ? 5 : DP == 128 ? 3 : 2;
     static constexpr int kStageBytes = kUnit * DP * 4;  // K and V
     // at 256 the warps' q as well (up to 12 registers per 16 elements)
-    static constexpr int kSmem = kWarps * (kStages * kStageBytes + (DP == 256 ? DP / 16 * 12 * 128 : 0));
+    static constexpr int kSmem = 512 + kWarps * (kStages * kStageBytes + (DP == 256 ? DP / 16 * 12 * 128 : 0));
 };
 // A part: maxima, sums and outputs of a group of H heads.
 __host__ __device__ constexpr int part_floats(int heads, int dp) { return heads * (dp + 8); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+// 16 bytes of which `real` (16 or 0) are copied and the rest zero
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-    return v;
+__device__ __forceinline__ void ldmatrix4(uint32_t (&v)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&v)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at)
+                 : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -128,26 +135,22 @@ __device__ __forceinline__ uint32_t take_part<__half>(float &a, float &b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <typename A>
-__device__ __forceinline__ void load8_as(const void *p, int64_t i, float *f) {
-    const Vec<A, 8> v = load_vec<A, 8>(static_cast<const A *>(p) + i);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = to_f(v.v[j]);
+// Two neighbouring elements of q; two or four of out.
+template <bool F32>
+__device__ __forceinline__ float2 load_pair(const void *p, int64_t i, int act) {
+    if (F32) return *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + i);
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i);
+    if (act == LEAN_BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
-__device__ __forceinline__ void load8(const void *p, int64_t i, int act, float *f) {
-    if (act == LEAN_F32) load8_as<float>(p, i, f);
-    else if (act == LEAN_BF16) load8_as<__nv_bfloat16>(p, i, f);
-    else load8_as<__half>(p, i, f);
+template <int N>
+__device__ __forceinline__ void store_out(void *p, int64_t i, int act, const float *f) {
+    if (act == LEAN_F32) store_vec<float, N>(static_cast<float *>(p) + i, f);
+    else if (act == LEAN_BF16) store_vec<__nv_bfloat16, N>(static_cast<__nv_bfloat16 *>(p) + i, f);
+    else store_vec<__half, N>(static_cast<__half *>(p) + i, f);
 }
-__device__ __forceinline__ void store8(void *p, int64_t i, int act, const float *f) {
-    if (act == LEAN_F32) store_vec<float, 8>(static_cast<float *>(p) + i, f);
-    else if (act == LEAN_BF16) store_vec<__nv_bfloat16, 8>(static_cast<__nv_bfloat16 *>(p) + i, f);
-    else store_vec<__half, 8>(static_cast<__half *>(p) + i, f);
-}
-__device__ __forceinline__ void store4(void *p, int64_t i, int act, const float *f) {
-    if (act == LEAN_F32) store_vec<float, 4>(static_cast<float *>(p) + i, f);
-    else if (act == LEAN_BF16) store_vec<__nv_bfloat16, 4>(static_cast<__nv_bfloat16 *>(p) + i, f);
-    else store_vec<__half, 4>(static_cast<__half *>(p) + i, f);
+__device__ __forceinline__ float natural_lse(float m, float sum) {
+    return sum == 0.f ? -CUDART_INF_F : (m + log2f(sum)) * 0.69314718056f;
 }
 
 // What of a sequence is attended: tokens start..len-1, in n units from base on.
@@ -167,44 +170,74 @@ __device__ __forceinline__ Span open_span(const AttArgs &p, int s) {
     return x;
 }
 
-// A place in the list of units.
+// A place in the list of units: sequence, kv head, tile of its query heads, unit.
+// Where units lie within pages (p.paged: pages of a multiple of 16 tokens), also
+// the page's number in the sequence and the unit's first place in it.
 struct Place {
-    int s, g, c;  // sequence, kv head and group of its heads (h * tiles + tile), unit of it
+    int s, kvh, tile, c;
+    int page_at, in_page;
     Span x;
 };
+__device__ __forceinline__ void to_page(const AttArgs &p, Place &at) {
+    const int tok = at.x.base + at.c * kUnit;
+    at.page_at = tok / p.page;
+    at.in_page = tok - at.page_at * p.page;
+}
 __device__ __forceinline__ void advance(const AttArgs &p, Place &at) {
-    if (++at.c < at.x.n) return;
+    if (++at.c < at.x.n) {
+        if ((at.in_page += kUnit) == p.page) {
+            at.in_page = 0;
+            ++at.page_at;
+        }
+        return;
+    }
     at.c = 0;
-    if (++at.g < p.hkv * p.tiles) return;
-    at.g = 0;
-    if (++at.s < p.n_seqs) at.x = open_span(p, at.s);
+    if (++at.tile == p.tiles) {
+        at.tile = 0;
+        if (++at.kvh == p.hkv) {
+            at.kvh = 0;
+            if (++at.s < p.n_seqs) at.x = open_span(p, at.s);
+        }
+    }
+    to_page(p, at);
 }
 
-// A joined record of the warps of a block, and where its group lies.
+// What a warp leaves of a group that it does not finish, or a block of one that
+// it does not: where the group lies and its maxima, sums and outputs.
 struct Record {
     int item;           // -1: none
     int n;              // units of the item
-    int64_t first;      // its first unit
-    const float *part;  // maxima, sums, outputs
+    int64_t first;      // its first unit, counted from the block's first one
+    const float *part;
 };
+
+// The most that running scores may exceed the reference of their exponentials by
+// before it moves, as a power of two: p stays below 2^8, and the accumulators are
+// rescaled a few times a run instead of in every unit with a new maximum.
+constexpr float kSlack = 8.f;
+// Units of a warp's time that joining blocks costs.
+constexpr int kJoinUnits = 8;
 
 // WIDE: 9 to 16 query heads in a group, one per row; else up to 8, two rows each.
 template <typename C, int DP, int PARTS, bool WIDE>
 __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(const AttArgs p) {
-    constexpr int W = AttShape<DP>::kWarps, S = AttShape<DP>::kStages, T = W * 32;
+    constexpr int W = AttShape<DP>::kWarps, S = AttShape<DP>::kStages, T = W * 32, STAGE = AttShape<DP>::kStageBytes;
     constexpr int H = WIDE ? 16 : 8, NH = WIDE ? 2 : 1;  // heads of a group, of a thread
-    constexpr int KX = DP / 32, VX = DP / 64;
-    constexpr int AREGS = WIDE ? 4 * PARTS : 4 + (PARTS > 2 ? 2 : 0);  // of q per 16 elements
+    constexpr int RB = DP * 2, LPR = RB / 16, RPI = 32 / LPR;  // a row's bytes and lanes, rows of a copy instruction
+    constexpr int KS = DP / 16;                                // steps of the contraction, and pairs of output tiles
+    constexpr int AREGS = WIDE ? 4 * PARTS : 4 + (PARTS > 2 ? 2 : 0);  // of q per step
     constexpr bool QSMEM = DP == 256;                                  // no registers left for q
     constexpr int PF = part_floats(H, DP), PO = 8 + DP;                // a head's row of a part: m, l, -, out
-    extern __shared__ __align__(16) uint8_t queue[];
+    extern __shared__ uint8_t queue_raw[];
+    uint8_t *queue = queue_raw + (512 - smem_addr(queue_raw) % 512) % 512;
     __shared__ int64_t scan[W];
+    __shared__ int longest[W];
     __shared__ struct {
         int s, g, c;
     } start_at[W];
     __shared__ Record rec[2 * W];
-    __shared__ float total_m[H], total_l[H];
-    __shared__ int last_block;
+    __shared__ float total_l[H];
+    __shared__ int last_block[2];
 
     step_begin();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -215,14 +248,23 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     const int per = (p.n_seqs + T - 1) / T;  // sequences a thread sums up
     const int s_lo = min(p.n_seqs, (int)threadIdx.x * per), s_hi = min(p.n_seqs, s_lo + per);
     int64_t mine = 0;
-    for (int s = s_lo; s < s_hi; ++s) mine += (int64_t)open_span(p, s).n * groups;
+    int most = 0;
+    for (int s = s_lo; s < s_hi; ++s) {
+        const int n = open_span(p, s).n;
+        mine += (int64_t)n * groups;
+        most = max(most, n);
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
         const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += u;
     }
-    if (lane == 31) scan[warp] = incl;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 31) {
+        scan[warp] = incl;
+        longest[warp] = most;
+    }
     if (threadIdx.x < 2 * W) rec[threadIdx.x].item = -1;
     __syncthreads();
     int64_t before = incl - mine, units = 0;
@@ -230,85 +272,120 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     for (int i = 0; i < W; ++i) {
         if (i < warp) before += scan[i];
         units += scan[i];
+        most = max(most, longest[i]);
     }
-    // blocks that get work: a unit a warp at least
-    const int blocks = (int)min((int64_t)gridDim.x, (units + W - 1) / W);
+    // Equal runs for all blocks (a unit a warp at least) have to be joined across blocks; where there are few
+    // items and none is long, a block for each is done sooner.
+    const int64_t items = (int64_t)p.n_seqs * groups;
+    const bool by_item = items <= gridDim.x && (most + W - 1) / W <= units / ((int64_t)gridDim.x * W) + kJoinUnits;
+    const int blocks = by_item ? (int)items : (int)min((int64_t)gridDim.x, (units + W - 1) / W);
     if ((int)blockIdx.x >= blocks) return;
-    auto bound = [&](int64_t w) { return units * w / ((int64_t)blocks * W); };  // first unit of warp w of the grid
-    const int64_t wg = (int64_t)blockIdx.x * W + warp;
-    const int64_t u_lo = bound(wg), u_hi = bound(wg + 1);
-    for (int i = 0; i < W; ++i) {
-        const int64_t b = bound((int64_t)blockIdx.x * W + i);
-        if (b < before || b >= before + mine) continue;
-        int64_t at = before;
-        for (int s = s_lo; s < s_hi; ++s) {
-            const int n = open_span(p, s).n;
-            if (b < at + (int64_t)n * groups) {
-                const int in = (int)(b - at);
-                start_at[i].s = s;
-                start_at[i].g = in / n;
-                start_at[i].c = in % n;
-                break;
+    int64_t b_lo = 0, b_n;  // first unit of the block, and how many (unit numbers below count from b_lo)
+    if (by_item) {
+        const int s = blockIdx.x / groups;
+        b_n = open_span(p, s).n;
+        if (threadIdx.x < W) {
+            start_at[threadIdx.x].s = s;
+            start_at[threadIdx.x].g = blockIdx.x % groups;
+            start_at[threadIdx.x].c = (int)(b_n * threadIdx.x / W);
+        }
+    } else {
+        b_lo = units * blockIdx.x / blocks;
+        b_n = units * (blockIdx.x + 1) / blocks - b_lo;
+        for (int i = 0; i < W; ++i) {
+            const int64_t b = b_lo + b_n * i / W;
+            if (b < before || b >= before + mine) continue;
+            int64_t at = before;
+            for (int s = s_lo; s < s_hi; ++s) {
+                const int n = open_span(p, s).n;
+                if (b < at + (int64_t)n * groups) {
+                    const int in = (int)(b - at);
+                    start_at[i].s = s;
+                    start_at[i].g = in / n;
+                    start_at[i].c = in % n;
+                    break;
+                }
+                at += (int64_t)n * groups;
             }
-            at += (int64_t)n * groups;
         }
     }
     __syncthreads();
+    const int64_t u_lo = b_n * warp / W, u_hi = b_n * (warp + 1) / W;
 
-    const uint32_t my_queue = smem_addr(queue) + warp * (S * AttShape<DP>::kStageBytes);
     if (u_lo < u_hi) {
+        const uint32_t my_queue = smem_addr(queue) + warp * (S * STAGE);
         Place next;  // to be loaded
         next.s = start_at[warp].s;
-        next.g = start_at[warp].g;
+        next.kvh = start_at[warp].g / p.tiles;
+        next.tile = start_at[warp].g - next.kvh * p.tiles;
         next.c = start_at[warp].c;
         next.x = open_span(p, next.s);
+        to_page(p, next);
         Place cur = next;  // to be computed
         int64_t u_next = u_lo;
 
-        // the page of token lane % 16 of the unit to be loaded next, fetched one unit ahead
+        // the page of token lane % 16 of the unit to be loaded next (paged: of the unit), fetched one unit ahead
         auto fetch_page = [&]() {
-            const int tok = next.x.base + next.c * kUnit + lane % kUnit;
-            const bool in = tok >= next.x.start && tok < next.x.len;
-            const int64_t e = (int64_t)next.s * p.table_stride + tok / p.page;
+            int at;
+            bool in;
+            if (p.paged) {
+                at = next.page_at;
+                in = next.x.len > 0;
+            } else {
+                const int tok = next.x.base + next.c * kUnit + lane % kUnit;
+                at = tok / p.page;
+                in = tok >= next.x.start && tok < next.x.len;
+            }
+            const int64_t e = (int64_t)next.s * p.table_stride + at;
             return in && LEAN_IN(e, (int64_t)(p.n_seqs - 1) * p.table_stride + p.width, p.err) ? p.table[e] : 0;
         };
         int page_id = fetch_page();
+        // a lane's piece of a row: its place in the caches, in a stage, and whether the head has it at all
+        const int lr = lane / LPR, col = lane % LPR;
+        const C *k_lane = static_cast<const C *>(p.k) + 8 * col, *v_lane = static_cast<const C *>(p.v) + 8 * col;
+        const uint32_t to_lane = my_queue + lr * RB + ((col ^ lr) * 16);
+        const int real = 8 * col < p.dim ? 16 : 0;
 
         auto load_unit = [&](int stage) {
             if (u_next < u_hi) {
-                const int tok = next.x.base + next.c * kUnit + lane % kUnit;
-                int64_t off = -1;  // of the token's row; -1: not attended, -2: outside the cache
-                if (tok >= next.x.start && tok < next.x.len) {
-                    off = (int64_t)page_id * p.page_stride + (int64_t)(tok % p.page) * p.place_stride +
-                          (int64_t)(next.g / p.tiles) * p.cache_hs;
-                    if (page_id < 0 || page_id >= p.n_pages) off = -2;
-                    else if (!LEAN_SPAN(off, p.dim, p.cache_extent, p.err)) off = -1;
-                }
-                if (__any_sync(0xffffffffu, off == -2) && lane == 0) atomicOr(p.err, kErrSlot);
-                const uint32_t ks = my_queue + stage * AttShape<DP>::kStageBytes + lane * 16;
-                const C *kb = static_cast<const C *>(p.k), *vb = static_cast<const C *>(p.v);
+                const uint32_t dst = to_lane + stage * STAGE;
+                const int t0 = next.x.base + next.c * kUnit;
+                const bool page_ok = page_id >= 0 && page_id < p.n_pages;
+                const int64_t unit_off = p.paged ? (int64_t)page_id * p.page_stride +
+                                                       (int64_t)next.in_page * p.place_stride +
+                                                       (int64_t)next.kvh * p.cache_hs
+                                                 : 0;
+                if (p.paged && page_ok && t0 >= next.x.start && t0 + kUnit <= next.x.len &&
+                    LEAN_SPAN(unit_off, (kUnit - 1) * p.place_stride + p.dim, p.cache_extent, p.err)) {
+                    // all of 16 tokens, one after the other
+                    int64_t off = unit_off + lr * p.place_stride;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int64_t o = __shfl_sync(0xffffffffu, off, 8 * j + r);
-#pragma unroll
-                    for (int x = 0; x < KX; ++x) {
-                        const int d = 32 * x + 8 * c4;
-                        const uint32_t dst = ks + (x * 2 + j) * 512;
-                        const bool real = o >= 0 && d < p.dim;
-                        if (o != -2)
-                            cp_async16(dst, real ? kb + o + d : kb, real);
-                        else  // keys that are not there: NaN, which reaches out and lse by itself
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0x7fff7fff) : "memory");
+                    for (int i = 0; i < kUnit / RPI; ++i) {
+                        const uint32_t to = i * RPI * RB + (dst ^ ((i * RPI & 7) * 16));
+                        cp_async16(to, k_lane + off, real);
+                        cp_async16(to + kUnit * RB, v_lane + off, real);
+                        off += RPI * p.place_stride;
                     }
-                }
+                } else {
+                    const int tok = t0 + lane % kUnit;
+                    int64_t off = -1;  // of the token's row; -1: not attended, -2: outside the cache
+                    if (tok >= next.x.start && tok < next.x.len) {
+                        off = p.paged ? unit_off + (int64_t)(lane % kUnit) * p.place_stride
+                                      : (int64_t)page_id * p.page_stride + (int64_t)(tok % p.page) * p.place_stride +
+                                            (int64_t)next.kvh * p.cache_hs;
+                        if (!page_ok) off = -2;
+                        else if (!LEAN_SPAN(off, p.dim, p.cache_extent, p.err)) off = -1;
+                    }
+                    if (__any_sync(0xffffffffu, off == -2) && lane == 0) atomicOr(p.err, kErrSlot);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t o = __shfl_sync(0xffffffffu, off, 2 * c4 + (i & 1) + 8 * (i >> 1));
-#pragma unroll
-                    for (int x = 0; x < VX; ++x) {
-                        const int d = 64 * x + 8 * r;
-                        const bool real = o >= 0 && d < p.dim;
-                        cp_async16(ks + kUnit * DP * 2 + (x * 4 + i) * 512, real ? vb + o + d : vb, real);
+                    for (int i = 0; i < kUnit / RPI; ++i) {
+                        const int64_t o = __shfl_sync(0xffffffffu, off, i * RPI + lr);
+                        const uint32_t to = i * RPI * RB + (dst ^ ((i * RPI & 7) * 16));
+                        if (o != -2)
+                            cp_async16(to, o >= 0 ? k_lane + o : static_cast<const C *>(p.k), o >= 0 ? real : 0);
+                        else  // keys that are not there: NaN, which reaches out and lse by itself
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to), "r"(0x7fff7fff) : "memory");
+                        cp_async16(to + kUnit * RB, o >= 0 ? v_lane + o : static_cast<const C *>(p.v), o >= 0 ? real : 0);
                     }
                 }
                 if (++u_next < u_hi) {
@@ -321,122 +398,114 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
 #pragma unroll
         for (int i = 0; i < S - 1; ++i) load_unit(i);
 
+        // ldmatrix rows of a lane: K, tokens 0-7 (8-15 from lane 16 on) and the even (odd) piece of a step; V,
+        // tokens 0-7 (8-15) and the even (odd) output tile of a pair
+        const uint32_t k_row = my_queue + ((lane >> 4) * 8 + (lane & 7)) * RB + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
+        const uint32_t v_row =
+            my_queue + kUnit * RB + (((lane >> 3) & 1) * 8 + (lane & 7)) * RB + (((lane >> 4) ^ (lane & 7)) * 16);
         // q as rows of the matrix instruction, part by part
-        uint32_t qa[QSMEM ? 1 : 2 * KX][AREGS];
-        uint32_t *q_shared = reinterpret_cast<uint32_t *>(queue + W * S * AttShape<DP>::kStageBytes) + warp * (2 * KX * AREGS * 32);
-        float acc[8 * VX][4], m[NH], l[NH], zs[NH];
+        uint32_t qa[QSMEM ? 1 : KS][AREGS];
+        uint32_t *q_shared = reinterpret_cast<uint32_t *>(queue + W * S * STAGE) + warp * (KS * AREGS * 32);
+        float acc[2 * KS][4], m[NH], l[NH], zs[NH];
         bool fresh = true;
         int stage = 0;
         for (int64_t u = u_lo; u < u_hi; ++u) {
             load_unit(stage == 0 ? S - 1 : stage - 1);
-            const int kvh = cur.g / p.tiles, tile = cur.g - kvh * p.tiles;
-            const int h0 = kvh * p.group + tile * H, nh = min(H, p.group - tile * H);
+            const int h0 = cur.kvh * p.group + cur.tile * H, nh = min(H, p.group - cur.tile * H);
             if (fresh) {
                 fresh = false;
-                // (read twice, the second time from L1: fewer registers than keeping it)
-                auto load_q = [&](int h, int x, float *f) {
-                    const int d = 32 * x + 8 * c4;
-                    const int64_t at = (int64_t)cur.s * p.qs + (int64_t)(h0 + r + 8 * h) * p.qhs + d;
-                    if (r + 8 * h < nh && d < p.dim && LEAN_SPAN(at, 8, p.q_extent, p.err)) {
-                        load8(p.q, at, p.act, f);
-                    } else {
+                float2 f[NH][2 * KS];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = 0.f;
+                for (int h = 0; h < NH; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2 * KS; ++i) {
+                        const int d = 8 * i + 2 * c4;
+                        const int64_t at = (int64_t)cur.s * p.qs + (int64_t)(h0 + r + 8 * h) * p.qhs + d;
+                        f[h][i] = r + 8 * h < nh && d < p.dim && LEAN_SPAN(at, 2, p.q_extent, p.err)
+                                      ? load_pair<(PARTS > 2)>(p.q, at, p.act)
+                                      : make_float2(0.f, 0.f);
                     }
-                };
-                float f[NH][8], up[NH];
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     float top = 0.f;
 #pragma unroll
-                    for (int x = 0; x < KX; ++x) {
-                        load_q(h, x, f[h]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[h][i]));
-                    }
+                    for (int i = 0; i < 2 * KS; ++i) top = fmaxf(top, fmaxf(fabsf(f[h][i].x), fabsf(f[h][i].y)));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     // a power of two that brings the largest element near 1 (1 where there is none)
                     const int e = (int)(__float_as_uint(top) >> 23);
                     const int fe = e == 0 || e == 255 ? 127 : max(1, 254 - e);
-                    up[h] = __uint_as_float((uint32_t)fe << 23);
+                    const float up = __uint_as_float((uint32_t)fe << 23);
                     zs[h] = p.scale_log2 * __uint_as_float((uint32_t)(254 - fe) << 23);
                     m[h] = -CUDART_INF_F;
                     l[h] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 2 * KS; ++i) {
+                        f[h][i].x *= up;
+                        f[h][i].y *= up;
+                    }
                 }
-                // element pairs (0,1) and (2,3) are the two halves of k of one instruction, (4,5) and (6,7) of the next
+                // pieces 2 st and 2 st + 1 are the two halves of k of step st
 #pragma unroll
-                for (int x = 0; x < KX; ++x) {
+                for (int st = 0; st < KS; ++st) {
+                    uint32_t a[AREGS];
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        load_q(h, x, f[h]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[h][i] *= up[h];
+                    for (int part = 0; part < PARTS; ++part) {
+                        const uint32_t lo = take_part<C>(f[0][2 * st].x, f[0][2 * st].y);
+                        const uint32_t hi = take_part<C>(f[0][2 * st + 1].x, f[0][2 * st + 1].y);
+                        if (WIDE) {
+                            a[4 * part] = lo;
+                            a[4 * part + 2] = hi;
+                            a[4 * part + 1] = take_part<C>(f[NH - 1][2 * st].x, f[NH - 1][2 * st].y);
+                            a[4 * part + 3] = take_part<C>(f[NH - 1][2 * st + 1].x, f[NH - 1][2 * st + 1].y);
+                        } else if (part < 2) {
+                            a[part] = lo;
+                            a[2 + part] = hi;
+                        } else {
+                            a[4] = lo;
+                            a[AREGS - 1] = hi;
+                        }
                     }
 #pragma unroll
-                    for (int st = 0; st < 2; ++st) {
-                        uint32_t a[AREGS];
-#pragma unroll
-                        for (int part = 0; part < PARTS; ++part) {
-                            const uint32_t lo = take_part<C>(f[0][4 * st], f[0][4 * st + 1]);
-                            const uint32_t hi = take_part<C>(f[0][4 * st + 2], f[0][4 * st + 3]);
-                            if (WIDE) {
-                                a[4 * part] = lo;
-                                a[4 * part + 2] = hi;
-                                a[4 * part + 1] = take_part<C>(f[NH - 1][4 * st], f[NH - 1][4 * st + 1]);
-                                a[4 * part + 3] = take_part<C>(f[NH - 1][4 * st + 2], f[NH - 1][4 * st + 3]);
-                            } else if (part < 2) {
-                                a[part] = lo;
-                                a[2 + part] = hi;
-                            } else {
-                                a[4] = lo;
-                                a[AREGS - 1] = hi;
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < AREGS; ++i) {
-                            if (QSMEM) q_shared[((2 * x + st) * AREGS + i) * 32 + lane] = a[i];
-                            else qa[QSMEM ? 0 : 2 * x + st][i] = a[i];
-                        }
+                    for (int i = 0; i < AREGS; ++i) {
+                        if (QSMEM) q_shared[(st * AREGS + i) * 32 + lane] = a[i];
+                        else qa[QSMEM ? 0 : st][i] = a[i];
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 8 * VX; ++j)
+                for (int j = 0; j < 2 * KS; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
             }
             cp_async_wait<S - 1>();
+            __syncwarp();
 
             // ---- scores of 16 tokens: two tiles of 8
-            const uint32_t ks = my_queue + stage * AttShape<DP>::kStageBytes + lane * 16;
             float sc[2][4] = {};
 #pragma unroll
-            for (int x = 0; x < KX; ++x)
+            for (int st = 0; st < KS; ++st) {
+                uint32_t b[4], a[AREGS];
+                ldmatrix4(b, (k_row + stage * STAGE) ^ (32 * st));
+#pragma unroll
+                for (int i = 0; i < AREGS; ++i)
+                    a[i] = QSMEM ? q_shared[(st * AREGS + i) * 32 + lane] : qa[QSMEM ? 0 : st][i];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint4 w = lds128(ks + (x * 2 + j) * 512);
+                    if (WIDE) {
 #pragma unroll
-                    for (int st = 0; st < 2; ++st) {
-                        uint32_t a[AREGS];
-#pragma unroll
-                        for (int i = 0; i < AREGS; ++i)
-                            a[i] = QSMEM ? q_shared[((2 * x + st) * AREGS + i) * 32 + lane] : qa[QSMEM ? 0 : 2 * x + st][i];
-                        const uint32_t b0 = st ? w.z : w.x, b1 = st ? w.w : w.y;
-                        if (WIDE) {
-#pragma unroll
-                            for (int part = 0; part < PARTS; ++part)
-                                mma<C>(sc[j], a[4 * part], a[4 * part + 1], a[4 * part + 2], a[4 * part + 3], b0, b1);
-                        } else {
-                            mma<C>(sc[j], a[0], a[1], a[2], a[3], b0, b1);
-                            if (PARTS > 2) mma<C>(sc[j], a[4], 0u, a[AREGS - 1], 0u, b0, b1);
-                        }
+                        for (int part = 0; part < PARTS; ++part)
+                            mma<C>(sc[j], a[4 * part], a[4 * part + 1], a[4 * part + 2], a[4 * part + 3], b[2 * j],
+                                   b[2 * j + 1]);
+                    } else {
+                        mma<C>(sc[j], a[0], a[1], a[2], a[3], b[2 * j], b[2 * j + 1]);
+                        if (PARTS > 2) mma<C>(sc[j], a[AREGS - 2], 0u, a[AREGS - 1], 0u, b[2 * j], b[2 * j + 1]);
                     }
                 }
+            }
             // ---- running maximum and sum; p as rows of the next instruction
             const int t0 = cur.x.base + cur.c * kUnit + 2 * c4;
-            float e[NH][4];
+            float e[NH][4], fall[NH];
             bool moved = false;
-            float fall[NH];
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 float top = -CUDART_INF_F;
@@ -449,8 +518,10 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float mn = fmaxf(m[h], top), ms = mn == -CUDART_INF_F ? 0.f : mn;
-                moved |= mn > m[h];
+                // m: the reference of the exponentials, within kSlack of the largest score so far
+                const float mn = top > m[h] + kSlack || m[h] == -CUDART_INF_F ? top : m[h];
+                const float ms = mn == -CUDART_INF_F ? 0.f : mn;
+                moved |= mn != m[h];
                 fall[h] = ex2(m[h] - ms);
                 m[h] = mn;
                 float sum = 0.f;
@@ -463,7 +534,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
             }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int j = 0; j < 8 * VX; ++j)
+                for (int j = 0; j < 2 * KS; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] *= fall[WIDE ? i >> 1 : 0];
             }
@@ -475,26 +546,21 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     pa[part][h] = take_part<C>(e[h][0], e[h][1]);
                     pa[part][2 + h] = take_part<C>(e[h][2], e[h][3]);
                 }
-            // ---- values: tokens (2c, 2c+1) and (2c+8, 2c+9) are the two halves of k
+            // ---- values, two output tiles of 8 at a time
 #pragma unroll
-            for (int x = 0; x < VX; ++x) {
-                uint4 v[4];
+            for (int st = 0; st < KS; ++st) {
+                uint32_t b[4];
+                ldmatrix4_trans(b, (v_row + stage * STAGE) ^ (32 * st));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = lds128(ks + kUnit * DP * 2 + (x * 4 + i) * 512);
-#pragma unroll
-                for (int jj = 0; jj < 8; ++jj) {
-                    auto word = [&](const uint4 &q4) { return jj < 2 ? q4.x : jj < 4 ? q4.y : jj < 6 ? q4.z : q4.w; };
-                    const uint32_t sel = jj & 1 ? 0x7632 : 0x5410;
-                    const uint32_t b0 = __byte_perm(word(v[0]), word(v[1]), sel);
-                    const uint32_t b1 = __byte_perm(word(v[2]), word(v[3]), sel);
-                    float(&d)[4] = acc[8 * x + jj];
+                for (int j = 0; j < 2; ++j) {
+                    float(&d)[4] = acc[2 * st + j];
                     if (WIDE) {
 #pragma unroll
                         for (int part = 0; part < PARTS; ++part)
-                            mma<C>(d, pa[part][0], pa[part][1], pa[part][2], pa[part][3], b0, b1);
+                            mma<C>(d, pa[part][0], pa[part][1], pa[part][2], pa[part][3], b[2 * j], b[2 * j + 1]);
                     } else {
-                        mma<C>(d, pa[0][0], pa[1][0], pa[0][2], pa[1][2], b0, b1);
-                        if (PARTS > 2) mma<C>(d, pa[PARTS - 1][0], 0u, pa[PARTS - 1][2], 0u, b0, b1);
+                        mma<C>(d, pa[0][0], pa[1][0], pa[0][2], pa[1][2], b[2 * j], b[2 * j + 1]);
+                        if (PARTS > 2) mma<C>(d, pa[PARTS - 1][0], 0u, pa[PARTS - 1][2], 0u, b[2 * j], b[2 * j + 1]);
                     }
                 }
             }
@@ -503,59 +569,38 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
             if (cur.c == cur.x.n - 1 || u == u_hi - 1) {
                 fresh = true;
                 const int64_t first = u - cur.c;
-                const bool whole = first >= u_lo && cur.c == cur.x.n - 1;
-                const bool at_end = u == u_hi - 1;
-                const int slot = at_end ? 1 : 0;
+                const bool whole = first >= u_lo && cur.c == cur.x.n - 1, at_end = u == u_hi - 1;
                 // a part that others continue: the run's last in this warp's own queue (nothing is under way to
                 // it any more), an earlier one in the workspace
-                float *part = at_end ? reinterpret_cast<float *>(queue + warp * (S * AttShape<DP>::kStageBytes))
-                                     : p.warp_parts + wg * PF;
+                float *part = at_end ? reinterpret_cast<float *>(queue + warp * (S * STAGE))
+                                     : p.warp_parts + ((int64_t)blockIdx.x * W + warp) * PF;
+                __syncwarp();
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     float sum = l[h];
                     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                     const int row = r + 8 * h;
-                    if (whole) {
-                        if (row < nh) {
-                            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                            if (p.lse && c4 == 0)
-                                p.lse[(int64_t)cur.s * p.hq + h0 + row] =
-                                    sum == 0.f ? -CUDART_INF_F : (m[h] + log2f(sum)) * 0.69314718056f;
+                    if (whole && row >= nh) continue;
+                    const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                    const int64_t at = (int64_t)cur.s * p.os + (int64_t)(h0 + row) * p.ohs + 2 * c4;
+                    if (c4 == 0) {
+                        if (!whole) *reinterpret_cast<float2 *>(part + row * PO) = make_float2(m[h], sum);
+                        else if (p.lse) p.lse[(int64_t)cur.s * p.hq + h0 + row] = natural_lse(m[h], sum);
+                    }
 #pragma unroll
-                            for (int x = 0; x < VX; ++x)
+                    for (int j = 0; j < 2 * KS; ++j) {
+                        float o[2];
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const int d = 64 * x + 16 * c4 + 8 * i;
-                                    float o[8];
-#pragma unroll
-                                    for (int jj = 0; jj < 8; ++jj)
-                                        o[jj] = (WIDE ? acc[8 * x + jj][2 * h + i]
-                                                      : acc[8 * x + jj][i] + acc[8 * x + jj][2 + i]) * inv;
-                                    const int64_t at = (int64_t)cur.s * p.os + (int64_t)(h0 + row) * p.ohs + d;
-                                    if (d < p.dim && LEAN_SPAN(at, 8, p.out_extent, p.err)) store8(p.out, at, p.act, o);
-                                }
-                        }
-                    } else {
-                        if (c4 == 0) {
-                            part[row * PO] = m[h];
-                            part[row * PO + 1] = sum;
-                        }
-#pragma unroll
-                        for (int x = 0; x < VX; ++x)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                float o[8];
-#pragma unroll
-                                for (int jj = 0; jj < 8; ++jj)
-                                    o[jj] = WIDE ? acc[8 * x + jj][2 * h + i] : acc[8 * x + jj][i] + acc[8 * x + jj][2 + i];
-                                store_vec<float, 8>(part + row * PO + 8 + 64 * x + 16 * c4 + 8 * i, o);
-                            }
+                        for (int i = 0; i < 2; ++i) o[i] = (WIDE ? acc[j][2 * h + i] : acc[j][i] + acc[j][2 + i]) * inv;
+                        if (!whole) *reinterpret_cast<float2 *>(part + row * PO + 8 + 8 * j + 2 * c4) = make_float2(o[0], o[1]);
+                        else if (8 * j < p.dim && LEAN_SPAN(at + 8 * j, 2, p.out_extent, p.err))
+                            store_out<2>(p.out, at + 8 * j, p.act, o);
                     }
                 }
                 if (!whole && lane == 0) {
-                    Record &q = rec[2 * warp + slot];
-                    q.item = cur.s * groups + cur.g;
+                    Record &q = rec[2 * warp + at_end];
+                    q.item = cur.s * groups + cur.kvh * p.tiles + cur.tile;
                     q.n = cur.x.n;
                     q.first = first;
                     q.part = part;
@@ -564,133 +609,140 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
             advance(p, cur);
             stage = stage + 1 == S ? 0 : stage + 1;
         }
-        cp_async_wait<0>();
     }
+    cp_async_wait<0>();
     __syncthreads();
 
-    // ---- groups shared by warps of this block, and with other blocks
-    // (the parts' weights lie behind the first warp's part, in its own queue)
-    static_assert((PF + kAttMaxCtas * H) * 4 <= S * AttShape<DP>::kStageBytes, "room for the weights");
-    float(*weight)[H] = reinterpret_cast<float(*)[H]>(queue + PF * 4);
-    const int64_t b_lo = bound((int64_t)blockIdx.x * W), b_hi = bound((int64_t)blockIdx.x * W + W);
-    auto finish = [&](int item) {  // total_m and total_l are set; out = weighted sum of `parts` / total
-        const int s = item / groups, g = item % groups, kvh = g / p.tiles, tile = g % p.tiles;
-        const int nh = min(H, p.group - tile * H);
-        return make_int4(s, kvh * p.group + tile * H, nh, 0);
+    // ---- groups shared by the warps of this block: each 32 x 4 outputs of one are added up by a warp
+    struct Head {  // of an item: its sequence, first query head and number of heads
+        int s, h0, nh;
     };
+    auto open_item = [&](int item) {
+        const int g = item % groups, tile = g % p.tiles;
+        return Head{item / groups, g / p.tiles * p.group + tile * H, min(H, p.group - tile * H)};
+    };
+    auto cta_part = [&](int64_t b, int slot) { return p.cta_parts + (b * 2 + slot) * PF; };
+    auto store_result = [&](const Head &f, int h, int d, float4 o, float top, float sum) {
+        if (h >= f.nh || d >= p.dim) return;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+        const int64_t at = (int64_t)f.s * p.os + (int64_t)(f.h0 + h) * p.ohs + d;
+        if (LEAN_SPAN(at, 4, p.out_extent, p.err)) store_out<4>(p.out, at, p.act, v);
+        if (d == 0 && p.lse) p.lse[(int64_t)f.s * p.hq + f.h0 + h] = natural_lse(top, sum);
+    };
+    int n_split = 0, job = 0;  // groups that other blocks share: the block's first, its last, or both
+    int split_item[2], split_n[2];
+    int64_t split_first[2];
     for (int i = 0; i < 2 * W;) {
-        if (rec[i].item < 0) {
+        const Record head = rec[i];
+        if (head.item < 0) {
             ++i;
             continue;
         }
-        const Record head = rec[i];
-        int end = i + 1, parts = 1;  // the group's records: the item's next ones
-        while (end < 2 * W && (rec[end].item < 0 || rec[end].item == head.item)) {
-            parts += rec[end].item >= 0;
-            ++end;
-        }
-        for (int h = threadIdx.x; h < H; h += T) {
+        int end = i + 1;  // the group's records: all up to the next item's
+        while (end < 2 * W && (rec[end].item < 0 || rec[end].item == head.item)) ++end;
+        const bool whole = head.first >= 0 && head.first + head.n <= b_n;
+        const int slot = head.first < 0 ? 0 : 1;
+        const Head f = open_item(head.item);
+        for (int j = 0; j < H * DP / 128; ++j, ++job) {
+            if (job % W != warp) continue;
+            const int h = (j * 32 + lane) * 4 / DP, d = (j * 32 + lane) * 4 % DP;
             float top = -CUDART_INF_F, sum = 0.f;
             for (int k = i; k < end; ++k)
                 if (rec[k].item >= 0) top = fmaxf(top, rec[k].part[h * PO]);
             const float ref = top == -CUDART_INF_F ? 0.f : top;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int k = i; k < end; ++k) {
                 if (rec[k].item < 0) continue;
-                const float w = ex2(rec[k].part[h * PO] - ref);
-                weight[k][h] = w;
-                sum = fmaf(w, rec[k].part[h * PO + 1], sum);
-            }
-            total_m[h] = top;
-            total_l[h] = sum;
-        }
-        __syncthreads();
-        const bool whole = head.first >= b_lo && head.first + head.n <= b_hi;
-        const int slot = head.first < b_lo ? 0 : 1;
-        float *part = p.cta_parts + ((int64_t)blockIdx.x * 2 + slot) * PF;
-        const int4 f = finish(head.item);
-        for (int k = threadIdx.x; k < H * DP / 4; k += T) {
-            const int h = k / (DP / 4), d = k % (DP / 4) * 4;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int q = i; q < end; ++q) {
-                if (rec[q].item < 0) continue;
-                const float w = weight[q][h];
-                const float4 v = *reinterpret_cast<const float4 *>(rec[q].part + h * PO + 8 + d);
+                const float *row = rec[k].part + h * PO;
+                const float w = ex2(row[0] - ref);
+                const float4 v = *reinterpret_cast<const float4 *>(row + 8 + d);
+                sum = fmaf(w, row[1], sum);
                 o.x = fmaf(w, v.x, o.x);
                 o.y = fmaf(w, v.y, o.y);
                 o.z = fmaf(w, v.z, o.z);
                 o.w = fmaf(w, v.w, o.w);
             }
-            if (!whole) {
-                *reinterpret_cast<float4 *>(part + h * PO + 8 + d) = o;
-            } else if (h < f.z && d < p.dim) {
-                const float sum = total_l[h], inv = sum == 0.f ? 0.f : 1.f / sum;
-                const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-                const int64_t at = (int64_t)f.x * p.os + (int64_t)(f.y + h) * p.ohs + d;
-                if (LEAN_SPAN(at, 4, p.out_extent, p.err)) store4(p.out, at, p.act, v);
-            }
-        }
-        for (int h = threadIdx.x; h < H; h += T) {
-            if (!whole) {
-                part[h * PO] = total_m[h];
-                part[h * PO + 1] = total_l[h];
-            } else if (h < f.z && p.lse) {
-                p.lse[(int64_t)f.x * p.hq + f.y + h] =
-                    total_l[h] == 0.f ? -CUDART_INF_F : (total_m[h] + log2f(total_l[h])) * 0.69314718056f;
+            if (whole) {
+                store_result(f, h, d, o, top, sum);
+            } else {
+                float *row = cta_part(blockIdx.x, slot) + h * PO;
+                *reinterpret_cast<float4 *>(row + 8 + d) = o;
+                if (d == 0) *reinterpret_cast<float2 *>(row) = make_float2(top, sum);
             }
         }
         if (!whole) {
-            // the blocks of the item: first_b .. last_b; the last of them to arrive adds the parts up
-            auto block_of = [&](int64_t u) { return (int)(((u + 1) * blocks - 1) / units); };
-            const int first_b = block_of(head.first), last_b = block_of(head.first + head.n - 1), np = last_b - first_b + 1;
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                const bool last = atomicAdd(p.counters + first_b, 1u) == (unsigned)(np - 1);
-                if (last) p.counters[first_b] = 0;
-                last_block = last;
+            split_item[n_split & 1] = head.item;
+            split_n[n_split & 1] = head.n;
+            split_first[n_split & 1] = head.first + b_lo;
+            ++n_split;
+        }
+        i = end;
+    }
+    if (n_split == 0) return;
+
+    // ---- groups shared with other blocks: the last of them to arrive adds the parts up, in their order
+    auto block_of = [&](int64_t u) { return (int)(((u + 1) * blocks - 1) / units); };
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x < n_split) {
+        const int k = threadIdx.x;
+        const int first_b = block_of(split_first[k]), np = block_of(split_first[k] + split_n[k] - 1) - first_b + 1;
+        // (an item is the last of its first block, so a counter per block will do)
+        const bool last = atomicAdd(p.counters + first_b, 1u) == (unsigned)(np - 1);
+        if (last) p.counters[first_b] = 0;
+        last_block[k] = last;
+    }
+    __syncthreads();
+    // weights and sums of the parts; the queues are free
+    float(*weight)[H] = reinterpret_cast<float(*)[H]>(queue);
+    float(*sums)[H] = weight + kAttMaxCtas;
+    for (int s = 0; s < n_split; ++s) {
+        if (!last_block[s]) continue;
+        __threadfence();
+        const int first_b = block_of(split_first[s]), np = block_of(split_first[s] + split_n[s] - 1) - first_b + 1;
+        const Head f = open_item(split_item[s]);
+        auto part_of = [&](int k) { return cta_part(first_b + k, k == 0 ? 1 : 0); };
+        for (int k = threadIdx.x; k < np * H; k += T) {
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_of(k / H) + k % H * PO));
+            weight[k / H][k % H] = ml.x;
+            sums[k / H][k % H] = ml.y;
+        }
+        __syncthreads();
+        for (int h = warp; h < H; h += W) {
+            float top = -CUDART_INF_F, sum = 0.f;
+            for (int k = lane; k < np; k += 32) top = fmaxf(top, weight[k][h]);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float ref = top == -CUDART_INF_F ? 0.f : top;
+            for (int k = lane; k < np; k += 32) {
+                const float w = ex2(weight[k][h] - ref);
+                weight[k][h] = w;
+                sum = fmaf(w, sums[k][h], sum);
             }
-            __syncthreads();
-            if (last_block) {
-                __threadfence();
-                // (the item is not its first block's first, but every later block's first part)
-                auto part_of = [&](int k) { return p.cta_parts + ((int64_t)(first_b + k) * 2 + (k == 0 ? 1 : 0)) * PF; };
-                for (int h = threadIdx.x; h < H; h += T) {
-                    float top = -CUDART_INF_F, sum = 0.f;
-                    for (int k = 0; k < np; ++k) top = fmaxf(top, __ldcg(part_of(k) + h * PO));
-                    const float ref = top == -CUDART_INF_F ? 0.f : top;
-                    for (int k = 0; k < np; ++k) {
-                        const float w = ex2(__ldcg(part_of(k) + h * PO) - ref);
-                        weight[k][h] = w;
-                        sum = fmaf(w, __ldcg(part_of(k) + h * PO + 1), sum);
-                    }
-                    total_l[h] = sum;
-                    if (h < f.z && p.lse)
-                        p.lse[(int64_t)f.x * p.hq + f.y + h] =
-                            sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * 0.69314718056f;
-                }
-                __syncthreads();
-                for (int k = threadIdx.x; k < H * DP / 4; k += T) {
-                    const int h = k / (DP / 4), d = k % (DP / 4) * 4;
-                    if (h >= f.z || d >= p.dim) continue;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int q = 0; q < np; ++q) {
-                        const float w = weight[q][h];
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(part_of(q) + h * PO + 8 + d));
-                        o.x = fmaf(w, v.x, o.x);
-                        o.y = fmaf(w, v.y, o.y);
-                        o.z = fmaf(w, v.z, o.z);
-                        o.w = fmaf(w, v.w, o.w);
-                    }
-                    const float sum = total_l[h], inv = sum == 0.f ? 0.f : 1.f / sum;
-                    const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-                    const int64_t at = (int64_t)f.x * p.os + (int64_t)(f.y + h) * p.ohs + d;
-                    if (LEAN_SPAN(at, 4, p.out_extent, p.err)) store4(p.out, at, p.act, v);
-                }
+            sum = warp_sum(sum);
+            if (lane == 0) {
+                total_l[h] = sum;
+                sums[0][h] = top;  // (its own sum has been read)
             }
         }
         __syncthreads();
-        i = end;
+        for (int k = threadIdx.x; k < H * DP / 4; k += T) {
+            const int h = k / (DP / 4), d = k % (DP / 4) * 4;
+            if (h >= f.nh || d >= p.dim) continue;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 16
+            for (int q = 0; q < np; ++q) {
+                const float w = weight[q][h];
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(part_of(q) + h * PO + 8 + d));
+                o.x = fmaf(w, v.x, o.x);
+                o.y = fmaf(w, v.y, o.y);
+                o.z = fmaf(w, v.z, o.z);
+                o.w = fmaf(w, v.w, o.w);
+            }
+            store_result(f, h, d, o, sums[0][h], total_l[h]);
+        }
+        __syncthreads();
     }
 }
 
@@ -789,6 +841,7 @@ extern "C" lean_status lean_paged_attention(const lean_attention_args *a, void *
     p.tiles = p.group > 8 ? (p.group + 15) / 16 : 1;
     p.dim = (int)a->head_dim;
     p.page = (int)a->page_size;
+    p.paged = a->page_size % kUnit == 0;
     p.width = (int)a->table_width;
     p.window = (int)std::min<int64_t>(a->window, INT32_MAX);
     p.act = (int)a->act_dtype;
