@@ -25,8 +25,8 @@
 //     rows 8-15 the second, so that one instruction serves both.
 //   - Running maximum and sum per warp; a warp's first and last group may be
 //     shared with its neighbours: the warps of a block join through shared
-//     memory, blocks through the workspace, where the block that arrives last
-//     adds the parts up in their order (results do not depend on timing).
+//     memory, blocks through the workspace and a second kernel, launched early,
+//     that adds the parts up in their order.
 //
 // q and p are split into parts of the cache's type, x = x0 + x1 (+ x2), 8 (bf16)
 // or 11 bits each: three parts for fp32 q and out, which leave nothing of fp32's
@@ -41,14 +41,18 @@ namespace {
 constexpr int kAttMaxDim = 256;
 constexpr int kAttMaxCtas = 160;  // of a launch: at most one per SM
 constexpr int kUnit = 16;         // tokens
-constexpr int64_t kCounterBytes = 1024;  // an arrival counter per block
+constexpr int64_t kSharedBytes = 2048;  // a Shared for each block
+
+struct Shared {  // an item that begins in a block and goes on in others (-1: none), and how many blocks it has
+    int item, parts;
+};
 
 struct AttArgs {
     const void *q, *k, *v;
     void *out;
     float *lse;
     const int32_t *table, *lens;
-    unsigned *counters;
+    Shared *shared;
     float *warp_parts, *cta_parts;
     int64_t qs, qhs, os, ohs, page_stride, place_stride, cache_hs, table_stride, n_pages;
     int n_seqs, hq, hkv, group, tiles, dim, page, paged, width, window;
@@ -69,7 +73,17 @@ struct AttShape {
     static constexpr int kSmem = 512 + kWarps * (kStages * kStageBytes + (DP == 256 ? DP / 16 * 12 * 128 : 0));
 };
 // A part: maxima, sums and outputs of a group of H heads.
-__host__ __device__ constexpr int part_floats(int heads, int dp) { return heads * (dp + 8); }
+__host__ __device__ constexpr int part_floats(int heads, int dp) { return heads * (dp + 4); }
+// Shared memory of a block: queues; q at 256 (above); and, where it fits, a part per warp.
+constexpr int kMaxSmem = 232448 - 1024;  // of 227 KB, less static variables
+template <int DP>
+__host__ __device__ constexpr bool parts_in_smem(int heads) {
+    return AttShape<DP>::kSmem + AttShape<DP>::kWarps * part_floats(heads, DP) * 4 <= kMaxSmem;
+}
+template <int DP>
+__host__ __device__ constexpr int att_smem(int heads) {
+    return AttShape<DP>::kSmem + (parts_in_smem<DP>(heads) ? AttShape<DP>::kWarps * part_floats(heads, DP) * 4 : 0);
+}
 
 // 16 bytes of which `real` (16 or 0) are copied and the rest zero
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int real) {
@@ -149,6 +163,10 @@ __device__ __forceinline__ void store_out(void *p, int64_t i, int act, const flo
     else if (act == LEAN_BF16) store_vec<__nv_bfloat16, N>(static_cast<__nv_bfloat16 *>(p) + i, f);
     else store_vec<__half, N>(static_cast<__half *>(p) + i, f);
 }
+__device__ __forceinline__ int nth_bit(unsigned m, int n) {  // place of the n-th (from 0) bit that is set
+    for (; n > 0; --n) m &= m - 1;
+    return __ffs(m) - 1;
+}
 __device__ __forceinline__ float natural_lse(float m, float sum) {
     return sum == 0.f ? -CUDART_INF_F : (m + log2f(sum)) * 0.69314718056f;
 }
@@ -172,24 +190,19 @@ __device__ __forceinline__ Span open_span(const AttArgs &p, int s) {
 
 // A place in the list of units: sequence, kv head, tile of its query heads, unit.
 // Where units lie within pages (p.paged: pages of a multiple of 16 tokens), also
-// the page's number in the sequence and the unit's first place in it.
+// the unit's first place in its page.
 struct Place {
     int s, kvh, tile, c;
-    int page_at, in_page;
+    int in_page;
     Span x;
 };
 __device__ __forceinline__ void to_page(const AttArgs &p, Place &at) {
-    const int tok = at.x.base + at.c * kUnit;
-    at.page_at = tok / p.page;
-    at.in_page = tok - at.page_at * p.page;
+    at.in_page = (at.x.base + at.c * kUnit) % p.page;
 }
-__device__ __forceinline__ void advance(const AttArgs &p, Place &at) {
+__device__ __forceinline__ bool advance(const AttArgs &p, Place &at) {  // true: to another item
     if (++at.c < at.x.n) {
-        if ((at.in_page += kUnit) == p.page) {
-            at.in_page = 0;
-            ++at.page_at;
-        }
-        return;
+        if ((at.in_page += kUnit) == p.page) at.in_page = 0;
+        return false;
     }
     at.c = 0;
     if (++at.tile == p.tiles) {
@@ -200,6 +213,7 @@ __device__ __forceinline__ void advance(const AttArgs &p, Place &at) {
         }
     }
     to_page(p, at);
+    return true;
 }
 
 // What a warp leaves of a group that it does not finish, or a block of one that
@@ -208,15 +222,34 @@ struct Record {
     int item;           // -1: none
     int n;              // units of the item
     int64_t first;      // its first unit, counted from the block's first one
-    const float *part;
 };
 
 // The most that running scores may exceed the reference of their exponentials by
 // before it moves, as a power of two: p stays below 2^8, and the accumulators are
 // rescaled a few times a run instead of in every unit with a new maximum.
 constexpr float kSlack = 8.f;
-// Units of a warp's time that joining blocks costs.
+// Units of a warp's time that joining blocks costs, and that an item costs beside its
+// units (q, the first maximum, the result): that many empty ones are counted to it
+// when the runs are cut.
 constexpr int kJoinUnits = 8;
+constexpr int kItemUnits = 3;
+
+struct Head {  // of an item: its sequence, first query head and number of heads
+    int s, h0, nh;
+};
+__device__ __forceinline__ Head open_item(const AttArgs &p, int item, int heads) {
+    const int groups = p.hkv * p.tiles, g = item % groups, tile = g % p.tiles;
+    return Head{item / groups, g / p.tiles * p.group + tile * heads, min(heads, p.group - tile * heads)};
+}
+__device__ __forceinline__ void store_result(const AttArgs &p, const Head &f, int h, int d, float4 o, float top,
+                                             float sum) {
+    if (h >= f.nh || d >= p.dim) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+    const int64_t at = (int64_t)f.s * p.os + (int64_t)(f.h0 + h) * p.ohs + d;
+    if (LEAN_SPAN(at, 4, p.out_extent, p.err)) store_out<4>(p.out, at, p.act, v);
+    if (d == 0 && p.lse) p.lse[(int64_t)f.s * p.hq + f.h0 + h] = natural_lse(top, sum);
+}
 
 // WIDE: 9 to 16 query heads in a group, one per row; else up to 8, two rows each.
 template <typename C, int DP, int PARTS, bool WIDE>
@@ -227,7 +260,10 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     constexpr int KS = DP / 16;                                // steps of the contraction, and pairs of output tiles
     constexpr int AREGS = WIDE ? 4 * PARTS : 4 + (PARTS > 2 ? 2 : 0);  // of q per step
     constexpr bool QSMEM = DP == 256;                                  // no registers left for q
-    constexpr int PF = part_floats(H, DP), PO = 8 + DP;                // a head's row of a part: m, l, -, out
+    constexpr int PF = part_floats(H, DP), PO = 4 + DP;                // a head's row of a part: m, l, -, out
+    constexpr bool PSMEM = parts_in_smem<DP>(H);
+    constexpr bool EARLY_Q = !WIDE && DP <= 128;  // registers for the next q beside the accumulators
+    static_assert(PF * 4 <= S * STAGE, "a part fits a queue");
     extern __shared__ uint8_t queue_raw[];
     uint8_t *queue = queue_raw + (512 - smem_addr(queue_raw) % 512) % 512;
     __shared__ int64_t scan[W];
@@ -236,8 +272,6 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         int s, g, c;
     } start_at[W];
     __shared__ Record rec[2 * W];
-    __shared__ float total_l[H];
-    __shared__ int last_block[2];
 
     step_begin();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -251,7 +285,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     int most = 0;
     for (int s = s_lo; s < s_hi; ++s) {
         const int n = open_span(p, s).n;
-        mine += (int64_t)n * groups;
+        mine += (int64_t)(n + kItemUnits) * groups;
         most = max(most, n);
     }
     int64_t incl = mine;
@@ -279,7 +313,10 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     const int64_t items = (int64_t)p.n_seqs * groups;
     const bool by_item = items <= gridDim.x && (most + W - 1) / W <= units / ((int64_t)gridDim.x * W) + kJoinUnits;
     const int blocks = by_item ? (int)items : (int)min((int64_t)gridDim.x, (units + W - 1) / W);
-    if ((int)blockIdx.x >= blocks) return;
+    if ((int)blockIdx.x >= blocks) {
+        if (threadIdx.x == 0) p.shared[blockIdx.x] = Shared{-1, 0};
+        return;
+    }
     int64_t b_lo = 0, b_n;  // first unit of the block, and how many (unit numbers below count from b_lo)
     if (by_item) {
         const int s = blockIdx.x / groups;
@@ -297,7 +334,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
             if (b < before || b >= before + mine) continue;
             int64_t at = before;
             for (int s = s_lo; s < s_hi; ++s) {
-                const int n = open_span(p, s).n;
+                const int n = open_span(p, s).n + kItemUnits;
                 if (b < at + (int64_t)n * groups) {
                     const int in = (int)(b - at);
                     start_at[i].s = s;
@@ -310,36 +347,43 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         }
     }
     __syncthreads();
-    const int64_t u_lo = b_n * warp / W, u_hi = b_n * (warp + 1) / W;
-
+    int64_t u_lo = b_n * warp / W;
+    const int64_t u_hi = b_n * (warp + 1) / W;
+    Place next;  // to be loaded
     if (u_lo < u_hi) {
-        const uint32_t my_queue = smem_addr(queue) + warp * (S * STAGE);
-        Place next;  // to be loaded
         next.s = start_at[warp].s;
         next.kvh = start_at[warp].g / p.tiles;
         next.tile = start_at[warp].g - next.kvh * p.tiles;
         next.c = start_at[warp].c;
         next.x = open_span(p, next.s);
-        to_page(p, next);
+        if (next.c >= next.x.n) {  // in the item's empty units: on to the next item
+            u_lo += next.x.n + kItemUnits - next.c;
+            next.c = next.x.n - 1;
+            advance(p, next);
+        } else {
+            to_page(p, next);
+        }
+    }
+    uint8_t *const tail_part = queue + warp * (S * STAGE);  // where a warp's last part goes, and an earlier one
+    uint8_t *const head_part = PSMEM ? queue + AttShape<DP>::kSmem - 512 + warp * (PF * 4)
+                                     : reinterpret_cast<uint8_t *>(p.warp_parts + ((int64_t)blockIdx.x * W + warp) * PF);
+
+    if (u_lo < u_hi) {
+        const uint32_t my_queue = smem_addr(queue) + warp * (S * STAGE);
         Place cur = next;  // to be computed
         int64_t u_next = u_lo;
 
-        // the page of token lane % 16 of the unit to be loaded next (paged: of the unit), fetched one unit ahead
-        auto fetch_page = [&]() {
-            int at;
-            bool in;
-            if (p.paged) {
-                at = next.page_at;
-                in = next.x.len > 0;
-            } else {
-                const int tok = next.x.base + next.c * kUnit + lane % kUnit;
-                at = tok / p.page;
-                in = tok >= next.x.start && tok < next.x.len;
-            }
-            const int64_t e = (int64_t)next.s * p.table_stride + at;
+        // Pages, fetched before they are needed: (paged) those of units pages_from + lane of the item, 32 at a
+        // time, else those of token lane % 16 of the unit to be loaded next.
+        int pages_from = next.c;
+        auto fetch_pages = [&]() {
+            int tok = next.x.base + (p.paged ? (pages_from + lane) * kUnit : next.c * kUnit + lane % kUnit);
+            if (p.paged) tok = max(tok, next.x.start);
+            const bool in = tok >= next.x.start && tok < next.x.len;
+            const int64_t e = (int64_t)next.s * p.table_stride + tok / p.page;
             return in && LEAN_IN(e, (int64_t)(p.n_seqs - 1) * p.table_stride + p.width, p.err) ? p.table[e] : 0;
         };
-        int page_id = fetch_page();
+        int pages = fetch_pages();
         // a lane's piece of a row: its place in the caches, in a stage, and whether the head has it at all
         const int lr = lane / LPR, col = lane % LPR;
         const C *k_lane = static_cast<const C *>(p.k) + 8 * col, *v_lane = static_cast<const C *>(p.v) + 8 * col;
@@ -350,6 +394,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
             if (u_next < u_hi) {
                 const uint32_t dst = to_lane + stage * STAGE;
                 const int t0 = next.x.base + next.c * kUnit;
+                const int page_id = p.paged ? __shfl_sync(0xffffffffu, pages, next.c - pages_from) : pages;
                 const bool page_ok = page_id >= 0 && page_id < p.n_pages;
                 const int64_t unit_off = p.paged ? (int64_t)page_id * p.page_stride +
                                                        (int64_t)next.in_page * p.place_stride +
@@ -388,13 +433,33 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                         cp_async16(to + kUnit * RB, o >= 0 ? v_lane + o : static_cast<const C *>(p.v), o >= 0 ? real : 0);
                     }
                 }
-                if (++u_next < u_hi) {
-                    advance(p, next);
-                    page_id = fetch_page();
+                u_next += next.c == next.x.n - 1 ? 1 + kItemUnits : 1;
+                if (u_next < u_hi) {
+                    const bool other = advance(p, next);
+                    if (!p.paged || other || next.c == pages_from + 32) {
+                        pages_from = next.c;
+                        pages = fetch_pages();
+                    }
                 }
             }
             cp_async_commit();
         };
+        // q of the current item, asked for before its first keys (after them it would wait for them)
+        float2 f[NH][2 * KS];
+        auto load_q = [&]() {
+            const int h0 = cur.kvh * p.group + cur.tile * H, nh = min(H, p.group - cur.tile * H);
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+#pragma unroll
+                for (int i = 0; i < 2 * KS; ++i) {
+                    const int d = 8 * i + 2 * c4;
+                    const int64_t at = (int64_t)cur.s * p.qs + (int64_t)(h0 + r + 8 * h) * p.qhs + d;
+                    f[h][i] = r + 8 * h < nh && d < p.dim && LEAN_SPAN(at, 2, p.q_extent, p.err)
+                                  ? load_pair<(PARTS > 2)>(p.q, at, p.act)
+                                  : make_float2(0.f, 0.f);
+                }
+        };
+        if (EARLY_Q) load_q();
 #pragma unroll
         for (int i = 0; i < S - 1; ++i) load_unit(i);
 
@@ -409,22 +474,12 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         float acc[2 * KS][4], m[NH], l[NH], zs[NH];
         bool fresh = true;
         int stage = 0;
-        for (int64_t u = u_lo; u < u_hi; ++u) {
+        for (int64_t u = u_lo; u < u_hi;) {
             load_unit(stage == 0 ? S - 1 : stage - 1);
             const int h0 = cur.kvh * p.group + cur.tile * H, nh = min(H, p.group - cur.tile * H);
             if (fresh) {
                 fresh = false;
-                float2 f[NH][2 * KS];
-#pragma unroll
-                for (int h = 0; h < NH; ++h)
-#pragma unroll
-                    for (int i = 0; i < 2 * KS; ++i) {
-                        const int d = 8 * i + 2 * c4;
-                        const int64_t at = (int64_t)cur.s * p.qs + (int64_t)(h0 + r + 8 * h) * p.qhs + d;
-                        f[h][i] = r + 8 * h < nh && d < p.dim && LEAN_SPAN(at, 2, p.q_extent, p.err)
-                                      ? load_pair<(PARTS > 2)>(p.q, at, p.act)
-                                      : make_float2(0.f, 0.f);
-                    }
+                if (!EARLY_Q) load_q();
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     float top = 0.f;
@@ -566,14 +621,15 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
             }
 
             // ---- the end of a group, or of the run
-            if (cur.c == cur.x.n - 1 || u == u_hi - 1) {
+            const bool item_end = cur.c == cur.x.n - 1;
+            const int64_t u_then = u + (item_end ? 1 + kItemUnits : 1);
+            if (item_end || u_then >= u_hi) {
                 fresh = true;
                 const int64_t first = u - cur.c;
-                const bool whole = first >= u_lo && cur.c == cur.x.n - 1, at_end = u == u_hi - 1;
+                const bool whole = first >= u_lo && item_end, at_end = u_then >= u_hi;
                 // a part that others continue: the run's last in this warp's own queue (nothing is under way to
-                // it any more), an earlier one in the workspace
-                float *part = at_end ? reinterpret_cast<float *>(queue + warp * (S * STAGE))
-                                     : p.warp_parts + ((int64_t)blockIdx.x * W + warp) * PF;
+                // it any more)
+                float *part = reinterpret_cast<float *>(at_end ? tail_part : head_part);
                 __syncwarp();
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
@@ -593,7 +649,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                         float o[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) o[i] = (WIDE ? acc[j][2 * h + i] : acc[j][i] + acc[j][2 + i]) * inv;
-                        if (!whole) *reinterpret_cast<float2 *>(part + row * PO + 8 + 8 * j + 2 * c4) = make_float2(o[0], o[1]);
+                        if (!whole) *reinterpret_cast<float2 *>(part + row * PO + 4 + 8 * j + 2 * c4) = make_float2(o[0], o[1]);
                         else if (8 * j < p.dim && LEAN_SPAN(at + 8 * j, 2, p.out_extent, p.err))
                             store_out<2>(p.out, at + 8 * j, p.act, o);
                     }
@@ -603,10 +659,13 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     q.item = cur.s * groups + cur.kvh * p.tiles + cur.tile;
                     q.n = cur.x.n;
                     q.first = first;
-                    q.part = part;
                 }
+                advance(p, cur);
+                if (EARLY_Q && !at_end) load_q();
+            } else {
+                advance(p, cur);
             }
-            advance(p, cur);
+            u = u_then;
             stage = stage + 1 == S ? 0 : stage + 1;
         }
     }
@@ -614,148 +673,135 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     __syncthreads();
 
     // ---- groups shared by the warps of this block: each 32 x 4 outputs of one are added up by a warp
-    struct Head {  // of an item: its sequence, first query head and number of heads
-        int s, h0, nh;
-    };
-    auto open_item = [&](int item) {
-        const int g = item % groups, tile = g % p.tiles;
-        return Head{item / groups, g / p.tiles * p.group + tile * H, min(H, p.group - tile * H)};
-    };
-    auto cta_part = [&](int64_t b, int slot) { return p.cta_parts + (b * 2 + slot) * PF; };
-    auto store_result = [&](const Head &f, int h, int d, float4 o, float top, float sum) {
-        if (h >= f.nh || d >= p.dim) return;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-        const int64_t at = (int64_t)f.s * p.os + (int64_t)(f.h0 + h) * p.ohs + d;
-        if (LEAN_SPAN(at, 4, p.out_extent, p.err)) store_out<4>(p.out, at, p.act, v);
-        if (d == 0 && p.lse) p.lse[(int64_t)f.s * p.hq + f.h0 + h] = natural_lse(top, sum);
-    };
-    int n_split = 0, job = 0;  // groups that other blocks share: the block's first, its last, or both
-    int split_item[2], split_n[2];
-    int64_t split_first[2];
-    for (int i = 0; i < 2 * W;) {
+    // lane k knows record k; a group begins where the item changes
+    const bool has = lane < 2 * W && rec[lane].item >= 0;
+    const unsigned have = __ballot_sync(0xffffffffu, has);
+    const unsigned below = have & ((1u << lane) - 1);
+    const bool leads = has && (below == 0 || rec[31 - __clz(below)].item != rec[lane].item);
+    const unsigned leaders = __ballot_sync(0xffffffffu, leads);
+    constexpr int JOBS = H * DP / 128;
+    const int n_groups = __popc(leaders);
+    for (int job = warp; job < n_groups * JOBS; job += W) {
+        const int i = nth_bit(leaders, job / JOBS), j = job % JOBS;
+        const unsigned later = leaders & ~((2u << i) - 1);
+        unsigned members = have & ~((1u << i) - 1) & (later ? (later & -later) - 1 : 0xffffffffu);
         const Record head = rec[i];
-        if (head.item < 0) {
-            ++i;
-            continue;
+        const Head f = open_item(p, head.item, H);
+        const int h = (j * 32 + lane) * 4 / DP, d = (j * 32 + lane) * 4 % DP;
+        float top = -CUDART_INF_F, sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        while (members) {
+            const int k = __ffs(members) - 1;
+            members &= members - 1;
+            const float *row = reinterpret_cast<const float *>(k & 1 ? tail_part + (k / 2 - warp) * (S * STAGE)
+                                                                     : head_part + (int64_t)(k / 2 - warp) * (PF * 4)) + h * PO;
+            const float2 ml = *reinterpret_cast<const float2 *>(row);
+            const float4 v = *reinterpret_cast<const float4 *>(row + 4 + d);
+            const float now = fmaxf(top, ml.x), ref = now == -CUDART_INF_F ? 0.f : now;
+            const float old = ex2(top - ref), w = ex2(ml.x - ref);
+            top = now;
+            sum = fmaf(sum, old, w * ml.y);
+            o.x = fmaf(o.x, old, w * v.x);
+            o.y = fmaf(o.y, old, w * v.y);
+            o.z = fmaf(o.z, old, w * v.z);
+            o.w = fmaf(o.w, old, w * v.w);
         }
-        int end = i + 1;  // the group's records: all up to the next item's
-        while (end < 2 * W && (rec[end].item < 0 || rec[end].item == head.item)) ++end;
-        const bool whole = head.first >= 0 && head.first + head.n <= b_n;
-        const int slot = head.first < 0 ? 0 : 1;
-        const Head f = open_item(head.item);
-        for (int j = 0; j < H * DP / 128; ++j, ++job) {
-            if (job % W != warp) continue;
-            const int h = (j * 32 + lane) * 4 / DP, d = (j * 32 + lane) * 4 % DP;
-            float top = -CUDART_INF_F, sum = 0.f;
-            for (int k = i; k < end; ++k)
-                if (rec[k].item >= 0) top = fmaxf(top, rec[k].part[h * PO]);
-            const float ref = top == -CUDART_INF_F ? 0.f : top;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = i; k < end; ++k) {
-                if (rec[k].item < 0) continue;
-                const float *row = rec[k].part + h * PO;
-                const float w = ex2(row[0] - ref);
-                const float4 v = *reinterpret_cast<const float4 *>(row + 8 + d);
-                sum = fmaf(w, row[1], sum);
-                o.x = fmaf(w, v.x, o.x);
-                o.y = fmaf(w, v.y, o.y);
-                o.z = fmaf(w, v.z, o.z);
-                o.w = fmaf(w, v.w, o.w);
-            }
-            if (whole) {
-                store_result(f, h, d, o, top, sum);
-            } else {
-                float *row = cta_part(blockIdx.x, slot) + h * PO;
-                *reinterpret_cast<float4 *>(row + 8 + d) = o;
-                if (d == 0) *reinterpret_cast<float2 *>(row) = make_float2(top, sum);
-            }
+        if (head.first >= 0 && head.first + head.n <= b_n) {
+            store_result(p, f, h, d, o, top, sum);
+        } else {  // the block's part of the item that began before it, or of the one that goes on after it
+            float *row = p.cta_parts + ((int64_t)blockIdx.x * 2 + (head.first < 0 ? 0 : 1)) * PF + h * PO;
+            *reinterpret_cast<float4 *>(row + 4 + d) = o;
+            if (d == 0) *reinterpret_cast<float2 *>(row) = make_float2(top, sum);
         }
-        if (!whole) {
-            split_item[n_split & 1] = head.item;
-            split_n[n_split & 1] = head.n;
-            split_first[n_split & 1] = head.first + b_lo;
-            ++n_split;
-        }
-        i = end;
     }
-    if (n_split == 0) return;
+    // The item that begins in this block and goes on in the next ones, for the kernel that adds its parts up.
+    if (threadIdx.x == 0) {
+        Shared x = {-1, 0};
+        if (leaders) {
+            const Record q = rec[31 - __clz(leaders)];
+            if (q.first >= 0 && q.first + q.n > b_n) {
+                const int64_t last = q.first + b_lo + q.n - 1;  // the last of its units, and the block that has it
+                x.item = q.item;
+                x.parts = (int)(((last + 1) * blocks - 1) / units) - (int)blockIdx.x + 1;
+            }
+        }
+        p.shared[blockIdx.x] = x;
+    }
+}
 
-    // ---- groups shared with other blocks: the last of them to arrive adds the parts up, in their order
-    auto block_of = [&](int64_t u) { return (int)(((u + 1) * blocks - 1) / units); };
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x < n_split) {
-        const int k = threadIdx.x;
-        const int first_b = block_of(split_first[k]), np = block_of(split_first[k] + split_n[k] - 1) - first_b + 1;
-        // (an item is the last of its first block, so a counter per block will do)
-        const bool last = atomicAdd(p.counters + first_b, 1u) == (unsigned)(np - 1);
-        if (last) p.counters[first_b] = 0;
-        last_block[k] = last;
-    }
-    __syncthreads();
-    // weights and sums of the parts; the queues are free
-    float(*weight)[H] = reinterpret_cast<float(*)[H]>(queue);
-    float(*sums)[H] = weight + kAttMaxCtas;
-    for (int s = 0; s < n_split; ++s) {
-        if (!last_block[s]) continue;
-        __threadfence();
-        const int first_b = block_of(split_first[s]), np = block_of(split_first[s] + split_n[s] - 1) - first_b + 1;
-        const Head f = open_item(split_item[s]);
-        auto part_of = [&](int k) { return cta_part(first_b + k, k == 0 ? 1 : 0); };
-        for (int k = threadIdx.x; k < np * H; k += T) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part_of(k / H) + k % H * PO));
-            weight[k / H][k % H] = ml.x;
-            sums[k / H][k % H] = ml.y;
-        }
-        __syncthreads();
-        for (int h = warp; h < H; h += W) {
-            float top = -CUDART_INF_F, sum = 0.f;
-            for (int k = lane; k < np; k += 32) top = fmaxf(top, weight[k][h]);
+// The parts of items shared by blocks: a block for each 32 x 4 outputs of the item that begins in block blockIdx.x
+// / JOBS of the kernel before, if one does.  Its warps take the parts in turn, so that all are under way at once.
+constexpr int kSumWarps = 8, kSumParts = kAttMaxCtas / kSumWarps;
+template <int H, int DP>
+__global__ void __launch_bounds__(kSumWarps * 32) attend_sum_kernel(const AttArgs p) {
+    constexpr int JOBS = H * DP / 128, PF = part_floats(H, DP), PO = 4 + DP;
+    __shared__ float4 out_s[kSumWarps][32];
+    __shared__ float2 ml_s[kSumWarps][32];
+    step_begin();
+    const int b = blockIdx.x / JOBS, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const Shared x = p.shared[b];
+    if (x.item < 0) return;
+    const int e = (blockIdx.x % JOBS * 32 + lane) * 4, h = e / DP, d = e % DP;
+    float2 ml[kSumParts];
+    float4 v[kSumParts];
 #pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float ref = top == -CUDART_INF_F ? 0.f : top;
-            for (int k = lane; k < np; k += 32) {
-                const float w = ex2(weight[k][h] - ref);
-                weight[k][h] = w;
-                sum = fmaf(w, sums[k][h], sum);
-            }
-            sum = warp_sum(sum);
-            if (lane == 0) {
-                total_l[h] = sum;
-                sums[0][h] = top;  // (its own sum has been read)
-            }
+    for (int i = 0; i < kSumParts; ++i) {
+        const int k = warp + i * kSumWarps;
+        ml[i] = make_float2(-CUDART_INF_F, 0.f);
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < x.parts) {
+            const float *row = p.cta_parts + ((int64_t)(b + k) * 2 + (k == 0)) * PF + h * PO;
+            ml[i] = *reinterpret_cast<const float2 *>(row);
+            v[i] = *reinterpret_cast<const float4 *>(row + 4 + d);
         }
-        __syncthreads();
-        for (int k = threadIdx.x; k < H * DP / 4; k += T) {
-            const int h = k / (DP / 4), d = k % (DP / 4) * 4;
-            if (h >= f.nh || d >= p.dim) continue;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 16
-            for (int q = 0; q < np; ++q) {
-                const float w = weight[q][h];
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(part_of(q) + h * PO + 8 + d));
-                o.x = fmaf(w, v.x, o.x);
-                o.y = fmaf(w, v.y, o.y);
-                o.z = fmaf(w, v.z, o.z);
-                o.w = fmaf(w, v.w, o.w);
-            }
-            store_result(f, h, d, o, sums[0][h], total_l[h]);
-        }
-        __syncthreads();
     }
+    float top = -CUDART_INF_F, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float2 a, float4 u, float ref) {
+        const float w = ex2(a.x - ref);
+        sum = fmaf(w, a.y, sum);
+        o.x = fmaf(w, u.x, o.x);
+        o.y = fmaf(w, u.y, o.y);
+        o.z = fmaf(w, u.z, o.z);
+        o.w = fmaf(w, u.w, o.w);
+    };
+#pragma unroll
+    for (int i = 0; i < kSumParts; ++i) top = fmaxf(top, ml[i].x);
+    float ref = top == -CUDART_INF_F ? 0.f : top;
+#pragma unroll
+    for (int i = 0; i < kSumParts; ++i)
+        if (warp + i * kSumWarps < x.parts) add(ml[i], v[i], ref);
+    ml_s[warp][lane] = make_float2(top, sum);
+    out_s[warp][lane] = o;
+    __syncthreads();
+    if (warp > 0) return;
+    sum = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kSumWarps; ++i) top = fmaxf(top, ml_s[i][lane].x);
+    ref = top == -CUDART_INF_F ? 0.f : top;
+#pragma unroll
+    for (int i = 0; i < kSumWarps; ++i) add(ml_s[i][lane], out_s[i][lane], ref);
+    store_result(p, open_item(p, x.item, H), h, d, o, top, sum);
 }
 
 template <typename C, int DP, int PARTS, bool WIDE>
 lean_status launch_attend(const AttArgs &p, int64_t flags, void *stream) {
     static std::atomic<uint64_t> done{0};
     auto kern = attend_kernel<C, DP, PARTS, WIDE>;
-    if (!step_ensure_smem(kern, AttShape<DP>::kSmem, done)) return LEAN_ERR_CUDA;
+    if (!step_ensure_smem(kern, att_smem<DP>(WIDE ? 16 : 8), done)) return LEAN_ERR_CUDA;
     // no more blocks than there can be units for
     constexpr int W = AttShape<DP>::kWarps;
     const int64_t units = ((int64_t)p.width * p.page + 2 * kUnit) / kUnit * p.n_seqs * p.hkv * p.tiles;
     const int64_t grid = std::min<int64_t>(std::min(step_sm_count(), kAttMaxCtas), std::max<int64_t>(1, units / W));
-    return step_launch(kern, grid, W * 32, AttShape<DP>::kSmem, flags, stream, p);
+    const lean_status st = step_launch(kern, grid, W * 32, att_smem<DP>(WIDE ? 16 : 8), flags, stream, p);
+    // (no item can be shared by blocks where each gets its own whatever the lengths are)
+    const int64_t most = ((int64_t)p.width * p.page + 2 * kUnit - 1) / kUnit;
+    const bool by_item = (int64_t)p.n_seqs * p.hkv * p.tiles <= grid && (most + W - 1) / W <= kJoinUnits;
+    if (st != LEAN_OK || grid == 1 || by_item) return st;
+    constexpr int H = WIDE ? 16 : 8;
+    return step_launch(attend_sum_kernel<H, DP>, grid * (H * DP / 128), kSumWarps * 32, 0, LEAN_FLAG_EARLY_WEIGHTS,
+                       stream, p);
 }
 template <typename C, int DP>
 lean_status pick_attend(const AttArgs &p, int64_t flags, void *stream) {
@@ -785,8 +831,8 @@ bool att_sizes_ok(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim) {
 extern "C" int64_t lean_paged_attention_workspace_bytes(int64_t n_seqs, int64_t n_q_heads, int64_t n_kv_heads,
                                                         int64_t head_dim) {
     if (!att_sizes_ok(n_seqs, n_q_heads, n_kv_heads, head_dim)) return -1;
-    // counters, a part per warp and two per block, of the largest grid
-    return kCounterBytes + kAttMaxCtas * (8 + 2) * att_part_bytes(n_q_heads, n_kv_heads, head_dim);
+    // what blocks share, a part per warp and two per block, of the largest grid
+    return kSharedBytes + kAttMaxCtas * (8 + 2) * att_part_bytes(n_q_heads, n_kv_heads, head_dim);
 }
 
 extern "C" lean_status lean_paged_attention(const lean_attention_args *a, void *stream) {
@@ -822,8 +868,8 @@ extern "C" lean_status lean_paged_attention(const lean_attention_args *a, void *
     p.table = a->block_table;
     p.lens = a->seq_lens;
     uint8_t *ws = static_cast<uint8_t *>(a->workspace);
-    p.counters = reinterpret_cast<unsigned *>(ws);
-    p.warp_parts = reinterpret_cast<float *>(ws + kCounterBytes);
+    p.shared = reinterpret_cast<Shared *>(ws);
+    p.warp_parts = reinterpret_cast<float *>(ws + kSharedBytes);
     p.cta_parts = p.warp_parts + kAttMaxCtas * 8 * att_part_bytes(a->n_q_heads, a->n_kv_heads, a->head_dim) / 4;
     p.qs = a->q_stride;
     p.qhs = a->q_head_stride;

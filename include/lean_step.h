@@ -217,8 +217,8 @@ lean_status lean_kv_pages(const lean_kv_pages_args *args, void *stream);
  * fp32, so that fp32 q keeps its precision (relative error about 2^-17).
  * q, out and the caches: 16-byte aligned, strides multiples of 8 elements.
  * workspace: lean_paged_attention_workspace_bytes() bytes, 256-byte aligned,
- * zeroed once; every call leaves its counters zero.  Calls that may run at the
- * same time must not share one.  Results do not depend on timing.
+ * any contents.  Calls that may run at the same time must not share one.
+ * Results do not depend on timing.
  * LEAN_ERR_SHAPE: a size <= 0, heads that do not divide, head_dim not a multiple
  * of 8 or above 256, window < 0, table_width * page_size above 2^31 - 1, more
  * than 2^31 - 1 sequences x kv heads, or a workspace too small.  LEAN_ERR_ALIGN,
