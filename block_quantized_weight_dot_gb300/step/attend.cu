@@ -75,7 +75,7 @@ struct AttShape {
 // A part: maxima, sums and outputs of a group of H heads.
 __host__ __device__ constexpr int part_floats(int heads, int dp) { return heads * (dp + 4); }
 // Shared memory of a block: queues; q at 256 (above); and, where it fits, a part per warp.
-constexpr int kMaxSmem = 232448 - 1024;  // of 227 KB, less static variables
+constexpr int kMaxSmem = 232448 - 1536;  // of 227 KB, less static variables
 template <int DP>
 __host__ __device__ constexpr bool parts_in_smem(int heads) {
     return AttShape<DP>::kSmem + AttShape<DP>::kWarps * part_floats(heads, DP) * 4 <= kMaxSmem;
@@ -221,7 +221,7 @@ __device__ __forceinline__ bool advance(const AttArgs &p, Place &at) {  // true:
 struct Record {
     int item;           // -1: none
     int n;              // units of the item
-    int64_t first;      // its first unit, counted from the block's first one
+    int first;          // its first unit, counted from the block's first one
 };
 
 // The most that running scores may exceed the reference of their exponentials by
@@ -232,7 +232,7 @@ constexpr float kSlack = 8.f;
 // units (q, the first maximum, the result): that many empty ones are counted to it
 // when the runs are cut.
 constexpr int kJoinUnits = 8;
-constexpr int kItemUnits = 3;
+constexpr int kItemUnits = 4;
 
 struct Head {  // of an item: its sequence, first query head and number of heads
     int s, h0, nh;
@@ -262,15 +262,14 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     constexpr bool QSMEM = DP == 256;                                  // no registers left for q
     constexpr int PF = part_floats(H, DP), PO = 4 + DP;                // a head's row of a part: m, l, -, out
     constexpr bool PSMEM = parts_in_smem<DP>(H);
-    constexpr bool EARLY_Q = !WIDE && DP <= 128;  // registers for the next q beside the accumulators
+    // registers for q as it was read: beside the accumulators, and all through the item before
+    constexpr bool EARLY_Q = !WIDE && DP <= 128, AHEAD_Q = !WIDE && DP == 64;
     static_assert(PF * 4 <= S * STAGE, "a part fits a queue");
     extern __shared__ uint8_t queue_raw[];
     uint8_t *queue = queue_raw + (512 - smem_addr(queue_raw) % 512) % 512;
-    __shared__ int64_t scan[W];
+    __shared__ unsigned scan[W];
     __shared__ int longest[W];
-    __shared__ struct {
-        int s, g, c;
-    } start_at[W];
+    __shared__ unsigned units_before[T];
     __shared__ Record rec[2 * W];
 
     step_begin();
@@ -281,17 +280,17 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     // ---- the list of units, and this block's and warp's run of it
     const int per = (p.n_seqs + T - 1) / T;  // sequences a thread sums up
     const int s_lo = min(p.n_seqs, (int)threadIdx.x * per), s_hi = min(p.n_seqs, s_lo + per);
-    int64_t mine = 0;
+    unsigned mine = 0;
     int most = 0;
     for (int s = s_lo; s < s_hi; ++s) {
         const int n = open_span(p, s).n;
-        mine += (int64_t)(n + kItemUnits) * groups;
+        mine += (unsigned)(n + kItemUnits) * groups;
         most = max(most, n);
     }
-    int64_t incl = mine;
+    unsigned incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += u;
     }
     most = __reduce_max_sync(0xffffffffu, most);
@@ -301,7 +300,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     }
     if (threadIdx.x < 2 * W) rec[threadIdx.x].item = -1;
     __syncthreads();
-    int64_t before = incl - mine, units = 0;
+    unsigned before = incl - mine, units = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
         if (i < warp) before += scan[i];
@@ -311,51 +310,52 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     // Equal runs for all blocks (a unit a warp at least) have to be joined across blocks; where there are few
     // items and none is long, a block for each is done sooner.
     const int64_t items = (int64_t)p.n_seqs * groups;
-    const bool by_item = items <= gridDim.x && (most + W - 1) / W <= units / ((int64_t)gridDim.x * W) + kJoinUnits;
-    const int blocks = by_item ? (int)items : (int)min((int64_t)gridDim.x, (units + W - 1) / W);
+    const bool by_item = items <= gridDim.x && (unsigned)((most + W - 1) / W) <= units / (gridDim.x * W) + kJoinUnits;
+    const int blocks = by_item ? (int)items : (int)min(gridDim.x, units / W + (units % W != 0));
     if ((int)blockIdx.x >= blocks) {
         if (threadIdx.x == 0) p.shared[blockIdx.x] = Shared{-1, 0};
         return;
     }
-    int64_t b_lo = 0, b_n;  // first unit of the block, and how many (unit numbers below count from b_lo)
-    if (by_item) {
-        const int s = blockIdx.x / groups;
-        b_n = open_span(p, s).n;
-        if (threadIdx.x < W) {
-            start_at[threadIdx.x].s = s;
-            start_at[threadIdx.x].g = blockIdx.x % groups;
-            start_at[threadIdx.x].c = (int)(b_n * threadIdx.x / W);
-        }
-    } else {
-        b_lo = units * blockIdx.x / blocks;
-        b_n = units * (blockIdx.x + 1) / blocks - b_lo;
-        for (int i = 0; i < W; ++i) {
-            const int64_t b = b_lo + b_n * i / W;
-            if (b < before || b >= before + mine) continue;
-            int64_t at = before;
-            for (int s = s_lo; s < s_hi; ++s) {
-                const int n = open_span(p, s).n + kItemUnits;
-                if (b < at + (int64_t)n * groups) {
-                    const int in = (int)(b - at);
-                    start_at[i].s = s;
-                    start_at[i].g = in / n;
-                    start_at[i].c = in % n;
-                    break;
-                }
-                at += (int64_t)n * groups;
-            }
-        }
-    }
+    units_before[threadIdx.x] = before;
     __syncthreads();
-    int64_t u_lo = b_n * warp / W;
-    const int64_t u_hi = b_n * (warp + 1) / W;
+    unsigned b_lo = 0;
+    int b_n;  // first unit of the block, and how many (unit numbers below count from b_lo)
+    if (by_item) {
+        b_n = open_span(p, blockIdx.x / groups).n;
+    } else {
+        const unsigned q = units / blocks, rest = units - q * blocks;  // the first `rest` blocks have one more
+        b_lo = q * blockIdx.x + min(blockIdx.x, rest);
+        b_n = (int)(q + (blockIdx.x < rest));
+    }
+    int u_lo = (int)((int64_t)b_n * warp / W);
+    const int u_hi = (int)((int64_t)b_n * (warp + 1) / W);
     Place next;  // to be loaded
     if (u_lo < u_hi) {
-        next.s = start_at[warp].s;
-        next.kvh = start_at[warp].g / p.tiles;
-        next.tile = start_at[warp].g - next.kvh * p.tiles;
-        next.c = start_at[warp].c;
-        next.x = open_span(p, next.s);
+        int at = 0;  // kv head and tile
+        if (by_item) {
+            next.s = blockIdx.x / groups;
+            at = blockIdx.x - next.s * groups;
+            next.c = u_lo;
+            next.x = open_span(p, next.s);
+        } else {
+            // the thread whose sequences have the run's first unit, and among them the one that has it
+            const unsigned b = b_lo + u_lo;
+            int begun = 0;
+#pragma unroll
+            for (int i = 0; i < W; ++i) begun += units_before[i * 32 + lane] <= b;
+            const int t = __reduce_add_sync(0xffffffffu, begun) - 1;
+            unsigned in = b - units_before[t];
+            next.s = t * per;
+            next.x = open_span(p, next.s);
+            while (in >= (unsigned)(next.x.n + kItemUnits) * groups) {
+                in -= (unsigned)(next.x.n + kItemUnits) * groups;
+                next.x = open_span(p, ++next.s);
+            }
+            at = (int)(in / (next.x.n + kItemUnits));
+            next.c = (int)(in - (unsigned)at * (next.x.n + kItemUnits));
+        }
+        next.kvh = at / p.tiles;
+        next.tile = at - next.kvh * p.tiles;
         if (next.c >= next.x.n) {  // in the item's empty units: on to the next item
             u_lo += next.x.n + kItemUnits - next.c;
             next.c = next.x.n - 1;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     if (u_lo < u_hi) {
         const uint32_t my_queue = smem_addr(queue) + warp * (S * STAGE);
         Place cur = next;  // to be computed
-        int64_t u_next = u_lo;
+        int u_next = u_lo;
 
         // Pages, fetched before they are needed: (paged) those of units pages_from + lane of the item, 32 at a
         // time, else those of token lane % 16 of the unit to be loaded next.
@@ -446,21 +446,21 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         };
         // q of the current item, asked for before its first keys (after them it would wait for them)
         float2 f[NH][2 * KS];
-        auto load_q = [&]() {
-            const int h0 = cur.kvh * p.group + cur.tile * H, nh = min(H, p.group - cur.tile * H);
+        auto load_q = [&](int s, int kvh, int tile) {
+            const int h0 = kvh * p.group + tile * H, nh = min(H, p.group - tile * H);
 #pragma unroll
             for (int h = 0; h < NH; ++h)
 #pragma unroll
                 for (int i = 0; i < 2 * KS; ++i) {
                     const int d = 8 * i + 2 * c4;
-                    const int64_t at = (int64_t)cur.s * p.qs + (int64_t)(h0 + r + 8 * h) * p.qhs + d;
+                    const int64_t at = (int64_t)s * p.qs + (int64_t)(h0 + r + 8 * h) * p.qhs + d;
                     f[h][i] = r + 8 * h < nh && d < p.dim && LEAN_SPAN(at, 2, p.q_extent, p.err)
                                   ? load_pair<(PARTS > 2)>(p.q, at, p.act)
                                   : make_float2(0.f, 0.f);
                 }
         };
-        if (EARLY_Q) load_q();
-#pragma unroll
+        if (EARLY_Q) load_q(cur.s, cur.kvh, cur.tile);
+#pragma unroll 1
         for (int i = 0; i < S - 1; ++i) load_unit(i);
 
         // ldmatrix rows of a lane: K, tokens 0-7 (8-15 from lane 16 on) and the even (odd) piece of a step; V,
@@ -474,12 +474,12 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         float acc[2 * KS][4], m[NH], l[NH], zs[NH];
         bool fresh = true;
         int stage = 0;
-        for (int64_t u = u_lo; u < u_hi;) {
+        for (int u = u_lo; u < u_hi;) {
             load_unit(stage == 0 ? S - 1 : stage - 1);
             const int h0 = cur.kvh * p.group + cur.tile * H, nh = min(H, p.group - cur.tile * H);
             if (fresh) {
                 fresh = false;
-                if (!EARLY_Q) load_q();
+                if (!EARLY_Q) load_q(cur.s, cur.kvh, cur.tile);
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     float top = 0.f;
@@ -531,6 +531,11 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                 for (int j = 0; j < 2 * KS; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+                if (AHEAD_Q && u + cur.x.n - cur.c + kItemUnits < u_hi) {  // another item follows
+                    const bool other_tile = cur.tile + 1 < p.tiles, other_head = other_tile || cur.kvh + 1 < p.hkv;
+                    load_q(other_head ? cur.s : cur.s + 1, other_tile ? cur.kvh : other_head ? cur.kvh + 1 : 0,
+                           other_tile ? cur.tile + 1 : 0);
+                }
             }
             cp_async_wait<S - 1>();
             __syncwarp();
@@ -622,10 +627,10 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
 
             // ---- the end of a group, or of the run
             const bool item_end = cur.c == cur.x.n - 1;
-            const int64_t u_then = u + (item_end ? 1 + kItemUnits : 1);
+            const int u_then = u + (item_end ? 1 + kItemUnits : 1);
             if (item_end || u_then >= u_hi) {
                 fresh = true;
-                const int64_t first = u - cur.c;
+                const int first = u - cur.c;
                 const bool whole = first >= u_lo && item_end, at_end = u_then >= u_hi;
                 // a part that others continue: the run's last in this warp's own queue (nothing is under way to
                 // it any more)
@@ -661,7 +666,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     q.first = first;
                 }
                 advance(p, cur);
-                if (EARLY_Q && !at_end) load_q();
+                if (EARLY_Q && !AHEAD_Q && !at_end) load_q(cur.s, cur.kvh, cur.tile);
             } else {
                 advance(p, cur);
             }
@@ -720,9 +725,10 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         if (leaders) {
             const Record q = rec[31 - __clz(leaders)];
             if (q.first >= 0 && q.first + q.n > b_n) {
-                const int64_t last = q.first + b_lo + q.n - 1;  // the last of its units, and the block that has it
-                x.item = q.item;
-                x.parts = (int)(((last + 1) * blocks - 1) / units) - (int)blockIdx.x + 1;
+                const unsigned last = q.first + b_lo + q.n - 1;  // the last of its units, and the block that has it
+                const unsigned n = units / blocks, rest = units - n * blocks;
+                const unsigned b = last < rest * (n + 1) ? last / (n + 1) : rest + (last - rest * (n + 1)) / n;
+                x = Shared{q.item, (int)(b - blockIdx.x) + 1};
             }
         }
         p.shared[blockIdx.x] = x;
@@ -856,6 +862,9 @@ extern "C" lean_status lean_paged_attention(const lean_attention_args *a, void *
         !step_aligned(a->out, 16) || !step_aligned(a->block_table, 4) || !step_aligned(a->seq_lens, 4) ||
         !step_aligned(a->lse, 4) || !step_aligned(a->workspace, 256))
         return LEAN_ERR_ALIGN;
+    const int64_t group = a->n_q_heads / a->n_kv_heads, tiles = group > 8 ? (group + 15) / 16 : 1;
+    if ((a->table_width * a->page_size / kUnit + 2 + kItemUnits) * a->n_seqs * a->n_kv_heads * tiles > UINT32_MAX)
+        return LEAN_ERR_SHAPE;  // units are counted in 32 bits
     if (a->workspace_bytes <
         lean_paged_attention_workspace_bytes(a->n_seqs, a->n_q_heads, a->n_kv_heads, a->head_dim))
         return LEAN_ERR_SHAPE;
@@ -883,8 +892,8 @@ extern "C" lean_status lean_paged_attention(const lean_attention_args *a, void *
     p.n_seqs = (int)a->n_seqs;
     p.hq = (int)a->n_q_heads;
     p.hkv = (int)a->n_kv_heads;
-    p.group = p.hq / p.hkv;
-    p.tiles = p.group > 8 ? (p.group + 15) / 16 : 1;
+    p.group = (int)group;
+    p.tiles = (int)tiles;
     p.dim = (int)a->head_dim;
     p.page = (int)a->page_size;
     p.paged = a->page_size % kUnit == 0;

@@ -221,7 +221,8 @@ lean_status lean_kv_pages(const lean_kv_pages_args *args, void *stream);
  * Results do not depend on timing.
  * LEAN_ERR_SHAPE: a size <= 0, heads that do not divide, head_dim not a multiple
  * of 8 or above 256, window < 0, table_width * page_size above 2^31 - 1, more
- * than 2^31 - 1 sequences x kv heads, or a workspace too small.  LEAN_ERR_ALIGN,
+ * than 2^31 - 1 sequences x heads, sequences x kv heads x table_width x page_size
+ * / 16 near 2^32 or above, or a workspace too small.  LEAN_ERR_ALIGN,
  * LEAN_ERR_NULL, LEAN_ERR_FORMAT as for the other calls (cache_dtype: LEAN_BF16
  * or LEAN_F16). */
 typedef struct {
