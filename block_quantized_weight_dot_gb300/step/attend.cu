@@ -234,6 +234,26 @@ constexpr float kSlack = 8.f;
 constexpr int kJoinUnits = 8;
 constexpr int kItemUnits = 4;
 
+// Parts added up: maximum, sum and outputs.
+struct Sums {
+    float top, sum;
+    float4 o;
+    __device__ __forceinline__ void clear() {
+        top = -CUDART_INF_F;
+        sum = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ void add(float2 ml, float4 v) {
+        const float now = fmaxf(top, ml.x), ref = now == -CUDART_INF_F ? 0.f : now;
+        const float old = ex2(top - ref), w = ex2(ml.x - ref);
+        top = now;
+        sum = fmaf(sum, old, w * ml.y);
+        o.x = fmaf(o.x, old, w * v.x);
+        o.y = fmaf(o.y, old, w * v.y);
+        o.z = fmaf(o.z, old, w * v.z);
+        o.w = fmaf(o.w, old, w * v.w);
+    }
+};
 struct Head {  // of an item: its sequence, first query head and number of heads
     int s, h0, nh;
 };
@@ -693,30 +713,21 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         const Record head = rec[i];
         const Head f = open_item(p, head.item, H);
         const int h = (j * 32 + lane) * 4 / DP, d = (j * 32 + lane) * 4 % DP;
-        float top = -CUDART_INF_F, sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        Sums t;
+        t.clear();
         while (members) {
             const int k = __ffs(members) - 1;
             members &= members - 1;
             const float *row = reinterpret_cast<const float *>(k & 1 ? tail_part + (k / 2 - warp) * (S * STAGE)
                                                                      : head_part + (int64_t)(k / 2 - warp) * (PF * 4)) + h * PO;
-            const float2 ml = *reinterpret_cast<const float2 *>(row);
-            const float4 v = *reinterpret_cast<const float4 *>(row + 4 + d);
-            const float now = fmaxf(top, ml.x), ref = now == -CUDART_INF_F ? 0.f : now;
-            const float old = ex2(top - ref), w = ex2(ml.x - ref);
-            top = now;
-            sum = fmaf(sum, old, w * ml.y);
-            o.x = fmaf(o.x, old, w * v.x);
-            o.y = fmaf(o.y, old, w * v.y);
-            o.z = fmaf(o.z, old, w * v.z);
-            o.w = fmaf(o.w, old, w * v.w);
+            t.add(*reinterpret_cast<const float2 *>(row), *reinterpret_cast<const float4 *>(row + 4 + d));
         }
         if (head.first >= 0 && head.first + head.n <= b_n) {
-            store_result(p, f, h, d, o, top, sum);
+            store_result(p, f, h, d, t.o, t.top, t.sum);
         } else {  // the block's part of the item that began before it, or of the one that goes on after it
             float *row = p.cta_parts + ((int64_t)blockIdx.x * 2 + (head.first < 0 ? 0 : 1)) * PF + h * PO;
-            *reinterpret_cast<float4 *>(row + 4 + d) = o;
-            if (d == 0) *reinterpret_cast<float2 *>(row) = make_float2(top, sum);
+            *reinterpret_cast<float4 *>(row + 4 + d) = t.o;
+            if (d == 0) *reinterpret_cast<float2 *>(row) = make_float2(t.top, t.sum);
         }
     }
     // The item that begins in this block and goes on in the next ones, for the kernel that adds its parts up.
@@ -735,60 +746,83 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     }
 }
 
-// The parts of items shared by blocks: a block for each 32 x 4 outputs of the item that begins in block blockIdx.x
-// / JOBS of the kernel before, if one does.  Its warps take the parts in turn, so that all are under way at once.
-constexpr int kSumWarps = 8, kSumParts = kAttMaxCtas / kSumWarps;
+// Parts of items shared by blocks, added up: 32 x 4 outputs of an item at a time, up to kAtOnce parts' loads under
+// way in a warp.  Items of few parts are taken by single warps, those of many by whole blocks, whose warps take the
+// parts in turn.
+constexpr int kSumWarps = 8, kAtOnce = 10;
 template <int H, int DP>
-__global__ void __launch_bounds__(kSumWarps * 32) attend_sum_kernel(const AttArgs p) {
+__global__ void __launch_bounds__(kSumWarps * 32) attend_sum_kernel(const AttArgs p, int blocks) {
     constexpr int JOBS = H * DP / 128, PF = part_floats(H, DP), PO = 4 + DP;
+    __shared__ Shared item[kAttMaxCtas];
+    __shared__ unsigned few_s[kSumWarps], many_s[kSumWarps];
     __shared__ float4 out_s[kSumWarps][32];
     __shared__ float2 ml_s[kSumWarps][32];
     step_begin();
-    const int b = blockIdx.x / JOBS, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const Shared x = p.shared[b];
-    if (x.item < 0) return;
-    const int e = (blockIdx.x % JOBS * 32 + lane) * 4, h = e / DP, d = e % DP;
-    float2 ml[kSumParts];
-    float4 v[kSumParts];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    Shared mine = {-1, 0};
+    if (threadIdx.x < blocks) item[threadIdx.x] = mine = p.shared[threadIdx.x];
+    const unsigned few = __ballot_sync(0xffffffffu, mine.item >= 0 && mine.parts <= kAtOnce);
+    const unsigned many = __ballot_sync(0xffffffffu, mine.parts > kAtOnce);
+    if (lane == 0) {
+        few_s[warp] = few;
+        many_s[warp] = many;
+    }
+    __syncthreads();
+    auto nth_block = [&](const unsigned *m, int n) {  // block whose bit is the n-th that is set, -1: there are fewer
+        for (int i = 0; i < kSumWarps; ++i) {
+            const int c = __popc(m[i]);
+            if (n < c) return 32 * i + nth_bit(m[i], n);
+            n -= c;
+        }
+        return -1;
+    };
+    Sums t;
+    auto take = [&](int b, int job, int from, int step) {  // parts from, from + step .. of the item that begins in block b
+        const int parts = item[b].parts, e = (job * 32 + lane) * 4;
+        const float *at = p.cta_parts + ((int64_t)b * 2) * PF + e / DP * PO;
+        t.clear();
+        for (int k0 = from; k0 < parts; k0 += kAtOnce * step) {
+            float2 ml[kAtOnce];
+            float4 v[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < kSumParts; ++i) {
-        const int k = warp + i * kSumWarps;
-        ml[i] = make_float2(-CUDART_INF_F, 0.f);
-        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k < x.parts) {
-            const float *row = p.cta_parts + ((int64_t)(b + k) * 2 + (k == 0)) * PF + h * PO;
-            ml[i] = *reinterpret_cast<const float2 *>(row);
-            v[i] = *reinterpret_cast<const float4 *>(row + 4 + d);
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int k = k0 + i * step;
+                if (k < parts) {
+                    const float *row = at + (int64_t)(k * 2 + (k == 0)) * PF;
+                    ml[i] = *reinterpret_cast<const float2 *>(row);
+                    v[i] = *reinterpret_cast<const float4 *>(row + 4 + e % DP);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (k0 + i * step < parts) t.add(ml[i], v[i]);
+        }
+    };
+    auto store = [&](int b, int job) {
+        const int e = (job * 32 + lane) * 4;
+        store_result(p, open_item(p, item[b].item, H), e / DP, e % DP, t.o, t.top, t.sum);
+    };
+    for (int job = blockIdx.x;; job += gridDim.x) {
+        const int b = nth_block(many_s, job / JOBS);
+        if (b < 0) break;
+        take(b, job % JOBS, warp, kSumWarps);
+        __syncthreads();
+        ml_s[warp][lane] = make_float2(t.top, t.sum);
+        out_s[warp][lane] = t.o;
+        __syncthreads();
+        if (warp == 0) {
+            t.clear();
+#pragma unroll
+            for (int i = 0; i < kSumWarps; ++i) t.add(ml_s[i][lane], out_s[i][lane]);
+            store(b, job % JOBS);
         }
     }
-    float top = -CUDART_INF_F, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float2 a, float4 u, float ref) {
-        const float w = ex2(a.x - ref);
-        sum = fmaf(w, a.y, sum);
-        o.x = fmaf(w, u.x, o.x);
-        o.y = fmaf(w, u.y, o.y);
-        o.z = fmaf(w, u.z, o.z);
-        o.w = fmaf(w, u.w, o.w);
-    };
-#pragma unroll
-    for (int i = 0; i < kSumParts; ++i) top = fmaxf(top, ml[i].x);
-    float ref = top == -CUDART_INF_F ? 0.f : top;
-#pragma unroll
-    for (int i = 0; i < kSumParts; ++i)
-        if (warp + i * kSumWarps < x.parts) add(ml[i], v[i], ref);
-    ml_s[warp][lane] = make_float2(top, sum);
-    out_s[warp][lane] = o;
-    __syncthreads();
-    if (warp > 0) return;
-    sum = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < kSumWarps; ++i) top = fmaxf(top, ml_s[i][lane].x);
-    ref = top == -CUDART_INF_F ? 0.f : top;
-#pragma unroll
-    for (int i = 0; i < kSumWarps; ++i) add(ml_s[i][lane], out_s[i][lane], ref);
-    store_result(p, open_item(p, x.item, H), h, d, o, top, sum);
+    for (int job = blockIdx.x + warp * gridDim.x;; job += gridDim.x * kSumWarps) {
+        const int b = nth_block(few_s, job / JOBS);
+        if (b < 0) break;
+        take(b, job % JOBS, 0, 1);
+        store(b, job % JOBS);
+    }
 }
 
 template <typename C, int DP, int PARTS, bool WIDE>
@@ -806,8 +840,7 @@ lean_status launch_attend(const AttArgs &p, int64_t flags, void *stream) {
     const bool by_item = (int64_t)p.n_seqs * p.hkv * p.tiles <= grid && (most + W - 1) / W <= kJoinUnits;
     if (st != LEAN_OK || grid == 1 || by_item) return st;
     constexpr int H = WIDE ? 16 : 8;
-    return step_launch(attend_sum_kernel<H, DP>, grid * (H * DP / 128), kSumWarps * 32, 0, LEAN_FLAG_EARLY_WEIGHTS,
-                       stream, p);
+    return step_launch(attend_sum_kernel<H, DP>, grid, kSumWarps * 32, 0, LEAN_FLAG_EARLY_WEIGHTS, stream, p, (int)grid);
 }
 template <typename C, int DP>
 lean_status pick_attend(const AttArgs &p, int64_t flags, void *stream) {
