@@ -8,17 +8,16 @@
 // logits come near the rate of exponentials, 16 a clock and SM).
 //
 //   - Units of 2 KB of a row; every warp of the GPU takes an equal run of them,
-//     whatever rows they belong to, and walks it without barriers, the next
-//     unit's loads under way while one is computed.  Maxima and sums are kept
-//     per lane and joined where a row ends.
-//   - Top alternatives: of every half unit the largest logit is kept, and of
-//     every lane the largest of each half.  The k-th largest of those 64 is a
-//     value that k logits of the row reach, so that only half units that reach
-//     it are read again (from L2) when the row ends; what reaches it there, a
-//     few more than k, is ranked by counting.  Cost does not depend on the order
-//     of the logits; ties go by the token id.
-//   - Rows shared by warps join through shared memory, rows shared by blocks
-//     through the workspace and a second kernel, launched early.
+//     whatever rows they belong to, and walks it alone, the next unit's loads
+//     under way while one is computed.  Maxima and sums are kept per lane and
+//     joined where a row or the run ends; what a warp has of a row goes to the
+//     workspace.
+//   - A second kernel, launched early, finishes the rows.  For the top
+//     alternatives the first one leaves every half unit's largest logit: the k
+//     half units with the largest ones (ties: the first) hold the row's k
+//     largest logits, so only they are read again, 1 KB each, and what reaches
+//     the k-th of the threads' largest is ranked by counting.  The cost does not
+//     depend on the order of the logits; ties go by the token id.
 #include <type_traits>
 
 #include "step_common.cuh"
@@ -28,15 +27,13 @@ using namespace lean;
 namespace {
 
 constexpr int kLpWarps = 8, kLpThreads = kLpWarps * 32, kLpCtas = 3;  // blocks an SM
-constexpr int kLpMaxCtas = 160 * kLpCtas;
-constexpr int kVecs = 4;            // 16-byte pieces of a lane in a unit
-constexpr int kUnitVecs = 32 * kVecs;
-constexpr int kHalves = 128;        // half units whose maxima a warp keeps before it takes their top logits
-constexpr int kList = 256;          // candidates of a warp
+constexpr int kLpMaxWarps = 160 * kLpCtas * kLpWarps;
+constexpr int kVecs = 4;  // 16-byte pieces of a lane in a unit
+constexpr int kUnitVecs = 32 * kVecs, kHalfVecs = kUnitVecs / 2;
 constexpr int kTop = LEAN_MAX_TOP;
+constexpr int kEndThreads = 128, kEndPieces = 10;  // of the second kernel; pieces of a thread in a round
 constexpr float kLowest = -3.402823466e38f;
-constexpr float kFar = 1e30f;       // a power of two of minus this is 0, and it is far from overflow
-constexpr int64_t kLpSharedBytes = 4096;  // what blocks share, per block
+constexpr float kFar = 1e30f;  // a power of two of minus this is 0, and it is far from overflow
 
 struct Entry {  // a logit and its token
     float v;
@@ -48,26 +45,20 @@ struct Stats {  // largest logit, sums relative to it, logits above the given to
     float m, s, w;
     int above;
 };
-struct Part {  // of a row: its first token's place does not matter, ids are the row's
-    Stats st;
-    int n;  // entries
-    int pad[3];
-    Entry top[kTop];
-};
-struct LpShared {  // a row that begins in a block and goes on in others (-1: none), and how many blocks it has
-    int row, parts;
-};
+#define LP_NONE (Entry{-CUDART_INF_F, INT32_MAX})  // no entry: beaten by every one
 
 struct LpArgs {
     const void *x;
     const int32_t *ids;
     float *logprobs, *entropy, *top_lp;
     int32_t *ranks, *top_ids;
-    LpShared *shared;
-    Part *parts;
+    Stats *runs;   // of a warp: of the row that began before it, and of the one that goes on after it
+    Stats *whole;  // of a row that lies in one warp's run
+    int *halves;   // [row][half unit]: largest logits, as ordered()
     int64_t stride;
     int rows, vocab, top_k;
-    int row_units, units;
+    int row_units;
+    unsigned units, warps, q, rest;  // a warp has q units, the first `rest` warps one more
     float scale, c;  // c = scale * log2 e
     float far;       // a reference m up to here has m c <= kFar
     float low;       // and one from here on (to far) makes 0 of what pair<CLAMP> makes of -inf
@@ -239,51 +230,6 @@ struct Row {
     }
 };
 
-// ---- a warp's candidates ---------------------------------------------------------------
-
-struct Candidates {
-    Entry *list, *best;  // kList, and kTop in order
-    int n, k;
-    float reach;  // candidates have to reach it,
-    float kth;    // and where k are known already (full), to exceed the last of them
-    bool full;
-
-    // the k largest of the list, in order, to best; *kept: how many
-    __device__ int rank(int lane) {
-        __syncwarp();
-        for (int i = lane; i < n; i += 32) {
-            const Entry mine = list[i];
-            int r = 0;
-            for (int j = 0; j < n; ++j) r += beats(list[j], mine);
-            if (r < k) best[r] = mine;
-        }
-        __syncwarp();
-        return n < k ? n : k;
-    }
-    __device__ void shrink(int lane) {
-        n = rank(lane);
-        for (int i = lane; i < n; i += 32) list[i] = best[i];
-        __syncwarp();
-        if (n == k) {
-            full = true;
-            kth = list[k - 1].v;
-        }
-    }
-    // candidates come in rising order of their ids, so that one equal to the k-th already known loses to it
-    __device__ bool wants(float v) const { return v >= reach && v > (full ? kth : -CUDART_INF_F); }
-    __device__ void push(int lane, bool mine, float v, int id) {
-        unsigned m = __ballot_sync(0xffffffffu, mine);
-        if (m == 0) return;
-        if (n + 32 > kList) {
-            shrink(lane);
-            mine = mine && wants(v);
-            m = __ballot_sync(0xffffffffu, mine);
-        }
-        if (mine) list[n + __popc(m & ((1u << lane) - 1))] = Entry{v, id};
-        n += __popc(m);
-    }
-};
-
 __device__ __forceinline__ float log_prob(const LpArgs &p, float x, const Stats &a) {
     const float t = place_of(p, x, a.m);
     // (a logit near the lowest of fp32: beyond it in powers of two, not in powers of e)
@@ -343,323 +289,275 @@ __device__ __forceinline__ void add_words(const LpArgs &p, const uint32_t (&w)[4
     a.w += v.x + v.y;
 }
 
-struct LpRecord {
-    int row, first;  // row (-1: none), and its first unit counted from the block's first one
-};
-
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads, kLpCtas) logprobs_kernel(const LpArgs p, int blocks) {
-    constexpr int E = Lane<T>::kPer, WORDS = 4 * kVecs;
-    __shared__ Entry lists[kLpWarps][kList];
-    __shared__ Entry bests[kLpWarps][kTop];
-    __shared__ int halves[kLpWarps][kHalves];
-    __shared__ Part part_s[2 * kLpWarps];
-    __shared__ LpRecord rec[2 * kLpWarps];
-    step_begin();
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    if (threadIdx.x < 2 * kLpWarps) rec[threadIdx.x].row = -1;
-    __syncthreads();
-    // equal runs of units
-    const unsigned q = (unsigned)p.units / blocks, rest = (unsigned)p.units - q * blocks;
-    const unsigned b_lo = q * blockIdx.x + min(blockIdx.x, rest);
-    const int b_n = (int)(q + (blockIdx.x < rest));
-    const int u_lo = (int)((int64_t)b_n * warp / kLpWarps), u_hi = (int)((int64_t)b_n * (warp + 1) / kLpWarps);
-    const bool tops = p.top_k > 0;
-
-    if (u_lo < u_hi) {
-        int row = (int)((b_lo + u_lo) / p.row_units), c = (int)((b_lo + u_lo) - (unsigned)row * p.row_units);
-        Row<T> at(p, row);
-        auto load = [&](const Row<T> &from, int unit, uint4 (&v)[kVecs]) {
-            const int v0 = unit * kUnitVecs + lane;
-            // (all of a unit inside the row: no piece needs a look)
-            if (v0 - lane > 0 && (v0 - lane + kUnitVecs) * E - from.before <= p.vocab) {
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j)
-                    if (LEAN_SPAN((int64_t)(v0 + 32 * j) * E - from.before, E, p.vocab, p.err))
-                        v[j] = __ldg(reinterpret_cast<const uint4 *>(from.base) + v0 + 32 * j);
-            } else {
-#pragma unroll
-                for (int j = 0; j < kVecs; ++j) v[j] = from.load(p, v0 + 32 * j);
-            }
-        };
-        uint4 next[kVecs];
-        load(at, c, next);
-        Stats a;
-        float given = 0.f, lane_max[2];
-        uint32_t given2 = 0;
-        Candidates cand;
-        cand.list = lists[warp];
-        cand.best = bests[warp];
-        cand.k = p.top_k;
-        int taken = 0;  // unit of the row from which half maxima are kept
-        bool fresh = true;
-        for (int u = u_lo; u < u_hi; ++u) {
-            if (fresh) {
-                fresh = false;
-                a = Stats{kLowest, 0.f, 0.f, 0};
-                lane_max[0] = lane_max[1] = -CUDART_INF_F;
-                cand.n = 0;
-                cand.full = false;
-                cand.reach = -CUDART_INF_F;
-                taken = c;
-                given = CUDART_INF_F;  // nothing is above it
-                if (p.ids) {
-                    const int id = p.ids[row];
-                    if (id >= 0 && id < p.vocab) given = to_f(static_cast<const T *>(p.x)[(int64_t)row * p.stride + id]);
-                    else if (lane == 0) atomicOr(p.err, kErrTokenId);
-                }
-                given2 = Lane<T>::twice(given);
-            }
-            uint32_t w[WORDS];
-#pragma unroll
-            for (int j = 0; j < kVecs; ++j) {
-                w[4 * j] = next[j].x;
-                w[4 * j + 1] = next[j].y;
-                w[4 * j + 2] = next[j].z;
-                w[4 * j + 3] = next[j].w;
-            }
-            const bool row_end = c == p.row_units - 1, at_end = u == u_hi - 1;
-            if (!at_end) {
-                if (row_end) at = Row<T>(p, row + 1);
-                load(at, row_end ? 0 : c + 1, next);
-            }
-            const float top0 = Lane<T>::largest(w, WORDS / 2), top1 = Lane<T>::largest(w + WORDS / 2, WORDS / 2);
-            const float m = fmaxf(a.m, fmaxf(top0, top1));
-            if (p.ranks) a.above += Lane<T>::above(w, WORDS, given, given2);
-            move_to(p, a, m);
-            if (__any_sync(0xffffffffu, !(m >= p.low && m <= p.far))) add_words<T, true>(p, w, a);
-            else add_words<T, false>(p, w, a);
-            if (tops) {
-                lane_max[0] = fmaxf(lane_max[0], top0);
-                lane_max[1] = fmaxf(lane_max[1], top1);
-                const int h0 = __reduce_max_sync(0xffffffffu, ordered(top0)), h1 = __reduce_max_sync(0xffffffffu, ordered(top1));
-                if (lane < 2) halves[warp][2 * (c - taken) + lane] = lane ? h1 : h0;
-                if (row_end || at_end || c - taken == kHalves / 2 - 1) {
-                    // the k-th largest of the lanes' 64 maxima, bit by bit; -inf where fewer lanes have any
-                    const int o0 = ordered(lane_max[0]), o1 = ordered(lane_max[1]), none = ordered(-CUDART_INF_F);
-                    unsigned t = 0;  // order of unsigned numbers: the sign turned round
-#pragma unroll 1
-                    for (unsigned bit = 1u << 31; bit; bit >>= 1) {
-                        const unsigned try_ = t | bit;
-                        const int n = __popc(__ballot_sync(0xffffffffu, ((unsigned)o0 ^ 0x80000000u) >= try_)) +
-                                      __popc(__ballot_sync(0xffffffffu, ((unsigned)o1 ^ 0x80000000u) >= try_));
-                        if (n >= p.top_k) t = try_;
-                    }
-                    const int reach = max((int)(t ^ 0x80000000u), none);
-                    cand.reach = fmaxf(cand.reach, unordered(reach));
-                    __syncwarp();
-                    // the half units that reach it, again, in their order
-                    const int n_half = 2 * (c - taken + 1);
-                    const Row<T> self(p, row);
-                    for (int i0 = 0; i0 < n_half; i0 += 32) {
-                        const int hm = i0 + lane < n_half ? halves[warp][i0 + lane] : none;
-                        unsigned todo = __ballot_sync(0xffffffffu, hm > none && hm >= ordered(cand.reach));
-                        while (todo) {
-                            const int i = i0 + __ffs(todo) - 1;
-                            todo &= todo - 1;
-                            const int v0 = taken * kUnitVecs + i * (kUnitVecs / 2) + lane;
-                            uint4 r[kVecs / 2];
-#pragma unroll
-                            for (int j = 0; j < kVecs / 2; ++j) r[j] = self.load(p, v0 + 32 * j);
-#pragma unroll
-                            for (int j = 0; j < kVecs / 2; ++j) {
-                                const uint32_t x[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
-                                // whether any lane has a candidate among its pieces at all
-                                if (!__any_sync(0xffffffffu, cand.wants(Lane<T>::largest(x, 4)))) continue;
-                                // ids rise from lane to lane and within a lane, so a lane's all go in before the next's
-                                int mine = 0;
-#pragma unroll
-                                for (int e = 0; e < E; ++e) mine |= (int)cand.wants(Lane<T>::get(x[e * 4 / E], e & 1)) << e;
-                                for (unsigned lanes = __ballot_sync(0xffffffffu, mine != 0); lanes; lanes &= lanes - 1) {
-                                    const int l = __ffs(lanes) - 1;
-                                    const int its = __shfl_sync(0xffffffffu, mine, l);
-#pragma unroll
-                                    for (int e = 0; e < E; ++e) {
-                                        if (!(its >> e & 1)) continue;
-                                        const float v = Lane<T>::get(x[e * 4 / E], e & 1);
-                                        cand.push(lane, lane == l && cand.wants(v), v, (v0 + 32 * j) * E - self.before + e);
-                                    }
-                                }
-                            }
-                        }
-                    }
-                    taken = c + 1;
-                    cand.shrink(lane);
-                }
-            }
-            if (row_end || at_end) {
-                fresh = true;
-#pragma unroll
-                for (int o = 16; o; o >>= 1) join(p, a, shuffle(a, o));
-                const int first = u - c;
-                const int n = tops ? cand.n : 0;
-                if (first >= u_lo && row_end) {
-                    write_row(p, row, a, cand.list, n, lane, 32);
-                    if (lane == 0) write_given<T>(p, row, a);
-                } else {
-                    Part &x = part_s[2 * warp + at_end];
-                    for (int i = lane; i < n; i += 32) x.top[i] = cand.list[i];
-                    if (lane == 0) {
-                        x.st = a;
-                        x.n = n;
-                        rec[2 * warp + at_end] = LpRecord{row, first};
-                    }
-                }
-                __syncwarp();
-            }
-            c = row_end ? 0 : c + 1;
-            row += row_end;
-        }
-    }
-    __syncthreads();
-
-    // ---- rows shared by warps: record by record, the whole block on each row
-    Entry *all = lists[0];  // 2048 entries
-    static_assert(kLpWarps * kList >= 2 * kLpWarps * kTop, "room for all records' entries");
-    LpShared goes_on = {-1, 0};
-    for (int i = 0; i < 2 * kLpWarps;) {
-        const LpRecord head = rec[i];
-        if (head.row < 0) {
-            ++i;
-            continue;
-        }
-        int end = i + 1;
-        while (end < 2 * kLpWarps && (rec[end].row < 0 || rec[end].row == head.row)) ++end;
-        Stats a = part_s[i].st;
-        int n = 0;
-        for (int k = i; k < end; ++k) {
-            if (rec[k].row < 0) continue;
-            if (k > i) join(p, a, part_s[k].st);
-            const int more = part_s[k].n;
-            for (int e = threadIdx.x; e < more; e += kLpThreads) all[n + e] = part_s[k].top[e];
-            n += more;
-        }
-        __syncthreads();
-        Entry *best = bests[0];
-        for (int e = threadIdx.x; e < n; e += kLpThreads) {
-            const Entry mine = all[e];
-            int r = 0;
-            for (int k = 0; k < n; ++k) r += beats(all[k], mine);
-            if (r < p.top_k) best[r] = mine;
-        }
-        __syncthreads();
-        n = min(n, p.top_k);
-        const bool whole = head.first >= 0 && head.first + p.row_units <= b_n;
-        if (whole) {
-            write_row(p, head.row, a, best, n, threadIdx.x, kLpThreads);
-            if (threadIdx.x == 0) write_given<T>(p, head.row, a);
-        } else {
-            Part &x = p.parts[blockIdx.x * 2 + (head.first < 0 ? 0 : 1)];
-            for (int e = threadIdx.x; e < n; e += kLpThreads) x.top[e] = best[e];
-            if (threadIdx.x == 0) {
-                x.st = a;
-                x.n = n;
-            }
-            if (head.first >= 0) {
-                const unsigned last = b_lo + head.first + p.row_units - 1;
-                const unsigned b = last < rest * (q + 1) ? last / (q + 1) : rest + (last - rest * (q + 1)) / q;
-                goes_on = LpShared{head.row, (int)(b - blockIdx.x) + 1};
-            }
-        }
-        __syncthreads();
-        i = end;
-    }
-    if (threadIdx.x == 0) p.shared[blockIdx.x] = goes_on;
+// first unit of warp g, and the warp that has unit u
+__device__ __forceinline__ unsigned first_unit(const LpArgs &p, unsigned g) { return p.q * g + min(g, p.rest); }
+__device__ __forceinline__ unsigned warp_of(const LpArgs &p, unsigned u) {
+    const unsigned more = p.rest * (p.q + 1);
+    return u < more ? u / (p.q + 1) : p.rest + (u - more) / p.q;
 }
 
-// Rows shared by blocks: a block for each row that begins in block blockIdx.x of the kernel before and goes on.
-constexpr int kMostCand = 4096;  // k parts' entries at most, see below
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads) logprobs_sum_kernel(const LpArgs p) {
-    __shared__ Entry list[kMostCand];
-    __shared__ Entry best[kTop], firsts[kLpMaxCtas];
-    __shared__ Stats stats[kLpWarps];
-    __shared__ Entry least_s;
-    __shared__ int n_s;
+template <typename T, bool TOPS>
+__global__ void __launch_bounds__(kLpThreads, kLpCtas) logprobs_kernel(const LpArgs p) {
+    constexpr int E = Lane<T>::kPer, WORDS = 4 * kVecs;
     step_begin();
-    const LpShared x = p.shared[blockIdx.x];
-    if (x.row < 0) return;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    auto part = [&](int k) -> const Part & { return p.parts[(blockIdx.x + k) * 2 + (k == 0)]; };
-    if (threadIdx.x == 0) {
-        least_s = Entry{-CUDART_INF_F, INT32_MAX};
-        n_s = 0;
-    }
-    Stats a = {kLowest, 0.f, 0.f, 0};
-    for (int k = threadIdx.x; k < x.parts; k += kLpThreads) {
-        const Part &y = part(k);
-        const int n = y.n;
-        firsts[k] = n > 0 && p.top_k > 0 ? y.top[0] : Entry{-CUDART_INF_F, INT32_MAX};
-        join(p, a, y.st);
-    }
+    const int lane = threadIdx.x % 32;
+    const unsigned g = blockIdx.x * kLpWarps + threadIdx.x / 32;
+    if (g >= p.warps) return;
+    const unsigned lo = first_unit(p, g);
+    const int n = (int)(first_unit(p, g + 1) - lo);
+    int row = (int)(lo / p.row_units), c = (int)(lo - (unsigned)row * p.row_units);
+    Row<T> at(p, row);
+    auto load = [&](const Row<T> &from, int unit, uint4 (&v)[kVecs]) {
+        const int v0 = unit * kUnitVecs + lane;
+        // (all of a unit inside the row: no piece needs a look)
+        if (v0 - lane > 0 && (v0 - lane + kUnitVecs) * E - from.before <= p.vocab) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) join(p, a, shuffle(a, o));
-    if (lane == 0) stats[warp] = a;
-    __syncthreads();
-    a = stats[0];
-    for (int i = 1; i < kLpWarps; ++i) join(p, a, stats[i]);
-    int n = 0;
-    if (p.top_k > 0) {
-        // the k-th of the parts' first entries: k entries are as good, so no other one counts (at most the k parts
-        // that are as good have any: k * k entries)
-        for (int k = threadIdx.x; k < x.parts; k += kLpThreads) {
-            const Entry mine = firsts[k];
-            int r = 0;
-            for (int j = 0; j < x.parts; ++j) r += beats(firsts[j], mine);
-            if (r == p.top_k - 1 && mine.id != INT32_MAX) least_s = mine;
+            for (int j = 0; j < kVecs; ++j)
+                if (LEAN_SPAN((int64_t)(v0 + 32 * j) * E - from.before, E, p.vocab, p.err))
+                    v[j] = __ldg(reinterpret_cast<const uint4 *>(from.base) + v0 + 32 * j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j) v[j] = from.load(p, v0 + 32 * j);
         }
-        __syncthreads();
-        const Entry least = least_s;
-        for (int e = threadIdx.x; e < x.parts * p.top_k; e += kLpThreads) {
-            const int k = e / p.top_k, i = e - k * p.top_k;
-            if (beats(least, firsts[k]) || firsts[k].id == INT32_MAX) continue;
-            const Part &y = part(k);
-            if (i >= y.n) continue;
-            const Entry mine = y.top[i];
-            if (!beats(least, mine)) {
-                const int to = atomicAdd(&n_s, 1);
-                if (to < kMostCand) list[to] = mine;
+    };
+    uint4 next[kVecs];
+    load(at, c, next);
+    Stats a;
+    float given = 0.f;
+    uint32_t given2 = 0;
+    bool fresh = true, began_here = c == 0;
+    for (int i = 0; i < n; ++i) {
+        if (fresh) {
+            fresh = false;
+            a = Stats{kLowest, 0.f, 0.f, 0};
+            given = CUDART_INF_F;  // nothing is above it
+            if (p.ids) {
+                const int id = p.ids[row];
+                if (id >= 0 && id < p.vocab) given = to_f(static_cast<const T *>(p.x)[(int64_t)row * p.stride + id]);
+                else if (lane == 0) atomicOr(p.err, kErrTokenId);
             }
+            given2 = Lane<T>::twice(given);
         }
-        __syncthreads();
-        n = min(n_s, kMostCand);
-        for (int e = threadIdx.x; e < n; e += kLpThreads) {
-            const Entry mine = list[e];
-            int r = 0;
-            for (int k = 0; k < n && r < p.top_k; ++k) r += beats(list[k], mine);
-            if (r < p.top_k) best[r] = mine;
+        uint32_t w[WORDS];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            w[4 * j] = next[j].x;
+            w[4 * j + 1] = next[j].y;
+            w[4 * j + 2] = next[j].z;
+            w[4 * j + 3] = next[j].w;
         }
-        __syncthreads();
-        n = min(n, p.top_k);
+        const bool row_end = c == p.row_units - 1, at_end = i == n - 1;
+        if (!at_end) {
+            if (row_end) at = Row<T>(p, row + 1);
+            load(at, row_end ? 0 : c + 1, next);
+        }
+        const float top0 = Lane<T>::largest(w, WORDS / 2), top1 = Lane<T>::largest(w + WORDS / 2, WORDS / 2);
+        const float m = fmaxf(a.m, fmaxf(top0, top1));
+        if (p.ranks) a.above += Lane<T>::above(w, WORDS, given, given2);
+        move_to(p, a, m);
+        if (__any_sync(0xffffffffu, !(m >= p.low && m <= p.far))) add_words<T, true>(p, w, a);
+        else add_words<T, false>(p, w, a);
+        if (TOPS) {
+            // (a lane that has only NaN: -inf)
+            const int h0 = __reduce_max_sync(0xffffffffu, ordered(fmaxf(top0, -CUDART_INF_F)));
+            const int h1 = __reduce_max_sync(0xffffffffu, ordered(fmaxf(top1, -CUDART_INF_F)));
+            if (lane == 0) *reinterpret_cast<int2 *>(p.halves + ((int64_t)row * p.row_units + c) * 2) = make_int2(h0, h1);
+        }
+        if (row_end || at_end) {
+            fresh = true;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) join(p, a, shuffle(a, o));
+            if (lane == 0) {
+                if (!began_here) {
+                    p.runs[2 * g] = a;
+                } else if (!row_end) {
+                    p.runs[2 * g + 1] = a;
+                } else if (TOPS) {
+                    p.whole[row] = a;
+                } else {
+                    write_row(p, row, a, nullptr, 0, 0, 1);
+                    write_given<T>(p, row, a);
+                }
+            }
+            began_here = true;
+        }
+        c = row_end ? 0 : c + 1;
+        row += row_end;
     }
-    write_row(p, x.row, a, best, n, threadIdx.x, kLpThreads);
-    if (threadIdx.x == 0) write_given<T>(p, x.row, a);
+}
+
+// The order of entries as one number: the greater beats.
+__device__ __forceinline__ unsigned long long key_of(const Entry &e) {
+    return (unsigned long long)((unsigned)ordered(e.v) ^ 0x80000000u) << 32 | (unsigned)(INT32_MAX - e.id);
+}
+
+// The k best of all threads' entries, in order, to best; how many there are.  `mine`: the thread's best; each(f) calls f
+// with all of its entries (and may leave out those that mine does not beat or equal).  Entries at -inf are none.  k
+// threads' bests are as good as the k-th of them, so that only entries that it does not beat count, and only k threads
+// have any.  list: room for n entries that are there already, and all of k threads.
+struct Pick {
+    alignas(16) unsigned long long keys[kEndThreads];
+    unsigned long long least;
+    int n;
+};
+template <typename F>
+__device__ __forceinline__ int pick_best(Pick &sh, Entry *list, int n, Entry *best, int k, const Entry &mine, F each) {
+    const unsigned long long key = key_of(mine), none = key_of(Entry{-CUDART_INF_F, 0}) | 0xffffffffu;
+    sh.keys[threadIdx.x] = key;
+    if (threadIdx.x == 0) sh.n = n;
+    __syncthreads();
+    // (keys of threads without an entry are equal: told apart by the thread)
+    int r = 0;
+#pragma unroll 16
+    for (int i = 0; i < kEndThreads; i += 2) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(sh.keys + i);
+        r += q.x > key || (q.x == key && i < (int)threadIdx.x);
+        r += q.y > key || (q.y == key && i + 1 < (int)threadIdx.x);
+    }
+    if (r == k - 1) sh.least = max(key, none + 1);
+    __syncthreads();
+    const unsigned long long least = sh.least;
+    if (key >= least)
+        each([&](const Entry &e) {
+            if (key_of(e) >= least && e.v <= CUDART_INF_F) list[atomicAdd(&sh.n, 1)] = e;  // (NaN is none either)
+        });
+    __syncthreads();
+    n = sh.n;
+    for (int i = threadIdx.x; i < n; i += kEndThreads) {
+        const Entry e = list[i];
+        int q = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) q += beats(list[j], e);
+        if (q < k) best[q] = e;
+    }
+    __syncthreads();
+    return n < k ? n : k;
+}
+
+// The rows' ends: sums joined, top logits found.  TOPS: a block per row; else a block per warp of the kernel before,
+// for the row that begins in its run and goes on after it.
+template <typename T, bool TOPS>
+__global__ void __launch_bounds__(kEndThreads) logprobs_end_kernel(const LpArgs p) {
+    constexpr int E = Lane<T>::kPer, W = kEndThreads / 32;
+    extern __shared__ __align__(16) uint8_t list_raw[];  // candidates: of k threads at most, and the k so far
+    Entry *list = reinterpret_cast<Entry *>(list_raw);
+    __shared__ Entry best[kTop];
+    __shared__ int picked[kTop];
+    __shared__ Stats stats[W];
+    __shared__ Pick pick;
+    step_begin();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n_half = 2 * p.row_units, k = p.top_k;
+    int row = blockIdx.x;
+    unsigned u0 = (unsigned)row * p.row_units;
+    if (!TOPS) {
+        const unsigned lo = first_unit(p, blockIdx.x), hi = first_unit(p, blockIdx.x + 1);
+        row = (int)((hi - 1) / p.row_units);
+        u0 = (unsigned)row * p.row_units;
+        if (u0 < lo || u0 + p.row_units <= hi) return;
+    }
+    const unsigned g0 = warp_of(p, u0), g1 = warp_of(p, u0 + p.row_units - 1);
+    Stats a = {kLowest, 0.f, 0.f, 0};
+    if (g0 == g1) {
+        a = p.whole[row];
+    } else {
+        for (unsigned i = g0 + threadIdx.x; i <= g1; i += kEndThreads) join(p, a, p.runs[2 * i + (i == g0)]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) join(p, a, shuffle(a, o));
+        if (lane == 0) stats[warp] = a;
+    }
+    __syncthreads();
+    if (g0 != g1) {
+        a = stats[0];
+        for (int i = 1; i < W; ++i) join(p, a, stats[i]);
+    }
+    int n = 0;
+    if (TOPS) {
+        // the k half units with the largest maxima, equal ones in their order
+        const int *halves = p.halves + (int64_t)row * n_half;
+        Entry mine = LP_NONE;
+        for (int i = threadIdx.x; i < n_half; i += kEndThreads) {
+            const float v = unordered(halves[i]);
+            if (v > mine.v) mine = Entry{v, i};
+        }
+        const int n_picked = pick_best(pick, list, 0, best, k, mine, [&](auto f) {
+            for (int i = threadIdx.x; i < n_half; i += kEndThreads) f(Entry{unordered(halves[i]), i});
+        });
+        if (threadIdx.x < n_picked) picked[threadIdx.x] = best[threadIdx.x].id;
+        __syncthreads();
+        // their logits, in rounds of kEndPieces pieces a thread, the best so far carried on
+        const int pieces = n_picked * kHalfVecs;
+        const Row<T> at(p, row);
+        for (int from = 0; from < pieces; from += kEndPieces * kEndThreads) {
+            uint4 v[kEndPieces];
+            int id[kEndPieces];
+            mine = LP_NONE;
+#pragma unroll
+            for (int j = 0; j < kEndPieces; ++j) {
+                const int i = from + j * kEndThreads + threadIdx.x;
+                if (i >= pieces) break;
+                const int piece = picked[i / kHalfVecs] * kHalfVecs + i % kHalfVecs;
+                id[j] = piece * E - at.before;
+                v[j] = at.load(p, piece);
+            }
+            auto each = [&](auto f) {
+#pragma unroll
+                for (int j = 0; j < kEndPieces; ++j) {
+                    if (from + j * kEndThreads + (int)threadIdx.x >= pieces) break;
+                    const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                    for (int e = 0; e < E; ++e) f(Entry{Lane<T>::get(x[e * 4 / E], e & 1), id[j] + e});
+                }
+            };
+            each([&](const Entry &e) {
+                if (beats(e, mine)) mine = e;
+            });
+            for (int i = threadIdx.x; i < n; i += kEndThreads) list[i] = best[i];
+            n = pick_best(pick, list, n, best, k, mine, each);
+        }
+    }
+    write_row(p, row, a, best, n, threadIdx.x, kEndThreads);
+    if (threadIdx.x == 0) write_given<T>(p, row, a);
+}
+
+// units of a row of 16-byte pieces, which may begin anywhere in one
+int64_t lp_row_units(int64_t vocab, int64_t size, bool aligned) {
+    const int64_t per = 16 / size;
+    return ((vocab + (aligned ? 0 : per - 1) + per - 1) / per + kUnitVecs - 1) / kUnitVecs;
 }
 
 template <typename T>
 lean_status launch_logprobs(LpArgs p, int64_t flags, void *stream) {
-    // pieces of a row that begins anywhere in one
-    const int64_t vecs = ((int64_t)p.vocab + 2 * Lane<T>::kPer - 2) / Lane<T>::kPer;
-    const bool aligned = (p.stride * sizeof(T)) % 16 == 0 && (uintptr_t)p.x % 16 == 0;
-    p.row_units = (int)(((aligned ? ((int64_t)p.vocab + Lane<T>::kPer - 1) / Lane<T>::kPer : vecs) + kUnitVecs - 1) / kUnitVecs);
+    p.row_units = (int)lp_row_units(p.vocab, sizeof(T), (p.stride * sizeof(T)) % 16 == 0 && (uintptr_t)p.x % 16 == 0);
     const int64_t units = (int64_t)p.rows * p.row_units;
     if (units > INT32_MAX) return LEAN_ERR_SHAPE;
-    p.units = (int)units;
+    p.units = (unsigned)units;
     // a unit a warp at least
-    const int64_t grid = std::min<int64_t>(std::min(step_sm_count() * kLpCtas, kLpMaxCtas), (units + kLpWarps - 1) / kLpWarps);
+    const int64_t grid = std::min<int64_t>(std::min(step_sm_count(), 160) * kLpCtas, (units + kLpWarps - 1) / kLpWarps);
+    p.warps = (unsigned)std::min<int64_t>(grid * kLpWarps, units);
+    p.q = p.units / p.warps;
+    p.rest = p.units % p.warps;
     // (the largest scales go by the far path always)
-    const float clamp = sizeof(T) == 2 && std::is_same<T, __half>::value ? -65504.f : -9.9e29f;
+    const float clamp = std::is_same<T, __half>::value ? -65504.f : -9.9e29f;
     p.low = p.c > 1e6f ? 3.4e38f : std::max(-p.far, clamp + 160.f / p.c);
-    const lean_status st = step_launch(logprobs_kernel<T>, grid, kLpThreads, 0, flags, stream, p, (int)grid);
-    if (st != LEAN_OK || grid == 1) return st;
-    return step_launch(logprobs_sum_kernel<T>, grid, kLpThreads, 0, LEAN_FLAG_EARLY_WEIGHTS, stream, p);
+    const bool tops = p.top_k > 0;
+    const lean_status st = tops ? step_launch(logprobs_kernel<T, true>, grid, kLpThreads, 0, flags, stream, p)
+                                : step_launch(logprobs_kernel<T, false>, grid, kLpThreads, 0, flags, stream, p);
+    if (st != LEAN_OK) return st;
+    if (!tops && p.warps == 1) return st;  // no row is shared
+    const int per_thread = std::max(kEndPieces * Lane<T>::kPer, (2 * p.row_units + kEndThreads - 1) / kEndThreads);
+    const size_t smem = tops ? sizeof(Entry) * p.top_k * (per_thread + 1) : 0;
+    return tops ? step_launch(logprobs_end_kernel<T, true>, p.rows, kEndThreads, smem, LEAN_FLAG_EARLY_WEIGHTS, stream, p)
+                : step_launch(logprobs_end_kernel<T, false>, p.warps, kEndThreads, smem, LEAN_FLAG_EARLY_WEIGHTS, stream, p);
 }
 
 }  // namespace
 
 extern "C" int64_t lean_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top_k) {
     if (rows <= 0 || rows > INT32_MAX || vocab < 1 || vocab > (1 << 20) || top_k < 0 || top_k > LEAN_MAX_TOP) return -1;
-    return kLpSharedBytes + (int64_t)kLpMaxCtas * 2 * sizeof(Part);
+    // sums of the warps' runs; with top logits, sums of every row and the largest logits of its half units (of 16-bit
+    // logits there are half as many)
+    const int64_t runs = (int64_t)kLpMaxWarps * 2 * sizeof(Stats);
+    return top_k == 0 ? runs : runs + rows * (int64_t)sizeof(Stats) + rows * lp_row_units(vocab, 4, false) * 2 * (int64_t)sizeof(int);
 }
 
 extern "C" lean_status lean_token_logprobs(const lean_logprobs_args *a, void *stream) {
@@ -684,8 +582,9 @@ extern "C" lean_status lean_token_logprobs(const lean_logprobs_args *a, void *st
     p.top_lp = a->top_logprobs;
     p.ranks = a->ranks;
     p.top_ids = a->top_ids;
-    p.shared = static_cast<LpShared *>(a->workspace);
-    p.parts = reinterpret_cast<Part *>(static_cast<uint8_t *>(a->workspace) + kLpSharedBytes);
+    p.runs = static_cast<Stats *>(a->workspace);
+    p.whole = p.runs + 2 * kLpMaxWarps;
+    p.halves = reinterpret_cast<int *>(p.whole + a->rows);
     p.stride = a->stride;
     p.rows = (int)a->rows;
     p.vocab = (int)a->vocab;
