@@ -31,7 +31,7 @@ constexpr int kLpMaxWarps = 160 * kLpCtas * kLpWarps;
 constexpr int kVecs = 4;  // 16-byte pieces of a lane in a unit
 constexpr int kUnitVecs = 32 * kVecs, kHalfVecs = kUnitVecs / 2;
 constexpr int kTop = LEAN_MAX_TOP;
-constexpr int kEndThreads = 128, kEndPieces = 10;  // of the second kernel; pieces of a thread in a round
+constexpr int kEndThreads = 128;  // of the second kernel
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar = 1e30f;  // a power of two of minus this is 0, and it is far from overflow
 
@@ -391,34 +391,48 @@ __device__ __forceinline__ unsigned long long key_of(const Entry &e) {
     return (unsigned long long)((unsigned)ordered(e.v) ^ 0x80000000u) << 32 | (unsigned)(INT32_MAX - e.id);
 }
 
-// The k best of all threads' entries, in order, to best; how many there are.  `mine`: the thread's best; each(f) calls f
-// with all of its entries (and may leave out those that mine does not beat or equal).  Entries at -inf are none.  k
-// threads' bests are as good as the k-th of them, so that only entries that it does not beat count, and only k threads
-// have any.  list: room for n entries that are there already, and all of k threads.
+// The k best of all threads' entries, in order, to best; how many there are.  `mine`: the thread's best; each(t, f)
+// calls f with all of its entries that reach t, and may call it with more.  Entries at -inf are none.  k threads' bests
+// are as good as the k-th of them, so that only entries that it does not beat count, and only k threads have any.
+// list: room for n entries that are there already, and all of k threads.
 struct Pick {
     alignas(16) unsigned long long keys[kEndThreads];
     unsigned long long least;
-    int n;
+    int kth, n;
 };
 template <typename F>
 __device__ __forceinline__ int pick_best(Pick &sh, Entry *list, int n, Entry *best, int k, const Entry &mine, F each) {
-    const unsigned long long key = key_of(mine), none = key_of(Entry{-CUDART_INF_F, 0}) | 0xffffffffu;
-    sh.keys[threadIdx.x] = key;
-    if (threadIdx.x == 0) sh.n = n;
-    __syncthreads();
-    // (keys of threads without an entry are equal: told apart by the thread)
-    int r = 0;
-#pragma unroll 16
-    for (int i = 0; i < kEndThreads; i += 2) {
-        const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(sh.keys + i);
-        r += q.x > key || (q.x == key && i < (int)threadIdx.x);
-        r += q.y > key || (q.y == key && i + 1 < (int)threadIdx.x);
+    const int none = ordered(-CUDART_INF_F), v = ordered(mine.v);
+    int *values = reinterpret_cast<int *>(sh.keys);
+    values[threadIdx.x] = v;
+    if (threadIdx.x == 0) {
+        sh.n = n;
+        sh.kth = INT32_MAX;
     }
-    if (r == k - 1) sh.least = max(key, none + 1);
     __syncthreads();
-    const unsigned long long least = sh.least;
-    if (key >= least)
-        each([&](const Entry &e) {
+    int r = 0;  // threads whose best is larger
+#pragma unroll 8
+    for (int i = 0; i < kEndThreads; i += 4) {
+        const int4 q = *reinterpret_cast<const int4 *>(values + i);
+        r += (q.x > v) + (q.y > v) + (q.z > v) + (q.w > v);
+    }
+    if (r < k) atomicMin(&sh.kth, v);
+    const int as_good = __syncthreads_count(r < k);
+    const int t = max(sh.kth, none + 1);  // (the k-th largest; of what is not -inf, the least)
+    // the lowest key that counts: all that reach t, unless more than k threads do
+    unsigned long long least = (unsigned long long)((unsigned)t ^ 0x80000000u) << 32;
+    if (as_good > k && sh.kth > none) {
+        const unsigned long long key = key_of(mine);
+        sh.keys[threadIdx.x] = key;
+        __syncthreads();
+        r = 0;
+        for (int i = 0; i < kEndThreads; ++i) r += sh.keys[i] > key || (sh.keys[i] == key && i < (int)threadIdx.x);
+        if (r == k - 1) sh.least = key;
+        __syncthreads();
+        least = sh.least;
+    }
+    if (v >= t)
+        each(unordered(t), [&](const Entry &e) {
             if (key_of(e) >= least && e.v <= CUDART_INF_F) list[atomicAdd(&sh.n, 1)] = e;  // (NaN is none either)
         });
     __syncthreads();
@@ -436,7 +450,7 @@ __device__ __forceinline__ int pick_best(Pick &sh, Entry *list, int n, Entry *be
 
 // The rows' ends: sums joined, top logits found.  TOPS: a block per row; else a block per warp of the kernel before,
 // for the row that begins in its run and goes on after it.
-template <typename T, bool TOPS>
+template <typename T, bool TOPS, int PIECES>
 __global__ void __launch_bounds__(kEndThreads) logprobs_end_kernel(const LpArgs p) {
     constexpr int E = Lane<T>::kPer, W = kEndThreads / 32;
     extern __shared__ __align__(16) uint8_t list_raw[];  // candidates: of k threads at most, and the k so far
@@ -479,38 +493,52 @@ __global__ void __launch_bounds__(kEndThreads) logprobs_end_kernel(const LpArgs 
             const float v = unordered(halves[i]);
             if (v > mine.v) mine = Entry{v, i};
         }
-        const int n_picked = pick_best(pick, list, 0, best, k, mine, [&](auto f) {
+        const int n_picked = pick_best(pick, list, 0, best, k, mine, [&](float, auto f) {
             for (int i = threadIdx.x; i < n_half; i += kEndThreads) f(Entry{unordered(halves[i]), i});
         });
         if (threadIdx.x < n_picked) picked[threadIdx.x] = best[threadIdx.x].id;
         __syncthreads();
-        // their logits, in rounds of kEndPieces pieces a thread, the best so far carried on
+        // their logits, in rounds of PIECES pieces a thread, the best so far carried on
         const int pieces = n_picked * kHalfVecs;
         const Row<T> at(p, row);
-        for (int from = 0; from < pieces; from += kEndPieces * kEndThreads) {
-            uint4 v[kEndPieces];
-            int id[kEndPieces];
+        for (int from = 0; from < pieces; from += PIECES * kEndThreads) {
+            uint4 v[PIECES];
+            int id[PIECES];
             mine = LP_NONE;
 #pragma unroll
-            for (int j = 0; j < kEndPieces; ++j) {
+            for (int j = 0; j < PIECES; ++j) {
                 const int i = from + j * kEndThreads + threadIdx.x;
                 if (i >= pieces) break;
                 const int piece = picked[i / kHalfVecs] * kHalfVecs + i % kHalfVecs;
                 id[j] = piece * E - at.before;
                 v[j] = at.load(p, piece);
             }
-            auto each = [&](auto f) {
+            auto each = [&](float t, auto f) {
 #pragma unroll
-                for (int j = 0; j < kEndPieces; ++j) {
+                for (int j = 0; j < PIECES; ++j) {
                     if (from + j * kEndThreads + (int)threadIdx.x >= pieces) break;
                     const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                    if (!(Lane<T>::largest(x, 4) >= t)) continue;
 #pragma unroll
                     for (int e = 0; e < E; ++e) f(Entry{Lane<T>::get(x[e * 4 / E], e & 1), id[j] + e});
                 }
             };
-            each([&](const Entry &e) {
-                if (beats(e, mine)) mine = e;
-            });
+#pragma unroll
+            for (int j = 0; j < PIECES; ++j) {
+                if (from + j * kEndThreads + (int)threadIdx.x >= pieces) break;
+                const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+                const float top = Lane<T>::largest(x, 4);
+                if (top > mine.v) {
+                    mine.v = top;
+#pragma unroll
+                    for (int e = E - 1; e >= 0; --e)
+                        if (Lane<T>::get(x[e * 4 / E], e & 1) == top) mine.id = id[j] + e;
+                } else if (top == mine.v) {  // (picked half units are in the order of their maxima: ids do not rise)
+#pragma unroll
+                    for (int e = E - 1; e >= 0; --e)
+                        if (Lane<T>::get(x[e * 4 / E], e & 1) == top) mine.id = min(mine.id, id[j] + e);
+                }
+            }
             for (int i = threadIdx.x; i < n; i += kEndThreads) list[i] = best[i];
             n = pick_best(pick, list, n, best, k, mine, each);
         }
@@ -544,10 +572,14 @@ lean_status launch_logprobs(LpArgs p, int64_t flags, void *stream) {
                                 : step_launch(logprobs_kernel<T, false>, grid, kLpThreads, 0, flags, stream, p);
     if (st != LEAN_OK) return st;
     if (!tops && p.warps == 1) return st;  // no row is shared
-    const int per_thread = std::max(kEndPieces * Lane<T>::kPer, (2 * p.row_units + kEndThreads - 1) / kEndThreads);
-    const size_t smem = tops ? sizeof(Entry) * p.top_k * (per_thread + 1) : 0;
-    return tops ? step_launch(logprobs_end_kernel<T, true>, p.rows, kEndThreads, smem, LEAN_FLAG_EARLY_WEIGHTS, stream, p)
-                : step_launch(logprobs_end_kernel<T, false>, p.warps, kEndThreads, smem, LEAN_FLAG_EARLY_WEIGHTS, stream, p);
+    if (!tops) return step_launch(logprobs_end_kernel<T, false, 1>, p.warps, kEndThreads, 0, LEAN_FLAG_EARLY_WEIGHTS, stream, p);
+    // pieces of a thread in a round: 4 take 8 half units at once, 10 take 20
+    auto end = [&](auto kern, int pieces) {
+        const int per_thread = std::max(pieces * Lane<T>::kPer, (2 * p.row_units + kEndThreads - 1) / kEndThreads);
+        return step_launch(kern, p.rows, kEndThreads, sizeof(Entry) * p.top_k * (per_thread + 1), LEAN_FLAG_EARLY_WEIGHTS,
+                           stream, p);
+    };
+    return p.top_k <= 8 ? end(logprobs_end_kernel<T, true, 4>, 4) : end(logprobs_end_kernel<T, true, 10>, 10);
 }
 
 }  // namespace
