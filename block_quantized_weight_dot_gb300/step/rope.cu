@@ -6,20 +6,22 @@
 // already gone.  (In fp32, p * freq alone is off by 0.004 radians at position
 // 100000.)  sincospif takes the fraction of a turn as it is.
 //
-// A block takes a few tokens: its threads first compute the tokens' cosines and
-// sines into shared memory, once for all heads, then run over (token, head,
-// piece), where a piece is V pairs: two runs of V elements (halves) or one of
-// 2 V (neighbours and the unrotated rest).  All traffic is 16-byte accesses at
-// V = 8 (4 for fp32) and every element moves once, so HBM bounds it.
+// A block takes a few tokens: their cosines and sines go to shared memory, once
+// for all heads.  A thread has one piece of one head, for all of the block's
+// tokens (its addresses then only step by the tokens' strides), where a piece is
+// V pairs: two runs of V elements (halves) or one of 2 V (neighbours and the
+// unrotated rest).  All traffic is 16-byte accesses at V = 8 (4 for fp32), four
+// tokens' loads at a time, the first ones before the angles are computed; every
+// element moves once, so HBM bounds it.
 #include "step_common.cuh"
 
 using namespace lean;
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxThreads = 384;
 constexpr int kRopeMaxDim = 512;
-constexpr int kRopeMaxTokens = 16;  // of a block
+constexpr int kRopeMaxTokens = 64;  // of a block
 
 struct RopeArgs {
     const void *q, *k, *v;
@@ -37,28 +39,153 @@ struct RopeArgs {
     unsigned *err;
 };
 
-template <typename A, int V>
-__device__ __forceinline__ void load_f(const A *p, float *f) {
-    const Vec<A, V> v = load_vec<A, V>(p);
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = to_f(v.v[i]);
-}
 template <int V>
 __device__ __forceinline__ void store_cache(void *base, int64_t at, const float *f, int bf16) {
     if (bf16) store_vec<__nv_bfloat16, V>(static_cast<__nv_bfloat16 *>(base) + at, f);
     else store_vec<__half, V>(static_cast<__half *>(base) + at, f);
 }
 
+// V elements as they lie in memory, in registers.
+template <typename A, int V>
+struct alignas(sizeof(A) * V) Piece {
+    uint32_t w[sizeof(A) * V / 4];
+};
+template <>
+struct Piece<__nv_bfloat16, 1> {
+    __nv_bfloat16 w;
+};
+template <>
+struct Piece<__half, 1> {
+    __half w;
+};
+__device__ __forceinline__ void unpack_piece(const Piece<float, 4> &x, float *f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(x.w[i]);
+}
+__device__ __forceinline__ void unpack_piece(const Piece<float, 1> &x, float *f) { f[0] = __uint_as_float(x.w[0]); }
+__device__ __forceinline__ void unpack_piece(const Piece<__nv_bfloat16, 8> &x, float *f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(x.w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(x.w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack_piece(const Piece<__half, 8> &x, float *f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&x.w[i]));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+    }
+}
+__device__ __forceinline__ void unpack_piece(const Piece<__nv_bfloat16, 1> &x, float *f) { f[0] = to_f(x.w); }
+__device__ __forceinline__ void unpack_piece(const Piece<__half, 1> &x, float *f) { f[0] = to_f(x.w); }
+
 // V: pairs of a piece; INTER: pairs are neighbours.
 template <typename A, int V, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
+__global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs p) {
     step_begin();
-    extern __shared__ float2 cs[];  // [token][pair]: cosine, sine
+    constexpr int U = 4;  // tokens of a thread at a time
+    extern __shared__ __align__(16) float2 cs[];  // [token][pair]: cosine, sine
     __shared__ int64_t place[kRopeMaxTokens];  // in the caches, or -1
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
     const int nt = (int)(p.n_tokens - t0 < p.tokens ? p.n_tokens - t0 : p.tokens);
     const int half = p.rot / 2;
-    for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+    const int per_token = (p.hq + p.hkv + p.hv) * p.pieces;
+    // tokens side by side, where a token has few pieces; a thread's first piece and first token
+    const int T = blockDim.x, sub = max(1, T / per_token);
+    const int first = per_token <= T ? (int)threadIdx.x / per_token : 0;
+    const int64_t cache_end = (p.n_slots / p.page - 1) * p.page_stride + (p.page - 1) * p.place_stride +
+                              (p.hkv - 1) * p.cache_hs + p.dim;
+
+    Piece<A, V> x[U][2];
+    struct Run {  // a thread's piece of a head: where its two runs of V elements begin in token t0's row, and go to
+        const A *src;
+        A *dst;
+        void *cache;
+        int64_t step, to_step, cache_at;
+        int b, piece;
+        bool rotate;
+    };
+    auto open = [&](int slot) {
+        Run q;
+        const int head = slot / p.pieces;
+        q.piece = slot - head * p.pieces;
+        const bool rotated = q.piece < p.rot_pieces, apart = !INTER && rotated;
+        const int a = apart ? q.piece * V : q.piece * 2 * V;
+        q.b = apart ? half : V;
+        const bool is_q = head < p.hq, is_k = !is_q && head < p.hq + p.hkv;
+        const int kvh = head - p.hq - (is_k ? 0 : p.hkv);
+        q.rotate = rotated && (is_q || is_k);
+        q.step = is_q ? p.qs : is_k ? p.ks : p.vs;
+        q.to_step = is_q ? p.qos : p.kos;
+        q.src = (is_q ? static_cast<const A *>(p.q) + head * p.qhs
+                 : is_k ? static_cast<const A *>(p.k) + kvh * p.khs
+                        : static_cast<const A *>(p.v) + kvh * p.vhs) + t0 * q.step + a;
+        q.dst = is_q ? static_cast<A *>(p.q_out) + head * p.qohs + t0 * q.to_step + a
+                : is_k && p.k_out ? static_cast<A *>(p.k_out) + kvh * p.kohs + t0 * q.to_step + a
+                                  : nullptr;
+        q.cache = is_q || !p.k_cache ? nullptr : is_k ? p.k_cache : p.v_cache;
+        q.cache_at = kvh * p.cache_hs + a;
+        return q;
+    };
+    auto load = [&](const Run &q, int t1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t1 + u * sub;
+            if (t < nt) {
+                x[u][0] = *reinterpret_cast<const Piece<A, V> *>(q.src + t * q.step);
+                x[u][1] = *reinterpret_cast<const Piece<A, V> *>(q.src + t * q.step + q.b);
+            }
+        }
+    };
+    auto finish = [&](const Run &q, int t1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t1 + u * sub;
+            if (t >= nt) break;
+            float f[2 * V];
+            unpack_piece(x[u][0], f);
+            unpack_piece(x[u][1], f + V);
+            if (q.rotate) {
+                const float2 *w = cs + t * half + q.piece * V;
+                alignas(16) float2 cw[V];
+                if (V > 1) {
+#pragma unroll
+                    for (int j = 0; j < V; j += 2)
+                        *reinterpret_cast<float4 *>(cw + j) = *reinterpret_cast<const float4 *>(w + j);
+                } else {
+                    cw[0] = w[0];
+                }
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float &e0 = INTER ? f[2 * j] : f[j], &e1 = INTER ? f[2 * j + 1] : f[V + j];
+                    const float2 c = cw[j];
+                    const float n0 = e0 * c.x - e1 * c.y, n1 = fmaf(e0, c.y, e1 * c.x);
+                    e0 = n0;
+                    e1 = n1;
+                }
+            }
+            if (q.dst) {
+                store_vec<A, V>(q.dst + t * q.to_step, f);
+                store_vec<A, V>(q.dst + t * q.to_step + q.b, f + V);
+            }
+            if (q.cache && place[t] >= 0) {
+                const int64_t at = place[t] + q.cache_at;
+                if (LEAN_SPAN(at, V, cache_end, p.err)) store_cache<V>(q.cache, at, f, p.cache_bf16);
+                if (LEAN_SPAN(at + q.b, V, cache_end, p.err)) store_cache<V>(q.cache, at + q.b, f + V, p.cache_bf16);
+            }
+        }
+    };
+
+    int slot = per_token <= T ? threadIdx.x - first * per_token : threadIdx.x;
+    const bool live = first < sub && slot < per_token;
+    Run run;
+    if (live) {
+        run = open(slot);
+        load(run, first);  // under way while the angles are computed
+    }
+    for (int i = threadIdx.x; i < nt * half; i += T) {
         const int t = i / half, j = i - t * half;
         const int32_t pos = p.positions[t0 + t];
         const uint64_t f = p.turns[j];
@@ -70,56 +197,24 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
         cs[i] = make_float2(c * p.scale, s * p.scale);
     }
     if (p.k_cache && threadIdx.x < nt) {
-        const int32_t slot = p.slots[t0 + threadIdx.x];
+        const int32_t s = p.slots[t0 + threadIdx.x];
         int64_t at = -1;
-        if (slot >= p.n_slots) atomicOr(p.err, kErrSlot);
-        else if (slot >= 0) at = (int64_t)(slot / p.page) * p.page_stride + (int64_t)(slot % p.page) * p.place_stride;
+        if (s >= p.n_slots) atomicOr(p.err, kErrSlot);
+        else if (s >= 0) at = (int64_t)(s / p.page) * p.page_stride + (int64_t)(s % p.page) * p.place_stride;
         place[threadIdx.x] = at;
     }
     __syncthreads();
-
-    const int per_token = (p.hq + p.hkv + p.hv) * p.pieces;
-    const int64_t cache_end = (p.n_slots / p.page - 1) * p.page_stride + (p.page - 1) * p.place_stride +
-                              (p.hkv - 1) * p.cache_hs + p.dim;
-#pragma unroll 2
-    for (int i = threadIdx.x; i < nt * per_token; i += kRopeThreads) {
-        const int t = i / per_token, hp = i - t * per_token, head = hp / p.pieces, piece = hp - head * p.pieces;
-        const bool rotated = piece < p.rot_pieces;
-        const int64_t tok = t0 + t;
-        // where the piece's two runs of V elements begin
-        const bool apart = !INTER && rotated;
-        const int a = apart ? piece * V : piece * 2 * V, b = apart ? a + half : a + V;
-        const bool is_q = head < p.hq, is_k = !is_q && head < p.hq + p.hkv;
-        const int kvh = head - p.hq - (is_k ? 0 : p.hkv);
-        const A *src = is_q ? static_cast<const A *>(p.q) + tok * p.qs + head * p.qhs
-                     : is_k ? static_cast<const A *>(p.k) + tok * p.ks + kvh * p.khs
-                            : static_cast<const A *>(p.v) + tok * p.vs + kvh * p.vhs;
-        float x[2 * V];
-        load_f<A, V>(src + a, x);
-        load_f<A, V>(src + b, x + V);
-        if (rotated && (is_q || is_k)) {
-            const float2 *w = cs + t * half + piece * V;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float &u = INTER ? x[2 * j] : x[j], &v = INTER ? x[2 * j + 1] : x[V + j];
-                const float2 c = w[j];
-                const float nu = u * c.x - v * c.y, nv = fmaf(u, c.y, v * c.x);
-                u = nu;
-                v = nv;
-            }
+    if (!live) return;
+    for (int t1 = first;;) {
+        finish(run, t1);
+        t1 += U * sub;
+        if (t1 >= nt) {  // on to the thread's next piece
+            slot += T;
+            if (per_token <= T || slot >= per_token) return;
+            run = open(slot);
+            t1 = first;
         }
-        if (is_q || (is_k && p.k_out)) {
-            A *dst = is_q ? static_cast<A *>(p.q_out) + tok * p.qos + head * p.qohs
-                          : static_cast<A *>(p.k_out) + tok * p.kos + kvh * p.kohs;
-            store_vec<A, V>(dst + a, x);
-            store_vec<A, V>(dst + b, x + V);
-        }
-        if (!is_q && p.k_cache && place[t] >= 0) {
-            void *cache = is_k ? p.k_cache : p.v_cache;
-            const int64_t at = place[t] + kvh * p.cache_hs;
-            if (LEAN_SPAN(at + a, V, cache_end, p.err)) store_cache<V>(cache, at + a, x, p.cache_bf16);
-            if (LEAN_SPAN(at + b, V, cache_end, p.err)) store_cache<V>(cache, at + b, x + V, p.cache_bf16);
-        }
+        load(run, t1);
     }
 }
 
@@ -128,14 +223,20 @@ lean_status launch_rope(RopeArgs p, bool inter, int64_t flags, void *stream) {
     p.pieces = p.dim / (2 * V);
     p.rot_pieces = p.rot / (2 * V);
     const int64_t items = (int64_t)(p.hq + p.hkv + p.hv) * p.pieces;
-    // about eight pieces a thread, but no fewer blocks than SMs while there are tokens for them
-    int64_t tokens = std::max<int64_t>(1, 8 * kRopeThreads / items);
-    tokens = std::min(tokens, std::max<int64_t>(1, p.n_tokens / (2 * step_sm_count())));
+    // A thread for each piece of a token, or of several tokens side by side, and no more threads than that: idle ones
+    // cost resident blocks.  (At 16384 tokens of 16/2 bf16 heads of 128, 80 registers: 160 threads and eight tokens a
+    // block 34.3 us, 256 threads and twelve 34.8; 64 registers spill, 37.3; two tokens' loads at a time 42.)
+    const int64_t sub = std::max<int64_t>(1, 256 / items);
+    const int64_t passes = (items + kRopeMaxThreads - 1) / kRopeMaxThreads;
+    const int threads = (int)(((sub * items + passes - 1) / passes + 31) / 32 * 32);
+    // eight tokens a thread, but no fewer blocks than SMs while there are tokens for them
+    int64_t tokens = std::min<int64_t>(8 * sub, std::max<int64_t>(1, p.n_tokens / (2 * step_sm_count())));
+    tokens = std::min<int64_t>(tokens, std::max(1, 4096 / std::max(p.rot / 2, 1)));  // angles: 32 KB at most
     p.tokens = (int)std::min<int64_t>(tokens, kRopeMaxTokens);
-    const size_t smem = sizeof(float2) * p.tokens * std::max(p.rot / 2, 1);  // 32 KB at most
+    const size_t smem = sizeof(float2) * p.tokens * std::max(p.rot / 2, 1);
     const int64_t grid = (p.n_tokens + p.tokens - 1) / p.tokens;
-    if (inter) return step_launch(rope_kernel<A, V, true>, grid, kRopeThreads, smem, flags, stream, p);
-    return step_launch(rope_kernel<A, V, false>, grid, kRopeThreads, smem, flags, stream, p);
+    if (inter) return step_launch(rope_kernel<A, V, true>, grid, threads, smem, flags, stream, p);
+    return step_launch(rope_kernel<A, V, false>, grid, threads, smem, flags, stream, p);
 }
 
 // Pairs per piece: the most for which every run of elements is a whole number
