@@ -122,40 +122,68 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesArgs
             gave = part[1][i] > gave ? part[1][i] : gave;
         }
 
-        // tokens of the chunk, one per thread of the grid
+        // tokens of the chunk, over the threads of the grid
         const int n = p.n_seqs - first < kPagesThreads ? p.n_seqs - first : kPagesThreads;
         const int from = tok[0], to = tok[n];
-        for (int64_t i = (int64_t)from + blockIdx.x * kPagesThreads + threadIdx.x; i < to; i += (int64_t)G * kPagesThreads) {
-            int lo = 0, hi = n;  // the last sequence that begins at or before i
+        // (Four neighbours a thread where there are more than threads: one search, mostly one page and one 16-byte store
+        // for them, 12.1 -> 11.1 us at 255000 tokens; else one, since a decode step's neighbours are of different
+        // sequences, whose pages would be looked up one after the other.)
+        const int K = to - from > G * kPagesThreads ? 4 : 1;
+        for (int64_t i4 = (int64_t)from / K * K + K * ((int64_t)blockIdx.x * kPagesThreads + threadIdx.x); i4 < to;
+             i4 += (int64_t)K * G * kPagesThreads) {
+            int lo = 0, hi = n;  // the last sequence that begins at or before the first of them
+            const int64_t at = i4 > from ? i4 : from;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
-                if (tok[mid] <= i) lo = mid;
+                if (tok[mid] <= at) lo = mid;
                 else hi = mid;
             }
-            const bool ok = len_s[lo] >= 0;
-            const int had_len = ok ? len_s[lo] : -1 - len_s[lo];
-            const int pos = had_len + (int)(i - tok[lo]);
-            int slot = -1;
-            if (ok) {
-                const int page_at = pos / p.page, in = pos - page_at * p.page;
-                const int had_pages = (int)(((int64_t)had_len + p.page - 1) / p.page);
-                const int64_t entry = (int64_t)(first + lo) * p.table_stride + page_at;
-                int id;
-                if (page_at < had_pages) {
-                    id = LEAN_IN(entry, (p.n_seqs - 1) * p.table_stride + p.width, p.err) ? p.table[entry] : 0;
-                } else {
-                    id = p.ring[around((unsigned)head + take_s[lo] + page_at - had_pages, p.ring_size)];
-                    // a new page begins with a new token: that one enters it in the table
-                    if (in == 0 && LEAN_IN(entry, (p.n_seqs - 1) * p.table_stride + p.width, p.err))
-                        p.table[entry] = id;
+            int slot[4], position[4], seq[4], page_known = -1, seq_known = -1, id = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t i = i4 + k;
+                slot[k] = -1;
+                position[k] = 0;
+                seq[k] = -1;
+                if (i < from || i >= to || k >= K) continue;
+                while (lo + 1 < n && tok[lo + 1] <= i) ++lo;
+                const bool ok = len_s[lo] >= 0;
+                const int had_len = ok ? len_s[lo] : -1 - len_s[lo];
+                const int pos = had_len + (int)(i - tok[lo]);
+                if (ok) {
+                    const int page_at = pos / p.page, in = pos - page_at * p.page;
+                    if (page_at != page_known || lo != seq_known) {
+                        page_known = page_at;
+                        seq_known = lo;
+                        const int had_pages = (int)(((int64_t)had_len + p.page - 1) / p.page);
+                        const int64_t entry = (int64_t)(first + lo) * p.table_stride + page_at;
+                        if (!LEAN_IN(entry, (int64_t)(p.n_seqs - 1) * p.table_stride + p.width, p.err)) continue;
+                        if (page_at < had_pages) {
+                            id = p.table[entry];
+                        } else {
+                            id = p.ring[around((unsigned)head + take_s[lo] + page_at - had_pages, p.ring_size)];
+                            // a new page begins with a new token: that one enters it in the table
+                            if (in == 0) p.table[entry] = id;
+                        }
+                    }
+                    slot[k] = (int)((int64_t)id * p.page + in);
                 }
-                slot = (int)((int64_t)id * p.page + in);
+                position[k] = pos;
+                seq[k] = first + lo;
             }
-            if (LEAN_IN(i, p.max_tokens, p.err)) {
-                if (p.slots) p.slots[i] = slot;
-                if (p.positions) p.positions[i] = pos;
-                if (p.seqs) p.seqs[i] = first + lo;
-            }
+            auto put = [&](int32_t *to_, const int(&v)[4]) {
+                if (!to_ || !LEAN_SPAN(at, (i4 + K < to ? i4 + K : to) - at, p.max_tokens, p.err)) return;
+                if (K == 4 && i4 >= from && i4 + 4 <= to && ((uintptr_t)to_ & 15) == 0) {
+                    *reinterpret_cast<int4 *>(to_ + i4) = make_int4(v[0], v[1], v[2], v[3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < K && i4 + k >= from && i4 + k < to) to_[i4 + k] = v[k];
+                }
+            };
+            put(p.slots, slot);
+            put(p.positions, position);
+            put(p.seqs, seq);
         }
         // pages given back, a warp per sequence over the whole grid
         const int lane = threadIdx.x % 32;
