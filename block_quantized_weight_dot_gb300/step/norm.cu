@@ -27,41 +27,80 @@ struct NormArgs {
 
 constexpr int kNormThreads = 512;  // of a row, at most
 
-// Sum over the tpr threads of a row (a power of two, 32 at least); part: one
-// float per warp of the block, not used for anything else.
-__device__ __forceinline__ float row_sum(float v, int tpr, float *part) {
+// Sum over the tpr threads of a row (whole warps); part: one float per warp of the block, not used for anything else.
+__device__ __forceinline__ float row_sum(float v, int tpr, int row_in_block, float *part) {
     v = warp_sum(v);
     if (tpr == 32) return v;
-    const int warp = threadIdx.x / 32, first = (threadIdx.x & ~(tpr - 1)) / 32;
-    if (threadIdx.x % 32 == 0) part[warp] = v;
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
     float s = 0.f;
-    for (int i = 0; i < tpr / 32; ++i) s += part[first + i];
+    for (int i = 0; i < tpr / 32; ++i) s += part[row_in_block * (tpr / 32) + i];
     return s;
+}
+
+// VEC elements as they lie in memory, in whole registers.
+template <typename A, int VEC>
+struct Raw {
+    uint32_t w[(sizeof(A) * VEC + 3) / 4];
+    __device__ __forceinline__ void load(const A *p) {
+        if (sizeof(A) * VEC >= 16) {
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(A) * VEC / 16); ++i) {
+                const uint4 q = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = q.x;
+                w[(4 * i + 1) % kWords] = q.y;
+                w[(4 * i + 2) % kWords] = q.z;
+                w[(4 * i + 3) % kWords] = q.w;
+            }
+        } else if (sizeof(A) == 4) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            w[0] = *reinterpret_cast<const uint16_t *>(p);
+        }
+    }
+    __device__ __forceinline__ float get(int i) const;
+    static constexpr int kWords = (sizeof(A) * VEC + 3) / 4;
+};
+template <typename A>
+__device__ __forceinline__ float raw_element(uint32_t w, int half);
+template <>
+__device__ __forceinline__ float raw_element<float>(uint32_t w, int) { return __uint_as_float(w); }
+template <>
+__device__ __forceinline__ float raw_element<__nv_bfloat16>(uint32_t w, int half) {
+    return __uint_as_float(half ? w & 0xffff0000u : w << 16);
+}
+template <>
+__device__ __forceinline__ float raw_element<__half>(uint32_t w, int half) {
+    const __half2 v = *reinterpret_cast<const __half2 *>(&w);
+    return half ? __high2float(v) : __low2float(v);
+}
+template <typename A, int VEC>
+__device__ __forceinline__ float Raw<A, VEC>::get(int i) const {
+    return raw_element<A>(w[i * sizeof(A) / 4], i & 1);
 }
 
 template <typename A, typename R, int VEC, int NV>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs p, int tpr) {
     step_begin();
     __shared__ float part[2][kNormThreads / 32];
-    const int t = threadIdx.x & (tpr - 1);
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    const int mine = (int)threadIdx.x / tpr, t = threadIdx.x - mine * tpr;
+    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + mine;
     const bool live = row < p.rows;
     const float inv = 1.f / (float)p.width;
 
-    Vec<A, VEC> xr[NV], gr[NV];
-    Vec<R, VEC> hr[NV];
+    Raw<A, VEC> xr[NV], gr[NV];
+    Raw<R, VEC> hr[NV];
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * tpr) * VEC;
         in[i] = live && c < p.width;
         if (in[i] && p.x && LEAN_SPAN(row * p.xs + c, VEC, (p.rows - 1) * p.xs + p.width, p.err))
-            xr[i] = load_vec<A, VEC>(static_cast<const A *>(p.x) + row * p.xs + c);
+            xr[i].load(static_cast<const A *>(p.x) + row * p.xs + c);
         if (in[i] && p.h && LEAN_SPAN(row * p.hs + c, VEC, (p.rows - 1) * p.hs + p.width, p.err))
-            hr[i] = load_vec<R, VEC>(static_cast<const R *>(p.h) + row * p.hs + c);
+            hr[i].load(static_cast<const R *>(p.h) + row * p.hs + c);
         if (in[i] && p.gate && LEAN_SPAN(row * p.gs + c, VEC, (p.rows - 1) * p.gs + p.width, p.err))
-            gr[i] = load_vec<A, VEC>(static_cast<const A *>(p.gate) + row * p.gs + c);
+            gr[i].load(static_cast<const A *>(p.gate) + row * p.gs + c);
     }
     float post = 1.f;
     if (p.post_w) {
@@ -70,8 +109,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs p, in
         for (int i = 0; i < NV; ++i)
             if (in[i])
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) s = fmaf(to_f(xr[i].v[j]), to_f(xr[i].v[j]), s);
-        post = rsqrtf(fmaf(row_sum(s, tpr, part[0]), inv, p.eps));
+                for (int j = 0; j < VEC; ++j) s = fmaf(xr[i].get(j), xr[i].get(j), s);
+        post = rsqrtf(fmaf(row_sum(s, tpr, mine, part[0]), inv, p.eps));
     }
     float v[NV][VEC];
     float s = 0.f;
@@ -79,33 +118,33 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs p, in
     for (int i = 0; i < NV; ++i) {
         if (!in[i]) continue;
         const int c = (t + i * tpr) * VEC;
-        Vec<float, VEC> pw;
-        if (p.post_w) pw = load_vec<float, VEC>(p.post_w + c);
+        Raw<float, VEC> pw;
+        if (p.post_w) pw.load(p.post_w + c);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
             float u = 0.f;
             if (p.x) {
-                u = to_f(xr[i].v[j]);
-                if (p.post_w) u = u * post * pw.v[j];
-                if (p.gate) u *= to_f(gr[i].v[j]);
+                u = xr[i].get(j);
+                if (p.post_w) u = u * post * pw.get(j);
+                if (p.gate) u *= gr[i].get(j);
                 u *= p.alpha;
             }
-            v[i][j] = p.h ? to_f(hr[i].v[j]) + u : u;
+            v[i][j] = p.h ? hr[i].get(j) + u : u;
             s = fmaf(v[i][j], v[i][j], s);
         }
         if (p.h_out && LEAN_SPAN(row * p.hos + c, VEC, (p.rows - 1) * p.hos + p.width, p.err))
             store_vec<R, VEC>(static_cast<R *>(p.h_out) + row * p.hos + c, v[i]);
     }
     if (!p.y) return;
-    const float r = rsqrtf(fmaf(row_sum(s, tpr, part[1]), inv, p.eps));
+    const float r = rsqrtf(fmaf(row_sum(s, tpr, mine, part[1]), inv, p.eps));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (!in[i]) continue;
         const int c = (t + i * tpr) * VEC;
-        Vec<float, VEC> wv;
-        if (p.w) wv = load_vec<float, VEC>(p.w + c);
+        Raw<float, VEC> wv;
+        if (p.w) wv.load(p.w + c);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) v[i][j] *= p.w ? r * wv.v[j] : r;
+        for (int j = 0; j < VEC; ++j) v[i][j] *= p.w ? r * wv.get(j) : r;
         if (LEAN_SPAN(row * p.ys + c, VEC, (p.rows - 1) * p.ys + p.width, p.err))
             store_vec<A, VEC>(static_cast<A *>(p.y) + row * p.ys + c, v[i]);
     }
@@ -128,7 +167,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_long_kernel(const NormArgs 
     if (p.post_w) {
         float s = 0.f;
         for (int c = threadIdx.x; c < p.width; c += kNormThreads) s = fmaf(to_f(x[c]), to_f(x[c]), s);
-        post = rsqrtf(fmaf(row_sum(s, kNormThreads, part[0]), inv, p.eps));
+        post = rsqrtf(fmaf(row_sum(s, kNormThreads, 0, part[0]), inv, p.eps));
     }
     auto value = [&](int c) {
         float u = 0.f;
@@ -147,7 +186,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_long_kernel(const NormArgs 
             const float v = value(c);
             s = fmaf(v, v, s);
         }
-        r = rsqrtf(fmaf(row_sum(s, kNormThreads, part[1]), inv, p.eps));
+        r = rsqrtf(fmaf(row_sum(s, kNormThreads, 0, part[1]), inv, p.eps));
     }
     for (int c = threadIdx.x; c < p.width; c += kNormThreads) {
         const float v = value(c);
@@ -158,31 +197,48 @@ __global__ void __launch_bounds__(kNormThreads) norm_long_kernel(const NormArgs 
     }
 }
 
-int pow2_at_least(int64_t v) {
-    int p = 1;
-    while (p < v) p *= 2;
-    return p;
+// How a row is cut: nv vectors for each of tpr threads.  Few rows: as many threads as vectors (latency).  Many: the cut
+// that leaves the fewest threads idle in the last vector, two or three vectors and 256 threads rather than more (a row
+// of 1024 vectors on 512 threads leaves one block an SM, whose barriers nothing hides: 59.8 us at 2048 x 8192 bf16
+// against XX on 256).
+struct Cut {
+    int nv, tpr;
+};
+Cut cut_row(int64_t nvec, const int *nvs, int n, bool few) {
+    Cut best = {0, 0};
+    float least = 1e30f;
+    for (int i = 0; i < n; ++i) {
+        const int64_t tpr = ((nvec + nvs[i] - 1) / nvs[i] + 31) / 32 * 32;
+        if (tpr > kNormThreads) continue;
+        const float idle = (float)(tpr * nvs[i]) / (float)nvec;
+        const float cost = few ? (float)nvs[i]
+                               : idle + (tpr > 256 ? 0.5f : 0.f) + (i == 0 ? 0.15f : 0.f) + (i == n - 1 ? 0.05f : 0.f);
+        if (cost < least) {
+            least = cost;
+            best = Cut{nvs[i], (int)tpr};
+        }
+    }
+    return best;
 }
 
 template <typename A, typename R>
 lean_status launch_norm(const NormArgs &p, bool vec8, int64_t flags, void *stream) {
-    const int vec = vec8 ? 8 : 1, most = vec8 ? 4 : 8;  // vectors of a thread, at most
-    const int64_t nvec = (p.width + vec - 1) / vec;
-    if (nvec > (int64_t)kNormThreads * most)
-        return step_launch(norm_long_kernel<A, R>, p.rows, kNormThreads, 0, flags, stream, p);
-    // few rows: as many threads as there are vectors (latency); many: two vectors a thread
-    const int want = p.rows <= 2 * step_sm_count() ? 1 : 2;
-    const int tpr = std::min(kNormThreads, std::max(32, pow2_at_least((nvec + want - 1) / want)));
-    const int block = std::max(tpr, 128), nv = pow2_at_least((nvec + tpr - 1) / tpr);
-    const int64_t grid = (p.rows + block / tpr - 1) / (block / tpr);
+    const bool few = p.rows <= 2 * step_sm_count();
+    static const int vec_nvs[] = {1, 2, 3, 4}, one_nvs[] = {2, 4, 8};
+    const Cut c = vec8 ? cut_row((p.width + 7) / 8, vec_nvs, 4, few) : cut_row(p.width, one_nvs, 3, few);
+    if (c.nv == 0) return step_launch(norm_long_kernel<A, R>, p.rows, kNormThreads, 0, flags, stream, p);
+    const int rows = std::max(1, 128 / c.tpr), block = rows * c.tpr;
+    const int64_t grid = (p.rows + rows - 1) / rows;
+    auto go = [&](auto kern) { return step_launch(kern, grid, block, 0, flags, stream, p, c.tpr); };
     if (vec8) {
-        if (nv == 1) return step_launch(norm_kernel<A, R, 8, 1>, grid, block, 0, flags, stream, p, tpr);
-        if (nv == 2) return step_launch(norm_kernel<A, R, 8, 2>, grid, block, 0, flags, stream, p, tpr);
-        return step_launch(norm_kernel<A, R, 8, 4>, grid, block, 0, flags, stream, p, tpr);
+        if (c.nv == 1) return go(norm_kernel<A, R, 8, 1>);
+        if (c.nv == 2) return go(norm_kernel<A, R, 8, 2>);
+        if (c.nv == 3) return go(norm_kernel<A, R, 8, 3>);
+        return go(norm_kernel<A, R, 8, 4>);
     }
-    if (nv <= 2) return step_launch(norm_kernel<A, R, 1, 2>, grid, block, 0, flags, stream, p, tpr);
-    if (nv == 4) return step_launch(norm_kernel<A, R, 1, 4>, grid, block, 0, flags, stream, p, tpr);
-    return step_launch(norm_kernel<A, R, 1, 8>, grid, block, 0, flags, stream, p, tpr);
+    if (c.nv == 2) return go(norm_kernel<A, R, 1, 2>);
+    if (c.nv == 4) return go(norm_kernel<A, R, 1, 4>);
+    return go(norm_kernel<A, R, 1, 8>);
 }
 
 }  // namespace
