@@ -19,7 +19,7 @@ struct NormArgs {
     const void *x, *h, *gate;
     const float *post_w, *w;
     void *h_out, *y;
-    int64_t rows, xs, hs, gs, hos, ys;
+    int64_t rows, xs, hs, gs, hos, ys, stride;  // stride: of all buffers, where it is one (SHIFT)
     int width;
     float eps, alpha;
     unsigned *err;
@@ -79,7 +79,37 @@ __device__ __forceinline__ float Raw<A, VEC>::get(int i) const {
     return raw_element<A>(w[i * sizeof(A) / 4], i & 1);
 }
 
-template <typename A, typename R, int VEC, int NV>
+// A vector of a row that may begin before its first element or end past its last one: what is not the row's is 0 and
+// not stored.
+template <typename A, int VEC>
+__device__ __forceinline__ void load_part(Raw<A, VEC> &v, const A *row, int c, int width, bool vector) {
+    if (vector) {
+        v.load(row + c);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < Raw<A, VEC>::kWords; ++i) v.w[i] = 0;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        if (c + j < 0 || c + j >= width) continue;
+        if (sizeof(A) == 4) v.w[j % Raw<A, VEC>::kWords] = reinterpret_cast<const uint32_t *>(row)[c + j];
+        else v.w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row)[c + j] << (j & 1 ? 16 : 0);
+    }
+}
+template <typename A, int VEC>
+__device__ __forceinline__ void store_part(A *row, int c, int width, const float *f, bool vector) {
+    if (vector) {
+        store_vec<A, VEC>(row + c, f);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+        if (c + j >= 0 && c + j < width) row[c + j] = from_f<A>(f[j]);
+}
+
+// SHIFT: rows that do not begin on 16 bytes, with one stride for all buffers, so that all of them have vectors at the
+// same columns; the first and the last vector of a row are then partial.
+template <typename A, typename R, int VEC, int NV, bool SHIFT>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs p, int tpr) {
     step_begin();
     __shared__ float part[2][kNormThreads / 32];
@@ -87,20 +117,29 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs p, in
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + mine;
     const bool live = row < p.rows;
     const float inv = 1.f / (float)p.width;
+    // column of the thread's vector i
+    const int shift = SHIFT ? -(int)(row * p.stride % VEC) : 0;
+    auto column = [&](int i) { return (t + i * tpr) * VEC + shift; };
+    auto whole = [&](int c) { return !SHIFT || (c >= 0 && c + VEC <= p.width); };
+
+    auto inside = [&](int64_t at, bool v, int64_t stride) {  // (a partial vector looks at every element for itself)
+        return !v || LEAN_SPAN(at, VEC, (p.rows - 1) * stride + p.width, p.err);
+    };
 
     Raw<A, VEC> xr[NV], gr[NV];
     Raw<R, VEC> hr[NV];
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * tpr) * VEC;
+        const int c = column(i);
+        const bool v = whole(c);
         in[i] = live && c < p.width;
-        if (in[i] && p.x && LEAN_SPAN(row * p.xs + c, VEC, (p.rows - 1) * p.xs + p.width, p.err))
-            xr[i].load(static_cast<const A *>(p.x) + row * p.xs + c);
-        if (in[i] && p.h && LEAN_SPAN(row * p.hs + c, VEC, (p.rows - 1) * p.hs + p.width, p.err))
-            hr[i].load(static_cast<const R *>(p.h) + row * p.hs + c);
-        if (in[i] && p.gate && LEAN_SPAN(row * p.gs + c, VEC, (p.rows - 1) * p.gs + p.width, p.err))
-            gr[i].load(static_cast<const A *>(p.gate) + row * p.gs + c);
+        if (in[i] && p.x && inside(row * p.xs + c, v, p.xs))
+            load_part(xr[i], static_cast<const A *>(p.x) + row * p.xs, c, p.width, v);
+        if (in[i] && p.h && inside(row * p.hs + c, v, p.hs))
+            load_part(hr[i], static_cast<const R *>(p.h) + row * p.hs, c, p.width, v);
+        if (in[i] && p.gate && inside(row * p.gs + c, v, p.gs))
+            load_part(gr[i], static_cast<const A *>(p.gate) + row * p.gs, c, p.width, v && !(SHIFT && p.gs == 0));
     }
     float post = 1.f;
     if (p.post_w) {
@@ -117,9 +156,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs p, in
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (!in[i]) continue;
-        const int c = (t + i * tpr) * VEC;
+        const int c = column(i);
         Raw<float, VEC> pw;
-        if (p.post_w) pw.load(p.post_w + c);
+        if (p.post_w) load_part(pw, p.post_w, c, p.width, !SHIFT);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
             float u = 0.f;
@@ -132,21 +171,21 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs p, in
             v[i][j] = p.h ? hr[i].get(j) + u : u;
             s = fmaf(v[i][j], v[i][j], s);
         }
-        if (p.h_out && LEAN_SPAN(row * p.hos + c, VEC, (p.rows - 1) * p.hos + p.width, p.err))
-            store_vec<R, VEC>(static_cast<R *>(p.h_out) + row * p.hos + c, v[i]);
+        if (p.h_out && inside(row * p.hos + c, whole(c), p.hos))
+            store_part<R, VEC>(static_cast<R *>(p.h_out) + row * p.hos, c, p.width, v[i], whole(c));
     }
     if (!p.y) return;
     const float r = rsqrtf(fmaf(row_sum(s, tpr, mine, part[1]), inv, p.eps));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (!in[i]) continue;
-        const int c = (t + i * tpr) * VEC;
+        const int c = column(i);
         Raw<float, VEC> wv;
-        if (p.w) wv.load(p.w + c);
+        if (p.w) load_part(wv, p.w, c, p.width, !SHIFT);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) v[i][j] *= p.w ? r * wv.get(j) : r;
-        if (LEAN_SPAN(row * p.ys + c, VEC, (p.rows - 1) * p.ys + p.width, p.err))
-            store_vec<A, VEC>(static_cast<A *>(p.y) + row * p.ys + c, v[i]);
+        if (inside(row * p.ys + c, whole(c), p.ys))
+            store_part<A, VEC>(static_cast<A *>(p.y) + row * p.ys, c, p.width, v[i], whole(c));
     }
 }
 
@@ -200,7 +239,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_long_kernel(const NormArgs 
 // How a row is cut: nv vectors for each of tpr threads.  Few rows: as many threads as vectors (latency).  Many: the cut
 // that leaves the fewest threads idle in the last vector, two or three vectors and 256 threads rather than more (a row
 // of 1024 vectors on 512 threads leaves one block an SM, whose barriers nothing hides: 59.8 us at 2048 x 8192 bf16
-// against XX on 256).
+// against 46.7 on 256).
 struct Cut {
     int nv, tpr;
 };
@@ -222,23 +261,31 @@ Cut cut_row(int64_t nvec, const int *nvs, int n, bool few) {
 }
 
 template <typename A, typename R>
-lean_status launch_norm(const NormArgs &p, bool vec8, int64_t flags, void *stream) {
+lean_status launch_norm(const NormArgs &p, bool vec8, bool shifted, int64_t flags, void *stream) {
     const bool few = p.rows <= 2 * step_sm_count();
     static const int vec_nvs[] = {1, 2, 3, 4}, one_nvs[] = {2, 4, 8};
-    const Cut c = vec8 ? cut_row((p.width + 7) / 8, vec_nvs, 4, few) : cut_row(p.width, one_nvs, 3, few);
+    const Cut c = vec8      ? cut_row((p.width + 7) / 8, vec_nvs, 4, few)
+                  : shifted ? cut_row((p.width + 14) / 8, vec_nvs, 4, few)
+                            : cut_row(p.width, one_nvs, 3, few);
     if (c.nv == 0) return step_launch(norm_long_kernel<A, R>, p.rows, kNormThreads, 0, flags, stream, p);
     const int rows = std::max(1, 128 / c.tpr), block = rows * c.tpr;
     const int64_t grid = (p.rows + rows - 1) / rows;
     auto go = [&](auto kern) { return step_launch(kern, grid, block, 0, flags, stream, p, c.tpr); };
     if (vec8) {
-        if (c.nv == 1) return go(norm_kernel<A, R, 8, 1>);
-        if (c.nv == 2) return go(norm_kernel<A, R, 8, 2>);
-        if (c.nv == 3) return go(norm_kernel<A, R, 8, 3>);
-        return go(norm_kernel<A, R, 8, 4>);
+        if (c.nv == 1) return go(norm_kernel<A, R, 8, 1, false>);
+        if (c.nv == 2) return go(norm_kernel<A, R, 8, 2, false>);
+        if (c.nv == 3) return go(norm_kernel<A, R, 8, 3, false>);
+        return go(norm_kernel<A, R, 8, 4, false>);
     }
-    if (c.nv == 2) return go(norm_kernel<A, R, 1, 2>);
-    if (c.nv == 4) return go(norm_kernel<A, R, 1, 4>);
-    return go(norm_kernel<A, R, 1, 8>);
+    if (shifted) {
+        if (c.nv == 1) return go(norm_kernel<A, R, 8, 1, true>);
+        if (c.nv == 2) return go(norm_kernel<A, R, 8, 2, true>);
+        if (c.nv == 3) return go(norm_kernel<A, R, 8, 3, true>);
+        return go(norm_kernel<A, R, 8, 4, true>);
+    }
+    if (c.nv == 2) return go(norm_kernel<A, R, 1, 2, false>);
+    if (c.nv == 4) return go(norm_kernel<A, R, 1, 4, false>);
+    return go(norm_kernel<A, R, 1, 8, false>);
 }
 
 }  // namespace
@@ -261,11 +308,15 @@ extern "C" lean_status lean_residual_norm(const lean_norm_args *a, void *stream)
         return LEAN_ERR_ALIGN;
     // 16-byte vectors when every row of every buffer allows them
     const int64_t any = a->width | a->x_stride | a->h_stride | a->gate_stride | a->h_out_stride | a->y_stride;
-    const bool vec8 = any % 8 == 0 && step_aligned(a->x, 16) && step_aligned(a->h, 16) &&
-                      step_aligned(a->gate, 16) && step_aligned(a->h_out, 16) && step_aligned(a->y, 16) &&
-                      step_aligned(a->w, 16) && step_aligned(a->post_w, 16);
+    const bool on16 = step_aligned(a->x, 16) && step_aligned(a->h, 16) && step_aligned(a->gate, 16) &&
+                      step_aligned(a->h_out, 16) && step_aligned(a->y, 16);
+    const bool vec8 = on16 && any % 8 == 0 && step_aligned(a->w, 16) && step_aligned(a->post_w, 16);
+    // or where they all begin at the same distance from one
+    const int64_t stride = a->x ? a->x_stride : a->h_stride;
+    const bool shifted = on16 && !vec8 && (!a->h || a->h_stride == stride) && (!a->h_out || a->h_out_stride == stride) &&
+                         (!a->y || a->y_stride == stride) && (!a->gate || a->gate_stride == stride || a->gate_stride == 0);
     NormArgs p = {a->x, a->h, a->gate, a->post_w, a->w, a->h_out, a->y, a->rows, a->x_stride, a->h_stride,
-                  a->gate_stride, a->h_out_stride, a->y_stride, (int)a->width, (float)a->eps,
+                  a->gate_stride, a->h_out_stride, a->y_stride, stride, (int)a->width, (float)a->eps,
                   (float)a->res_scale, nullptr};
 #ifdef LEAN_DEBUG
     p.err = error_word();
@@ -273,12 +324,12 @@ extern "C" lean_status lean_residual_norm(const lean_norm_args *a, void *stream)
     typedef __nv_bfloat16 b16;
     const bool same = a->res_dtype == a->act_dtype;
     switch (a->act_dtype) {
-    case LEAN_F32: return launch_norm<float, float>(p, vec8, a->flags, stream);
+    case LEAN_F32: return launch_norm<float, float>(p, vec8, shifted, a->flags, stream);
     case LEAN_BF16:
-        return same ? launch_norm<b16, b16>(p, vec8, a->flags, stream)
-                    : launch_norm<b16, float>(p, vec8, a->flags, stream);
+        return same ? launch_norm<b16, b16>(p, vec8, shifted, a->flags, stream)
+                    : launch_norm<b16, float>(p, vec8, shifted, a->flags, stream);
     default:
-        return same ? launch_norm<__half, __half>(p, vec8, a->flags, stream)
-                    : launch_norm<__half, float>(p, vec8, a->flags, stream);
+        return same ? launch_norm<__half, __half>(p, vec8, shifted, a->flags, stream)
+                    : launch_norm<__half, float>(p, vec8, shifted, a->flags, stream);
     }
 }
