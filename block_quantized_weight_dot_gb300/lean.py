@@ -339,42 +339,43 @@ _PAGES = struct.Struct("<3q3Q2qQqQ2Q5Qq")
 _ATTENTION = struct.Struct("<6qQ2q2Q5qQ2qQQ2qQdqQqq")
 _LOGPROBS = struct.Struct("<3qQqQdq5QQqq")
 _dtypes = {}
+_i32 = _f32 = _i64t = None  # torch's, once a call has needed them
+
+
+def _types():
+    global _i32, _f32, _i64t
+    import torch
+    _dtypes.update({torch.float32: LEAN_F32, torch.bfloat16: LEAN_BF16, torch.float16: LEAN_F16})
+    _i32, _f32, _i64t = torch.int32, torch.float32, torch.int64
 
 
 def _dtype(t):
-    if not _dtypes:
-        import torch
-        _dtypes.update({torch.float32: LEAN_F32, torch.bfloat16: LEAN_BF16, torch.float16: LEAN_F16})
-    try:
-        return _dtypes[t.dtype]
-    except KeyError:
-        raise ValueError("element type %s: float32, bfloat16 or float16 is wanted" % t.dtype) from None
+    code = _dtypes.get(t.dtype)
+    if code is None:
+        raise ValueError("element type %s: float32, bfloat16 or float16 is wanted" % t.dtype)
+    return code
 
 
-def _array(t, shape, like, name):
+def _array(t, shape, dtype, name):
     """(address, stride of each dimension but the last) of a GPU tensor of that
-    shape and of the element type of `like` (a tensor), its last dimension
-    contiguous; zeros for None."""
+    shape and element type, its last dimension contiguous; zeros for None."""
     if t is None:
         return (0,) * len(shape)
-    if t.shape != shape or t.dtype != like.dtype or not t.is_cuda:
-        raise ValueError("%s is %s %s on %s: %s %s on the GPU is wanted"
-                         % (name, t.dtype, tuple(t.shape), t.device, like.dtype, tuple(shape)))
     st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
-        raise ValueError("%s: the last dimension is not contiguous" % name)
-    return (t.data_ptr(),) + st[:-1]
+    if t.shape == shape and t.dtype is dtype and t.is_cuda and (st[-1] == 1 or shape[-1] == 1):
+        return (t.data_ptr(),) + st[:-1]
+    raise ValueError("%s is %s %s on %s, strides %s: %s %s on the GPU is wanted, the last dimension contiguous"
+                     % (name, t.dtype, tuple(t.shape), t.device, st, dtype, tuple(shape)))
 
 
-def _plain(t, size, kind, name):
-    """Address of a contiguous GPU tensor of `size` elements of a dtype given by its
-    name ("torch.int32" and so on); 0 for None."""
+def _plain(t, size, dtype, name):
+    """Address of a contiguous GPU tensor of `size` elements of that type; 0 for None."""
     if t is None:
         return 0
-    if t.numel() != size or str(t.dtype) != kind or not t.is_cuda or not t.is_contiguous():
-        raise ValueError("%s is %s %s on %s: %d contiguous elements of %s on the GPU are wanted"
-                         % (name, t.dtype, tuple(t.shape), t.device, size, kind))
-    return t.data_ptr()
+    if t.dtype is dtype and t.numel() == size and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("%s is %s %s on %s: %d contiguous elements of %s on the GPU are wanted"
+                     % (name, t.dtype, tuple(t.shape), t.device, size, dtype))
 
 
 def lean_residual_norm(x, h, w, h_out, y, eps: float = 1e-6, post_w=None, gate=None,
@@ -384,6 +385,8 @@ def lean_residual_norm(x, h, w, h_out, y, eps: float = 1e-6, post_w=None, gate=N
     post_w the weights of the norm after the block (None: x as it is), gate
     [rows, width] or [width] (None: 1), w of the norm before the next one.
     h_out or y may be None."""
+    if _i32 is None:
+        _types()
     one = x if x is not None else h
     if one is None or one.dim() != 2:
         raise ValueError("x or h: [rows, width] is wanted")
@@ -391,15 +394,16 @@ def lean_residual_norm(x, h, w, h_out, y, eps: float = 1e-6, post_w=None, gate=N
     res = h if h is not None else h_out if h_out is not None else act
     shape = one.shape
     rows, width = shape
+    at, rt = act.dtype, res.dtype
     if gate is None:
         g = (0, 0)
     elif gate.dim() == 1 or gate.shape[0] == 1:
-        g = _array(gate.reshape(1, -1), (1, width), act, "gate")[0], 0
+        g = _array(gate.reshape(1, -1), (1, width), at, "gate")[0], 0
     else:
-        g = _array(gate, shape, act, "gate")
-    args = _NORM.pack(rows, width, _dtype(act), _dtype(res), *_array(x, shape, act, "x"), *_array(h, shape, res, "h"), *g,
-                      _plain(post_w, width, "torch.float32", "post_w"), _plain(w, width, "torch.float32", "w"),
-                      *_array(h_out, shape, res, "h_out"), *_array(y, shape, act, "y"), eps, res_scale, flags)
+        g = _array(gate, shape, at, "gate")
+    args = _NORM.pack(rows, width, _dtype(act), _dtype(res), *_array(x, shape, at, "x"), *_array(h, shape, rt, "h"), *g,
+                      _plain(post_w, width, _f32, "post_w"), _plain(w, width, _f32, "w"),
+                      *_array(h_out, shape, rt, "h_out"), *_array(y, shape, at, "y"), eps, res_scale, flags)
     st = _lib.lean_residual_norm(args, _stream(stream))
     if st:
         raise LeanError("lean_residual_norm", st)
@@ -429,25 +433,28 @@ def lean_rope_append(q, k, v, positions, slots, turns, q_out, k_cache, v_cache, 
     """Rotate the first rot_dim elements of each head of q and k ([tokens, heads,
     dim]) to `positions`, into q_out (and k_out), and store k and v at `slots` of
     the caches ([pages, page_size, kv_heads, dim], strides of their own)."""
+    if _i32 is None:
+        _types()
     one = q if q is not None else k
     if one is None or one.dim() != 3:
         raise ValueError("q or k: [tokens, heads, dim] is wanted")
     n, _, dim = one.shape
+    at = one.dtype
     hq = q.shape[1] if q is not None else 0
     hkv = k.shape[1] if k is not None else 0
     qs, ks = (n, hq, dim), (n, hkv, dim)
     if k_cache is not None:
         pages, page = k_cache.shape[:2]
-        kc = _array(k_cache, (pages, page, hkv, dim), k_cache, "k_cache")
-        if _array(v_cache, (pages, page, hkv, dim), k_cache, "v_cache")[1:] != kc[1:]:
+        kc = _array(k_cache, (pages, page, hkv, dim), k_cache.dtype, "k_cache")
+        if _array(v_cache, (pages, page, hkv, dim), k_cache.dtype, "v_cache")[1:] != kc[1:]:
             raise ValueError("k_cache and v_cache have different strides")
         cache, cdt, vc = (pages, page) + kc[1:], _dtype(k_cache), v_cache.data_ptr()
     else:
         cache, cdt, kc, vc = (0,) * 5, 0, (0,), 0
-    args = _ROPE.pack(n, hq, hkv, dim, rot_dim, 1 if interleaved else 0, _dtype(one), cdt, *_array(q, qs, one, "q"),
-                      *_array(k, ks, one, "k"), *_array(v, ks, one, "v"), *_array(q_out, qs, one, "q_out"),
-                      *_array(k_out, ks, one, "k_out"), _plain(positions, n, "torch.int32", "positions"),
-                      _plain(slots, n, "torch.int32", "slots"), _plain(turns, rot_dim // 2, "torch.int64", "turns"),
+    args = _ROPE.pack(n, hq, hkv, dim, rot_dim, 1 if interleaved else 0, _dtype(one), cdt, *_array(q, qs, at, "q"),
+                      *_array(k, ks, at, "k"), *_array(v, ks, at, "v"), *_array(q_out, qs, at, "q_out"),
+                      *_array(k_out, ks, at, "k_out"), _plain(positions, n, _i32, "positions"),
+                      _plain(slots, n, _i32, "slots"), _plain(turns, rot_dim // 2, _i64t, "turns"),
                       kc[0], vc, *cache, rot_scale, flags)
     st = _lib.lean_rope_append(args, _stream(stream))
     if st:
@@ -461,13 +468,15 @@ def lean_kv_pages(lens, targets, block_table, free_ring, ring_state, page_size: 
     given back to the free ring, block_table [seqs, width] follows, and the new
     tokens' slots, positions and sequences are written as one packed batch
     (int32 throughout)."""
+    if _i32 is None:
+        _types()
     n = lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table: [%d, width] is wanted" % n)
     some = slots if slots is not None else positions if positions is not None else token_seqs
     most = some.numel() if some is not None else 0
-    i32 = "torch.int32"
-    table, stride = _array(block_table, block_table.shape, lens, "block_table")
+    i32 = _i32
+    table, stride = _array(block_table, block_table.shape, i32, "block_table")
     args = _PAGES.pack(n, page_size, most, _plain(lens, n, i32, "lens"), _plain(targets, n, i32, "targets"), table,
                        block_table.shape[1], stride, _plain(free_ring, free_ring.numel(), i32, "free_ring"),
                        free_ring.numel(), _plain(ring_state, 2, i32, "ring_state"), _plain(lens_out, n, i32, "lens_out"),
@@ -489,20 +498,22 @@ def lean_paged_attention(q, k_cache, v_cache, block_table, seq_lens, out, scale:
     caches as for lean_rope_append, block_table [seqs, width], lse [seqs, heads]
     (None: not wanted); workspace: a once-zeroed uint8 tensor of
     lean_paged_attention_workspace_bytes."""
-    shape = q.shape
+    if _i32 is None:
+        _types()
+    shape, at, ct = q.shape, q.dtype, k_cache.dtype
     n, hq, dim = shape
     pages, page, hkv = k_cache.shape[:3]
-    kc = _array(k_cache, (pages, page, hkv, dim), k_cache, "k_cache")
-    vc = _array(v_cache, (pages, page, hkv, dim), k_cache, "v_cache")
+    kc = _array(k_cache, (pages, page, hkv, dim), ct, "k_cache")
+    vc = _array(v_cache, (pages, page, hkv, dim), ct, "v_cache")
     if vc[1:] != kc[1:]:
         raise ValueError("k_cache and v_cache have different strides")
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table: [%d, width] is wanted" % n)
-    table = _array(block_table, block_table.shape, seq_lens, "block_table")
-    args = _ATTENTION.pack(n, hq, hkv, dim, _dtype(q), _dtype(k_cache), *_array(q, shape, q, "q"), kc[0], vc[0], pages,
+    table = _array(block_table, block_table.shape, _i32, "block_table")
+    args = _ATTENTION.pack(n, hq, hkv, dim, _dtype(q), _dtype(k_cache), *_array(q, shape, at, "q"), kc[0], vc[0], pages,
                            page, *kc[1:], table[0], block_table.shape[1], table[1],
-                           _plain(seq_lens, n, "torch.int32", "seq_lens"), *_array(out, shape, q, "out"),
-                           _plain(lse, n * hq, "torch.float32", "lse"), scale, window, _addr(workspace) or 0,
+                           _plain(seq_lens, n, _i32, "seq_lens"), *_array(out, shape, at, "out"),
+                           _plain(lse, n * hq, _f32, "lse"), scale, window, _addr(workspace) or 0,
                            0 if workspace is None else workspace.numel(), flags)
     st = _lib.lean_paged_attention(args, _stream(stream))
     if st:
@@ -519,13 +530,15 @@ def lean_token_logprobs(logits, ids, logprobs, ranks=None, entropy=None, top_ids
     how many logits are larger, the entropy, and the top_ids.shape[1] most likely
     ids with theirs.  Outputs that are None are left out; workspace: a once-zeroed
     uint8 tensor of lean_token_logprobs_workspace_bytes."""
+    if _i32 is None:
+        _types()
     rows, vocab = logits.shape
     k = 0 if top_ids is None else top_ids.numel() // rows
-    x = _array(logits, (rows, vocab), logits, "logits")
-    f32 = "torch.float32"
-    args = _LOGPROBS.pack(rows, vocab, _dtype(logits), *x, _plain(ids, rows, "torch.int32", "ids"), scale, k,
-                          _plain(logprobs, rows, f32, "logprobs"), _plain(ranks, rows, "torch.int32", "ranks"),
-                          _plain(entropy, rows, f32, "entropy"), _plain(top_ids, rows * k, "torch.int32", "top_ids"),
+    x = _array(logits, (rows, vocab), logits.dtype, "logits")
+    f32 = _f32
+    args = _LOGPROBS.pack(rows, vocab, _dtype(logits), *x, _plain(ids, rows, _i32, "ids"), scale, k,
+                          _plain(logprobs, rows, f32, "logprobs"), _plain(ranks, rows, _i32, "ranks"),
+                          _plain(entropy, rows, f32, "entropy"), _plain(top_ids, rows * k, _i32, "top_ids"),
                           _plain(top_logprobs, rows * k, f32, "top_logprobs"), _addr(workspace) or 0,
                           0 if workspace is None else workspace.numel(), flags)
     st = _lib.lean_token_logprobs(args, _stream(stream))
