@@ -547,6 +547,150 @@ __global__ void __launch_bounds__(kEndThreads) logprobs_end_kernel(const LpArgs 
     if (threadIdx.x == 0) write_given<T>(p, row, a);
 }
 
+// The same with a warp per row, for many rows: no barriers, a sixth of the instructions.  k <= 32.
+constexpr int kRowWarps = 4, kRowList = 32 + 32 * 8 + 32;  // candidates: the best so far and a step's
+// The k best of a warp's list of n, in order, to its front; how many they are.  (A call: it is rare, and its state must
+// not make the list's live in memory.)
+__device__ __noinline__ int rank_list(Entry *list, Entry *best, int n, int k) {
+    const int lane = threadIdx.x % 32;
+    __syncwarp();
+    for (int i = lane; i < n; i += 32) {
+        const Entry e = list[i];
+        int q = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) q += beats(list[j], e);
+        if (q < k) best[q] = e;
+    }
+    __syncwarp();
+    n = min(n, k);
+    if (lane < n) list[lane] = best[lane];
+    __syncwarp();
+    return n;
+}
+struct WarpList {
+    Entry *list, *best;
+    int n, k;
+    bool full;  // k are known: others have to beat or equal the last of them
+    Entry kth;
+
+    __device__ __forceinline__ void clear() {
+        n = 0;
+        full = false;
+    }
+    __device__ __forceinline__ void rank() {
+        n = rank_list(list, best, n, k);
+        full = n == k;
+        if (full) kth = list[k - 1];
+    }
+    __device__ __forceinline__ bool counts(const Entry &e, float least) const {
+        return e.v >= least && e.v > -CUDART_INF_F && !(full && beats(kth, e));
+    }
+    __device__ __forceinline__ void push(bool mine, const Entry &e) {
+        const unsigned m = __ballot_sync(0xffffffffu, mine);
+        if (mine) list[n + __popc(m & ((1u << (threadIdx.x % 32)) - 1))] = e;
+        n += __popc(m);
+    }
+    __device__ __forceinline__ void room(int more) {
+        if (n + more > kRowList) rank();
+    }
+};
+// The k-th largest of the lanes' values (none where fewer lanes have more than none): k of them reach it.
+__device__ __forceinline__ int kth_of_lanes(int *values, int v, int k) {
+    const int lane = threadIdx.x % 32;
+    __syncwarp();
+    values[lane] = v;
+    __syncwarp();
+    int r = 0;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const int4 q = *reinterpret_cast<const int4 *>(values + i);
+        r += (q.x > v) + (q.y > v) + (q.z > v) + (q.w > v);
+    }
+    return __reduce_min_sync(0xffffffffu, r < k ? v : INT32_MAX);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowWarps * 32) logprobs_rows_kernel(const LpArgs p) {
+    constexpr int E = Lane<T>::kPer, PIECES = 8;  // a lane's in a round
+    __shared__ Entry lists[kRowWarps][kRowList], bests[kRowWarps][32];
+    __shared__ alignas(16) int values[kRowWarps][32];
+    step_begin();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n_half = 2 * p.row_units, k = p.top_k;
+    const int64_t row64 = (int64_t)blockIdx.x * kRowWarps + warp;
+    if (row64 >= p.rows) return;
+    const int row = (int)row64;
+    const unsigned u0 = (unsigned)row * p.row_units, g0 = warp_of(p, u0), g1 = warp_of(p, u0 + p.row_units - 1);
+    // the half units with the largest maxima
+    const int *halves = p.halves + (int64_t)row * n_half;
+    int most = ordered(-CUDART_INF_F);
+    for (int i = lane; i < n_half; i += 32) most = max(most, halves[i]);
+    Stats a = p.whole[row];
+    if (g0 != g1) {
+        a = p.runs[2 * g0 + 1];
+        if (g1 - g0 < 8) {
+            for (unsigned g = g0 + 1; g <= g1; ++g) join(p, a, p.runs[2 * g]);
+        } else {
+            if (lane > 0) a = Stats{kLowest, 0.f, 0.f, 0};
+            for (unsigned g = g0 + 1 + lane; g <= g1; g += 32) join(p, a, p.runs[2 * g]);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) join(p, a, shuffle(a, o));
+        }
+    }
+    WarpList w;
+    w.list = lists[warp];
+    w.best = bests[warp];
+    w.k = k;
+    w.clear();
+    float least = unordered(kth_of_lanes(values[warp], most, k));
+    for (int i0 = 0; i0 < n_half; i0 += 32) {
+        const int i = i0 + lane;
+        const Entry e = {i < n_half ? unordered(halves[i]) : -CUDART_INF_F, i};
+        w.room(32);
+        w.push(w.counts(e, least), e);
+    }
+    w.rank();
+    const int n_picked = w.n, picked = lane < n_picked ? w.list[lane].id : 0;
+    w.clear();
+    // their logits
+    const int pieces = n_picked * kHalfVecs;
+    const Row<T> at(p, row);
+    for (int from = 0; from < pieces; from += PIECES * 32) {
+        uint4 v[PIECES];
+        int id[PIECES];
+        float top[PIECES], mine = -CUDART_INF_F;
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const int i = from + j * 32 + lane;  // (a half unit is two steps of the warp)
+            const int piece = __shfl_sync(0xffffffffu, picked, min(i / kHalfVecs, 31)) * kHalfVecs + i % kHalfVecs;
+            id[j] = piece * E - at.before;
+            v[j] = make_uint4(Lane<T>::kMasked, Lane<T>::kMasked, Lane<T>::kMasked, Lane<T>::kMasked);
+            if (i < pieces) v[j] = at.load(p, piece);
+        }
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            top[j] = fmaxf(Lane<T>::largest(x, 4), -CUDART_INF_F);
+            mine = fmaxf(mine, top[j]);
+        }
+        least = unordered(kth_of_lanes(values[warp], ordered(mine), k));
+#pragma unroll
+        for (int j = 0; j < PIECES; ++j) {
+            // (an id of this piece at the least)
+            if (!__any_sync(0xffffffffu, w.counts(Entry{top[j], id[j]}, least))) continue;
+            w.room(32 * E);
+            const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const Entry it = {Lane<T>::get(x[e * 4 / E], e & 1), id[j] + e};
+                w.push(w.counts(it, least), it);
+            }
+        }
+        w.rank();
+    }
+    write_row(p, row, a, w.list, w.n, lane, 32);
+    if (lane == 0) write_given<T>(p, row, a);
+}
+
 // units of a row of 16-byte pieces, which may begin anywhere in one
 int64_t lp_row_units(int64_t vocab, int64_t size, bool aligned) {
     const int64_t per = 16 / size;
@@ -579,6 +723,10 @@ lean_status launch_logprobs(LpArgs p, int64_t flags, void *stream) {
         return step_launch(kern, p.rows, kEndThreads, sizeof(Entry) * p.top_k * (per_thread + 1), LEAN_FLAG_EARLY_WEIGHTS,
                            stream, p);
     };
+    // a warp per row where there is more than a row for every SM: 2048 x 151936 bf16, 8 alternatives, 23 us against 32
+    if (p.top_k <= 32 && p.rows > step_sm_count() && p.row_units <= 1024)
+        return step_launch(logprobs_rows_kernel<T>, ((int64_t)p.rows + kRowWarps - 1) / kRowWarps, kRowWarps * 32, 0,
+                           LEAN_FLAG_EARLY_WEIGHTS, stream, p);
     return p.top_k <= 8 ? end(logprobs_end_kernel<T, true, 4>, 4) : end(logprobs_end_kernel<T, true, 10>, 10);
 }
 
