@@ -149,14 +149,31 @@ __device__ __forceinline__ uint32_t take_part<__half>(float &a, float &b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// Two neighbouring elements of q; two or four of out.
+// Two neighbouring elements of q as they were read (nothing waits for them until they are used) and as fp32; two or
+// four of out.
 template <bool F32>
-__device__ __forceinline__ float2 load_pair(const void *p, int64_t i, int act) {
-    if (F32) return *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + i);
-    const uint32_t u = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i);
-    if (act == LEAN_BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
-}
+struct RawPair;
+template <>
+struct RawPair<true> {
+    float2 v;
+    __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        v = *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + i);
+    }
+    __device__ __forceinline__ float2 get(int) const { return v; }
+};
+template <>
+struct RawPair<false> {
+    uint32_t v;
+    __device__ __forceinline__ void zero() { v = 0; }
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        v = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i);
+    }
+    __device__ __forceinline__ float2 get(int act) const {
+        if (act == LEAN_BF16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    }
+};
 template <int N>
 __device__ __forceinline__ void store_out(void *p, int64_t i, int act, const float *f) {
     if (act == LEAN_F32) store_vec<float, N>(static_cast<float *>(p) + i, f);
@@ -465,7 +482,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
             cp_async_commit();
         };
         // q of the current item, asked for before its first keys (after them it would wait for them)
-        float2 f[NH][2 * KS];
+        RawPair<(PARTS > 2)> raw[NH][2 * KS];
         auto load_q = [&](int s, int kvh, int tile) {
             const int h0 = kvh * p.group + tile * H, nh = min(H, p.group - tile * H);
 #pragma unroll
@@ -474,9 +491,8 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                 for (int i = 0; i < 2 * KS; ++i) {
                     const int d = 8 * i + 2 * c4;
                     const int64_t at = (int64_t)s * p.qs + (int64_t)(h0 + r + 8 * h) * p.qhs + d;
-                    f[h][i] = r + 8 * h < nh && d < p.dim && LEAN_SPAN(at, 2, p.q_extent, p.err)
-                                  ? load_pair<(PARTS > 2)>(p.q, at, p.act)
-                                  : make_float2(0.f, 0.f);
+                    if (r + 8 * h < nh && d < p.dim && LEAN_SPAN(at, 2, p.q_extent, p.err)) raw[h][i].load(p.q, at);
+                    else raw[h][i].zero();
                 }
         };
         if (EARLY_Q) load_q(cur.s, cur.kvh, cur.tile);
@@ -500,9 +516,12 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
             if (fresh) {
                 fresh = false;
                 if (!EARLY_Q) load_q(cur.s, cur.kvh, cur.tile);
+                float2 f[NH][2 * KS];
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
                     float top = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 2 * KS; ++i) f[h][i] = raw[h][i].get(p.act);
 #pragma unroll
                     for (int i = 0; i < 2 * KS; ++i) top = fmaxf(top, fmaxf(fabsf(f[h][i].x), fabsf(f[h][i].y)));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
