@@ -496,7 +496,7 @@ def lean_paged_attention(q, k_cache, v_cache, block_table, seq_lens, out, scale:
                          workspace=None, flags: int = 0, stream=None) -> None:
     """Attention of one new token per sequence: q and out [seqs, heads, dim], the
     caches as for lean_rope_append, block_table [seqs, width], lse [seqs, heads]
-    (None: not wanted); workspace: a once-zeroed uint8 tensor of
+    (None: not wanted); workspace: a uint8 tensor of
     lean_paged_attention_workspace_bytes."""
     if _i32 is None:
         _types()
@@ -528,8 +528,8 @@ def lean_token_logprobs(logits, ids, logprobs, ranks=None, entropy=None, top_ids
                         scale: float = 1.0, workspace=None, flags: int = 0, stream=None) -> None:
     """Log probabilities of ids [rows] under softmax(scale * logits [rows, vocab]),
     how many logits are larger, the entropy, and the top_ids.shape[1] most likely
-    ids with theirs.  Outputs that are None are left out; workspace: a once-zeroed
-    uint8 tensor of lean_token_logprobs_workspace_bytes."""
+    ids with theirs.  Outputs that are None are left out; workspace: a uint8 tensor
+    of lean_token_logprobs_workspace_bytes."""
     if _i32 is None:
         _types()
     rows, vocab = logits.shape

@@ -200,7 +200,7 @@ __device__ __forceinline__ Span open_span(const AttArgs &p, int s) {
     x.len = len > most ? (int)most : len;
     x.start = p.window > 0 && x.len > p.window ? x.len - p.window : 0;
     x.base = x.start & ~(kUnit - 1);
-    x.n = (x.len - x.base + kUnit - 1) / kUnit;
+    x.n = (x.len - x.base) / kUnit + ((x.len - x.base) % kUnit != 0);
     x.n = x.n < 1 ? 1 : x.n;  // an empty sequence is one unit in which nothing is attended
     return x;
 }

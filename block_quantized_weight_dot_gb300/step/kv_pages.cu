@@ -225,6 +225,9 @@ extern "C" lean_status lean_kv_pages(const lean_kv_pages_args *a, void *stream) 
         a->table_stride < a->table_width || a->ring_size <= 0 || a->n_seqs >= big || a->page_size > big ||
         a->max_tokens > big || a->table_stride > big || a->ring_size > big)
         return LEAN_ERR_SHAPE;
+    // (blocks read the inputs while others write the outputs)
+    if (a->lens_out && (a->lens_out == a->lens || a->lens_out == a->targets)) return LEAN_ERR_SHAPE;
+    if (a->ring_state_out && a->ring_state_out == a->ring_state) return LEAN_ERR_SHAPE;
     if (!a->lens || !a->targets || !a->block_table || !a->free_ring || !a->ring_state || !a->lens_out ||
         !a->ring_state_out || !a->status || !a->token_starts)
         return LEAN_ERR_NULL;

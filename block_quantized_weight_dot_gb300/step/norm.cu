@@ -295,7 +295,7 @@ extern "C" lean_status lean_residual_norm(const lean_norm_args *a, void *stream)
     if (!known_dtype(a->act_dtype) || (a->res_dtype != LEAN_F32 && a->res_dtype != a->act_dtype) ||
         !step_flags_ok(a->flags))
         return LEAN_ERR_FORMAT;
-    if (a->rows <= 0 || a->width <= 0 || a->width > INT32_MAX / 2 || a->x_stride < 0 || a->h_stride < 0 ||
+    if (a->rows <= 0 || a->width <= 0 || a->rows > INT32_MAX / 2 || a->width > INT32_MAX / 2 || a->x_stride < 0 || a->h_stride < 0 ||
         a->gate_stride < 0 || a->h_out_stride < 0 || a->y_stride < 0)
         return LEAN_ERR_SHAPE;
     if (a->rows > 1 && ((a->h_out && a->h_out_stride < a->width) || (a->y && a->y_stride < a->width)))

@@ -370,7 +370,7 @@ int64_t lean_fixed_workspace_bytes(void);
  * a stream producer for a free slot, 4 the tensor-core product for a stage, 8
  * lean_wait_selftest, 16 lean_embed_rows was given an id outside 0 .. N-1, 32
  * (LEAN_DEBUG builds only) a kernel computed an index outside the buffers its
- * arguments describe and skipped that access.  Reads it
+ * arguments describe and skipped that access, 64 and 256 as lean_step.h says.  Reads it
  * synchronously (the device is synchronised first) and clears it when
  * `clear` is non-zero.  Returns 0xFFFFFFFF if the word cannot be read. */
 unsigned lean_device_error(int clear);

@@ -50,7 +50,7 @@ typedef enum { LEAN_F32 = 0, LEAN_BF16 = 1, LEAN_F16 = 2 } lean_dtype;
  * the branch alone).  y is computed from h' before h' is rounded for h_out.
  * h_out and y may be NULL (not stored), and may be the buffers of h and x with
  * the same strides; otherwise outputs overlap nothing.
- * LEAN_ERR_SHAPE: rows or width <= 0, a negative stride, or an output's stride
+ * LEAN_ERR_SHAPE: rows or width <= 0 or above 2^30 - 1, a negative stride, or an output's stride
  * below width with more than one row.  LEAN_ERR_NULL: x and h both NULL, h_out
  * and y both NULL, or a gate or post_w without x.  LEAN_ERR_FORMAT: an unknown
  * type, or a residual type that is neither LEAN_F32 nor act_dtype. */
@@ -178,11 +178,13 @@ lean_status lean_rope_append(const lean_rope_args *args, void *stream);
  *   1  the ring ran out (then every later sequence that needs pages fails too)
  *   2  more pages than a row of the table has
  *   3  its tokens end past max_tokens (those past it are not written)
- *   4  a negative length, or a ring_state outside the ring
+ *   4  a negative length, a ring_state outside the ring, or more pages given back
+ *      than the ring has room for (then every later one that gives any fails too)
  * lens_out and ring_state_out must not overlap lens, targets or ring_state (use
  * two sets in turn); all other outputs overlap nothing.
  * LEAN_ERR_SHAPE: n_seqs, page_size, table_width or ring_size <= 0, max_tokens <
- * 0, table_stride < table_width, any of these above 2^31 - 1.  LEAN_ERR_NULL: a
+ * 0, table_stride < table_width, any of these above 2^31 - 1, lens_out that is
+ * lens or targets, or ring_state_out that is ring_state.  LEAN_ERR_NULL: a
  * missing pointer (slots, positions and token_seqs may be NULL: not wanted). */
 typedef struct {
     int64_t n_seqs, page_size, max_tokens;
@@ -265,11 +267,14 @@ int64_t lean_paged_attention_workspace_bytes(int64_t n_seqs, int64_t n_q_heads, 
  * and rank -1 and sets bit 256 of the device error word.
  * ids may be NULL (then logprobs and ranks are not computed); each output may be
  * NULL.  logits: aligned to their element; rows that start on 16 bytes are read
- * fastest.  workspace as for lean_paged_attention.
+ * fastest.  workspace: lean_token_logprobs_workspace_bytes() bytes (with
+ * alternatives, a 64th of the logits in fp32), 256-byte aligned, any contents;
+ * calls that may run at the same time must not share one.
  * LEAN_ERR_SHAPE: rows <= 0, vocab not in 1..2^20, stride < vocab with more than
- * one row, top_k not in 0..LEAN_MAX_TOP, scale not finite or <= 0, or a
- * workspace too small.  LEAN_ERR_NULL: no logits, no workspace, logprobs or
- * ranks without ids, or top_k > 0 without top_ids and top_logprobs. */
+ * one row, rows x vocab past about 2^40, top_k not in 0..LEAN_MAX_TOP, scale not
+ * finite or <= 0, or a workspace too small.  LEAN_ERR_NULL: no logits, no
+ * workspace, logprobs or ranks without ids, or top_k > 0 without top_ids and
+ * top_logprobs. */
 #define LEAN_MAX_TOP 64
 typedef struct {
     int64_t rows, vocab;

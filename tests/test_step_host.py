@@ -249,3 +249,24 @@ def test_wrapper_checks(lean):
     with pytest.raises(ValueError):
         lean.lean_kv_pages(torch.zeros(3, dtype=torch.int32), None, torch.zeros(2, 2, dtype=torch.int32), None, None, 16,
                            None, None, None, None)
+
+
+def test_pages_in_place_refused(lean):
+    """Results written over the inputs that other blocks still read."""
+    call = Call(lean, "lean_kv_pages_args", "lean_kv_pages",
+                dict(n_seqs=2, page_size=16, max_tokens=8, lens=P, targets=P + 256, block_table=P, table_width=4,
+                     table_stride=4, free_ring=P, ring_size=8, ring_state=P + 512, lens_out=P + 768,
+                     ring_state_out=P + 1024, status=P, token_starts=P))
+    check_errors(call, lean, [("SHAPE", dict(lens_out=P)), ("SHAPE", dict(lens_out=P + 256)),
+                              ("SHAPE", dict(ring_state_out=P + 512))])
+
+
+def test_unit_count_limit(lean):
+    """Attention over more 16-token units than 32 bits count is refused."""
+    size = lean.lean_paged_attention_workspace_bytes(1 << 16, 8, 8, 64)
+    call = Call(lean, "lean_attention_args", "lean_paged_attention",
+                dict(n_seqs=1 << 16, n_q_heads=8, n_kv_heads=8, head_dim=64, cache_dtype=1, q=P, q_stride=512,
+                     q_head_stride=64, k_cache=P, v_cache=P, n_pages=4, page_size=16, page_stride=8192, place_stride=512,
+                     cache_head_stride=64, block_table=P, table_width=1 << 14, table_stride=1 << 14, seq_lens=P, out=P,
+                     out_stride=512, out_head_stride=64, scale=0.125, workspace=P, workspace_bytes=size))
+    check_errors(call, lean, [("SHAPE", {})])
