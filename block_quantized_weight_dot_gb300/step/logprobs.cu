@@ -18,6 +18,11 @@
 //     largest logits, so only they are read again, 1 KB each, and what reaches
 //     the k-th of the threads' largest is ranked by counting.  The cost does not
 //     depend on the order of the logits; ties go by the token id.
+//
+// Measured (GB300, calls in a graph): 2048 x 151936 bf16, 8 alternatives, 122 us
+// (104 without, 6.0 TB/s of the 6.78 that a copy reaches; 74% of issue slots);
+// fp32 230 (203 without); one row of 151936 fp32, 20 alternatives, 12.7 us (5.1
+// without); 37 x 32003 fp32, 5 alternatives, 9.4 us.
 #include <type_traits>
 
 #include "step_common.cuh"

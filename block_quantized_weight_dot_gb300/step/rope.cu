@@ -13,6 +13,10 @@
 // unrotated rest).  All traffic is 16-byte accesses at V = 8 (4 for fp32), four
 // tokens' loads at a time, the first ones before the angles are computed; every
 // element moves once, so HBM bounds it.
+//
+// Measured (GB300, calls in a graph): 16384 tokens of 16 query and 2 kv heads of
+// 128 (half of them rotated) 34 us in bf16 (4.9 TB/s), 53 us in fp32 (6.0 TB/s;
+// a copy reaches 6.78); four tokens of 15/5 heads of 64 2.7 us.
 #include "step_common.cuh"
 
 using namespace lean;
