@@ -9,14 +9,18 @@
 // A block takes a few tokens: their cosines and sines go to shared memory, once
 // for all heads.  A thread has one piece of one head, for all of the block's
 // tokens (its addresses then only step by the tokens' strides), where a piece is
-// V pairs: two runs of V elements (halves) or one of 2 V (neighbours and the
-// unrotated rest).  All traffic is 16-byte accesses at V = 8 (4 for fp32), four
-// tokens' loads at a time, the first ones before the angles are computed; every
-// element moves once, so HBM bounds it.
+// two runs of V elements: the two sides of V pairs (halves), or V / 2 pairs each
+// (neighbours) or none (the unrotated rest) from the two halves of what there is,
+// so that neighbouring threads read neighbouring 16 bytes (runs of 2 V elements a
+// thread read every other 16: 34.1 us in place of 30.1 at the sizes below).  All
+// traffic is 16-byte accesses at V = 8 (4 for fp32), four tokens' loads at a time,
+// the first ones before the angles are computed; every element moves once, so HBM
+// bounds it.  (Tokens staged in shared memory by asynchronous copies: 41 us.)
 //
 // Measured (GB300, calls in a graph): 16384 tokens of 16 query and 2 kv heads of
-// 128 (half of them rotated) 34 us in bf16 (4.9 TB/s), 53 us in fp32 (6.0 TB/s;
-// a copy reaches 6.78); four tokens of 15/5 heads of 64 2.7 us.
+// 128 (half of them rotated) 30.1 us in bf16 (5.6 TB/s; pairs of halves 33.8), 50.8
+// us in fp32 (6.3 TB/s; a copy reaches 6.78); 2000 tokens 5.1 us; four tokens of
+// 15/5 heads of 64 2.6 us.
 #include "step_common.cuh"
 
 using namespace lean;
@@ -85,7 +89,15 @@ __device__ __forceinline__ void unpack_piece(const Piece<__half, 8> &x, float *f
 __device__ __forceinline__ void unpack_piece(const Piece<__nv_bfloat16, 1> &x, float *f) { f[0] = to_f(x.w); }
 __device__ __forceinline__ void unpack_piece(const Piece<__half, 1> &x, float *f) { f[0] = to_f(x.w); }
 
-// V: pairs of a piece; INTER: pairs are neighbours.
+// Two pairs of neighbours.
+template <typename F>
+__device__ __forceinline__ void turn2(const float2 *w, float *f, F turn) {
+    const float4 c = *reinterpret_cast<const float4 *>(w);
+    turn(f[0], f[1], make_float2(c.x, c.y));
+    turn(f[2], f[3], make_float2(c.z, c.w));
+}
+
+// V: elements of a run; INTER: pairs are neighbours.
 template <typename A, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs p) {
     step_begin();
@@ -108,19 +120,34 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs
         A *dst;
         void *cache;
         int64_t step, to_step, cache_at;
-        int b, piece;
-        bool rotate;
+        int b, pair_a, pair_b;  // the second run's distance; the runs' first pairs, -1: not rotated
     };
     auto open = [&](int slot) {
         Run q;
-        const int head = slot / p.pieces;
-        q.piece = slot - head * p.pieces;
-        const bool rotated = q.piece < p.rot_pieces, apart = !INTER && rotated;
-        const int a = apart ? q.piece * V : q.piece * 2 * V;
-        q.b = apart ? half : V;
+        const int head = slot / p.pieces, piece = slot - head * p.pieces;
+        const bool rotated = piece < p.rot_pieces;
+        int a;
+        if (INTER && V > 1) {  // runs of whole pairs
+            a = piece * V;
+            q.b = p.dim / 2;
+        } else if (INTER) {
+            a = 2 * piece;
+            q.b = 1;
+        } else if (rotated) {
+            a = piece * V;
+            q.b = half;
+        } else {
+            a = p.rot + (piece - p.rot_pieces) * V;
+            q.b = (p.dim - p.rot) / 2;
+        }
         const bool is_q = head < p.hq, is_k = !is_q && head < p.hq + p.hkv;
         const int kvh = head - p.hq - (is_k ? 0 : p.hkv);
-        q.rotate = rotated && (is_q || is_k);
+        if (INTER && V > 1) {
+            q.pair_a = (is_q || is_k) && a < p.rot ? a / 2 : -1;
+            q.pair_b = (is_q || is_k) && a + q.b < p.rot ? (a + q.b) / 2 : -1;
+        } else {
+            q.pair_a = q.pair_b = (is_q || is_k) && rotated ? piece * V : -1;
+        }
         q.step = is_q ? p.qs : is_k ? p.ks : p.vs;
         q.to_step = is_q ? p.qos : p.kos;
         q.src = (is_q ? static_cast<const A *>(p.q) + head * p.qhs
@@ -151,23 +178,29 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs
             float f[2 * V];
             unpack_piece(x[u][0], f);
             unpack_piece(x[u][1], f + V);
-            if (q.rotate) {
-                const float2 *w = cs + t * half + q.piece * V;
-                alignas(16) float2 cw[V];
+            auto turn = [&](float &e0, float &e1, float2 c) {
+                const float n0 = e0 * c.x - e1 * c.y, n1 = fmaf(e0, c.y, e1 * c.x);
+                e0 = n0;
+                e1 = n1;
+            };
+            const float2 *w = cs + t * half;
+            if (INTER && V > 1) {
+                if (q.pair_a >= 0)
+#pragma unroll
+                    for (int j = 0; j < V; j += 4) turn2(w + q.pair_a + j / 2, f + j, turn);
+                if (q.pair_b >= 0)
+#pragma unroll
+                    for (int j = 0; j < V; j += 4) turn2(w + q.pair_b + j / 2, f + V + j, turn);
+            } else if (q.pair_a >= 0) {
                 if (V > 1) {
 #pragma unroll
-                    for (int j = 0; j < V; j += 2)
-                        *reinterpret_cast<float4 *>(cw + j) = *reinterpret_cast<const float4 *>(w + j);
+                    for (int j = 0; j < V; j += 2) {
+                        const float4 c = *reinterpret_cast<const float4 *>(w + q.pair_a + j);
+                        turn(f[j], f[V + j], make_float2(c.x, c.y));
+                        turn(f[j + 1], f[V + j + 1], make_float2(c.z, c.w));
+                    }
                 } else {
-                    cw[0] = w[0];
-                }
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float &e0 = INTER ? f[2 * j] : f[j], &e1 = INTER ? f[2 * j + 1] : f[V + j];
-                    const float2 c = cw[j];
-                    const float n0 = e0 * c.x - e1 * c.y, n1 = fmaf(e0, c.y, e1 * c.x);
-                    e0 = n0;
-                    e1 = n1;
+                    turn(f[0], f[V], w[q.pair_a]);
                 }
             }
             if (q.dst) {
@@ -229,7 +262,8 @@ lean_status launch_rope(RopeArgs p, bool inter, int64_t flags, void *stream) {
     const int64_t items = (int64_t)(p.hq + p.hkv + p.hv) * p.pieces;
     // A thread for each piece of a token, or of several tokens side by side, and no more threads than that: idle ones
     // cost resident blocks.  (At 16384 tokens of 16/2 bf16 heads of 128, 80 registers: 160 threads and eight tokens a
-    // block 34.3 us, 256 threads and twelve 34.8; 64 registers spill, 37.3; two tokens' loads at a time 42.)
+    // block 30.1 us, four tokens 33.7, twelve 31.7, two tokens side by side in 320 threads 31.4; 64 registers spill,
+    // 33.8; two tokens' loads at a time 38.7.)
     const int64_t sub = std::max<int64_t>(1, 256 / items);
     const int64_t passes = (items + kRopeMaxThreads - 1) / kRopeMaxThreads;
     const int threads = (int)(((sub * items + passes - 1) / passes + 31) / 32 * 32);
