@@ -39,6 +39,9 @@
 // the stream itself runs at 6 TB/s and more, 3 us pass before the first keys
 // arrive (lengths, table, keys, one after the other) and 8 after the last (joins,
 // the second kernel, the launch); 613 tokens of 15/5 heads of 64: 9.1 us.
+// Pages of 16 tokens or more hold a unit in one page or two, and two pages cost
+// little (384 sequences as above: 67 us with pages of 24, 68 of 20).  In smaller
+// pages every token is looked up: 86 us with pages of 8, 98 of one.
 #include "step_common.cuh"
 
 using namespace lean;
@@ -62,7 +65,7 @@ struct AttArgs {
     Shared *shared;
     float *warp_parts, *cta_parts;
     int64_t qs, qhs, os, ohs, page_stride, place_stride, cache_hs, table_stride, n_pages;
-    int n_seqs, hq, hkv, group, tiles, dim, page, paged, width, window;
+    int n_seqs, hq, hkv, group, tiles, dim, page, paged, whole, width, window;
     int act;
     float scale_log2;
     int64_t cache_extent, q_extent, out_extent;  // elements, for the checked build
@@ -213,11 +216,11 @@ __device__ __forceinline__ Span open_span(const AttArgs &p, int s) {
 }
 
 // A place in the list of units: sequence, kv head, tile of its query heads, unit.
-// Where units lie within pages (p.paged: pages of a multiple of 16 tokens), also
-// the unit's first place in its page.
+// Where units lie in one page or two (p.paged: pages of 16 tokens or more), also
+// the place of the unit's first token in its page.
 struct Place {
     int s, kvh, tile, c;
-    int in_page;
+    unsigned in_page;
     Span x;
 };
 __device__ __forceinline__ void to_page(const AttArgs &p, Place &at) {
@@ -225,7 +228,8 @@ __device__ __forceinline__ void to_page(const AttArgs &p, Place &at) {
 }
 __device__ __forceinline__ bool advance(const AttArgs &p, Place &at) {  // true: to another item
     if (++at.c < at.x.n) {
-        if ((at.in_page += kUnit) == p.page) at.in_page = 0;
+        at.in_page += kUnit;
+        if (at.in_page >= (unsigned)p.page) at.in_page -= p.page;
         return false;
     }
     at.c = 0;
@@ -417,17 +421,25 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         Place cur = next;  // to be computed
         int u_next = u_lo;
 
-        // Pages, fetched before they are needed: (paged) those of units pages_from + lane of the item, 32 at a
-        // time, else those of token lane % 16 of the unit to be loaded next.
+        // Pages, fetched before they are needed: (paged) those of the first and the last attended token of units
+        // pages_from + lane of the item, 32 at a time, else those of token lane % 16 of the unit to be loaded next.
         int pages_from = next.c;
-        auto fetch_pages = [&]() {
-            int tok = next.x.base + (p.paged ? (pages_from + lane) * kUnit : next.c * kUnit + lane % kUnit);
-            if (p.paged) tok = max(tok, next.x.start);
-            const bool in = tok >= next.x.start && tok < next.x.len;
-            const int64_t e = (int64_t)next.s * p.table_stride + tok / p.page;
+        auto fetch_page = [&](unsigned tok) {
+            const bool in = tok >= (unsigned)next.x.start && tok < (unsigned)next.x.len;
+            const int64_t e = (int64_t)next.s * p.table_stride + tok / (unsigned)p.page;
             return in && LEAN_IN(e, (int64_t)(p.n_seqs - 1) * p.table_stride + p.width, p.err) ? p.table[e] : 0;
         };
-        int pages = fetch_pages();
+        int pages, last_pages = 0;
+        auto fetch_pages = [&]() {
+            if (p.paged) {
+                const unsigned tok = next.x.base + (pages_from + lane) * kUnit;
+                pages = fetch_page(max(tok, (unsigned)next.x.start));
+                if (!p.whole) last_pages = fetch_page(min(tok + kUnit, (unsigned)next.x.len) - 1);
+            } else {
+                pages = fetch_page(next.x.base + next.c * kUnit + lane % kUnit);
+            }
+        };
+        fetch_pages();
         // a lane's piece of a row: its place in the caches, in a stage, and whether the head has it at all
         const int lr = lane / LPR, col = lane % LPR;
         const C *k_lane = static_cast<const C *>(p.k) + 8 * col, *v_lane = static_cast<const C *>(p.v) + 8 * col;
@@ -440,11 +452,10 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                 const int t0 = next.x.base + next.c * kUnit;
                 const int page_id = p.paged ? __shfl_sync(0xffffffffu, pages, next.c - pages_from) : pages;
                 const bool page_ok = page_id >= 0 && page_id < p.n_pages;
-                const int64_t unit_off = p.paged ? (int64_t)page_id * p.page_stride +
-                                                       (int64_t)next.in_page * p.place_stride +
-                                                       (int64_t)next.kvh * p.cache_hs
-                                                 : 0;
-                if (p.paged && page_ok && t0 >= next.x.start && t0 + kUnit <= next.x.len &&
+                const unsigned in_first = p.page - next.in_page;  // the unit's tokens in its first page, 16 or more: all
+                const int64_t unit_off = (int64_t)page_id * p.page_stride + (int64_t)next.in_page * p.place_stride +
+                                         (int64_t)next.kvh * p.cache_hs;
+                if (p.paged && in_first >= kUnit && page_ok && t0 >= next.x.start && t0 <= next.x.len - kUnit &&
                     LEAN_SPAN(unit_off, (kUnit - 1) * p.place_stride + p.dim, p.cache_extent, p.err)) {
                     // all of 16 tokens, one after the other
                     int64_t off = unit_off + lr * p.place_stride;
@@ -456,25 +467,38 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                         off += RPI * p.place_stride;
                     }
                 } else {
-                    const int tok = t0 + lane % kUnit;
+                    const int in_unit = lane % kUnit;
+                    const int last_id = __shfl_sync(0xffffffffu, last_pages, next.c - pages_from);
                     int64_t off = -1;  // of the token's row; -1: not attended, -2: outside the cache
-                    if (tok >= next.x.start && tok < next.x.len) {
-                        off = p.paged ? unit_off + (int64_t)(lane % kUnit) * p.place_stride
-                                      : (int64_t)page_id * p.page_stride + (int64_t)(tok % p.page) * p.place_stride +
-                                            (int64_t)next.kvh * p.cache_hs;
-                        if (!page_ok) off = -2;
+                    if (in_unit >= next.x.start - t0 && in_unit < next.x.len - t0) {
+                        const bool first = !p.paged || in_unit < in_first;
+                        const int id = first ? page_id : last_id;
+                        const int64_t place = !p.paged ? (t0 + in_unit) % p.page
+                                                       : (int64_t)next.in_page + in_unit - (first ? 0 : p.page);
+                        off = (int64_t)id * p.page_stride + place * p.place_stride + (int64_t)next.kvh * p.cache_hs;
+                        if (id < 0 || id >= p.n_pages) off = -2;
                         else if (!LEAN_SPAN(off, p.dim, p.cache_extent, p.err)) off = -1;
                     }
-                    if (__any_sync(0xffffffffu, off == -2) && lane == 0) atomicOr(p.err, kErrSlot);
+                    if (__all_sync(0xffffffffu, off >= 0)) {
 #pragma unroll
-                    for (int i = 0; i < kUnit / RPI; ++i) {
-                        const int64_t o = __shfl_sync(0xffffffffu, off, i * RPI + lr);
-                        const uint32_t to = i * RPI * RB + (dst ^ ((i * RPI & 7) * 16));
-                        if (o != -2)
-                            cp_async16(to, o >= 0 ? k_lane + o : static_cast<const C *>(p.k), o >= 0 ? real : 0);
-                        else  // keys that are not there: NaN, which reaches out and lse by itself
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to), "r"(0x7fff7fff) : "memory");
-                        cp_async16(to + kUnit * RB, o >= 0 ? v_lane + o : static_cast<const C *>(p.v), o >= 0 ? real : 0);
+                        for (int i = 0; i < kUnit / RPI; ++i) {
+                            const int64_t o = __shfl_sync(0xffffffffu, off, i * RPI + lr);
+                            const uint32_t to = i * RPI * RB + (dst ^ ((i * RPI & 7) * 16));
+                            cp_async16(to, k_lane + o, real);
+                            cp_async16(to + kUnit * RB, v_lane + o, real);
+                        }
+                    } else {
+                        if (__any_sync(0xffffffffu, off == -2) && lane == 0) atomicOr(p.err, kErrSlot);
+#pragma unroll
+                        for (int i = 0; i < kUnit / RPI; ++i) {
+                            const int64_t o = __shfl_sync(0xffffffffu, off, i * RPI + lr);
+                            const uint32_t to = i * RPI * RB + (dst ^ ((i * RPI & 7) * 16));
+                            if (o != -2)
+                                cp_async16(to, o >= 0 ? k_lane + o : static_cast<const C *>(p.k), o >= 0 ? real : 0);
+                            else  // keys that are not there: NaN, which reaches out and lse by itself
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(to), "r"(0x7fff7fff) : "memory");
+                            cp_async16(to + kUnit * RB, o >= 0 ? v_lane + o : static_cast<const C *>(p.v), o >= 0 ? real : 0);
+                        }
                     }
                 }
                 u_next += next.c == next.x.n - 1 ? 1 + kItemUnits : 1;
@@ -482,7 +506,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     const bool other = advance(p, next);
                     if (!p.paged || other || next.c == pages_from + 32) {
                         pages_from = next.c;
-                        pages = fetch_pages();
+                        fetch_pages();
                     }
                 }
             }
@@ -955,7 +979,8 @@ extern "C" lean_status lean_paged_attention(const lean_attention_args *a, void *
     p.tiles = (int)tiles;
     p.dim = (int)a->head_dim;
     p.page = (int)a->page_size;
-    p.paged = a->page_size % kUnit == 0;
+    p.paged = a->page_size >= kUnit;
+    p.whole = a->page_size % kUnit == 0;
     p.width = (int)a->table_width;
     p.window = (int)std::min<int64_t>(a->window, INT32_MAX);
     p.act = (int)a->act_dtype;

@@ -141,6 +141,33 @@ def test_bad_pages(lean):
         assert lean.lean_device_error(True) == 0
 
 
+@pytest.mark.parametrize("page", [5, 17, 20, 24])
+def test_pages_that_end_inside_a_unit(lean, page):
+    """Windows that begin at every place of a page; table entries of no attended token may be anything, the entry of
+    one attended token may not."""
+    torch = torch_cuda()
+    assert lean.lean_device_error(True) == 0
+    for window in range(60, 60 + page):
+        run_attend(lean, [0, 59, 200, 3 * page], 4, 2, 64, page=page, window=window, seed=window)
+    length, window = 10 * page + 1, 2 * page + 1  # the last three pages, one token of the last
+    q, kc, vc, table = make_attend([length] * 2, 4, 2, 64, page, "f32", "bf16", seed=page, width=13)
+    want, _, size, _ = attend_ref(q, kc, vc, table, [length] * 2, 0.125, window)
+    ws = torch.zeros(lean.lean_paged_attention_workspace_bytes(2, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    ld = torch.tensor([length] * 2, dtype=torch.int32, device="cuda")
+    out = torch.zeros((2, 4, 64), device="cuda")
+    table[:, :8] = -1
+    lean.lean_paged_attention(q, kc, vc, table, ld, out, scale=0.125, window=window, workspace=ws)
+    assert lean.lean_device_error(True) == 0
+    close(out, want, 1e-3 * size, "entries of no attended token")
+    for entry in (8, 10):
+        bad = table.clone()
+        bad[0, entry] = kc.shape[0]
+        lean.lean_paged_attention(q, kc, vc, bad, ld, out, scale=0.125, window=window, workspace=ws)
+        assert lean.lean_device_error(True) == 64
+        assert bool(torch.isnan(out[0]).all())
+        close(out[1], want[1], 1e-3 * size[1], "beside a bad page")
+
+
 def test_lse_joins_two_caches(lean):
     """Attention over two halves, joined by their lse, is attention over the whole."""
     torch = torch_cuda()
