@@ -19,10 +19,10 @@
 //     the k-th of the threads' largest is ranked by counting.  The cost does not
 //     depend on the order of the logits; ties go by the token id.
 //
-// Measured (GB300, calls in a graph): 2048 x 151936 bf16, 8 alternatives, 122 us
+// Measured (GB300, calls in a graph): 2048 x 151936 bf16, 8 alternatives, 119 us
 // (104 without, 6.0 TB/s of the 6.78 that a copy reaches; 74% of issue slots);
-// fp32 230 (203 without); one row of 151936 fp32, 20 alternatives, 12.7 us (5.1
-// without); 37 x 32003 fp32, 5 alternatives, 9.4 us.
+// fp32 229 (203 without); one row of 151936 fp32, 20 alternatives, 12.3 us (5.1
+// without); 37 x 32003 fp32, 5 alternatives, 9.5 us; 90 x 18478 f16, 5: 10.7 us.
 #include <type_traits>
 
 #include "step_common.cuh"
@@ -403,24 +403,24 @@ __device__ __forceinline__ unsigned long long key_of(const Entry &e) {
 // are as good as the k-th of them, so that only entries that it does not beat count, and only k threads have any.
 // list: room for n entries that are there already, and all of k threads.
 struct Pick {
-    alignas(16) unsigned long long keys[kEndThreads];
+    alignas(16) int values[kEndThreads], ids[kEndThreads];
     unsigned long long least;
-    int kth, n;
+    int kth, n, ties;
 };
 template <typename F>
 __device__ __forceinline__ int pick_best(Pick &sh, Entry *list, int n, Entry *best, int k, const Entry &mine, F each) {
     const int none = ordered(-CUDART_INF_F), v = ordered(mine.v);
-    int *values = reinterpret_cast<int *>(sh.keys);
-    values[threadIdx.x] = v;
+    sh.values[threadIdx.x] = v;
     if (threadIdx.x == 0) {
         sh.n = n;
+        sh.ties = 0;
         sh.kth = INT32_MAX;
     }
     __syncthreads();
     int r = 0;  // threads whose best is larger
 #pragma unroll 8
     for (int i = 0; i < kEndThreads; i += 4) {
-        const int4 q = *reinterpret_cast<const int4 *>(values + i);
+        const int4 q = *reinterpret_cast<const int4 *>(sh.values + i);
         r += (q.x > v) + (q.y > v) + (q.z > v) + (q.w > v);
     }
     if (r < k) atomicMin(&sh.kth, v);
@@ -429,12 +429,15 @@ __device__ __forceinline__ int pick_best(Pick &sh, Entry *list, int n, Entry *be
     // the lowest key that counts: all that reach t, unless more than k threads do
     unsigned long long least = (unsigned long long)((unsigned)t ^ 0x80000000u) << 32;
     if (as_good > k && sh.kth > none) {
-        const unsigned long long key = key_of(mine);
-        sh.keys[threadIdx.x] = key;
+        // of equal bests the lowest ids count; their threads come after r others (a rare path: short code, which
+        // is not in the instruction cache)
+        if (v == t) sh.ids[atomicAdd(&sh.ties, 1)] = mine.id;
         __syncthreads();
-        r = 0;
-        for (int i = 0; i < kEndThreads; ++i) r += sh.keys[i] > key || (sh.keys[i] == key && i < (int)threadIdx.x);
-        if (r == k - 1) sh.least = key;
+        if (v == t) {
+#pragma unroll 1
+            for (int i = sh.ties; --i >= 0;) r += sh.ids[i] < mine.id;
+            if (r == k - 1) sh.least = key_of(mine);
+        }
         __syncthreads();
         least = sh.least;
     }
@@ -455,17 +458,22 @@ __device__ __forceinline__ int pick_best(Pick &sh, Entry *list, int n, Entry *be
     return n < k ? n : k;
 }
 
+struct EndShared {
+    Entry best[kTop];
+    int picked[kTop];
+    Stats stats[kEndThreads / 32];
+    Pick pick;
+};
+
 // The rows' ends: sums joined, top logits found.  TOPS: a block per row; else a block per warp of the kernel before,
 // for the row that begins in its run and goes on after it.
 template <typename T, bool TOPS, int PIECES>
 __global__ void __launch_bounds__(kEndThreads) logprobs_end_kernel(const LpArgs p) {
-    constexpr int E = Lane<T>::kPer, W = kEndThreads / 32;
+    constexpr int E = Lane<T>::kPer;
     extern __shared__ __align__(16) uint8_t list_raw[];  // candidates: of k threads at most, and the k so far
     Entry *list = reinterpret_cast<Entry *>(list_raw);
-    __shared__ Entry best[kTop];
-    __shared__ int picked[kTop];
-    __shared__ Stats stats[W];
-    __shared__ Pick pick;
+    __shared__ EndShared sh;
+    Entry *const best = sh.best;
     step_begin();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n_half = 2 * p.row_units, k = p.top_k;
     int row = blockIdx.x;
@@ -483,12 +491,12 @@ __global__ void __launch_bounds__(kEndThreads) logprobs_end_kernel(const LpArgs 
     } else {
         for (unsigned i = g0 + threadIdx.x; i <= g1; i += kEndThreads) join(p, a, p.runs[2 * i + (i == g0)]);
         join_lanes(p, a);
-        if (lane == 0) stats[warp] = a;
+        if (lane == 0) sh.stats[warp] = a;
     }
     __syncthreads();
     if (g0 != g1) {
-        a = stats[0];
-        for (int i = 1; i < W; ++i) join(p, a, stats[i]);
+        a = sh.stats[0];
+        for (int i = 1; i < kEndThreads / 32; ++i) join(p, a, sh.stats[i]);
     }
     int n = 0;
     if (TOPS) {
@@ -499,10 +507,10 @@ __global__ void __launch_bounds__(kEndThreads) logprobs_end_kernel(const LpArgs 
             const float v = unordered(halves[i]);
             if (v > mine.v) mine = Entry{v, i};
         }
-        const int n_picked = pick_best(pick, list, 0, best, k, mine, [&](float, auto f) {
+        const int n_picked = pick_best(sh.pick, list, 0, best, k, mine, [&](float, auto f) {
             for (int i = threadIdx.x; i < n_half; i += kEndThreads) f(Entry{unordered(halves[i]), i});
         });
-        if (threadIdx.x < n_picked) picked[threadIdx.x] = best[threadIdx.x].id;
+        if (threadIdx.x < n_picked) sh.picked[threadIdx.x] = best[threadIdx.x].id;
         __syncthreads();
         // their logits, in rounds of PIECES pieces a thread, the best so far carried on
         const int pieces = n_picked * kHalfVecs;
@@ -515,7 +523,7 @@ __global__ void __launch_bounds__(kEndThreads) logprobs_end_kernel(const LpArgs 
             for (int j = 0; j < PIECES; ++j) {
                 const int i = from + j * kEndThreads + threadIdx.x;
                 if (i >= pieces) break;
-                const int piece = picked[i / kHalfVecs] * kHalfVecs + i % kHalfVecs;
+                const int piece = sh.picked[i / kHalfVecs] * kHalfVecs + i % kHalfVecs;
                 id[j] = piece * E - at.before;
                 v[j] = at.load(p, piece);
             }
@@ -546,7 +554,7 @@ __global__ void __launch_bounds__(kEndThreads) logprobs_end_kernel(const LpArgs 
                 }
             }
             for (int i = threadIdx.x; i < n; i += kEndThreads) list[i] = best[i];
-            n = pick_best(pick, list, n, best, k, mine, each);
+            n = pick_best(sh.pick, list, n, best, k, mine, each);
         }
     }
     write_row(p, row, a, best, n, threadIdx.x, kEndThreads);
@@ -575,29 +583,39 @@ __device__ __noinline__ int rank_list(Entry *list, Entry *best, int n, int k) {
 }
 struct WarpList {
     Entry *list, *best;
-    int n, k;
-    bool full;  // k are known: others have to beat or equal the last of them
+    int *count;  // entries in the list
+    int most;    // and how many there may be
+    int n, k;    // after rank(): entries
+    bool full;   // k are known: others have to beat the last of them
     Entry kth;
 
     __device__ __forceinline__ void clear() {
-        n = 0;
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) *count = 0;
+        __syncwarp();
+        most = 0;
         full = false;
     }
     __device__ __forceinline__ void rank() {
-        n = rank_list(list, best, n, k);
+        __syncwarp();
+        n = rank_list(list, best, *count, k);
+        if (threadIdx.x % 32 == 0) *count = n;
+        __syncwarp();
+        most = n;
         full = n == k;
         if (full) kth = list[k - 1];
     }
-    __device__ __forceinline__ bool counts(const Entry &e, float least) const {
-        return e.v >= least && e.v > -CUDART_INF_F && !(full && beats(kth, e));
+    // What a logit has to reach to count: not less than the k-th, and more than -inf.
+    __device__ __forceinline__ float reach(float least) const {
+        return fmaxf(full ? fmaxf(least, kth.v) : least, kLowest);
     }
-    __device__ __forceinline__ void push(bool mine, const Entry &e) {
-        const unsigned m = __ballot_sync(0xffffffffu, mine);
-        if (mine) list[n + __popc(m & ((1u << (threadIdx.x % 32)) - 1))] = e;
-        n += __popc(m);
+    // One lane's entry.  (Few lanes have one: their turns cost less than a vote of all lanes for every logit.)
+    __device__ __forceinline__ void add(const Entry &e) {
+        if (!(full && beats(kth, e))) list[atomicAdd(count, 1)] = e;
     }
     __device__ __forceinline__ void room(int more) {
-        if (n + more > kRowList) rank();
+        if (most + more > kRowList) rank();
+        most += more;
     }
 };
 // The k-th largest of the lanes' values (none where fewer lanes have more than none): k of them reach it.
@@ -615,11 +633,16 @@ __device__ __forceinline__ int kth_of_lanes(int *values, int v, int k) {
     return __reduce_min_sync(0xffffffffu, r < k ? v : INT32_MAX);
 }
 
+struct RowsShared {
+    Entry lists[kRowWarps][kRowList], bests[kRowWarps][32];
+    alignas(16) int values[kRowWarps][32];
+    int counts[kRowWarps];
+};
+
 template <typename T>
 __global__ void __launch_bounds__(kRowWarps * 32) logprobs_rows_kernel(const LpArgs p) {
     constexpr int E = Lane<T>::kPer, PIECES = 8;  // a lane's in a round
-    __shared__ Entry lists[kRowWarps][kRowList], bests[kRowWarps][32];
-    __shared__ alignas(16) int values[kRowWarps][32];
+    __shared__ RowsShared sh;
     step_begin();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n_half = 2 * p.row_units, k = p.top_k;
     const int64_t row64 = (int64_t)blockIdx.x * kRowWarps + warp;
@@ -642,16 +665,17 @@ __global__ void __launch_bounds__(kRowWarps * 32) logprobs_rows_kernel(const LpA
         }
     }
     WarpList w;
-    w.list = lists[warp];
-    w.best = bests[warp];
+    w.list = sh.lists[warp];
+    w.best = sh.bests[warp];
+    w.count = &sh.counts[warp];
     w.k = k;
     w.clear();
-    float least = unordered(kth_of_lanes(values[warp], most, k));
+    float least = unordered(kth_of_lanes(sh.values[warp], most, k));
     for (int i0 = 0; i0 < n_half; i0 += 32) {
         const int i = i0 + lane;
-        const Entry e = {i < n_half ? unordered(halves[i]) : -CUDART_INF_F, i};
+        const float v = i < n_half ? unordered(halves[i]) : -CUDART_INF_F;
         w.room(32);
-        w.push(w.counts(e, least), e);
+        if (v >= w.reach(least)) w.add(Entry{v, i});
     }
     w.rank();
     const int n_picked = w.n, picked = lane < n_picked ? w.list[lane].id : 0;
@@ -677,17 +701,20 @@ __global__ void __launch_bounds__(kRowWarps * 32) logprobs_rows_kernel(const LpA
             top[j] = fmaxf(Lane<T>::largest(x, 4), -CUDART_INF_F);
             mine = fmaxf(mine, top[j]);
         }
-        least = unordered(kth_of_lanes(values[warp], ordered(mine), k));
+        least = unordered(kth_of_lanes(sh.values[warp], ordered(mine), k));
 #pragma unroll
         for (int j = 0; j < PIECES; ++j) {
-            // (an id of this piece at the least)
-            if (!__any_sync(0xffffffffu, w.counts(Entry{top[j], id[j]}, least))) continue;
-            w.room(32 * E);
-            const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            const float t = w.reach(least);
+            const unsigned lanes = __ballot_sync(0xffffffffu, top[j] >= t);
+            if (!lanes) continue;
+            w.room(__popc(lanes) * E);
+            if (top[j] >= t) {
+                const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const Entry it = {Lane<T>::get(x[e * 4 / E], e & 1), id[j] + e};
-                w.push(w.counts(it, least), it);
+                for (int e = 0; e < E; ++e) {
+                    const Entry it = {Lane<T>::get(x[e * 4 / E], e & 1), id[j] + e};
+                    if (it.v >= t) w.add(it);
+                }
             }
         }
         w.rank();
@@ -716,23 +743,38 @@ lean_status launch_logprobs(LpArgs p, int64_t flags, void *stream) {
     // (the largest scales go by the far path always)
     const float clamp = std::is_same<T, __half>::value ? -65504.f : -9.9e29f;
     p.low = p.c > 1e6f ? 3.4e38f : std::max(-p.far, clamp + 160.f / p.c);
-    const bool tops = p.top_k > 0;
-    const lean_status st = tops ? step_launch(logprobs_kernel<T, true>, grid, kLpThreads, 0, flags, stream, p)
-                                : step_launch(logprobs_kernel<T, false>, grid, kLpThreads, 0, flags, stream, p);
-    if (st != LEAN_OK) return st;
-    if (!tops && p.warps == 1) return st;  // no row is shared
-    if (!tops) return step_launch(logprobs_end_kernel<T, false, 1>, p.warps, kEndThreads, 0, LEAN_FLAG_EARLY_WEIGHTS, stream, p);
+    // The second kernel's blocks come while the first one's end, which takes the same amount of shared memory from L1
+    // for both: what the blocks of the second that an SM gets need, its registers allow five.  (Left to the driver, 90
+    // x 18478 f16, 5 alternatives, took 16.0 us in place of 10.7: an SM changes its amount when it is idle.  Too little
+    // costs blocks at a time: 2885 x 2638 f16 45 us with 18 KB in place of 33.7, 37 x 32003 fp32 10.6 with 9 in place of
+    // 9.5.  Too much leaves no L1 to load into: 2048 x 151936 bf16 130 with all of it in place of 119.)
+    auto launch = [&](auto first, auto second, int64_t blocks, int threads, size_t fixed, size_t list) {
+        const int64_t of_sm = std::min<int64_t>(5, (blocks + step_sm_count() - 1) / step_sm_count());
+        const int64_t need = std::max<int64_t>(of_sm * (int64_t)(fixed + list + 1024) + kLpCtas * 2048, 13 << 10);
+        const int shared = (int)std::min<int64_t>(100, (100 * need + 228 * 1024 - 1) / (228 * 1024));
+        const lean_status st = step_launch_with(shared, first, grid, kLpThreads, 0, flags, stream, p);
+        if (st != LEAN_OK || blocks == 0) return st;
+        return step_launch_with(shared, second, blocks, threads, list, LEAN_FLAG_EARLY_WEIGHTS, stream, p);
+    };
+    if (p.top_k == 0)  // (no row is shared by warps if there is one)
+        return launch(logprobs_kernel<T, false>, logprobs_end_kernel<T, false, 1>, p.warps == 1 ? 0 : p.warps, kEndThreads,
+                      sizeof(EndShared), 0);
+    // A warp per row where there are so many that a barrier's wait counts more than a row's own time, which grows with
+    // the half units that it reads.  Measured, us a call, block and warp per row: 16-bit 2048 x 151936, 8 alternatives
+    // 134 119; 780 x 32000, 5: 22.1 21.3; 600 x 32000, 1: 17.9 15.6; 6000 x 32000, 20: 202 179; 3040 x 151936, 20: 228
+    // 229; 512 x 151936, 8: 41.6 43.9; fp32 500 x 32000, 1: 24.1 21.4; 8000 x 32000, 5: 234 222; 1000 x 32000, 5: 36.8
+    // 37.9; 6000 x 5843, 20: 119 151.
+    const int64_t reads = std::min(p.top_k, 2 * p.row_units);
+    const bool wide = sizeof(T) == 4;
+    if (p.top_k <= 32 && p.rows >= (wide ? 2 : 1) * reads * step_sm_count() && (!wide || reads <= 8))
+        return launch(logprobs_kernel<T, true>, logprobs_rows_kernel<T>, ((int64_t)p.rows + kRowWarps - 1) / kRowWarps,
+                      kRowWarps * 32, sizeof(RowsShared), 0);
     // pieces of a thread in a round: 4 take 8 half units at once, 10 take 20
     auto end = [&](auto kern, int pieces) {
         const int per_thread = std::max(pieces * Lane<T>::kPer, (2 * p.row_units + kEndThreads - 1) / kEndThreads);
-        return step_launch(kern, p.rows, kEndThreads, sizeof(Entry) * p.top_k * (per_thread + 1), LEAN_FLAG_EARLY_WEIGHTS,
-                           stream, p);
+        return launch(logprobs_kernel<T, true>, kern, p.rows, kEndThreads, sizeof(EndShared),
+                      sizeof(Entry) * p.top_k * (per_thread + 1));
     };
-    // a warp per row where every SM has several: 2048 x 151936 bf16, 8 alternatives, 23 us against 32; 512 rows the same;
-    // 221 rows of 5843 fp32, 20 alternatives, 41 us against 15.7 a call
-    if (p.top_k <= 32 && p.rows >= 8 * step_sm_count())
-        return step_launch(logprobs_rows_kernel<T>, ((int64_t)p.rows + kRowWarps - 1) / kRowWarps, kRowWarps * 32, 0,
-                           LEAN_FLAG_EARLY_WEIGHTS, stream, p);
     return p.top_k <= 8 ? end(logprobs_end_kernel<T, true, 4>, 4) : end(logprobs_end_kernel<T, true, 10>, 10);
 }
 

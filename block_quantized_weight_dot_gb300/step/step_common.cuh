@@ -55,24 +55,34 @@ inline bool step_ensure_smem(Kern kern, size_t bytes, std::atomic<uint64_t> &don
     return true;
 }
 
+// shared: how much of an SM's L1 should be shared memory, in percent (-1: as the driver likes).  Two kernels that are
+// to overlap ask for the same: an SM has to be idle to change it.
 template <typename... KArgs, typename... Args>
-inline lean_status step_launch(void (*kern)(KArgs...), int64_t grid, int block, size_t smem, int64_t flags,
-                               void *stream, Args... args) {
+inline lean_status step_launch_with(int shared, void (*kern)(KArgs...), int64_t grid, int block, size_t smem,
+                                    int64_t flags, void *stream, Args... args) {
     if (grid < 1 || grid > INT32_MAX) return LEAN_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3((unsigned)block, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = (cudaStream_t)stream;
     if (flags & LEAN_FLAG_EARLY_WEIGHTS) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
     }
+    if (shared >= 0) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+        attr[cfg.numAttrs++].val.sharedMemCarveout = shared;
+    }
+    cfg.attrs = attr;
     cudaGetLastError();
     return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? LEAN_OK : LEAN_ERR_CUDA;
+}
+template <typename... KArgs, typename... Args>
+inline lean_status step_launch(void (*kern)(KArgs...), int64_t grid, int block, size_t smem, int64_t flags,
+                               void *stream, Args... args) {
+    return step_launch_with(-1, kern, grid, block, smem, flags, stream, args...);
 }
 
 // First thing in every kernel here: let the next kernel's launch begin, and

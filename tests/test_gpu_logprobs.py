@@ -6,7 +6,7 @@ import math
 import pytest
 
 from lean_testlib import torch_cuda
-from step_testlib import close, dtype, gen, logprobs_ref, normal, run_logprobs, strided
+from step_testlib import U, close, dtype, gen, logprobs_ref, normal, run_logprobs, strided
 
 pytestmark = pytest.mark.gpu
 
@@ -122,6 +122,44 @@ def test_scales(lean, scale):
 def test_shifted_logits(lean, shift):
     """A constant added to all logits changes nothing but their own rounding."""
     run_logprobs(lean, normal(gen(8), 3, 5000, std=2.0) + shift, ids_of(3, 5000), k=4)
+
+
+@pytest.mark.parametrize("t,vocab,k,rows", [("f16", 1100, 32, 700), ("bf16", 16400, 32, 4900), ("f32", 600, 20, 1300),
+                                            ("f32", 5003, 8, 2500), ("bf16", 32003, 1, 170), ("f16", 5003, 5, 800),
+                                            ("bf16", 7, 3, 400), ("f32", 32003, 2, 700)])
+def test_many_rows(lean, t, vocab, k, rows):
+    """The rows that can go wrong, over and over: ties, orders, masks, NaN and infinities."""
+    torch = torch_cuda()
+    x = normal(gen(vocab), 13, vocab, t=t, std=2.0)
+    x[1] = torch.round(x[1] * 2)
+    x[2] = 1.5
+    x[3] = torch.where(x[3] > 0, 0.0, -0.0).to(x.dtype)
+    x[4] = torch.linspace(-20, 5, vocab, device="cuda").to(x.dtype)
+    x[5] = x[4].flip(0)
+    x[6, ::2] = -math.inf
+    x[7] = -math.inf
+    x[8, 1:] = -math.inf
+    x[9, vocab // 2] = math.nan
+    x[10] = math.nan
+    x[11, vocab - 1] = math.inf
+    x[12] = torch.finfo(x.dtype).min
+    x[12, 3] = 0
+    n = -(-rows // 13)
+    ids = [(5 * r) % vocab for r in range(13)]
+    want_lp, want_rk, want_en, want_ti, want_tl = logprobs_ref(x, ids, 1.0, k)
+    idd = torch.tensor(ids * n, dtype=torch.int32, device="cuda")
+    lp, en = torch.full((13 * n,), 7.0, device="cuda"), torch.full((13 * n,), 7.0, device="cuda")
+    rk, ti = idd.clone(), torch.full((13 * n, k), 7, dtype=torch.int32, device="cuda")
+    tl = torch.full((13 * n, k), 7.0, device="cuda")
+    ws = torch.zeros(lean.lean_token_logprobs_workspace_bytes(13 * n, vocab, k), dtype=torch.uint8, device="cuda")
+    lean.lean_token_logprobs(x.repeat(n, 1), idd, lp, ranks=rk, entropy=en, top_ids=ti, top_logprobs=tl, workspace=ws)
+    rel = (vocab / 128 + 128) * U  # (as in run_logprobs)
+    fin = lambda v: torch.where(torch.isfinite(v), v, 0.0).abs()
+    assert rk.tolist() == want_rk * n
+    assert ti.tolist() == want_ti * n
+    close(lp, want_lp.repeat(n), rel + 4 * U * fin(want_lp).repeat(n), "logprobs")
+    close(en, want_en.repeat(n), rel * (2 + fin(want_en).repeat(n)), "entropy")
+    close(tl, want_tl.repeat(n, 1), rel + 4 * U * fin(want_tl).repeat(n, 1), "top logprobs")
 
 
 def test_bad_ids(lean):
