@@ -71,16 +71,18 @@ __device__ __forceinline__ void unpack_piece(const Piece<float, 4> &x, float *f)
     for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(x.w[i]);
 }
 __device__ __forceinline__ void unpack_piece(const Piece<float, 1> &x, float *f) { f[0] = __uint_as_float(x.w[0]); }
-__device__ __forceinline__ void unpack_piece(const Piece<__nv_bfloat16, 8> &x, float *f) {
+template <int V>
+__device__ __forceinline__ void unpack_piece(const Piece<__nv_bfloat16, V> &x, float *f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V / 2; ++i) {
         f[2 * i] = __uint_as_float(x.w[i] << 16);
         f[2 * i + 1] = __uint_as_float(x.w[i] & 0xffff0000u);
     }
 }
-__device__ __forceinline__ void unpack_piece(const Piece<__half, 8> &x, float *f) {
+template <int V>
+__device__ __forceinline__ void unpack_piece(const Piece<__half, V> &x, float *f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V / 2; ++i) {
         const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&x.w[i]));
         f[2 * i] = v.x;
         f[2 * i + 1] = v.y;
@@ -277,13 +279,18 @@ lean_status launch_rope(RopeArgs p, bool inter, int64_t flags, void *stream) {
     return step_launch(rope_kernel<A, V, false>, grid, threads, smem, flags, stream, p);
 }
 
-// Pairs per piece: the most for which every run of elements is a whole number
-// of them and lies on 16 bytes (8 or 4 elements), else one.
+// Elements of a run: as many as 16 bytes have where every run is a whole number of
+// them and lies on 16 bytes, of 16-bit types else half as many, else one (2000
+// tokens of 32/8 bf16 heads of 80, 40 of them rotated: pairs of neighbours 7.6 us by
+// eight and 19.3 by one, of halves 7.8 by four and 20.1 by one).
 template <typename A>
 lean_status pick_rope(const RopeArgs &p, bool inter, int64_t any_stride, bool on16, int64_t flags, void *stream) {
     constexpr int V = 16 / sizeof(A);
-    if (on16 && any_stride % V == 0 && p.rot / 2 % V == 0 && p.dim % (2 * V) == 0 && p.rot % (2 * V) == 0)
-        return launch_rope<A, V>(p, inter, flags, stream);
+    auto fits = [&](int v) {
+        return on16 && any_stride % v == 0 && p.dim % (2 * v) == 0 && p.rot % (inter ? v : 2 * v) == 0;
+    };
+    if (fits(V)) return launch_rope<A, V>(p, inter, flags, stream);
+    if (V == 8 && fits(4)) return launch_rope<A, 4>(p, inter, flags, stream);
     return launch_rope<A, 1>(p, inter, flags, stream);
 }
 
