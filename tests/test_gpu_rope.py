@@ -49,6 +49,15 @@ def test_layouts(lean, act, kw):
     run_rope(lean, 12, 6, 3, 64, 48, act, "bf16", page=16, seed=2, **kw)
 
 
+@pytest.mark.parametrize("dim,rot", [(80, 40), (72, 24), (64, 24), (64, 8), (16, 8), (48, 20), (64, 4)])
+@pytest.mark.parametrize("kw", [dict(), dict(pad=4), dict(pad=8, k_out=True), dict(pad=4, in_place=True), dict(pad=2)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_run_widths(lean, dim, rot, kw, inter):
+    """Heads and strides that allow 16, 8 or 2 bytes at a time, the rotated part ending inside a wider run."""
+    for act in ("f32", "bf16", "f16"):
+        run_rope(lean, 7, 5, 2, dim, rot, act, "bf16", inter, page=16, seed=dim + rot, **kw)
+
+
 def test_q_or_kv_alone(lean):
     run_rope(lean, 4, 3, 0, 64, 64)
     run_rope(lean, 4, 0, 3, 64, 64, k_out=True)
