@@ -23,7 +23,8 @@
 //     time the bytes take (tcgen05 wants 64 rows or more; a group has 1 to 16).
 //     With up to 8 heads in a group, rows 0-7 hold the first part of q (or p) and
 //     rows 8-15 the second, so that one instruction serves both.
-//   - Running maximum and sum per warp; a warp's first and last group may be
+//   - Running maximum and sum per warp, the sums folded every 64 units so that long
+//     runs keep fp32's precision; a warp's first and last group may be
 //     shared with its neighbours: the warps of a block join through shared
 //     memory, blocks through the workspace and a second kernel, launched early,
 //     that adds the parts up in their order.
@@ -64,6 +65,7 @@ struct AttArgs {
     const int32_t *table, *lens;
     Shared *shared;
     float *warp_parts, *cta_parts;
+    f32x2 *folds;  // a warp's: the sums of its item up to the last fold
     int64_t qs, qhs, os, ohs, page_stride, place_stride, cache_hs, table_stride, n_pages;
     int n_seqs, hq, hkv, group, tiles, dim, page, paged, whole, width, window;
     int act;
@@ -84,6 +86,8 @@ struct AttShape {
 };
 // A part: maxima, sums and outputs of a group of H heads.
 __host__ __device__ constexpr int part_floats(int heads, int dp) { return heads * (dp + 4); }
+// What a warp folds: each lane's outputs, references and sums.
+__host__ __device__ constexpr int fold_floats(int heads, int dp) { return heads * (dp + 8); }
 // Shared memory of a block: queues; q at 256 (above); and, where it fits, a part per warp.
 constexpr int kMaxSmem = 232448 - 1536;  // of 227 KB, less static variables
 template <int DP>
@@ -253,9 +257,12 @@ struct Record {
 };
 
 // The most that running scores may exceed the reference of their exponentials by
-// before it moves, as a power of two: p stays below 2^8, and the accumulators are
-// rescaled a few times a run instead of in every unit with a new maximum.
+// before it moves, as a power of two: p stays below 2^8, and the sums are rescaled
+// (a rounding each) a few times a run instead of in every unit with a new maximum.
 constexpr float kSlack = 8.f;
+// Units after which a warp's sums of an item go to the workspace and begin again: sums of N units err by (kFold + N /
+// kFold) U in place of N U (U = 2^-24), for 2% of the traffic, in L2.
+constexpr int kFold = 64;
 // Units of a warp's time that joining blocks costs, and that an item costs beside its
 // units (q, the first maximum, the result): that many empty ones are counted to it
 // when the runs are cut.
@@ -313,6 +320,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     // registers for q as it was read: beside the accumulators, and all through the item before
     constexpr bool EARLY_Q = !WIDE && DP <= 128, AHEAD_Q = !WIDE && DP == 64;
     static_assert(PF * 4 <= S * STAGE, "a part fits a queue");
+    constexpr int AT = 2;  // steps of the values whose products are under way at once (more spill)
     extern __shared__ uint8_t queue_raw[];
     uint8_t *queue = queue_raw + (512 - smem_addr(queue_raw) % 512) % 512;
     __shared__ unsigned scan[W];
@@ -538,7 +546,11 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         // q as rows of the matrix instruction, part by part
         uint32_t qa[QSMEM ? 1 : KS][AREGS];
         uint32_t *q_shared = reinterpret_cast<uint32_t *>(queue + W * S * STAGE) + warp * (KS * AREGS * 32);
-        float acc[2 * KS][4], m[NH], l[NH], zs[NH];
+        // outputs and sums of the item since its last fold, with reference m
+        f32x2 acc[2 * KS][NH];
+        float m[NH], l[NH], zs[NH];
+        f32x2 *const folded = p.folds + ((int64_t)blockIdx.x * W + warp) * (fold_floats(H, DP) / 2) + lane;
+        int done = 0;  // units of the item so far
         bool fresh = true;
         int stage = 0;
         for (int u = u_lo; u < u_hi;) {
@@ -600,7 +612,8 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
 #pragma unroll
                 for (int j = 0; j < 2 * KS; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+                    for (int h = 0; h < NH; ++h) acc[j][h] = 0;
+                done = 0;
                 if (AHEAD_Q && u + cur.x.n - cur.c + kItemUnits < u_hi) {  // another item follows
                     const bool other_tile = cur.tile + 1 < p.tiles, other_head = other_tile || cur.kvh + 1 < p.hkv;
                     load_q(other_head ? cur.s : cur.s + 1, other_tile ? cur.kvh : other_head ? cur.kvh + 1 : 0,
@@ -611,7 +624,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
             __syncwarp();
 
             // ---- scores of 16 tokens: two tiles of 8
-            float sc[2][4] = {};
+            float sc[2][4] = {}, sd[2][4] = {};  // each in two sums: half as many instructions wait for one another
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
                 uint32_t b[4], a[AREGS];
@@ -624,35 +637,46 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     if (WIDE) {
 #pragma unroll
                         for (int part = 0; part < PARTS; ++part)
-                            mma<C>(sc[j], a[4 * part], a[4 * part + 1], a[4 * part + 2], a[4 * part + 3], b[2 * j],
-                                   b[2 * j + 1]);
+                            mma<C>(st & 1 ? sd[j] : sc[j], a[4 * part], a[4 * part + 1], a[4 * part + 2], a[4 * part + 3],
+                                   b[2 * j], b[2 * j + 1]);
                     } else {
                         mma<C>(sc[j], a[0], a[1], a[2], a[3], b[2 * j], b[2 * j + 1]);
-                        if (PARTS > 2) mma<C>(sc[j], a[AREGS - 2], 0u, a[AREGS - 1], 0u, b[2 * j], b[2 * j + 1]);
+                        if (PARTS > 2) mma<C>(sd[j], a[AREGS - 2], 0u, a[AREGS - 1], 0u, b[2 * j], b[2 * j + 1]);
                     }
                 }
             }
-            // ---- running maximum and sum; p as rows of the next instruction
-            const int t0 = cur.x.base + cur.c * kUnit + 2 * c4;
-            float e[NH][4], fall[NH];
-            bool moved = false;
+            // ---- running maximum and sum; p as rows of the next instruction (tokens are looked at one by one where
+            // not all of the unit is attended; always with two heads a thread, whose registers a branch would spill)
+            const int u0 = cur.x.base + cur.c * kUnit, t0 = u0 + 2 * c4;
+            const bool inside = u0 >= cur.x.start && u0 <= cur.x.len - kUnit;
+            float e[NH][4];
+            f32x2 fall2[NH];
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 float top = -CUDART_INF_F;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int j = i >> 1, tok = t0 + 8 * j + (i & 1);
-                    const float raw = WIDE ? sc[j][2 * h + (i & 1)] : sc[j][i & 1] + sc[j][2 + (i & 1)];
-                    e[h][i] = tok >= cur.x.start && tok < cur.x.len ? raw * zs[h] : -CUDART_INF_F;
-                    top = fmaxf(top, e[h][i]);
+                    const int j = i >> 1;
+                    const float raw = WIDE ? sc[j][2 * h + (i & 1)] + sd[j][2 * h + (i & 1)]
+                                           : sc[j][i & 1] + (sc[j][2 + (i & 1)] + sd[j][i & 1]);
+                    e[h][i] = raw * zs[h];
                 }
+                if (WIDE || !inside) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = t0 + 8 * (i >> 1) + (i & 1);
+                        if (tok < cur.x.start || tok >= cur.x.len) e[h][i] = -CUDART_INF_F;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, e[h][i]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // m: the reference of the exponentials, within kSlack of the largest score so far
                 const float mn = top > m[h] + kSlack || m[h] == -CUDART_INF_F ? top : m[h];
                 const float ms = mn == -CUDART_INF_F ? 0.f : mn;
-                moved |= mn != m[h];
-                fall[h] = ex2(m[h] - ms);
+                const float fall = ex2(m[h] - ms);
+                fall2[h] = pack2(fall, fall);
                 m[h] = mn;
                 float sum = 0.f;
 #pragma unroll
@@ -660,13 +684,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     e[h][i] = ex2(e[h][i] - ms);
                     sum += e[h][i];
                 }
-                l[h] = fmaf(l[h], fall[h], sum);
-            }
-            if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                for (int j = 0; j < 2 * KS; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j][i] *= fall[WIDE ? i >> 1 : 0];
+                l[h] = fmaf(l[h], fall, sum);
             }
             uint32_t pa[PARTS][4];
 #pragma unroll
@@ -676,23 +694,60 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     pa[part][h] = take_part<C>(e[h][0], e[h][1]);
                     pa[part][2 + h] = take_part<C>(e[h][2], e[h][3]);
                 }
-            // ---- values, two output tiles of 8 at a time
+            // ---- values: a unit's products summed from 0, then one addition in fp32 (the instruction cuts off what is
+            // small next to its accumulator: 8192 keys 17 nats below one left nothing there, 2.3e-4 of the output)
 #pragma unroll
-            for (int st = 0; st < KS; ++st) {
-                uint32_t b[4];
-                ldmatrix4_trans(b, (v_row + stage * STAGE) ^ (32 * st));
+            for (int st = 0; st < KS; st += AT) {
+                uint32_t b[AT][4];
+                float d[2 * AT][4] = {};
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float(&d)[4] = acc[2 * st + j];
-                    if (WIDE) {
+                for (int i = 0; i < AT; ++i) ldmatrix4_trans(b[i], (v_row + stage * STAGE) ^ (32 * (st + i)));
 #pragma unroll
-                        for (int part = 0; part < PARTS; ++part)
-                            mma<C>(d, pa[part][0], pa[part][1], pa[part][2], pa[part][3], b[2 * j], b[2 * j + 1]);
-                    } else {
-                        mma<C>(d, pa[0][0], pa[1][0], pa[0][2], pa[1][2], b[2 * j], b[2 * j + 1]);
-                        if (PARTS > 2) mma<C>(d, pa[PARTS - 1][0], 0u, pa[PARTS - 1][2], 0u, b[2 * j], b[2 * j + 1]);
+                for (int part = 0; part < (WIDE ? PARTS : PARTS - 1); ++part)
+#pragma unroll
+                    for (int i = 0; i < 2 * AT; ++i) {
+                        const uint32_t b0 = b[i / 2][2 * (i & 1)], b1 = b[i / 2][2 * (i & 1) + 1];
+                        if (WIDE) mma<C>(d[i], pa[part][0], pa[part][1], pa[part][2], pa[part][3], b0, b1);
+                        else if (part == 0) mma<C>(d[i], pa[0][0], pa[1][0], pa[0][2], pa[1][2], b0, b1);
+                        else mma<C>(d[i], pa[PARTS - 1][0], 0u, pa[PARTS - 1][2], 0u, b0, b1);
                     }
+#pragma unroll
+                for (int i = 0; i < 2 * AT; ++i) {
+                    f32x2(&a)[NH] = acc[2 * st + i];
+                    const f32x2 lo = pack2(d[i][0], d[i][1]), hi = pack2(d[i][2], d[i][3]);
+                    a[0] = fma2(a[0], fall2[0], WIDE ? lo : add2(lo, hi));
+                    if (WIDE) a[NH - 1] = fma2(a[NH - 1], fall2[NH - 1], hi);
                 }
+            }
+            // ---- what was folded of the item, added with the present reference
+            auto unfold = [&]() {
+                f32x2 f2[NH];
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    const float2 ml = unpack2(folded[(2 * KS * NH + h) * 32]);
+                    const float f = ex2(ml.x - (m[h] == -CUDART_INF_F ? 0.f : m[h]));
+                    l[h] = fmaf(ml.y, f, l[h]);
+                    f2[h] = pack2(f, f);
+                }
+#pragma unroll
+                for (int j = 0; j < 2 * KS; ++j)
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) acc[j][h] = fma2(folded[(j * NH + h) * 32], f2[h], acc[j][h]);
+            };
+            if (++done % kFold == 0) {
+                if (done > kFold) unfold();
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {
+                    folded[(2 * KS * NH + h) * 32] = pack2(m[h], l[h]);
+                    l[h] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 2 * KS; ++j)
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        folded[(j * NH + h) * 32] = acc[j][h];
+                        acc[j][h] = 0;
+                    }
             }
 
             // ---- the end of a group, or of the run
@@ -705,6 +760,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                 // a part that others continue: the run's last in this warp's own queue (nothing is under way to
                 // it any more)
                 float *part = reinterpret_cast<float *>(at_end ? tail_part : head_part);
+                if (done >= kFold) unfold();
                 __syncwarp();
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
@@ -721,9 +777,8 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     }
 #pragma unroll
                     for (int j = 0; j < 2 * KS; ++j) {
-                        float o[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) o[i] = (WIDE ? acc[j][2 * h + i] : acc[j][i] + acc[j][2 + i]) * inv;
+                        const float2 a = unpack2(acc[j][h]);
+                        const float o[2] = {a.x * inv, a.y * inv};
                         if (!whole) *reinterpret_cast<float2 *>(part + row * PO + 4 + 8 * j + 2 * c4) = make_float2(o[0], o[1]);
                         else if (8 * j < p.dim && LEAN_SPAN(at + 8 * j, 2, p.out_extent, p.err))
                             store_out<2>(p.out, at + 8 * j, p.act, o);
@@ -906,9 +961,8 @@ lean_status pick_dim(const AttArgs &p, int64_t flags, void *stream) {
     return pick_attend<C, 256>(p, flags, stream);
 }
 
-int64_t att_part_bytes(int64_t hq, int64_t hkv, int64_t dim) {
-    return 4 * part_floats(hq / hkv > 8 ? 16 : 8, dim <= 64 ? 64 : dim <= 128 ? 128 : 256);
-}
+int att_heads(int64_t hq, int64_t hkv) { return hq / hkv > 8 ? 16 : 8; }
+int att_dim(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
 bool att_sizes_ok(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim) {
     return n_seqs > 0 && hkv > 0 && hq > 0 && hq <= 65536 && hq % hkv == 0 && dim > 0 && dim % 8 == 0 &&
@@ -920,8 +974,9 @@ bool att_sizes_ok(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim) {
 extern "C" int64_t lean_paged_attention_workspace_bytes(int64_t n_seqs, int64_t n_q_heads, int64_t n_kv_heads,
                                                         int64_t head_dim) {
     if (!att_sizes_ok(n_seqs, n_q_heads, n_kv_heads, head_dim)) return -1;
-    // what blocks share, a part per warp and two per block, of the largest grid
-    return kSharedBytes + kAttMaxCtas * (8 + 2) * att_part_bytes(n_q_heads, n_kv_heads, head_dim);
+    // what blocks share, a part per warp and two per block, and what a warp folds, of the largest grid
+    const int h = att_heads(n_q_heads, n_kv_heads), d = att_dim(head_dim);
+    return kSharedBytes + (int64_t)kAttMaxCtas * 4 * ((8 + 2) * part_floats(h, d) + 8 * fold_floats(h, d));
 }
 
 extern "C" lean_status lean_paged_attention(const lean_attention_args *a, void *stream) {
@@ -962,7 +1017,9 @@ extern "C" lean_status lean_paged_attention(const lean_attention_args *a, void *
     uint8_t *ws = static_cast<uint8_t *>(a->workspace);
     p.shared = reinterpret_cast<Shared *>(ws);
     p.warp_parts = reinterpret_cast<float *>(ws + kSharedBytes);
-    p.cta_parts = p.warp_parts + kAttMaxCtas * 8 * att_part_bytes(a->n_q_heads, a->n_kv_heads, a->head_dim) / 4;
+    const int part = part_floats(att_heads(a->n_q_heads, a->n_kv_heads), att_dim(a->head_dim));
+    p.cta_parts = p.warp_parts + kAttMaxCtas * 8 * part;
+    p.folds = reinterpret_cast<f32x2 *>(p.cta_parts + kAttMaxCtas * 2 * part);
     p.qs = a->q_stride;
     p.qhs = a->q_head_stride;
     p.os = a->out_stride;

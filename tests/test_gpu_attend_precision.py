@@ -1,0 +1,77 @@
+"""lean_paged_attention where few keys outweigh very many: what the many give has
+to arrive in the output as it does in 64 bits.  Tolerances come from the kernel's
+arithmetic and are derived here, beside each test."""
+import math
+
+import pytest
+
+from lean_testlib import torch_cuda
+from step_testlib import U, close, dtype
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lean():
+    torch_cuda()
+    from block_quantized_weight_dot_gb300 import lean as L
+    return L
+
+
+def attend(lean, q, kc, vc, length, scale=1.0):
+    """The same pages for every sequence; (out, lse)."""
+    torch = torch_cuda()
+    n, hq, dim = q.shape
+    hkv = kc.shape[2]
+    table = torch.arange(kc.shape[0], device="cuda", dtype=torch.int32)[None].repeat(n, 1).contiguous()
+    lens = torch.full((n,), length, device="cuda", dtype=torch.int32)
+    out, lse = torch.full_like(q, 7.0), torch.full((n, hq), 7.0, device="cuda")
+    ws = torch.full((lean.lean_paged_attention_workspace_bytes(n, hq, hkv, dim),), 255, dtype=torch.uint8, device="cuda")
+    lean.lean_paged_attention(q, kc, vc, table, lens, out, scale=scale, lse=lse, workspace=ws)
+    return out, lse
+
+
+def run_one_key_outweighs(lean, cache, n, gap, place, hq, dim, seqs=2500):
+    """One key `gap` nats above n - 1 equal ones, in so many sequences that single warps walk whole ones (with 2500, every
+    warp's run has one).  Values: 1 for all keys in the first half of the dimensions; in the second 1 for the many and 0
+    for the one."""
+    torch = torch_cuda()
+    page = 128
+    kc = torch.zeros((-(-n // page), page, 1, dim), device="cuda", dtype=dtype(cache))
+    vc = torch.full_like(kc, float("nan"))
+    vc.view(-1, dim)[:n] = 1
+    at = {"first": 0, "middle": n // 2, "last": n - 1}[place]
+    kc.view(-1, dim)[at, 0] = gap
+    vc.view(-1, dim)[at, dim // 2:] = 0
+    q = torch.zeros((seqs, hq, dim), device="cuda")
+    q[:, :, 0] = 1
+    out, lse = attend(lean, q, kc, vc, n)
+    tail = (n - 1) * math.exp(-gap)
+    want = torch.ones((dim,), dtype=torch.float64, device="cuda")
+    want[dim // 2:] = tail / (1 + tail)
+    # A warp adds its units of 16 tokens in chains of 64, and the chains' sums in a chain of their own, half an ulp each;
+    # a unit's 16 products are cut off at 2^-24 of the largest of them or below
+    units = -(-n // 16)
+    chain = (min(64, units) + units / 64 + 2) * U + 16 * U
+    # e^(z - m): three roundings of an argument of `gap` nats, and the power of two itself, 2^-22
+    power = 3 * U * gap + 2.0 ** -22
+    tol = torch.full((dim,), 2 * chain + 4 * U, dtype=torch.float64, device="cuda")  # sum and normaliser
+    tol[dim // 2:] = want[dim // 2:] * (2 * chain + 2 * power + 4 * U)
+    what = "%s n %d gap %g %s hq %d dim %d" % (cache, n, gap, place, hq, dim)
+    close(out, want, tol, what)
+    want_lse = torch.full((1,), gap + math.log1p(tail), dtype=torch.float64, device="cuda")
+    close(lse, want_lse, chain + power + 4 * U * (1 + gap), what + " lse")
+
+
+@pytest.mark.parametrize("gap", [10.0, 14.0, 17.375])
+@pytest.mark.parametrize("n", [1008, 1024, 1025, 2048, 8192, 131072])
+def test_one_key_outweighs_many_bf16(lean, n, gap):
+    run_one_key_outweighs(lean, "bf16", n, gap, "first", 4, 64)
+
+
+@pytest.mark.parametrize("place", ["first", "middle", "last"])
+@pytest.mark.parametrize("hq", [1, 8, 9, 16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_one_key_outweighs_many_bf16_everywhere(lean, dim, hq, place):
+    run_one_key_outweighs(lean, "bf16", 8192, 17.375, place, hq, dim)
+    run_one_key_outweighs(lean, "bf16", 8192, 17.375, place, hq, dim, seqs=1)
