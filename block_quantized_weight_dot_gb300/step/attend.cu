@@ -31,7 +31,8 @@
 //
 // q and p are split into parts of the cache's type, x = x0 + x1 (+ x2), 8 (bf16)
 // or 11 bits each: three parts for fp32 q and out, which leave nothing of fp32's
-// 24 bits behind; two for 16-bit ones, whose rounding of out is larger.  q is
+// 24 bits behind; two for 16-bit ones, whose rounding of out is larger.  (p in f16:
+// of probabilities near the largest; small ones are held to 2^-38 of it.)  q is
 // first scaled by a power of two so that no part can overflow or vanish.
 //
 // Measured (GB300, calls in a graph): 384 sequences of 1 to 8192 tokens, 32 query
@@ -257,9 +258,20 @@ struct Record {
 };
 
 // The most that running scores may exceed the reference of their exponentials by
-// before it moves, as a power of two: p stays below 2^8, and the sums are rescaled
-// (a rounding each) a few times a run instead of in every unit with a new maximum.
-constexpr float kSlack = 8.f;
+// before it moves, as a power of two: the sums are rescaled (a rounding each) a few
+// times a run instead of in every unit with a new maximum.  And what probabilities
+// are multiplied by before they are split: bf16 has fp32's range, f16 ends at 2^-24
+// below and 2^16 above, so there they lie as high as they can, up to 2^15, and what
+// is lost of one is 2^-38 of the reference at most (without: one below 2^-25 left
+// nothing, 8192 keys 17 nats below one 2.3e-4 of the output).
+template <typename C>
+struct ProbRange {
+    static constexpr float kSlack = 8.f, kLift = 1.f;
+};
+template <>
+struct ProbRange<__half> {
+    static constexpr float kSlack = 2.f, kLift = 8192.f;
+};
 // Units after which a warp's sums of an item go to the workspace and begin again: sums of N units err by (kFold + N /
 // kFold) U in place of N U (U = 2^-24), for 2% of the traffic, in L2.
 constexpr int kFold = 64;
@@ -672,8 +684,9 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                 for (int i = 0; i < 4; ++i) top = fmaxf(top, e[h][i]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // m: the reference of the exponentials, within kSlack of the largest score so far
-                const float mn = top > m[h] + kSlack || m[h] == -CUDART_INF_F ? top : m[h];
+                // m: the reference of the exponentials, within kSlack of the largest score so far (the difference of
+                // neighbours is exact; from -inf, infinite or NaN)
+                const float mn = top - m[h] <= ProbRange<C>::kSlack ? m[h] : top;
                 const float ms = mn == -CUDART_INF_F ? 0.f : mn;
                 const float fall = ex2(m[h] - ms);
                 fall2[h] = pack2(fall, fall);
@@ -681,7 +694,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    e[h][i] = ex2(e[h][i] - ms);
+                    e[h][i] = ex2(e[h][i] - ms) * ProbRange<C>::kLift;
                     sum += e[h][i];
                 }
                 l[h] = fmaf(l[h], fall, sum);
@@ -769,7 +782,8 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                     const int row = r + 8 * h;
                     if (whole && row >= nh) continue;
-                    const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                    const float inv = !whole ? 1.f / ProbRange<C>::kLift : sum == 0.f ? 0.f : 1.f / sum;
+                    sum *= 1.f / ProbRange<C>::kLift;
                     const int64_t at = (int64_t)cur.s * p.os + (int64_t)(h0 + row) * p.ohs + 2 * c4;
                     if (c4 == 0) {
                         if (!whole) *reinterpret_cast<float2 *>(part + row * PO) = make_float2(m[h], sum);

@@ -57,10 +57,12 @@ def run_one_key_outweighs(lean, cache, n, gap, place, hq, dim, seqs=2500):
     power = 3 * U * gap + 2.0 ** -22
     tol = torch.full((dim,), 2 * chain + 4 * U, dtype=torch.float64, device="cuda")  # sum and normaliser
     tol[dim // 2:] = want[dim // 2:] * (2 * chain + 2 * power + 4 * U)
+    if cache == "f16":  # a probability is held to 2^-38 of a reference that is the largest one or up to 4 times smaller
+        tol += n * 2.0 ** -38
     what = "%s n %d gap %g %s hq %d dim %d" % (cache, n, gap, place, hq, dim)
-    close(out, want, tol, what)
+    close(out, want.expand_as(out), tol.expand_as(out), what)
     want_lse = torch.full((1,), gap + math.log1p(tail), dtype=torch.float64, device="cuda")
-    close(lse, want_lse, chain + power + 4 * U * (1 + gap), what + " lse")
+    close(lse, want_lse.expand_as(lse), chain + power + 4 * U * (1 + gap), what + " lse")
 
 
 @pytest.mark.parametrize("gap", [10.0, 14.0, 17.375])
@@ -75,3 +77,41 @@ def test_one_key_outweighs_many_bf16(lean, n, gap):
 def test_one_key_outweighs_many_bf16_everywhere(lean, dim, hq, place):
     run_one_key_outweighs(lean, "bf16", 8192, 17.375, place, hq, dim)
     run_one_key_outweighs(lean, "bf16", 8192, 17.375, place, hq, dim, seqs=1)
+
+
+@pytest.mark.parametrize("gap", [10.0, 14.0, 17.375])
+@pytest.mark.parametrize("n", [1008, 1025, 8192, 131072])
+def test_one_key_outweighs_many_f16(lean, n, gap):
+    """f16 holds nothing below 2^-24: e^-17.4 is 2^-25."""
+    run_one_key_outweighs(lean, "f16", n, gap, "first", 4, 64)
+
+
+@pytest.mark.parametrize("place", ["middle", "last"])
+@pytest.mark.parametrize("hq", [8, 16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_one_key_outweighs_many_f16_everywhere(lean, dim, hq, place):
+    run_one_key_outweighs(lean, "f16", 8192, 17.375, place, hq, dim)
+    run_one_key_outweighs(lean, "f16", 8192, 17.375, place, hq, dim, seqs=1)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", [3e5, 5e7, 2e9])
+def test_large_scores(lean, cache, scale):
+    """Scores so large that a reference below the maximum, or a sum with the slack, would round past it: rising and
+    falling ones, and ties of the largest, whose values' mean is the output."""
+    torch = torch_cuda()
+    n, dim = 512, 64
+    kc, vc = (torch.zeros((4, 128, 1, dim), device="cuda", dtype=dtype(cache)) for _ in range(2))
+    steps = torch.arange(n, device="cuda").float() / 512  # exact in both types up to 256 / 512
+    kc.view(-1, dim)[:, 0] = steps.to(kc.dtype)
+    vc.view(-1, dim)[:, 0] = (torch.arange(n, device="cuda") % 8).to(vc.dtype)
+    q = torch.zeros((2, 4, dim), device="cuda")
+    q[0, :, 0], q[1, :, 0] = 1, -1
+    out, lse = attend(lean, q, kc, vc, n, scale=scale)
+    k = kc.view(-1, dim)[:, 0].double()
+    for s, best in ((0, k.max()), (1, k.min())):
+        z = scale * best * (1 if s == 0 else -1)
+        want = vc.view(-1, dim)[:, 0].double()[k == best].mean()
+        close(out[s, :, 0], want.expand(4), 4 * U * want.abs(), "large scores")
+        ties = math.log(int((k == best).sum()))
+        close(lse[s], (z + ties).expand(4), 8 * U * (z.abs() + ties), "large scores lse")
