@@ -33,7 +33,8 @@
 // or 11 bits each: three parts for fp32 q and out, which leave nothing of fp32's
 // 24 bits behind; two for 16-bit ones, whose rounding of out is larger.  (p in f16:
 // of probabilities near the largest; small ones are held to 2^-38 of it.)  q is
-// first scaled by a power of two so that no part can overflow or vanish.
+// first scaled by a power of two so that no part can overflow or vanish (f16: none
+// above 2^-38 of the largest element).
 //
 // Measured (GB300, calls in a graph): 384 sequences of 1 to 8192 tokens, 32 query
 // and 4 kv heads of 64, bf16: 67 us, 5.5 TB/s of the 6.78 that a copy reaches; one
@@ -263,14 +264,17 @@ struct Record {
 // are multiplied by before they are split: bf16 has fp32's range, f16 ends at 2^-24
 // below and 2^16 above, so there they lie as high as they can, up to 2^15, and what
 // is lost of one is 2^-38 of the reference at most (without: one below 2^-25 left
-// nothing, 8192 keys 17 nats below one 2.3e-4 of the output).
+// nothing, 8192 keys 17 nats below one 2.3e-4 of the output).  The same for q, whose
+// largest element is brought to 2^kLiftQ.
 template <typename C>
-struct ProbRange {
+struct PartRange {
     static constexpr float kSlack = 8.f, kLift = 1.f;
+    static constexpr int kLiftQ = 0;
 };
 template <>
-struct ProbRange<__half> {
+struct PartRange<__half> {
     static constexpr float kSlack = 2.f, kLift = 8192.f;
+    static constexpr int kLiftQ = 14;
 };
 // Units after which a warp's sums of an item go to the workspace and begin again: sums of N units err by (kFold + N /
 // kFold) U in place of N U (U = 2^-24), for 2% of the traffic, in L2.
@@ -581,9 +585,10 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     for (int i = 0; i < 2 * KS; ++i) top = fmaxf(top, fmaxf(fabsf(f[h][i].x), fabsf(f[h][i].y)));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    // a power of two that brings the largest element near 1 (1 where there is none)
+                    // a power of two that brings the largest element near 1, or as high as f16 takes it, so that its
+                    // steps below are small next to the others as well (1 where there is no largest element)
                     const int e = (int)(__float_as_uint(top) >> 23);
-                    const int fe = e == 0 || e == 255 ? 127 : max(1, 254 - e);
+                    const int fe = e == 0 || e == 255 ? 127 : min(253, max(1, 254 + PartRange<C>::kLiftQ - e));
                     const float up = __uint_as_float((uint32_t)fe << 23);
                     zs[h] = p.scale_log2 * __uint_as_float((uint32_t)(254 - fe) << 23);
                     m[h] = -CUDART_INF_F;
@@ -686,7 +691,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // m: the reference of the exponentials, within kSlack of the largest score so far (the difference of
                 // neighbours is exact; from -inf, infinite or NaN)
-                const float mn = top - m[h] <= ProbRange<C>::kSlack ? m[h] : top;
+                const float mn = top - m[h] <= PartRange<C>::kSlack ? m[h] : top;
                 const float ms = mn == -CUDART_INF_F ? 0.f : mn;
                 const float fall = ex2(m[h] - ms);
                 fall2[h] = pack2(fall, fall);
@@ -694,7 +699,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    e[h][i] = ex2(e[h][i] - ms) * ProbRange<C>::kLift;
+                    e[h][i] = ex2(e[h][i] - ms) * PartRange<C>::kLift;
                     sum += e[h][i];
                 }
                 l[h] = fmaf(l[h], fall, sum);
@@ -782,8 +787,8 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                     const int row = r + 8 * h;
                     if (whole && row >= nh) continue;
-                    const float inv = !whole ? 1.f / ProbRange<C>::kLift : sum == 0.f ? 0.f : 1.f / sum;
-                    sum *= 1.f / ProbRange<C>::kLift;
+                    const float inv = !whole ? 1.f / PartRange<C>::kLift : sum == 0.f ? 0.f : 1.f / sum;
+                    sum *= 1.f / PartRange<C>::kLift;
                     const int64_t at = (int64_t)cur.s * p.os + (int64_t)(h0 + row) * p.ohs + 2 * c4;
                     if (c4 == 0) {
                         if (!whole) *reinterpret_cast<float2 *>(part + row * PO) = make_float2(m[h], sum);

@@ -218,8 +218,8 @@ lean_status lean_kv_pages(const lean_kv_pages_args *args, void *stream);
  * q and p are split in parts of the cache's type, three for fp32 q and out and
  * two for 16-bit ones, and sums are fp32, so that fp32 q keeps its precision: out
  * errs by about 2^-17 of sum p |v|, and by fp32's rounding of the scores.  With an
- * f16 cache each p errs by up to 2^-38 of the sequence's largest one as well (f16
- * has no smaller steps).
+ * f16 cache each p errs by up to 2^-38 of the sequence's largest one as well, and
+ * each element of q by 2^-38 of its head's largest (f16 has no smaller steps).
  * q, out and the caches: 16-byte aligned, strides multiples of 8 elements.
  * workspace: lean_paged_attention_workspace_bytes() bytes, 256-byte aligned,
  * any contents.  Calls that may run at the same time must not share one.

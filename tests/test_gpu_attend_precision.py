@@ -6,7 +6,7 @@ import math
 import pytest
 
 from lean_testlib import torch_cuda
-from step_testlib import U, close, dtype
+from step_testlib import U, close, dtype, gen, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,67 @@ def test_large_scores(lean, cache, scale):
         close(out[s, :, 0], want.expand(4), 4 * U * want.abs(), "large scores")
         ties = math.log(int((k == best).sum()))
         close(lse[s], (z + ties).expand(4), 8 * U * (z.abs() + ties), "large scores lse")
+
+
+def run_lone_keys(lean, cache, outlier, hq, dim):
+    """Sequence s has one key, 1 in dimension s + 1: its lse is that element of q, whatever the size of element 0."""
+    torch = torch_cuda()
+    n = dim - 1
+    kc = torch.zeros((n, 16, 1, dim), device="cuda", dtype=dtype(cache))
+    kc[torch.arange(n), 0, 0, torch.arange(n) + 1] = 1
+    vc = torch.ones_like(kc)
+    q = normal(gen(dim + hq), n, hq, dim)
+    q[:, :, 0] = outlier
+    table = torch.arange(n, device="cuda", dtype=torch.int32)[:, None].contiguous()
+    lens = torch.ones((n,), device="cuda", dtype=torch.int32)
+    out, lse = torch.empty_like(q), torch.empty((n, hq), device="cuda")
+    ws = torch.zeros(lean.lean_paged_attention_workspace_bytes(n, hq, 1, dim), dtype=torch.uint8, device="cuda")
+    lean.lean_paged_attention(q, kc, vc, table, lens, out, scale=1.0, lse=lse, workspace=ws)
+    want = q[torch.arange(n), :, torch.arange(n) + 1].double()
+    # three parts leave less than U of an element; f16 has steps of 2^-24, which scaling the largest element to 2^14 or
+    # more makes 2^-38 of it; scale * log2 e, the product with it, the product with ln 2 and the results round
+    tol = 8 * U * want.abs() + (2.0 ** -38 * q.abs().amax(-1).double() if cache == "f16" else 0)
+    close(lse, want, tol, "lone keys %s outlier %g hq %d dim %d" % (cache, outlier, hq, dim))
+    return q, want, tol
+
+
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_third_part_of_q(lean, dim, hq):
+    q, want, tol = run_lone_keys(lean, "bf16", 1.0, hq, dim)
+    two = want.bfloat16().double()
+    two = two + (want - two).bfloat16().double()
+    assert bool(((two - want).abs() > tol).any())  # two parts would not do
+
+
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("cache,outlier", [("bf16", 4096.0), ("f16", 1.0), ("f16", 300.0), ("f16", -4096.0), ("f16", 60000.0)])
+def test_one_large_element_of_q(lean, cache, outlier, dim, hq):
+    """An element of q that is far larger than the others must not cost them their lower bits."""
+    run_lone_keys(lean, cache, outlier, hq, dim)
+
+
+@pytest.mark.parametrize("hq", [4, 16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("cache", ["bf16", "f16"])
+def test_third_part_of_p(lean, cache, dim, hq):
+    """Key and value j are 1 in dimension j alone: out is the softmax of q."""
+    torch = torch_cuda()
+    n, seqs = 48, 64
+    kc = torch.zeros((3, 16, 1, dim), device="cuda", dtype=dtype(cache))
+    kc.view(48, dim)[torch.arange(n), torch.arange(n)] = 1
+    q = torch.zeros((seqs, hq, dim), device="cuda")
+    q[:, :, :n] = -0.5 * torch.rand((seqs, hq, n), generator=gen(7), device="cuda")
+    out, lse = attend(lean, q, kc, kc.clone(), n)
+    want = torch.softmax(q[:, :, :n].double(), -1)
+    # a score of half a nat at most rounds three times, its power is good to 2^-22; the sum has 48 terms in chains of
+    # 12 and 3; then the parts' products, their sum and the quotient
+    tol = (2 * (3 * 0.5 + 4) + 16 + 4) * U * want
+    close(out[:, :, :n], want, tol, "softmax as output")
+    assert not bool(out[:, :, n:].any())
+    if cache == "bf16":
+        p = torch.exp(q[:, :, :n].double() - q[:, :, :n].double().amax(-1, keepdim=True))
+        two = p.bfloat16().double()
+        two = two + (p - two).bfloat16().double()
+        assert bool(((two - p).abs() * (want / p) > tol).any())  # two parts would not do
