@@ -463,18 +463,21 @@ def lean_rope_append(q, k, v, positions, slots, turns, q_out, k_cache, v_cache, 
 
 def lean_kv_pages(lens, targets, block_table, free_ring, ring_state, page_size: int, lens_out, ring_state_out,
                   status, token_starts, slots=None, positions=None, token_seqs=None, flags: int = 0,
-                  stream=None) -> None:
+                  stream=None, max_tokens=None) -> None:
     """Sequences go from `lens` to `targets` tokens: pages are taken from and
     given back to the free ring, block_table [seqs, width] follows, and the new
     tokens' slots, positions and sequences are written as one packed batch
-    (int32 throughout)."""
+    (int32 throughout).  Each of the three may be left out.  max_tokens: the most
+    new tokens of a call, past which sequences fail; None: as many as the maps
+    given hold (without any: 0, so that only sequences that do not grow succeed;
+    2 ** 31 - 1 sets no limit)."""
     if _i32 is None:
         _types()
     n = lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table: [%d, width] is wanted" % n)
     some = slots if slots is not None else positions if positions is not None else token_seqs
-    most = some.numel() if some is not None else 0
+    most = max_tokens if max_tokens is not None else some.numel() if some is not None else 0
     i32 = _i32
     table, stride = _array(block_table, block_table.shape, i32, "block_table")
     args = _PAGES.pack(n, page_size, most, _plain(lens, n, i32, "lens"), _plain(targets, n, i32, "targets"), table,

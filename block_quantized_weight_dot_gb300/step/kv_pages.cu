@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesArgs
         }
         __syncthreads();
     }
-    // the unused end of the batch
-    const int64_t used = tokens < p.max_tokens ? tokens : p.max_tokens;
+    // the unused end of the batch (a limit without maps may be far past any batch)
+    const int64_t used = p.slots || p.positions || p.seqs ? min(tokens, (int64_t)p.max_tokens) : p.max_tokens;
     for (int64_t i = used + (int64_t)blockIdx.x * kPagesThreads + threadIdx.x; i < p.max_tokens;
          i += (int64_t)G * kPagesThreads) {
         if (p.slots) p.slots[i] = -1;

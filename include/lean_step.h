@@ -177,7 +177,8 @@ lean_status lean_rope_append(const lean_rope_args *args, void *stream);
  * tokens get slot -1:
  *   1  the ring ran out (then every later sequence that needs pages fails too)
  *   2  more pages than a row of the table has
- *   3  its tokens end past max_tokens (those past it are not written)
+ *   3  its tokens end past max_tokens (those past it are not written), also when
+ *      no map is wanted (2^31 - 1 then sets no limit)
  *   4  a negative length, a ring_state outside the ring, or more pages given back
  *      than the ring has room for (then every later one that gives any fails too)
  * lens_out and ring_state_out must not overlap lens, targets or ring_state (use
