@@ -330,8 +330,8 @@ def lean_wait_selftest(limit_us: int, stream=None) -> None:
 #
 # These take torch tensors on the GPU and read sizes, strides and element types
 # off them (a caller without torch fills the C structs); every output is the
-# caller's.  A tensor of a wrong shape, type or device is a ValueError, what the
-# library refuses a LeanError.
+# caller's.  A tensor of a wrong shape or type, or on another device than the
+# current GPU, is a ValueError, what the library refuses a LeanError.
 
 _NORM = struct.Struct("<4qQqQqQqQQQqQq2dq")
 _ROPE = struct.Struct("<8q" + "Q2q" * 5 + "3Q2Q5qdq")
@@ -339,14 +339,23 @@ _PAGES = struct.Struct("<3q3Q2qQqQ2Q5Qq")
 _ATTENTION = struct.Struct("<6qQ2q2Q5qQ2qQQ2qQdqQqq")
 _LOGPROBS = struct.Struct("<3qQqQdq5QQqq")
 _dtypes = {}
-_i32 = _f32 = _i64t = None  # torch's, once a call has needed them
+_i32 = _f32 = _i64t = _u8 = None  # torch's, once a call has needed them
+_device = None
 
 
-def _types():
-    global _i32, _f32, _i64t
+def _here():
+    """Index of the current GPU, as tensors on it have it; -2 without any."""
+    global _i32, _f32, _i64t, _u8, _device
+    if _device is not None:
+        return _device()
     import torch
     _dtypes.update({torch.float32: LEAN_F32, torch.bfloat16: LEAN_BF16, torch.float16: LEAN_F16})
-    _i32, _f32, _i64t = torch.int32, torch.float32, torch.int64
+    _i32, _f32, _i64t, _u8 = torch.int32, torch.float32, torch.int64, torch.uint8
+    if not torch.cuda.is_available():
+        return -2
+    here = torch.cuda.current_device()
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return here
 
 
 def _dtype(t):
@@ -356,26 +365,36 @@ def _dtype(t):
     return code
 
 
-def _array(t, shape, dtype, name):
-    """(address, stride of each dimension but the last) of a GPU tensor of that
-    shape and element type, its last dimension contiguous; zeros for None."""
+def _array(t, shape, dtype, name, here):
+    """(address, stride of each dimension but the last) of a tensor on the current GPU of
+    that shape and element type, its last dimension contiguous; zeros for None."""
     if t is None:
         return (0,) * len(shape)
     st = t.stride()
-    if t.shape == shape and t.dtype is dtype and t.is_cuda and (st[-1] == 1 or shape[-1] == 1):
+    if t.shape == shape and t.dtype is dtype and t.get_device() == here and (st[-1] == 1 or shape[-1] == 1):
         return (t.data_ptr(),) + st[:-1]
-    raise ValueError("%s is %s %s on %s, strides %s: %s %s on the GPU is wanted, the last dimension contiguous"
+    raise ValueError("%s is %s %s on %s, strides %s: %s %s on the current GPU is wanted, the last dimension contiguous"
                      % (name, t.dtype, tuple(t.shape), t.device, st, dtype, tuple(shape)))
 
 
-def _plain(t, size, dtype, name):
-    """Address of a contiguous GPU tensor of `size` elements of that type; 0 for None."""
+def _plain(t, size, dtype, name, here):
+    """Address of a contiguous tensor on the current GPU of `size` elements of that type; 0 for None."""
     if t is None:
         return 0
-    if t.dtype is dtype and t.numel() == size and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.numel() == size and t.get_device() == here and t.is_contiguous():
         return t.data_ptr()
-    raise ValueError("%s is %s %s on %s: %d contiguous elements of %s on the GPU are wanted"
+    raise ValueError("%s is %s %s on %s: %d contiguous elements of %s on the current GPU are wanted"
                      % (name, t.dtype, tuple(t.shape), t.device, size, dtype))
+
+
+def _workspace(t, here):
+    """(address, bytes) of a workspace; zeros for None."""
+    if t is None:
+        return 0, 0
+    if t.dtype is _u8 and t.get_device() == here and t.is_contiguous():
+        return t.data_ptr(), t.numel()
+    raise ValueError("workspace is %s %s on %s, strides %s: contiguous bytes (uint8) on the current GPU are wanted"
+                     % (t.dtype, tuple(t.shape), t.device, t.stride()))
 
 
 def lean_residual_norm(x, h, w, h_out, y, eps: float = 1e-6, post_w=None, gate=None,
@@ -385,8 +404,7 @@ def lean_residual_norm(x, h, w, h_out, y, eps: float = 1e-6, post_w=None, gate=N
     post_w the weights of the norm after the block (None: x as it is), gate
     [rows, width] or [width] (None: 1), w of the norm before the next one.
     h_out or y may be None."""
-    if _i32 is None:
-        _types()
+    here = _here()
     one = x if x is not None else h
     if one is None or one.dim() != 2:
         raise ValueError("x or h: [rows, width] is wanted")
@@ -398,12 +416,13 @@ def lean_residual_norm(x, h, w, h_out, y, eps: float = 1e-6, post_w=None, gate=N
     if gate is None:
         g = (0, 0)
     elif gate.dim() == 1 or gate.shape[0] == 1:
-        g = _array(gate.reshape(1, -1), (1, width), at, "gate")[0], 0
+        g = _array(gate.reshape(1, -1), (1, width), at, "gate", here)[0], 0
     else:
-        g = _array(gate, shape, at, "gate")
-    args = _NORM.pack(rows, width, _dtype(act), _dtype(res), *_array(x, shape, at, "x"), *_array(h, shape, rt, "h"), *g,
-                      _plain(post_w, width, _f32, "post_w"), _plain(w, width, _f32, "w"),
-                      *_array(h_out, shape, rt, "h_out"), *_array(y, shape, at, "y"), eps, res_scale, flags)
+        g = _array(gate, shape, at, "gate", here)
+    args = _NORM.pack(rows, width, _dtype(act), _dtype(res), *_array(x, shape, at, "x", here),
+                      *_array(h, shape, rt, "h", here), *g, _plain(post_w, width, _f32, "post_w", here),
+                      _plain(w, width, _f32, "w", here),
+                      *_array(h_out, shape, rt, "h_out", here), *_array(y, shape, at, "y", here), eps, res_scale, flags)
     st = _lib.lean_residual_norm(args, _stream(stream))
     if st:
         raise LeanError("lean_residual_norm", st)
@@ -433,8 +452,7 @@ def lean_rope_append(q, k, v, positions, slots, turns, q_out, k_cache, v_cache, 
     """Rotate the first rot_dim elements of each head of q and k ([tokens, heads,
     dim]) to `positions`, into q_out (and k_out), and store k and v at `slots` of
     the caches ([pages, page_size, kv_heads, dim], strides of their own)."""
-    if _i32 is None:
-        _types()
+    here = _here()
     one = q if q is not None else k
     if one is None or one.dim() != 3:
         raise ValueError("q or k: [tokens, heads, dim] is wanted")
@@ -445,17 +463,17 @@ def lean_rope_append(q, k, v, positions, slots, turns, q_out, k_cache, v_cache, 
     qs, ks = (n, hq, dim), (n, hkv, dim)
     if k_cache is not None:
         pages, page = k_cache.shape[:2]
-        kc = _array(k_cache, (pages, page, hkv, dim), k_cache.dtype, "k_cache")
-        if _array(v_cache, (pages, page, hkv, dim), k_cache.dtype, "v_cache")[1:] != kc[1:]:
+        kc = _array(k_cache, (pages, page, hkv, dim), k_cache.dtype, "k_cache", here)
+        if _array(v_cache, (pages, page, hkv, dim), k_cache.dtype, "v_cache", here)[1:] != kc[1:]:
             raise ValueError("k_cache and v_cache have different strides")
         cache, cdt, vc = (pages, page) + kc[1:], _dtype(k_cache), v_cache.data_ptr()
     else:
         cache, cdt, kc, vc = (0,) * 5, 0, (0,), 0
-    args = _ROPE.pack(n, hq, hkv, dim, rot_dim, 1 if interleaved else 0, _dtype(one), cdt, *_array(q, qs, at, "q"),
-                      *_array(k, ks, at, "k"), *_array(v, ks, at, "v"), *_array(q_out, qs, at, "q_out"),
-                      *_array(k_out, ks, at, "k_out"), _plain(positions, n, _i32, "positions"),
-                      _plain(slots, n, _i32, "slots"), _plain(turns, rot_dim // 2, _i64t, "turns"),
-                      kc[0], vc, *cache, rot_scale, flags)
+    args = _ROPE.pack(n, hq, hkv, dim, rot_dim, 1 if interleaved else 0, _dtype(one), cdt,
+                      *_array(q, qs, at, "q", here), *_array(k, ks, at, "k", here), *_array(v, ks, at, "v", here),
+                      *_array(q_out, qs, at, "q_out", here), *_array(k_out, ks, at, "k_out", here),
+                      _plain(positions, n, _i32, "positions", here), _plain(slots, n, _i32, "slots", here),
+                      _plain(turns, rot_dim // 2, _i64t, "turns", here), kc[0], vc, *cache, rot_scale, flags)
     st = _lib.lean_rope_append(args, _stream(stream))
     if st:
         raise LeanError("lean_rope_append", st)
@@ -471,21 +489,22 @@ def lean_kv_pages(lens, targets, block_table, free_ring, ring_state, page_size: 
     new tokens of a call, past which sequences fail; None: as many as the maps
     given hold (without any: 0, so that only sequences that do not grow succeed;
     2 ** 31 - 1 sets no limit)."""
-    if _i32 is None:
-        _types()
+    here = _here()
     n = lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table: [%d, width] is wanted" % n)
     some = slots if slots is not None else positions if positions is not None else token_seqs
     most = max_tokens if max_tokens is not None else some.numel() if some is not None else 0
     i32 = _i32
-    table, stride = _array(block_table, block_table.shape, i32, "block_table")
-    args = _PAGES.pack(n, page_size, most, _plain(lens, n, i32, "lens"), _plain(targets, n, i32, "targets"), table,
-                       block_table.shape[1], stride, _plain(free_ring, free_ring.numel(), i32, "free_ring"),
-                       free_ring.numel(), _plain(ring_state, 2, i32, "ring_state"), _plain(lens_out, n, i32, "lens_out"),
-                       _plain(ring_state_out, 2, i32, "ring_state_out"), _plain(status, n, i32, "status"),
-                       _plain(token_starts, n + 1, i32, "token_starts"), _plain(slots, most, i32, "slots"),
-                       _plain(positions, most, i32, "positions"), _plain(token_seqs, most, i32, "token_seqs"), flags)
+    table, stride = _array(block_table, block_table.shape, i32, "block_table", here)
+    args = _PAGES.pack(n, page_size, most, _plain(lens, n, i32, "lens", here), _plain(targets, n, i32, "targets", here),
+                       table, block_table.shape[1], stride,
+                       _plain(free_ring, free_ring.numel(), i32, "free_ring", here), free_ring.numel(),
+                       _plain(ring_state, 2, i32, "ring_state", here), _plain(lens_out, n, i32, "lens_out", here),
+                       _plain(ring_state_out, 2, i32, "ring_state_out", here), _plain(status, n, i32, "status", here),
+                       _plain(token_starts, n + 1, i32, "token_starts", here), _plain(slots, most, i32, "slots", here),
+                       _plain(positions, most, i32, "positions", here),
+                       _plain(token_seqs, most, i32, "token_seqs", here), flags)
     st = _lib.lean_kv_pages(args, _stream(stream))
     if st:
         raise LeanError("lean_kv_pages", st)
@@ -501,23 +520,21 @@ def lean_paged_attention(q, k_cache, v_cache, block_table, seq_lens, out, scale:
     caches as for lean_rope_append, block_table [seqs, width], lse [seqs, heads]
     (None: not wanted); workspace: a uint8 tensor of
     lean_paged_attention_workspace_bytes."""
-    if _i32 is None:
-        _types()
+    here = _here()
     shape, at, ct = q.shape, q.dtype, k_cache.dtype
     n, hq, dim = shape
     pages, page, hkv = k_cache.shape[:3]
-    kc = _array(k_cache, (pages, page, hkv, dim), ct, "k_cache")
-    vc = _array(v_cache, (pages, page, hkv, dim), ct, "v_cache")
+    kc = _array(k_cache, (pages, page, hkv, dim), ct, "k_cache", here)
+    vc = _array(v_cache, (pages, page, hkv, dim), ct, "v_cache", here)
     if vc[1:] != kc[1:]:
         raise ValueError("k_cache and v_cache have different strides")
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table: [%d, width] is wanted" % n)
-    table = _array(block_table, block_table.shape, _i32, "block_table")
-    args = _ATTENTION.pack(n, hq, hkv, dim, _dtype(q), _dtype(k_cache), *_array(q, shape, at, "q"), kc[0], vc[0], pages,
-                           page, *kc[1:], table[0], block_table.shape[1], table[1],
-                           _plain(seq_lens, n, _i32, "seq_lens"), *_array(out, shape, at, "out"),
-                           _plain(lse, n * hq, _f32, "lse"), scale, window, _addr(workspace) or 0,
-                           0 if workspace is None else workspace.numel(), flags)
+    table = _array(block_table, block_table.shape, _i32, "block_table", here)
+    args = _ATTENTION.pack(n, hq, hkv, dim, _dtype(q), _dtype(k_cache), *_array(q, shape, at, "q", here), kc[0], vc[0],
+                           pages, page, *kc[1:], table[0], block_table.shape[1], table[1],
+                           _plain(seq_lens, n, _i32, "seq_lens", here), *_array(out, shape, at, "out", here),
+                           _plain(lse, n * hq, _f32, "lse", here), scale, window, *_workspace(workspace, here), flags)
     st = _lib.lean_paged_attention(args, _stream(stream))
     if st:
         raise LeanError("lean_paged_attention", st)
@@ -533,17 +550,16 @@ def lean_token_logprobs(logits, ids, logprobs, ranks=None, entropy=None, top_ids
     how many logits are larger, the entropy, and the top_ids.shape[1] most likely
     ids with theirs.  Outputs that are None are left out; workspace: a uint8 tensor
     of lean_token_logprobs_workspace_bytes."""
-    if _i32 is None:
-        _types()
+    here = _here()
     rows, vocab = logits.shape
     k = 0 if top_ids is None else top_ids.numel() // rows
-    x = _array(logits, (rows, vocab), logits.dtype, "logits")
+    x = _array(logits, (rows, vocab), logits.dtype, "logits", here)
     f32 = _f32
-    args = _LOGPROBS.pack(rows, vocab, _dtype(logits), *x, _plain(ids, rows, _i32, "ids"), scale, k,
-                          _plain(logprobs, rows, f32, "logprobs"), _plain(ranks, rows, _i32, "ranks"),
-                          _plain(entropy, rows, f32, "entropy"), _plain(top_ids, rows * k, _i32, "top_ids"),
-                          _plain(top_logprobs, rows * k, f32, "top_logprobs"), _addr(workspace) or 0,
-                          0 if workspace is None else workspace.numel(), flags)
+    args = _LOGPROBS.pack(rows, vocab, _dtype(logits), *x, _plain(ids, rows, _i32, "ids", here), scale, k,
+                          _plain(logprobs, rows, f32, "logprobs", here), _plain(ranks, rows, _i32, "ranks", here),
+                          _plain(entropy, rows, f32, "entropy", here), _plain(top_ids, rows * k, _i32, "top_ids", here),
+                          _plain(top_logprobs, rows * k, f32, "top_logprobs", here), *_workspace(workspace, here),
+                          flags)
     st = _lib.lean_token_logprobs(args, _stream(stream))
     if st:
         raise LeanError("lean_token_logprobs", st)
