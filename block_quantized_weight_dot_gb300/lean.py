@@ -461,19 +461,21 @@ def lean_rope_append(q, k, v, positions, slots, turns, q_out, k_cache, v_cache, 
     hq = q.shape[1] if q is not None else 0
     hkv = k.shape[1] if k is not None else 0
     qs, ks = (n, hq, dim), (n, hkv, dim)
-    if k_cache is not None:
-        pages, page = k_cache.shape[:2]
-        kc = _array(k_cache, (pages, page, hkv, dim), k_cache.dtype, "k_cache", here)
-        if _array(v_cache, (pages, page, hkv, dim), k_cache.dtype, "v_cache", here)[1:] != kc[1:]:
+    some = k_cache if k_cache is not None else v_cache
+    if some is not None:  # (one alone is refused by the library)
+        pages, page = some.shape[:2]
+        kc, vc = (_array(t, (pages, page, hkv, dim), some.dtype, name, here)
+                  for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")))
+        if kc[0] and vc[0] and vc[1:] != kc[1:]:
             raise ValueError("k_cache and v_cache have different strides")
-        cache, cdt, vc = (pages, page) + kc[1:], _dtype(k_cache), v_cache.data_ptr()
+        cache, cdt = (pages, page) + (kc if kc[0] else vc)[1:], _dtype(some)
     else:
-        cache, cdt, kc, vc = (0,) * 5, 0, (0,), 0
+        cache, cdt, kc, vc = (0,) * 5, 0, (0,), (0,)
     args = _ROPE.pack(n, hq, hkv, dim, rot_dim, 1 if interleaved else 0, _dtype(one), cdt,
                       *_array(q, qs, at, "q", here), *_array(k, ks, at, "k", here), *_array(v, ks, at, "v", here),
                       *_array(q_out, qs, at, "q_out", here), *_array(k_out, ks, at, "k_out", here),
                       _plain(positions, n, _i32, "positions", here), _plain(slots, n, _i32, "slots", here),
-                      _plain(turns, rot_dim // 2, _i64t, "turns", here), kc[0], vc, *cache, rot_scale, flags)
+                      _plain(turns, rot_dim // 2, _i64t, "turns", here), kc[0], vc[0], *cache, rot_scale, flags)
     st = _lib.lean_rope_append(args, _stream(stream))
     if st:
         raise LeanError("lean_rope_append", st)

@@ -134,3 +134,14 @@ def test_workspace(lean, call):
     assert lean._lib.calls == 0
     getattr(lean, fn)(stream=0, **dict(args, workspace=Tensor((1024, 4096), U8)))
     assert lean._lib.calls == 1
+
+
+def test_one_cache_alone(lean, monkeypatch):
+    """k_cache or v_cache without the other reaches the library, which refuses it; nothing is dropped on the way."""
+    monkeypatch.setattr(lean, "_lib", lean._lib.real)
+    fn, args = rope()
+    for missing in ("k_cache", "v_cache"):
+        for k_out in (args["k_out"], None):
+            with pytest.raises(lean.LeanError) as e:
+                lean.lean_rope_append(stream=0, **dict(args, k_out=k_out, **{missing: None}))
+            assert e.value.status == lean.LEAN_ERR_NULL
