@@ -387,6 +387,13 @@ def _plain(t, size, dtype, name, here):
                      % (name, t.dtype, tuple(t.shape), t.device, size, dtype))
 
 
+def _rows(t, rows, size, dtype, name, here):
+    """As _plain, for `size` elements of each row: [rows, size], or all in one dimension."""
+    if t is not None and t.dim() != 1 and t.shape != (rows, size):
+        raise ValueError("%s is %s: [%d, %d] is wanted" % (name, tuple(t.shape), rows, size))
+    return _plain(t, rows * size, dtype, name, here)
+
+
 def _workspace(t, here):
     """(address, bytes) of a workspace; zeros for None."""
     if t is None:
@@ -536,7 +543,7 @@ def lean_paged_attention(q, k_cache, v_cache, block_table, seq_lens, out, scale:
     args = _ATTENTION.pack(n, hq, hkv, dim, _dtype(q), _dtype(k_cache), *_array(q, shape, at, "q", here), kc[0], vc[0],
                            pages, page, *kc[1:], table[0], block_table.shape[1], table[1],
                            _plain(seq_lens, n, _i32, "seq_lens", here), *_array(out, shape, at, "out", here),
-                           _plain(lse, n * hq, _f32, "lse", here), scale, window, *_workspace(workspace, here), flags)
+                           _rows(lse, n, hq, _f32, "lse", here), scale, window, *_workspace(workspace, here), flags)
     st = _lib.lean_paged_attention(args, _stream(stream))
     if st:
         raise LeanError("lean_paged_attention", st)
@@ -554,14 +561,13 @@ def lean_token_logprobs(logits, ids, logprobs, ranks=None, entropy=None, top_ids
     of lean_token_logprobs_workspace_bytes."""
     here = _here()
     rows, vocab = logits.shape
-    k = 0 if top_ids is None else top_ids.numel() // rows
+    k = 0 if top_ids is None else top_ids.shape[1] if top_ids.dim() == 2 else top_ids.numel() // max(1, rows)
     x = _array(logits, (rows, vocab), logits.dtype, "logits", here)
     f32 = _f32
     args = _LOGPROBS.pack(rows, vocab, _dtype(logits), *x, _plain(ids, rows, _i32, "ids", here), scale, k,
                           _plain(logprobs, rows, f32, "logprobs", here), _plain(ranks, rows, _i32, "ranks", here),
-                          _plain(entropy, rows, f32, "entropy", here), _plain(top_ids, rows * k, _i32, "top_ids", here),
-                          _plain(top_logprobs, rows * k, f32, "top_logprobs", here), *_workspace(workspace, here),
-                          flags)
+                          _plain(entropy, rows, f32, "entropy", here), _rows(top_ids, rows, k, _i32, "top_ids", here),
+                          _rows(top_logprobs, rows, k, f32, "top_logprobs", here), *_workspace(workspace, here), flags)
     st = _lib.lean_token_logprobs(args, _stream(stream))
     if st:
         raise LeanError("lean_token_logprobs", st)

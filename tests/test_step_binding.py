@@ -145,3 +145,23 @@ def test_one_cache_alone(lean, monkeypatch):
             with pytest.raises(lean.LeanError) as e:
                 lean.lean_rope_append(stream=0, **dict(args, k_out=k_out, **{missing: None}))
             assert e.value.status == lean.LEAN_ERR_NULL
+
+
+@pytest.mark.parametrize("call,name", [(attention, "lse"), (logprobs, "top_ids"), (logprobs, "top_logprobs")])
+def test_rows_first(lean, call, name):
+    """Outputs with a value or more for each row: rows are the first dimension, whatever the number of elements is."""
+    fn, args = call()
+    rows, k = args[name].shape
+    for shape in ((k, rows), (rows * k, 1), (rows, k, 1), (1, rows * k), (rows, k + 1)):
+        with pytest.raises(ValueError, match=name if name != "top_ids" else "top_"):
+            getattr(lean, fn)(stream=0, **dict(args, **{name: Tensor(shape, args[name].dtype)}))
+    assert lean._lib.calls == 0
+
+
+def test_no_rows(lean, monkeypatch):
+    """No rows at all: the library's answer, as for the other sizes that it refuses."""
+    monkeypatch.setattr(lean, "_lib", lean._lib.real)
+    with pytest.raises(lean.LeanError) as e:
+        lean.lean_token_logprobs(Tensor((0, 100), BF16), None, None, top_ids=Tensor((0, 3), I32),
+                                 top_logprobs=Tensor((0, 3), F32), workspace=Tensor((1 << 22,), U8), stream=0)
+    assert e.value.status == lean.LEAN_ERR_SHAPE
