@@ -170,7 +170,10 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesArgs
                             if (in == 0) p.table[entry] = id;
                         }
                     }
-                    slot[k] = (int)((int64_t)id * p.page + in);
+                    // (a page that is none, or whose slots pass 31 bits, is no place in any cache)
+                    const int64_t at_slot = (int64_t)id * p.page + in;
+                    if (id >= 0 && at_slot < INT32_MAX) slot[k] = (int)at_slot;
+                    else atomicOr(p.err, kErrSlot);
                 }
                 position[k] = pos;
                 seq[k] = first + lo;
@@ -243,9 +246,8 @@ extern "C" lean_status lean_kv_pages(const lean_kv_pages_args *a, void *stream) 
                    a->ring_state_out, a->status, a->token_starts, a->slots, a->positions, a->token_seqs,
                    a->table_stride, (int)a->n_seqs, (int)a->page_size, (int)a->max_tokens, (int)a->table_width,
                    (int)a->ring_size, nullptr};
-#ifdef LEAN_DEBUG
     p.err = error_word();
-#endif
+    if (!p.err) return LEAN_ERR_CUDA;
     // a block for every 512 tokens or 16 sequences, and one block per SM at most
     const int64_t grid = std::min<int64_t>(step_sm_count(),
                                            std::max<int64_t>((a->max_tokens + kPagesThreads - 1) / kPagesThreads,

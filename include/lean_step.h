@@ -173,6 +173,9 @@ lean_status lean_rope_append(const lean_rope_args *args, void *stream);
  * given back are appended in that order; those given back in a call are not
  * taken in the same call.  Table entries that a shorter sequence no longer
  * needs keep their old values.
+ * A page in the ring or the table that is negative, or whose slots pass 2^31 - 2,
+ * is handed on as it is, but its tokens get slot -1 and bit 64 of the device error
+ * word is set.
  * status[s] (0: done).  Otherwise the sequence stays at lens[s], and its new
  * tokens get slot -1:
  *   1  the ring ran out (then every later sequence that needs pages fails too)
