@@ -227,9 +227,9 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesArgs
 extern "C" lean_status lean_kv_pages(const lean_kv_pages_args *a, void *stream) {
     if (!a) return LEAN_ERR_NULL;
     if (!step_flags_ok(a->flags)) return LEAN_ERR_FORMAT;
-    const int64_t big = INT32_MAX;
+    const int64_t big = INT32_MAX;  // (of sequences half: a chunk past the last one still has to be counted in 32 bits)
     if (a->n_seqs <= 0 || a->page_size <= 0 || a->max_tokens < 0 || a->table_width <= 0 ||
-        a->table_stride < a->table_width || a->ring_size <= 0 || a->n_seqs >= big || a->page_size > big ||
+        a->table_stride < a->table_width || a->ring_size <= 0 || a->n_seqs > big / 2 || a->page_size > big ||
         a->max_tokens > big || a->table_stride > big || a->ring_size > big)
         return LEAN_ERR_SHAPE;
     // (blocks read the inputs while others write the outputs)

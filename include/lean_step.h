@@ -187,9 +187,10 @@ lean_status lean_rope_append(const lean_rope_args *args, void *stream);
  * lens_out and ring_state_out must not overlap lens, targets or ring_state (use
  * two sets in turn); all other outputs overlap nothing.
  * LEAN_ERR_SHAPE: n_seqs, page_size, table_width or ring_size <= 0, max_tokens <
- * 0, table_stride < table_width, any of these above 2^31 - 1, lens_out that is
- * lens or targets, or ring_state_out that is ring_state.  LEAN_ERR_NULL: a
- * missing pointer (slots, positions and token_seqs may be NULL: not wanted). */
+ * 0, table_stride < table_width, n_seqs above 2^30 - 1, another of these above
+ * 2^31 - 1, lens_out that is lens or targets, or ring_state_out that is
+ * ring_state.  LEAN_ERR_NULL: a missing pointer (slots, positions and token_seqs
+ * may be NULL: not wanted). */
 typedef struct {
     int64_t n_seqs, page_size, max_tokens;
     const int32_t *lens;      /* int32[n_seqs]                                 */

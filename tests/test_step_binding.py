@@ -165,3 +165,11 @@ def test_no_rows(lean, monkeypatch):
         lean.lean_token_logprobs(Tensor((0, 100), BF16), None, None, top_ids=Tensor((0, 3), I32),
                                  top_logprobs=Tensor((0, 3), F32), workspace=Tensor((1 << 22,), U8), stream=0)
     assert e.value.status == lean.LEAN_ERR_SHAPE
+
+
+def test_most_sequences(lean):
+    """Page bookkeeping counts chunks of sequences in 32 bits: 2^30 of them are refused, on the host."""
+    lib, P = lean._lib.real, 1 << 20
+    for n in (1 << 30, (1 << 31) - 600, (1 << 31) - 2):
+        args = lean._PAGES.pack(n, 16, 8, P, P, P, 4, 4, P, 8, P, P + 256, P + 512, P, P, 0, 0, 0, 0)
+        assert lib.lean_kv_pages(args, None) == lean.LEAN_ERR_SHAPE, n
