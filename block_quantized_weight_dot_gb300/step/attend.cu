@@ -73,6 +73,7 @@ struct AttArgs {
     int act;
     float scale_log2;
     int64_t cache_extent, q_extent, out_extent;  // elements, for the checked build
+    int64_t warp_extent, part_extent, fold_extent;
     unsigned *err;
 };
 
@@ -211,7 +212,7 @@ struct Span {
 __device__ __forceinline__ Span open_span(const AttArgs &p, int s) {
     Span x;
     const int64_t most = (int64_t)p.width * p.page;
-    int len = p.lens[s];
+    int len = LEAN_IN(s, p.n_seqs, p.err) ? p.lens[s] : 0;
     len = len < 0 ? 0 : len;
     x.len = len > most ? (int)most : len;
     x.start = p.window > 0 && x.len > p.window ? x.len - p.window : 0;
@@ -319,7 +320,8 @@ __device__ __forceinline__ void store_result(const AttArgs &p, const Head &f, in
     const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
     const int64_t at = (int64_t)f.s * p.os + (int64_t)(f.h0 + h) * p.ohs + d;
     if (LEAN_SPAN(at, 4, p.out_extent, p.err)) store_out<4>(p.out, at, p.act, v);
-    if (d == 0 && p.lse) p.lse[(int64_t)f.s * p.hq + f.h0 + h] = natural_lse(top, sum);
+    const int64_t at_lse = (int64_t)f.s * p.hq + f.h0 + h;
+    if (d == 0 && p.lse && LEAN_IN(at_lse, (int64_t)p.n_seqs * p.hq, p.err)) p.lse[at_lse] = natural_lse(top, sum);
 }
 
 // WIDE: 9 to 16 query heads in a group, one per row; else up to 8, two rows each.
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
     const bool by_item = items <= gridDim.x && (unsigned)((most + W - 1) / W) <= units / (gridDim.x * W) + kJoinUnits;
     const int blocks = by_item ? (int)items : (int)min(gridDim.x, units / W + (units % W != 0));
     if ((int)blockIdx.x >= blocks) {
-        if (threadIdx.x == 0) p.shared[blockIdx.x] = Shared{-1, 0};
+        if (threadIdx.x == 0 && LEAN_IN(blockIdx.x, kAttMaxCtas, p.err)) p.shared[blockIdx.x] = Shared{-1, 0};
         return;
     }
     units_before[threadIdx.x] = before;
@@ -565,6 +567,9 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         // outputs and sums of the item since its last fold, with reference m
         f32x2 acc[2 * KS][NH];
         float m[NH], l[NH], zs[NH];
+        const bool can_leave = PSMEM || LEAN_SPAN(((int64_t)blockIdx.x * W + warp) * PF, PF, p.warp_extent, p.err);
+        const bool can_fold = LEAN_SPAN(((int64_t)blockIdx.x * W + warp) * fold_floats(H, DP), fold_floats(H, DP), p.fold_extent,
+                                        p.err);
         f32x2 *const folded = p.folds + ((int64_t)blockIdx.x * W + warp) * (fold_floats(H, DP) / 2) + lane;
         int done = 0;  // units of the item so far
         bool fresh = true;
@@ -752,7 +757,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
 #pragma unroll
                     for (int h = 0; h < NH; ++h) acc[j][h] = fma2(folded[(j * NH + h) * 32], f2[h], acc[j][h]);
             };
-            if (++done % kFold == 0) {
+            if (++done % kFold == 0 && can_fold) {
                 if (done > kFold) unfold();
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
@@ -775,10 +780,11 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                 fresh = true;
                 const int first = u - cur.c;
                 const bool whole = first >= u_lo && item_end, at_end = u_then >= u_hi;
+                const bool leaves = !whole && (at_end || can_leave);
                 // a part that others continue: the run's last in this warp's own queue (nothing is under way to
                 // it any more)
                 float *part = reinterpret_cast<float *>(at_end ? tail_part : head_part);
-                if (done >= kFold) unfold();
+                if (done >= kFold && can_fold) unfold();
                 __syncwarp();
 #pragma unroll
                 for (int h = 0; h < NH; ++h) {
@@ -791,19 +797,20 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                     sum *= 1.f / PartRange<C>::kLift;
                     const int64_t at = (int64_t)cur.s * p.os + (int64_t)(h0 + row) * p.ohs + 2 * c4;
                     if (c4 == 0) {
-                        if (!whole) *reinterpret_cast<float2 *>(part + row * PO) = make_float2(m[h], sum);
-                        else if (p.lse) p.lse[(int64_t)cur.s * p.hq + h0 + row] = natural_lse(m[h], sum);
+                        if (leaves) *reinterpret_cast<float2 *>(part + row * PO) = make_float2(m[h], sum);
+                        else if (whole && p.lse && LEAN_IN((int64_t)cur.s * p.hq + h0 + row, (int64_t)p.n_seqs * p.hq, p.err))
+                            p.lse[(int64_t)cur.s * p.hq + h0 + row] = natural_lse(m[h], sum);
                     }
 #pragma unroll
                     for (int j = 0; j < 2 * KS; ++j) {
                         const float2 a = unpack2(acc[j][h]);
                         const float o[2] = {a.x * inv, a.y * inv};
-                        if (!whole) *reinterpret_cast<float2 *>(part + row * PO + 4 + 8 * j + 2 * c4) = make_float2(o[0], o[1]);
-                        else if (8 * j < p.dim && LEAN_SPAN(at + 8 * j, 2, p.out_extent, p.err))
+                        if (leaves) *reinterpret_cast<float2 *>(part + row * PO + 4 + 8 * j + 2 * c4) = make_float2(o[0], o[1]);
+                        else if (whole && 8 * j < p.dim && LEAN_SPAN(at + 8 * j, 2, p.out_extent, p.err))
                             store_out<2>(p.out, at + 8 * j, p.act, o);
                     }
                 }
-                if (!whole && lane == 0) {
+                if (leaves && lane == 0) {
                     Record &q = rec[2 * warp + at_end];
                     q.item = cur.s * groups + cur.kvh * p.tiles + cur.tile;
                     q.n = cur.x.n;
@@ -842,6 +849,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         while (members) {
             const int k = __ffs(members) - 1;
             members &= members - 1;
+            if (!PSMEM && !(k & 1) && !LEAN_SPAN(((int64_t)blockIdx.x * W + k / 2) * PF, PF, p.warp_extent, p.err)) continue;
             const float *row = reinterpret_cast<const float *>(k & 1 ? tail_part + (k / 2 - warp) * (S * STAGE)
                                                                      : head_part + (int64_t)(k / 2 - warp) * (PF * 4)) + h * PO;
             t.add(*reinterpret_cast<const float2 *>(row), *reinterpret_cast<const float4 *>(row + 4 + d));
@@ -849,7 +857,9 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
         if (head.first >= 0 && head.first + head.n <= b_n) {
             store_result(p, f, h, d, t.o, t.top, t.sum);
         } else {  // the block's part of the item that began before it, or of the one that goes on after it
-            float *row = p.cta_parts + ((int64_t)blockIdx.x * 2 + (head.first < 0 ? 0 : 1)) * PF + h * PO;
+            const int64_t at = ((int64_t)blockIdx.x * 2 + (head.first < 0 ? 0 : 1)) * PF + h * PO;
+            float *row = p.cta_parts + at;
+            if (!LEAN_SPAN(at, 8 + d, p.part_extent, p.err)) continue;
             *reinterpret_cast<float4 *>(row + 4 + d) = t.o;
             if (d == 0) *reinterpret_cast<float2 *>(row) = make_float2(t.top, t.sum);
         }
@@ -866,7 +876,7 @@ __global__ void __launch_bounds__(AttShape<DP>::kWarps * 32, 1) attend_kernel(co
                 x = Shared{q.item, (int)(b - blockIdx.x) + 1};
             }
         }
-        p.shared[blockIdx.x] = x;
+        if (LEAN_IN(blockIdx.x, kAttMaxCtas, p.err)) p.shared[blockIdx.x] = x;
     }
 }
 
@@ -884,7 +894,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) attend_sum_kernel(const AttArg
     step_begin();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     Shared mine = {-1, 0};
-    if (threadIdx.x < blocks) item[threadIdx.x] = mine = p.shared[threadIdx.x];
+    if (threadIdx.x < blocks && LEAN_IN(threadIdx.x, kAttMaxCtas, p.err)) item[threadIdx.x] = mine = p.shared[threadIdx.x];
     const unsigned few = __ballot_sync(0xffffffffu, mine.item >= 0 && mine.parts <= kAtOnce);
     const unsigned many = __ballot_sync(0xffffffffu, mine.parts > kAtOnce);
     if (lane == 0) {
@@ -903,7 +913,8 @@ __global__ void __launch_bounds__(kSumWarps * 32) attend_sum_kernel(const AttArg
     Sums t;
     auto take = [&](int b, int job, int from, int step) {  // parts from, from + step .. of the item that begins in block b
         const int parts = item[b].parts, e = (job * 32 + lane) * 4;
-        const float *at = p.cta_parts + ((int64_t)b * 2) * PF + e / DP * PO;
+        const int64_t first = (int64_t)b * 2 * PF + e / DP * PO;
+        const float *at = p.cta_parts + first;
         t.clear();
         for (int k0 = from; k0 < parts; k0 += kAtOnce * step) {
             float2 ml[kAtOnce];
@@ -912,9 +923,14 @@ __global__ void __launch_bounds__(kSumWarps * 32) attend_sum_kernel(const AttArg
             for (int i = 0; i < kAtOnce; ++i) {
                 const int k = k0 + i * step;
                 if (k < parts) {
-                    const float *row = at + (int64_t)(k * 2 + (k == 0)) * PF;
-                    ml[i] = *reinterpret_cast<const float2 *>(row);
-                    v[i] = *reinterpret_cast<const float4 *>(row + 4 + e % DP);
+                    const int64_t skip = (int64_t)(k * 2 + (k == 0)) * PF;
+                    const float *row = at + skip;
+                    ml[i] = make_float2(-CUDART_INF_F, 0.f);
+                    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (LEAN_SPAN(first + skip, 8 + e % DP, p.part_extent, p.err)) {
+                        ml[i] = *reinterpret_cast<const float2 *>(row);
+                        v[i] = *reinterpret_cast<const float4 *>(row + 4 + e % DP);
+                    }
                 }
             }
 #pragma unroll
@@ -1063,6 +1079,9 @@ extern "C" lean_status lean_paged_attention(const lean_attention_args *a, void *
     p.scale_log2 = (float)(a->scale * 1.4426950408889634);
     p.cache_extent = (a->n_pages - 1) * a->page_stride + (a->page_size - 1) * a->place_stride +
                      (a->n_kv_heads - 1) * a->cache_head_stride + a->head_dim;
+    p.warp_extent = (int64_t)kAttMaxCtas * 8 * part;
+    p.part_extent = (int64_t)kAttMaxCtas * 2 * part;
+    p.fold_extent = (int64_t)kAttMaxCtas * 8 * fold_floats(att_heads(a->n_q_heads, a->n_kv_heads), att_dim(a->head_dim));
     p.q_extent = (a->n_seqs - 1) * a->q_stride + (a->n_q_heads - 1) * a->q_head_stride + a->head_dim;
     p.out_extent = (a->n_seqs - 1) * a->out_stride + (a->n_q_heads - 1) * a->out_head_stride + a->head_dim;
     p.err = error_word();

@@ -63,6 +63,8 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesArgs
     __shared__ int tok[kPagesThreads + 1];            // first token of the chunk's sequences
     __shared__ int len_s[kPagesThreads];              // length, or -1 - length where the sequence failed
     __shared__ int take_s[kPagesThreads], give_s[kPagesThreads], gives[kPagesThreads];
+    // entries of the ring
+    auto from_ring = [&](unsigned at) { return LEAN_IN(at, p.ring_size, p.err) ? p.ring[at] : -1; };
     const int head = p.ring_state[0], count = p.ring_state[1];
     const bool ring_ok = head >= 0 && head < p.ring_size && count >= 0 && count <= p.ring_size;
     // running sums over the chunks; int64: lengths of failed sequences count among the tokens
@@ -73,7 +75,7 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesArgs
 
     for (int first = 0; first < p.n_seqs; first += kPagesThreads) {
         const int s = first + threadIdx.x;
-        const bool have_seq = s < p.n_seqs;
+        const bool have_seq = s < p.n_seqs && LEAN_IN(s, p.n_seqs, p.err);
         const int len = have_seq ? p.lens[s] : 0, target = have_seq ? p.targets[s] : 0;
         int st = !ring_ok || len < 0 || target < 0 ? 4 : 0;
         const int64_t had = len > 0 ? ((int64_t)len + p.page - 1) / p.page : 0;
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesArgs
                         if (page_at < had_pages) {
                             id = p.table[entry];
                         } else {
-                            id = p.ring[around((unsigned)head + take_s[lo] + page_at - had_pages, p.ring_size)];
+                            id = from_ring(around((unsigned)head + take_s[lo] + page_at - had_pages, p.ring_size));
                             // a new page begins with a new token: that one enters it in the table
                             if (in == 0) p.table[entry] = id;
                         }
@@ -203,7 +205,8 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesArgs
             const unsigned tail = around((unsigned)head + count, p.ring_size) + give_s[k];
 #pragma unroll 4
             for (int j = lane; j < g; j += 32)
-                if (LEAN_IN(entry + j, (p.n_seqs - 1) * p.table_stride + p.width, p.err))
+                if (LEAN_IN(entry + j, (p.n_seqs - 1) * p.table_stride + p.width, p.err) &&
+                    LEAN_IN(around(tail + j, p.ring_size), p.ring_size, p.err))
                     p.ring[around(tail + j, p.ring_size)] = p.table[entry + j];
         }
         __syncthreads();
@@ -212,6 +215,7 @@ __global__ void __launch_bounds__(kPagesThreads) kv_pages_kernel(const PagesArgs
     const int64_t used = p.slots || p.positions || p.seqs ? min(tokens, (int64_t)p.max_tokens) : p.max_tokens;
     for (int64_t i = used + (int64_t)blockIdx.x * kPagesThreads + threadIdx.x; i < p.max_tokens;
          i += (int64_t)G * kPagesThreads) {
+        if (!LEAN_IN(i, p.max_tokens, p.err)) break;
         if (p.slots) p.slots[i] = -1;
         if (p.positions) p.positions[i] = 0;
         if (p.seqs) p.seqs[i] = -1;

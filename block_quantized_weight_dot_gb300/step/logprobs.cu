@@ -60,6 +60,7 @@ struct LpArgs {
     Stats *runs;   // of a warp: of the row that began before it, and of the one that goes on after it
     Stats *whole;  // of a row that lies in one warp's run
     int *halves;   // [row][half unit]: largest logits, as ordered()
+    int64_t n_runs, n_whole, n_halves;  // entries there are, for the checked build
     int64_t stride;
     int rows, vocab, top_k;
     int row_units;
@@ -205,12 +206,33 @@ struct Lane<__half> {
     static constexpr uint32_t kMasked = 0xfc00fc00u;
 };
 
+// Entries of the workspace (what is outside it is not there in the checked build).
+__device__ __forceinline__ Stats load_stats(const LpArgs &p, const Stats *v, int64_t i, int64_t n) {
+    return LEAN_IN(i, n, p.err) ? v[i] : Stats{kLowest, 0.f, 0.f, 0};
+}
+__device__ __forceinline__ Stats load_run(const LpArgs &p, unsigned i) { return load_stats(p, p.runs, i, p.n_runs); }
+__device__ __forceinline__ Stats load_whole(const LpArgs &p, int64_t row) { return load_stats(p, p.whole, row, p.n_whole); }
+__device__ __forceinline__ int load_half(const LpArgs &p, const int *of_row, int i) {
+    return LEAN_IN(of_row - p.halves + i, p.n_halves, p.err) ? of_row[i] : ordered(-CUDART_INF_F);
+}
+// A row's given token (-1: none, or outside the vocabulary) and its logit.
+__device__ __forceinline__ int given_id(const LpArgs &p, int row) {
+    const int id = p.ids && LEAN_IN(row, p.rows, p.err) ? p.ids[row] : -1;
+    return id >= 0 && id < p.vocab ? id : -1;
+}
+template <typename T>
+__device__ __forceinline__ float logit_of(const LpArgs &p, int row, int id) {
+    const int64_t at = (int64_t)row * p.stride + id;
+    return LEAN_IN(at, (p.rows - 1) * p.stride + p.vocab, p.err) ? to_f(static_cast<const T *>(p.x)[at]) : 0.f;
+}
+
 // A row as 16-byte pieces from the one that holds its first logit; `before` elements of that one are not the row's.
 template <typename T>
 struct Row {
     const uint8_t *base;
     int before;
     __device__ Row(const LpArgs &p, int row) {
+        if (!LEAN_IN(row, p.rows, p.err)) row = 0;
         const uint8_t *at = static_cast<const uint8_t *>(p.x) + (int64_t)row * p.stride * sizeof(T);
         const int off = (int)((uintptr_t)at & 15);
         base = at - off;
@@ -245,9 +267,9 @@ __device__ __forceinline__ float log_prob(const LpArgs &p, float x, const Stats 
 }
 __device__ __forceinline__ void write_row(const LpArgs &p, int row, const Stats &a, const Entry *top, int n, int t, int step) {
     const float log_s = log2f(a.s), ln2 = 0.69314718056f;
+    if (!LEAN_IN(row, p.rows, p.err)) return;
     if (t == 0) {
-        const int id = p.ids ? p.ids[row] : -1;
-        const bool ok = id >= 0 && id < p.vocab;
+        const bool ok = given_id(p, row) >= 0;
         // (the mark of an id outside the vocabulary was left where its logit was looked up)
         if (p.ranks) p.ranks[row] = ok ? a.above : -1;
         if (p.entropy) p.entropy[row] = a.s == 0.f ? 0.f : ln2 * (log_s - a.w / a.s);
@@ -259,11 +281,11 @@ __device__ __forceinline__ void write_row(const LpArgs &p, int row, const Stats 
 }
 template <typename T>
 __device__ __forceinline__ void write_given(const LpArgs &p, int row, const Stats &a) {
-    if (!p.logprobs) return;
+    if (!p.logprobs || !LEAN_IN(row, p.rows, p.err)) return;
     const int id = p.ids[row];
     float lp = CUDART_NAN_F;
     if (id >= 0 && id < p.vocab) {
-        const float x = to_f(static_cast<const T *>(p.x)[(int64_t)row * p.stride + id]);
+        const float x = logit_of<T>(p, row, id);
         lp = a.s == 0.f ? -CUDART_INF_F : log_prob(p, x, a);
     }
     p.logprobs[row] = lp;
@@ -340,8 +362,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprobs_kernel(const LpA
             a = Stats{kLowest, 0.f, 0.f, 0};
             given = CUDART_INF_F;  // nothing is above it
             if (p.ids) {
-                const int id = p.ids[row];
-                if (id >= 0 && id < p.vocab) given = to_f(static_cast<const T *>(p.x)[(int64_t)row * p.stride + id]);
+                const int id = given_id(p, row);
+                if (id >= 0) given = logit_of<T>(p, row, id);
                 else if (lane == 0) atomicOr(p.err, kErrTokenId);
             }
             given2 = Lane<T>::twice(given);
@@ -369,18 +391,19 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprobs_kernel(const LpA
             // (a lane that has only NaN: -inf)
             const int h0 = __reduce_max_sync(0xffffffffu, ordered(fmaxf(top0, -CUDART_INF_F)));
             const int h1 = __reduce_max_sync(0xffffffffu, ordered(fmaxf(top1, -CUDART_INF_F)));
-            if (lane == 0) *reinterpret_cast<int2 *>(p.halves + ((int64_t)row * p.row_units + c) * 2) = make_int2(h0, h1);
+            const int64_t at_half = ((int64_t)row * p.row_units + c) * 2;
+            if (lane == 0 && LEAN_SPAN(at_half, 2, p.n_halves, p.err))
+                *reinterpret_cast<int2 *>(p.halves + at_half) = make_int2(h0, h1);
         }
         if (row_end || at_end) {
             fresh = true;
             join_lanes(p, a);
             if (lane == 0) {
-                if (!began_here) {
-                    p.runs[2 * g] = a;
-                } else if (!row_end) {
-                    p.runs[2 * g + 1] = a;
+                if (!began_here || !row_end) {
+                    const unsigned run = 2 * g + began_here;
+                    if (LEAN_IN(run, p.n_runs, p.err)) p.runs[run] = a;
                 } else if (TOPS) {
-                    p.whole[row] = a;
+                    if (LEAN_IN(row, p.n_whole, p.err)) p.whole[row] = a;
                 } else {
                     write_row(p, row, a, nullptr, 0, 0, 1);
                     write_given<T>(p, row, a);
@@ -487,9 +510,9 @@ __global__ void __launch_bounds__(kEndThreads) logprobs_end_kernel(const LpArgs 
     const unsigned g0 = warp_of(p, u0), g1 = warp_of(p, u0 + p.row_units - 1);
     Stats a = {kLowest, 0.f, 0.f, 0};
     if (g0 == g1) {
-        a = p.whole[row];
+        a = load_whole(p, row);
     } else {
-        for (unsigned i = g0 + threadIdx.x; i <= g1; i += kEndThreads) join(p, a, p.runs[2 * i + (i == g0)]);
+        for (unsigned i = g0 + threadIdx.x; i <= g1; i += kEndThreads) join(p, a, load_run(p, 2 * i + (i == g0)));
         join_lanes(p, a);
         if (lane == 0) sh.stats[warp] = a;
     }
@@ -504,11 +527,11 @@ __global__ void __launch_bounds__(kEndThreads) logprobs_end_kernel(const LpArgs 
         const int *halves = p.halves + (int64_t)row * n_half;
         Entry mine = LP_NONE;
         for (int i = threadIdx.x; i < n_half; i += kEndThreads) {
-            const float v = unordered(halves[i]);
+            const float v = unordered(load_half(p, halves, i));
             if (v > mine.v) mine = Entry{v, i};
         }
         const int n_picked = pick_best(sh.pick, list, 0, best, k, mine, [&](float, auto f) {
-            for (int i = threadIdx.x; i < n_half; i += kEndThreads) f(Entry{unordered(halves[i]), i});
+            for (int i = threadIdx.x; i < n_half; i += kEndThreads) f(Entry{unordered(load_half(p, halves, i)), i});
         });
         if (threadIdx.x < n_picked) sh.picked[threadIdx.x] = best[threadIdx.x].id;
         __syncthreads();
@@ -652,15 +675,15 @@ __global__ void __launch_bounds__(kRowWarps * 32) logprobs_rows_kernel(const LpA
     // the half units with the largest maxima
     const int *halves = p.halves + (int64_t)row * n_half;
     int most = ordered(-CUDART_INF_F);
-    for (int i = lane; i < n_half; i += 32) most = max(most, halves[i]);
-    Stats a = p.whole[row];
+    for (int i = lane; i < n_half; i += 32) most = max(most, load_half(p, halves, i));
+    Stats a = load_whole(p, row);
     if (g0 != g1) {
-        a = p.runs[2 * g0 + 1];
+        a = load_run(p, 2 * g0 + 1);
         if (g1 - g0 < 8) {
-            for (unsigned g = g0 + 1; g <= g1; ++g) join(p, a, p.runs[2 * g]);
+            for (unsigned g = g0 + 1; g <= g1; ++g) join(p, a, load_run(p, 2 * g));
         } else {
             if (lane > 0) a = Stats{kLowest, 0.f, 0.f, 0};
-            for (unsigned g = g0 + 1 + lane; g <= g1; g += 32) join(p, a, p.runs[2 * g]);
+            for (unsigned g = g0 + 1 + lane; g <= g1; g += 32) join(p, a, load_run(p, 2 * g));
             join_lanes(p, a);
         }
     }
@@ -673,7 +696,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) logprobs_rows_kernel(const LpA
     float least = unordered(kth_of_lanes(sh.values[warp], most, k));
     for (int i0 = 0; i0 < n_half; i0 += 32) {
         const int i = i0 + lane;
-        const float v = i < n_half ? unordered(halves[i]) : -CUDART_INF_F;
+        const float v = i < n_half ? unordered(load_half(p, halves, i)) : -CUDART_INF_F;
         w.room(32);
         if (v >= w.reach(least)) w.add(Entry{v, i});
     }
@@ -813,6 +836,9 @@ extern "C" lean_status lean_token_logprobs(const lean_logprobs_args *a, void *st
     p.runs = static_cast<Stats *>(a->workspace);
     p.whole = p.runs + 2 * kLpMaxWarps;
     p.halves = reinterpret_cast<int *>(p.whole + a->rows);
+    p.n_runs = 2 * kLpMaxWarps;
+    p.n_whole = a->top_k ? a->rows : 0;
+    p.n_halves = a->top_k ? a->rows * lp_row_units(a->vocab, 4, false) * 2 : 0;
     p.stride = a->stride;
     p.rows = (int)a->rows;
     p.vocab = (int)a->vocab;

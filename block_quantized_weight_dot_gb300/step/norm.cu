@@ -84,15 +84,16 @@ __device__ __forceinline__ float Raw<A, VEC>::get(int i) const {
 }
 
 // A vector of a row that may begin before its first element or end past its last one: what is not the row's is 0 and
-// not stored.
+// not stored.  `there`: false if the buffer has no such vector (checked build).
 template <typename A, int VEC>
-__device__ __forceinline__ void load_part(Raw<A, VEC> &v, const A *row, int c, int width, bool vector) {
-    if (vector) {
+__device__ __forceinline__ void load_part(Raw<A, VEC> &v, const A *row, int c, int width, bool vector, bool there) {
+    if (vector && there) {
         v.load(row + c);
         return;
     }
 #pragma unroll
     for (int i = 0; i < Raw<A, VEC>::kWords; ++i) v.w[i] = 0;
+    if (!there) return;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
         if (c + j < 0 || c + j >= width) continue;
@@ -138,12 +139,13 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs p, in
         const int c = column(i);
         const bool v = whole(c);
         in[i] = live && c < p.width;
-        if (in[i] && p.x && inside(row * p.xs + c, v, p.xs))
-            load_part(xr[i], static_cast<const A *>(p.x) + row * p.xs, c, p.width, v);
-        if (in[i] && p.h && inside(row * p.hs + c, v, p.hs))
-            load_part(hr[i], static_cast<const R *>(p.h) + row * p.hs, c, p.width, v);
-        if (in[i] && p.gate && inside(row * p.gs + c, v, p.gs))
-            load_part(gr[i], static_cast<const A *>(p.gate) + row * p.gs, c, p.width, v && !(SHIFT && p.gs == 0));
+        if (in[i] && p.x)
+            load_part(xr[i], static_cast<const A *>(p.x) + row * p.xs, c, p.width, v, inside(row * p.xs + c, v, p.xs));
+        if (in[i] && p.h)
+            load_part(hr[i], static_cast<const R *>(p.h) + row * p.hs, c, p.width, v, inside(row * p.hs + c, v, p.hs));
+        if (in[i] && p.gate)
+            load_part(gr[i], static_cast<const A *>(p.gate) + row * p.gs, c, p.width, v && !(SHIFT && p.gs == 0),
+                      inside(row * p.gs + c, v, p.gs));
     }
     float post = 1.f;
     if (p.post_w) {
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs p, in
         if (!in[i]) continue;
         const int c = column(i);
         Raw<float, VEC> pw;
-        if (p.post_w) load_part(pw, p.post_w, c, p.width, !SHIFT);
+        if (p.post_w) load_part(pw, p.post_w, c, p.width, !SHIFT, inside(c, !SHIFT, 0));
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
             float u = 0.f;
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs p, in
         if (!in[i]) continue;
         const int c = column(i);
         Raw<float, VEC> wv;
-        if (p.w) load_part(wv, p.w, c, p.width, !SHIFT);
+        if (p.w) load_part(wv, p.w, c, p.width, !SHIFT, inside(c, !SHIFT, 0));
 #pragma unroll
         for (int j = 0; j < VEC; ++j) v[i][j] *= p.w ? r * wv.get(j) : r;
         if (inside(row * p.ys + c, whole(c), p.ys))
@@ -206,21 +208,24 @@ __global__ void __launch_bounds__(kNormThreads) norm_long_kernel(const NormArgs 
     const A *gate = p.gate ? static_cast<const A *>(p.gate) + row * p.gs : nullptr;
     const R *h = p.h ? static_cast<const R *>(p.h) + row * p.hs : nullptr;
     const float inv = 1.f / (float)p.width;
+    auto at = [&](const auto *v, int c, int64_t stride) {  // element c of the row
+        return LEAN_IN(row * stride + c, (p.rows - 1) * stride + p.width, p.err) ? to_f(v[c]) : 0.f;
+    };
     float post = 1.f;
     if (p.post_w) {
         float s = 0.f;
-        for (int c = threadIdx.x; c < p.width; c += kNormThreads) s = fmaf(to_f(x[c]), to_f(x[c]), s);
+        for (int c = threadIdx.x; c < p.width; c += kNormThreads) s = fmaf(at(x, c, p.xs), at(x, c, p.xs), s);
         post = rsqrtf(fmaf(row_sum(s, kNormThreads, 0, part[0]), inv, p.eps));
     }
     auto value = [&](int c) {
         float u = 0.f;
         if (x) {
-            u = to_f(x[c]);
-            if (p.post_w) u = u * post * p.post_w[c];
-            if (gate) u *= to_f(gate[c]);
+            u = at(x, c, p.xs);
+            if (p.post_w) u = u * post * at(p.post_w, c, 0);
+            if (gate) u *= at(gate, c, p.gs);
             u *= p.alpha;
         }
-        return h ? to_f(h[c]) + u : u;
+        return h ? at(h, c, p.hs) + u : u;
     };
     float r = 0.f;
     if (p.y) {
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_long_kernel(const NormArgs 
         if (p.h_out && LEAN_IN(row * p.hos + c, (p.rows - 1) * p.hos + p.width, p.err))
             static_cast<R *>(p.h_out)[row * p.hos + c] = from_f<R>(v);
         if (p.y && LEAN_IN(row * p.ys + c, (p.rows - 1) * p.ys + p.width, p.err))
-            static_cast<A *>(p.y)[row * p.ys + c] = from_f<A>(v * (p.w ? r * p.w[c] : r));
+            static_cast<A *>(p.y)[row * p.ys + c] = from_f<A>(v * (p.w ? r * at(p.w, c, 0) : r));
     }
 }
 

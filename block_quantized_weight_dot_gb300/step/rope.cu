@@ -39,6 +39,7 @@ struct RopeArgs {
     int64_t qs, qhs, ks, khs, vs, vhs, qos, qohs, kos, kohs;
     int64_t page_stride, place_stride, cache_hs;
     int64_t n_tokens, n_slots;
+    int64_t q_end, k_end, v_end, qo_end, ko_end;  // elements, for the checked build
     int hq, hkv, hv, dim, rot, page; // hv: heads of v, 0 without caches
     int tokens;            // of a block
     int pieces, rot_pieces; // of a head; the rotated ones come first
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs
         A *dst;
         void *cache;
         int64_t step, to_step, cache_at;
+        int64_t at, end, to, to_end;  // the same places as offsets, and what there is (checked build)
         int b, pair_a, pair_b;  // the second run's distance; the runs' first pairs, -1: not rotated
     };
     auto open = [&](int slot) {
@@ -158,6 +160,10 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs
         q.dst = is_q ? static_cast<A *>(p.q_out) + head * p.qohs + t0 * q.to_step + a
                 : is_k && p.k_out ? static_cast<A *>(p.k_out) + kvh * p.kohs + t0 * q.to_step + a
                                   : nullptr;
+        q.at = (is_q ? head * p.qhs : kvh * (is_k ? p.khs : p.vhs)) + t0 * q.step + a;
+        q.end = is_q ? p.q_end : is_k ? p.k_end : p.v_end;
+        q.to = (is_q ? head * p.qohs : kvh * p.kohs) + t0 * q.to_step + a;
+        q.to_end = is_q ? p.qo_end : p.ko_end;
         q.cache = is_q || !p.k_cache ? nullptr : is_k ? p.k_cache : p.v_cache;
         q.cache_at = kvh * p.cache_hs + a;
         return q;
@@ -167,8 +173,11 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs
         for (int u = 0; u < U; ++u) {
             const int t = t1 + u * sub;
             if (t < nt) {
-                x[u][0] = *reinterpret_cast<const Piece<A, V> *>(q.src + t * q.step);
-                x[u][1] = *reinterpret_cast<const Piece<A, V> *>(q.src + t * q.step + q.b);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (LEAN_SPAN(q.at + t * q.step + i * q.b, V, q.end, p.err))
+                        x[u][i] = *reinterpret_cast<const Piece<A, V> *>(q.src + t * q.step + i * q.b);
+                    else x[u][i] = Piece<A, V>{};
             }
         }
     };
@@ -206,8 +215,9 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs
                 }
             }
             if (q.dst) {
-                store_vec<A, V>(q.dst + t * q.to_step, f);
-                store_vec<A, V>(q.dst + t * q.to_step + q.b, f + V);
+                const int64_t to = q.to + t * q.to_step;
+                if (LEAN_SPAN(to, V, q.to_end, p.err)) store_vec<A, V>(q.dst + t * q.to_step, f);
+                if (LEAN_SPAN(to + q.b, V, q.to_end, p.err)) store_vec<A, V>(q.dst + t * q.to_step + q.b, f + V);
             }
             if (q.cache && place[t] >= 0) {
                 const int64_t at = place[t] + q.cache_at;
@@ -226,8 +236,8 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs
     }
     for (int i = threadIdx.x; i < nt * half; i += T) {
         const int t = i / half, j = i - t * half;
-        const int32_t pos = p.positions[t0 + t];
-        const uint64_t f = p.turns[j];
+        const int32_t pos = LEAN_IN(t0 + t, p.n_tokens, p.err) ? p.positions[t0 + t] : 0;
+        const uint64_t f = LEAN_IN(j, p.rot / 2, p.err) ? p.turns[j] : 0;
         // upper half of pos * f mod 2^64, pos signed
         const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32), u = (uint32_t)pos;
         const uint32_t turn = __umulhi(u, lo) + u * hi - (pos < 0 ? lo : 0u);
@@ -236,7 +246,7 @@ __global__ void __launch_bounds__(kRopeMaxThreads, 2) rope_kernel(const RopeArgs
         cs[i] = make_float2(c * p.scale, s * p.scale);
     }
     if (p.k_cache && threadIdx.x < nt) {
-        const int32_t s = p.slots[t0 + threadIdx.x];
+        const int32_t s = LEAN_IN(t0 + threadIdx.x, p.n_tokens, p.err) ? p.slots[t0 + threadIdx.x] : -1;
         int64_t at = -1;
         if (s >= p.n_slots) atomicOr(p.err, kErrSlot);
         else if (s >= 0) at = (int64_t)(s / p.page) * p.page_stride + (int64_t)(s % p.page) * p.place_stride;
@@ -361,6 +371,14 @@ extern "C" lean_status lean_rope_append(const lean_rope_args *a, void *stream) {
     p.place_stride = a->place_stride;
     p.cache_hs = a->cache_head_stride;
     p.n_tokens = a->n_tokens;
+    auto end = [&](int64_t stride, int64_t heads, int64_t head_stride) {
+        return (a->n_tokens - 1) * stride + (heads - 1) * head_stride + a->head_dim;
+    };
+    p.q_end = end(a->q_stride, a->n_q_heads, a->q_head_stride);
+    p.k_end = end(a->k_stride, a->n_kv_heads, a->k_head_stride);
+    p.v_end = end(a->v_stride, a->n_kv_heads, a->v_head_stride);
+    p.qo_end = end(a->q_out_stride, a->n_q_heads, a->q_out_head_stride);
+    p.ko_end = end(a->k_out_stride, a->n_kv_heads, a->k_out_head_stride);
     p.hq = (int)a->n_q_heads;
     p.hkv = (int)a->n_kv_heads;
     p.hv = cached ? p.hkv : 0;
