@@ -4,9 +4,10 @@
 //   z_j = scale q . k_j,  p_j = e^(z_j - m),  m = max z_j,
 //   out = sum p_j v_j / sum p_j,  lse = m + ln sum p_j
 //
-// Every key and value of the cache is needed once per kv head, whatever the
-// number of query heads that share it: HBM bounds the call, 2 * dim * 2 bytes a
-// token and kv head.  So the design is about keeping loads in flight:
+// Every key and value of the cache is read once for up to 16 query heads that
+// share its kv head (for more, once per 16 of them: 239 us at 48 heads of 128 where
+// 12 take 98): HBM bounds the call, 2 * dim * 2 bytes a token and kv head.  So the
+// design is about keeping loads in flight:
 //
 //   - The work is a list of units: 16 tokens of one (sequence, kv head, group of
 //     query heads).  Every warp of the GPU takes an equal run of units, whatever
@@ -37,14 +38,17 @@
 // above 2^-38 of the largest element).
 //
 // Measured (GB300, calls in a graph): 384 sequences of 1 to 8192 tokens, 32 query
-// and 4 kv heads of 64, bf16: 67 us, 5.5 TB/s of the 6.78 that a copy reaches; one
-// sequence of 131072, 16/2 heads of 128, fp32 q: 33.3 us, 4.0 TB/s (5.7 at 524288):
-// the stream itself runs at 6 TB/s and more, 3 us pass before the first keys
-// arrive (lengths, table, keys, one after the other) and 8 after the last (joins,
-// the second kernel, the launch); 613 tokens of 15/5 heads of 64: 9.1 us.
+// and 4 kv heads of 64, bf16: 68 us, 5.4 TB/s of the 6.78 that a copy reaches, with
+// fp32 q 72.6; one sequence of 131072, 16/2 heads of 128, fp32 q: 33.7 us, 4.0 TB/s
+// (5.8 at 524288): the stream itself runs at 6 TB/s and more, 3 us pass before the
+// first keys arrive (lengths, table, keys, one after the other) and 8 after the last
+// (joins, the second kernel, the launch); 613 tokens of 15/5 heads of 64: 9.2 us.
+// What bounds the rest is a warp's time for a unit, not HBM: 192 sequences as above
+// with heads of 128 and fp32 q, 8 query heads a group 73 us, 12 98 (floor 54); 96
+// sequences with heads of 256, 88 and 131.
 // Pages of 16 tokens or more hold a unit in one page or two, and two pages cost
-// little (384 sequences as above: 67 us with pages of 24, 68 of 20).  In smaller
-// pages every token is looked up: 86 us with pages of 8, 98 of one.
+// little (384 sequences as above: 69 us with pages of 24, 72 of 20).  In smaller
+// pages every token is looked up: 90 us with pages of 8, 99 of one.
 #include "step_common.cuh"
 
 using namespace lean;

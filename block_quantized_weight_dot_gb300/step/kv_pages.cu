@@ -10,9 +10,11 @@
 // writes what there is one of per sequence.  Inputs are never written (but for
 // table and ring entries that no block reads), so the blocks need no order.
 //
-// Measured (GB300, calls in a graph): 64 sequences growing by a token 6.3 us, 509
-// growing by 255000 tokens together 11.2 us.  Latency bounds both: a launch, the
-// lengths, three sums with their barriers, the ring, the table.
+// Measured (GB300, calls in a graph): 64 sequences growing by a token 6.4 us, 509
+// growing by 255000 tokens together 11.3 us.  Latency bounds both: a launch, the
+// lengths, three sums with their barriers, the ring, the table.  The chain is longer
+// than it has to be: pages taken and pages given back could share a sum, and the
+// ring's new state could be left to block 0 after its tokens.
 #include "step_common.cuh"
 
 using namespace lean;

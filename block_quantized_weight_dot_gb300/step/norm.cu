@@ -12,7 +12,9 @@
 //
 // Measured (GB300, calls in a graph): 8192 x 2048 bf16 with gate, norm after and
 // fp32 residual 38.1 us, 6.16 TB/s of the 6.78 that a copy reaches; fp32 6.27
-// TB/s; one row of 960 fp32 2.1 us.
+// TB/s; one row of 960 fp32 2.1 us.  On odd widths weights and a shared gate are read
+// one element at a time: 8192 x 2049 63 us (35 at that rate of a copy), 16000 x 1001 59
+// (33); rows past 16384 go by single elements, up to three times: 1024 x 20480 162 (43).
 #include "step_common.cuh"
 
 using namespace lean;

@@ -18,9 +18,9 @@
 // bounds it.  (Tokens staged in shared memory by asynchronous copies: 41 us.)
 //
 // Measured (GB300, calls in a graph): 16384 tokens of 16 query and 2 kv heads of
-// 128 (half of them rotated) 30.1 us in bf16 (5.6 TB/s; pairs of halves 33.8), 50.8
-// us in fp32 (6.3 TB/s; a copy reaches 6.78); 2000 tokens 5.1 us; four tokens of
-// 15/5 heads of 64 2.6 us.
+// 128 (half of them rotated, neighbours) 30.4 us in bf16 (5.5 TB/s), 51.4 in fp32
+// (6.2 TB/s; a copy reaches 6.78); pairs of halves in bf16 34.1, over the whole head
+// 37.0, in fp32 52.2; 2000 tokens 5.3 us; four tokens of 15/5 heads of 64 2.6 us.
 #include "step_common.cuh"
 
 using namespace lean;
@@ -274,8 +274,8 @@ lean_status launch_rope(RopeArgs p, bool inter, int64_t flags, void *stream) {
     const int64_t items = (int64_t)(p.hq + p.hkv + p.hv) * p.pieces;
     // A thread for each piece of a token, or of several tokens side by side, and no more threads than that: idle ones
     // cost resident blocks.  (At 16384 tokens of 16/2 bf16 heads of 128, 80 registers: 160 threads and eight tokens a
-    // block 30.1 us, four tokens 33.7, twelve 31.7, two tokens side by side in 320 threads 31.4; 64 registers spill,
-    // 33.8; two tokens' loads at a time 38.7.)
+    // block 30.1 us, four tokens 33.7, twelve 31.7, two tokens side by side in 320 threads 31.4; 64 registers
+    // 33.8; two tokens' loads at a time 38.7.  At 80 registers the 16-bit kernels spill 5 to 22 words, at 64 more.)
     const int64_t sub = std::max<int64_t>(1, 256 / items);
     const int64_t passes = (items + kRopeMaxThreads - 1) / kRopeMaxThreads;
     const int threads = (int)(((sub * items + passes - 1) / passes + 31) / 32 * 32);

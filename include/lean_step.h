@@ -220,6 +220,8 @@ lean_status lean_kv_pages(const lean_kv_pages_args *args, void *stream);
  * window, is never used, whatever it is.  A page outside 0..n_pages-1 among
  * those needed gives NaN for its sequence and sets bit 64 of the device error
  * word; a length below 0 counts as 0, one past table_width * page_size as that.
+ * What is not finite among the attended keys and values gives NaN or infinities
+ * in the outputs that it reaches.
  * q and p are split in parts of the cache's type, three for fp32 q and out and
  * two for 16-bit ones, and sums are fp32, so that fp32 q keeps its precision: out
  * errs by about 2^-17 of sum p |v|, and by fp32's rounding of the scores.  With an
