@@ -1,5 +1,5 @@
 """ctypes binding of ``liblean_qmatmul.so`` (C ABI in ``include/lean_qmatmul.h``,
-``include/lean_quant.h`` and ``include/lean_step.h``).
+``include/lean_quant.h``, ``include/lean_step.h`` and ``include/lean_cache.h``).
 
 Argument marshalling only: every computation of the product runs in the CUDA
 library.  Functions keep the C names.  Buffers may be given as torch tensors
@@ -29,7 +29,7 @@ LEAN_FLAG_X_PLANES = 2
 LEAN_FLAG_STREAM = 4
 LEAN_FLAG_X_INT8 = 8
 
-LEAN_F32, LEAN_BF16, LEAN_F16 = 0, 1, 2
+LEAN_F32, LEAN_BF16, LEAN_F16, LEAN_I8 = 0, 1, 2, 3
 (LEAN_ROPE_PLAIN, LEAN_ROPE_LINEAR, LEAN_ROPE_BASE, LEAN_ROPE_RAMP, LEAN_ROPE_BANDS) = range(5)
 LEAN_MAX_TOP = 64
 
@@ -66,6 +66,7 @@ SIGNATURES = {
     "lean_rope_frequencies": (_int, [_int, _i64] + [ctypes.c_double] * 5 + [_vp]),
     "lean_rope_append": (_int, [_vp, _vp]),
     "lean_kv_pages": (_int, [_vp, _vp]),
+    "lean_kv_read": (_int, [_vp, _vp]),
     "lean_paged_attention": (_int, [_vp, _vp]),
     "lean_paged_attention_workspace_bytes": (_i64, [_i64] * 4),
     "lean_token_logprobs": (_int, [_vp, _vp]),
@@ -326,7 +327,7 @@ def lean_wait_selftest(limit_us: int, stream=None) -> None:
     _check("lean_wait_selftest", _lib.lean_wait_selftest(limit_us, _stream(stream)))
 
 
-# ---- the operators of a serving step (include/lean_step.h) ----
+# ---- the operators of a serving step (include/lean_step.h, include/lean_cache.h) ----
 #
 # These take torch tensors on the GPU and read sizes, strides and element types
 # off them (a caller without torch fills the C structs); every output is the
@@ -334,23 +335,25 @@ def lean_wait_selftest(limit_us: int, stream=None) -> None:
 # current GPU, is a ValueError, what the library refuses a LeanError.
 
 _NORM = struct.Struct("<4qQqQqQqQQQqQq2dq")
-_ROPE = struct.Struct("<8q" + "Q2q" * 5 + "3Q2Q5qdq")
+_ROPE = struct.Struct("<8q" + "Q2q" * 5 + "3Q2Q5qdq" + "2Q3q")
 _PAGES = struct.Struct("<3q3Q2qQqQ2Q5Qq")
-_ATTENTION = struct.Struct("<6qQ2q2Q5qQ2qQQ2qQdqQqq")
+_ATTENTION = struct.Struct("<6qQ2q2Q5qQ2qQQ2qQdqQqq" + "2Q3q")
+_KV_READ = struct.Struct("<5q2Q5q2Q3qQQ2qQ2qq")
 _LOGPROBS = struct.Struct("<3qQqQdq5QQqq")
 _dtypes = {}
-_i32 = _f32 = _i64t = _u8 = None  # torch's, once a call has needed them
+_i32 = _f32 = _i64t = _u8 = _i8 = None  # torch's, once a call has needed them
+_NO_SCALES = (0,) * 5
 _device = None
 
 
 def _here():
     """Index of the current GPU, as tensors on it have it; -2 without any."""
-    global _i32, _f32, _i64t, _u8, _device
+    global _i32, _f32, _i64t, _u8, _i8, _device
     if _device is not None:
         return _device()
     import torch
     _dtypes.update({torch.float32: LEAN_F32, torch.bfloat16: LEAN_BF16, torch.float16: LEAN_F16})
-    _i32, _f32, _i64t, _u8 = torch.int32, torch.float32, torch.int64, torch.uint8
+    _i32, _f32, _i64t, _u8, _i8 = torch.int32, torch.float32, torch.int64, torch.uint8, torch.int8
     if not torch.cuda.is_available():
         return -2
     here = torch.cuda.current_device()
@@ -375,6 +378,34 @@ def _array(t, shape, dtype, name, here):
         return (t.data_ptr(),) + st[:-1]
     raise ValueError("%s is %s %s on %s, strides %s: %s %s on the current GPU is wanted, the last dimension contiguous"
                      % (name, t.dtype, tuple(t.shape), t.device, st, dtype, tuple(shape)))
+
+
+def _cache_dtype(t):
+    """Code of a cache's element type, int8 among them."""
+    return LEAN_I8 if t.dtype is _i8 else _dtype(t)
+
+
+def _scales(cache, k_scales, v_scales, here):
+    """The addresses and the three strides of the scales of caches in 8 bits, [pages, page_size, kv heads] float32;
+    zeros for caches of 16 bits, which have none."""
+    if k_scales is None and v_scales is None:
+        return _NO_SCALES
+    if cache is None or cache.dtype is not _i8:
+        raise ValueError("k_scales and v_scales go with caches of int8")
+    shape, out, at = cache.shape[:3], None, []
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t is None:
+            at.append(0)
+            continue
+        if t.shape != shape or t.dtype is not _f32 or t.get_device() != here:
+            raise ValueError("%s is %s %s on %s: %s %s on the current GPU is wanted"
+                             % (name, t.dtype, tuple(t.shape), t.device, _f32, tuple(shape)))
+        st = t.stride()
+        if out is not None and st != out:
+            raise ValueError("k_scales and v_scales have different strides")
+        out = st
+        at.append(t.data_ptr())
+    return (*at, *out)
 
 
 def _plain(t, size, dtype, name, here):
@@ -455,10 +486,12 @@ def lean_rope_turns(freq) -> np.ndarray:
 
 def lean_rope_append(q, k, v, positions, slots, turns, q_out, k_cache, v_cache, rot_dim: int,
                      interleaved: bool = False, rot_scale: float = 1.0, k_out=None, flags: int = 0,
-                     stream=None) -> None:
+                     stream=None, k_scales=None, v_scales=None) -> None:
     """Rotate the first rot_dim elements of each head of q and k ([tokens, heads,
     dim]) to `positions`, into q_out (and k_out), and store k and v at `slots` of
-    the caches ([pages, page_size, kv_heads, dim], strides of their own)."""
+    the caches ([pages, page_size, kv_heads, dim], strides of their own).  Caches
+    of int8 are written in 8 bits, with a scale for each token and kv head in
+    k_scales and v_scales ([pages, page_size, kv_heads] float32, any strides)."""
     here = _here()
     one = q if q is not None else k
     if one is None or one.dim() != 3:
@@ -475,14 +508,15 @@ def lean_rope_append(q, k, v, positions, slots, turns, q_out, k_cache, v_cache, 
                   for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")))
         if kc[0] and vc[0] and vc[1:] != kc[1:]:
             raise ValueError("k_cache and v_cache have different strides")
-        cache, cdt = (pages, page) + (kc if kc[0] else vc)[1:], _dtype(some)
+        cache, cdt = (pages, page) + (kc if kc[0] else vc)[1:], _cache_dtype(some)
     else:
         cache, cdt, kc, vc = (0,) * 5, 0, (0,), (0,)
     args = _ROPE.pack(n, hq, hkv, dim, rot_dim, 1 if interleaved else 0, _dtype(one), cdt,
                       *_array(q, qs, at, "q", here), *_array(k, ks, at, "k", here), *_array(v, ks, at, "v", here),
                       *_array(q_out, qs, at, "q_out", here), *_array(k_out, ks, at, "k_out", here),
                       _plain(positions, n, _i32, "positions", here), _plain(slots, n, _i32, "slots", here),
-                      _plain(turns, rot_dim // 2, _i64t, "turns", here), kc[0], vc[0], *cache, rot_scale, flags)
+                      _plain(turns, rot_dim // 2, _i64t, "turns", here), kc[0], vc[0], *cache, rot_scale, flags,
+                      *_scales(some, k_scales, v_scales, here))
     st = _lib.lean_rope_append(args, _stream(stream))
     if st:
         raise LeanError("lean_rope_append", st)
@@ -519,14 +553,39 @@ def lean_kv_pages(lens, targets, block_table, free_ring, ring_state, page_size: 
         raise LeanError("lean_kv_pages", st)
 
 
+def lean_kv_read(k_cache, v_cache, slots, k_out, v_out, k_scales=None, v_scales=None, flags: int = 0,
+                 stream=None) -> None:
+    """The tokens at `slots` of the caches ([pages, page_size, kv_heads, dim]) as
+    rows of k_out and v_out [tokens, kv_heads, dim], float32, bfloat16 or float16,
+    whatever the caches are (int8 with k_scales and v_scales as for
+    lean_rope_append).  Either cache may be None with its output."""
+    here = _here()
+    some, out = (k_cache, k_out) if k_cache is not None else (v_cache, v_out)
+    if some is None or out is None or some.dim() != 4:
+        raise ValueError("k_cache with k_out or v_cache with v_out: [pages, page_size, kv_heads, dim] and"
+                         " [tokens, kv_heads, dim] are wanted")
+    shape, ct = some.shape, some.dtype
+    n, rows = slots.numel(), (slots.numel(),) + shape[2:]
+    kc, vc = _array(k_cache, shape, ct, "k_cache", here), _array(v_cache, shape, ct, "v_cache", here)
+    if kc[0] and vc[0] and vc[1:] != kc[1:]:
+        raise ValueError("k_cache and v_cache have different strides")
+    args = _KV_READ.pack(n, *shape[2:], _dtype(out), _cache_dtype(some), kc[0], vc[0], *shape[:2],
+                         *(kc if kc[0] else vc)[1:], *_scales(some, k_scales, v_scales, here),
+                         _plain(slots, n, _i32, "slots", here), *_array(k_out, rows, out.dtype, "k_out", here),
+                         *_array(v_out, rows, out.dtype, "v_out", here), flags)
+    st = _lib.lean_kv_read(args, _stream(stream))
+    if st:
+        raise LeanError("lean_kv_read", st)
+
+
 def lean_paged_attention_workspace_bytes(n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
     return _lib.lean_paged_attention_workspace_bytes(n_seqs, n_q_heads, n_kv_heads, head_dim)
 
 
 def lean_paged_attention(q, k_cache, v_cache, block_table, seq_lens, out, scale: float, window: int = 0, lse=None,
-                         workspace=None, flags: int = 0, stream=None) -> None:
+                         workspace=None, flags: int = 0, stream=None, k_scales=None, v_scales=None) -> None:
     """Attention of one new token per sequence: q and out [seqs, heads, dim], the
-    caches as for lean_rope_append, block_table [seqs, width], lse [seqs, heads]
+    caches (and scales) as for lean_rope_append, block_table [seqs, width], lse [seqs, heads]
     (None: not wanted); workspace: a uint8 tensor of
     lean_paged_attention_workspace_bytes."""
     here = _here()
@@ -540,10 +599,11 @@ def lean_paged_attention(q, k_cache, v_cache, block_table, seq_lens, out, scale:
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table: [%d, width] is wanted" % n)
     table = _array(block_table, block_table.shape, _i32, "block_table", here)
-    args = _ATTENTION.pack(n, hq, hkv, dim, _dtype(q), _dtype(k_cache), *_array(q, shape, at, "q", here), kc[0], vc[0],
+    args = _ATTENTION.pack(n, hq, hkv, dim, _dtype(q), _cache_dtype(k_cache), *_array(q, shape, at, "q", here), kc[0], vc[0],
                            pages, page, *kc[1:], table[0], block_table.shape[1], table[1],
                            _plain(seq_lens, n, _i32, "seq_lens", here), *_array(out, shape, at, "out", here),
-                           _rows(lse, n, hq, _f32, "lse", here), scale, window, *_workspace(workspace, here), flags)
+                           _rows(lse, n, hq, _f32, "lse", here), scale, window, *_workspace(workspace, here), flags,
+                           *_scales(k_cache, k_scales, v_scales, here))
     st = _lib.lean_paged_attention(args, _stream(stream))
     if st:
         raise LeanError("lean_paged_attention", st)

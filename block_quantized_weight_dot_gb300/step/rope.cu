@@ -46,6 +46,10 @@ struct RopeArgs {
     int cache_bf16;
     float scale;
     unsigned *err;
+    // caches in 8 bits
+    float *k_scales, *v_scales;
+    int64_t scale_page, scale_place, scale_hs;
+    int lanes;             // of a row
 };
 
 template <int V>
@@ -289,6 +293,226 @@ lean_status launch_rope(RopeArgs p, bool inter, int64_t flags, void *stream) {
     return step_launch(rope_kernel<A, V, false>, grid, threads, smem, flags, stream, p);
 }
 
+// ---- caches in 8 bits -------------------------------------------------------------
+
+// A row of a head as it goes to a cache in 8 bits: scale s = max |x| / 127, codes x / s to the nearest whole number,
+// halves away from 0.  The nearest is found from |x| * (1 / s), which is within 2^-15 of the quotient, and then put
+// right by the remainder |x| - c s, which fp32 holds exactly (it is a multiple of the smaller of the operands' last
+// places and below s): no division for each element, and the codes are those of the exact quotients.
+struct Quantizer {
+    float s, inv, up;  // scale, its inverse and the scale that |x| is compared with, both times `up`
+    float us;
+    bool some;  // a scale that is finite and not 0
+    // top: the largest |x|, as bits (an infinity or NaN is above every number)
+    __device__ __forceinline__ explicit Quantizer(uint32_t top) {
+        const float m = __uint_as_float(top);
+        s = __fdiv_rn(m, 127.f);
+        some = top < 0x7f800000u && s > 0.f;
+        if (top >= 0x7f800000u) s = CUDART_NAN_F;  // what is not finite makes the whole row NaN
+        up = m < 1e-18f ? 18446744073709551616.f : 1.f;  // 2^64: nothing below is subnormal
+        us = s * up;
+        inv = some ? 1.f / us : 0.f;
+    }
+    __device__ __forceinline__ uint32_t code(float x) const {  // in the low 8 bits
+        const float a = fabsf(x) * up;
+        const float t = fmaf(a, inv, 12582912.f);  // 1.5 * 2^23: a whole number in the low bits
+        const float r = fmaf(12582912.f - t, us, a), r2 = r + r;
+        int c = __float_as_int(t) - 0x4b400000;
+        c += r2 >= us ? 1 : 0;
+        c -= -r2 > us ? 1 : 0;
+        c = some ? min(c, 127) : 0;  // (above 127 where the scale is subnormal and rounded down)
+        return (uint32_t)(x < 0.f ? -c : c) & 0xffu;
+    }
+};
+template <int V>
+__device__ __forceinline__ void store_codes(int8_t *to, const float *f, const Quantizer &z) {
+    if constexpr (V == 1) {
+        *to = (int8_t)z.code(f[0]);
+    } else {
+        uint32_t w[V / 4];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            w[i] = z.code(f[4 * i]) | z.code(f[4 * i + 1]) << 8 | z.code(f[4 * i + 2]) << 16 | z.code(f[4 * i + 3]) << 24;
+        if constexpr (V == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(to) = w[0];
+    }
+}
+
+// A row (one head of q, k or v of one token) belongs to p.lanes neighbouring lanes, a power of two: each has up to 16
+// of its elements, in pieces of two runs as above, so that a row's largest element is found by shuffles alone and a
+// thread has U rows' loads under way.
+template <typename A, int V, bool INTER>
+__global__ void __launch_bounds__(256, 3) rope8_kernel(const RopeArgs p) {
+    step_begin();
+    constexpr int NP = 8 / V, U = V == 1 ? 1 : 4;  // pieces of a lane, rows at a time
+    extern __shared__ __align__(16) float2 cs[];  // [token][pair]: cosine, sine
+    __shared__ int64_t place[kRopeMaxTokens], scale_at[kRopeMaxTokens];
+    const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+    const int nt = (int)(p.n_tokens - t0 < p.tokens ? p.n_tokens - t0 : p.tokens);
+    const int half = p.rot / 2, G = p.lanes, heads = p.hq + 2 * p.hkv, rows = nt * heads;
+    const int lane = threadIdx.x % G, stride = 256 / G;
+    const int64_t cache_end = (p.n_slots / p.page - 1) * p.page_stride + (p.page - 1) * p.place_stride +
+                              (p.hkv - 1) * p.cache_hs + p.dim;
+    const int64_t scale_end = (p.n_slots / p.page - 1) * p.scale_page + (p.page - 1) * p.scale_place +
+                              (p.hkv - 1) * p.scale_hs + 1;
+    // a piece's runs: where they begin in a row, and their first pairs (-1: not rotated)
+    int a[NP], b[NP], pair_a[NP], pair_b[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int piece = lane + i * G;
+        const bool rotated = piece < p.rot_pieces;
+        if (INTER && V > 1) {
+            a[i] = piece * V;
+            b[i] = a[i] + p.dim / 2;
+            pair_a[i] = a[i] < p.rot ? a[i] / 2 : -1;
+            pair_b[i] = b[i] < p.rot ? b[i] / 2 : -1;
+        } else {
+            a[i] = INTER ? 2 * piece : rotated ? piece * V : p.rot + (piece - p.rot_pieces) * V;
+            b[i] = a[i] + (INTER ? 1 : rotated ? half : (p.dim - p.rot) / 2);
+            pair_a[i] = pair_b[i] = rotated ? piece * V : -1;
+        }
+        if (piece >= p.pieces) a[i] = -1;
+    }
+    Piece<A, V> x[U][NP][2];
+    auto load = [&](int row0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = row0 + u * stride;
+            const int t = row / heads, head = row - t * heads;
+            const bool is_q = head < p.hq, is_k = !is_q && head < p.hq + p.hkv;
+            const int kvh = head - p.hq - (is_k ? 0 : p.hkv);
+            const A *base = static_cast<const A *>(is_q ? p.q : is_k ? p.k : p.v);
+            const int64_t at = is_q ? (t0 + t) * p.qs + head * p.qhs : is_k ? (t0 + t) * p.ks + kvh * p.khs
+                                                                            : (t0 + t) * p.vs + kvh * p.vhs;
+            const int64_t end = is_q ? p.q_end : is_k ? p.k_end : p.v_end;
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    x[u][i][j] = Piece<A, V>{};
+                    const int64_t e = at + (j ? b[i] : a[i]);
+                    if (row < rows && a[i] >= 0 && LEAN_SPAN(e, V, end, p.err))
+                        x[u][i][j] = *reinterpret_cast<const Piece<A, V> *>(base + e);
+                }
+        }
+    };
+    const int first = threadIdx.x / G;
+    load(first);  // under way while the angles are computed
+    for (int i = threadIdx.x; i < nt * half; i += 256) {
+        const int t = i / half, j = i - t * half;
+        const int32_t pos = LEAN_IN(t0 + t, p.n_tokens, p.err) ? p.positions[t0 + t] : 0;
+        const uint64_t f = LEAN_IN(j, p.rot / 2, p.err) ? p.turns[j] : 0;
+        const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32), n = (uint32_t)pos;
+        const uint32_t turn = __umulhi(n, lo) + n * hi - (pos < 0 ? lo : 0u);
+        float sine, cosine;
+        sincospif((float)(int32_t)turn * (1.f / 2147483648.f), &sine, &cosine);
+        cs[i] = make_float2(cosine * p.scale, sine * p.scale);
+    }
+    if (threadIdx.x < nt) {
+        const int32_t s = LEAN_IN(t0 + threadIdx.x, p.n_tokens, p.err) ? p.slots[t0 + threadIdx.x] : -1;
+        int64_t at = -1, at_scale = -1;
+        if (s >= p.n_slots) atomicOr(p.err, kErrSlot);
+        else if (s >= 0) {
+            at = (int64_t)(s / p.page) * p.page_stride + (int64_t)(s % p.page) * p.place_stride;
+            at_scale = (int64_t)(s / p.page) * p.scale_page + (int64_t)(s % p.page) * p.scale_place;
+        }
+        place[threadIdx.x] = at;
+        scale_at[threadIdx.x] = at_scale;
+    }
+    __syncthreads();
+    // (every thread takes every turn of the loop: rows past the end are empty, and lanes of a warp stay together)
+    for (int row0 = first; row0 - first < rows; row0 += U * stride) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = row0 + u * stride;
+            const int t = min(row / heads, nt - 1), head = row - row / heads * heads;
+            const bool is_q = head < p.hq, is_k = !is_q && head < p.hq + p.hkv;
+            const int kvh = head - p.hq - (is_k ? 0 : p.hkv);
+            float f[NP][2 * V];
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                unpack_piece(x[u][i][0], f[i]);
+                unpack_piece(x[u][i][1], f[i] + V);
+                auto turn = [&](float &e0, float &e1, float2 c) {
+                    const float n0 = e0 * c.x - e1 * c.y, n1 = fmaf(e0, c.y, e1 * c.x);
+                    e0 = n0;
+                    e1 = n1;
+                };
+                const float2 *w = cs + t * half;
+                if ((is_q || is_k) && a[i] >= 0) {
+                    if (INTER && V > 1) {
+                        if (pair_a[i] >= 0)
+#pragma unroll
+                            for (int j = 0; j < V; j += 4) turn2(w + pair_a[i] + j / 2, f[i] + j, turn);
+                        if (pair_b[i] >= 0)
+#pragma unroll
+                            for (int j = 0; j < V; j += 4) turn2(w + pair_b[i] + j / 2, f[i] + V + j, turn);
+                    } else if (pair_a[i] >= 0) {
+                        if (V > 1) {
+#pragma unroll
+                            for (int j = 0; j < V; j += 2) {
+                                const float4 c = *reinterpret_cast<const float4 *>(w + pair_a[i] + j);
+                                turn(f[i][j], f[i][V + j], make_float2(c.x, c.y));
+                                turn(f[i][j + 1], f[i][V + j + 1], make_float2(c.z, c.w));
+                            }
+                        } else {
+                            turn(f[i][0], f[i][V], w[pair_a[i]]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 2 * V; ++j) top = max(top, __float_as_uint(f[i][j]) & 0x7fffffffu);
+            }
+            for (int o = G / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (row >= rows) continue;
+            A *dst = is_q ? static_cast<A *>(p.q_out) : is_k ? static_cast<A *>(p.k_out) : nullptr;
+            if (dst) {
+                const int64_t at = is_q ? (t0 + t) * p.qos + head * p.qohs : (t0 + t) * p.kos + kvh * p.kohs;
+                const int64_t end = is_q ? p.qo_end : p.ko_end;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    if (a[i] < 0) continue;
+                    if (LEAN_SPAN(at + a[i], V, end, p.err)) store_vec<A, V>(dst + at + a[i], f[i]);
+                    if (LEAN_SPAN(at + b[i], V, end, p.err)) store_vec<A, V>(dst + at + b[i], f[i] + V);
+                }
+            }
+            if (!is_q && place[t] >= 0) {
+                const Quantizer z(top);
+                int8_t *cache = static_cast<int8_t *>(is_k ? p.k_cache : p.v_cache);
+                const int64_t at = place[t] + kvh * p.cache_hs;
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    if (a[i] < 0) continue;
+                    if (LEAN_SPAN(at + a[i], V, cache_end, p.err)) store_codes<V>(cache + at + a[i], f[i], z);
+                    if (LEAN_SPAN(at + b[i], V, cache_end, p.err)) store_codes<V>(cache + at + b[i], f[i] + V, z);
+                }
+                const int64_t to = scale_at[t] + kvh * p.scale_hs;
+                if (lane == 0 && LEAN_IN(to, scale_end, p.err)) (is_k ? p.k_scales : p.v_scales)[to] = z.s;
+            }
+        }
+        if (row0 - first + U * stride < rows) load(row0 + U * stride);
+    }
+}
+
+template <typename A, int V>
+lean_status launch_rope8(RopeArgs p, bool inter, int64_t flags, void *stream) {
+    p.pieces = p.dim / (2 * V);
+    p.rot_pieces = p.rot / (2 * V);
+    p.lanes = 2;
+    while (p.lanes < p.pieces && p.lanes < 32) p.lanes *= 2;
+    // two rounds of rows a block, but no fewer blocks than two for an SM while there are tokens for them
+    const int64_t heads = p.hq + 2 * p.hkv, rows = 2 * (V == 1 ? 1 : 4) * 256 / p.lanes;
+    int64_t tokens = std::min<int64_t>(std::max<int64_t>(1, rows / heads),
+                                       std::max<int64_t>(1, p.n_tokens / (2 * step_sm_count())));
+    tokens = std::min<int64_t>(tokens, std::max(1, 4096 / std::max(p.rot / 2, 1)));  // angles: 32 KB at most
+    p.tokens = (int)std::min<int64_t>(tokens, kRopeMaxTokens);
+    const size_t smem = sizeof(float2) * p.tokens * std::max(p.rot / 2, 1);
+    const int64_t grid = (p.n_tokens + p.tokens - 1) / p.tokens;
+    if (inter) return step_launch(rope8_kernel<A, V, true>, grid, 256, smem, flags, stream, p);
+    return step_launch(rope8_kernel<A, V, false>, grid, 256, smem, flags, stream, p);
+}
+
 // Elements of a run: as many as 16 bytes have where every run is a whole number of
 // them and lies on 16 bytes, of 16-bit types else half as many, else one (2000
 // tokens of 32/8 bf16 heads of 80, 40 of them rotated: pairs of neighbours 7.6 us by
@@ -299,6 +523,11 @@ lean_status pick_rope(const RopeArgs &p, bool inter, int64_t any_stride, bool on
     auto fits = [&](int v) {
         return on16 && any_stride % v == 0 && p.dim % (2 * v) == 0 && p.rot % (inter ? v : 2 * v) == 0;
     };
+    if (p.k_scales) {
+        if (fits(V)) return launch_rope8<A, V>(p, inter, flags, stream);
+        if (V == 8 && fits(4)) return launch_rope8<A, 4>(p, inter, flags, stream);
+        return launch_rope8<A, 1>(p, inter, flags, stream);
+    }
     if (fits(V)) return launch_rope<A, V>(p, inter, flags, stream);
     if (V == 8 && fits(4)) return launch_rope<A, 4>(p, inter, flags, stream);
     return launch_rope<A, 1>(p, inter, flags, stream);
@@ -310,7 +539,8 @@ extern "C" lean_status lean_rope_append(const lean_rope_args *a, void *stream) {
     if (!a) return LEAN_ERR_NULL;
     if (!known_dtype(a->act_dtype) || !step_flags_ok(a->flags)) return LEAN_ERR_FORMAT;
     const bool cached = a->k_cache || a->v_cache;
-    if (cached && a->cache_dtype != LEAN_BF16 && a->cache_dtype != LEAN_F16) return LEAN_ERR_FORMAT;
+    const bool in8 = cached && a->cache_dtype == LEAN_I8;  // (the scales' fields are read for such caches only)
+    if (cached && !in8 && a->cache_dtype != LEAN_BF16 && a->cache_dtype != LEAN_F16) return LEAN_ERR_FORMAT;
     const int64_t strides[] = {a->q_stride, a->q_head_stride, a->k_stride, a->k_head_stride, a->v_stride,
                                a->v_head_stride, a->q_out_stride, a->q_out_head_stride, a->k_out_stride,
                                a->k_out_head_stride};
@@ -331,10 +561,12 @@ extern "C" lean_status lean_rope_append(const lean_rope_args *a, void *stream) {
             any |= s;
         }
         if (a->page_size <= 0 || a->n_pages <= 0 || a->n_pages > INT32_MAX / a->page_size) return LEAN_ERR_SHAPE;
+        if (in8 && (a->scale_page_stride < 0 || a->scale_place_stride < 0 || a->scale_head_stride < 0)) return LEAN_ERR_SHAPE;
     }
     if ((a->n_q_heads > 0) != (a->q != nullptr) || !a->q != !a->q_out || (a->n_kv_heads > 0) != (a->k != nullptr) ||
         (a->k_cache && !a->v_cache) || (a->v_cache && !a->k_cache) || (cached && (!a->k || !a->v || !a->slots)) ||
-        (a->k && !cached && !a->k_out) || (a->k_out && !a->k) || !a->positions || (a->rot_dim > 0 && !a->turns))
+        (a->k && !cached && !a->k_out) || (a->k_out && !a->k) || !a->positions || (a->rot_dim > 0 && !a->turns) ||
+        (in8 && (!a->k_scales || !a->v_scales)))
         return LEAN_ERR_NULL;
     const int64_t size = dtype_size(a->act_dtype);
     const void *acts[] = {a->q, a->k, a->v, a->q_out, a->k_out};
@@ -343,8 +575,10 @@ extern "C" lean_status lean_rope_append(const lean_rope_args *a, void *stream) {
         if (!step_aligned(q, size)) return LEAN_ERR_ALIGN;
         on16 = on16 && step_aligned(q, 16);
     }
-    if (!step_aligned(a->k_cache, 2) || !step_aligned(a->v_cache, 2) || !step_aligned(a->positions, 4) ||
-        !step_aligned(a->slots, 4) || !step_aligned(a->turns, 8))
+    const uintptr_t element = in8 ? 1 : 2;
+    if (!step_aligned(a->k_cache, element) || !step_aligned(a->v_cache, element) || !step_aligned(a->positions, 4) ||
+        !step_aligned(a->slots, 4) || !step_aligned(a->turns, 8) ||
+        (in8 && (!step_aligned(a->k_scales, 4) || !step_aligned(a->v_scales, 4))))
         return LEAN_ERR_ALIGN;
     RopeArgs p = {};
     p.q = a->q;
@@ -388,6 +622,13 @@ extern "C" lean_status lean_rope_append(const lean_rope_args *a, void *stream) {
     p.n_slots = cached ? a->n_pages * a->page_size : 1;
     p.cache_bf16 = a->cache_dtype == LEAN_BF16;
     p.scale = (float)a->rot_scale;
+    if (in8) {
+        p.k_scales = a->k_scales;
+        p.v_scales = a->v_scales;
+        p.scale_page = a->scale_page_stride;
+        p.scale_place = a->scale_place_stride;
+        p.scale_hs = a->scale_head_stride;
+    }
     p.err = error_word();
     if (!p.err) return LEAN_ERR_CUDA;
     const bool inter = a->interleaved != 0;

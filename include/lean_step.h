@@ -37,8 +37,14 @@
 extern "C" {
 #endif
 
-/* Element types of activations, residuals and caches. */
-typedef enum { LEAN_F32 = 0, LEAN_BF16 = 1, LEAN_F16 = 2 } lean_dtype;
+/* Element types of activations, residuals and caches.  LEAN_I8: of caches only
+ * (lean_rope_append, lean_paged_attention and the calls of lean_cache.h), whole
+ * numbers c in -127..127 with one fp32 scale s for each token and kv head, which
+ * stand for c * s.  The scales lie in two arrays beside the caches, at page *
+ * scale_page_stride + place * scale_place_stride + kv head * scale_head_stride
+ * (a head's places beside one another are read fastest: scale_place_stride 1).
+ * Their fields end the structs and are read for such caches only. */
+typedef enum { LEAN_F32 = 0, LEAN_BF16 = 1, LEAN_F16 = 2, LEAN_I8 = 3 } lean_dtype;
 
 /* Residual sum with the norms before and after a block, for each of `rows`
  * rows of `width` elements:
@@ -123,11 +129,15 @@ lean_status lean_rope_frequencies(int kind, int64_t rot_dim, double base, double
  * 0), and so may k, v and both caches (n_kv_heads 0).  k_out, optional, receives
  * the rotated k as well.  q_out may be q and k_out may be k, with the same
  * strides; otherwise outputs overlap nothing.
+ * LEAN_I8 caches: a head's elements x (of k as rotated in fp32, before k_out's
+ * rounding) are stored as s = max |x| / 127, rounded to fp32, and c = the whole
+ * number nearest to x / s, halves away from 0; s = 0 and c = 0 where all x are
+ * 0, s = NaN and c = 0 where one is not finite.  k_scales and v_scales hold s.
  * LEAN_ERR_SHAPE: n_tokens <= 0, negative head counts or both 0, head_dim odd
  * or not in 2..512, rot_dim odd, < 0 or > head_dim, a negative stride, page_size or
  * n_pages <= 0 or more than 2^31 - 1 slots (caches given).  LEAN_ERR_NULL: a
- * part missing.  LEAN_ERR_FORMAT: an unknown type or a cache_dtype that is
- * neither LEAN_BF16 nor LEAN_F16. */
+ * part missing.  LEAN_ERR_FORMAT: an unknown type or a cache_dtype that is none
+ * of LEAN_BF16, LEAN_F16 and LEAN_I8. */
 typedef struct {
     int64_t n_tokens, n_q_heads, n_kv_heads, head_dim;
     int64_t rot_dim;
@@ -153,6 +163,8 @@ typedef struct {
     int64_t page_stride, place_stride, cache_head_stride;
     double rot_scale;
     int64_t flags;
+    float *k_scales, *v_scales; /* LEAN_I8: float[page][place][kv head] by strides */
+    int64_t scale_page_stride, scale_place_stride, scale_head_stride;
 } lean_rope_args;
 lean_status lean_rope_append(const lean_rope_args *args, void *stream);
 
@@ -222,12 +234,17 @@ lean_status lean_kv_pages(const lean_kv_pages_args *args, void *stream);
  * word; a length below 0 counts as 0, one past table_width * page_size as that.
  * What is not finite among the attended keys and values gives NaN or infinities
  * in the outputs that it reaches.
+ * LEAN_I8 caches: k_j = c s of k_scales, v_j of v_scales; a scale that is not
+ * finite counts as a key or value that is not.
  * q and p are split in parts of the cache's type, three for fp32 q and out and
  * two for 16-bit ones, and sums are fp32, so that fp32 q keeps its precision: out
  * errs by about 2^-17 of sum p |v|, and by fp32's rounding of the scores.  With an
  * f16 cache each p errs by up to 2^-38 of the sequence's largest one as well, and
- * each element of q by 2^-38 of its head's largest (f16 has no smaller steps).
- * q, out and the caches: 16-byte aligned, strides multiples of 8 elements.
+ * each element of q by 2^-38 of its head's largest (f16 has no smaller steps);
+ * with a LEAN_I8 cache p times its token's v_scales is so held, to 2^-38 of the
+ * largest p times the largest of the v_scales.
+ * q, out and the caches: 16-byte aligned, strides multiples of 8 elements
+ * (LEAN_I8 caches: of 16, and head_dim as well).
  * workspace: lean_paged_attention_workspace_bytes() bytes, 256-byte aligned,
  * any contents.  Calls that may run at the same time must not share one.
  * Results do not depend on timing.
@@ -235,8 +252,8 @@ lean_status lean_kv_pages(const lean_kv_pages_args *args, void *stream);
  * of 8 or above 256, window < 0, table_width * page_size above 2^31 - 1, more
  * than 2^31 - 1 sequences x heads, sequences x kv heads x table_width x page_size
  * / 16 near 2^32 or above, or a workspace too small.  LEAN_ERR_ALIGN,
- * LEAN_ERR_NULL, LEAN_ERR_FORMAT as for the other calls (cache_dtype: LEAN_BF16
- * or LEAN_F16). */
+ * LEAN_ERR_NULL, LEAN_ERR_FORMAT as for the other calls (cache_dtype: LEAN_BF16,
+ * LEAN_F16 or LEAN_I8). */
 typedef struct {
     int64_t n_seqs, n_q_heads, n_kv_heads, head_dim;
     int64_t act_dtype;         /* of q and out                                 */
@@ -257,6 +274,8 @@ typedef struct {
     void *workspace;
     int64_t workspace_bytes;
     int64_t flags;
+    const float *k_scales, *v_scales; /* LEAN_I8: as for lean_rope_append      */
+    int64_t scale_page_stride, scale_place_stride, scale_head_stride;
 } lean_attention_args;
 lean_status lean_paged_attention(const lean_attention_args *args, void *stream);
 /* -1 for sizes that lean_paged_attention refuses. */

@@ -1,0 +1,207 @@
+"""Plain 64-bit forms of the cache in 8 bits and runners that call the library on
+small inputs and compare.  U, HALF, TINY and the tolerances' reasoning: step_testlib."""
+import math
+
+import numpy as np
+
+from lean_testlib import torch_cuda
+from step_testlib import HALF, TINY, U, attend_ref, close, dtype, gen, normal, rotate_ref, strided
+
+
+def codes_ref(x):
+    """(codes, scales) of rows of fp32 x [..., dim] by the definition: s = max |x| / 127 rounded to fp32, c nearest to
+    x / s, halves away from 0.  The quotient of two fp32 numbers is either half-way between whole numbers or further
+    from it than the last place of a double, so that it may be taken in 64 bits."""
+    torch = torch_cuda()
+    x = x.float()
+    top = x.abs().amax(-1)
+    ok = torch.isfinite(x).all(-1)
+    s = torch.where(ok, (torch.where(ok, top, 0.0).double() / 127).float(), math.nan)  # (two roundings: see below)
+    r = x.double() / s.double()[..., None]
+    r = torch.where(torch.isfinite(r), r, 0.0)
+    c = torch.trunc(r + torch.where(r < 0, -0.5, 0.5)).clamp(-127, 127)
+    return c.to(torch.int8), s
+
+
+# (A quotient by 127 rounded to 53 and then to 24 bits is the one rounded to 24: its expansion in base 2 has period 7,
+# so that no run of 29 equal digits, which a second rounding could turn over, follows the 24th place.)
+
+
+def scales_like(cache, heads_first, fill=7.0):
+    """[pages, page, kv heads] float32 beside a cache: the places of a head, or the heads of a place, next to one another."""
+    torch = torch_cuda()
+    p, n, h = cache.shape[:3]
+    if heads_first:
+        return torch.full((p, h, n), fill, device="cuda").transpose(1, 2)
+    return torch.full((p, n, h), fill, device="cuda")
+
+
+def make_cache8(pool, page, hkv, dim, seed, spread=0.5, heads_first=True):
+    """Random codes and scales (log-normal) of a whole cache."""
+    torch = torch_cuda()
+    g = gen(7000 + seed)
+    out = []
+    for _ in range(2):
+        c = torch.randint(-127, 128, (pool, page, hkv, dim), generator=g, device="cuda", dtype=torch.int32).to(torch.int8)
+        s = scales_like(c, heads_first)
+        s.copy_(torch.exp(spread * torch.randn((pool, page, hkv), generator=g, device="cuda")) / 73)
+        out += [c, s]
+    return out  # k, its scales, v, its scales
+
+
+def run_append8(lean, tokens, hq, hkv, dim, rot, act="f32", inter=False, page=16, start=0, scale=1.0, seed=0, pad=0,
+                in_place=False, k_out=False, padding=(), heads_first=True, cache_pad=0, flags=0, stream=None, x=None):
+    torch = torch_cuda()
+    g = gen(7100 + seed)
+    q = normal(g, tokens, hq, dim, t=act) if hq else None
+    k, v = (normal(g, tokens, hkv, dim, t=act) for _ in range(2)) if x is None else x
+    freq = lean.lean_rope_frequencies(lean.LEAN_ROPE_PLAIN, rot, 10000.0) if rot else np.zeros(0)
+    turns = torch.from_numpy(lean.lean_rope_turns(freq)).cuda() if rot else None
+    pos = (torch.arange(tokens, device="cuda") * 7 + start).to(torch.int32)
+    pages = -(-tokens // page) + 2
+    order = torch.randperm(pages, generator=g, device="cuda")
+    at = torch.arange(tokens, device="cuda")
+    slots = (order[at // page] * page + at % page).to(torch.int32)
+    for t in padding:
+        slots[t] = -1
+    kc, vc = (torch.full((pages, page, hkv, dim + cache_pad), 99, device="cuda", dtype=torch.int8)[..., :dim] for _ in range(2))
+    ks, vs = (scales_like(kc, heads_first) for _ in range(2))
+    # without a rotation x is what it is; with one, k errs as in step_testlib.run_rope
+    rel = (4 + 2 * math.pi + 3) * U if rot else 0.0
+    want_q = rotate_ref(q, pos, freq, rot, inter, scale) if hq else None
+    want_k = rotate_ref(k, pos, freq, rot, inter, scale)
+    size = lambda t: t.double().abs().amax(-1, keepdim=True) * 2 * abs(scale)  # noqa: E731
+    qsize, ksize = size(q) if hq else None, size(k)
+    k_is, v_is = k.float(), v.float()
+    if pad:
+        q, k, v = (strided(t, pad) if t is not None else None for t in (q, k, v))
+    qo = None if not hq else q if in_place else torch.empty((tokens, hq, dim), device="cuda", dtype=dtype(act))
+    ko = None if not k_out else k if in_place else torch.empty((tokens, hkv, dim), device="cuda", dtype=dtype(act))
+    torch.cuda.synchronize()
+    lean.lean_rope_append(q, k, v, pos, slots, turns, qo, kc, vc, rot_dim=rot, interleaved=inter, rot_scale=scale, k_out=ko,
+                          flags=flags, stream=stream, k_scales=ks, v_scales=vs)
+    torch.cuda.synchronize()
+    what = "append8 %dx%d/%dx%d rot %d %s" % (tokens, hq, hkv, dim, rot, act)
+    if hq:
+        close(qo, want_q, rel * qsize + HALF[act] * (want_q.abs() + rel * qsize) + TINY[act], what + " q")
+    if ko is not None:
+        close(ko, want_k, rel * ksize + HALF[act] * (want_k.abs() + rel * ksize) + TINY[act], what + " k_out")
+    kept = [t for t in range(tokens) if t not in set(padding)]
+    s = slots[kept].long()
+    where = s // page, s % page
+    for name, is_x, codes, scales in (("v", v_is, vc, vs), ("k", k_is, kc, ks)):
+        got_c, got_s = codes[where], scales[where]
+        if name == "v" or not rot:
+            want_c, want_s = codes_ref(is_x[kept])
+            same = (got_s == want_s) | (torch.isnan(got_s) & torch.isnan(want_s))
+            assert bool(same.all()), what + " %s scales: %r" % (name, (~same).nonzero()[:3])
+            assert torch.equal(got_c, want_c), what + " %s codes: %r" % (name, (got_c != want_c).nonzero()[:3])
+        else:
+            err = (rel * ksize[kept])[..., 0]
+            top = want_k[kept].abs().amax(-1)
+            close(got_s, top / 127, err / 127 + U * (top + err) / 127, what + " k scales")
+            # half a step, of the scale that was stored, and what x and the quotient by 127 err by
+            close(got_c.double() * got_s.double()[..., None], want_k[kept],
+                  (0.5 * (1 + 4 * U) * got_s.double() + 2 * err + 127 * U * got_s.double())[..., None], what + " k values")
+            assert int(got_c.abs().amax()) == 127
+    for codes, scales in ((kc, ks), (vc, vs)):  # every other place untouched
+        codes[where], scales[where] = 99, 7.0
+        assert bool((codes == 99).all()) and bool((scales == 7.0).all()), what + ": a write outside the slots"
+
+
+def run_read(lean, tokens, hkv, dim, page=16, cache="i8", out="f32", pool=None, heads_first=True, pad=0, cache_pad=0,
+             slots=None, which="kv", seed=0, flags=0, stream=None, heads_major=False):
+    torch = torch_cuda()
+    g = gen(7200 + seed)
+    pool = pool or -(-tokens // page) + 2
+    ks = vs = None
+    if cache == "i8":
+        kc, ks, vc, vs = make_cache8(pool, page, hkv, dim + cache_pad, seed, heads_first=heads_first)
+        kc, vc = kc[..., :dim], vc[..., :dim]
+    else:
+        kc, vc = (normal(g, pool, page, hkv, dim + cache_pad, t=cache)[..., :dim] for _ in range(2))
+    if slots is None:
+        slots = torch.randint(0, pool * page, (tokens,), generator=g, device="cuda").tolist()  # some of them twice
+    sd = torch.tensor(slots, dtype=torch.int32, device="cuda")
+
+    def room():
+        if heads_major:
+            return torch.full((hkv, tokens, dim), 7.0, device="cuda", dtype=dtype(out)).transpose(0, 1)
+        return strided(torch.full((tokens, hkv, dim), 7.0, device="cuda", dtype=dtype(out)), pad) if pad else \
+            torch.full((tokens, hkv, dim), 7.0, device="cuda", dtype=dtype(out))
+    ko, vo = room() if "k" in which else None, room() if "v" in which else None
+    torch.cuda.synchronize()
+    lean.lean_kv_read(kc if "k" in which else None, vc if "v" in which else None, sd, ko, vo,
+                      k_scales=ks if "k" in which else None, v_scales=vs if "v" in which else None, flags=flags, stream=stream)
+    torch.cuda.synchronize()
+    s = sd.long()
+    ok, none = (s >= 0) & (s < pool * page), s < 0
+    at = torch.where(ok, s, 0)
+    for name, got, c, sc in (("k", ko, kc, ks), ("v", vo, vc, vs)):
+        if got is None:
+            continue
+        want = c[at // page, at % page].double()
+        if sc is not None:  # (the product is exact in 64 bits; fp32, then the output's type)
+            want = want * sc[at // page, at % page].double()[..., None]
+        want = want.float().to(dtype(out))
+        want[none] = 0
+        want[~ok & ~none] = math.nan
+        same = (got == want) | (torch.isnan(got) & torch.isnan(want))
+        assert bool(same.all()), "read %s %s: %r" % (name, cache, (~same).nonzero()[:3])
+        if pad and tokens > 1:
+            flat = got.as_strided((tokens - 1, got.stride(0)), (got.stride(0), 1))[:, hkv * dim:]
+            assert bool(torch.isnan(flat).all()), "a write between the rows"
+
+
+def make_attend8(lens, hq, hkv, dim, page, act, seed=0, width=None, heads_first=True, spread=0.5, junk=math.nan):
+    """q, caches with their scales and the table of a batch; scales that no sequence holds are junk, and table entries
+    past a sequence's pages far outside the cache."""
+    torch = torch_cuda()
+    need = [-(-max(x, 0) // page) for x in lens]
+    pool = sum(need) + 3
+    width = width or max(1, max(need))
+    kc, ks, vc, vs = make_cache8(pool, page, hkv, dim, seed, spread, heads_first)
+    g = gen(7300 + seed)
+    order = torch.randperm(pool, generator=g, device="cuda").tolist()
+    table = torch.full((len(lens), width), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    held = torch.zeros((pool, page), dtype=torch.bool, device="cuda")
+    for s, x in enumerate(lens):
+        for j in range(need[s]):
+            pg = order.pop()
+            table[s, j] = pg
+            held[pg, :min(page, x - j * page)] = True
+    for t in (ks, vs):
+        t[~held] = junk
+    q = normal(g, len(lens), hq, dim, t=act, std=1.5)
+    return q, kc, ks, vc, vs, table
+
+
+def run_attend8(lean, lens, hq, hkv, dim, page=16, act="f32", window=0, seed=0, lse=True, pad=0, heads_first=True, width=None,
+                flags=0, scale=None, stream=None, inputs=None, workspace=None, spread=0.5, junk=math.nan):
+    torch = torch_cuda()
+    q, kc, ks, vc, vs, table = inputs or make_attend8(lens, hq, hkv, dim, page, act, seed, width, heads_first, spread, junk)
+    scale = 1 / math.sqrt(dim) if scale is None else scale
+    if pad:
+        q = strided(q, pad)
+    ld = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = torch.full((len(lens), hq, dim), 7.0, device="cuda", dtype=dtype(act))
+    ls = torch.full((len(lens), hq), 7.0, device="cuda") if lse else None
+    ws = workspace
+    if ws is None:
+        ws = torch.zeros(lean.lean_paged_attention_workspace_bytes(len(lens), hq, hkv, dim), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    lean.lean_paged_attention(q, kc, vc, table, ld, out, scale=scale, window=window, lse=ls, workspace=ws, flags=flags,
+                              stream=stream, k_scales=ks, v_scales=vs)
+    torch.cuda.synchronize()
+    kd, vd = kc.double() * ks.double()[..., None], vc.double() * vs.double()[..., None]
+    want, want_lse, size, reach = attend_ref(q, kd, vd, table, lens, scale, window)
+    # as step_testlib.run_attend; codes are exact in the instruction's type, two more products by scales in fp32
+    seen = max([1] + [min(x, window) if window else x for x in lens])
+    rel = (2 * 2.0 ** -16 + 20 * U) * reach + 2.0 ** -16 + (seen / 8 + 68) * U
+    what = "attend8 %s heads %d/%d dim %d page %d %s window %d" % (lens[:4], hq, hkv, dim, page, act, window)
+    top = torch.where(torch.isfinite(vd), vd.abs(), 0.0).max()
+    err = rel[..., None] * size + 2.0 ** -37 * top
+    close(out, want, err + HALF[act] * (want.abs() + err) + TINY[act], what)
+    if lse:
+        close(ls, want_lse, rel + 4 * U * torch.where(want_lse.isinf(), 0.0, want_lse).abs(), what + " lse")
+    return out, ls
