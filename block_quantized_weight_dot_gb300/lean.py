@@ -69,6 +69,8 @@ SIGNATURES = {
     "lean_kv_read": (_int, [_vp, _vp]),
     "lean_paged_attention": (_int, [_vp, _vp]),
     "lean_paged_attention_workspace_bytes": (_i64, [_i64] * 4),
+    "lean_prefix_attention": (_int, [_vp, _vp]),
+    "lean_prefix_attention_workspace_bytes": (_i64, [_i64] * 5),
     "lean_token_logprobs": (_int, [_vp, _vp]),
     "lean_token_logprobs_workspace_bytes": (_i64, [_i64] * 3),
 }
@@ -339,6 +341,7 @@ _ROPE = struct.Struct("<8q" + "Q2q" * 5 + "3Q2Q5qdq" + "2Q3q")
 _PAGES = struct.Struct("<3q3Q2qQqQ2Q5Qq")
 _ATTENTION = struct.Struct("<6qQ2q2Q5qQ2qQQ2qQdqQqq" + "2Q3q")
 _KV_READ = struct.Struct("<5q2Q5q2Q3qQQ2qQ2qq")
+_PREFIX = struct.Struct("<6qQ2q2Q5q2Q3qqQ2q3Q2qQQ2qQdQqq")
 _LOGPROBS = struct.Struct("<3qQqQdq5QQqq")
 _dtypes = {}
 _i32 = _f32 = _i64t = _u8 = _i8 = None  # torch's, once a call has needed them
@@ -607,6 +610,46 @@ def lean_paged_attention(q, k_cache, v_cache, block_table, seq_lens, out, scale:
     st = _lib.lean_paged_attention(args, _stream(stream))
     if st:
         raise LeanError("lean_paged_attention", st)
+
+
+def lean_prefix_attention_workspace_bytes(n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                                          n_prefixes: int) -> int:
+    return _lib.lean_prefix_attention_workspace_bytes(n_seqs, n_q_heads, n_kv_heads, head_dim, n_prefixes)
+
+
+def lean_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, seq_starts, block_table, seq_lens, out,
+                          scale: float, lse=None, workspace=None, flags: int = 0, stream=None, k_scales=None,
+                          v_scales=None) -> None:
+    """Attention of one new token per sequence where sequences seq_starts[p] ..
+    seq_starts[p + 1] - 1 begin with prefix p: prefix_table [prefixes, width] and
+    prefix_lens [prefixes] have its pages and length, block_table [seqs, width] and
+    seq_lens [seqs] those of the sequences' own tokens after it; the rest as for
+    lean_paged_attention.  workspace: a uint8 tensor of
+    lean_prefix_attention_workspace_bytes."""
+    here = _here()
+    shape, at, ct = q.shape, q.dtype, k_cache.dtype
+    n, hq, dim = shape
+    pages, page, hkv = k_cache.shape[:3]
+    kc = _array(k_cache, (pages, page, hkv, dim), ct, "k_cache", here)
+    vc = _array(v_cache, (pages, page, hkv, dim), ct, "v_cache", here)
+    if vc[1:] != kc[1:]:
+        raise ValueError("k_cache and v_cache have different strides")
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError("block_table: [%d, width] is wanted" % n)
+    if prefix_table.dim() != 2:
+        raise ValueError("prefix_table: [prefixes, width] is wanted")
+    prefixes = prefix_table.shape[0]
+    shared = _array(prefix_table, prefix_table.shape, _i32, "prefix_table", here)
+    table = _array(block_table, block_table.shape, _i32, "block_table", here)
+    args = _PREFIX.pack(n, hq, hkv, dim, _dtype(q), _cache_dtype(k_cache), *_array(q, shape, at, "q", here), kc[0], vc[0],
+                        pages, page, *kc[1:], *_scales(k_cache, k_scales, v_scales, here), prefixes, shared[0],
+                        prefix_table.shape[1], shared[1], _plain(prefix_lens, prefixes, _i32, "prefix_lens", here),
+                        _plain(seq_starts, prefixes + 1, _i32, "seq_starts", here), table[0], block_table.shape[1], table[1],
+                        _plain(seq_lens, n, _i32, "seq_lens", here), *_array(out, shape, at, "out", here),
+                        _rows(lse, n, hq, _f32, "lse", here), scale, *_workspace(workspace, here), flags)
+    st = _lib.lean_prefix_attention(args, _stream(stream))
+    if st:
+        raise LeanError("lean_prefix_attention", st)
 
 
 def lean_token_logprobs_workspace_bytes(rows: int, vocab: int, top_k: int) -> int:

@@ -74,7 +74,7 @@ extern "C" lean_status lean_paged_attention(const lean_attention_args *a, void *
         !step_aligned(a->lse, 4) || !step_aligned(a->workspace, 256))
         return LEAN_ERR_ALIGN;
     const int64_t group = a->n_q_heads / a->n_kv_heads, tiles = group > 8 ? (group + 15) / 16 : 1;
-    if ((a->table_width * a->page_size / kUnit + 2 + kItemUnits) * a->n_seqs * a->n_kv_heads * tiles > UINT32_MAX)
+    if ((a->table_width * a->page_size / kUnit + 2 + kAttItemUnits) * a->n_seqs * a->n_kv_heads * tiles > UINT32_MAX)
         return LEAN_ERR_SHAPE;  // units are counted in 32 bits
     if (a->workspace_bytes <
         lean_paged_attention_workspace_bytes(a->n_seqs, a->n_q_heads, a->n_kv_heads, a->head_dim))

@@ -61,6 +61,7 @@ constexpr int kAttMaxDim = 256;
 constexpr int kAttMaxCtas = 160;  // of a launch: at most one per SM
 constexpr int kAttMaxWarps = 8;   // of a block
 constexpr int kUnit = 16;         // tokens
+constexpr int kAttItemUnits = 4;  // empty units counted to an item (below)
 constexpr int64_t kSharedBytes = 2048;  // a Shared for each block
 
 struct Shared {  // an item that begins in a block and goes on in others (-1: none), and how many blocks it has
@@ -334,7 +335,7 @@ constexpr int kFold = 64;
 // units (q, the first maximum, the result): that many empty ones are counted to it
 // when the runs are cut.
 constexpr int kJoinUnits = 8;
-constexpr int kItemUnits = 4;
+constexpr int kItemUnits = kAttItemUnits;
 
 // Parts added up: maximum, sum and outputs.
 struct Sums {
@@ -740,6 +741,11 @@ __global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel
                                                                     stage * AttShape<C, DP>::kScaleBytes) + c4;
                 ks[0] = at[0];
                 ks[1] = at[4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {  // an infinite one is NaN, as the scores of such a key are
+                    ks[j].x += ks[j].x - ks[j].x;
+                    ks[j].y += ks[j].y - ks[j].y;
+                }
                 vs[0] = at[8];
                 vs[1] = at[12];
             }

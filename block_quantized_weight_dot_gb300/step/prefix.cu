@@ -1,0 +1,200 @@
+// prefix.cu -- lean_prefix_attention: the call, and the kernels of prefix.cuh for
+// caches of 16 bits.
+#include "prefix.cuh"
+
+namespace lean {
+
+lean_status prefix_cache16(const PrefixArgs &p, bool bf16, bool two, int64_t flags, void *stream) {
+    if (bf16)
+        return p.dim <= 64 ? pick_prefix<__nv_bfloat16, 64>(p, two, flags, stream)
+                           : pick_prefix<__nv_bfloat16, 128>(p, two, flags, stream);
+    return p.dim <= 64 ? pick_prefix<__half, 64>(p, two, flags, stream) : pick_prefix<__half, 128>(p, two, flags, stream);
+}
+
+}  // namespace lean
+
+namespace {
+
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+int prefix_dim(int64_t dim) { return dim <= 64 ? 64 : 128; }
+
+bool prefix_sizes_ok(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim, int64_t n_prefixes) {
+    return att_sizes_ok(n_seqs, hq, hkv, dim) && dim <= 128 && n_prefixes > 0 && n_prefixes <= n_seqs;
+}
+
+// The workspace's parts: that of attend.cuh, the list, sequences' own results, maxima and sums, outputs.
+struct PrefixRoom {
+    int64_t plan, own_out, own_lse, ml, o, bytes, parts;
+};
+PrefixRoom prefix_room(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim, int64_t n_prefixes) {
+    PrefixRoom r;
+    const int64_t rows = n_seqs * hq;
+    r.parts = 2 * rows + kPrefixMaxCtas * 256;
+    r.plan = up256(att_workspace_bytes(hq, hkv, dim));
+    r.own_out = r.plan + up256((n_prefixes + 1) * 8);
+    r.own_lse = r.own_out + up256(rows * dim * 4);
+    r.ml = r.own_lse + up256(rows * 4);
+    r.o = r.ml + up256(r.parts * 8);
+    r.bytes = r.o + r.parts * prefix_dim(dim) * 4;
+    return r;
+}
+
+}  // namespace
+
+extern "C" int64_t lean_prefix_attention_workspace_bytes(int64_t n_seqs, int64_t n_q_heads, int64_t n_kv_heads,
+                                                         int64_t head_dim, int64_t n_prefixes) {
+    if (!prefix_sizes_ok(n_seqs, n_q_heads, n_kv_heads, head_dim, n_prefixes)) return -1;
+    return prefix_room(n_seqs, n_q_heads, n_kv_heads, head_dim, n_prefixes).bytes;
+}
+
+extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *stream) {
+    if (!a) return LEAN_ERR_NULL;
+    const bool in8 = a->cache_dtype == LEAN_I8;
+    if (!known_dtype(a->act_dtype) || (!in8 && a->cache_dtype != LEAN_BF16 && a->cache_dtype != LEAN_F16) ||
+        !step_flags_ok(a->flags))
+        return LEAN_ERR_FORMAT;
+    if (!prefix_sizes_ok(a->n_seqs, a->n_q_heads, a->n_kv_heads, a->head_dim, a->n_prefixes) || a->n_pages <= 0 ||
+        a->n_pages > INT32_MAX || a->page_size <= 0 || a->table_width <= 0 || a->table_width > INT32_MAX / a->page_size ||
+        a->table_stride < a->table_width || a->prefix_width <= 0 || a->prefix_width > INT32_MAX / a->page_size ||
+        a->prefix_stride < a->prefix_width)
+        return LEAN_ERR_SHAPE;
+    if (in8 && (a->head_dim % 16 || a->scale_page_stride < 0 || a->scale_place_stride < 0 || a->scale_head_stride < 0))
+        return LEAN_ERR_SHAPE;
+    if (!a->q || !a->k_cache || !a->v_cache || !a->prefix_table || !a->prefix_lens || !a->seq_starts || !a->block_table ||
+        !a->seq_lens || !a->out || !a->workspace || (in8 && (!a->k_scales || !a->v_scales)))
+        return LEAN_ERR_NULL;
+    const int64_t act_strides[] = {a->q_stride, a->q_head_stride, a->out_stride, a->out_head_stride};
+    const int64_t cache_strides[] = {a->page_stride, a->place_stride, a->cache_head_stride};
+    for (int64_t s : act_strides) {
+        if (s < 0) return LEAN_ERR_SHAPE;
+        if (s % 8) return LEAN_ERR_ALIGN;
+    }
+    for (int64_t s : cache_strides) {
+        if (s < 0) return LEAN_ERR_SHAPE;
+        if (s % (in8 ? 16 : 8)) return LEAN_ERR_ALIGN;
+    }
+    const void *on16[] = {a->q, a->k_cache, a->v_cache, a->out}, *on4[] = {a->prefix_table, a->prefix_lens, a->seq_starts,
+                                                                           a->block_table, a->seq_lens, a->lse};
+    for (const void *x : on16)
+        if (!step_aligned(x, 16)) return LEAN_ERR_ALIGN;
+    for (const void *x : on4)
+        if (!step_aligned(x, 4)) return LEAN_ERR_ALIGN;
+    if (!step_aligned(a->workspace, 256) || (in8 && (!step_aligned(a->k_scales, 4) || !step_aligned(a->v_scales, 4))))
+        return LEAN_ERR_ALIGN;
+    const int64_t group = a->n_q_heads / a->n_kv_heads, tiles = group > 8 ? (group + 15) / 16 : 1;
+    if ((a->table_width * a->page_size / kUnit + 2 + kAttItemUnits) * a->n_seqs * a->n_kv_heads * tiles > UINT32_MAX)
+        return LEAN_ERR_SHAPE;  // attend.cuh counts units of sequences' own tokens in 32 bits
+    const PrefixRoom room = prefix_room(a->n_seqs, a->n_q_heads, a->n_kv_heads, a->head_dim, a->n_prefixes);
+    if (a->workspace_bytes < room.bytes) return LEAN_ERR_SHAPE;
+    uint8_t *const ws = static_cast<uint8_t *>(a->workspace);
+    unsigned *const err = error_word();
+    if (!err) return LEAN_ERR_CUDA;
+
+    AttArgs own = {};
+    own.q = a->q;
+    own.k = a->k_cache;
+    own.v = a->v_cache;
+    own.out = ws + room.own_out;
+    own.lse = reinterpret_cast<float *>(ws + room.own_lse);
+    own.table = a->block_table;
+    own.lens = a->seq_lens;
+    own.qs = a->q_stride;
+    own.qhs = a->q_head_stride;
+    own.os = a->n_q_heads * a->head_dim;
+    own.ohs = a->head_dim;
+    own.page_stride = a->page_stride;
+    own.place_stride = a->place_stride;
+    own.cache_hs = a->cache_head_stride;
+    own.table_stride = a->table_stride;
+    own.n_pages = a->n_pages;
+    own.n_seqs = (int)a->n_seqs;
+    own.hq = (int)a->n_q_heads;
+    own.hkv = (int)a->n_kv_heads;
+    own.group = (int)group;
+    own.tiles = (int)tiles;
+    own.dim = (int)a->head_dim;
+    own.page = (int)a->page_size;
+    own.paged = a->page_size >= kUnit;
+    own.whole = a->page_size % kUnit == 0;
+    own.width = (int)a->table_width;
+    own.act = (int)a->act_dtype;
+    own.out_act = LEAN_F32;
+    own.scale_log2 = (float)(a->scale * 1.4426950408889634);
+    own.cache_extent = (a->n_pages - 1) * a->page_stride + (a->page_size - 1) * a->place_stride +
+                       (a->n_kv_heads - 1) * a->cache_head_stride + a->head_dim;
+    own.q_extent = (a->n_seqs - 1) * a->q_stride + (a->n_q_heads - 1) * a->q_head_stride + a->head_dim;
+    own.out_extent = a->n_seqs * a->n_q_heads * a->head_dim;
+    own.err = err;
+    att_workspace(own, ws);
+    if (in8) {
+        own.k_scales = a->k_scales;
+        own.v_scales = a->v_scales;
+        own.scale_page = a->scale_page_stride;
+        own.scale_place = a->scale_place_stride;
+        own.scale_hs = a->scale_head_stride;
+        own.scale_extent = (a->n_pages - 1) * a->scale_page_stride + (a->page_size - 1) * a->scale_place_stride +
+                           (a->n_kv_heads - 1) * a->scale_head_stride + 1;
+    }
+
+    PrefixArgs p = {};
+    p.q = own.q;
+    p.k = own.k;
+    p.v = own.v;
+    p.k_scales = own.k_scales;
+    p.v_scales = own.v_scales;
+    p.table = a->prefix_table;
+    p.lens = a->prefix_lens;
+    p.starts = a->seq_starts;
+    p.qs = own.qs;
+    p.qhs = own.qhs;
+    p.page_stride = own.page_stride;
+    p.place_stride = own.place_stride;
+    p.cache_hs = own.cache_hs;
+    p.scale_page = own.scale_page;
+    p.scale_place = own.scale_place;
+    p.scale_hs = own.scale_hs;
+    p.table_stride = a->prefix_stride;
+    p.n_pages = own.n_pages;
+    p.n_prefixes = (int)a->n_prefixes;
+    p.n_seqs = own.n_seqs;
+    p.hq = own.hq;
+    p.hkv = own.hkv;
+    p.group = own.group;
+    p.dim = own.dim;
+    p.page = own.page;
+    p.width = (int)a->prefix_width;
+    p.act = own.act;
+    p.scale_log2 = own.scale_log2;
+    p.plan = reinterpret_cast<unsigned long long *>(ws + room.plan);
+    p.ml = reinterpret_cast<float2 *>(ws + room.ml);
+    p.o = reinterpret_cast<float *>(ws + room.o);
+    p.parts = room.parts;
+    p.own_out = static_cast<const float *>(own.out);
+    p.own_lse = own.lse;
+    p.out = a->out;
+    p.lse = a->lse;
+    p.os = a->out_stride;
+    p.ohs = a->out_head_stride;
+    p.cache_extent = own.cache_extent;
+    p.scale_extent = own.scale_extent;
+    p.q_extent = own.q_extent;
+    p.out_extent = (a->n_seqs - 1) * a->out_stride + (a->n_q_heads - 1) * a->out_head_stride + a->head_dim;
+    p.err = err;
+
+    // Two tiles of rows where a prefix has more than one of them on average (below that the second would be empty).
+    const bool two = a->act_dtype != LEAN_F32 && !(a->act_dtype == LEAN_F16 && a->cache_dtype == LEAN_BF16) &&
+                     a->n_seqs * group > a->n_prefixes * kTileRows;
+    const bool bf16 = a->cache_dtype == LEAN_BF16;
+    lean_status st = in8 ? prefix_cache8(p, two, a->flags, stream) : prefix_cache16(p, bf16, two, a->flags, stream);
+    if (st != LEAN_OK) return st;
+    st = in8 ? attend_cache8(own, LEAN_FLAG_EARLY_WEIGHTS, stream)
+             : attend_cache16(own, bf16, LEAN_FLAG_EARLY_WEIGHTS, stream);
+    if (st != LEAN_OK) return st;
+    const int64_t grid = (a->n_seqs * a->n_q_heads + 7) / 8;
+    const unsigned blocks = (unsigned)std::min(step_sm_count(), kPrefixMaxCtas);
+    if (p.dim <= 64)
+        return step_launch(two ? prefix_sum_kernel<64, 2> : prefix_sum_kernel<64, 1>, grid, 256, 0, LEAN_FLAG_EARLY_WEIGHTS,
+                           stream, p, blocks);
+    return step_launch(two ? prefix_sum_kernel<128, 2> : prefix_sum_kernel<128, 1>, grid, 256, 0, LEAN_FLAG_EARLY_WEIGHTS,
+                       stream, p, blocks);
+}

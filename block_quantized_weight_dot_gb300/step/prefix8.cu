@@ -1,0 +1,10 @@
+// prefix8.cu -- the kernels of prefix.cuh for caches in 8 bits.
+#include "prefix.cuh"
+
+namespace lean {
+
+lean_status prefix_cache8(const PrefixArgs &p, bool two, int64_t flags, void *stream) {
+    return p.dim <= 64 ? pick_prefix<int8_t, 64>(p, two, flags, stream) : pick_prefix<int8_t, 128>(p, two, flags, stream);
+}
+
+}  // namespace lean

@@ -205,3 +205,113 @@ def run_attend8(lean, lens, hq, hkv, dim, page=16, act="f32", window=0, seed=0, 
     if lse:
         close(ls, want_lse, rel + 4 * U * torch.where(want_lse.isinf(), 0.0, want_lse).abs(), what + " lse")
     return out, ls
+
+
+# ---- shared prefixes ------------------------------------------------------------------------
+
+def prefix_ref(q, kd, vd, prefix_table, prefix_lens, starts, table, lens, scale):
+    """(out, lse, sum p |v|, the largest sum |q k| scale) in 64 bits; kd, vd: the caches' values as float64."""
+    torch = torch_cuda()
+    n, hq, d = q.shape
+    page, hkv = kd.shape[1], kd.shape[2]
+    out, size = (torch.zeros((n, hq, d), dtype=torch.float64, device="cuda") for _ in range(2))
+    lse = torch.full((n, hq), -math.inf, dtype=torch.float64, device="cuda")
+    reach = torch.zeros((n, hq), dtype=torch.float64, device="cuda")
+
+    def rows(tab, length):
+        length = min(max(length, 0), tab.shape[0] * page)
+        t = torch.arange(length, device="cuda")
+        at = tab.long()[t // page], t % page
+        return kd[at], vd[at]
+    for s in range(n):
+        mine = [i for i in range(len(prefix_lens)) if starts[i] <= s < starts[i + 1]]
+        parts = [rows(prefix_table[i], prefix_lens[i]) for i in mine] + [rows(table[s], lens[s])]
+        k, v = torch.cat([x[0] for x in parts]), torch.cat([x[1] for x in parts])
+        if not k.shape[0]:
+            continue
+        x = q[s].double().view(hkv, hq // hkv, d)
+        z = scale * torch.einsum("grd,lgd->grl", x, k)
+        p = torch.softmax(z, -1)
+        lse[s] = torch.logsumexp(z, -1).view(-1)
+        out[s] = torch.einsum("grl,lgd->grd", p, v).reshape(hq, d)
+        size[s] = torch.einsum("grl,lgd->grd", p, v.abs()).reshape(hq, d)
+        reach[s] = abs(scale) * torch.einsum("grd,lgd->grl", x.abs(), k.abs()).amax(-1).view(-1)
+    return out, lse, size, reach
+
+
+def make_prefix(prefix_lens, lens, hq, hkv, dim, page=16, act="f32", cache="bf16", seed=0, heads_first=True, spread=0.5,
+                junk=math.nan, extra=0):
+    """q, caches, scales, both tables; what nobody holds is junk (scales of it in 8 bits), and table entries past the
+    pages that are held far outside the cache."""
+    torch = torch_cuda()
+    g = gen(7500 + seed)
+    every = [max(x, 0) for x in list(prefix_lens) + list(lens)]
+    need = [-(-x // page) for x in every]
+    pool = sum(need) + 3
+    order = torch.randperm(pool, generator=g, device="cuda").tolist()
+    held = torch.zeros((pool, page), dtype=torch.bool)
+    tables = []
+    for part, ls in ((need[:len(prefix_lens)], every[:len(prefix_lens)]), (need[len(prefix_lens):], every[len(prefix_lens):])):
+        tab = torch.full((len(part), max(1, max(part)) + extra), 2 ** 31 - 1, dtype=torch.int32)
+        for s, x in enumerate(ls):
+            for j in range(part[s]):
+                tab[s, j] = order.pop()
+                held[tab[s, j], :min(page, x - j * page)] = True
+        tables.append(tab.cuda())
+    held = held.cuda()
+    if cache == "i8":
+        kc, ks, vc, vs = make_cache8(pool, page, hkv, dim, seed, spread, heads_first)
+        ks[~held], vs[~held] = junk, junk
+    else:
+        ks = vs = None
+        shape = (pool, hkv, page, dim) if heads_first else (pool, page, hkv, dim)
+        kc, vc = (normal(g, *shape, t=cache) for _ in range(2))
+        if heads_first:
+            kc, vc = kc.transpose(1, 2), vc.transpose(1, 2)
+        kc[~held], vc[~held] = junk, junk
+    q = normal(g, len(lens), hq, dim, t=act, std=1.5)
+    return q, kc, ks, vc, vs, tables[0], tables[1]
+
+
+def run_prefix(lean, prefix_lens, starts, lens, hq, hkv, dim, page=16, act="f32", cache="bf16", seed=0, lse=True, pad=0,
+               heads_first=True, flags=0, scale=None, stream=None, inputs=None, workspace=None, spread=0.5, junk=math.nan,
+               extra=0):
+    torch = torch_cuda()
+    inputs = inputs or make_prefix(prefix_lens, lens, hq, hkv, dim, page, act, cache, seed, heads_first, spread, junk, extra)
+    q, kc, ks, vc, vs, shared, table = inputs
+    scale = 1 / math.sqrt(dim) if scale is None else scale
+    if pad:
+        q = strided(q, pad)
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    pl, st, ld = ints(prefix_lens), ints(starts), ints(lens)
+    out = torch.full((len(lens), hq, dim), 7.0, device="cuda", dtype=dtype(act))
+    if pad:
+        out = strided(out, pad)
+    ls = torch.full((len(lens), hq), 7.0, device="cuda") if lse else None
+    ws = workspace
+    if ws is None:  # (what it holds does not matter)
+        size = lean.lean_prefix_attention_workspace_bytes(len(lens), hq, hkv, dim, len(prefix_lens))
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    lean.lean_prefix_attention(q, kc, vc, shared, pl, st, table, ld, out, scale=scale, lse=ls, workspace=ws, flags=flags,
+                               stream=stream, k_scales=ks, v_scales=vs)
+    torch.cuda.synchronize()
+    kd, vd = (c.double() if s is None else c.double() * s.double()[..., None] for c, s in ((kc, ks), (vc, vs)))
+    want, want_lse, size, reach = prefix_ref(q, kd, vd, shared, prefix_lens, starts, table, lens, scale)
+    # a sequence's own part as step_testlib.run_attend: the parts of q and p, and fp32.  The prefix's: sums of scores and
+    # of a tile's products are taken 16 terms at a time, each rounded towards zero (2 U), up to 24 times, and tiles of
+    # 128 keys are added one by one; p in one part of the operands' type errs by half a step.  Joins: a few U.
+    seen = max([1] + [max(x, 0) for x in prefix_lens] + [max(x, 0) for x in lens])
+    one = HALF["bf16"] if cache == "bf16" else HALF["f16"]
+    split = act == "f32" or (act == "f16" and cache == "bf16")
+    rel = (2 * 2.0 ** -16 + 80 * U) * reach + 2.0 ** -16 + (seen / 8 + 200) * U
+    what = "prefix %s %s own %s heads %d/%d dim %d page %d %s/%s" % (prefix_lens[:4], starts[:4], lens[:4], hq, hkv, dim, page, act, cache)
+    top = torch.where(torch.isfinite(vd), vd.abs(), 0.0).max()
+    err = (rel[..., None] + (0.0 if split else one)) * size + 2.0 ** -37 * top
+    close(out, want, err + HALF[act] * (want.abs() + err) + TINY[act], what)
+    if lse:
+        close(ls, want_lse, rel + 4 * U * torch.where(want_lse.isinf(), 0.0, want_lse).abs(), what + " lse")
+    if pad and len(lens) > 1:
+        flat = out.as_strided((len(lens) - 1, out.stride(0)), (out.stride(0), 1))[:, hq * dim:]
+        assert bool(torch.isnan(flat).all()), what + ": a write between the rows"
+    return out, ls

@@ -14,7 +14,7 @@ from test_step_host import P, c_structs as step_structs
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "lean_cache.h")
 I8 = torch.int8
-STRUCTS = {"lean_kv_read_args": "_KV_READ"}
+STRUCTS = {"lean_kv_read_args": "_KV_READ", "lean_prefix_args": "_PREFIX"}
 
 
 @pytest.fixture(scope="module")
@@ -108,6 +108,37 @@ def test_read_refusals(lean):
         ("ALIGN", dict(cache_dtype=1, k_cache=P + 1)), ("ALIGN", dict(out_dtype=0, v_out=P + 2))])
 
 
+def test_prefix_refusals(lean):
+    size = lean.lean_prefix_attention_workspace_bytes(4, 8, 2, 64, 2)
+    good = dict(n_seqs=4, n_q_heads=8, n_kv_heads=2, head_dim=64, cache_dtype=1, q=P, q_stride=512, q_head_stride=64,
+                k_cache=P, v_cache=P, n_pages=4, page_size=16, page_stride=2048, place_stride=128, cache_head_stride=64,
+                n_prefixes=2, prefix_table=P, prefix_width=3, prefix_stride=3, prefix_lens=P, seq_starts=P, block_table=P,
+                table_width=2, table_stride=2, seq_lens=P, out=P, out_stride=512, out_head_stride=64, scale=0.125,
+                workspace=P, workspace_bytes=size)
+    fields, call = cache_structs()["lean_prefix_args"], (lean, "lean_prefix_attention", lean._PREFIX)
+    refused(*call, fields, good, [
+        ("FORMAT", dict(act_dtype=3)), ("FORMAT", dict(cache_dtype=0)), ("FORMAT", dict(flags=2)), ("SHAPE", dict(n_seqs=0)),
+        ("SHAPE", dict(n_q_heads=7)), ("SHAPE", dict(n_kv_heads=0)), ("SHAPE", dict(head_dim=60)), ("SHAPE", dict(head_dim=136)),
+        ("SHAPE", dict(n_prefixes=0)), ("SHAPE", dict(n_prefixes=5)), ("SHAPE", dict(n_pages=0)), ("SHAPE", dict(page_size=0)),
+        ("SHAPE", dict(prefix_width=0)), ("SHAPE", dict(prefix_stride=2)), ("SHAPE", dict(table_stride=1)),
+        ("SHAPE", dict(prefix_width=1 << 28, prefix_stride=1 << 28)), ("SHAPE", dict(table_width=1 << 28, table_stride=1 << 28)),
+        ("SHAPE", dict(q_stride=-8)), ("SHAPE", dict(page_stride=-8)), ("SHAPE", dict(workspace_bytes=size - 1)),
+        ("NULL", dict(q=0)), ("NULL", dict(v_cache=0)), ("NULL", dict(prefix_table=0)), ("NULL", dict(prefix_lens=0)),
+        ("NULL", dict(seq_starts=0)), ("NULL", dict(block_table=0)), ("NULL", dict(seq_lens=0)), ("NULL", dict(out=0)),
+        ("NULL", dict(workspace=0)), ("ALIGN", dict(q_stride=516)), ("ALIGN", dict(q=P + 8)), ("ALIGN", dict(out=P + 8)),
+        ("ALIGN", dict(k_cache=P + 2)), ("ALIGN", dict(place_stride=132)), ("ALIGN", dict(workspace=P + 16)),
+        ("ALIGN", dict(seq_starts=P + 2)), ("ALIGN", dict(lse=P + 1))])
+    refused(*call, fields, dict(good, cache_dtype=3, **SCALES), [
+        ("NULL", dict(k_scales=0)), ("NULL", dict(v_scales=0)), ("SHAPE", dict(head_dim=72)), ("ALIGN", dict(place_stride=136)),
+        ("SHAPE", dict(scale_place_stride=-1)), ("ALIGN", dict(v_scales=P + 2))])
+    for bad in ((0, 8, 2, 64, 1), (4, 7, 2, 64, 1), (4, 8, 2, 144, 1), (4, 8, 2, 64, 0), (4, 8, 2, 64, 5), (4, 8, 2, 20, 1)):
+        assert lean.lean_prefix_attention_workspace_bytes(*bad) == -1
+    # own tokens in more 16-token units than 32 bits count
+    big = dict(good, n_seqs=1 << 16, n_q_heads=8, n_kv_heads=8, table_width=1 << 14, table_stride=1 << 14,
+               workspace_bytes=lean.lean_prefix_attention_workspace_bytes(1 << 16, 8, 8, 64, 2))
+    refused(*call, fields, big, [("SHAPE", {})])
+
+
 # ---- the binding, with stand-ins for tensors and for the library ----------------------------
 
 @pytest.fixture
@@ -138,10 +169,23 @@ def read8():
     return fn, args
 
 
-CALLS = [append8, attention8, read8]
+def prefix():
+    cache = lambda: Tensor((3, 16, 2, 64), BF16)  # noqa: E731
+    return "lean_prefix_attention", dict(q=Tensor((5, 8, 64), F32), k_cache=cache(), v_cache=cache(),
+                                         prefix_table=Tensor((2, 7), I32), prefix_lens=Tensor((2,), I32),
+                                         seq_starts=Tensor((3,), I32), block_table=Tensor((5, 3), I32),
+                                         seq_lens=Tensor((5,), I32), out=Tensor((5, 8, 64), F32), scale=1.0,
+                                         lse=Tensor((5, 8), F32), workspace=Tensor((1 << 26,), torch.uint8))
 
 
-@pytest.mark.parametrize("call", CALLS)
+def prefix8():
+    return in8(prefix)
+
+
+CALLS = [append8, attention8, read8, prefix8]
+
+
+@pytest.mark.parametrize("call", CALLS + [prefix])
 def test_current_gpu_alone(binding, call):
     fn, args = call()
     getattr(binding, fn)(stream=0, **args)
@@ -193,3 +237,14 @@ def test_read_of_one_cache(binding):
         with pytest.raises(ValueError):
             getattr(binding, fn)(stream=0, **dict(args, **bad))
     assert binding._lib.calls == 2
+
+
+def test_prefix_shapes(binding):
+    fn, args = prefix()
+    for bad in (dict(prefix_lens=Tensor((3,), I32)), dict(seq_starts=Tensor((2,), I32)), dict(block_table=Tensor((4, 3), I32)),
+                dict(prefix_table=Tensor((14,), I32)), dict(prefix_table=Tensor((2, 7), torch.int64)), dict(seq_lens=Tensor((4,), I32)),
+                dict(lse=Tensor((8, 5), F32)), dict(out=Tensor((5, 8, 64), BF16)), dict(workspace=Tensor((1 << 26,), I8)),
+                dict(v_cache=Tensor((3, 16, 2, 64), BF16, stride=(4096, 128, 64, 1)))):
+        with pytest.raises(ValueError):
+            getattr(binding, fn)(stream=0, **dict(args, **bad))
+    assert binding._lib.calls == 0

@@ -211,7 +211,7 @@ def test_attend_zero_and_tiny_scales(lean):
 def test_attend_not_finite(lean):
     """A NaN or infinite scale reaches its sequence and kv head and no other."""
     torch = torch_cuda()
-    for which, bad in ((2, math.nan), (4, math.nan), (4, math.inf)):
+    for which, bad in ((2, math.nan), (4, math.nan), (4, math.inf), (2, math.inf), (2, -math.inf)):
         lens = [40, 70, 33]
         inputs = list(make_attend8(lens, 4, 2, 64, 16, "f32"))
         clean, _ = run_attend8(lean, lens, 4, 2, 64, inputs=inputs)
