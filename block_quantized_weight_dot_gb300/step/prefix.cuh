@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.k_full[i], IN8 ? 4 : 132);
             mbar_init(&bars.v_full[i], IN8 ? 4 : 132);
-            mbar_init(&bars.k_empty[i], 1);
-            mbar_init(&bars.v_empty[i], 1);
+            mbar_init(&bars.k_empty[i], NQ);  // (with one tile of rows each tile of keys is one group's)
+            mbar_init(&bars.v_empty[i], NQ);
             mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.p_full[i], 4);
             mbar_init(&bars.o_full[i], 1);
@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
         for (int i = 0; i < 4; ++i) mbar_init(&bars.scales_full[i], 4);
         for (int i = 0; i < 2; ++i) mbar_init(&bars.rows_full[i], 4);
         mbar_init(&bars.q_full, 8);
-        mbar_init(&bars.q_free, 8);
-        mbar_init(&bars.last, 1);
+        mbar_init(&bars.q_free, 10);
+        mbar_init(&bars.last, 4);
         bars.dead = 0;
         bars.start_i = -1;
         fence_mbar_init();
@@ -572,28 +572,32 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
             __syncwarp();
             if (lane == 0) mbar_arrive(full);
         };
+        auto page_of = [&](int tok) {
+            const int64_t e = (int64_t)w.i * p.table_stride + tok / p.page;
+            return tok < w.x.len && LEAN_IN(e, (int64_t)(p.n_prefixes - 1) * p.table_stride + p.width, p.err) ? p.table[e] : 0;
+        };
         while (ok && w.next(p, ROWS)) {
+            int next_id = page_of(w.from * kTileKeys + t);
             for (int kt = w.from; ok && kt < w.to; ++kt, ++n) {
-                const int tok = kt * kTileKeys + t;
-                int64_t off = -1;
-                float sk = 1.f, sv = 0.f;
+                const int tok = kt * kTileKeys + t, id = next_id;
+                if (kt + 1 < w.to) next_id = page_of(tok + kTileKeys);  // under way during this tile
+                int64_t off = -1, at_scale = -1;
                 if (tok < w.x.len) {
-                    const int64_t e = (int64_t)w.i * p.table_stride + tok / p.page;
-                    const int id = LEAN_IN(e, (int64_t)(p.n_prefixes - 1) * p.table_stride + p.width, p.err) ? p.table[e] : 0;
                     const int place = tok % p.page;
                     if (id < 0 || id >= p.n_pages) {
                         off = -2;
-                        sk = CUDART_NAN_F;
                         atomicOr(p.err, kErrSlot);
                     } else {
                         off = (int64_t)id * p.page_stride + (int64_t)place * p.place_stride + (int64_t)w.kvh * p.cache_hs;
                         if (!LEAN_SPAN(off, p.dim, p.cache_extent, p.err)) off = -1;
-                        const int64_t at = (int64_t)id * p.scale_page + (int64_t)place * p.scale_place + (int64_t)w.kvh * p.scale_hs;
-                        if (IN8 && LEAN_IN(at, p.scale_extent, p.err)) {
-                            sk = p.k_scales[at];
-                            sv = p.v_scales[at];
-                        }
+                        at_scale = (int64_t)id * p.scale_page + (int64_t)place * p.scale_place + (int64_t)w.kvh * p.scale_hs;
+                        if (IN8 && !LEAN_IN(at_scale, p.scale_extent, p.err)) at_scale = -1;
                     }
+                }
+                float sk = off == -2 ? CUDART_NAN_F : 1.f, sv = 0.f;
+                if (IN8 && at_scale >= 0) {
+                    sk = p.k_scales[at_scale];
+                    sv = p.v_scales[at_scale];
                 }
                 int64_t *const offs = row_off + (n & 1) * kTileKeys;
                 offs[t] = off;
@@ -633,70 +637,79 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
         for (unsigned j = n > VS ? n - VS : 0; ok && j < n; ++j) ok = warp_wait(bars, &bars.v_empty[j % VS], j / VS & 1, p.err);
     } else {
         regs_down<40>();
-        if (warp == 12 && lane == 0) {
-            // ---- matrix instructions
-            const uint32_t qk_idesc = tile_idesc(BF16, kTileKeys, false), pv_idesc = tile_idesc(BF16, DP, true);
-            const uint32_t q_at = smem_addr(q_tiles), k_at = smem_addr(k_tiles), v_at = smem_addr(v_tiles);
-            const int steps = (p.dim + 15) / 16;
+        if (lane == 0) {
+            // ---- matrix instructions: warps 12 and 13 issue the groups' scores, 14 and 15 their products.  (One thread
+            // needs about 110 cycles for an instruction that runs for 64: one warp for all of them 58 us where four
+            // take XX, 96 sequences on 32768 tokens.)
+            const int g = warp % 2;
             unsigned n = 0;
-            uint32_t q_phase = 0, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
             bool ok = true;
-            auto qk = [&](int g, unsigned j, bool last) {  // scores of group g and the run's tile j
-                ok = ok && phase_wait(bars, &bars.k_full[j % KS], j / KS & 1, p.err);
-                if (!ok) return;
-                smem_to_async();
-                tm_after();
-                const uint32_t d = tmem + g * 128;
+            if (warp < 14) {
+                const uint32_t idesc = tile_idesc(BF16, kTileKeys, false);
+                const uint32_t q_lower = tile_lower(smem_addr(q_tiles + (NQ == 2 ? g * QP * S::kTileBytes : 0)), 16);
+                const uint32_t k_lower = tile_lower(smem_addr(k_tiles), 16);
+                const int steps = (p.dim + 15) / 16;
+                uint32_t q_phase = 0, o_phase = 0;
+                while (ok && w.next(p, ROWS)) {
+                    ok = phase_wait(bars, &bars.q_full, q_phase, p.err);
+                    q_phase ^= 1;
+                    const unsigned tiles = w.to - w.from;
+                    for (unsigned t = NQ == 2 ? 0 : g; ok && t < tiles; t += NQ == 2 ? 1 : 2) {
+                        const unsigned j = n + t;
+                        ok = phase_wait(bars, &bars.k_full[j % KS], j / KS & 1, p.err);
+                        // P lies where the scores go: its products first
+                        if (t >= (NQ == 2 ? 1 : 2)) ok = ok && phase_wait(bars, &bars.o_full[g], o_phase ^ 1, p.err);
+                        if (!ok) break;
+                        o_phase ^= 1;
+                        smem_to_async();
+                        tm_after();
+                        const uint32_t d = tmem + g * 128, b = k_lower + j % KS * (S::kTileBytes >> 4);
 #pragma unroll
-                for (int part = 0; part < QP; ++part)
-                    for (int s = 0; s < steps; ++s) {
-                        const uint32_t in = s / 4 * S::kChunkBytes + s % 4 * 32;
-                        tm_mma_ss(d, tile_desc(q_at + ((NQ == 2 ? g : 0) * QP + part) * S::kTileBytes + in, 16),
-                                  tile_desc(k_at + j % KS * S::kTileBytes + in, 16), qk_idesc, part > 0 || s > 0);
+                        for (int part = 0; part < QP; ++part)
+#pragma unroll
+                            for (int s = 0; s < DP / 16; ++s) {
+                                const uint32_t in = (s / 4 * S::kChunkBytes + s % 4 * 32) >> 4;
+                                if (s < steps) tm_mma_ss(d, q_lower + (part * S::kTileBytes >> 4) + in, b + in, kTileUpper, idesc, part + s > 0);
+                            }
+                        tm_commit(&bars.s_full[g]);
+                        tm_commit(&bars.k_empty[j % KS]);
                     }
-                tm_commit(&bars.s_full[g]);
-                if (last) tm_commit(&bars.k_empty[j % KS]);
-            };
-            auto pv = [&](int g, unsigned j, bool last) {  // its products
-                ok = ok && phase_wait(bars, &bars.p_full[g], p_phase[g], p.err);
-                ok = ok && phase_wait(bars, &bars.v_full[j % VS], j / VS & 1, p.err);
-                if (!ok) return;
-                p_phase[g] ^= 1;
-                smem_to_async();
-                tm_after();
-                const uint32_t a = tmem + g * 128, d = tmem + 256 + g * DP;
-#pragma unroll
-                for (int s = 0; s < kTileKeys / 16; ++s)
-#pragma unroll
-                    for (int part = 0; part < PP; ++part)
-                        tm_mma_ts(d, a + s / 2 * 32 + s % 2 * 8 + 16 * part,
-                                  tile_desc(v_at + j % VS * S::kTileBytes + s * 2048, S::kChunkBytes), pv_idesc, part > 0 || s > 0);
-                tm_commit(&bars.o_full[g]);
-                if (last) tm_commit(&bars.v_empty[j % VS]);
-            };
-            while (ok && w.next(p, ROWS)) {
-                const int tiles = w.to - w.from;
-                ok = phase_wait(bars, &bars.q_full, q_phase, p.err);
-                q_phase ^= 1;
-                if (NQ == 2) {
-                    qk(0, n, false);
-                    qk(1, n, true);
-                } else {
-                    qk(0, n, true);
-                    if (tiles > 1) qk(1, n + 1, true);
+                    if (ok) mbar_arrive(&bars.q_free);  // (this phase of q_full has been seen)
+                    n += tiles;
                 }
-                for (int t = 0; ok && t < tiles; t += NQ == 2 ? 1 : 2)
+            } else {
+                // (with one stage for values, one thread takes both groups' tiles: each sees every phase of the stage)
+                constexpr bool ALL = VS == 1;
+                static_assert(!ALL || NQ == 1, "tiles in turn");
+                const uint32_t idesc = tile_idesc(BF16, DP, true);
+                const uint32_t v_lower = tile_lower(smem_addr(v_tiles), S::kChunkBytes);
+                uint32_t p_phase[2] = {0, 0};
+                while (ok && w.next(p, ROWS) && !(ALL && g == 1)) {
+                    const unsigned tiles = w.to - w.from;
+                    for (unsigned t = NQ == 2 || ALL ? 0 : g; ok && t < tiles; t += NQ == 2 || ALL ? 1 : 2) {
+                        const unsigned j = n + t;
+                        const int of = ALL ? t % 2 : g;  // group
+                        // (P first: then what came before in this stage is done, and a phase is not mistaken for the one
+                        // two before it)
+                        ok = phase_wait(bars, &bars.p_full[of], p_phase[of], p.err);
+                        ok = ok && phase_wait(bars, &bars.v_full[j % VS], j / VS & 1, p.err);
+                        if (!ok) break;
+                        p_phase[of] ^= 1;
+                        smem_to_async();
+                        tm_after();
+                        const uint32_t a = tmem + of * 128, d = tmem + 256 + of * DP;
+                        const uint32_t b = v_lower + j % VS * (S::kTileBytes >> 4);
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const int mine = NQ == 2 ? t : t + g, then = mine + (NQ == 2 ? 1 : 2);
-                        if (mine >= tiles) continue;
-                        pv(g, n + mine, NQ == 1 || g == 1);
-                        // P lies where the next scores go: its products first
-                        ok = ok && phase_wait(bars, &bars.o_full[g], o_phase[g], p.err);
-                        o_phase[g] ^= 1;
-                        if (then < tiles) qk(g, n + then, NQ == 1 || g == 1);
+                        for (int s = 0; s < kTileKeys / 16; ++s)
+#pragma unroll
+                            for (int part = 0; part < PP; ++part)
+                                tm_mma_ts(d, a + s / 2 * 32 + s % 2 * 8 + 16 * part, b + s * (2048 >> 4), kTileUpper, idesc,
+                                          part + s > 0);
+                        tm_commit(&bars.o_full[of]);
+                        tm_commit(&bars.v_empty[j % VS]);
                     }
-                n += tiles;
+                    n += tiles;
+                }
             }
             tm_commit(&bars.last);
             const uint64_t t0 = globaltimer_ns();

@@ -58,20 +58,23 @@ __device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D (+)= A B^T, both in shared memory
-__device__ __forceinline__ void tm_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// D (+)= A B^T, both in shared memory, their descriptors in halves (a thread issues one of these every 50 to 100 cycles,
+// and what it computes between them counts: an operand's place is one addition to the lower half)
+__device__ __forceinline__ void tm_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t upper, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(upper), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 // the same with A in tensor memory
-__device__ __forceinline__ void tm_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tm_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t upper, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(upper), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 // arrive on `bar` when every matrix instruction that this thread has issued is done
@@ -84,10 +87,8 @@ __device__ __forceinline__ void tm_commit(uint64_t *bar) {
 // bytes, version 1 in bits 46-47, 128-byte swizzle (2) in bits 61-63.  K-major: groups of 8 rows are 1024 bytes apart
 // and a step of 16 along the contraction is 32 bytes further on (the other stride is not used).  MN-major: groups of 8
 // rows along the contraction are 1024 bytes apart, chunks of 64 along the other dimension `chunk` bytes.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t at, uint32_t chunk) {
-    return (uint64_t)((at >> 4) & 0x3FFFu) | ((uint64_t)(chunk >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
-           (2ull << 61);
-}
+__device__ __forceinline__ uint32_t tile_lower(uint32_t at, uint32_t chunk) { return (at >> 4 & 0x3FFFu) | chunk >> 4 << 16; }
+constexpr uint32_t kTileUpper = 1024 >> 4 | 1u << 14 | 2u << 29;
 // Instruction descriptor of kind::f16: fp32 results, bf16 (1) or f16 (0) operands, 128 rows of A by n of B; b_rows: B is
 // MN-major.
 __device__ __forceinline__ uint32_t tile_idesc(bool bf16, int n, bool b_rows) {
