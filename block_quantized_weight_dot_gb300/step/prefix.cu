@@ -2,13 +2,63 @@
 // caches of 16 bits.
 #include "prefix.cuh"
 
+namespace {
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+
+// The caches as tensors in boxes of as many places as a tile and every page are whole numbers of; box 0 where there are
+// none of 8 or more (rows of a box lie in groups of 8), or a stride is 0 between rows that are not one.
+PrefixMaps make_maps(const PrefixArgs &p, bool bf16) {
+    PrefixMaps m = {};
+    int box = kTileKeys;
+    while (p.page % box) box /= 2;
+    const EncodeTiled encode = encode_tiled();
+    if (box < 8 || !encode || (p.page > 1 && p.place_stride == 0) || (p.hkv > 1 && p.cache_hs == 0) ||
+        (p.n_pages > 1 && p.page_stride == 0))
+        return m;
+    const int64_t strides[3] = {p.place_stride, p.cache_hs, p.page_stride};
+    cuuint64_t bytes[3];
+    for (int i = 0; i < 3; ++i) {
+        if (strides[i] >= (int64_t)1 << 38) return m;
+        bytes[i] = strides[i] ? 2 * strides[i] : 16;
+    }
+    const cuuint64_t dims[4] = {(cuuint64_t)p.dim, (cuuint64_t)p.page, (cuuint64_t)p.hkv, (cuuint64_t)p.n_pages};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const void *from[2] = {p.k, p.v};
+    CUtensorMap *to[2] = {&m.k, &m.v};
+    for (int i = 0; i < 2; ++i)
+        if (encode(to[i], type, 4, const_cast<void *>(from[i]), dims, bytes, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return m;
+    m.box = box;
+    return m;
+}
+
+}  // namespace
+
 namespace lean {
 
 lean_status prefix_cache16(const PrefixArgs &p, bool bf16, bool two, int64_t flags, void *stream) {
+    const PrefixMaps maps = make_maps(p, bf16);
     if (bf16)
-        return p.dim <= 64 ? pick_prefix<__nv_bfloat16, 64>(p, two, flags, stream)
-                           : pick_prefix<__nv_bfloat16, 128>(p, two, flags, stream);
-    return p.dim <= 64 ? pick_prefix<__half, 64>(p, two, flags, stream) : pick_prefix<__half, 128>(p, two, flags, stream);
+        return p.dim <= 64 ? pick_prefix<__nv_bfloat16, 64>(maps, p, two, flags, stream)
+                           : pick_prefix<__nv_bfloat16, 128>(maps, p, two, flags, stream);
+    return p.dim <= 64 ? pick_prefix<__half, 64>(maps, p, two, flags, stream)
+                       : pick_prefix<__half, 128>(maps, p, two, flags, stream);
 }
 
 }  // namespace lean

@@ -36,6 +36,8 @@
 //     multiplied by the keys' scales, p by the values', relative to the tile's
 //     largest.
 #pragma once
+#include <cuda.h>
+
 #include <type_traits>
 
 #include "../../include/lean_cache.h"
@@ -44,11 +46,14 @@
 
 namespace lean {
 
-constexpr int kTileRows = 128, kTileKeys = 128;
+constexpr int kTileRows = 128, kTileKeys = 128, kHalfKeys = 64;
 constexpr int kPrefixMaxCtas = 160;
 constexpr int kPrefixThreads = 512;
 // Tiles of a block's time that an item costs beside its own (q, the first scores, the last outputs).
 constexpr int kItemTiles = 2;
+// Halves of tiles whose products are summed in tensor memory before they are added in fp32 (one part of p): what is below
+// 2^-24 of a sum is cut off when it is added, 16 keys at a time, so that a row errs by 2^-16 of its largest sum at most.
+constexpr int kFoldHalves = 32;
 
 struct PrefixArgs {
     const void *q, *k, *v;
@@ -70,6 +75,13 @@ struct PrefixArgs {
     int64_t os, ohs;
     int64_t cache_extent, scale_extent, q_extent, out_extent;  // elements, for the checked build
     unsigned *err;
+};
+
+// Keys and values of caches of 16 bits as tensors [page][head][place][dim] for the copy engine, in boxes of `box` places by
+// 64 dimensions (box 0: pages whose size no multiple of 8 divides, or strides that it does not take).
+struct PrefixMaps {
+    CUtensorMap k, v;
+    int box;
 };
 
 lean_status prefix_cache16(const PrefixArgs &p, bool bf16, bool two, int64_t flags, void *stream);
@@ -170,13 +182,20 @@ struct PrefixShape {
     static constexpr int kBars = kScaleAt + (kIn8 ? 4 * 2 * kTileKeys * 4 : 0);
     static constexpr int kSmem = kBars + 512;
     static constexpr int kSmemAsked = kSmem + 1008;  // (the tiles begin on 1024 bytes)
+    // Tensor memory, 512 columns: for each group of rows its outputs, in what is left buffers for the scores of 64 keys,
+    // which become p: part 0 (and 1) of 32 keys in the first 16 (and next 16) of their own 32 columns, a third beyond them.
+    static constexpr int kWidth = PP == 3 ? 96 : 64, kBuffers = (256 - DP) / kWidth;
+    static_assert(kBuffers >= 1 && kBuffers <= 3, "tensor memory");
+    __device__ static __forceinline__ uint32_t scores(int g, unsigned b) { return (g * kBuffers + b) * kWidth; }
+    __device__ static __forceinline__ uint32_t outputs(int g) { return 512 - 2 * DP + g * DP; }
+    __device__ static __forceinline__ uint32_t part(int chunk, int k) { return k < 2 ? 32 * chunk + 16 * k : 64 + 16 * chunk; }
 };
 
 struct PrefixBars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // a stage's tile is there, was used
-    uint64_t s_full[2], p_full[2], o_full[2];               // a group's scores, probabilities, products
+    uint64_t s_full[2][3], p_full[2][3], o_full[2][3];      // of a group's buffers: scores, p, products are done
     uint64_t q_full, q_free;                                // q is there; both groups are done with it
-    uint64_t rows_full[2];                                  // the rows' places of a tile of keys are there
+    uint64_t rows_full[2], tops_full[2];                    // a tile's rows' places, the warps' largest scales are there
     uint64_t scales_full[4];
     uint64_t last;                                          // every matrix instruction is done
     uint32_t tmem;
@@ -188,8 +207,17 @@ struct PrefixBars {
 };
 static_assert(sizeof(PrefixBars) <= 512, "room for the barriers");
 
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+// A box of a tensor map into shared memory; its bytes are counted on `bar`.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int place, int head, int page, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2,%3,%4,%5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(place), "r"(head), "r"(page), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void store8(float *to, const float *f) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]),
+                 "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                 : "memory");
 }
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -229,11 +257,11 @@ __device__ __forceinline__ bool row_of(const PrefixArgs &p, const Walk &w, int64
 }
 
 template <typename C, int DP, int QP, int PP, int NQ>
-__global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixArgs p) {
+__global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_constant__ PrefixMaps maps, const PrefixArgs p) {
     using S = PrefixShape<C, DP, QP, PP, NQ>;
     using T = typename Operand<C>::type;
     constexpr bool IN8 = S::kIn8, BF16 = std::is_same<T, __nv_bfloat16>::value;
-    constexpr int KS = S::kKStages, VS = S::kVStages, ROWS = NQ * kTileRows;
+    constexpr int KS = S::kKStages, VS = S::kVStages, NB = S::kBuffers, ROWS = NQ * kTileRows;
     extern __shared__ uint8_t raw_smem[];
     uint8_t *smem = raw_smem + (1024 - smem_addr(raw_smem) % 1024) % 1024;
     uint8_t *const q_tiles = smem, *const k_tiles = smem + S::kQ, *const v_tiles = k_tiles + KS * S::kTileBytes;
@@ -258,16 +286,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
     if (lane == 31) before[warp] = incl;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.k_full[i], IN8 ? 4 : 132);
-            mbar_init(&bars.v_full[i], IN8 ? 4 : 132);
+            mbar_init(&bars.k_full[i], 4);
+            mbar_init(&bars.v_full[i], 4);
             mbar_init(&bars.k_empty[i], NQ);  // (with one tile of rows each tile of keys is one group's)
             mbar_init(&bars.v_empty[i], NQ);
-            mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], 4);
-            mbar_init(&bars.o_full[i], 1);
+            for (int b = 0; b < 3; ++b) {
+                mbar_init(&bars.s_full[i][b], 1);
+                mbar_init(&bars.p_full[i][b], 4);
+                mbar_init(&bars.o_full[i][b], 1);
+            }
         }
         for (int i = 0; i < 4; ++i) mbar_init(&bars.scales_full[i], 4);
-        for (int i = 0; i < 2; ++i) mbar_init(&bars.rows_full[i], 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.rows_full[i], 4);
+            mbar_init(&bars.tops_full[i], 4);
+        }
         mbar_init(&bars.q_full, 8);
         mbar_init(&bars.q_free, 10);
         mbar_init(&bars.last, 4);
@@ -317,21 +350,28 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
 
     if (warp < 8) {
         // ---- scores to probabilities, products to outputs: a thread has a row
-        regs_up<192>();
+        regs_up<PP == 1 ? 168 : 192>();
         const int g = warp / 4, r = threadIdx.x % kTileRows;
         const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // this warp's 32 lanes of tensor memory
-        const uint32_t s_at = tmem + lanes + g * 128, o_at = tmem + lanes + 256 + g * DP;
-        uint32_t s_phase = 0, o_phase = 0;
+        const uint32_t s_group = tmem + lanes + S::scores(g, 0), o_at = tmem + lanes + S::outputs(g);
+        unsigned done = 0;          // half tiles of this group so far: buffer done % NB, whose phase is done / NB
         unsigned tiles_before = 0;  // of the run, by loader's count (scales)
         bool ok = true;
         uint32_t q_phase = 1;  // (the phase before the first counts as done)
         while (ok && w.next(p, ROWS)) {
+            // where this row's part goes (-1: the item has no such row)
+            int seq, head;
+            const bool real = row_of(p, w, (int64_t)w.tile * ROWS + (NQ == 2 ? g * kTileRows : 0) + r, seq, head);
+            int64_t part_at = -1;
+            if (real) {
+                const int64_t first = (int64_t)seq * p.hq + head;
+                part_at = w.from == 0 ? (NQ == 2 ? first : 2 * first + g)
+                                      : (NQ == 2 ? 1 : 2) * (int64_t)p.n_seqs * p.hq + (int64_t)blockIdx.x * 256 + g * kTileRows + r;
+                if (!LEAN_IN(part_at, p.parts, p.err)) part_at = -1;
+            }
             // q of this row, scaled by a power of two, in parts
-            f32x2 acc[DP / 2];
             float zs;
             {
-                int seq, head;
-                const bool real = row_of(p, w, (int64_t)w.tile * ROWS + (NQ == 2 ? g * kTileRows : 0) + r, seq, head);
                 float f[DP];
                 const int64_t at = real ? (int64_t)seq * p.qs + (int64_t)head * p.qhs : 0;
                 float top = 0.f;
@@ -395,58 +435,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.q_full);
             }
-#pragma unroll
-            for (int i = 0; i < DP / 2; ++i) acc[i] = 0;
+            constexpr float kLog2Lift = PartRange<T>::kLift == 1.f ? 0.f : 13.f, kDown = 1.f / PartRange<T>::kLift;
             float m = -CUDART_INF_F, l = 0.f;
             int v_ref = 1;
-            for (int t = w.from + (NQ == 2 ? 0 : g); t < w.to; t += NQ == 2 ? 1 : 2) {
-                const int limit = w.x.len - t * kTileKeys;  // keys from there on are not there
-                const unsigned slot = (tiles_before + (t - w.from)) % 4;
-                const float *ks = scales + slot * 2 * kTileKeys, *vs = ks + kTileKeys;
-                if (IN8) ok = ok && warp_wait(bars, &bars.scales_full[slot], (tiles_before + (t - w.from)) / 4 & 1, p.err);
-                ok = ok && warp_wait(bars, &bars.s_full[g], s_phase, p.err);
-                if (!ok) break;
-                s_phase ^= 1;
-                tm_after();
-                if (limit < kTileKeys) {  // keys that are not there score -inf
-#pragma unroll 1
-                    for (int c = limit / 32 * 32; c < kTileKeys; c += 32) {
-                        uint32_t x[32];
-                        tm_ld32(s_at + c, x);
-                        tm_wait_ld(x);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t y[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) y[i] = c + 16 * h + i < limit ? x[16 * h + i] : 0xff800000u;
-                            tm_st16(s_at + c + 16 * h, y);
-                        }
-                    }
-                    tm_wait_st();
-                }
-                // largest score
-                float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-                for (int c = 0; c < kTileKeys; c += 32) {
-                    uint32_t x[32];
-                    tm_ld32(s_at + c, x);
-                    tm_wait_ld(x);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float z = __uint_as_float(x[i]);
-                        if (IN8) z *= ks[c + i];
-                        tops[i % 4] = fmaxf(tops[i % 4], z);
-                    }
-                }
-                float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                top *= zs;
+            // What a tile's largest score and scales make of the references: m, v_ref; what is multiplied with the sums
+            // and the outputs so far, added to the exponents, and multiplied with the sum of p.
+            float fall, o_fall, shift, back;
+            auto refer = [&](float top, unsigned slot) {
                 // (m as in attend.cuh: within kSlack of the largest score so far)
                 const float mn = top - m <= PartRange<T>::kSlack ? m : top;
                 const float ms = mn == -CUDART_INF_F ? 0.f : mn;
-                const float fall = ex2(m - ms);
-                float o_fall = fall;
+                fall = o_fall = ex2(m - ms);
+                bool moved = !(mn == m);
                 m = mn;
-                float shift = (PartRange<T>::kLift == 1.f ? 0.f : 13.f) - ms, back = 1.f;
+                shift = kLog2Lift - ms;
+                back = 1.f;
                 if (IN8) {
                     // values' scales lie in 0.5..1 times 2^(exponent of the tile's largest - 126); sums are relative to
                     // 2^(v_ref - 126); what is below 2^-60 of the largest may count as 2^-60 of it
@@ -454,94 +457,291 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
                     o_fall *= __uint_as_float((uint32_t)max(0, 127 + v_ref - now) << 23);
                     shift -= (float)below;
                     back = __uint_as_float((uint32_t)(127 + below) << 23);
+                    moved = moved || now != v_ref;
                     v_ref = now;
                 }
-                const f32x2 zs2 = pack2(zs, zs), shift2 = pack2(shift, shift);
-                f32x2 sum2[2] = {0, 0};
-#pragma unroll
-                for (int c = 0; c < kTileKeys; c += 32) {
-                    uint32_t x[32];
-                    tm_ld32(s_at + c, x);
-                    tm_wait_ld(x);
-                    uint32_t part[PP][16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        f32x2 z = pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                        if (IN8) z = mul2(z, *reinterpret_cast<const f32x2 *>(ks + c + i));
-                        const float2 a = unpack2(fma2(z, zs2, shift2));
-                        float2 e = make_float2(ex2(a.x), ex2(a.y));
-                        sum2[i / 2 % 2] = add2(sum2[i / 2 % 2], pack2(e.x, e.y));
-                        if (IN8) e = unpack2(mul2(pack2(e.x, e.y), *reinterpret_cast<const f32x2 *>(vs + c + i)));
-#pragma unroll
-                        for (int k = 0; k < PP; ++k) part[k][i / 2] = take_part<T>(e.x, e.y);
-                    }
-#pragma unroll
-                    for (int k = 0; k < PP; ++k) tm_st16(s_at + c + 16 * k, part[k]);  // over scores already used
-                }
+                return moved;
+            };
+            auto size = [&]() { return IN8 ? kDown * __uint_as_float((uint32_t)(v_ref + 1) << 23) : kDown; };
+            // Halves of tiles in turn (of the last one the second may have no keys; keys that are not there score -inf).
+            int t = w.from + (NQ == 2 ? 0 : g), half = 0, limit = 0;  // limit: keys of the half that are there, or more
+            unsigned n = 0, slot = 0;
+            uint32_t s_at = 0;
+            const float *ks = nullptr, *vs = nullptr;
+            auto scores_wait = [&]() {
+                limit = w.x.len - t * kTileKeys - half * kHalfKeys;
+                n = tiles_before + (t - w.from);
+                slot = n % 4;
+                ks = scales + slot * 2 * kTileKeys + half * kHalfKeys;
+                vs = ks + kTileKeys;
+                s_at = s_group + done % NB * S::kWidth;
+                bool got = true;
+                if (IN8 && half == 0) got = warp_wait(bars, &bars.scales_full[slot], n / 4 & 1, p.err);
+                got = got && warp_wait(bars, &bars.s_full[g][done % NB], done / NB & 1, p.err);
+                tm_after();
+                return got;
+            };
+            auto publish = [&]() {
                 tm_wait_st();
                 tm_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[g]);
-                const float2 sum = unpack2(add2(sum2[0], sum2[1]));
-                l = fmaf(l, fall, (sum.x + sum.y) * back);
-                // outputs
-                ok = warp_wait(bars, &bars.o_full[g], o_phase, p.err);
-                if (!ok) break;
-                o_phase ^= 1;
+                if (lane == 0) mbar_arrive(&bars.p_full[g][done % NB]);
+                ++done;
+            };
+            auto products_wait = [&]() {  // of all that were published
+                const bool got = warp_wait(bars, &bars.o_full[g][(done - 1) % NB], (done - 1) / NB & 1, p.err);
                 tm_after();
-                const f32x2 fall2 = pack2(o_fall, o_fall);
-#pragma unroll
-                for (int c = 0; c < DP; c += 32) {
-                    uint32_t x[32];
-                    tm_ld32(o_at + c, x);
-                    tm_wait_ld(x);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        acc[(c + i) / 2] = fma2(acc[(c + i) / 2], fall2, pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+                return got;
+            };
+            auto advance_half = [&]() {
+                if (half == 0 && limit > kHalfKeys) {
+                    half = 1;
+                } else {
+                    half = 0;
+                    t += NQ == 2 ? 1 : 2;
                 }
-                tm_before();
-            }
-            tiles_before += w.to - w.from;
-            if (!ok) break;
-            if (lane == 0) mbar_arrive(&bars.q_free);  // (its last products are done)
-            // the part of this row
-            int seq, head;
-            const int64_t row = (int64_t)w.tile * ROWS + (NQ == 2 ? g * kTileRows : 0) + r;
-            if (row_of(p, w, row, seq, head)) {
-                const int64_t first = (int64_t)seq * p.hq + head;
-                const int64_t at = w.from == 0 ? (NQ == 2 ? first : 2 * first + g)
-                                               : (NQ == 2 ? 1 : 2) * (int64_t)p.n_seqs * p.hq + (int64_t)blockIdx.x * 256 +
-                                                     g * kTileRows + r;
-                const float lift = 1.f / PartRange<T>::kLift;
-                const float size = IN8 ? lift * __uint_as_float((uint32_t)(v_ref + 1) << 23) : lift;
-                if (LEAN_IN(at, p.parts, p.err)) {
-                    p.ml[at] = make_float2(m, l * lift);
-                    float *o = p.o + at * DP;
+            };
+            if constexpr (PP == 1) {
+                // outputs stay in tensor memory for kFoldHalves halves, then go to the row's part in the workspace
+                int in_sum = 0;       // halves whose products lie there
+                bool folded = false;  // the part has some already, with reference m_part
+                float m_part = -CUDART_INF_F;
+                while (t < w.to) {
+                    ok = scores_wait();
+                    if (!ok) break;
+                    uint32_t x[2][32];
 #pragma unroll
-                    for (int d = 0; d < DP; d += 4) {
-                        const float2 a = unpack2(acc[d / 2]), b = unpack2(acc[d / 2 + 1]);
-                        *reinterpret_cast<float4 *>(o + d) = make_float4(a.x * size, a.y * size, b.x * size, b.y * size);
+                    for (int c = 0; c < 2; ++c) tm_ld32(s_at + 32 * c, x[c]);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) tm_wait_ld(x[c]);
+                    if (IN8) {
+#pragma unroll
+                        for (int i = 0; i < kHalfKeys; i += 2) {
+                            const float2 z = unpack2(mul2(pack2(__uint_as_float(x[i / 32][i % 32]), __uint_as_float(x[i / 32][i % 32 + 1])),
+                                                          *reinterpret_cast<const f32x2 *>(ks + i)));
+                            x[i / 32][i % 32] = __float_as_uint(z.x);
+                            x[i / 32][i % 32 + 1] = __float_as_uint(z.y);
+                        }
+                    }
+                    if (limit < kHalfKeys) {
+#pragma unroll
+                        for (int i = 0; i < kHalfKeys; ++i)
+                            if (i >= limit) x[i / 32][i % 32] = 0xff800000u;
+                    }
+                    float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                    for (int i = 0; i < kHalfKeys; ++i) tops[i % 4] = fmaxf(tops[i % 4], __uint_as_float(x[i / 32][i % 32]));
+                    const bool moved = refer(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * zs, slot);
+                    const f32x2 zs2 = pack2(zs, zs), shift2 = pack2(shift, shift);
+                    f32x2 sum2[2] = {0, 0};
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t part[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 a = unpack2(fma2(pack2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), zs2, shift2));
+                            float2 e = make_float2(ex2(a.x), ex2(a.y));
+                            sum2[i / 2 % 2] = add2(sum2[i / 2 % 2], pack2(e.x, e.y));
+                            if (IN8) e = unpack2(mul2(pack2(e.x, e.y), *reinterpret_cast<const f32x2 *>(vs + 32 * c + i)));
+                            part[i / 2] = take_part<T>(e.x, e.y);
+                        }
+                        tm_st16(s_at + S::part(c, 0), part);  // (over the scores, which are in registers)
+                    }
+                    if (__any_sync(0xffffffffu, moved) && in_sum > 0) {  // new references: what is there is rescaled
+                        ok = products_wait();
+                        if (!ok) break;
+#pragma unroll
+                        for (int c = 0; c < DP; c += 32) {
+                            uint32_t y[32];
+                            tm_ld32(o_at + c, y);
+                            tm_wait_ld(y);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t z[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) z[i] = __float_as_uint(__uint_as_float(y[16 * h + i]) * o_fall);
+                                tm_st16(o_at + c + 16 * h, z);
+                            }
+                        }
+                    }
+                    publish();
+                    const float2 sum = unpack2(add2(sum2[0], sum2[1]));
+                    l = fmaf(l, fall, (sum.x + sum.y) * back);
+                    advance_half();
+                    if (++in_sum == kFoldHalves || t >= w.to) {
+                        ok = products_wait();
+                        if (!ok) break;
+                        const float f = ex2(m_part - (m == -CUDART_INF_F ? 0.f : m)), up = size();
+                        float *o = p.o + part_at * DP;
+#pragma unroll
+                        for (int c = 0; c < DP; c += 32) {
+                            uint32_t y[32];
+                            tm_ld32(o_at + c, y);
+                            tm_wait_ld(y);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8) {
+                                if (part_at < 0) break;
+                                float z[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) z[k] = __uint_as_float(y[i + k]) * up;
+                                if (folded) {
+                                    const Vec<float, 4> a = load_vec<float, 4>(o + c + i), b = load_vec<float, 4>(o + c + i + 4);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        z[k] = fmaf(a.v[k], f, z[k]);
+                                        z[4 + k] = fmaf(b.v[k], f, z[4 + k]);
+                                    }
+                                }
+                                store8(o + c + i, z);
+                            }
+                            __syncwarp();
+                        }
+                        tm_before();
+                        folded = true;
+                        m_part = m;
+                        in_sum = 0;
+                    }
+                }
+                tiles_before += w.to - w.from;
+                if (!ok) break;
+            } else {
+                f32x2 acc[DP / 2];
+#pragma unroll
+                for (int i = 0; i < DP / 2; ++i) acc[i] = 0;
+                while (t < w.to) {
+                    ok = scores_wait();
+                    if (!ok) break;
+                    if (limit < kHalfKeys) {
+#pragma unroll 1
+                        for (int c = limit / 32 * 32; c < kHalfKeys; c += 32) {
+                            uint32_t x[32];
+                            tm_ld32(s_at + c, x);
+                            tm_wait_ld(x);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t y[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) y[i] = c + 16 * h + i < limit ? x[16 * h + i] : 0xff800000u;
+                                tm_st16(s_at + c + 16 * h, y);
+                            }
+                        }
+                        tm_wait_st();
+                    }
+                    float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                    for (int c = 0; c < kHalfKeys; c += 32) {
+                        uint32_t x[32];
+                        tm_ld32(s_at + c, x);
+                        tm_wait_ld(x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            float z = __uint_as_float(x[i]);
+                            if (IN8) z *= ks[c + i];
+                            tops[i % 4] = fmaxf(tops[i % 4], z);
+                        }
+                    }
+                    refer(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * zs, slot);
+                    const f32x2 zs2 = pack2(zs, zs), shift2 = pack2(shift, shift);
+                    f32x2 sum2[2] = {0, 0};
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t x[32];
+                        tm_ld32(s_at + 32 * c, x);
+                        tm_wait_ld(x);
+                        uint32_t part[PP][16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            f32x2 z = pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                            if (IN8) z = mul2(z, *reinterpret_cast<const f32x2 *>(ks + 32 * c + i));
+                            const float2 a = unpack2(fma2(z, zs2, shift2));
+                            float2 e = make_float2(ex2(a.x), ex2(a.y));
+                            sum2[i / 2 % 2] = add2(sum2[i / 2 % 2], pack2(e.x, e.y));
+                            if (IN8) e = unpack2(mul2(pack2(e.x, e.y), *reinterpret_cast<const f32x2 *>(vs + 32 * c + i)));
+#pragma unroll
+                            for (int k = 0; k < PP; ++k) part[k][i / 2] = take_part<T>(e.x, e.y);
+                        }
+#pragma unroll
+                        for (int k = 0; k < PP; ++k) tm_st16(s_at + S::part(c, k), part[k]);  // over scores already used
+                    }
+                    publish();
+                    const float2 sum = unpack2(add2(sum2[0], sum2[1]));
+                    l = fmaf(l, fall, (sum.x + sum.y) * back);
+                    ok = products_wait();
+                    if (!ok) break;
+                    const f32x2 fall2 = pack2(o_fall, o_fall);
+#pragma unroll
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t x[32];
+                        tm_ld32(o_at + c, x);
+                        tm_wait_ld(x);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            acc[(c + i) / 2] = fma2(acc[(c + i) / 2], fall2, pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+                    }
+                    tm_before();
+                    advance_half();
+                }
+                tiles_before += w.to - w.from;
+                if (!ok) break;
+                if (part_at >= 0) {
+                    const float up = size();
+#pragma unroll
+                    for (int d = 0; d < DP; d += 8) {
+                        float z[8];
+#pragma unroll
+                        for (int k = 0; k < 8; k += 2) {
+                            const float2 a = unpack2(acc[(d + k) / 2]);
+                            z[k] = a.x * up;
+                            z[k + 1] = a.y * up;
+                        }
+                        store8(p.o + part_at * DP + d, z);
                     }
                 }
             }
+            if (lane == 0) mbar_arrive(&bars.q_free);  // (its last products are done)
+            if (part_at >= 0) p.ml[part_at] = make_float2(m, l * kDown);
         }
     } else if (warp < 12) {
-        // ---- keys and values into shared memory: a thread looks up a key's row, then copies pieces of all rows
-        regs_down<88>();
+        // ---- keys and values into shared memory
+        regs_down<PP == 1 ? 112 : IN8 ? 88 : 72>();
         const int t = threadIdx.x - 256;
-        constexpr int PR = IN8 ? DP / 16 : DP / 8;  // 16-byte pieces of a row in the cache
         unsigned n = 0;
         bool ok = true;
-        auto copy = [&](const C *cache, const int64_t *off, uint8_t *tile, bool is_k) {
-            if constexpr (IN8) {
-                uint4 x[PR];
+        auto page_of = [&](int tok) {
+            const int64_t e = (int64_t)w.i * p.table_stride + tok / p.page;
+            return tok < w.x.len && LEAN_IN(e, (int64_t)(p.n_prefixes - 1) * p.table_stride + p.width, p.err) ? p.table[e] : 0;
+        };
+        // place of token `tok`, in page `id`, in the caches; -1: past the prefix, -2: no page of the cache
+        auto place_of = [&](int tok, int id) -> int64_t {
+            if (tok >= w.x.len) return -1;
+            if (id < 0 || id >= p.n_pages) {
+                atomicOr(p.err, kErrSlot);
+                return -2;
+            }
+            const int64_t off = (int64_t)id * p.page_stride + (int64_t)(tok % p.page) * p.place_stride + (int64_t)w.kvh * p.cache_hs;
+            return LEAN_SPAN(off, p.dim, p.cache_extent, p.err) ? off : -1;
+        };
+        auto arrive = [&](uint64_t *bar) {  // of four warps, what each of whose lanes has written
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        if constexpr (IN8) {
+            // A thread looks up a key's row and scales, then takes 16-byte pieces of all rows through registers, where
+            // they become f16: the pieces of the next tile are under way while this one's are converted.
+            constexpr int PR = DP / 16;  // pieces of a row
+            uint4 xk[PR], xv[PR];
+            float sk = 1.f, sv = 0.f;
+            auto load = [&](const void *cache, unsigned tile, uint4 (&x)[PR]) {
+                const int64_t *off = row_off + (tile & 1) * kTileKeys;
 #pragma unroll
                 for (int i = 0; i < PR; ++i) {
-                    const int row = (i * kTileKeys + t) / PR, c = t % PR;
-                    const int64_t o = off[row];
+                    const int c = t % PR;
+                    const int64_t o = off[(i * kTileKeys + t) / PR];
                     x[i] = make_uint4(0, 0, 0, 0);
-                    if (o >= 0 && 16 * c < p.dim) x[i] = *reinterpret_cast<const uint4 *>(cache + o + 16 * c);
+                    if (o >= 0 && 16 * c < p.dim) x[i] = *reinterpret_cast<const uint4 *>(static_cast<const int8_t *>(cache) + o + 16 * c);
                 }
+            };
+            auto convert = [&](uint8_t *tile, const uint4 (&x)[PR]) {
 #pragma unroll
                 for (int i = 0; i < PR; ++i) {
                     const int row = (i * kTileKeys + t) / PR, c = t % PR;
@@ -553,7 +753,82 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
                         make_uint4(codes_f16<0x4140>(u[2]), codes_f16<0x4342>(u[2]), codes_f16<0x4140>(u[3]), codes_f16<0x4342>(u[3]));
                 }
                 smem_to_async();
-            } else {
+            };
+            // the rows of tile number m of the run, at kt of its prefix, whose pages are known; scales under way
+            auto rows = [&](unsigned m, int kt, int id) {
+                const int tok = kt * kTileKeys + t;
+                const int64_t off = place_of(tok, id);
+                row_off[(m & 1) * kTileKeys + t] = off;
+                sk = off == -2 ? CUDART_NAN_F : 1.f;
+                sv = 0.f;
+                if (off >= 0) {
+                    const int64_t at = (int64_t)id * p.scale_page + (int64_t)(tok % p.page) * p.scale_place + (int64_t)w.kvh * p.scale_hs;
+                    if (LEAN_IN(at, p.scale_extent, p.err)) {
+                        sk = p.k_scales[at];
+                        sv = p.v_scales[at];
+                    }
+                }
+                arrive(&bars.rows_full[m & 1]);
+            };
+            auto wait_rows = [&](unsigned m) { return warp_wait(bars, &bars.rows_full[m & 1], m / 2 & 1, p.err); };
+            auto finish_scales = [&](unsigned m) {  // relative to the tile's largest
+                float top = fmaxf(sv, 0.f);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                if (lane == 0) bars.warp_top[m & 1][warp - 8] = top;
+                arrive(&bars.tops_full[m & 1]);
+                if (!warp_wait(bars, &bars.tops_full[m & 1], m / 2 & 1, p.err)) return false;
+                const float *tops = bars.warp_top[m & 1];
+                top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                const int e = min(252, max(1, (int)(__float_as_uint(top) >> 23)));
+                float *to = scales + m % 4 * 2 * kTileKeys + t;
+                to[0] = sk + (sk - sk);  // (an infinite one is NaN, as the scores of such a key are)
+                to[kTileKeys] = sv * __uint_as_float((uint32_t)(253 - e) << 23);
+                if (t == 0) bars.tile_exp[m % 4] = e;
+                arrive(&bars.scales_full[m % 4]);
+                return true;
+            };
+            while (ok && w.next(p, ROWS)) {
+                rows(n, w.from, page_of(w.from * kTileKeys + t));
+                int next_id = w.from + 1 < w.to ? page_of((w.from + 1) * kTileKeys + t) : 0;
+                ok = wait_rows(n);
+                if (!ok) break;
+                load(p.k, n, xk);
+                load(p.v, n, xv);
+                ok = finish_scales(n);
+                for (int kt = w.from; ok && kt < w.to; ++kt, ++n) {
+                    const bool more = kt + 1 < w.to;
+                    if (more) {
+                        rows(n + 1, kt + 1, next_id);
+                        if (kt + 2 < w.to) next_id = page_of((kt + 2) * kTileKeys + t);
+                    }
+                    if (n >= KS) ok = warp_wait(bars, &bars.k_empty[n % KS], (n / KS - 1) & 1, p.err);
+                    if (!ok) break;
+                    convert(k_tiles + n % KS * S::kTileBytes, xk);
+                    arrive(&bars.k_full[n % KS]);
+                    if (more) {
+                        ok = wait_rows(n + 1);
+                        if (!ok) break;
+                        load(p.k, n + 1, xk);
+                    }
+                    if (n >= VS) ok = warp_wait(bars, &bars.v_empty[n % VS], (n / VS - 1) & 1, p.err);
+                    if (!ok) break;
+                    convert(v_tiles + n % VS * S::kTileBytes, xv);
+                    arrive(&bars.v_full[n % VS]);
+                    if (more) {
+                        load(p.v, n + 1, xv);
+                        ok = finish_scales(n + 1);
+                    }
+                }
+            }
+        } else {
+            // Whole tiles in pages that the cache has: boxes of a page each, by the copy engine; a lane issues its own
+            // page's.  (By cp.async, 32 for each of 128 threads: XX us.)  Others, whose last rows have to be zeros: row by
+            // row.
+            constexpr int PR = DP / 8;  // 16-byte pieces of a row
+            const int boxes = maps.box > 0 ? kTileKeys / maps.box : 0;
+            auto copy_rows = [&](const void *from, const int64_t *off, uint8_t *tile, bool is_k) {
+                const C *cache = static_cast<const C *>(from);
 #pragma unroll
                 for (int i = 0; i < PR; ++i) {
                     const int row = (i * kTileKeys + t) / PR, c = t % PR;
@@ -565,78 +840,75 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
                     else
                         cp_async16(to, in ? cache + o + 8 * c : cache, in ? 16 : 0);
                 }
-            }
-        };
-        auto done = [&](uint64_t *full) {
-            if (!IN8) cp_async_arrive(full);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full);
-        };
-        auto page_of = [&](int tok) {
-            const int64_t e = (int64_t)w.i * p.table_stride + tok / p.page;
-            return tok < w.x.len && LEAN_IN(e, (int64_t)(p.n_prefixes - 1) * p.table_stride + p.width, p.err) ? p.table[e] : 0;
-        };
-        while (ok && w.next(p, ROWS)) {
-            int next_id = page_of(w.from * kTileKeys + t);
-            for (int kt = w.from; ok && kt < w.to; ++kt, ++n) {
-                const int tok = kt * kTileKeys + t, id = next_id;
-                if (kt + 1 < w.to) next_id = page_of(tok + kTileKeys);  // under way during this tile
-                int64_t off = -1, at_scale = -1;
-                if (tok < w.x.len) {
-                    const int place = tok % p.page;
-                    if (id < 0 || id >= p.n_pages) {
-                        off = -2;
-                        atomicOr(p.err, kErrSlot);
+                cp_async_commit();
+            };
+            auto copy_boxes = [&](const CUtensorMap *map, uint8_t *tile, uint64_t *full, int tok, int id) {
+                if (warp == 8) {
+                    if (lane == 0) mbar_arrive_expect_tx(full, S::kTileBytes);
+                    __syncwarp();
+                    if (lane < boxes) {
+#pragma unroll
+                        for (int c = 0; c < S::kChunks; ++c)
+                            copy_box(smem_addr(tile + c * S::kChunkBytes + lane * maps.box * 128), map, 64 * c, tok % p.page, w.kvh, id, full);
+                    }
+                } else if (lane == 0) {
+                    mbar_arrive(full);
+                }
+            };
+            // the token whose page a thread looks up ahead: its box's first, or its row's
+            auto mine = [&](int kt) { return kt * kTileKeys + (boxes > 0 ? lane * maps.box : t); };
+            auto ahead = [&](int kt) { return boxes > 0 && lane >= boxes ? 0 : page_of(mine(kt)); };
+            unsigned rows_n = 0;  // tiles taken row by row so far
+            while (ok && w.next(p, ROWS)) {
+                int next_id = ahead(w.from);
+                for (int kt = w.from; ok && kt < w.to; ++kt, ++n) {
+                    const int tok = mine(kt);
+                    int id = next_id;
+                    if (kt + 1 < w.to) next_id = ahead(kt + 1);
+                    bool whole = boxes > 0 && kt * kTileKeys + kTileKeys <= w.x.len;
+                    if (whole) {
+                        bool fits = lane >= boxes || (id >= 0 && id < p.n_pages);
+                        if (lane < boxes && fits)
+                            fits = LEAN_SPAN((int64_t)id * p.page_stride + (int64_t)(tok % p.page) * p.place_stride + (int64_t)w.kvh * p.cache_hs,
+                                             (maps.box - 1) * p.place_stride + p.dim, p.cache_extent, p.err);
+                        whole = __all_sync(0xffffffffu, fits);
+                    }
+                    uint8_t *const kt_at = k_tiles + n % KS * S::kTileBytes, *const vt_at = v_tiles + n % VS * S::kTileBytes;
+                    int64_t *offs = nullptr;
+                    if (!whole) {
+                        if (boxes > 0) id = page_of(kt * kTileKeys + t);
+                        offs = row_off + (rows_n & 1) * kTileKeys;
+                        offs[t] = place_of(kt * kTileKeys + t, id);
+                        arrive(&bars.rows_full[rows_n & 1]);
+                        ok = warp_wait(bars, &bars.rows_full[rows_n & 1], rows_n / 2 & 1, p.err);
+                        if (!ok) break;
+                        ++rows_n;
+                    }
+                    if (n >= KS) ok = warp_wait(bars, &bars.k_empty[n % KS], (n / KS - 1) & 1, p.err);
+                    if (!ok) break;
+                    if (whole) copy_boxes(&maps.k, kt_at, &bars.k_full[n % KS], tok, id);
+                    else copy_rows(p.k, offs, kt_at, true);
+                    if (n >= VS) ok = warp_wait(bars, &bars.v_empty[n % VS], (n / VS - 1) & 1, p.err);
+                    if (!ok) break;
+                    if (whole) {
+                        copy_boxes(&maps.v, vt_at, &bars.v_full[n % VS], tok, id);
                     } else {
-                        off = (int64_t)id * p.page_stride + (int64_t)place * p.place_stride + (int64_t)w.kvh * p.cache_hs;
-                        if (!LEAN_SPAN(off, p.dim, p.cache_extent, p.err)) off = -1;
-                        at_scale = (int64_t)id * p.scale_page + (int64_t)place * p.scale_place + (int64_t)w.kvh * p.scale_hs;
-                        if (IN8 && !LEAN_IN(at_scale, p.scale_extent, p.err)) at_scale = -1;
+                        copy_rows(p.v, offs, vt_at, false);
+                        cp_async_wait<1>();
+                        smem_to_async();
+                        arrive(&bars.k_full[n % KS]);
+                        cp_async_wait<0>();
+                        smem_to_async();
+                        arrive(&bars.v_full[n % VS]);
                     }
                 }
-                float sk = off == -2 ? CUDART_NAN_F : 1.f, sv = 0.f;
-                if (IN8 && at_scale >= 0) {
-                    sk = p.k_scales[at_scale];
-                    sv = p.v_scales[at_scale];
-                }
-                int64_t *const offs = row_off + (n & 1) * kTileKeys;
-                offs[t] = off;
-                if (IN8) {
-                    float top = fmaxf(sv, 0.f);
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    if (lane == 0) bars.warp_top[n & 1][warp - 8] = top;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.rows_full[n & 1]);
-                ok = warp_wait(bars, &bars.rows_full[n & 1], n / 2 & 1, p.err);
-                if (!ok) break;
-                if (IN8) {
-                    const float *tops = bars.warp_top[n & 1];
-                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    const int e = min(252, max(1, (int)(__float_as_uint(top) >> 23)));
-                    float *to = scales + n % 4 * 2 * kTileKeys + t;
-                    to[0] = sk + (sk - sk);  // (an infinite one is NaN, as the scores of such a key are)
-                    to[kTileKeys] = sv * __uint_as_float((uint32_t)(253 - e) << 23);
-                    if (t == 0) bars.tile_exp[n % 4] = e;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.scales_full[n % 4]);
-                }
-                if (n >= KS) ok = warp_wait(bars, &bars.k_empty[n % KS], (n / KS - 1) & 1, p.err);
-                if (!ok) break;
-                copy(static_cast<const C *>(p.k), offs, k_tiles + n % KS * S::kTileBytes, true);
-                done(&bars.k_full[n % KS]);
-                if (n >= VS) ok = warp_wait(bars, &bars.v_empty[n % VS], (n / VS - 1) & 1, p.err);
-                if (!ok) break;
-                copy(static_cast<const C *>(p.v), offs, v_tiles + n % VS * S::kTileBytes, false);
-                done(&bars.v_full[n % VS]);
             }
+            cp_async_wait<0>();
         }
-        cp_async_wait<0>();
         for (unsigned j = n > KS ? n - KS : 0; ok && j < n; ++j) ok = warp_wait(bars, &bars.k_empty[j % KS], j / KS & 1, p.err);
         for (unsigned j = n > VS ? n - VS : 0; ok && j < n; ++j) ok = warp_wait(bars, &bars.v_empty[j % VS], j / VS & 1, p.err);
     } else {
-        regs_down<40>();
+        regs_down<PP == 1 ? 64 : IN8 ? 40 : 56>();
         if (lane == 0) {
             // ---- matrix instructions: warps 12 and 13 issue the groups' scores, 14 and 15 their products.  (One thread
             // needs about 110 cycles for an instruction that runs for 64: one warp for all of them 58 us where four
@@ -644,12 +916,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
             const int g = warp % 2;
             unsigned n = 0;
             bool ok = true;
+            auto halves_of = [&](unsigned t) { return w.x.len - (w.from + (int)t) * kTileKeys > kHalfKeys ? 2 : 1; };
             if (warp < 14) {
-                const uint32_t idesc = tile_idesc(BF16, kTileKeys, false);
+                const uint32_t idesc = tile_idesc(BF16, kHalfKeys, false);
                 const uint32_t q_lower = tile_lower(smem_addr(q_tiles + (NQ == 2 ? g * QP * S::kTileBytes : 0)), 16);
                 const uint32_t k_lower = tile_lower(smem_addr(k_tiles), 16);
                 const int steps = (p.dim + 15) / 16;
-                uint32_t q_phase = 0, o_phase = 0;
+                uint32_t q_phase = 0;
+                unsigned u = 0;  // half tiles of this group
                 while (ok && w.next(p, ROWS)) {
                     ok = phase_wait(bars, &bars.q_full, q_phase, p.err);
                     q_phase ^= 1;
@@ -657,21 +931,25 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
                     for (unsigned t = NQ == 2 ? 0 : g; ok && t < tiles; t += NQ == 2 ? 1 : 2) {
                         const unsigned j = n + t;
                         ok = phase_wait(bars, &bars.k_full[j % KS], j / KS & 1, p.err);
-                        // P lies where the scores go: its products first
-                        if (t >= (NQ == 2 ? 1 : 2)) ok = ok && phase_wait(bars, &bars.o_full[g], o_phase ^ 1, p.err);
-                        if (!ok) break;
-                        o_phase ^= 1;
-                        smem_to_async();
-                        tm_after();
-                        const uint32_t d = tmem + g * 128, b = k_lower + j % KS * (S::kTileBytes >> 4);
+                        const int halves = halves_of(t);
+                        for (int half = 0; ok && half < halves; ++half, ++u) {
+                            // p lies where the scores go: its products first
+                            if (u >= NB) ok = phase_wait(bars, &bars.o_full[g][u % NB], (u / NB - 1) & 1, p.err);
+                            if (!ok) break;
+                            smem_to_async();
+                            tm_after();
+                            const uint32_t d = tmem + S::scores(g, u % NB);
+                            const uint32_t b = k_lower + (j % KS * S::kTileBytes + half * kHalfKeys * 128 >> 4);
 #pragma unroll
-                        for (int part = 0; part < QP; ++part)
+                            for (int part = 0; part < QP; ++part)
 #pragma unroll
-                            for (int s = 0; s < DP / 16; ++s) {
-                                const uint32_t in = (s / 4 * S::kChunkBytes + s % 4 * 32) >> 4;
-                                if (s < steps) tm_mma_ss(d, q_lower + (part * S::kTileBytes >> 4) + in, b + in, kTileUpper, idesc, part + s > 0);
-                            }
-                        tm_commit(&bars.s_full[g]);
+                                for (int s = 0; s < DP / 16; ++s) {
+                                    const uint32_t in = (s / 4 * S::kChunkBytes + s % 4 * 32) >> 4;
+                                    if (s < steps)
+                                        tm_mma_ss(d, q_lower + (part * S::kTileBytes >> 4) + in, b + in, kTileUpper, idesc, part + s > 0);
+                                }
+                            tm_commit(&bars.s_full[g][u % NB]);
+                        }
                         tm_commit(&bars.k_empty[j % KS]);
                     }
                     if (ok) mbar_arrive(&bars.q_free);  // (this phase of q_full has been seen)
@@ -683,29 +961,37 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const PrefixA
                 static_assert(!ALL || NQ == 1, "tiles in turn");
                 const uint32_t idesc = tile_idesc(BF16, DP, true);
                 const uint32_t v_lower = tile_lower(smem_addr(v_tiles), S::kChunkBytes);
-                uint32_t p_phase[2] = {0, 0};
+                unsigned u0 = 0, u1 = 0;  // half tiles of this group, or of both
                 while (ok && w.next(p, ROWS) && !(ALL && g == 1)) {
                     const unsigned tiles = w.to - w.from;
+                    unsigned in_sum = 0;
                     for (unsigned t = NQ == 2 || ALL ? 0 : g; ok && t < tiles; t += NQ == 2 || ALL ? 1 : 2) {
                         const unsigned j = n + t;
                         const int of = ALL ? t % 2 : g;  // group
-                        // (P first: then what came before in this stage is done, and a phase is not mistaken for the one
-                        // two before it)
-                        ok = phase_wait(bars, &bars.p_full[of], p_phase[of], p.err);
-                        ok = ok && phase_wait(bars, &bars.v_full[j % VS], j / VS & 1, p.err);
-                        if (!ok) break;
-                        p_phase[of] ^= 1;
-                        smem_to_async();
-                        tm_after();
-                        const uint32_t a = tmem + of * 128, d = tmem + 256 + of * DP;
-                        const uint32_t b = v_lower + j % VS * (S::kTileBytes >> 4);
+                        const int halves = halves_of(t);
+                        for (int half = 0; ok && half < halves; ++half) {
+                            const unsigned u = ALL && of ? u1 : u0;
+                            // (p first: then what came before in this stage is done, and a phase is not mistaken for the
+                            // one two before it)
+                            ok = phase_wait(bars, &bars.p_full[of][u % NB], u / NB & 1, p.err);
+                            if (half == 0) ok = ok && phase_wait(bars, &bars.v_full[j % VS], j / VS & 1, p.err);
+                            if (!ok) break;
+                            smem_to_async();
+                            tm_after();
+                            const uint32_t a = tmem + S::scores(of, u % NB), d = tmem + S::outputs(of);
+                            const uint32_t b = v_lower + (j % VS * S::kTileBytes + half * kHalfKeys * 128 >> 4);
+                            const bool add = PP == 1 && in_sum % kFoldHalves > 0;
 #pragma unroll
-                        for (int s = 0; s < kTileKeys / 16; ++s)
+                            for (int s = 0; s < kHalfKeys / 16; ++s)
 #pragma unroll
-                            for (int part = 0; part < PP; ++part)
-                                tm_mma_ts(d, a + s / 2 * 32 + s % 2 * 8 + 16 * part, b + s * (2048 >> 4), kTileUpper, idesc,
-                                          part + s > 0);
-                        tm_commit(&bars.o_full[of]);
+                                for (int part = 0; part < PP; ++part)
+                                    tm_mma_ts(d, a + S::part(s / 2, part) + s % 2 * 8, b + s * (2048 >> 4), kTileUpper, idesc,
+                                              part + s > 0 || add);
+                            tm_commit(&bars.o_full[of][u % NB]);
+                            if (ALL && of) ++u1;
+                            else ++u0;
+                            ++in_sum;
+                        }
                         tm_commit(&bars.v_empty[j % VS]);
                     }
                     n += tiles;
@@ -806,21 +1092,21 @@ __global__ void __launch_bounds__(256) prefix_sum_kernel(const PrefixArgs p, uns
 }
 
 template <typename C, int DP, int QP, int PP, int NQ>
-lean_status launch_prefix(const PrefixArgs &p, int64_t flags, void *stream) {
+lean_status launch_prefix(const PrefixMaps &maps, const PrefixArgs &p, int64_t flags, void *stream) {
     static std::atomic<uint64_t> done{0};
     using S = PrefixShape<C, DP, QP, PP, NQ>;
     static_assert(S::kSmemAsked <= 232448, "shared memory");
     auto kern = prefix_kernel<C, DP, QP, PP, NQ>;
     if (!step_ensure_smem(kern, S::kSmemAsked, done)) return LEAN_ERR_CUDA;
-    return step_launch(kern, std::min(step_sm_count(), kPrefixMaxCtas), kPrefixThreads, S::kSmemAsked, flags, stream, p);
+    return step_launch(kern, std::min(step_sm_count(), kPrefixMaxCtas), kPrefixThreads, S::kSmemAsked, flags, stream, maps, p);
 }
 // 16-bit activations whose q is exact in one part (f16 on bf16 caches is not): one part each, two tiles of rows where
 // prefixes have more than one; else three parts of q and two of p.
 template <typename C, int DP>
-lean_status pick_prefix(const PrefixArgs &p, bool two, int64_t flags, void *stream) {
+lean_status pick_prefix(const PrefixMaps &maps, const PrefixArgs &p, bool two, int64_t flags, void *stream) {
     const bool split = p.act == LEAN_F32 || (p.act == LEAN_F16 && std::is_same<C, __nv_bfloat16>::value);
-    if (split) return launch_prefix<C, DP, 3, 2, 1>(p, flags, stream);
-    return two ? launch_prefix<C, DP, 1, 1, 2>(p, flags, stream) : launch_prefix<C, DP, 1, 1, 1>(p, flags, stream);
+    if (split) return launch_prefix<C, DP, 3, 3, 1>(maps, p, flags, stream);
+    return two ? launch_prefix<C, DP, 1, 1, 2>(maps, p, flags, stream) : launch_prefix<C, DP, 1, 1, 1>(maps, p, flags, stream);
 }
 
 }  // namespace

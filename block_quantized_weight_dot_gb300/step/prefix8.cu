@@ -4,7 +4,9 @@
 namespace lean {
 
 lean_status prefix_cache8(const PrefixArgs &p, bool two, int64_t flags, void *stream) {
-    return p.dim <= 64 ? pick_prefix<int8_t, 64>(p, two, flags, stream) : pick_prefix<int8_t, 128>(p, two, flags, stream);
+    const PrefixMaps none = {};
+    return p.dim <= 64 ? pick_prefix<int8_t, 64>(none, p, two, flags, stream)
+                       : pick_prefix<int8_t, 128>(none, p, two, flags, stream);
 }
 
 }  // namespace lean
