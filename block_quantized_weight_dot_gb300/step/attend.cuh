@@ -68,6 +68,45 @@ struct Shared {  // an item that begins in a block and goes on in others (-1: no
     int item, parts;
 };
 
+// Prefixes that sequences share (prefix.cuh): prefix i's tokens, its sequences starts[i]..starts[i + 1] - 1, whose query
+// heads that share a kv head are rows, and its part of the list of items, `rows` rows by tiles of 128 keys.
+constexpr int kTileRows = 128, kTileKeys = 128;
+// Tiles of a block's time that an item costs beside its own (q, the first scores, the last outputs).
+constexpr int kItemTiles = 2;
+struct PrefixList {
+    const int32_t *starts, *lens;
+    int n, n_seqs, group, hkv, rows, most;  // most: tokens that a prefix's pages can hold
+    unsigned sms, own_most;                 // SMs, and the most blocks that sequences' own tokens can take
+    float unit_ns, tile_ns;                 // what a unit of those and a tile of a prefix take of an SM's time
+};
+struct Prefix {
+    int first, count, len, keys, tiles;  // keys: tiles of keys; tiles: of rows, for a kv head
+    __device__ __forceinline__ unsigned cost(int hkv) const {  // (the call refuses lists that 32 bits do not count)
+        return (unsigned)hkv * tiles * (keys + (keys > 0 ? kItemTiles : 0));
+    }
+};
+__device__ __forceinline__ Prefix open_prefix(const PrefixList &p, int i, unsigned *err) {
+    Prefix x;
+    const bool in = LEAN_IN(i, p.n, err);
+    x.first = in ? min(max(p.starts[i], 0), p.n_seqs) : 0;
+    const int end = in ? min(max(p.starts[i + 1], 0), p.n_seqs) : 0;
+    x.count = max(0, end - x.first);
+    x.len = min(in ? max(p.lens[i], 0) : 0, p.most);
+    x.keys = x.len / kTileKeys + (x.len % kTileKeys != 0);
+    x.tiles = (x.count * p.group - 1 + p.rows) / p.rows;  // (rows + 255 is below 2^31: the call's limits)
+    if (x.tiles == 0) x.keys = 0;
+    return x;
+}
+// The two kernels of one call run beside one another: of the SMs, as many as this for `units` units of sequences' own
+// tokens where the prefixes have `tiles` tiles, by their times; the SMs that no tile needs at least.  Both kernels come to
+// the same number.
+__device__ __forceinline__ unsigned own_blocks(const PrefixList &p, unsigned units, unsigned tiles) {
+    if (tiles == 0) return p.own_most;
+    const float a = (float)units * p.unit_ns, b = (float)tiles * p.tile_ns;
+    const unsigned n = (unsigned)__float2int_rn(p.sms * __fdiv_rn(a, a + b));
+    return min(p.own_most, min(p.sms - 1, max(max(1u, n), p.sms > tiles ? p.sms - tiles : 1)));
+}
+
 struct AttArgs {
     const void *q, *k, *v;
     void *out;
@@ -79,6 +118,9 @@ struct AttArgs {
     int64_t qs, qhs, os, ohs, page_stride, place_stride, cache_hs, table_stride, n_pages;
     int n_seqs, hq, hkv, group, tiles, dim, page, paged, whole, width, window;
     int act, out_act;
+    // beside a kernel for prefixes (list.n > 0), whose blocks may begin only when what came before this one is done (they
+    // do not wait for it themselves): blocks as own_blocks() says, parts of shared items left to the kernel after both
+    PrefixList list;
     float scale_log2;
     const float *k_scales, *v_scales;  // of caches in 8 bits
     int64_t scale_page, scale_place, scale_hs;
@@ -398,12 +440,17 @@ __global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel
     constexpr int AT = 2;  // steps of the values whose products are under way at once (more spill)
     extern __shared__ uint8_t queue_raw[];
     uint8_t *queue = queue_raw + (512 - smem_addr(queue_raw) % 512) % 512;
-    __shared__ unsigned scan[W];
+    __shared__ unsigned scan[W], tile_scan[W];
     __shared__ int longest[W];
     __shared__ unsigned units_before[T];
     __shared__ Record rec[2 * W];
 
-    step_begin();
+    if (p.list.n > 0) {
+        pdl_wait();
+        pdl_launch_dependents();
+    } else {
+        step_begin();
+    }
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int r = lane / 4, c4 = lane % 4;
     // The dimension of the first of a thread's pair j, of q's rows and of the outputs: in 16 bits as the matrix
@@ -431,6 +478,12 @@ __global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel
         if (lane >= o) incl += u;
     }
     most = __reduce_max_sync(0xffffffffu, most);
+    if (p.list.n > 0) {
+        unsigned tiles = 0;
+        for (int i = threadIdx.x; i < p.list.n; i += T) tiles += open_prefix(p.list, i, p.err).cost(p.hkv);
+        tiles = __reduce_add_sync(0xffffffffu, tiles);
+        if (lane == 0) tile_scan[warp] = tiles;
+    }
     if (lane == 31) {
         scan[warp] = incl;
         longest[warp] = most;
@@ -446,9 +499,16 @@ __global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel
     }
     // Equal runs for all blocks (a unit a warp at least) have to be joined across blocks; where there are few
     // items and none is long, a block for each is done sooner.
+    unsigned grid = gridDim.x;
+    if (p.list.n > 0) {
+        unsigned tiles = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) tiles += tile_scan[i];
+        grid = own_blocks(p.list, units, tiles);
+    }
     const int64_t items = (int64_t)p.n_seqs * groups;
-    const bool by_item = items <= gridDim.x && (unsigned)((most + W - 1) / W) <= units / (gridDim.x * W) + kJoinUnits;
-    const int blocks = by_item ? (int)items : (int)min(gridDim.x, units / W + (units % W != 0));
+    const bool by_item = items <= grid && (unsigned)((most + W - 1) / W) <= units / (grid * W) + kJoinUnits;
+    const int blocks = by_item ? (int)items : (int)min(grid, units / W + (units % W != 0));
     if ((int)blockIdx.x >= blocks) {
         if (threadIdx.x == 0 && LEAN_IN(blockIdx.x, kAttMaxCtas, p.err)) p.shared[blockIdx.x] = Shared{-1, 0};
         return;
@@ -1119,20 +1179,24 @@ __global__ void __launch_bounds__(kSumWarps * 32) attend_sum_kernel(const AttArg
     }
 }
 
+// No more blocks of W warps than there can be units for.
+inline int64_t att_grid(const AttArgs &p, int W) {
+    const int64_t units = ((int64_t)p.width * p.page + 2 * kUnit) / kUnit * p.n_seqs * p.hkv * p.tiles;
+    return std::min<int64_t>(std::min(step_sm_count(), kAttMaxCtas), std::max<int64_t>(1, units / W));
+}
+
 template <typename C, int DP, int PARTS, bool WIDE>
 lean_status launch_attend(const AttArgs &p, int64_t flags, void *stream) {
     static std::atomic<uint64_t> done{0};
     auto kern = attend_kernel<C, DP, PARTS, WIDE>;
     if (!step_ensure_smem(kern, att_smem<C, DP>(WIDE ? 16 : 8), done)) return LEAN_ERR_CUDA;
-    // no more blocks than there can be units for
     constexpr int W = AttShape<C, DP>::kWarps;
-    const int64_t units = ((int64_t)p.width * p.page + 2 * kUnit) / kUnit * p.n_seqs * p.hkv * p.tiles;
-    const int64_t grid = std::min<int64_t>(std::min(step_sm_count(), kAttMaxCtas), std::max<int64_t>(1, units / W));
+    const int64_t grid = att_grid(p, W);
     const lean_status st = step_launch(kern, grid, W * 32, att_smem<C, DP>(WIDE ? 16 : 8), flags, stream, p);
     // (no item can be shared by blocks where each gets its own whatever the lengths are)
     const int64_t most = ((int64_t)p.width * p.page + 2 * kUnit - 1) / kUnit;
     const bool by_item = (int64_t)p.n_seqs * p.hkv * p.tiles <= grid && (most + W - 1) / W <= kJoinUnits;
-    if (st != LEAN_OK || grid == 1 || by_item) return st;
+    if (st != LEAN_OK || grid == 1 || by_item || p.list.n > 0) return st;
     constexpr int H = WIDE ? 16 : 8;
     return step_launch(attend_sum_kernel<H, DP>, grid, kSumWarps * 32, 0, LEAN_FLAG_EARLY_WEIGHTS, stream, p, (int)grid);
 }

@@ -19,14 +19,13 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// The caches as tensors in boxes of as many places as a tile and every page are whole numbers of; box 0 where there are
-// none of 8 or more (rows of a box lie in groups of 8), or a stride is 0 between rows that are not one.
+// The caches as tensors in boxes of prefix_box() places (8 or more: rows of a tile lie in groups of 8); none where a
+// stride is 0 between rows that are not one.
 PrefixMaps make_maps(const PrefixArgs &p, bool bf16) {
     PrefixMaps m = {};
-    int box = kTileKeys;
-    while (p.page % box) box /= 2;
+    const int box = prefix_box(p.page);
     const EncodeTiled encode = encode_tiled();
-    if (box < 8 || !encode || (p.page > 1 && p.place_stride == 0) || (p.hkv > 1 && p.cache_hs == 0) ||
+    if (box == 0 || !encode || (p.page > 1 && p.place_stride == 0) || (p.hkv > 1 && p.cache_hs == 0) ||
         (p.n_pages > 1 && p.page_stride == 0))
         return m;
     const int64_t strides[3] = {p.place_stride, p.cache_hs, p.page_stride};
@@ -69,19 +68,20 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 int prefix_dim(int64_t dim) { return dim <= 64 ? 64 : 128; }
 
 bool prefix_sizes_ok(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim, int64_t n_prefixes) {
-    return att_sizes_ok(n_seqs, hq, hkv, dim) && dim <= 128 && n_prefixes > 0 && n_prefixes <= n_seqs;
+    return att_sizes_ok(n_seqs, hq, hkv, dim) && dim <= 128 && n_prefixes > 0 && n_prefixes <= n_seqs &&
+           n_seqs <= (INT32_MAX - 512) / (hq / hkv);
 }
 
-// The workspace's parts: that of attend.cuh, the list, sequences' own results, maxima and sums, outputs.
+// The workspace's parts: that of attend.cuh, rows' first parts, sequences' own results, maxima and sums, outputs.
 struct PrefixRoom {
-    int64_t plan, own_out, own_lse, ml, o, bytes, parts;
+    int64_t first, own_out, own_lse, ml, o, bytes, parts;
 };
-PrefixRoom prefix_room(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim, int64_t n_prefixes) {
+PrefixRoom prefix_room(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim) {
     PrefixRoom r;
     const int64_t rows = n_seqs * hq;
     r.parts = 2 * rows + kPrefixMaxCtas * 256;
-    r.plan = up256(att_workspace_bytes(hq, hkv, dim));
-    r.own_out = r.plan + up256((n_prefixes + 1) * 8);
+    r.first = up256(att_workspace_bytes(hq, hkv, dim));
+    r.own_out = r.first + up256(rows * 8);
     r.own_lse = r.own_out + up256(rows * dim * 4);
     r.ml = r.own_lse + up256(rows * 4);
     r.o = r.ml + up256(r.parts * 8);
@@ -94,7 +94,7 @@ PrefixRoom prefix_room(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim, int
 extern "C" int64_t lean_prefix_attention_workspace_bytes(int64_t n_seqs, int64_t n_q_heads, int64_t n_kv_heads,
                                                          int64_t head_dim, int64_t n_prefixes) {
     if (!prefix_sizes_ok(n_seqs, n_q_heads, n_kv_heads, head_dim, n_prefixes)) return -1;
-    return prefix_room(n_seqs, n_q_heads, n_kv_heads, head_dim, n_prefixes).bytes;
+    return prefix_room(n_seqs, n_q_heads, n_kv_heads, head_dim).bytes;
 }
 
 extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *stream) {
@@ -134,7 +134,10 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     const int64_t group = a->n_q_heads / a->n_kv_heads, tiles = group > 8 ? (group + 15) / 16 : 1;
     if ((a->table_width * a->page_size / kUnit + 2 + kAttItemUnits) * a->n_seqs * a->n_kv_heads * tiles > UINT32_MAX)
         return LEAN_ERR_SHAPE;  // attend.cuh counts units of sequences' own tokens in 32 bits
-    const PrefixRoom room = prefix_room(a->n_seqs, a->n_q_heads, a->n_kv_heads, a->head_dim, a->n_prefixes);
+    // as prefix.cuh its items' tiles: a prefix's sequences fill at least all but one of its tiles of rows
+    const int64_t columns = (a->prefix_width * a->page_size / kTileKeys + 1 + kItemTiles) * a->n_kv_heads;
+    if (columns > UINT32_MAX / (a->n_seqs * group / kTileRows + a->n_prefixes)) return LEAN_ERR_SHAPE;
+    const PrefixRoom room = prefix_room(a->n_seqs, a->n_q_heads, a->n_kv_heads, a->head_dim);
     if (a->workspace_bytes < room.bytes) return LEAN_ERR_SHAPE;
     uint8_t *const ws = static_cast<uint8_t *>(a->workspace);
     unsigned *const err = error_word();
@@ -193,8 +196,6 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     p.k_scales = own.k_scales;
     p.v_scales = own.v_scales;
     p.table = a->prefix_table;
-    p.lens = a->prefix_lens;
-    p.starts = a->seq_starts;
     p.qs = own.qs;
     p.qhs = own.qhs;
     p.page_stride = own.page_stride;
@@ -215,7 +216,7 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     p.width = (int)a->prefix_width;
     p.act = own.act;
     p.scale_log2 = own.scale_log2;
-    p.plan = reinterpret_cast<unsigned long long *>(ws + room.plan);
+    p.first = reinterpret_cast<int2 *>(ws + room.first);
     p.ml = reinterpret_cast<float2 *>(ws + room.ml);
     p.o = reinterpret_cast<float *>(ws + room.o);
     p.parts = room.parts;
@@ -235,16 +236,38 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     const bool two = a->act_dtype != LEAN_F32 && !(a->act_dtype == LEAN_F16 && a->cache_dtype == LEAN_BF16) &&
                      a->n_seqs * group > a->n_prefixes * kTileRows;
     const bool bf16 = a->cache_dtype == LEAN_BF16;
-    lean_status st = in8 ? prefix_cache8(p, two, a->flags, stream) : prefix_cache16(p, bf16, two, a->flags, stream);
+    // Both kernels run beside one another.  A unit of 16 tokens moves its keys and values at about 40 GB/s of an SM's, a
+    // tile takes 0.9 us for each of its tiles of rows.
+    PrefixList list = {};
+    list.starts = a->seq_starts;
+    list.lens = a->prefix_lens;
+    list.n = p.n_prefixes;
+    list.n_seqs = p.n_seqs;
+    list.group = p.group;
+    list.hkv = p.hkv;
+    list.rows = two ? 2 * kTileRows : kTileRows;
+    list.most = (int)(a->prefix_width * a->page_size);
+    list.sms = (unsigned)std::min(step_sm_count(), kPrefixMaxCtas);
+    list.own_most = (unsigned)att_grid(own, 8);
+    list.unit_ns = (float)(kUnit * 2 * a->head_dim * (in8 ? 1 : 2)) / 40.f;
+    list.tile_ns = two ? 1800.f : 900.f;
+    p.list = own.list = list;
+    p.own_lens = a->seq_lens;
+    p.own_most = (int)(a->table_width * a->page_size);
+    p.own_groups = own.hkv * own.tiles;
+    p.own_heads = group > 8 ? 16 : 8;
+    p.own_tiles = own.tiles;
+    p.own_grid = (int)list.own_most;
+    p.shared = own.shared;
+    p.cta_parts = own.cta_parts;
+    p.part_extent = own.part_extent;
+    // Sequences' own tokens first: blocks of the prefixes' kernel begin beside theirs.
+    lean_status st = in8 ? attend_cache8(own, a->flags, stream) : attend_cache16(own, bf16, a->flags, stream);
     if (st != LEAN_OK) return st;
-    st = in8 ? attend_cache8(own, LEAN_FLAG_EARLY_WEIGHTS, stream)
-             : attend_cache16(own, bf16, LEAN_FLAG_EARLY_WEIGHTS, stream);
+    constexpr int64_t early = LEAN_FLAG_EARLY_WEIGHTS;
+    st = in8 ? prefix_cache8(p, two, early, stream) : prefix_cache16(p, bf16, two, early, stream);
     if (st != LEAN_OK) return st;
     const int64_t grid = (a->n_seqs * a->n_q_heads + 7) / 8;
-    const unsigned blocks = (unsigned)std::min(step_sm_count(), kPrefixMaxCtas);
-    if (p.dim <= 64)
-        return step_launch(two ? prefix_sum_kernel<64, 2> : prefix_sum_kernel<64, 1>, grid, 256, 0, LEAN_FLAG_EARLY_WEIGHTS,
-                           stream, p, blocks);
-    return step_launch(two ? prefix_sum_kernel<128, 2> : prefix_sum_kernel<128, 1>, grid, 256, 0, LEAN_FLAG_EARLY_WEIGHTS,
-                       stream, p, blocks);
+    if (p.dim <= 64) return step_launch(two ? prefix_sum_kernel<64, 2> : prefix_sum_kernel<64, 1>, grid, 256, 0, early, stream, p);
+    return step_launch(two ? prefix_sum_kernel<128, 2> : prefix_sum_kernel<128, 1>, grid, 256, 0, early, stream, p);
 }

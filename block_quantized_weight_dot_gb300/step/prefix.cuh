@@ -46,11 +46,9 @@
 
 namespace lean {
 
-constexpr int kTileRows = 128, kTileKeys = 128, kHalfKeys = 64;
+constexpr int kHalfKeys = 64;  // of a tile
 constexpr int kPrefixMaxCtas = 160;
 constexpr int kPrefixThreads = 512;
-// Tiles of a block's time that an item costs beside its own (q, the first scores, the last outputs).
-constexpr int kItemTiles = 2;
 // Halves of tiles whose products are summed in tensor memory before they are added in fp32 (one part of p): what is below
 // 2^-24 of a sum is cut off when it is added, 16 keys at a time, so that a row errs by 2^-16 of its largest sum at most.
 constexpr int kFoldHalves = 32;
@@ -58,18 +56,26 @@ constexpr int kFoldHalves = 32;
 struct PrefixArgs {
     const void *q, *k, *v;
     const float *k_scales, *v_scales;
-    const int32_t *table, *lens, *starts;
+    const int32_t *table;
+    PrefixList list;
     int64_t qs, qhs, page_stride, place_stride, cache_hs, scale_page, scale_place, scale_hs, table_stride, n_pages;
     int n_prefixes, n_seqs, hq, hkv, group, dim, page, width, act;
+    // sequences' own tokens: lengths, the most that their pages can hold, groups of query heads of a sequence
+    const int32_t *own_lens;
+    int own_most, own_groups;
     float scale_log2;
-    // workspace: where each prefix's items begin in the list (and, last, how long it is); maxima and sums, outputs, of
-    // the parts that begin an item, by row (and half, with one tile of rows), then those that go on with one, by block
-    unsigned long long *plan;
+    // workspace: maxima and sums, outputs, of the parts that begin an item, by row (and half, with one tile of rows), then
+    // those that go on with one, by block
+    int2 *first;  // of a row with a prefix: the block that begins its item, and how many parts it has
     float2 *ml;
     float *o;
     int64_t parts;  // how many there are
     // a sequence's own tokens, and what comes out
     const float *own_out, *own_lse;
+    const Shared *shared;     // items that blocks share, and their parts (attend.cuh)
+    const float *cta_parts;
+    int64_t part_extent;
+    int own_heads, own_tiles, own_grid;
     void *out;
     float *lse;
     int64_t os, ohs;
@@ -84,6 +90,13 @@ struct PrefixMaps {
     int box;
 };
 
+// As many places as a tile and every page are whole numbers of; 0 if fewer than 8.
+inline int prefix_box(int page) {
+    int box = kTileKeys;
+    while (page % box) box /= 2;
+    return box < 8 ? 0 : box;
+}
+
 lean_status prefix_cache16(const PrefixArgs &p, bool bf16, bool two, int64_t flags, void *stream);
 lean_status prefix_cache8(const PrefixArgs &p, bool two, int64_t flags, void *stream);
 
@@ -94,46 +107,19 @@ namespace {
 constexpr unsigned kErrPrefixWait = 4u;  // as the tensor-core products: a bounded wait ran out
 constexpr uint64_t kPrefixWaitNs = 2000000000ull;
 
-// A prefix: its sequences, keys, and its items in the list.
-struct Prefix {
-    int first, count, len, keys, tiles;  // keys: tiles of keys; tiles: of rows, for a kv head
-    __device__ __forceinline__ unsigned long long cost(int hkv) const {
-        return (unsigned long long)hkv * tiles * (keys + (keys > 0 ? kItemTiles : 0));
-    }
-};
-__device__ __forceinline__ Prefix open_prefix(const PrefixArgs &p, int i, int rows) {
-    Prefix x;
-    const bool in = LEAN_IN(i, p.n_prefixes, p.err);
-    x.first = in ? min(max(p.starts[i], 0), p.n_seqs) : 0;
-    const int end = in ? min(max(p.starts[i + 1], 0), p.n_seqs) : 0;
-    x.count = max(0, end - x.first);
-    const int64_t most = (int64_t)p.width * p.page;
-    const int len = in ? max(p.lens[i], 0) : 0;
-    x.len = len > most ? (int)most : len;
-    x.keys = x.len / kTileKeys + (x.len % kTileKeys != 0);
-    x.tiles = (int)(((int64_t)x.count * p.group + rows - 1) / rows);
-    if (x.tiles == 0) x.keys = 0;
-    return x;
-}
 // A list of units cut into equal runs, none of them empty (blocks past the units have none): where a block's run begins,
 // and the block that has a unit.
 struct Runs {
-    unsigned long long each;
-    unsigned rest, blocks;
-    __device__ __forceinline__ Runs(unsigned long long total, unsigned n) {
-        blocks = total < n ? max(1u, (unsigned)total) : n;
+    unsigned each, rest, blocks;  // the first `rest` blocks have one more
+    __device__ __forceinline__ Runs(unsigned total, unsigned n) {
+        blocks = min(max(1u, total), n);
         each = total / blocks;
-        rest = (unsigned)(total % blocks);
+        rest = total - each * blocks;
     }
-    __device__ __forceinline__ unsigned long long begin(unsigned b) const { return each * b + rest * b / blocks; }
-    __device__ __forceinline__ unsigned of(unsigned long long u) const {
-        unsigned lo = 0, hi = blocks - 1;  // the last block that begins at u or before it
-        while (lo < hi) {
-            const unsigned mid = (lo + hi + 1) / 2;
-            if (begin(mid) <= u) lo = mid;
-            else hi = mid - 1;
-        }
-        return lo;
+    __device__ __forceinline__ unsigned begin(unsigned b) const { return each * b + min(b, rest); }
+    __device__ __forceinline__ unsigned of(unsigned u) const {
+        const unsigned longer = rest * (each + 1);
+        return u < longer ? u / (each + 1) : rest + (u - longer) / each;
     }
 };
 
@@ -141,25 +127,28 @@ struct Runs {
 struct Walk {
     int i;                       // prefix
     Prefix x;
-    unsigned long long off;      // place in the prefix's part of the list
-    unsigned long long left;     // of the run
+    unsigned off;                // place in the prefix's part of the list
+    unsigned left;               // of the run
+    unsigned unit, begin;        // the run's next unit, the first one of the part below
     // the part of an item that comes next: keys' tiles from..to-1
     int kvh, tile, from, to;
     // false: no more
-    __device__ __forceinline__ bool next(const PrefixArgs &p, int rows) {
+    __device__ __forceinline__ bool next(const PrefixArgs &p) {
         while (left > 0) {
             while (off >= x.cost(p.hkv)) {
                 off -= x.cost(p.hkv);
                 if (++i >= p.n_prefixes) return false;
-                x = open_prefix(p, i, rows);
+                x = open_prefix(p.list, i, p.err);
             }
             const int each = x.keys + kItemTiles;
             const int item = (int)(off / each);
-            from = (int)(off - (unsigned long long)item * each);
-            const int take = (int)min(left, (unsigned long long)(each - from));
+            from = (int)(off - (unsigned)item * each);
+            const int take = (int)min(left, (unsigned)(each - from));
             to = min(from + take, x.keys);
+            begin = unit;
             off += take;
             left -= take;
+            unit += take;
             if (from < to) {
                 kvh = item / x.tiles;
                 tile = item - kvh * x.tiles;
@@ -195,15 +184,14 @@ struct PrefixBars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];  // a stage's tile is there, was used
     uint64_t s_full[2][3], p_full[2][3], o_full[2][3];      // of a group's buffers: scores, p, products are done
     uint64_t q_full, q_free;                                // q is there; both groups are done with it
-    uint64_t rows_full[2], tops_full[2];                    // a tile's rows' places, the warps' largest scales are there
+    uint64_t rows_full[2];                                  // a tile's rows' places are there
     uint64_t scales_full[4];
     uint64_t last;                                          // every matrix instruction is done
     uint32_t tmem;
     int dead;            // a wait ran out: everyone leaves
-    int tile_exp[4];     // exponents of the tiles' largest value scales
-    float warp_top[2][4];
+    int value_exp[4][4]; // exponents of the largest value scales of 32 keys, of four tiles
     int start_i;         // the run's first prefix and place in it
-    unsigned long long start_off;
+    unsigned start_off;
 };
 static_assert(sizeof(PrefixBars) <= 512, "room for the barriers");
 
@@ -248,12 +236,95 @@ __device__ __forceinline__ bool warp_wait(PrefixBars &b, uint64_t *bar, uint32_t
     return __all_sync(0xffffffffu, phase_wait(b, bar, parity, err));
 }
 
-// Row r of a tile's item: its sequence and query head; false: the item has fewer.
-__device__ __forceinline__ bool row_of(const PrefixArgs &p, const Walk &w, int64_t r, int &seq, int &head) {
-    if (r >= (int64_t)w.x.count * p.group) return false;
-    seq = w.x.first + (int)(r / p.group);
-    head = w.kvh * p.group + (int)(r % p.group);
+// q of a warp's 32 rows, lane l's at q_at (-1: none), as it is into a tile of q, with the signs turned by `flip`; read as
+// below.
+template <typename S, int DP, typename Mine, typename Ready>
+__device__ __forceinline__ bool copy_q(const PrefixArgs &p, int64_t q_at, uint8_t *tile, int row0, int lane, uint32_t flip, Mine mine, Ready ready) {
+    constexpr int LPR = DP / 8, RPI = 32 / LPR;
+    const int c = lane % LPR;
+    uint4 x[LPR];
+#pragma unroll
+    for (int i = 0; i < LPR; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, q_at, i * RPI + lane / LPR);
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (mine(i) && at >= 0 && 8 * c < p.dim && LEAN_SPAN(at + 8 * c, 8, p.q_extent, p.err))
+            x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at + 8 * c);
+    }
+    if (!ready()) return false;
+#pragma unroll
+    for (int i = 0; i < LPR; ++i) {
+        const int row = row0 + i * RPI + lane / LPR;
+        if (mine(i))
+            *reinterpret_cast<uint4 *>(tile + c / 8 * S::kChunkBytes + row * 128 + ((c % 8) ^ (row & 7)) * 16) =
+                make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
+    }
     return true;
+}
+
+// q of a warp's 32 rows, lane l's at q_at (-1: none): scaled by a power of two and split in parts into tiles of q, E
+// elements to a lane (16 bytes of them), so that a row is read by neighbouring lanes.  Rows whose turn is not `mine` are
+// looked at but not written.  Returns the largest element of the lane's own row, as bits.
+template <typename S, typename T, int DP, int QP, int E, typename Mine, typename Ready>
+__device__ __forceinline__ uint32_t load_q(const PrefixArgs &p, int64_t q_at, uint8_t *tiles, int row0, int lane, float sign, Mine mine, Ready ready) {
+    constexpr int LPR = DP / E, RPI = 32 / LPR, B = LPR < 8 ? LPR : 8;  // lanes of a row, rows at a time, times under way
+    const int c = lane % LPR;
+    uint32_t own = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int it0 = 0; it0 < LPR; it0 += B) {
+        uint4 x[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int64_t at = __shfl_sync(0xffffffffu, q_at, (it0 + i) * RPI + lane / LPR);
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (at >= 0 && E * c < p.dim && LEAN_SPAN(at + E * c, E, p.q_extent, p.err))
+                x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.q) + (at + E * c) * (16 / E));
+        }
+        if (it0 == 0) ok = ready();
+        if (!ok) return 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int it = it0 + i;
+            float f[E];
+            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (E == 4) {
+                    f[k] = __uint_as_float(u[k]);
+                } else {
+                    RawPair<false> pair;
+                    pair.v = u[k];
+                    const float2 v = pair.get(p.act);
+                    f[2 * k % E] = v.x;
+                    f[(2 * k + 1) % E] = v.y;
+                }
+            }
+            float top = 0.f;
+#pragma unroll
+            for (int k = 0; k < E; ++k) top = fmaxf(top, fabsf(f[k]));
+#pragma unroll
+            for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const uint32_t of_own = __float_as_uint(__shfl_sync(0xffffffffu, top, lane % RPI * LPR));
+            if (lane / RPI == it) own = of_own;
+            if (!mine(it)) continue;
+            const int e = (int)(__float_as_uint(top) >> 23);
+            const int fe = e == 0 || e == 255 ? 127 : min(253, max(1, 254 + PartRange<T>::kLiftQ - e));
+            const float up = sign * __uint_as_float((uint32_t)fe << 23);
+#pragma unroll
+            for (int k = 0; k < E; ++k) f[k] *= up;
+            const int row = row0 + it * RPI + lane / LPR, piece = E == 8 ? c : c / 2;
+            uint8_t *to = tiles + piece / 8 * S::kChunkBytes + row * 128 + ((piece % 8) ^ (row & 7)) * 16 + (E == 8 ? 0 : c % 2 * 8);
+#pragma unroll
+            for (int part = 0; part < QP; ++part) {
+                uint32_t a[E / 2];
+#pragma unroll
+                for (int k = 0; k < E / 2; ++k) a[k] = take_part<T>(f[2 * k], f[2 * k + 1]);
+                if constexpr (E == 8) *reinterpret_cast<uint4 *>(to + part * S::kTileBytes) = make_uint4(a[0], a[1], a[2], a[3]);
+                else *reinterpret_cast<uint2 *>(to + part * S::kTileBytes) = make_uint2(a[0], a[1]);
+            }
+        }
+    }
+    return own;
 }
 
 template <typename C, int DP, int QP, int PP, int NQ>
@@ -268,22 +339,32 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     int64_t *const row_off = reinterpret_cast<int64_t *>(smem + S::kOff);
     float *const scales = reinterpret_cast<float *>(smem + S::kScaleAt);  // [tile % 4][key's, value's][128]
     PrefixBars &bars = *reinterpret_cast<PrefixBars *>(smem + S::kBars);
-    step_begin();
+    // (No wait: the kernel before is attend.cuh's for this call, whose blocks let this one begin only when what came
+    // before them is done, and nothing here is read or written there.  What they leave is waited for at the end, for the
+    // kernel after this one.)
+    pdl_launch_dependents();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 
     // ---- this block's run of the list
-    unsigned long long *const before = reinterpret_cast<unsigned long long *>(smem);  // (the tiles' room, unused yet)
+    unsigned *const before = reinterpret_cast<unsigned *>(smem);  // (the tiles' room, unused yet)
     const int per = (p.n_prefixes + kPrefixThreads - 1) / kPrefixThreads;
     const int lo = min(p.n_prefixes, (int)threadIdx.x * per), hi = min(p.n_prefixes, lo + per);
-    unsigned long long mine = 0;
-    for (int i = lo; i < hi; ++i) mine += open_prefix(p, i, ROWS).cost(p.hkv);
-    unsigned long long incl = mine;
+    unsigned mine = 0;
+    for (int i = lo; i < hi; ++i) mine += open_prefix(p.list, i, p.err).cost(p.hkv);
+    unsigned incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-        const unsigned long long u = __shfl_up_sync(0xffffffffu, incl, o);
+        const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += u;
     }
     if (lane == 31) before[warp] = incl;
+    unsigned own = 0;  // units of sequences' own tokens, as attend.cuh counts them
+    for (int i = threadIdx.x; i < p.n_seqs; i += kPrefixThreads) {
+        const int len = min(LEAN_IN(i, p.n_seqs, p.err) ? max(p.own_lens[i], 0) : 0, p.own_most);
+        own += (unsigned)(max(1, len / kUnit + (len % kUnit != 0)) + kAttItemUnits) * p.own_groups;
+    }
+    own = __reduce_add_sync(0xffffffffu, own);
+    if (lane == 0) before[32 + warp] = own;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.k_full[i], 4);
@@ -297,10 +378,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             }
         }
         for (int i = 0; i < 4; ++i) mbar_init(&bars.scales_full[i], 4);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.rows_full[i], 4);
-            mbar_init(&bars.tops_full[i], 4);
-        }
+        for (int i = 0; i < 2; ++i) mbar_init(&bars.rows_full[i], 4);
         mbar_init(&bars.q_full, 8);
         mbar_init(&bars.q_free, 10);
         mbar_init(&bars.last, 4);
@@ -309,28 +387,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         fence_mbar_init();
     }
     __syncthreads();
-    unsigned long long begins = incl - mine, total = 0;
+    unsigned begins = incl - mine, total = 0;
+    own = 0;
 #pragma unroll
     for (int i = 0; i < kPrefixThreads / 32; ++i) {
         if (i < warp) begins += before[i];
         total += before[i];
+        own += before[32 + i];
     }
-    const Runs runs(total, gridDim.x);
+    // (blocks past these find the SMs of attend.cuh's kernel free, when it is done, and have nothing to do)
+    const Runs runs(total, max(1u, gridDim.x - min(gridDim.x, own_blocks(p.list, own, total))));
     const bool has_run = blockIdx.x < runs.blocks;
-    const unsigned long long run_lo = has_run ? runs.begin(blockIdx.x) : 0, run_hi = has_run ? runs.begin(blockIdx.x + 1) : 0;
-    if (blockIdx.x == 0) {  // for the kernel that adds the parts up
-        unsigned long long at = begins;
-        for (int i = lo; i < hi; ++i) {
-            if (LEAN_IN(i, p.n_prefixes + 1, p.err)) p.plan[i] = at;
-            at += open_prefix(p, i, ROWS).cost(p.hkv);
-        }
-        if (threadIdx.x == 0 && LEAN_IN(p.n_prefixes, p.n_prefixes + 1, p.err)) p.plan[p.n_prefixes] = total;
-    }
+    const unsigned run_lo = has_run ? runs.begin(blockIdx.x) : 0, run_hi = has_run ? runs.begin(blockIdx.x + 1) : 0;
     if (run_lo < run_hi && begins <= run_lo && run_lo < begins + mine) {  // one thread's
-        unsigned long long off = run_lo - begins;
+        unsigned off = run_lo - begins;
         int i = lo;
         for (;; ++i) {
-            const unsigned long long c = open_prefix(p, i, ROWS).cost(p.hkv);
+            const unsigned c = open_prefix(p.list, i, p.err).cost(p.hkv);
             if (off < c) break;
             off -= c;
         }
@@ -346,7 +419,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     w.i = max(bars.start_i, 0);
     w.off = bars.start_off;
     w.left = bars.start_i < 0 ? 0 : run_hi - run_lo;
-    if (w.left > 0) w.x = open_prefix(p, w.i, ROWS);
+    w.unit = run_lo;
+    if (w.left > 0) w.x = open_prefix(p.list, w.i, p.err);
 
     if (warp < 8) {
         // ---- scores to probabilities, products to outputs: a thread has a row
@@ -358,79 +432,44 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         unsigned tiles_before = 0;  // of the run, by loader's count (scales)
         bool ok = true;
         uint32_t q_phase = 1;  // (the phase before the first counts as done)
-        while (ok && w.next(p, ROWS)) {
-            // where this row's part goes (-1: the item has no such row)
-            int seq, head;
-            const bool real = row_of(p, w, (int64_t)w.tile * ROWS + (NQ == 2 ? g * kTileRows : 0) + r, seq, head);
-            int64_t part_at = -1;
-            if (real) {
+        while (ok && w.next(p)) {
+            // this row: where its q lies and its part goes (-1: the item has no such row)
+            const int row = w.tile * ROWS + (NQ == 2 ? g * kTileRows : 0) + r;
+            int64_t part_at = -1, q_at = -1;
+            if (row < (int64_t)w.x.count * p.group) {
+                const int seq = w.x.first + row / p.group, head = w.kvh * p.group + row % p.group;
                 const int64_t first = (int64_t)seq * p.hq + head;
+                q_at = (int64_t)seq * p.qs + (int64_t)head * p.qhs;
                 part_at = w.from == 0 ? (NQ == 2 ? first : 2 * first + g)
                                       : (NQ == 2 ? 1 : 2) * (int64_t)p.n_seqs * p.hq + (int64_t)blockIdx.x * 256 + g * kTileRows + r;
                 if (!LEAN_IN(part_at, p.parts, p.err)) part_at = -1;
+                if (w.from == 0 && (NQ == 2 || g == 0) && LEAN_IN(first, (int64_t)p.n_seqs * p.hq, p.err)) {
+                    p.first[first] = make_int2(blockIdx.x, (int)(runs.of(w.begin + w.x.keys - 1) - blockIdx.x) + 1);
+                }
             }
-            // q of this row, scaled by a power of two, in parts
+            // q of this warp's rows; the scale of this one's scores
             float zs;
             {
-                float f[DP];
-                const int64_t at = real ? (int64_t)seq * p.qs + (int64_t)head * p.qhs : 0;
-                float top = 0.f;
-#pragma unroll
-                for (int d = 0; d < DP; d += 8) {
-                    const bool in = real && d < p.dim && LEAN_SPAN(at + d, 8, p.q_extent, p.err);
-                    if (QP == 3 && p.act == LEAN_F32) {
-                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-                        if (in) {
-                            a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at + d);
-                            b = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at + d + 4);
-                        }
-                        f[d] = a.x; f[d + 1] = a.y; f[d + 2] = a.z; f[d + 3] = a.w;
-                        f[d + 4] = b.x; f[d + 5] = b.y; f[d + 6] = b.z; f[d + 7] = b.w;
-                    } else {
-                        uint4 a = make_uint4(0, 0, 0, 0);
-                        if (in) a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at + d);
-                        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            RawPair<false> pair;
-                            pair.v = u[i];
-                            const float2 v = pair.get(p.act);
-                            f[d + 2 * i] = v.x;
-                            f[d + 2 * i + 1] = v.y;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[d + i]));
+                const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;  // (so that the largest product is the largest score)
+                auto ready = [&]() { return warp_wait(bars, &bars.q_free, q_phase, p.err); };
+                uint8_t *const tiles = q_tiles + (NQ == 2 ? g * QP * S::kTileBytes : 0);
+                auto turn = [&](int it) { return NQ == 2 || it % 2 == g; };  // (both groups have the same rows: half each)
+                const int row0 = r - lane;
+                zs = fabsf(p.scale_log2);
+                if (QP == 1 && p.act == (BF16 ? LEAN_BF16 : LEAN_F16)) {  // the operands' own type: nothing to split or scale
+                    ok = copy_q<S, DP>(p, q_at, tiles, row0, lane, sign < 0.f ? 0x80008000u : 0u, turn, ready);
+                } else {
+                    const uint32_t top = QP == 3 && p.act == LEAN_F32
+                                             ? load_q<S, T, DP, QP, 4>(p, q_at, tiles, row0, lane, sign, turn, ready)
+                                             : load_q<S, T, DP, QP, 8>(p, q_at, tiles, row0, lane, sign, turn, ready);
+                    ok = top != 0xffffffffu;
+                    const int e = (int)(top >> 23 & 0xff);
+                    const int fe = e == 0 || e == 255 ? 127 : min(253, max(1, 254 + PartRange<T>::kLiftQ - e));
+                    zs *= __uint_as_float((uint32_t)(254 - fe) << 23);
                 }
-                const int e = (int)(__float_as_uint(top) >> 23);
-                const int fe = e == 0 || e == 255 ? 127 : min(253, max(1, 254 + PartRange<T>::kLiftQ - e));
-                float up = __uint_as_float((uint32_t)fe << 23);
-                zs = p.scale_log2 * __uint_as_float((uint32_t)(254 - fe) << 23);
-                if (zs < 0.f) {  // so that the largest product is the largest score
-                    zs = -zs;
-                    up = -up;
-                }
-                if (zs == 0.f) zs = 1.17549435e-38f;  // (masked scores are -inf times this)
-                ok = warp_wait(bars, &bars.q_free, q_phase, p.err);
                 if (!ok) break;
                 q_phase ^= 1;
-#pragma unroll
-                for (int d = 0; d < DP; d += 8) {
-                    // (with one tile of rows each group writes half of it)
-                    if (NQ == 1 && (DP == 128 ? d / 64 : d / 32) != g) continue;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[d + i] *= up;
-#pragma unroll
-                    for (int part = 0; part < QP; ++part) {
-                        uint4 a;
-                        a.x = take_part<T>(f[d], f[d + 1]);
-                        a.y = take_part<T>(f[d + 2], f[d + 3]);
-                        a.z = take_part<T>(f[d + 4], f[d + 5]);
-                        a.w = take_part<T>(f[d + 6], f[d + 7]);
-                        *reinterpret_cast<uint4 *>(q_tiles + ((NQ == 2 ? g : 0) * QP + part) * S::kTileBytes +
-                                                   d / 64 * S::kChunkBytes + r * 128 + ((d / 8 % 8) ^ (r & 7)) * 16) = a;
-                    }
-                }
+                if (zs == 0.f) zs = 1.17549435e-38f;  // (masked scores are -inf times this)
                 smem_to_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.q_full);
@@ -438,25 +477,29 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             constexpr float kLog2Lift = PartRange<T>::kLift == 1.f ? 0.f : 13.f, kDown = 1.f / PartRange<T>::kLift;
             float m = -CUDART_INF_F, l = 0.f;
             int v_ref = 1;
-            // What a tile's largest score and scales make of the references: m, v_ref; what is multiplied with the sums
-            // and the outputs so far, added to the exponents, and multiplied with the sum of p.
-            float fall, o_fall, shift, back;
-            auto refer = [&](float top, unsigned slot) {
+            // What a half's largest score and scales make of the references m and v_ref: what is multiplied with the sums
+            // and the outputs so far, added to the exponents of 32 keys, and multiplied with the sum of their p.
+            float fall, o_fall, shift[2], back[2];
+            auto refer = [&](float top, const int *exps) {
                 // (m as in attend.cuh: within kSlack of the largest score so far)
                 const float mn = top - m <= PartRange<T>::kSlack ? m : top;
                 const float ms = mn == -CUDART_INF_F ? 0.f : mn;
                 fall = o_fall = ex2(m - ms);
                 bool moved = !(mn == m);
                 m = mn;
-                shift = kLog2Lift - ms;
-                back = 1.f;
+                shift[0] = shift[1] = kLog2Lift - ms;
+                back[0] = back[1] = 1.f;
                 if (IN8) {
-                    // values' scales lie in 0.5..1 times 2^(exponent of the tile's largest - 126); sums are relative to
+                    // values' scales lie in 0.5..1 times 2^(exponent of the largest of 32 - 126); sums are relative to
                     // 2^(v_ref - 126); what is below 2^-60 of the largest may count as 2^-60 of it
-                    const int e = bars.tile_exp[slot], now = max(v_ref, e), below = min(now - e, 60);
+                    const int now = max(v_ref, max(exps[0], exps[1]));
                     o_fall *= __uint_as_float((uint32_t)max(0, 127 + v_ref - now) << 23);
-                    shift -= (float)below;
-                    back = __uint_as_float((uint32_t)(127 + below) << 23);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int below = min(now - exps[c], 60);
+                        shift[c] -= (float)below;
+                        back[c] = __uint_as_float((uint32_t)(127 + below) << 23);
+                    }
                     moved = moved || now != v_ref;
                     v_ref = now;
                 }
@@ -465,13 +508,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             auto size = [&]() { return IN8 ? kDown * __uint_as_float((uint32_t)(v_ref + 1) << 23) : kDown; };
             // Halves of tiles in turn (of the last one the second may have no keys; keys that are not there score -inf).
             int t = w.from + (NQ == 2 ? 0 : g), half = 0, limit = 0;  // limit: keys of the half that are there, or more
-            unsigned n = 0, slot = 0;
             uint32_t s_at = 0;
             const float *ks = nullptr, *vs = nullptr;
+            const int *exps = nullptr;
             auto scores_wait = [&]() {
                 limit = w.x.len - t * kTileKeys - half * kHalfKeys;
-                n = tiles_before + (t - w.from);
-                slot = n % 4;
+                const unsigned n = tiles_before + (t - w.from), slot = n % 4;
+                exps = bars.value_exp[slot] + 2 * half;
                 ks = scales + slot * 2 * kTileKeys + half * kHalfKeys;
                 vs = ks + kTileKeys;
                 s_at = s_group + done % NB * S::kWidth;
@@ -531,17 +574,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                     float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
                     for (int i = 0; i < kHalfKeys; ++i) tops[i % 4] = fmaxf(tops[i % 4], __uint_as_float(x[i / 32][i % 32]));
-                    const bool moved = refer(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * zs, slot);
-                    const f32x2 zs2 = pack2(zs, zs), shift2 = pack2(shift, shift);
-                    f32x2 sum2[2] = {0, 0};
+                    const bool moved = refer(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * zs, exps);
+                    const f32x2 zs2 = pack2(zs, zs);
+                    f32x2 sum2[2] = {0, 0};  // of the first 32 keys and of the others
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t part[16];
+                        const f32x2 shift2 = pack2(shift[c], shift[c]);
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             const float2 a = unpack2(fma2(pack2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), zs2, shift2));
                             float2 e = make_float2(ex2(a.x), ex2(a.y));
-                            sum2[i / 2 % 2] = add2(sum2[i / 2 % 2], pack2(e.x, e.y));
+                            sum2[c] = add2(sum2[c], pack2(e.x, e.y));
                             if (IN8) e = unpack2(mul2(pack2(e.x, e.y), *reinterpret_cast<const f32x2 *>(vs + 32 * c + i)));
                             part[i / 2] = take_part<T>(e.x, e.y);
                         }
@@ -565,8 +609,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                         }
                     }
                     publish();
-                    const float2 sum = unpack2(add2(sum2[0], sum2[1]));
-                    l = fmaf(l, fall, (sum.x + sum.y) * back);
+                    const float2 sum0 = unpack2(sum2[0]), sum1 = unpack2(sum2[1]);
+                    l = fmaf(l, fall, (sum0.x + sum0.y) * back[0] + (sum1.x + sum1.y) * back[1]);
                     advance_half();
                     if (++in_sum == kFoldHalves || t >= w.to) {
                         ok = products_wait();
@@ -640,22 +684,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                             tops[i % 4] = fmaxf(tops[i % 4], z);
                         }
                     }
-                    refer(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * zs, slot);
-                    const f32x2 zs2 = pack2(zs, zs), shift2 = pack2(shift, shift);
-                    f32x2 sum2[2] = {0, 0};
+                    refer(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * zs, exps);
+                    const f32x2 zs2 = pack2(zs, zs);
+                    f32x2 sum2[2] = {0, 0};  // of the first 32 keys and of the others
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t x[32];
                         tm_ld32(s_at + 32 * c, x);
                         tm_wait_ld(x);
                         uint32_t part[PP][16];
+                        const f32x2 shift2 = pack2(shift[c], shift[c]);
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
                             f32x2 z = pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                             if (IN8) z = mul2(z, *reinterpret_cast<const f32x2 *>(ks + 32 * c + i));
                             const float2 a = unpack2(fma2(z, zs2, shift2));
                             float2 e = make_float2(ex2(a.x), ex2(a.y));
-                            sum2[i / 2 % 2] = add2(sum2[i / 2 % 2], pack2(e.x, e.y));
+                            sum2[c] = add2(sum2[c], pack2(e.x, e.y));
                             if (IN8) e = unpack2(mul2(pack2(e.x, e.y), *reinterpret_cast<const f32x2 *>(vs + 32 * c + i)));
 #pragma unroll
                             for (int k = 0; k < PP; ++k) part[k][i / 2] = take_part<T>(e.x, e.y);
@@ -664,8 +709,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                         for (int k = 0; k < PP; ++k) tm_st16(s_at + S::part(c, k), part[k]);  // over scores already used
                     }
                     publish();
-                    const float2 sum = unpack2(add2(sum2[0], sum2[1]));
-                    l = fmaf(l, fall, (sum.x + sum.y) * back);
+                    const float2 sum0 = unpack2(sum2[0]), sum1 = unpack2(sum2[1]);
+                    l = fmaf(l, fall, (sum0.x + sum0.y) * back[0] + (sum1.x + sum1.y) * back[1]);
                     ok = products_wait();
                     if (!ok) break;
                     const f32x2 fall2 = pack2(o_fall, o_fall);
@@ -726,20 +771,72 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             if (lane == 0) mbar_arrive(bar);
         };
         if constexpr (IN8) {
-            // A thread looks up a key's row and scales, then takes 16-byte pieces of all rows through registers, where
-            // they become f16: the pieces of the next tile are under way while this one's are converted.
+            // A thread takes 16-byte pieces of all rows through registers, where they become f16: the pieces of the next
+            // tile are under way while this one's are converted.  Where rows lie: a lane looks up the page of a box of
+            // rows; pages that boxes do not fit are looked up row by row, through shared memory.
             constexpr int PR = DP / 16;  // pieces of a row
+            const int box = maps.box, boxes = box > 0 ? kTileKeys / box : 0, lg = box > 0 ? 31 - __clz(box) : 0;
             uint4 xk[PR], xv[PR];
-            float sk = 1.f, sv = 0.f;
-            auto load = [&](const void *cache, unsigned tile, uint4 (&x)[PR]) {
-                const int64_t *off = row_off + (tile & 1) * kTileKeys;
+            float sk, sv;
+            int64_t at_rows = -1, at_scales = -1;  // of a tile: the lane's box's rows and scales, or the thread's row's
+            auto mine = [&](int kt) { return kt * kTileKeys + (boxes > 0 ? lane * box : t); };
+            auto ahead = [&](int kt) { return boxes > 0 && lane >= boxes ? 0 : page_of(mine(kt)); };
+            unsigned looked = 0;  // tiles looked up so far
+            auto look = [&](int kt, int id) {
+                if (boxes > 0 && lane >= boxes) return;
+                const int tok = mine(kt);
+                at_rows = place_of(tok, id);
+                at_scales = at_rows < 0 ? -1 : (int64_t)id * p.scale_page + (int64_t)(tok % p.page) * p.scale_place + (int64_t)w.kvh * p.scale_hs;
+            };
+            auto share = [&]() {  // rows of a tile that are looked up one by one
+                if (boxes > 0) return true;
+                row_off[(looked & 1) * kTileKeys + t] = at_rows;
+                arrive(&bars.rows_full[looked & 1]);
+                const bool got = warp_wait(bars, &bars.rows_full[looked & 1], looked / 2 & 1, p.err);
+                ++looked;
+                return got;
+            };
+            auto load = [&](const void *cache, int kt, uint4 (&x)[PR]) {
+                const int64_t *off = row_off + ((looked - 1) & 1) * kTileKeys;
 #pragma unroll
                 for (int i = 0; i < PR; ++i) {
-                    const int c = t % PR;
-                    const int64_t o = off[(i * kTileKeys + t) / PR];
+                    const int row = (i * kTileKeys + t) / PR, c = t % PR;
+                    int64_t o;
+                    if (boxes > 0) {
+                        o = __shfl_sync(0xffffffffu, at_rows, row >> lg);
+                        if (o >= 0) o += (row & (box - 1)) * p.place_stride;
+                        if (kt * kTileKeys + row >= w.x.len) o = -1;
+                    } else {
+                        o = off[row];
+                    }
                     x[i] = make_uint4(0, 0, 0, 0);
-                    if (o >= 0 && 16 * c < p.dim) x[i] = *reinterpret_cast<const uint4 *>(static_cast<const int8_t *>(cache) + o + 16 * c);
+                    if (o >= 0 && 16 * c < p.dim && LEAN_SPAN(o + 16 * c, 16, p.cache_extent, p.err))
+                        x[i] = *reinterpret_cast<const uint4 *>(static_cast<const int8_t *>(cache) + o + 16 * c);
                 }
+            };
+            auto load_scales = [&](int kt) {  // of row t
+                int64_t o = at_rows, at = at_scales;
+                if (boxes > 0) {
+                    o = __shfl_sync(0xffffffffu, at_rows, t >> lg);
+                    at = __shfl_sync(0xffffffffu, at_scales, t >> lg) + (t & (box - 1)) * p.scale_place;
+                }
+                sk = o == -2 ? CUDART_NAN_F : 1.f;
+                sv = 0.f;
+                if (o >= 0 && kt * kTileKeys + t < w.x.len && LEAN_IN(at, p.scale_extent, p.err)) {
+                    sk = p.k_scales[at];
+                    sv = p.v_scales[at];
+                }
+            };
+            auto finish_scales = [&](unsigned m) {  // the values' relative to the largest of the warp's 32
+                float top = fmaxf(sv, 0.f);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int e = min(252, max(1, (int)(__float_as_uint(top) >> 23)));
+                float *to = scales + m % 4 * 2 * kTileKeys + t;
+                to[0] = sk + (sk - sk);  // (an infinite one is NaN, as the scores of such a key are)
+                to[kTileKeys] = sv * __uint_as_float((uint32_t)(253 - e) << 23);
+                if (lane == 0) bars.value_exp[m % 4][warp - 8] = e;
+                arrive(&bars.scales_full[m % 4]);
             };
             auto convert = [&](uint8_t *tile, const uint4 (&x)[PR]) {
 #pragma unroll
@@ -754,70 +851,38 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                 }
                 smem_to_async();
             };
-            // the rows of tile number m of the run, at kt of its prefix, whose pages are known; scales under way
-            auto rows = [&](unsigned m, int kt, int id) {
-                const int tok = kt * kTileKeys + t;
-                const int64_t off = place_of(tok, id);
-                row_off[(m & 1) * kTileKeys + t] = off;
-                sk = off == -2 ? CUDART_NAN_F : 1.f;
-                sv = 0.f;
-                if (off >= 0) {
-                    const int64_t at = (int64_t)id * p.scale_page + (int64_t)(tok % p.page) * p.scale_place + (int64_t)w.kvh * p.scale_hs;
-                    if (LEAN_IN(at, p.scale_extent, p.err)) {
-                        sk = p.k_scales[at];
-                        sv = p.v_scales[at];
-                    }
-                }
-                arrive(&bars.rows_full[m & 1]);
-            };
-            auto wait_rows = [&](unsigned m) { return warp_wait(bars, &bars.rows_full[m & 1], m / 2 & 1, p.err); };
-            auto finish_scales = [&](unsigned m) {  // relative to the tile's largest
-                float top = fmaxf(sv, 0.f);
-#pragma unroll
-                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                if (lane == 0) bars.warp_top[m & 1][warp - 8] = top;
-                arrive(&bars.tops_full[m & 1]);
-                if (!warp_wait(bars, &bars.tops_full[m & 1], m / 2 & 1, p.err)) return false;
-                const float *tops = bars.warp_top[m & 1];
-                top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                const int e = min(252, max(1, (int)(__float_as_uint(top) >> 23)));
-                float *to = scales + m % 4 * 2 * kTileKeys + t;
-                to[0] = sk + (sk - sk);  // (an infinite one is NaN, as the scores of such a key are)
-                to[kTileKeys] = sv * __uint_as_float((uint32_t)(253 - e) << 23);
-                if (t == 0) bars.tile_exp[m % 4] = e;
-                arrive(&bars.scales_full[m % 4]);
-                return true;
-            };
-            while (ok && w.next(p, ROWS)) {
-                rows(n, w.from, page_of(w.from * kTileKeys + t));
-                int next_id = w.from + 1 < w.to ? page_of((w.from + 1) * kTileKeys + t) : 0;
-                ok = wait_rows(n);
+            while (ok && w.next(p)) {
+                look(w.from, ahead(w.from));
+                int next_id = w.from + 1 < w.to ? ahead(w.from + 1) : 0;
+                ok = share();
                 if (!ok) break;
-                load(p.k, n, xk);
-                load(p.v, n, xv);
-                ok = finish_scales(n);
+                load(p.k, w.from, xk);
+                load_scales(w.from);
+                load(p.v, w.from, xv);
+                finish_scales(n);
                 for (int kt = w.from; ok && kt < w.to; ++kt, ++n) {
                     const bool more = kt + 1 < w.to;
                     if (more) {
-                        rows(n + 1, kt + 1, next_id);
-                        if (kt + 2 < w.to) next_id = page_of((kt + 2) * kTileKeys + t);
+                        look(kt + 1, next_id);
+                        if (kt + 2 < w.to) next_id = ahead(kt + 2);
                     }
                     if (n >= KS) ok = warp_wait(bars, &bars.k_empty[n % KS], (n / KS - 1) & 1, p.err);
                     if (!ok) break;
                     convert(k_tiles + n % KS * S::kTileBytes, xk);
                     arrive(&bars.k_full[n % KS]);
                     if (more) {
-                        ok = wait_rows(n + 1);
+                        ok = share();
                         if (!ok) break;
-                        load(p.k, n + 1, xk);
+                        load(p.k, kt + 1, xk);
+                        load_scales(kt + 1);
                     }
                     if (n >= VS) ok = warp_wait(bars, &bars.v_empty[n % VS], (n / VS - 1) & 1, p.err);
                     if (!ok) break;
                     convert(v_tiles + n % VS * S::kTileBytes, xv);
                     arrive(&bars.v_full[n % VS]);
                     if (more) {
-                        load(p.v, n + 1, xv);
-                        ok = finish_scales(n + 1);
+                        load(p.v, kt + 1, xv);
+                        finish_scales(n + 1);
                     }
                 }
             }
@@ -859,7 +924,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             auto mine = [&](int kt) { return kt * kTileKeys + (boxes > 0 ? lane * maps.box : t); };
             auto ahead = [&](int kt) { return boxes > 0 && lane >= boxes ? 0 : page_of(mine(kt)); };
             unsigned rows_n = 0;  // tiles taken row by row so far
-            while (ok && w.next(p, ROWS)) {
+            while (ok && w.next(p)) {
                 int next_id = ahead(w.from);
                 for (int kt = w.from; ok && kt < w.to; ++kt, ++n) {
                     const int tok = mine(kt);
@@ -924,7 +989,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                 const int steps = (p.dim + 15) / 16;
                 uint32_t q_phase = 0;
                 unsigned u = 0;  // half tiles of this group
-                while (ok && w.next(p, ROWS)) {
+                while (ok && w.next(p)) {
                     ok = phase_wait(bars, &bars.q_full, q_phase, p.err);
                     q_phase ^= 1;
                     const unsigned tiles = w.to - w.from;
@@ -962,7 +1027,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                 const uint32_t idesc = tile_idesc(BF16, DP, true);
                 const uint32_t v_lower = tile_lower(smem_addr(v_tiles), S::kChunkBytes);
                 unsigned u0 = 0, u1 = 0;  // half tiles of this group, or of both
-                while (ok && w.next(p, ROWS) && !(ALL && g == 1)) {
+                while (ok && w.next(p) && !(ALL && g == 1)) {
                     const unsigned tiles = w.to - w.from;
                     unsigned in_sum = 0;
                     for (unsigned t = NQ == 2 || ALL ? 0 : g; ok && t < tiles; t += NQ == 2 || ALL ? 1 : 2) {
@@ -1005,22 +1070,34 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     tm_before();
     __syncthreads();
     if (warp == 12) tm_free(tmem, 512);
+    pdl_wait();
 }
 
 // Parts of a row, and the sequence's own tokens, added up: a warp to a row.
 template <int DP, int NQ>
-__global__ void __launch_bounds__(256) prefix_sum_kernel(const PrefixArgs p, unsigned blocks) {
-    constexpr int V = DP / 32, ROWS = NQ * kTileRows, HALVES = NQ == 2 ? 1 : 2, U = 8;
+__global__ void __launch_bounds__(256) prefix_sum_kernel(const PrefixArgs p) {
+    constexpr int V = DP / 32, ROWS = NQ * kTileRows, HALVES = NQ == 2 ? 1 : 2, U = 16;
     step_begin();
     const int lane = threadIdx.x % 32;
     const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
     if (row >= (int64_t)p.n_seqs * p.hq) return;
     const int seq = (int)(row / p.hq), head = (int)(row % p.hq);
+    // asked for at once: the row's own result, and where its parts lie if it has a prefix
+    const float own = p.own_lse[row] * 1.4426950408889634f;
+    Vec<float, V> own_out = {};
+    if (lane * V < p.dim) own_out = load_vec<float, V>(p.own_out + row * p.dim + lane * V);
+    const int2 where = p.first[row];
+    Shared shared[kAttMaxCtas / 32];
+#pragma unroll
+    for (int i = 0; i < kAttMaxCtas / 32; ++i) {
+        const int b = 32 * i + lane;
+        shared[i] = b < p.own_grid && LEAN_IN(b, kAttMaxCtas, p.err) ? p.shared[b] : Shared{-1, 0};
+    }
     // its prefix: the last that begins at it or before
     int lo = 0, hi = p.n_prefixes;  // how many begin so: lo..hi
     while (lo < hi) {
         const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const bool so = at < hi && LEAN_IN(at, p.n_prefixes + 1, p.err) && p.starts[at] <= seq;
+        const bool so = at < hi && LEAN_IN(at, p.n_prefixes + 1, p.err) && p.list.starts[at] <= seq;
         const int n = __popc(__ballot_sync(0xffffffffu, so));
         if (n == 0) break;
         hi = min(hi, lo + n * step);
@@ -1029,32 +1106,73 @@ __global__ void __launch_bounds__(256) prefix_sum_kernel(const PrefixArgs p, uns
     int parts = 0;
     int64_t more = 0;  // the first part that goes on
     if (lo > 0) {
-        const Prefix x = open_prefix(p, lo - 1, ROWS);
+        const Prefix x = open_prefix(p.list, lo - 1, p.err);
         if (seq >= x.first && seq < x.first + x.count && x.keys > 0) {
-            const int64_t r = (int64_t)(seq - x.first) * p.group + head % p.group;
-            const int tile = (int)(r / ROWS), in = (int)(r % ROWS);
-            const Runs runs(p.plan[p.n_prefixes], blocks);
-            const unsigned long long at = p.plan[lo - 1] + ((unsigned long long)(head / p.group) * x.tiles + tile) * (x.keys + kItemTiles);
-            const unsigned first = runs.of(at), last = runs.of(at + x.keys - 1);
-            parts = (int)(last - first + 1) * HALVES;
-            more = (int64_t)HALVES * p.n_seqs * p.hq + (int64_t)(first + 1) * 256 + in;
+            const int r = ((seq - x.first) * p.group + head % p.group) % ROWS;
+            // (bounds: where seq_starts does not ascend, another prefix's block may have written it, or none)
+            parts = min(max(where.y, 0), kPrefixMaxCtas) * HALVES;
+            more = (int64_t)HALVES * p.n_seqs * p.hq + (int64_t)(min(max(where.x, 0), kPrefixMaxCtas) + 1) * 256 + r;
+        }
+    }
+    // its own item's parts, if blocks share it (attend.cuh): of the block where it begins, and of the next ones
+    const int item = (seq * p.hkv + head / p.group) * p.own_tiles + head % p.group / p.own_heads;
+    int own_parts = 0, own_block = 0;
+#pragma unroll
+    for (int i = 0; i < kAttMaxCtas / 32; ++i) {
+        const unsigned hit = __ballot_sync(0xffffffffu, shared[i].item == item);
+        if (hit) {
+            own_block = 32 * i + __ffs(hit) - 1;
+            own_parts = __shfl_sync(0xffffffffu, shared[i].parts, __ffs(hit) - 1);
         }
     }
     float top = -CUDART_INF_F, sum = 0.f, o[V] = {};
+    auto rescale = [&](float m) {  // to a reference not below m; what it is
+        const float now = fmaxf(m, top), ref = now == -CUDART_INF_F ? 0.f : now, old = ex2(top - ref);
+        top = now;
+        sum *= old;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] *= old;
+        return ref;
+    };
+    if (own_parts > 0) {
+        const int pf = part_floats(p.own_heads, DP), po = DP + 4;
+        for (int k0 = 0; k0 < own_parts; k0 += 8) {
+            float2 ml[8];
+            Vec<float, V> x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int64_t at = ((int64_t)(own_block + k0 + k) * 2 + (k0 + k == 0)) * pf + (int64_t)(head % p.group % p.own_heads) * po;
+                ml[k] = make_float2(-CUDART_INF_F, 0.f);
+                x[k] = Vec<float, V>{};
+                if (k0 + k < own_parts && LEAN_SPAN(at, po, p.part_extent, p.err)) {
+                    ml[k] = *reinterpret_cast<const float2 *>(p.cta_parts + at);
+                    x[k] = load_vec<float, V>(p.cta_parts + at + 4 + lane * V);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float w = ex2(ml[k].x - rescale(ml[k].x));
+                sum = fmaf(w, ml[k].y, sum);
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = fmaf(w, x[k].v[i], o[i]);
+            }
+        }
+    } else if (own != -CUDART_INF_F) {  // (its sum is 1)
+        const float w = ex2(own - rescale(own));
+        sum = w;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = w * own_out.v[i];
+    }
     for (int k0 = 0; k0 < parts; k0 += 32) {
         const int k = k0 + lane, n = min(32, parts - k0);
         const int64_t at = k < HALVES ? HALVES * row + k : more + (int64_t)(k / HALVES - 1) * 256 + k % HALVES * kTileRows;
         float2 ml = make_float2(-CUDART_INF_F, 0.f);
-        if (k < parts && LEAN_IN(at, p.parts, p.err)) ml = p.ml[at];
+        if (k < parts && at < p.parts) ml = p.ml[at];
         float now = ml.x;
 #pragma unroll
         for (int i = 16; i; i >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, i));
-        now = fmaxf(now, top);
-        const float ref = now == -CUDART_INF_F ? 0.f : now, old = ex2(top - ref), mine = ex2(ml.x - ref);
-        top = now;
-        sum = fmaf(sum, old, warp_sum(mine * ml.y));
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] *= old;
+        const float mine = ex2(ml.x - rescale(now));
+        sum += warp_sum(mine * ml.y);
         for (int j0 = 0; j0 < n; j0 += U) {
             Vec<float, V> x[U];
             float f[U];
@@ -1065,23 +1183,13 @@ __global__ void __launch_bounds__(256) prefix_sum_kernel(const PrefixArgs p, uns
                 x[j] = Vec<float, V>{};
                 if (j0 + j >= n) f[j] = 0.f;
                 // (a part without keys has no outputs: they are not looked at)
-                if (f[j] != 0.f && LEAN_IN(from, p.parts, p.err)) x[j] = load_vec<float, V>(p.o + from * DP + lane * V);
+                if (f[j] != 0.f && from < p.parts) x[j] = load_vec<float, V>(p.o + from * DP + lane * V);
             }
 #pragma unroll
             for (int j = 0; j < U; ++j)
 #pragma unroll
                 for (int i = 0; i < V; ++i) o[i] = fmaf(f[j], x[j].v[i], o[i]);
         }
-    }
-    const float own = p.own_lse[row] * 1.4426950408889634f;
-    if (own != -CUDART_INF_F) {  // (its sum is 1)
-        const float now = fmaxf(own, top), ref = now == -CUDART_INF_F ? 0.f : now, old = ex2(top - ref), mine = ex2(own - ref);
-        top = now;
-        sum = fmaf(sum, old, mine);
-        Vec<float, V> x = {};
-        if (lane * V < p.dim) x = load_vec<float, V>(p.own_out + row * p.dim + lane * V);
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = fmaf(mine, x.v[i], o[i] * old);
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
