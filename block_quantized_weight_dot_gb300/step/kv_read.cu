@@ -1,9 +1,12 @@
 // kv_read.cu -- lean_kv_read: tokens of the paged cache as contiguous rows.
 //
 // Values are c * s (caches in 8 bits) or the cache's own.  Every byte moves once,
-// so HBM bounds the call.  A thread writes 16 bytes of a row at a time (V
-// elements) and reads the V elements they come from; consecutive threads follow a
-// token's row through its heads, U pieces of a thread are under way at once.
+// so HBM bounds the call.  A thread has one piece of a token's row, V elements,
+// which are 16 bytes of the output, for all tokens of its block: addresses then
+// only step by the tokens' places, which the block looks up once, in shared memory.
+// U tokens' keys and values of a thread are under way at once.  (Pieces numbered
+// through, each with its own divisions and its own slot: 292 us in place of XX at
+// 131072 tokens of 8 heads of 128 in 8 bits to bf16.)
 #include "../../include/lean_cache.h"
 #include "step_common.cuh"
 
@@ -12,6 +15,7 @@ using namespace lean;
 namespace {
 
 constexpr int kReadThreads = 256;
+constexpr int kReadTokens = 256;  // of a block, at most
 
 struct ReadArgs {
     const void *k, *v;
@@ -26,57 +30,100 @@ struct ReadArgs {
     unsigned *err;
 };
 
-template <typename C>
-__device__ __forceinline__ float cached(C v) { return to_f(v); }
-template <>
-__device__ __forceinline__ float cached(int8_t v) {  // exact: 2^23 + (c + 128) has c + 128 in its low bits
-    return __uint_as_float(0x4b000000u | ((uint32_t)(uint8_t)v ^ 0x80u)) - 8388736.f;
-}
+// V elements of a cache as they lie there, and as fp32.
+template <typename C, int V>
+struct alignas(sizeof(C) * V >= 16 ? 16 : sizeof(C) * V) Cached {
+    C v[V];
+    __device__ __forceinline__ void values(float, float *f) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = to_f(v[i]);
+    }
+};
+template <int V>
+struct alignas(V) Cached<int8_t, V> {  // c * s: 2^23 + (c + 128) has c + 128 in its low bits, and the difference is exact
+    int8_t v[V];
+    __device__ __forceinline__ void values(float s, float *f) const {
+        if constexpr (V == 1) {
+            f[0] = (float)v[0] * s;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const uint32_t u = reinterpret_cast<const uint32_t *>(v)[i] ^ 0x80808080u;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[4 * i + k] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + k)) - 8388736.f) * s;
+            }
+        }
+    }
+};
 
-// C: of the cache, A: of the output.  Blocks of gridDim.y = 1 read values, of 0 keys (or the one there is).
+// C: of the cache, A: of the output.
 template <typename C, typename A, int V>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs p) {
     constexpr int U = 4;
     constexpr bool IN8 = sizeof(C) == 1;
+    __shared__ int64_t place[kReadTokens], scale_place[kReadTokens];  // -1: zeros, -2: NaN
     step_begin();
-    const bool is_k = p.k && blockIdx.y == 0;
-    const C *cache = static_cast<const C *>(is_k ? p.k : p.v);
-    const float *scales = is_k ? p.k_scales : p.v_scales;
-    A *out = static_cast<A *>(is_k ? p.k_out : p.v_out);
-    const int64_t os = is_k ? p.kos : p.vos, ohs = is_k ? p.kohs : p.vohs, out_end = is_k ? p.k_end : p.v_end;
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
-    const int nt = (int)min((int64_t)p.tokens, p.n_tokens - t0), n = nt * p.row;
-    for (int i0 = threadIdx.x; i0 < n; i0 += U * kReadThreads) {
-        Vec<C, V> x[U];
-        float s[U];
-        int64_t to[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * kReadThreads;
-            s[u] = 1.f;
-            x[u] = Vec<C, V>{};
-            if (i >= n) continue;
-            const int t = i / p.row, j = i - t * p.row, head = j / p.pieces, d = (j - head * p.pieces) * V;
-            to[u] = (t0 + t) * os + head * ohs + d;
-            const int32_t slot = LEAN_IN(t0 + t, p.n_tokens, p.err) ? p.slots[t0 + t] : -1;
-            if (slot >= p.n_slots) {
-                s[u] = CUDART_NAN_F;
-                if (j == 0) atomicOr(p.err, kErrSlot);
-            } else if (slot >= 0) {
-                const int64_t page = slot / p.page, place = slot - (int)page * p.page;
-                const int64_t at = page * p.page_stride + place * p.place_stride + head * p.cache_hs + d;
-                if (LEAN_SPAN(at, V, p.cache_end, p.err)) x[u] = load_vec<C, V>(cache + at);
-                const int64_t at_s = page * p.scale_page + place * p.scale_place + head * p.scale_hs;
-                if (IN8 && LEAN_IN(at_s, p.scale_end, p.err)) s[u] = scales[at_s];
-            }
+    const int nt = (int)min((int64_t)p.tokens, p.n_tokens - t0);
+    for (int t = threadIdx.x; t < nt; t += kReadThreads) {
+        const int32_t slot = LEAN_IN(t0 + t, p.n_tokens, p.err) ? p.slots[t0 + t] : -1;
+        int64_t at = -1, at_scale = 0;
+        if (slot >= p.n_slots) {
+            at = -2;
+            atomicOr(p.err, kErrSlot);
+        } else if (slot >= 0) {
+            const int page = slot / p.page, in = slot - page * p.page;
+            at = page * p.page_stride + in * p.place_stride;
+            at_scale = page * p.scale_page + in * p.scale_place;
         }
+        place[t] = at;
+        scale_place[t] = at_scale;
+    }
+    __syncthreads();
+    // tokens side by side, where a token has few pieces
+    const int sub = max(1, kReadThreads / p.row), first = p.row <= kReadThreads ? (int)threadIdx.x / p.row : 0;
+    if (first >= sub) return;
+    for (int j = p.row <= kReadThreads ? (int)threadIdx.x - first * p.row : threadIdx.x; j < p.row; j += kReadThreads) {
+        const int head = j / p.pieces, d = (j - head * p.pieces) * V;
+        const int64_t in_row = head * p.cache_hs + d, in_scales = head * p.scale_hs;
+        for (int t1 = first; t1 < nt; t1 += U * sub) {
+            Cached<C, V> x[2][U];
+            float s[2][U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u * kReadThreads >= n) break;
-            float f[V];
+            for (int u = 0; u < U; ++u) {
+                const int t = t1 + u * sub;
+                const int64_t at = t < nt ? place[t] : -1;
+                const int64_t at_scale = IN8 && t < nt ? scale_place[t] + in_scales : 0;
 #pragma unroll
-            for (int e = 0; e < V; ++e) f[e] = cached(x[u].v[e]) * s[u];
-            if (LEAN_SPAN(to[u], V, out_end, p.err)) store_vec<A, V>(out + to[u], f);
+                for (int i = 0; i < 2; ++i) {
+                    const C *cache = static_cast<const C *>(i ? p.v : p.k);
+                    x[i][u] = Cached<C, V>{};
+                    s[i][u] = at == -2 ? CUDART_NAN_F : 1.f;
+                    if (cache && at >= 0) {
+                        if (LEAN_SPAN(at + in_row, V, p.cache_end, p.err))
+                            x[i][u] = *reinterpret_cast<const Cached<C, V> *>(cache + at + in_row);
+                        if (IN8 && LEAN_IN(at_scale, p.scale_end, p.err)) s[i][u] = (i ? p.v_scales : p.k_scales)[at_scale];
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = t1 + u * sub;
+                if (t >= nt) break;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    A *out = static_cast<A *>(i ? p.v_out : p.k_out);
+                    if (!out) continue;
+                    float f[V];
+                    x[i][u].values(s[i][u], f);
+                    if (!IN8 && place[t] == -2) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) f[e] = CUDART_NAN_F;
+                    }
+                    const int64_t to = (t0 + t) * (i ? p.vos : p.kos) + head * (i ? p.vohs : p.kohs) + d;
+                    if (LEAN_SPAN(to, V, i ? p.v_end : p.k_end, p.err)) store_vec<A, V>(out + to, f);
+                }
+            }
         }
     }
 }
@@ -85,25 +132,11 @@ template <typename C, typename A, int V>
 lean_status launch_read(ReadArgs p, int64_t flags, void *stream) {
     p.pieces = p.dim / V;
     p.row = p.hkv * p.pieces;
-    // about two rounds of U pieces a thread, but no fewer blocks than two for an SM while there are tokens for them
-    int64_t tokens = std::max<int64_t>(1, 8 * kReadThreads / p.row);
+    // eight tokens a thread, but no fewer blocks than two for an SM while there are tokens for them
+    int64_t tokens = 8 * std::max(1, kReadThreads / p.row);
     tokens = std::min(tokens, std::max<int64_t>(1, p.n_tokens / (2 * step_sm_count())));
-    p.tokens = (int)tokens;
-    const int64_t grid = (p.n_tokens + tokens - 1) / tokens;
-    if (grid > INT32_MAX) return LEAN_ERR_SHAPE;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)grid, p.k && p.v ? 2 : 1, 1);
-    cfg.blockDim = dim3(kReadThreads, 1, 1);
-    cfg.stream = (cudaStream_t)stream;
-    if (flags & LEAN_FLAG_EARLY_WEIGHTS) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    cudaGetLastError();
-    return cudaLaunchKernelEx(&cfg, kv_read_kernel<C, A, V>, p) == cudaSuccess ? LEAN_OK : LEAN_ERR_CUDA;
+    p.tokens = (int)std::min<int64_t>(tokens, kReadTokens);
+    return step_launch(kv_read_kernel<C, A, V>, (p.n_tokens + p.tokens - 1) / p.tokens, kReadThreads, 0, flags, stream, p);
 }
 // Pieces of 16 bytes of the output where every row lies so that they and what they come from are whole accesses.
 template <typename C, typename A>

@@ -424,11 +424,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
 
     if (warp < 8) {
         // ---- scores to probabilities, products to outputs: a thread has a row
-        regs_up<PP == 1 ? 168 : 192>();
+        regs_up<PP == 1 ? 152 : 192>();
         const int g = warp / 4, r = threadIdx.x % kTileRows;
         const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // this warp's 32 lanes of tensor memory
         const uint32_t s_group = tmem + lanes + S::scores(g, 0), o_at = tmem + lanes + S::outputs(g);
-        unsigned done = 0;          // half tiles of this group so far: buffer done % NB, whose phase is done / NB
+        unsigned buf = 0, buf_phase = 0;  // the buffer of the next half tile, and its phase
         unsigned tiles_before = 0;  // of the run, by loader's count (scales)
         bool ok = true;
         uint32_t q_phase = 1;  // (the phase before the first counts as done)
@@ -474,36 +474,45 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.q_full);
             }
-            constexpr float kLog2Lift = PartRange<T>::kLift == 1.f ? 0.f : 13.f, kDown = 1.f / PartRange<T>::kLift;
+            // What p is multiplied with, as a power of two, and the sum of 32 of them up to which none is too large for its
+            // type.  bf16 has fp32's range; f16 ends at 2^-25 (half its smallest step) and 65504: in one part p is lifted so
+            // that 32 equal ones stay below that and references seldom move (what is lost of one is 2^-34 of the largest),
+            // in more as in attend.cuh.
+            constexpr float kLog2Lift = BF16 ? 0.f : PP == 1 ? 9.f : 13.f;
+            constexpr float kDown = BF16 ? 1.f : PP == 1 ? 1.f / 512 : 1.f / 8192;
+            constexpr float kMostSum = BF16 ? 1099511627776.f : 65504.f;
             float m = -CUDART_INF_F, l = 0.f;
             int v_ref = 1;
-            // What a half's largest score and scales make of the references m and v_ref: what is multiplied with the sums
-            // and the outputs so far, added to the exponents of 32 keys, and multiplied with the sum of their p.
-            float fall, o_fall, shift[2], back[2];
-            auto refer = [&](float top, const int *exps) {
+            // The references m and v_ref: what they make of exponents and sums of 32 keys each.
+            float shift[2], back[2];
+            auto refer_scales = [&](const int *exps) {
+                // values' scales lie in 0.5..1 times 2^(exponent of the largest of 32 - 126); sums are relative to
+                // 2^(v_ref - 126); what is below 2^-60 of the largest may count as 2^-60 of it
+                const float up = kLog2Lift - (m == -CUDART_INF_F ? 0.f : m);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int below = min(v_ref - exps[c], 60);
+                    shift[c] = up - (float)below;
+                    back[c] = __uint_as_float((uint32_t)(127 + max(below, 0)) << 23);
+                }
+                return exps[0] <= v_ref && exps[1] <= v_ref;
+            };
+            // New references for a half whose largest score is `top`, and what is multiplied with the sums and the outputs
+            // so far.
+            auto refer = [&](float top, const int *exps, float &fall, float &o_fall) {
                 // (m as in attend.cuh: within kSlack of the largest score so far)
                 const float mn = top - m <= PartRange<T>::kSlack ? m : top;
-                const float ms = mn == -CUDART_INF_F ? 0.f : mn;
-                fall = o_fall = ex2(m - ms);
-                bool moved = !(mn == m);
+                fall = o_fall = ex2(m - (mn == -CUDART_INF_F ? 0.f : mn));
                 m = mn;
-                shift[0] = shift[1] = kLog2Lift - ms;
-                back[0] = back[1] = 1.f;
                 if (IN8) {
-                    // values' scales lie in 0.5..1 times 2^(exponent of the largest of 32 - 126); sums are relative to
-                    // 2^(v_ref - 126); what is below 2^-60 of the largest may count as 2^-60 of it
                     const int now = max(v_ref, max(exps[0], exps[1]));
                     o_fall *= __uint_as_float((uint32_t)max(0, 127 + v_ref - now) << 23);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int below = min(now - exps[c], 60);
-                        shift[c] -= (float)below;
-                        back[c] = __uint_as_float((uint32_t)(127 + below) << 23);
-                    }
-                    moved = moved || now != v_ref;
                     v_ref = now;
+                    refer_scales(exps);
+                } else {
+                    shift[0] = shift[1] = kLog2Lift - (m == -CUDART_INF_F ? 0.f : m);
+                    back[0] = back[1] = 1.f;
                 }
-                return moved;
             };
             auto size = [&]() { return IN8 ? kDown * __uint_as_float((uint32_t)(v_ref + 1) << 23) : kDown; };
             // Halves of tiles in turn (of the last one the second may have no keys; keys that are not there score -inf).
@@ -513,14 +522,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             const int *exps = nullptr;
             auto scores_wait = [&]() {
                 limit = w.x.len - t * kTileKeys - half * kHalfKeys;
-                const unsigned n = tiles_before + (t - w.from), slot = n % 4;
-                exps = bars.value_exp[slot] + 2 * half;
-                ks = scales + slot * 2 * kTileKeys + half * kHalfKeys;
-                vs = ks + kTileKeys;
-                s_at = s_group + done % NB * S::kWidth;
                 bool got = true;
-                if (IN8 && half == 0) got = warp_wait(bars, &bars.scales_full[slot], n / 4 & 1, p.err);
-                got = got && warp_wait(bars, &bars.s_full[g][done % NB], done / NB & 1, p.err);
+                if (IN8) {
+                    const unsigned n = tiles_before + (t - w.from), slot = n % 4;
+                    exps = bars.value_exp[slot] + 2 * half;
+                    ks = scales + slot * 2 * kTileKeys + half * kHalfKeys;
+                    vs = ks + kTileKeys;
+                    if (half == 0) got = warp_wait(bars, &bars.scales_full[slot], n / 4 & 1, p.err);
+                }
+                s_at = s_group + buf * S::kWidth;
+                got = got && warp_wait(bars, &bars.s_full[g][buf], buf_phase, p.err);
                 tm_after();
                 return got;
             };
@@ -528,11 +539,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                 tm_wait_st();
                 tm_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[g][done % NB]);
-                ++done;
+                if (lane == 0) mbar_arrive(&bars.p_full[g][buf]);
+                if (++buf == NB) {
+                    buf = 0;
+                    buf_phase ^= 1;
+                }
             };
             auto products_wait = [&]() {  // of all that were published
-                const bool got = warp_wait(bars, &bars.o_full[g][(done - 1) % NB], (done - 1) / NB & 1, p.err);
+                const bool first = buf == 0;
+                const bool got = warp_wait(bars, &bars.o_full[g][first ? NB - 1 : buf - 1], first ? buf_phase ^ 1 : buf_phase, p.err);
                 tm_after();
                 return got;
             };
@@ -547,16 +562,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             if constexpr (PP == 1) {
                 // outputs stay in tensor memory for kFoldHalves halves, then go to the row's part in the workspace
                 int in_sum = 0;       // halves whose products lie there
+                unsigned in_run = 0;  // halves of this part of the item so far
                 bool folded = false;  // the part has some already, with reference m_part
                 float m_part = -CUDART_INF_F;
                 while (t < w.to) {
                     ok = scores_wait();
                     if (!ok) break;
                     uint32_t x[2][32];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) tm_ld32(s_at + 32 * c, x[c]);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) tm_wait_ld(x[c]);
+                    tm_ld64(s_at, x);
                     if (IN8) {
 #pragma unroll
                         for (int i = 0; i < kHalfKeys; i += 2) {
@@ -571,46 +584,63 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                         for (int i = 0; i < kHalfKeys; ++i)
                             if (i >= limit) x[i / 32][i % 32] = 0xff800000u;
                     }
-                    float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                    float sums[2];  // of the first 32 keys and of the others
+                    auto exponentials = [&]() {
+                        const f32x2 zs2 = pack2(zs, zs);
 #pragma unroll
-                    for (int i = 0; i < kHalfKeys; ++i) tops[i % 4] = fmaxf(tops[i % 4], __uint_as_float(x[i / 32][i % 32]));
-                    const bool moved = refer(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * zs, exps);
-                    const f32x2 zs2 = pack2(zs, zs);
-                    f32x2 sum2[2] = {0, 0};  // of the first 32 keys and of the others
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t part[16];
+                            const f32x2 shift2 = pack2(shift[c], shift[c]);
+                            f32x2 sum2 = 0;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t part[16];
-                        const f32x2 shift2 = pack2(shift[c], shift[c]);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float2 a = unpack2(fma2(pack2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), zs2, shift2));
-                            float2 e = make_float2(ex2(a.x), ex2(a.y));
-                            sum2[c] = add2(sum2[c], pack2(e.x, e.y));
-                            if (IN8) e = unpack2(mul2(pack2(e.x, e.y), *reinterpret_cast<const f32x2 *>(vs + 32 * c + i)));
-                            part[i / 2] = take_part<T>(e.x, e.y);
+                            for (int i = 0; i < 32; i += 2) {
+                                const float2 a = unpack2(fma2(pack2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), zs2, shift2));
+                                float2 e = make_float2(ex2(a.x), ex2(a.y));
+                                sum2 = add2(sum2, pack2(e.x, e.y));
+                                if (IN8) e = unpack2(mul2(pack2(e.x, e.y), *reinterpret_cast<const f32x2 *>(vs + 32 * c + i)));
+                                part[i / 2] = take_part<T>(e.x, e.y);
+                            }
+                            const float2 sum = unpack2(sum2);
+                            sums[c] = sum.x + sum.y;
+                            tm_st16(s_at + S::part(c, 0), part);  // (over the scores, which are in registers)
                         }
-                        tm_st16(s_at + S::part(c, 0), part);  // (over the scores, which are in registers)
+                    };
+                    // With the references of the half before, as long as no p is too large for its type; in the first half,
+                    // and where they have to move, the largest score is looked for and p is computed again.
+                    bool moves = in_run == 0;
+                    if (!moves) {
+                        if (IN8) moves = !refer_scales(exps);
+                        exponentials();
+                        moves = moves || !(fmaxf(sums[0], sums[1]) <= kMostSum);
                     }
-                    if (__any_sync(0xffffffffu, moved) && in_sum > 0) {  // new references: what is there is rescaled
-                        ok = products_wait();
-                        if (!ok) break;
+                    float fall = 1.f;
+                    if (__any_sync(0xffffffffu, moves)) {
+                        float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-                        for (int c = 0; c < DP; c += 32) {
-                            uint32_t y[32];
-                            tm_ld32(o_at + c, y);
-                            tm_wait_ld(y);
+                        for (int i = 0; i < kHalfKeys; ++i) tops[i % 4] = fmaxf(tops[i % 4], __uint_as_float(x[i / 32][i % 32]));
+                        float o_fall;
+                        refer(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * zs, exps, fall, o_fall);
+                        exponentials();
+                        if (in_sum > 0) {  // what is there is rescaled
+                            ok = products_wait();
+                            if (!ok) break;
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t z[16];
+                            for (int c = 0; c < DP; c += 32) {
+                                uint32_t y[32];
+                                tm_ld32(o_at + c, y);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) z[i] = __float_as_uint(__uint_as_float(y[16 * h + i]) * o_fall);
-                                tm_st16(o_at + c + 16 * h, z);
+                                for (int h = 0; h < 2; ++h) {
+                                    uint32_t z[16];
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) z[i] = __float_as_uint(__uint_as_float(y[16 * h + i]) * o_fall);
+                                    tm_st16(o_at + c + 16 * h, z);
+                                }
                             }
                         }
                     }
                     publish();
-                    const float2 sum0 = unpack2(sum2[0]), sum1 = unpack2(sum2[1]);
-                    l = fmaf(l, fall, (sum0.x + sum0.y) * back[0] + (sum1.x + sum1.y) * back[1]);
+                    l = fmaf(l, fall, IN8 ? sums[0] * back[0] + sums[1] * back[1] : sums[0] + sums[1]);
+                    ++in_run;
                     advance_half();
                     if (++in_sum == kFoldHalves || t >= w.to) {
                         ok = products_wait();
@@ -621,7 +651,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                         for (int c = 0; c < DP; c += 32) {
                             uint32_t y[32];
                             tm_ld32(o_at + c, y);
-                            tm_wait_ld(y);
 #pragma unroll
                             for (int i = 0; i < 32; i += 8) {
                                 if (part_at < 0) break;
@@ -660,7 +689,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                         for (int c = limit / 32 * 32; c < kHalfKeys; c += 32) {
                             uint32_t x[32];
                             tm_ld32(s_at + c, x);
-                            tm_wait_ld(x);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 uint32_t y[16];
@@ -676,7 +704,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                     for (int c = 0; c < kHalfKeys; c += 32) {
                         uint32_t x[32];
                         tm_ld32(s_at + c, x);
-                        tm_wait_ld(x);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             float z = __uint_as_float(x[i]);
@@ -684,14 +711,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                             tops[i % 4] = fmaxf(tops[i % 4], z);
                         }
                     }
-                    refer(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * zs, exps);
+                    float fall, o_fall;
+                    refer(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * zs, exps, fall, o_fall);
                     const f32x2 zs2 = pack2(zs, zs);
                     f32x2 sum2[2] = {0, 0};  // of the first 32 keys and of the others
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t x[32];
                         tm_ld32(s_at + 32 * c, x);
-                        tm_wait_ld(x);
                         uint32_t part[PP][16];
                         const f32x2 shift2 = pack2(shift[c], shift[c]);
 #pragma unroll
@@ -718,7 +745,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                     for (int c = 0; c < DP; c += 32) {
                         uint32_t x[32];
                         tm_ld32(o_at + c, x);
-                        tm_wait_ld(x);
 #pragma unroll
                         for (int i = 0; i < 32; i += 2)
                             acc[(c + i) / 2] = fma2(acc[(c + i) / 2], fall2, pack2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
@@ -748,7 +774,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         }
     } else if (warp < 12) {
         // ---- keys and values into shared memory
-        regs_down<PP == 1 ? 112 : IN8 ? 88 : 72>();
+        regs_down<PP == 1 ? 120 : IN8 ? 80 : 72>();
         const int t = threadIdx.x - 256;
         unsigned n = 0;
         bool ok = true;
@@ -973,7 +999,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         for (unsigned j = n > KS ? n - KS : 0; ok && j < n; ++j) ok = warp_wait(bars, &bars.k_empty[j % KS], j / KS & 1, p.err);
         for (unsigned j = n > VS ? n - VS : 0; ok && j < n; ++j) ok = warp_wait(bars, &bars.v_empty[j % VS], j / VS & 1, p.err);
     } else {
-        regs_down<PP == 1 ? 64 : IN8 ? 40 : 56>();
+        regs_down<PP == 1 ? 88 : IN8 ? 48 : 56>();
         if (lane == 0) {
             // ---- matrix instructions: warps 12 and 13 issue the groups' scores, 14 and 15 their products.  (One thread
             // needs about 110 cycles for an instruction that runs for 64: one warp for all of them 58 us where four

@@ -307,7 +307,11 @@ def run_prefix(lean, prefix_lens, starts, lens, hq, hkv, dim, page=16, act="f32"
     rel = (2 * 2.0 ** -16 + 80 * U) * reach + 2.0 ** -16 + (seen / 8 + 200) * U
     what = "prefix %s %s own %s heads %d/%d dim %d page %d %s/%s" % (prefix_lens[:4], starts[:4], lens[:4], hq, hkv, dim, page, act, cache)
     top = torch.where(torch.isfinite(vd), vd.abs(), 0.0).max()
-    err = (rel[..., None] + (0.0 if split else one)) * size + 2.0 ** -37 * top
+    # f16 operands lose what of p is below half their smallest step, 2^-25, of a p that lies 2^9 above its reference in
+    # one part and 2^13 in more; the reference is no larger than the largest p, and that no larger than the sum: 2^-34 (or
+    # 2^-38) of the sum for each of the keys, times the largest value
+    lost = 0.0 if cache == "bf16" else seen * 2.0 ** (-38 if split else -34)
+    err = (rel[..., None] + (0.0 if split else one)) * size + (lost + 2.0 ** -37) * top
     close(out, want, err + HALF[act] * (want.abs() + err) + TINY[act], what)
     if lse:
         close(ls, want_lse, rel + 4 * U * torch.where(want_lse.isinf(), 0.0, want_lse).abs(), what + " lse")
