@@ -49,7 +49,7 @@ struct RopeArgs {
     // caches in 8 bits
     float *k_scales, *v_scales;
     int64_t scale_page, scale_place, scale_hs;
-    int lanes;             // of a row
+    int lanes, kv_tokens;  // lanes of a row, tokens of a block of k and v
 };
 
 template <int V>
@@ -296,66 +296,105 @@ lean_status launch_rope(RopeArgs p, bool inter, int64_t flags, void *stream) {
 // ---- caches in 8 bits -------------------------------------------------------------
 
 // A row of a head as it goes to a cache in 8 bits: scale s = max |x| / 127, codes x / s to the nearest whole number,
-// halves away from 0.  The nearest is found from |x| * (1 / s), which is within 2^-15 of the quotient, and then put
-// right by the remainder |x| - c s, which fp32 holds exactly (it is a multiple of the smaller of the operands' last
-// places and below s): no division for each element, and the codes are those of the exact quotients.
+// halves away from 0.  The nearest c is found from x * (1 / s), which is within 2^-15 of the quotient: it is right where
+// the remainder x - c s, which fp32 holds exactly (a multiple of the smaller of the operands' last places, and below s),
+// is less than half of s.  Where it is not for one of a lane's elements (a quotient next to half-way), and for scales so
+// small that they would be subnormal, the remainder says which neighbour is the nearest.  So there is no division for
+// each element, and the codes are those of the exact quotients.
 struct Quantizer {
-    float s, inv, up;  // scale, its inverse and the scale that |x| is compared with, both times `up`
-    float us;
-    bool some;  // a scale that is finite and not 0
+    float s, inv;
+    bool some, plain;  // a scale that is finite and not 0; and neither it nor what is compared with it subnormal
     // top: the largest |x|, as bits (an infinity or NaN is above every number)
     __device__ __forceinline__ explicit Quantizer(uint32_t top) {
         const float m = __uint_as_float(top);
-        s = __fdiv_rn(m, 127.f);
-        some = top < 0x7f800000u && s > 0.f;
-        if (top >= 0x7f800000u) s = CUDART_NAN_F;  // what is not finite makes the whole row NaN
-        up = m < 1e-18f ? 18446744073709551616.f : 1.f;  // 2^64: nothing below is subnormal
-        us = s * up;
-        inv = some ? 1.f / us : 0.f;
+        // (the product with 1 / 127 and one correction are the rounded quotient for every mantissa)
+        const float r = 1.f / 127.f, q = m * r;
+        s = fmaf(fmaf(-q, 127.f, m), r, q);
+        plain = m >= 1e-18f && top < 0x7f800000u;
+        some = plain;
+        if (!plain) {
+            s = top >= 0x7f800000u ? CUDART_NAN_F : __fdiv_rn(m, 127.f);  // what is not finite makes the whole row NaN
+            some = s > 0.f;
+        }
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(plain ? s : 1.f));
     }
-    __device__ __forceinline__ uint32_t code(float x) const {  // in the low 8 bits
-        const float a = fabsf(x) * up;
-        const float t = fmaf(a, inv, 12582912.f);  // 1.5 * 2^23: a whole number in the low bits
+    // bits of 1.5 * 2^23 + c: c in the low 8 bits; far: the largest remainder
+    __device__ __forceinline__ uint32_t guess(float x, float &far) const {
+        const float t = fmaf(x, inv, 12582912.f);
+        far = fmaxf(far, fabsf(fmaf(12582912.f - t, s, x)));
+        return __float_as_uint(t);
+    }
+    __device__ __forceinline__ uint32_t exact(float x) const {
+        if (!some) return 0;
+        const float up = plain ? 1.f : 18446744073709551616.f;  // 2^64: nothing below is subnormal
+        const float a = fabsf(x) * up, us = s * up;
+        const float t = fmaf(a, 1.f / us, 12582912.f);
         const float r = fmaf(12582912.f - t, us, a), r2 = r + r;
         int c = __float_as_int(t) - 0x4b400000;
         c += r2 >= us ? 1 : 0;
         c -= -r2 > us ? 1 : 0;
-        c = some ? min(c, 127) : 0;  // (above 127 where the scale is subnormal and rounded down)
-        return (uint32_t)(x < 0.f ? -c : c) & 0xffu;
+        c = min(c, 127);  // (above it where the scale is subnormal and was rounded down)
+        return (uint32_t)(x < 0.f ? -c : c);
     }
 };
-template <int V>
-__device__ __forceinline__ void store_codes(int8_t *to, const float *f, const Quantizer &z) {
-    if constexpr (V == 1) {
-        *to = (int8_t)z.code(f[0]);
-    } else {
-        uint32_t w[V / 4];
+// Codes of a lane's pieces of 2 V elements: w[piece][run] holds a run's V bytes.
+template <int V, int NP>
+__device__ __forceinline__ void row_codes(const Quantizer &z, const float (&f)[NP][2 * V], uint32_t (&w)[NP][2][V < 4 ? 1 : V / 4]) {
+    uint32_t c[NP][2 * V];
+    float far = 0.f;
 #pragma unroll
-        for (int i = 0; i < V / 4; ++i)
-            w[i] = z.code(f[4 * i]) | z.code(f[4 * i + 1]) << 8 | z.code(f[4 * i + 2]) << 16 | z.code(f[4 * i + 3]) << 24;
-        if constexpr (V == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t *>(to) = w[0];
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) c[i][j] = z.guess(f[i][j], far);
+    if (!(z.plain && far + far < z.s)) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+            for (int j = 0; j < 2 * V; ++j) c[i][j] = z.exact(f[i][j]);
     }
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (V == 1) {
+                w[i][j][0] = c[i][j];
+            } else {
+#pragma unroll
+                for (int k = 0; k < V / 4; ++k) {
+                    const uint32_t *u = &c[i][j * V + 4 * k];
+                    w[i][j][k] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+                }
+            }
+        }
+}
+template <int V>
+__device__ __forceinline__ void store_codes(int8_t *to, const uint32_t *w) {
+    if constexpr (V == 1) *to = (int8_t)w[0];
+    else if constexpr (V == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(to) = w[0];
 }
 
-// A row (one head of q, k or v of one token) belongs to p.lanes neighbouring lanes, a power of two: each has up to 16
-// of its elements, in pieces of two runs as above, so that a row's largest element is found by shuffles alone and a
-// thread has U rows' loads under way.
-template <typename A, int V, bool INTER>
-__global__ void __launch_bounds__(256, 3) rope8_kernel(const RopeArgs p) {
-    step_begin();
-    constexpr int NP = 8 / V, U = V == 1 ? 1 : 4;  // pieces of a lane, rows at a time
-    extern __shared__ __align__(16) float2 cs[];  // [token][pair]: cosine, sine
-    __shared__ int64_t place[kRopeMaxTokens], scale_at[kRopeMaxTokens];
-    const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
-    const int nt = (int)(p.n_tokens - t0 < p.tokens ? p.n_tokens - t0 : p.tokens);
-    const int half = p.rot / 2, G = p.lanes, heads = p.hq + 2 * p.hkv, rows = nt * heads;
-    const int lane = threadIdx.x % G, stride = 256 / G;
+// A head belongs to p.lanes neighbouring lanes, a power of two, which have it for all of the block's tokens: each has up
+// to 16 of its elements, in pieces of two runs as above, so that a row's largest element is found by shuffles alone, and
+// U tokens' loads are under way.  Blocks have heads of q or of k and v (KV), which take three times the instructions.
+// (Both in one block 49 us, rows of all heads numbered through, each with its own divisions, 45, at the sizes above where
+// this takes XX.)
+template <typename A, int V, bool INTER, bool KV>
+__device__ __forceinline__ void rope8_block(const RopeArgs &p, float2 *cs, int64_t *place, int64_t *scale_at, int tokens) {
+    constexpr int NP = 8 / V, U = V == 8 && !KV ? 4 : 2;  // pieces of a lane, tokens at a time
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    if (t0 >= p.n_tokens) return;
+    const int nt = (int)(p.n_tokens - t0 < tokens ? p.n_tokens - t0 : tokens);
+    const int half = p.rot / 2, G = p.lanes, per_token = (KV ? 2 * p.hkv : p.hq) * G;
+    const int T = blockDim.x, sub = max(1, T / per_token);  // tokens side by side, where a token has few lanes
+    const int first = per_token <= T ? (int)threadIdx.x / per_token : 0;
+    const int lane = threadIdx.x % G;
+    const unsigned group = (G == 32 ? 0xffffffffu : (1u << G) - 1) << (threadIdx.x % 32 / G * G);
     const int64_t cache_end = (p.n_slots / p.page - 1) * p.page_stride + (p.page - 1) * p.place_stride +
                               (p.hkv - 1) * p.cache_hs + p.dim;
     const int64_t scale_end = (p.n_slots / p.page - 1) * p.scale_page + (p.page - 1) * p.scale_place +
                               (p.hkv - 1) * p.scale_hs + 1;
-    // a piece's runs: where they begin in a row, and their first pairs (-1: not rotated)
+    // a piece's runs: where they begin in a row (-1: no such piece), and their first pairs (-1: not rotated)
     int a[NP], b[NP], pair_a[NP], pair_b[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
@@ -374,62 +413,55 @@ __global__ void __launch_bounds__(256, 3) rope8_kernel(const RopeArgs p) {
         if (piece >= p.pieces) a[i] = -1;
     }
     Piece<A, V> x[U][NP][2];
-    auto load = [&](int row0) {
+    struct Run {  // a head's rows, from token t0 on
+        const A *src;
+        A *dst;
+        int8_t *cache;
+        float *scales;
+        int64_t step, to_step, cache_at, scale_at;
+        int64_t at, end, to, to_end;  // the same places as offsets, and what there is (checked build)
+        bool turned;
+    };
+    auto open = [&](int head) {
+        Run q;
+        const bool is_q = !KV, is_k = KV && head < p.hkv;
+        const int kvh = head - (is_k ? 0 : p.hkv);
+        q.step = is_q ? p.qs : is_k ? p.ks : p.vs;
+        q.to_step = is_q ? p.qos : p.kos;
+        q.at = (is_q ? head * p.qhs : kvh * (is_k ? p.khs : p.vhs)) + t0 * q.step;
+        q.end = is_q ? p.q_end : is_k ? p.k_end : p.v_end;
+        q.to = (is_q ? head * p.qohs : kvh * p.kohs) + t0 * q.to_step;
+        q.to_end = is_q ? p.qo_end : p.ko_end;
+        q.src = static_cast<const A *>(is_q ? p.q : is_k ? p.k : p.v) + q.at;
+        q.dst = is_q ? static_cast<A *>(p.q_out) + q.to : is_k && p.k_out ? static_cast<A *>(p.k_out) + q.to : nullptr;
+        q.cache = is_q ? nullptr : static_cast<int8_t *>(is_k ? p.k_cache : p.v_cache);
+        q.scales = is_k ? p.k_scales : p.v_scales;
+        q.cache_at = kvh * p.cache_hs;
+        q.scale_at = kvh * p.scale_hs;
+        q.turned = is_q || is_k;
+        return q;
+    };
+    auto load = [&](const Run &q, int t1) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int row = row0 + u * stride;
-            const int t = row / heads, head = row - t * heads;
-            const bool is_q = head < p.hq, is_k = !is_q && head < p.hq + p.hkv;
-            const int kvh = head - p.hq - (is_k ? 0 : p.hkv);
-            const A *base = static_cast<const A *>(is_q ? p.q : is_k ? p.k : p.v);
-            const int64_t at = is_q ? (t0 + t) * p.qs + head * p.qhs : is_k ? (t0 + t) * p.ks + kvh * p.khs
-                                                                            : (t0 + t) * p.vs + kvh * p.vhs;
-            const int64_t end = is_q ? p.q_end : is_k ? p.k_end : p.v_end;
+            const int t = t1 + u * sub;
 #pragma unroll
             for (int i = 0; i < NP; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     x[u][i][j] = Piece<A, V>{};
-                    const int64_t e = at + (j ? b[i] : a[i]);
-                    if (row < rows && a[i] >= 0 && LEAN_SPAN(e, V, end, p.err))
-                        x[u][i][j] = *reinterpret_cast<const Piece<A, V> *>(base + e);
+                    const int64_t e = t * q.step + (j ? b[i] : a[i]);
+                    if (t < nt && a[i] >= 0 && LEAN_SPAN(q.at + e, V, q.end, p.err))
+                        x[u][i][j] = *reinterpret_cast<const Piece<A, V> *>(q.src + e);
                 }
         }
     };
-    const int first = threadIdx.x / G;
-    load(first);  // under way while the angles are computed
-    for (int i = threadIdx.x; i < nt * half; i += 256) {
-        const int t = i / half, j = i - t * half;
-        const int32_t pos = LEAN_IN(t0 + t, p.n_tokens, p.err) ? p.positions[t0 + t] : 0;
-        const uint64_t f = LEAN_IN(j, p.rot / 2, p.err) ? p.turns[j] : 0;
-        const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32), n = (uint32_t)pos;
-        const uint32_t turn = __umulhi(n, lo) + n * hi - (pos < 0 ? lo : 0u);
-        float sine, cosine;
-        sincospif((float)(int32_t)turn * (1.f / 2147483648.f), &sine, &cosine);
-        cs[i] = make_float2(cosine * p.scale, sine * p.scale);
-    }
-    if (threadIdx.x < nt) {
-        const int32_t s = LEAN_IN(t0 + threadIdx.x, p.n_tokens, p.err) ? p.slots[t0 + threadIdx.x] : -1;
-        int64_t at = -1, at_scale = -1;
-        if (s >= p.n_slots) atomicOr(p.err, kErrSlot);
-        else if (s >= 0) {
-            at = (int64_t)(s / p.page) * p.page_stride + (int64_t)(s % p.page) * p.place_stride;
-            at_scale = (int64_t)(s / p.page) * p.scale_page + (int64_t)(s % p.page) * p.scale_place;
-        }
-        place[threadIdx.x] = at;
-        scale_at[threadIdx.x] = at_scale;
-    }
-    __syncthreads();
-    // (every thread takes every turn of the loop: rows past the end are empty, and lanes of a warp stay together)
-    for (int row0 = first; row0 - first < rows; row0 += U * stride) {
+    auto finish = [&](const Run &q, int t1) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int row = row0 + u * stride;
-            const int t = min(row / heads, nt - 1), head = row - row / heads * heads;
-            const bool is_q = head < p.hq, is_k = !is_q && head < p.hq + p.hkv;
-            const int kvh = head - p.hq - (is_k ? 0 : p.hkv);
+            const int t = t1 + u * sub;
+            if (t >= nt) break;
             float f[NP][2 * V];
-            uint32_t top = 0;
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 unpack_piece(x[u][i][0], f[i]);
@@ -440,7 +472,7 @@ __global__ void __launch_bounds__(256, 3) rope8_kernel(const RopeArgs p) {
                     e1 = n1;
                 };
                 const float2 *w = cs + t * half;
-                if ((is_q || is_k) && a[i] >= 0) {
+                if (q.turned && a[i] >= 0) {
                     if (INTER && V > 1) {
                         if (pair_a[i] >= 0)
 #pragma unroll
@@ -461,38 +493,88 @@ __global__ void __launch_bounds__(256, 3) rope8_kernel(const RopeArgs p) {
                         }
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < 2 * V; ++j) top = max(top, __float_as_uint(f[i][j]) & 0x7fffffffu);
             }
-            for (int o = G / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (row >= rows) continue;
-            A *dst = is_q ? static_cast<A *>(p.q_out) : is_k ? static_cast<A *>(p.k_out) : nullptr;
-            if (dst) {
-                const int64_t at = is_q ? (t0 + t) * p.qos + head * p.qohs : (t0 + t) * p.kos + kvh * p.kohs;
-                const int64_t end = is_q ? p.qo_end : p.ko_end;
+            if (q.dst) {
+                const int64_t to = t * q.to_step;
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     if (a[i] < 0) continue;
-                    if (LEAN_SPAN(at + a[i], V, end, p.err)) store_vec<A, V>(dst + at + a[i], f[i]);
-                    if (LEAN_SPAN(at + b[i], V, end, p.err)) store_vec<A, V>(dst + at + b[i], f[i] + V);
+                    if (LEAN_SPAN(q.to + to + a[i], V, q.to_end, p.err)) store_vec<A, V>(q.dst + to + a[i], f[i]);
+                    if (LEAN_SPAN(q.to + to + b[i], V, q.to_end, p.err)) store_vec<A, V>(q.dst + to + b[i], f[i] + V);
                 }
             }
-            if (!is_q && place[t] >= 0) {
+            if (KV && place[t] >= 0) {  // (a group's lanes have the same head and token)
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2 * V; ++j) top = max(top, __float_as_uint(f[i][j]) & 0x7fffffffu);
+                for (int o = G / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(group, top, o));
                 const Quantizer z(top);
-                int8_t *cache = static_cast<int8_t *>(is_k ? p.k_cache : p.v_cache);
-                const int64_t at = place[t] + kvh * p.cache_hs;
+                uint32_t w[NP][2][V < 4 ? 1 : V / 4];
+                row_codes<V, NP>(z, f, w);
+                const int64_t at = place[t] + q.cache_at;
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     if (a[i] < 0) continue;
-                    if (LEAN_SPAN(at + a[i], V, cache_end, p.err)) store_codes<V>(cache + at + a[i], f[i], z);
-                    if (LEAN_SPAN(at + b[i], V, cache_end, p.err)) store_codes<V>(cache + at + b[i], f[i] + V, z);
+                    if (LEAN_SPAN(at + a[i], V, cache_end, p.err)) store_codes<V>(q.cache + at + a[i], w[i][0]);
+                    if (LEAN_SPAN(at + b[i], V, cache_end, p.err)) store_codes<V>(q.cache + at + b[i], w[i][1]);
                 }
-                const int64_t to = scale_at[t] + kvh * p.scale_hs;
-                if (lane == 0 && LEAN_IN(to, scale_end, p.err)) (is_k ? p.k_scales : p.v_scales)[to] = z.s;
+                const int64_t to = scale_at[t] + q.scale_at;
+                if (lane == 0 && LEAN_IN(to, scale_end, p.err)) q.scales[to] = z.s;
             }
         }
-        if (row0 - first + U * stride < rows) load(row0 + U * stride);
+    };
+    int slot = per_token <= T ? threadIdx.x - first * per_token : threadIdx.x;
+    const bool live = first < sub && slot < per_token;
+    Run run;
+    if (live) {
+        run = open(slot / G);
+        load(run, first);  // under way while the angles are computed
     }
+    for (int i = threadIdx.x; i < nt * half; i += T) {
+        const int t = i / half, j = i - t * half;
+        const int32_t pos = LEAN_IN(t0 + t, p.n_tokens, p.err) ? p.positions[t0 + t] : 0;
+        const uint64_t f = LEAN_IN(j, p.rot / 2, p.err) ? p.turns[j] : 0;
+        const uint32_t lo = (uint32_t)f, hi = (uint32_t)(f >> 32), n = (uint32_t)pos;
+        const uint32_t turn = __umulhi(n, lo) + n * hi - (pos < 0 ? lo : 0u);
+        float sine, cosine;
+        sincospif((float)(int32_t)turn * (1.f / 2147483648.f), &sine, &cosine);
+        cs[i] = make_float2(cosine * p.scale, sine * p.scale);
+    }
+    if (KV && threadIdx.x < nt) {
+        const int32_t s = LEAN_IN(t0 + threadIdx.x, p.n_tokens, p.err) ? p.slots[t0 + threadIdx.x] : -1;
+        int64_t at = -1, at_scale = -1;
+        if (s >= p.n_slots) atomicOr(p.err, kErrSlot);
+        else if (s >= 0) {
+            at = (int64_t)(s / p.page) * p.page_stride + (int64_t)(s % p.page) * p.place_stride;
+            at_scale = (int64_t)(s / p.page) * p.scale_page + (int64_t)(s % p.page) * p.scale_place;
+        }
+        place[threadIdx.x] = at;
+        scale_at[threadIdx.x] = at_scale;
+    }
+    __syncthreads();
+    if (!live) return;
+    for (int t1 = first;;) {
+        finish(run, t1);
+        t1 += U * sub;
+        if (t1 >= nt) {  // on to the thread's next head
+            slot += T;
+            if (per_token <= T || slot >= per_token) return;
+            run = open(slot / G);
+            t1 = first;
+        }
+        load(run, t1);
+    }
+}
+
+template <typename A, int V, bool INTER>
+__global__ void __launch_bounds__(kRopeMaxThreads, 2) rope8_kernel(const RopeArgs p) {
+    step_begin();
+    extern __shared__ __align__(16) float2 cs[];  // [token][pair]: cosine, sine
+    __shared__ int64_t place[kRopeMaxTokens], scale_at[kRopeMaxTokens];
+    if (blockIdx.y == 0) rope8_block<A, V, INTER, true>(p, cs, place, scale_at, p.kv_tokens);
+    else rope8_block<A, V, INTER, false>(p, cs, place, scale_at, p.tokens);
 }
 
 template <typename A, int V>
@@ -501,16 +583,36 @@ lean_status launch_rope8(RopeArgs p, bool inter, int64_t flags, void *stream) {
     p.rot_pieces = p.rot / (2 * V);
     p.lanes = 2;
     while (p.lanes < p.pieces && p.lanes < 32) p.lanes *= 2;
-    // two rounds of rows a block, but no fewer blocks than two for an SM while there are tokens for them
-    const int64_t heads = p.hq + 2 * p.hkv, rows = 2 * (V == 1 ? 1 : 4) * 256 / p.lanes;
-    int64_t tokens = std::min<int64_t>(std::max<int64_t>(1, rows / heads),
-                                       std::max<int64_t>(1, p.n_tokens / (2 * step_sm_count())));
-    tokens = std::min<int64_t>(tokens, std::max(1, 4096 / std::max(p.rot / 2, 1)));  // angles: 32 KB at most
-    p.tokens = (int)std::min<int64_t>(tokens, kRopeMaxTokens);
-    const size_t smem = sizeof(float2) * p.tokens * std::max(p.rot / 2, 1);
-    const int64_t grid = (p.n_tokens + p.tokens - 1) / p.tokens;
-    if (inter) return step_launch(rope8_kernel<A, V, true>, grid, 256, smem, flags, stream, p);
-    return step_launch(rope8_kernel<A, V, false>, grid, 256, smem, flags, stream, p);
+    // as launch_rope, by lanes; blocks of q and of k and v have the same threads
+    const int64_t items = (int64_t)std::max(p.hq, 2 * p.hkv) * p.lanes;
+    const int64_t sub = std::max<int64_t>(1, 256 / items);
+    const int64_t passes = (items + kRopeMaxThreads - 1) / kRopeMaxThreads;
+    const int threads = (int)(((sub * items + passes - 1) / passes + 31) / 32 * 32);
+    auto tokens_of = [&](int64_t heads) {
+        int64_t n = 8 * std::max<int64_t>(1, threads / (heads * p.lanes));
+        n = std::min(n, std::max<int64_t>(1, p.n_tokens / (2 * step_sm_count())));
+        n = std::min<int64_t>(n, std::max(1, 4096 / std::max(p.rot / 2, 1)));  // angles: 32 KB at most
+        return (int)std::min<int64_t>(n, kRopeMaxTokens);
+    };
+    p.kv_tokens = tokens_of(2 * p.hkv);
+    p.tokens = p.hq > 0 ? tokens_of(p.hq) : p.kv_tokens;
+    const size_t smem = sizeof(float2) * std::max(p.tokens, p.kv_tokens) * std::max(p.rot / 2, 1);
+    const int fewest = std::min(p.tokens, p.kv_tokens);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)((p.n_tokens + fewest - 1) / fewest), p.hq > 0 ? 2 : 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = (cudaStream_t)stream;
+    if (flags & LEAN_FLAG_EARLY_WEIGHTS) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    cudaGetLastError();
+    auto kern = inter ? rope8_kernel<A, V, true> : rope8_kernel<A, V, false>;
+    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? LEAN_OK : LEAN_ERR_CUDA;
 }
 
 // Elements of a run: as many as 16 bytes have where every run is a whole number of
