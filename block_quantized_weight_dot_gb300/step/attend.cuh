@@ -59,7 +59,7 @@ namespace lean {
 
 constexpr int kAttMaxDim = 256;
 constexpr int kAttMaxCtas = 160;  // of a launch: at most one per SM
-constexpr int kAttMaxWarps = 8;   // of a block
+constexpr int kAttMaxWarps = 16;  // of a block
 constexpr int kUnit = 16;         // tokens
 constexpr int kAttItemUnits = 4;  // empty units counted to an item (below)
 constexpr int64_t kSharedBytes = 2048;  // a Shared for each block
@@ -142,13 +142,17 @@ void att_workspace(AttArgs &p, void *workspace);
 
 namespace {
 
-// Warps of a block, stages of a warp's queue: 128-192 KB of loads an SM can have
+// Warps of a block (in 8 bits a unit is half the bytes and more instructions: at heads of 64, where 128 registers do, 16
+// warps take 61 us where 8 take 78, 384 sequences as above), stages of a warp's queue: 128-192 KB of loads an SM can have
 // under way.
-template <typename C, int DP>
+__host__ __device__ constexpr int att_warps(bool in8, int dp, bool wide) {
+    return dp == 256 ? 4 : in8 && !wide && dp == 64 ? 16 : 8;
+}
+template <typename C, int DP, bool WIDE>
 struct AttShape {
     static constexpr bool kIn8 = sizeof(C) == 1;
-    static constexpr int kWarps = DP == 256 ? 4 : 8;
-    static constexpr int kStages = kIn8 ? (DP == 64 ? 8 : DP == 128 ? 5 : 3) : DP == 64 ? 5 : DP == 128 ? 3 : 2;
+    static constexpr int kWarps = att_warps(kIn8, DP, WIDE);
+    static constexpr int kStages = kIn8 ? (DP == 64 ? (WIDE ? 8 : 4) : DP == 128 ? 5 : 3) : DP == 64 ? 5 : DP == 128 ? 3 : 2;
     static constexpr int kStageBytes = kUnit * DP * 2 * (int)sizeof(C);  // K and V
     static constexpr int kScaleBytes = kIn8 ? 2 * kUnit * 4 : 0;         // their scales
     static constexpr int kQueues = kWarps * kStages * (kStageBytes + kScaleBytes);
@@ -170,14 +174,15 @@ __host__ __device__ constexpr int part_floats(int heads, int dp) { return heads 
 __host__ __device__ constexpr int fold_floats(int heads, int dp) { return heads * (dp + 8); }
 // Shared memory of a block: queues; q at 256 (above); and, where it fits, a part per warp.
 constexpr int kMaxSmem = 232448 - 1536;  // of 227 KB, less static variables
-template <typename C, int DP>
-__host__ __device__ constexpr bool parts_in_smem(int heads) {
-    return AttShape<C, DP>::kSmem + AttShape<C, DP>::kWarps * part_floats(heads, DP) * 4 <= kMaxSmem;
+template <typename C, int DP, bool WIDE>
+__host__ __device__ constexpr bool parts_in_smem() {
+    using S = AttShape<C, DP, WIDE>;
+    return S::kSmem + S::kWarps * part_floats(WIDE ? 16 : 8, DP) * 4 <= kMaxSmem;
 }
-template <typename C, int DP>
-__host__ __device__ constexpr int att_smem(int heads) {
-    return AttShape<C, DP>::kSmem +
-           (parts_in_smem<C, DP>(heads) ? AttShape<C, DP>::kWarps * part_floats(heads, DP) * 4 : 0);
+template <typename C, int DP, bool WIDE>
+__host__ __device__ constexpr int att_smem() {
+    using S = AttShape<C, DP, WIDE>;
+    return S::kSmem + (parts_in_smem<C, DP, WIDE>() ? S::kWarps * part_floats(WIDE ? 16 : 8, DP) * 4 : 0);
 }
 
 // 16 bytes of which `real` (16 or 0) are copied and the rest zero
@@ -419,11 +424,11 @@ __device__ __forceinline__ void store_result(const AttArgs &p, const Head &f, in
 
 // WIDE: 9 to 16 query heads in a group, one per row; else up to 8, two rows each.
 template <typename C, int DP, int PARTS, bool WIDE>
-__global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel(const AttArgs p) {
+__global__ void __launch_bounds__(AttShape<C, DP, WIDE>::kWarps * 32, 1) attend_kernel(const AttArgs p) {
     using P = typename Operand<C>::type;
-    constexpr bool IN8 = AttShape<C, DP>::kIn8;
-    constexpr int W = AttShape<C, DP>::kWarps, S = AttShape<C, DP>::kStages, T = W * 32;
-    constexpr int STAGE = AttShape<C, DP>::kStageBytes, EPP = 16 / (int)sizeof(C);  // elements of a 16-byte piece
+    constexpr bool IN8 = AttShape<C, DP, WIDE>::kIn8;
+    constexpr int W = AttShape<C, DP, WIDE>::kWarps, S = AttShape<C, DP, WIDE>::kStages, T = W * 32;
+    constexpr int STAGE = AttShape<C, DP, WIDE>::kStageBytes, EPP = 16 / (int)sizeof(C);  // elements of a 16-byte piece
     constexpr int H = WIDE ? 16 : 8, NH = WIDE ? 2 : 1;  // heads of a group, of a thread
     // a row's bytes and lanes, rows of a copy instruction
     constexpr int RB = DP * (int)sizeof(C), LPR = RB / 16, RPI = 32 / LPR;
@@ -431,12 +436,12 @@ __global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel
     constexpr int AREGS = WIDE ? 4 * PARTS : 4 + (PARTS > 2 ? 2 : 0);  // of q per step
     constexpr bool QSMEM = DP == 256;                                  // no registers left for q
     constexpr int PF = part_floats(H, DP), PO = 4 + DP;                // a head's row of a part: m, l, -, out
-    constexpr bool PSMEM = parts_in_smem<C, DP>(H);
+    constexpr bool PSMEM = parts_in_smem<C, DP, WIDE>();
     // registers for q as it was read: beside the accumulators, and all through the item before
     constexpr bool EARLY_Q = !WIDE && DP <= 128, AHEAD_Q = !WIDE && DP == 64;
     static_assert(PF * 4 <= S * STAGE, "a part fits a queue");
     static_assert(W <= kAttMaxWarps, "the workspace has parts for as many");
-    static_assert(AttShape<C, DP>::kSmem <= kMaxSmem, "shared memory");
+    static_assert(AttShape<C, DP, WIDE>::kSmem <= kMaxSmem, "shared memory");
     constexpr int AT = 2;  // steps of the values whose products are under way at once (more spill)
     extern __shared__ uint8_t queue_raw[];
     uint8_t *queue = queue_raw + (512 - smem_addr(queue_raw) % 512) % 512;
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel
         }
     }
     uint8_t *const tail_part = queue + warp * (S * STAGE);  // where a warp's last part goes, and an earlier one
-    uint8_t *const head_part = PSMEM ? queue + AttShape<C, DP>::kSmem - 512 + warp * (PF * 4)
+    uint8_t *const head_part = PSMEM ? queue + AttShape<C, DP, WIDE>::kSmem - 512 + warp * (PF * 4)
                                      : reinterpret_cast<uint8_t *>(p.warp_parts + ((int64_t)blockIdx.x * W + warp) * PF);
 
     if (u_lo < u_hi) {
@@ -595,7 +600,7 @@ __global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel
         const uint32_t to_lane = my_queue + lr * RB + ((col ^ turned(lr)) * 16);
         const int real = EPP * col < p.dim ? 16 : 0;
         // scales: of a unit's keys, lanes 0-15, and values
-        const uint32_t my_scales = smem_addr(queue) + W * S * STAGE + warp * (S * AttShape<C, DP>::kScaleBytes);
+        const uint32_t my_scales = smem_addr(queue) + W * S * STAGE + warp * (S * AttShape<C, DP, WIDE>::kScaleBytes);
         const float *scale_lane = lane < kUnit ? p.k_scales : p.v_scales;
 
         auto load_unit = [&](int stage) {
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel
                         const int64_t at = (int64_t)page_id * p.scale_page + (int64_t)(next.in_page + lane % kUnit) * p.scale_place +
                                            (int64_t)next.kvh * p.scale_hs;
                         const bool in = LEAN_IN(at, p.scale_extent, p.err);
-                        cp_async4(my_scales + stage * AttShape<C, DP>::kScaleBytes + 4 * lane, scale_lane + (in ? at : 0), in ? 4 : 0);
+                        cp_async4(my_scales + stage * AttShape<C, DP, WIDE>::kScaleBytes + 4 * lane, scale_lane + (in ? at : 0), in ? 4 : 0);
                     }
                     int64_t off = unit_off + lr * p.place_stride;
 #pragma unroll
@@ -643,7 +648,7 @@ __global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel
                         }
                     }
                     if (IN8) {  // what is not attended has scale 0, keys that are not there NaN, which reaches out and lse
-                        const uint32_t to = my_scales + stage * AttShape<C, DP>::kScaleBytes + 4 * lane;
+                        const uint32_t to = my_scales + stage * AttShape<C, DP, WIDE>::kScaleBytes + 4 * lane;
                         if (off == -2 && lane < kUnit) asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(0x7fffffff) : "memory");
                         else cp_async4(to, scale_lane + (at_scale >= 0 ? at_scale : 0), at_scale >= 0 ? 4 : 0);
                     }
@@ -707,7 +712,7 @@ __global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel
                                    : my_queue + ((lane >> 4) * 8 + (lane & 7)) * RB + ((((lane >> 3) & 1) ^ (lane & 7)) * 16);
         // q as rows of the matrix instruction, part by part
         uint32_t qa[QSMEM ? 1 : KS][AREGS];
-        uint32_t *q_shared = reinterpret_cast<uint32_t *>(queue + AttShape<C, DP>::kQueues) + warp * (KS * AREGS * 32);
+        uint32_t *q_shared = reinterpret_cast<uint32_t *>(queue + AttShape<C, DP, WIDE>::kQueues) + warp * (KS * AREGS * 32);
         // outputs and sums of the item since its last fold, with reference m
         f32x2 acc[2 * KS][NH];
         float m[NH], l[NH], zs[NH];
@@ -798,7 +803,7 @@ __global__ void __launch_bounds__(AttShape<C, DP>::kWarps * 32, 1) attend_kernel
             float2 ks[2], vs[2];  // scales of tokens 2 c4 and 2 c4 + 1, and of those 8 further on
             if constexpr (IN8) {
                 const float2 *at = reinterpret_cast<const float2 *>(queue + (my_scales - smem_addr(queue)) +
-                                                                    stage * AttShape<C, DP>::kScaleBytes) + c4;
+                                                                    stage * AttShape<C, DP, WIDE>::kScaleBytes) + c4;
                 ks[0] = at[0];
                 ks[1] = at[4];
 #pragma unroll
@@ -1189,10 +1194,10 @@ template <typename C, int DP, int PARTS, bool WIDE>
 lean_status launch_attend(const AttArgs &p, int64_t flags, void *stream) {
     static std::atomic<uint64_t> done{0};
     auto kern = attend_kernel<C, DP, PARTS, WIDE>;
-    if (!step_ensure_smem(kern, att_smem<C, DP>(WIDE ? 16 : 8), done)) return LEAN_ERR_CUDA;
-    constexpr int W = AttShape<C, DP>::kWarps;
+    if (!step_ensure_smem(kern, att_smem<C, DP, WIDE>(), done)) return LEAN_ERR_CUDA;
+    constexpr int W = AttShape<C, DP, WIDE>::kWarps;
     const int64_t grid = att_grid(p, W);
-    const lean_status st = step_launch(kern, grid, W * 32, att_smem<C, DP>(WIDE ? 16 : 8), flags, stream, p);
+    const lean_status st = step_launch(kern, grid, W * 32, att_smem<C, DP, WIDE>(), flags, stream, p);
     // (no item can be shared by blocks where each gets its own whatever the lengths are)
     const int64_t most = ((int64_t)p.width * p.page + 2 * kUnit - 1) / kUnit;
     const bool by_item = (int64_t)p.n_seqs * p.hkv * p.tiles <= grid && (most + W - 1) / W <= kJoinUnits;

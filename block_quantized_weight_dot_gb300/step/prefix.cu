@@ -19,11 +19,17 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// The caches as tensors in boxes of prefix_box() places (8 or more: rows of a tile lie in groups of 8); none where a
-// stride is 0 between rows that are not one.
-PrefixMaps make_maps(const PrefixArgs &p, bool bf16) {
+}  // namespace
+
+namespace lean {
+
+// The caches as tensors in boxes of prefix_box() places (8 or more: rows of a tile lie in groups of 8; in 8 bits half a
+// tile at most); none where a stride is 0 between rows that are not one.  16-bit rows are copied to where the matrix
+// instructions read them, rows in 8 bits as they lie.
+PrefixMaps prefix_maps(const PrefixArgs &p, PrefixCache type) {
     PrefixMaps m = {};
-    const int box = prefix_box(p.page);
+    const bool in8 = type == PrefixCache::kI8;
+    const int box = prefix_box(p.page, in8 ? kHalfKeys : kTileKeys);
     const EncodeTiled encode = encode_tiled();
     if (box == 0 || !encode || (p.page > 1 && p.place_stride == 0) || (p.hkv > 1 && p.cache_hs == 0) ||
         (p.n_pages > 1 && p.page_stride == 0))
@@ -32,27 +38,25 @@ PrefixMaps make_maps(const PrefixArgs &p, bool bf16) {
     cuuint64_t bytes[3];
     for (int i = 0; i < 3; ++i) {
         if (strides[i] >= (int64_t)1 << 38) return m;
-        bytes[i] = strides[i] ? 2 * strides[i] : 16;
+        bytes[i] = strides[i] ? (in8 ? 1 : 2) * strides[i] : 16;
     }
     const cuuint64_t dims[4] = {(cuuint64_t)p.dim, (cuuint64_t)p.page, (cuuint64_t)p.hkv, (cuuint64_t)p.n_pages};
-    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
-    const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint32_t boxes[4] = {in8 && p.dim > 64 ? 128u : 64u, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType types[] = {CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                                         CU_TENSOR_MAP_DATA_TYPE_UINT8};
     const void *from[2] = {p.k, p.v};
     CUtensorMap *to[2] = {&m.k, &m.v};
     for (int i = 0; i < 2; ++i)
-        if (encode(to[i], type, 4, const_cast<void *>(from[i]), dims, bytes, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        if (encode(to[i], types[(int)type], 4, const_cast<void *>(from[i]), dims, bytes, boxes, steps,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, in8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return m;
     m.box = box;
     return m;
 }
 
-}  // namespace
-
-namespace lean {
-
 lean_status prefix_cache16(const PrefixArgs &p, bool bf16, bool two, int64_t flags, void *stream) {
-    const PrefixMaps maps = make_maps(p, bf16);
+    const PrefixMaps maps = prefix_maps(p, bf16 ? PrefixCache::kBf16 : PrefixCache::kF16);
     if (bf16)
         return p.dim <= 64 ? pick_prefix<__nv_bfloat16, 64>(maps, p, two, flags, stream)
                            : pick_prefix<__nv_bfloat16, 128>(maps, p, two, flags, stream);
@@ -248,7 +252,7 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     list.rows = two ? 2 * kTileRows : kTileRows;
     list.most = (int)(a->prefix_width * a->page_size);
     list.sms = (unsigned)std::min(step_sm_count(), kPrefixMaxCtas);
-    list.own_most = (unsigned)att_grid(own, 8);
+    list.own_most = (unsigned)att_grid(own, att_warps(in8, prefix_dim(a->head_dim), group > 8));
     list.unit_ns = (float)(kUnit * 2 * a->head_dim * (in8 ? 1 : 2)) / 40.f;
     list.tile_ns = two ? 1800.f : 900.f;
     p.list = own.list = list;

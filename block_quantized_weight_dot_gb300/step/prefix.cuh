@@ -83,19 +83,22 @@ struct PrefixArgs {
     unsigned *err;
 };
 
-// Keys and values of caches of 16 bits as tensors [page][head][place][dim] for the copy engine, in boxes of `box` places by
-// 64 dimensions (box 0: pages whose size no multiple of 8 divides, or strides that it does not take).
+// Keys and values as tensors [page][head][place][dim] for the copy engine, in boxes of `box` places by 64 dimensions (in 8
+// bits all of them; box 0: pages whose size no multiple of 8 divides, or strides that it does not take).
 struct PrefixMaps {
     CUtensorMap k, v;
     int box;
 };
 
-// As many places as a tile and every page are whole numbers of; 0 if fewer than 8.
-inline int prefix_box(int page) {
-    int box = kTileKeys;
+// As many places, up to `most`, as a tile and every page are whole numbers of; 0 if fewer than 8.
+inline int prefix_box(int page, int most) {
+    int box = most;
     while (page % box) box /= 2;
     return box < 8 ? 0 : box;
 }
+
+enum class PrefixCache { kBf16, kF16, kI8 };
+PrefixMaps prefix_maps(const PrefixArgs &p, PrefixCache type);
 
 lean_status prefix_cache16(const PrefixArgs &p, bool bf16, bool two, int64_t flags, void *stream);
 lean_status prefix_cache8(const PrefixArgs &p, bool two, int64_t flags, void *stream);
@@ -168,8 +171,11 @@ struct PrefixShape {
     static constexpr int kKStages = 2, kVStages = QP == 3 && DP == 128 ? 1 : 2;
     static constexpr int kOff = kQ + (kKStages + kVStages) * kTileBytes;  // rows' places, two tiles
     static constexpr int kScaleAt = kOff + 2 * kTileKeys * 8;             // scales of four tiles, keys and values
-    static constexpr int kBars = kScaleAt + (kIn8 ? 4 * 2 * kTileKeys * 4 : 0);
-    static constexpr int kSmem = kBars + 512;
+    // caches in 8 bits: halves of tiles as they lie in the cache
+    static constexpr int kRaw = kIn8 ? (DP == 64 ? 6 : 3) : 0, kRawBytes = kHalfKeys * DP;
+    static constexpr int kRawAt = kScaleAt + (kIn8 ? 4 * 2 * kTileKeys * 4 : 0);  // (a multiple of 128)
+    static constexpr int kBars = kRawAt + kRaw * kRawBytes;
+    static constexpr int kSmem = kBars + 640;
     static constexpr int kSmemAsked = kSmem + 1008;  // (the tiles begin on 1024 bytes)
     // Tensor memory, 512 columns: for each group of rows its outputs, in what is left buffers for the scores of 64 keys,
     // which become p: part 0 (and 1) of 32 keys in the first 16 (and next 16) of their own 32 columns, a third beyond them.
@@ -186,6 +192,7 @@ struct PrefixBars {
     uint64_t q_full, q_free;                                // q is there; both groups are done with it
     uint64_t rows_full[2];                                  // a tile's rows' places are there
     uint64_t scales_full[4];
+    uint64_t raw_full[6], raw_empty[6];                     // halves of tiles in 8 bits are there, were used
     uint64_t last;                                          // every matrix instruction is done
     uint32_t tmem;
     int dead;            // a wait ran out: everyone leaves
@@ -193,7 +200,7 @@ struct PrefixBars {
     int start_i;         // the run's first prefix and place in it
     unsigned start_off;
 };
-static_assert(sizeof(PrefixBars) <= 512, "room for the barriers");
+static_assert(sizeof(PrefixBars) <= 640, "room for the barriers");
 
 // A box of a tensor map into shared memory; its bytes are counted on `bar`.
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int place, int head, int page, uint64_t *bar) {
@@ -378,6 +385,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             }
         }
         for (int i = 0; i < 4; ++i) mbar_init(&bars.scales_full[i], 4);
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(&bars.raw_full[i], 1);
+            mbar_init(&bars.raw_empty[i], 4);
+        }
         for (int i = 0; i < 2; ++i) mbar_init(&bars.rows_full[i], 4);
         mbar_init(&bars.q_full, 8);
         mbar_init(&bars.q_free, 10);
@@ -797,60 +808,36 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             if (lane == 0) mbar_arrive(bar);
         };
         if constexpr (IN8) {
-            // A thread takes 16-byte pieces of all rows through registers, where they become f16: the pieces of the next
-            // tile are under way while this one's are converted.  Where rows lie: a lane looks up the page of a box of
-            // rows; pages that boxes do not fit are looked up row by row, through shared memory.
-            constexpr int PR = DP / 16;  // pieces of a row
+            // Whole tiles in pages that the cache has come as boxes into a ring of halves of tiles, as they lie in the cache;
+            // all four warps turn them into f16 (codes are exact in it) in the operands' tiles.  (Through registers, each
+            // thread looking its rows up: XX us.)  Others, whose last rows have to be zeros: row by row through registers.
+            constexpr int PR = DP / 16, RS = S::kRaw;  // 16-byte pieces of a row; halves in the ring
             const int box = maps.box, boxes = box > 0 ? kTileKeys / box : 0, lg = box > 0 ? 31 - __clz(box) : 0;
-            uint4 xk[PR], xv[PR];
-            float sk, sv;
-            int64_t at_rows = -1, at_scales = -1;  // of a tile: the lane's box's rows and scales, or the thread's row's
-            auto mine = [&](int kt) { return kt * kTileKeys + (boxes > 0 ? lane * box : t); };
-            auto ahead = [&](int kt) { return boxes > 0 && lane >= boxes ? 0 : page_of(mine(kt)); };
-            unsigned looked = 0;  // tiles looked up so far
-            auto look = [&](int kt, int id) {
-                if (boxes > 0 && lane >= boxes) return;
-                const int tok = mine(kt);
-                at_rows = place_of(tok, id);
-                at_scales = at_rows < 0 ? -1 : (int64_t)id * p.scale_page + (int64_t)(tok % p.page) * p.scale_place + (int64_t)w.kvh * p.scale_hs;
+            uint8_t *const raw = smem + S::kRawAt;
+            // pages of a tile: a lane's box's, or a thread's row's
+            auto pages = [&](int kt) { return boxes > 0 && lane >= boxes ? 0 : page_of(kt * kTileKeys + (boxes > 0 ? lane * box : t)); };
+            auto is_whole = [&](int kt, int id) {
+                if (boxes == 0 || kt * kTileKeys + kTileKeys > w.x.len) return false;
+                bool fits = lane >= boxes || (id >= 0 && id < p.n_pages);
+                if (lane < boxes && fits)
+                    fits = LEAN_SPAN((int64_t)id * p.page_stride + (int64_t)((kt * kTileKeys + lane * box) % p.page) * p.place_stride +
+                                         (int64_t)w.kvh * p.cache_hs,
+                                     (box - 1) * p.place_stride + p.dim, p.cache_extent, p.err);
+                return (bool)__all_sync(0xffffffffu, fits);
             };
-            auto share = [&]() {  // rows of a tile that are looked up one by one
-                if (boxes > 0) return true;
-                row_off[(looked & 1) * kTileKeys + t] = at_rows;
-                arrive(&bars.rows_full[looked & 1]);
-                const bool got = warp_wait(bars, &bars.rows_full[looked & 1], looked / 2 & 1, p.err);
-                ++looked;
-                return got;
-            };
-            auto load = [&](const void *cache, int kt, uint4 (&x)[PR]) {
-                const int64_t *off = row_off + ((looked - 1) & 1) * kTileKeys;
-#pragma unroll
-                for (int i = 0; i < PR; ++i) {
-                    const int row = (i * kTileKeys + t) / PR, c = t % PR;
-                    int64_t o;
-                    if (boxes > 0) {
-                        o = __shfl_sync(0xffffffffu, at_rows, row >> lg);
-                        if (o >= 0) o += (row & (box - 1)) * p.place_stride;
-                        if (kt * kTileKeys + row >= w.x.len) o = -1;
-                    } else {
-                        o = off[row];
-                    }
-                    x[i] = make_uint4(0, 0, 0, 0);
-                    if (o >= 0 && 16 * c < p.dim && LEAN_SPAN(o + 16 * c, 16, p.cache_extent, p.err))
-                        x[i] = *reinterpret_cast<const uint4 *>(static_cast<const int8_t *>(cache) + o + 16 * c);
-                }
-            };
-            auto load_scales = [&](int kt) {  // of row t
-                int64_t o = at_rows, at = at_scales;
-                if (boxes > 0) {
-                    o = __shfl_sync(0xffffffffu, at_rows, t >> lg);
-                    at = __shfl_sync(0xffffffffu, at_scales, t >> lg) + (t & (box - 1)) * p.scale_place;
-                }
-                sk = o == -2 ? CUDART_NAN_F : 1.f;
+            float sk = 1.f, sv = 0.f;
+            int64_t off = -1;
+            auto row_and_scales = [&](int kt, int ids) {  // of row t: its place, and its scales under way
+                const int tok = kt * kTileKeys + t, id = boxes > 0 ? __shfl_sync(0xffffffffu, ids, t >> lg) : ids;
+                off = place_of(tok, id);
+                sk = off == -2 ? CUDART_NAN_F : 1.f;
                 sv = 0.f;
-                if (o >= 0 && kt * kTileKeys + t < w.x.len && LEAN_IN(at, p.scale_extent, p.err)) {
-                    sk = p.k_scales[at];
-                    sv = p.v_scales[at];
+                if (off >= 0) {
+                    const int64_t at = (int64_t)id * p.scale_page + (int64_t)(tok % p.page) * p.scale_place + (int64_t)w.kvh * p.scale_hs;
+                    if (LEAN_IN(at, p.scale_extent, p.err)) {
+                        sk = p.k_scales[at];
+                        sv = p.v_scales[at];
+                    }
                 }
             };
             auto finish_scales = [&](unsigned m) {  // the values' relative to the largest of the warp's 32
@@ -864,51 +851,106 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                 if (lane == 0) bars.value_exp[m % 4][warp - 8] = e;
                 arrive(&bars.scales_full[m % 4]);
             };
-            auto convert = [&](uint8_t *tile, const uint4 (&x)[PR]) {
-#pragma unroll
-                for (int i = 0; i < PR; ++i) {
-                    const int row = (i * kTileKeys + t) / PR, c = t % PR;
-                    const uint32_t u[4] = {x[i].x ^ 0x80808080u, x[i].y ^ 0x80808080u, x[i].z ^ 0x80808080u, x[i].w ^ 0x80808080u};
-                    uint8_t *to = tile + c / 4 * S::kChunkBytes + row * 128;
-                    *reinterpret_cast<uint4 *>(to + ((2 * c % 8) ^ (row & 7)) * 16) =
-                        make_uint4(codes_f16<0x4140>(u[0]), codes_f16<0x4342>(u[0]), codes_f16<0x4140>(u[1]), codes_f16<0x4342>(u[1]));
-                    *reinterpret_cast<uint4 *>(to + ((2 * c % 8 + 1) ^ (row & 7)) * 16) =
-                        make_uint4(codes_f16<0x4140>(u[2]), codes_f16<0x4342>(u[2]), codes_f16<0x4140>(u[3]), codes_f16<0x4342>(u[3]));
-                }
-                smem_to_async();
+            auto convert = [&](uint8_t *tile, int row, int c, uint4 x) {  // piece c of a row
+                const uint32_t u[4] = {x.x ^ 0x80808080u, x.y ^ 0x80808080u, x.z ^ 0x80808080u, x.w ^ 0x80808080u};
+                uint8_t *to = tile + c / 4 * S::kChunkBytes + row * 128;
+                *reinterpret_cast<uint4 *>(to + ((2 * c % 8) ^ (row & 7)) * 16) =
+                    make_uint4(codes_f16<0x4140>(u[0]), codes_f16<0x4342>(u[0]), codes_f16<0x4140>(u[1]), codes_f16<0x4342>(u[1]));
+                *reinterpret_cast<uint4 *>(to + ((2 * c % 8 + 1) ^ (row & 7)) * 16) =
+                    make_uint4(codes_f16<0x4140>(u[2]), codes_f16<0x4342>(u[2]), codes_f16<0x4140>(u[3]), codes_f16<0x4342>(u[3]));
             };
+            unsigned issued = 0, used = 0;  // halves
+            int ahead_kt = 0, ahead_part = 0, ahead_id = 0, ahead_next = 0;  // (pages are looked up a tile ahead)
+            bool ahead_whole = false;
+            auto issue = [&]() {  // warp 8: what the ring has room for, in the order of use
+                while (ahead_kt < w.to && issued - used < RS) {
+                    if (ahead_part == 0) ahead_whole = is_whole(ahead_kt, ahead_id);
+                    if (ahead_whole) {
+                        const unsigned slot = issued % RS;
+                        if (issued >= RS && !warp_wait(bars, &bars.raw_empty[slot], (issued / RS - 1) & 1, p.err)) return false;
+                        if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[slot], S::kRawBytes);
+                        __syncwarp();
+                        const int b0 = ahead_part % 2 * (boxes / 2);
+                        if (lane >= b0 && lane < b0 + boxes / 2)
+                            copy_box(smem_addr(raw + slot * S::kRawBytes + (lane - b0) * box * DP), ahead_part < 2 ? &maps.k : &maps.v, 0,
+                                     (ahead_kt * kTileKeys + lane * box) % p.page, w.kvh, ahead_id, &bars.raw_full[slot]);
+                        ++issued;
+                    }
+                    if (!ahead_whole || ++ahead_part == 4) {
+                        ahead_part = 0;
+                        ++ahead_kt;
+                        ahead_id = ahead_next;
+                        ahead_next = ahead_kt + 1 < w.to ? pages(ahead_kt + 1) : 0;
+                    }
+                }
+                return true;
+            };
+            unsigned shared_rows = 0;  // tiles taken row by row so far
             while (ok && w.next(p)) {
-                look(w.from, ahead(w.from));
-                int next_id = w.from + 1 < w.to ? ahead(w.from + 1) : 0;
-                ok = share();
-                if (!ok) break;
-                load(p.k, w.from, xk);
-                load_scales(w.from);
-                load(p.v, w.from, xv);
-                finish_scales(n);
+                ahead_kt = w.from;
+                ahead_part = 0;
+                ahead_id = pages(w.from);
+                ahead_next = w.from + 1 < w.to ? pages(w.from + 1) : 0;
+                int id = ahead_id, next_id = ahead_next;
+                if (warp == 8) ok = issue();
+                row_and_scales(w.from, id);
                 for (int kt = w.from; ok && kt < w.to; ++kt, ++n) {
-                    const bool more = kt + 1 < w.to;
-                    if (more) {
-                        look(kt + 1, next_id);
-                        if (kt + 2 < w.to) next_id = ahead(kt + 2);
+                    const int64_t row_at = off;  // (of this tile)
+                    finish_scales(n);
+                    const bool whole = is_whole(kt, id);
+                    if (kt + 1 < w.to) {
+                        id = next_id;
+                        next_id = kt + 2 < w.to ? pages(kt + 2) : 0;
+                        row_and_scales(kt + 1, id);
                     }
-                    if (n >= KS) ok = warp_wait(bars, &bars.k_empty[n % KS], (n / KS - 1) & 1, p.err);
-                    if (!ok) break;
-                    convert(k_tiles + n % KS * S::kTileBytes, xk);
-                    arrive(&bars.k_full[n % KS]);
-                    if (more) {
-                        ok = share();
+                    uint8_t *const tiles[2] = {k_tiles + n % KS * S::kTileBytes, v_tiles + n % VS * S::kTileBytes};
+                    if (whole) {
+#pragma unroll 1
+                        for (int part = 0; part < 4; ++part) {
+                            const unsigned slot = used % RS;
+                            if (part == 0 && n >= KS) ok = warp_wait(bars, &bars.k_empty[n % KS], (n / KS - 1) & 1, p.err);
+                            if (part == 2 && n >= VS) ok = ok && warp_wait(bars, &bars.v_empty[n % VS], (n / VS - 1) & 1, p.err);
+                            ok = ok && warp_wait(bars, &bars.raw_full[slot], used / RS & 1, p.err);
+                            if (!ok) break;
+                            uint4 x[PR / 2];
+#pragma unroll
+                            for (int i = 0; i < PR / 2; ++i)
+                                x[i] = *reinterpret_cast<const uint4 *>(raw + slot * S::kRawBytes + (i * 128 + t) * 16);
+#pragma unroll
+                            for (int i = 0; i < PR / 2; ++i)
+                                convert(part < 2 ? tiles[0] : tiles[1], part % 2 * kHalfKeys + (i * 128 + t) / PR, t % PR, x[i]);
+                            if (part % 2) smem_to_async();
+                            arrive(&bars.raw_empty[slot]);
+                            if (part % 2 && lane == 0) mbar_arrive(part < 2 ? &bars.k_full[n % KS] : &bars.v_full[n % VS]);
+                            ++used;
+                            if (warp == 8) ok = issue();
+                            if (!ok) break;
+                        }
+                    } else {
+                        int64_t *const offs = row_off + (shared_rows & 1) * kTileKeys;
+                        offs[t] = row_at;
+                        arrive(&bars.rows_full[shared_rows & 1]);
+                        ok = warp_wait(bars, &bars.rows_full[shared_rows & 1], shared_rows / 2 & 1, p.err);
+                        ++shared_rows;
+                        if (n >= KS) ok = ok && warp_wait(bars, &bars.k_empty[n % KS], (n / KS - 1) & 1, p.err);
+                        if (n >= VS) ok = ok && warp_wait(bars, &bars.v_empty[n % VS], (n / VS - 1) & 1, p.err);
                         if (!ok) break;
-                        load(p.k, kt + 1, xk);
-                        load_scales(kt + 1);
-                    }
-                    if (n >= VS) ok = warp_wait(bars, &bars.v_empty[n % VS], (n / VS - 1) & 1, p.err);
-                    if (!ok) break;
-                    convert(v_tiles + n % VS * S::kTileBytes, xv);
-                    arrive(&bars.v_full[n % VS]);
-                    if (more) {
-                        load(p.v, kt + 1, xv);
-                        finish_scales(n + 1);
+#pragma unroll 1
+                        for (int kv = 0; kv < 2; ++kv) {
+                            const int8_t *cache = static_cast<const int8_t *>(kv ? p.v : p.k);
+                            uint4 x[PR];
+#pragma unroll
+                            for (int i = 0; i < PR; ++i) {
+                                const int c = t % PR;
+                                const int64_t o = offs[(i * 128 + t) / PR];
+                                x[i] = make_uint4(0, 0, 0, 0);
+                                if (o >= 0 && 16 * c < p.dim) x[i] = *reinterpret_cast<const uint4 *>(cache + o + 16 * c);
+                            }
+#pragma unroll
+                            for (int i = 0; i < PR; ++i) convert(tiles[kv], (i * 128 + t) / PR, t % PR, x[i]);
+                            smem_to_async();
+                            arrive(kv ? &bars.v_full[n % VS] : &bars.k_full[n % KS]);
+                        }
                     }
                 }
             }
@@ -995,6 +1037,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                 }
             }
             cp_async_wait<0>();
+        }
+        if (!ok) {  // a wait ran out: copies on their way land before the block's memory is another's
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 1000000) {}
         }
         for (unsigned j = n > KS ? n - KS : 0; ok && j < n; ++j) ok = warp_wait(bars, &bars.k_empty[j % KS], j / KS & 1, p.err);
         for (unsigned j = n > VS ? n - VS : 0; ok && j < n; ++j) ok = warp_wait(bars, &bars.v_empty[j % VS], j / VS & 1, p.err);

@@ -4,8 +4,7 @@
 namespace lean {
 
 lean_status prefix_cache8(const PrefixArgs &p, bool two, int64_t flags, void *stream) {
-    PrefixMaps maps = {};  // (no tensors: the boxes' size alone)
-    maps.box = prefix_box(p.page);
+    const PrefixMaps maps = prefix_maps(p, PrefixCache::kI8);
     return p.dim <= 64 ? pick_prefix<int8_t, 64>(maps, p, two, flags, stream)
                        : pick_prefix<int8_t, 128>(maps, p, two, flags, stream);
 }
