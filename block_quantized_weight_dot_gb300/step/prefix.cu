@@ -23,13 +23,13 @@ EncodeTiled encode_tiled() {
 
 namespace lean {
 
-// The caches as tensors in boxes of prefix_box() places (8 or more: rows of a tile lie in groups of 8; in 8 bits half a
-// tile at most); none where a stride is 0 between rows that are not one.  16-bit rows are copied to where the matrix
+// The caches as tensors in boxes of prefix_box() places (8 or more: rows of a tile lie in groups of 8; in 8 bits what a
+// stage of the ring holds at most); none where a stride is 0 between rows that are not one.  16-bit rows are copied to where the matrix
 // instructions read them, rows in 8 bits as they lie.
 PrefixMaps prefix_maps(const PrefixArgs &p, PrefixCache type) {
     PrefixMaps m = {};
     const bool in8 = type == PrefixCache::kI8;
-    const int box = prefix_box(p.page, in8 ? kHalfKeys : kTileKeys);
+    const int box = prefix_box(p.page, !in8 ? kTileKeys : p.dim <= 64 ? 64 : 32);
     const EncodeTiled encode = encode_tiled();
     if (box == 0 || !encode || (p.page > 1 && p.place_stride == 0) || (p.hkv > 1 && p.cache_hs == 0) ||
         (p.n_pages > 1 && p.page_stride == 0))

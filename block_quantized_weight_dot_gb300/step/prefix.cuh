@@ -48,7 +48,23 @@ namespace lean {
 
 constexpr int kHalfKeys = 64;  // of a tile
 constexpr int kPrefixMaxCtas = 160;
-constexpr int kPrefixThreads = 512;
+// Threads of a block (in 8 bits a fifth group of four warps issues copies), and the registers that each of
+// its groups of 128 has after the start: together what the block is launched with, 128 (in 8 bits 96) for each thread.
+// setmaxnreg waits forever for more than that.
+constexpr int prefix_threads(bool in8) { return in8 ? 640 : 512; }
+struct PrefixRegs {
+    int rows, loaders, mma, issuer;
+};
+constexpr PrefixRegs prefix_regs(bool in8, int pp) {
+    return in8 ? (pp == 1 ? PrefixRegs{136, 72, 80, 56} : PrefixRegs{160, 56, 56, 48})
+               : (pp == 1 ? PrefixRegs{152, 120, 88, 0} : PrefixRegs{192, 72, 56, 0});
+}
+constexpr bool prefix_regs_fit(bool in8, int pp) {
+    const PrefixRegs r = prefix_regs(in8, pp);
+    return 2 * r.rows + r.loaders + r.mma + r.issuer <= (in8 ? 96 * 5 : 128 * 4);
+}
+static_assert(prefix_regs_fit(false, 1) && prefix_regs_fit(false, 3) && prefix_regs_fit(true, 1) && prefix_regs_fit(true, 3),
+              "registers of a block");
 // Halves of tiles whose products are summed in tensor memory before they are added in fp32 (one part of p): what is below
 // 2^-24 of a sum is cut off when it is added, 16 keys at a time, so that a row errs by 2^-16 of its largest sum at most.
 constexpr int kFoldHalves = 32;
@@ -171,8 +187,10 @@ struct PrefixShape {
     static constexpr int kKStages = 2, kVStages = QP == 3 && DP == 128 ? 1 : 2;
     static constexpr int kOff = kQ + (kKStages + kVStages) * kTileBytes;  // rows' places, two tiles
     static constexpr int kScaleAt = kOff + 2 * kTileKeys * 8;             // scales of four tiles, keys and values
-    // caches in 8 bits: halves of tiles as they lie in the cache
-    static constexpr int kRaw = kIn8 ? (DP == 64 ? 6 : 3) : 0, kRawBytes = kHalfKeys * DP;
+    // caches in 8 bits: runs of rows as they lie in the cache, keys' then values' of a tile, kRawDepth for each of the four
+    // warps that issue them in turn
+    static constexpr int kRawRows = DP == 64 ? 64 : 32, kRawBytes = kRawRows * DP, kRuns = 2 * kTileKeys / kRawRows;
+    static constexpr int kRawDepth = DP == 64 ? 2 : 1, kRaw = kIn8 ? 4 * kRawDepth : 0;
     static constexpr int kRawAt = kScaleAt + (kIn8 ? 4 * 2 * kTileKeys * 4 : 0);  // (a multiple of 128)
     static constexpr int kBars = kRawAt + kRaw * kRawBytes;
     static constexpr int kSmem = kBars + 640;
@@ -192,11 +210,13 @@ struct PrefixBars {
     uint64_t q_full, q_free;                                // q is there; both groups are done with it
     uint64_t rows_full[2];                                  // a tile's rows' places are there
     uint64_t scales_full[4];
-    uint64_t raw_full[6], raw_empty[6];                     // halves of tiles in 8 bits are there, were used
+    uint64_t raw_full[8], raw_empty[8];                     // runs of rows in 8 bits are there, were used
+    uint64_t tile_ready[4], tile_done[4];                   // what is known of a tile in 8 bits, and that it was taken
     uint64_t last;                                          // every matrix instruction is done
     uint32_t tmem;
     int dead;            // a wait ran out: everyone leaves
     int value_exp[4][4]; // exponents of the largest value scales of 32 keys, of four tiles
+    int tile_whole[4];   // tiles in 8 bits: whether their rows come through the ring
     int start_i;         // the run's first prefix and place in it
     unsigned start_off;
 };
@@ -335,7 +355,7 @@ __device__ __forceinline__ uint32_t load_q(const PrefixArgs &p, int64_t q_at, ui
 }
 
 template <typename C, int DP, int QP, int PP, int NQ>
-__global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_constant__ PrefixMaps maps, const PrefixArgs p) {
+__global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kernel(const __grid_constant__ PrefixMaps maps, const PrefixArgs p) {
     using S = PrefixShape<C, DP, QP, PP, NQ>;
     using T = typename Operand<C>::type;
     constexpr bool IN8 = S::kIn8, BF16 = std::is_same<T, __nv_bfloat16>::value;
@@ -354,7 +374,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
 
     // ---- this block's run of the list
     unsigned *const before = reinterpret_cast<unsigned *>(smem);  // (the tiles' room, unused yet)
-    const int per = (p.n_prefixes + kPrefixThreads - 1) / kPrefixThreads;
+    constexpr int THREADS = prefix_threads(IN8);
+    constexpr PrefixRegs REGS = prefix_regs(IN8, PP);
+    const int per = (p.n_prefixes + THREADS - 1) / THREADS;
     const int lo = min(p.n_prefixes, (int)threadIdx.x * per), hi = min(p.n_prefixes, lo + per);
     unsigned mine = 0;
     for (int i = lo; i < hi; ++i) mine += open_prefix(p.list, i, p.err).cost(p.hkv);
@@ -366,7 +388,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     }
     if (lane == 31) before[warp] = incl;
     unsigned own = 0;  // units of sequences' own tokens, as attend.cuh counts them
-    for (int i = threadIdx.x; i < p.n_seqs; i += kPrefixThreads) {
+    for (int i = threadIdx.x; i < p.n_seqs; i += THREADS) {
         const int len = min(LEAN_IN(i, p.n_seqs, p.err) ? max(p.own_lens[i], 0) : 0, p.own_most);
         own += (unsigned)(max(1, len / kUnit + (len % kUnit != 0)) + kAttItemUnits) * p.own_groups;
     }
@@ -384,8 +406,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                 mbar_init(&bars.o_full[i][b], 1);
             }
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&bars.scales_full[i], 4);
-        for (int i = 0; i < 6; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bars.scales_full[i], 4);
+            mbar_init(&bars.tile_ready[i], 4);
+            mbar_init(&bars.tile_done[i], 4);
+        }
+        for (int i = 0; i < 8; ++i) {
             mbar_init(&bars.raw_full[i], 1);
             mbar_init(&bars.raw_empty[i], 4);
         }
@@ -401,7 +427,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     unsigned begins = incl - mine, total = 0;
     own = 0;
 #pragma unroll
-    for (int i = 0; i < kPrefixThreads / 32; ++i) {
+    for (int i = 0; i < THREADS / 32; ++i) {
         if (i < warp) begins += before[i];
         total += before[i];
         own += before[32 + i];
@@ -435,7 +461,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
 
     if (warp < 8) {
         // ---- scores to probabilities, products to outputs: a thread has a row
-        regs_up<PP == 1 ? 152 : 192>();
+        regs_up<REGS.rows>();
         const int g = warp / 4, r = threadIdx.x % kTileRows;
         const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // this warp's 32 lanes of tensor memory
         const uint32_t s_group = tmem + lanes + S::scores(g, 0), o_at = tmem + lanes + S::outputs(g);
@@ -583,11 +609,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                     tm_ld64(s_at, x);
                     if (IN8) {
 #pragma unroll
-                        for (int i = 0; i < kHalfKeys; i += 2) {
-                            const float2 z = unpack2(mul2(pack2(__uint_as_float(x[i / 32][i % 32]), __uint_as_float(x[i / 32][i % 32 + 1])),
-                                                          *reinterpret_cast<const f32x2 *>(ks + i)));
-                            x[i / 32][i % 32] = __float_as_uint(z.x);
-                            x[i / 32][i % 32 + 1] = __float_as_uint(z.y);
+                        for (int i = 0; i < kHalfKeys; i += 4) {
+                            const float4 k = *reinterpret_cast<const float4 *>(ks + i);
+                            uint32_t *z = &x[i / 32][i % 32];
+                            const float2 a = unpack2(mul2(pack2(__uint_as_float(z[0]), __uint_as_float(z[1])), pack2(k.x, k.y)));
+                            const float2 b = unpack2(mul2(pack2(__uint_as_float(z[2]), __uint_as_float(z[3])), pack2(k.z, k.w)));
+                            z[0] = __float_as_uint(a.x);
+                            z[1] = __float_as_uint(a.y);
+                            z[2] = __float_as_uint(b.x);
+                            z[3] = __float_as_uint(b.y);
                         }
                     }
                     if (limit < kHalfKeys) {
@@ -603,12 +633,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                             uint32_t part[16];
                             const f32x2 shift2 = pack2(shift[c], shift[c]);
                             f32x2 sum2 = 0;
+                            float4 v;
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
                                 const float2 a = unpack2(fma2(pack2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), zs2, shift2));
                                 float2 e = make_float2(ex2(a.x), ex2(a.y));
                                 sum2 = add2(sum2, pack2(e.x, e.y));
-                                if (IN8) e = unpack2(mul2(pack2(e.x, e.y), *reinterpret_cast<const f32x2 *>(vs + 32 * c + i)));
+                                if (IN8) {
+                                    if (i % 4 == 0) v = *reinterpret_cast<const float4 *>(vs + 32 * c + i);
+                                    e = unpack2(mul2(pack2(e.x, e.y), i % 4 == 0 ? pack2(v.x, v.y) : pack2(v.z, v.w)));
+                                }
                                 part[i / 2] = take_part<T>(e.x, e.y);
                             }
                             const float2 sum = unpack2(sum2);
@@ -785,7 +819,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         }
     } else if (warp < 12) {
         // ---- keys and values into shared memory
-        regs_down<PP == 1 ? 120 : IN8 ? 80 : 72>();
+        regs_down<REGS.loaders>();
         const int t = threadIdx.x - 256;
         unsigned n = 0;
         bool ok = true;
@@ -808,49 +842,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             if (lane == 0) mbar_arrive(bar);
         };
         if constexpr (IN8) {
-            // Whole tiles in pages that the cache has come as boxes into a ring of halves of tiles, as they lie in the cache;
-            // all four warps turn them into f16 (codes are exact in it) in the operands' tiles.  (Through registers, each
-            // thread looking its rows up: XX us.)  Others, whose last rows have to be zeros: row by row through registers.
-            constexpr int PR = DP / 16, RS = S::kRaw;  // 16-byte pieces of a row; halves in the ring
-            const int box = maps.box, boxes = box > 0 ? kTileKeys / box : 0, lg = box > 0 ? 31 - __clz(box) : 0;
+            // Runs of rows as they lie in the cache, in the ring that the last four warps fill, become f16 (codes are
+            // exact in it) in the operands' tiles; tiles that are not whole come row by row through registers.  (Rows looked
+            // up and loaded by these threads: XX us, boxes issued between them: XX.)
+            constexpr int PR = DP / 16, RUNS = S::kRuns, PIECES = S::kRawRows * PR / 128;  // 16-byte pieces: of a row, of a thread
             uint8_t *const raw = smem + S::kRawAt;
-            // pages of a tile: a lane's box's, or a thread's row's
-            auto pages = [&](int kt) { return boxes > 0 && lane >= boxes ? 0 : page_of(kt * kTileKeys + (boxes > 0 ? lane * box : t)); };
-            auto is_whole = [&](int kt, int id) {
-                if (boxes == 0 || kt * kTileKeys + kTileKeys > w.x.len) return false;
-                bool fits = lane >= boxes || (id >= 0 && id < p.n_pages);
-                if (lane < boxes && fits)
-                    fits = LEAN_SPAN((int64_t)id * p.page_stride + (int64_t)((kt * kTileKeys + lane * box) % p.page) * p.place_stride +
-                                         (int64_t)w.kvh * p.cache_hs,
-                                     (box - 1) * p.place_stride + p.dim, p.cache_extent, p.err);
-                return (bool)__all_sync(0xffffffffu, fits);
-            };
-            float sk = 1.f, sv = 0.f;
-            int64_t off = -1;
-            auto row_and_scales = [&](int kt, int ids) {  // of row t: its place, and its scales under way
-                const int tok = kt * kTileKeys + t, id = boxes > 0 ? __shfl_sync(0xffffffffu, ids, t >> lg) : ids;
-                off = place_of(tok, id);
-                sk = off == -2 ? CUDART_NAN_F : 1.f;
-                sv = 0.f;
-                if (off >= 0) {
-                    const int64_t at = (int64_t)id * p.scale_page + (int64_t)(tok % p.page) * p.scale_place + (int64_t)w.kvh * p.scale_hs;
-                    if (LEAN_IN(at, p.scale_extent, p.err)) {
-                        sk = p.k_scales[at];
-                        sv = p.v_scales[at];
-                    }
-                }
-            };
-            auto finish_scales = [&](unsigned m) {  // the values' relative to the largest of the warp's 32
-                float top = fmaxf(sv, 0.f);
-#pragma unroll
-                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const int e = min(252, max(1, (int)(__float_as_uint(top) >> 23)));
-                float *to = scales + m % 4 * 2 * kTileKeys + t;
-                to[0] = sk + (sk - sk);  // (an infinite one is NaN, as the scores of such a key are)
-                to[kTileKeys] = sv * __uint_as_float((uint32_t)(253 - e) << 23);
-                if (lane == 0) bars.value_exp[m % 4][warp - 8] = e;
-                arrive(&bars.scales_full[m % 4]);
-            };
             auto convert = [&](uint8_t *tile, int row, int c, uint4 x) {  // piece c of a row
                 const uint32_t u[4] = {x.x ^ 0x80808080u, x.y ^ 0x80808080u, x.z ^ 0x80808080u, x.w ^ 0x80808080u};
                 uint8_t *to = tile + c / 4 * S::kChunkBytes + row * 128;
@@ -859,99 +855,54 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
                 *reinterpret_cast<uint4 *>(to + ((2 * c % 8 + 1) ^ (row & 7)) * 16) =
                     make_uint4(codes_f16<0x4140>(u[2]), codes_f16<0x4342>(u[2]), codes_f16<0x4140>(u[3]), codes_f16<0x4342>(u[3]));
             };
-            unsigned issued = 0, used = 0;  // halves
-            int ahead_kt = 0, ahead_part = 0, ahead_id = 0, ahead_next = 0;  // (pages are looked up a tile ahead)
-            bool ahead_whole = false;
-            auto issue = [&]() {  // warp 8: what the ring has room for, in the order of use
-                while (ahead_kt < w.to && issued - used < RS) {
-                    if (ahead_part == 0) ahead_whole = is_whole(ahead_kt, ahead_id);
-                    if (ahead_whole) {
-                        const unsigned slot = issued % RS;
-                        if (issued >= RS && !warp_wait(bars, &bars.raw_empty[slot], (issued / RS - 1) & 1, p.err)) return false;
-                        if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[slot], S::kRawBytes);
-                        __syncwarp();
-                        const int b0 = ahead_part % 2 * (boxes / 2);
-                        if (lane >= b0 && lane < b0 + boxes / 2)
-                            copy_box(smem_addr(raw + slot * S::kRawBytes + (lane - b0) * box * DP), ahead_part < 2 ? &maps.k : &maps.v, 0,
-                                     (ahead_kt * kTileKeys + lane * box) % p.page, w.kvh, ahead_id, &bars.raw_full[slot]);
-                        ++issued;
-                    }
-                    if (!ahead_whole || ++ahead_part == 4) {
-                        ahead_part = 0;
-                        ++ahead_kt;
-                        ahead_id = ahead_next;
-                        ahead_next = ahead_kt + 1 < w.to ? pages(ahead_kt + 1) : 0;
-                    }
-                }
-                return true;
-            };
-            unsigned shared_rows = 0;  // tiles taken row by row so far
+            unsigned used = 0;  // runs
             while (ok && w.next(p)) {
-                ahead_kt = w.from;
-                ahead_part = 0;
-                ahead_id = pages(w.from);
-                ahead_next = w.from + 1 < w.to ? pages(w.from + 1) : 0;
-                int id = ahead_id, next_id = ahead_next;
-                if (warp == 8) ok = issue();
-                row_and_scales(w.from, id);
                 for (int kt = w.from; ok && kt < w.to; ++kt, ++n) {
-                    const int64_t row_at = off;  // (of this tile)
-                    finish_scales(n);
-                    const bool whole = is_whole(kt, id);
-                    if (kt + 1 < w.to) {
-                        id = next_id;
-                        next_id = kt + 2 < w.to ? pages(kt + 2) : 0;
-                        row_and_scales(kt + 1, id);
-                    }
+                    ok = warp_wait(bars, &bars.tile_ready[n % 4], n / 4 & 1, p.err);
+                    if (!ok) break;
                     uint8_t *const tiles[2] = {k_tiles + n % KS * S::kTileBytes, v_tiles + n % VS * S::kTileBytes};
-                    if (whole) {
+                    if (bars.tile_whole[n % 4]) {
 #pragma unroll 1
-                        for (int part = 0; part < 4; ++part) {
-                            const unsigned slot = used % RS;
-                            if (part == 0 && n >= KS) ok = warp_wait(bars, &bars.k_empty[n % KS], (n / KS - 1) & 1, p.err);
-                            if (part == 2 && n >= VS) ok = ok && warp_wait(bars, &bars.v_empty[n % VS], (n / VS - 1) & 1, p.err);
-                            ok = ok && warp_wait(bars, &bars.raw_full[slot], used / RS & 1, p.err);
+                        for (int run = 0; run < RUNS; ++run) {
+                            const unsigned times = used / 4, slot = used % 4 + 4 * (times % S::kRawDepth);
+                            if (run == 0 && n >= KS) ok = warp_wait(bars, &bars.k_empty[n % KS], (n / KS - 1) & 1, p.err);
+                            if (run == RUNS / 2 && n >= VS) ok = ok && warp_wait(bars, &bars.v_empty[n % VS], (n / VS - 1) & 1, p.err);
+                            ok = ok && warp_wait(bars, &bars.raw_full[slot], times / S::kRawDepth & 1, p.err);
                             if (!ok) break;
-                            uint4 x[PR / 2];
+                            uint4 x[PIECES];
 #pragma unroll
-                            for (int i = 0; i < PR / 2; ++i)
+                            for (int i = 0; i < PIECES; ++i)
                                 x[i] = *reinterpret_cast<const uint4 *>(raw + slot * S::kRawBytes + (i * 128 + t) * 16);
 #pragma unroll
-                            for (int i = 0; i < PR / 2; ++i)
-                                convert(part < 2 ? tiles[0] : tiles[1], part % 2 * kHalfKeys + (i * 128 + t) / PR, t % PR, x[i]);
-                            if (part % 2) smem_to_async();
+                            for (int i = 0; i < PIECES; ++i)
+                                convert(tiles[run >= RUNS / 2], run % (RUNS / 2) * S::kRawRows + (i * 128 + t) / PR, t % PR, x[i]);
+                            const bool last = run % (RUNS / 2) == RUNS / 2 - 1;
+                            if (last) smem_to_async();
                             arrive(&bars.raw_empty[slot]);
-                            if (part % 2 && lane == 0) mbar_arrive(part < 2 ? &bars.k_full[n % KS] : &bars.v_full[n % VS]);
+                            if (last && lane == 0) mbar_arrive(run < RUNS / 2 ? &bars.k_full[n % KS] : &bars.v_full[n % VS]);
                             ++used;
-                            if (warp == 8) ok = issue();
-                            if (!ok) break;
                         }
                     } else {
-                        int64_t *const offs = row_off + (shared_rows & 1) * kTileKeys;
-                        offs[t] = row_at;
-                        arrive(&bars.rows_full[shared_rows & 1]);
-                        ok = warp_wait(bars, &bars.rows_full[shared_rows & 1], shared_rows / 2 & 1, p.err);
-                        ++shared_rows;
-                        if (n >= KS) ok = ok && warp_wait(bars, &bars.k_empty[n % KS], (n / KS - 1) & 1, p.err);
+                        const int64_t *const offs = row_off + (n & 1) * kTileKeys;
+                        if (n >= KS) ok = warp_wait(bars, &bars.k_empty[n % KS], (n / KS - 1) & 1, p.err);
                         if (n >= VS) ok = ok && warp_wait(bars, &bars.v_empty[n % VS], (n / VS - 1) & 1, p.err);
                         if (!ok) break;
 #pragma unroll 1
                         for (int kv = 0; kv < 2; ++kv) {
                             const int8_t *cache = static_cast<const int8_t *>(kv ? p.v : p.k);
-                            uint4 x[PR];
-#pragma unroll
+#pragma unroll 1
                             for (int i = 0; i < PR; ++i) {
-                                const int c = t % PR;
-                                const int64_t o = offs[(i * 128 + t) / PR];
-                                x[i] = make_uint4(0, 0, 0, 0);
-                                if (o >= 0 && 16 * c < p.dim) x[i] = *reinterpret_cast<const uint4 *>(cache + o + 16 * c);
+                                const int c = t % PR, row = (i * 128 + t) / PR;
+                                const int64_t o = offs[row];
+                                uint4 x = make_uint4(0, 0, 0, 0);
+                                if (o >= 0 && 16 * c < p.dim) x = *reinterpret_cast<const uint4 *>(cache + o + 16 * c);
+                                convert(tiles[kv], row, c, x);
                             }
-#pragma unroll
-                            for (int i = 0; i < PR; ++i) convert(tiles[kv], (i * 128 + t) / PR, t % PR, x[i]);
                             smem_to_async();
                             arrive(kv ? &bars.v_full[n % VS] : &bars.k_full[n % KS]);
                         }
                     }
+                    if (ok) arrive(&bars.tile_done[n % 4]);
                 }
             }
         } else {
@@ -1044,8 +995,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         }
         for (unsigned j = n > KS ? n - KS : 0; ok && j < n; ++j) ok = warp_wait(bars, &bars.k_empty[j % KS], j / KS & 1, p.err);
         for (unsigned j = n > VS ? n - VS : 0; ok && j < n; ++j) ok = warp_wait(bars, &bars.v_empty[j % VS], j / VS & 1, p.err);
-    } else {
-        regs_down<PP == 1 ? 88 : IN8 ? 48 : 56>();
+    } else if (warp < 16) {
+        regs_down<REGS.mma>();
         if (lane == 0) {
             // ---- matrix instructions: warps 12 and 13 issue the groups' scores, 14 and 15 their products.  (One thread
             // needs about 110 cycles for an instruction that runs for 64: one warp for all of them 58 us where four
@@ -1137,6 +1088,126 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             tm_commit(&bars.last);
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(&bars.last, 0) && globaltimer_ns() - t0 < kPrefixWaitNs) {}
+        }
+    }
+    if constexpr (IN8) {
+        if (warp >= 16) {
+            // ---- what is known of a tile, and its rows into the ring: each of four warps has 32 rows' scales and every
+            // fourth run of the tile's rows, in stages of the ring of its own.  A lane looks up the page of a box of rows,
+            // where pages do not fit boxes that of its row, a tile ahead.
+            regs_down<REGS.issuer>();
+            const int mine = warp - 16, box = maps.box, boxes = box > 0 ? kTileKeys / box : 0, lg = box > 0 ? 31 - __clz(box) : 0;
+            uint8_t *const raw = smem + S::kRawAt;
+            const int first_tok = boxes > 0 ? lane * box : 32 * mine + lane;  // of a tile: the lane's box's, or its row's
+            const int page_step = kTileKeys / p.page, place_step = kTileKeys - page_step * p.page;
+            unsigned n = 0, sent = 0;  // tiles, runs of this warp
+            bool ok = true;
+            while (ok && w.next(p)) {
+                // the page (of the prefix) and place of the lane's token in the tile that is looked up, and those of the tile
+                // at hand
+                int page = (w.from * kTileKeys + first_tok) / p.page, place = w.from * kTileKeys + first_tok - page * p.page;
+                auto look = [&](int kt) {
+                    const int64_t e = (int64_t)w.i * p.table_stride + page;
+                    const bool in = (boxes == 0 || lane < boxes) && kt * kTileKeys + first_tok < w.x.len &&
+                                    LEAN_IN(e, (int64_t)(p.n_prefixes - 1) * p.table_stride + p.width, p.err);
+                    return in ? p.table[e] : 0;
+                };
+                auto step = [&]() {
+                    page += page_step;
+                    place += place_step;
+                    if (place >= p.page) {
+                        place -= p.page;
+                        ++page;
+                    }
+                };
+                float sk, sv;
+                int64_t off;
+                bool whole;
+                int id = look(w.from), at_place = place;
+                step();
+                int next_id = w.from + 1 < w.to ? look(w.from + 1) : 0;
+                auto row = [&](int kt) {  // 32 mine + lane of tile kt; its scales under way
+                    const int r = 32 * mine + lane, tok = kt * kTileKeys + r;
+                    const bool real = id >= 0 && id < p.n_pages;
+                    whole = boxes > 0 && kt * kTileKeys + kTileKeys <= w.x.len;
+                    bool fits = (boxes > 0 && lane >= boxes) || real;
+                    if (boxes > 0 && lane < boxes && real && whole)
+                        fits = LEAN_SPAN((int64_t)id * p.page_stride + (int64_t)at_place * p.place_stride + (int64_t)w.kvh * p.cache_hs,
+                                         (box - 1) * p.place_stride + p.dim, p.cache_extent, p.err);
+                    whole = whole && __all_sync(0xffffffffu, fits);
+                    const int of_id = boxes > 0 ? __shfl_sync(0xffffffffu, id, r >> lg) : id;
+                    const int of_place = boxes > 0 ? __shfl_sync(0xffffffffu, at_place, r >> lg) + (r & (box - 1)) : at_place;
+                    off = -1;
+                    sk = 1.f;
+                    sv = 0.f;
+                    if (tok < w.x.len) {
+                        if (of_id < 0 || of_id >= p.n_pages) {
+                            off = -2;
+                            sk = CUDART_NAN_F;
+                            atomicOr(p.err, kErrSlot);
+                        } else {
+                            if (!whole) {
+                                off = (int64_t)of_id * p.page_stride + (int64_t)of_place * p.place_stride + (int64_t)w.kvh * p.cache_hs;
+                                if (!LEAN_SPAN(off, p.dim, p.cache_extent, p.err)) off = -1;
+                            }
+                            const int64_t at = (int64_t)of_id * p.scale_page + (int64_t)of_place * p.scale_place + (int64_t)w.kvh * p.scale_hs;
+                            if (LEAN_IN(at, p.scale_extent, p.err)) {
+                                sk = p.k_scales[at];
+                                sv = p.v_scales[at];
+                            }
+                        }
+                    }
+                };
+                row(w.from);
+                for (int kt = w.from; kt < w.to; ++kt, ++n) {
+                    // (with tile n - 2 taken, scores of n - 4 are done with their scales)
+                    if (n >= 2) ok = warp_wait(bars, &bars.tile_done[(n - 2) % 4], (n - 2) / 4 & 1, p.err);
+                    if (!ok) break;
+                    auto send = [&](int run) {
+                        const unsigned slot = mine + 4 * (sent % S::kRawDepth), times = sent / S::kRawDepth;
+                        if (times > 0 && !warp_wait(bars, &bars.raw_empty[slot], (times - 1) & 1, p.err)) return false;
+                        if (lane == 0) mbar_arrive_expect_tx(&bars.raw_full[slot], S::kRawBytes);
+                        __syncwarp();
+                        const int each = S::kRawRows >> lg, b = lane - run % (S::kRuns / 2) * each;
+                        if (b >= 0 && b < each)
+                            copy_box(smem_addr(raw + slot * S::kRawBytes + b * box * DP), run < S::kRuns / 2 ? &maps.k : &maps.v, 0,
+                                     at_place, w.kvh, id, &bars.raw_full[slot]);
+                        ++sent;
+                        return true;
+                    };
+                    if (whole) ok = send(mine);  // (first: it takes longest)
+                    if (!ok) break;
+                    // the values' scales relative to the largest of 32
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, sv > 0.f ? __float_as_uint(sv) : 0u);
+                    const int e = min(252, max(1, (int)(top >> 23)));
+                    float *const to = scales + n % 4 * 2 * kTileKeys + 32 * mine + lane;
+                    to[0] = sk + (sk - sk);  // (an infinite one is NaN, as the scores of such a key are)
+                    to[kTileKeys] = sv * __uint_as_float((uint32_t)(253 - e) << 23);
+                    if (!whole) row_off[(n & 1) * kTileKeys + 32 * mine + lane] = off;
+                    if (lane == 0) {
+                        bars.value_exp[n % 4][mine] = e;
+                        if (mine == 0) bars.tile_whole[n % 4] = whole;
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bars.tile_ready[n % 4]);
+                        mbar_arrive(&bars.scales_full[n % 4]);
+                    }
+                    for (int run = mine + 4; ok && whole && run < S::kRuns; run += 4) ok = send(run);
+                    if (!ok) break;
+                    if (kt + 1 < w.to) {
+                        id = next_id;
+                        at_place = place;
+                        row(kt + 1);
+                        step();
+                        if (kt + 2 < w.to) next_id = look(kt + 2);
+                    }
+                }
+            }
+            if (!ok) {  // as above
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 1000000) {}
+            }
         }
     }
     tm_before();
@@ -1278,7 +1349,7 @@ lean_status launch_prefix(const PrefixMaps &maps, const PrefixArgs &p, int64_t f
     static_assert(S::kSmemAsked <= 232448, "shared memory");
     auto kern = prefix_kernel<C, DP, QP, PP, NQ>;
     if (!step_ensure_smem(kern, S::kSmemAsked, done)) return LEAN_ERR_CUDA;
-    return step_launch(kern, std::min(step_sm_count(), kPrefixMaxCtas), kPrefixThreads, S::kSmemAsked, flags, stream, maps, p);
+    return step_launch(kern, std::min(step_sm_count(), kPrefixMaxCtas), prefix_threads(S::kIn8), S::kSmemAsked, flags, stream, maps, p);
 }
 // 16-bit activations whose q is exact in one part (f16 on bf16 caches is not): one part each, two tiles of rows where
 // prefixes have more than one; else three parts of q and two of p.
