@@ -5,7 +5,7 @@
 // which are 16 bytes of the output, for all tokens of its block: addresses then
 // only step by the tokens' places, which the block looks up once, in shared memory.
 // U tokens' keys and values of a thread are under way at once.  (Pieces numbered
-// through, each with its own divisions and its own slot: 292 us in place of XX at
+// through, each with its own divisions and its own slot: 292 us in place of 152 at
 // 131072 tokens of 8 heads of 128 in 8 bits to bf16.)
 #include "../../include/lean_cache.h"
 #include "step_common.cuh"

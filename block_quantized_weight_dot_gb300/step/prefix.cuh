@@ -9,32 +9,47 @@
 //
 // The query heads that share a kv head, of all sequences that share a prefix, are
 // rows of one matrix: S = Q K^T and O = P V are products that the fifth-generation
-// tensor cores take, 128 rows by 128 keys at a time, and a prefix's keys and
-// values are read once for 256 rows.  Below about 290 rows HBM bounds the call,
-// above it the tensor cores do.
+// tensor cores take, 128 rows at a time, and a prefix's keys and values are read
+// once for 256 rows.  HBM would bound calls below about 290 rows a prefix, the
+// tensor cores those above it; what does is the softmax between the two products
+// (below).
 //
 //   - Work is a list of items: 256 (or 128) rows of a prefix and kv head, over tiles
 //     of 128 keys.  Every block takes an equal run of tiles, whatever the prefixes'
 //     lengths and numbers of sequences are, and leaves maxima, sums and outputs of
-//     its part of an item in the workspace; a last kernel adds up the parts and the
-//     sequence's own tokens.
-//   - A block has four loader warps (keys and values into swizzled tiles, two of each
-//     under way), one warp that issues matrix instructions, and two groups of 128
-//     threads, a thread to a row, that turn S into P.  The groups take turns: while one
-//     works on its scores the tensor cores have the other's products.  With two tiles
-//     of rows (NQ = 2) each group has its own 128 rows and all keys; with one, both
-//     have the same rows and every other tile of keys.
-//   - S and O lie in tensor memory; P replaces S there and is read as an operand
-//     from it.  O is summed over one tile only and then added in fp32 registers: the
-//     tensor cores cut off what is small next to their accumulator, and a new maximum
-//     needs no pass over O.
-//   - q is scaled by a power of two as in attend.cuh and split in QP parts of the
-//     operands' type, p in PP: one each for 16-bit activations (q is exact in one; p
-//     errs by half a step, 2^-8 of itself in bf16, as out itself is rounded), three
-//     and two for fp32.
+//     its part of an item in the workspace.  Sequences' own tokens are attended at
+//     the same time on SMs of their own, as many as their share of the work asks for
+//     (own_blocks(); one kernel after the other: 61 us in place of 47.8, 96 sequences
+//     on 32768 tokens, 16/2 heads of 128); a last kernel adds up the parts of both.
+//   - A block has two groups of 128 threads, a thread to a row, that turn S into P;
+//     four warps that issue matrix instructions; and four that bring keys and values
+//     into swizzled tiles, two of each under way.  With two tiles of rows (NQ = 2) each
+//     group has its own 128 rows and all keys; with one, both have the same rows and
+//     every other tile of keys.
+//   - S and O lie in tensor memory, S in buffers of 64 keys, as many as fit (three for
+//     heads of 64, two for heads of 128), so that products for the next keys run while a
+//     group works on these.  P replaces S and is read as an operand from there.
+//   - The reference of the exponentials only moves where a p would not fit its type:
+//     p is computed with the last one, the sums say whether it held, and no maximum is
+//     looked for (77.6 -> 72.3 us, 256 sequences on 16384 tokens, 32/4 heads of 64).
+//   - O is summed over 2048 keys in tensor memory, then added to the part in the
+//     workspace in fp32: the tensor cores cut off what is small next to their
+//     accumulator.  With p in three parts it is summed over 64 keys only and added in
+//     registers (those spill 340 bytes and more a thread in heads of 128).
+//   - q is copied where the operands' type holds it; else it is scaled by a power of
+//     two as in attend.cuh and split in three parts of that type, and p in three: fp32
+//     out, and f16 out of bf16 caches.  16-bit out has p in one part, which errs by
+//     half a step (2^-8 of itself in bf16, as out itself is rounded).
 //   - Caches in 8 bits become f16 on the way into shared memory (exact); scores are
-//     multiplied by the keys' scales, p by the values', relative to the tile's
-//     largest.
+//     multiplied by the keys' scales, p by the values', relative to the largest of 32.
+//
+// Measured (GB300, in a graph, floors by bytes or tensor operations in brackets): 96
+// sequences on 32768 tokens, 16/2 heads of 128, bf16, 47.7 us (13.5); 256 on 16384,
+// 32/4 heads of 64, f16, 72 (18.0); 240 on 12 prompts in 8 bits, 96 (8.5); four on
+// 2000, fp32 q, 20.5 (0.4).  What bounds them is a group's time for 64 keys: 1500-1700
+// cycles (8 bits: 2400) in which two warps a scheduler wait for tensor memory, 64
+// exponentials and their sum, one after the other; issue slots are 45% busy, no pipe
+// is above 30%.  About 5 us pass before the first scores, and 10 in the last kernel.
 #pragma once
 #include <cuda.h>
 
@@ -843,8 +858,9 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
         };
         if constexpr (IN8) {
             // Runs of rows as they lie in the cache, in the ring that the last four warps fill, become f16 (codes are
-            // exact in it) in the operands' tiles; tiles that are not whole come row by row through registers.  (Rows looked
-            // up and loaded by these threads: XX us, boxes issued between them: XX.)
+            // exact in it) in the operands' tiles; tiles that are not whole come row by row through registers.  (240
+            // sequences on 12 prompts 96 us; rows looked up and loaded by these threads 103, boxes issued between their
+            // conversions 126.)
             constexpr int PR = DP / 16, RUNS = S::kRuns, PIECES = S::kRawRows * PR / 128;  // 16-byte pieces: of a row, of a thread
             uint8_t *const raw = smem + S::kRawAt;
             auto convert = [&](uint8_t *tile, int row, int c, uint4 x) {  // piece c of a row
@@ -907,8 +923,7 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
             }
         } else {
             // Whole tiles in pages that the cache has: boxes of a page each, by the copy engine; a lane issues its own
-            // page's.  (By cp.async, 32 for each of 128 threads: XX us.)  Others, whose last rows have to be zeros: row by
-            // row.
+            // page's.  Others, whose last rows have to be zeros: row by row, with cp.async.
             constexpr int PR = DP / 8;  // 16-byte pieces of a row
             const int boxes = maps.box > 0 ? kTileKeys / maps.box : 0;
             auto copy_rows = [&](const void *from, const int64_t *off, uint8_t *tile, bool is_k) {
@@ -999,8 +1014,8 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
         regs_down<REGS.mma>();
         if (lane == 0) {
             // ---- matrix instructions: warps 12 and 13 issue the groups' scores, 14 and 15 their products.  (One thread
-            // needs about 110 cycles for an instruction that runs for 64: one warp for all of them 58 us where four
-            // take XX, 96 sequences on 32768 tokens.)
+            // needs about 110 cycles for an instruction that runs for 64: with one warp for all of them 240 sequences on 12
+            // prompts in 8 bits took 105 us, with four 91.)
             const int g = warp % 2;
             unsigned n = 0;
             bool ok = true;
@@ -1352,7 +1367,7 @@ lean_status launch_prefix(const PrefixMaps &maps, const PrefixArgs &p, int64_t f
     return step_launch(kern, std::min(step_sm_count(), kPrefixMaxCtas), prefix_threads(S::kIn8), S::kSmemAsked, flags, stream, maps, p);
 }
 // 16-bit activations whose q is exact in one part (f16 on bf16 caches is not): one part each, two tiles of rows where
-// prefixes have more than one; else three parts of q and two of p.
+// prefixes have more than one; else three parts of each.
 template <typename C, int DP>
 lean_status pick_prefix(const PrefixMaps &maps, const PrefixArgs &p, bool two, int64_t flags, void *stream) {
     const bool split = p.act == LEAN_F32 || (p.act == LEAN_F16 && std::is_same<C, __nv_bfloat16>::value);
