@@ -2,7 +2,7 @@
 with quantized linears, a paged key-value cache and greedy decoding, all on the
 GPU (no value comes back to the host between steps).
 
-    python examples/decode.py [--layers 32] [--tokens 32] [--sequences 2] [--graph]
+    python examples/decode.py [--layers 32] [--tokens 32] [--sequences 2] [--graph] [--cache-bits 8]
 
 Weights are random, in the shapes of SmolLM2-360M (hidden 960, 15 query and 5 kv
 heads of 64, FFN 2560); the linears are Q4_0, the embedding and lm_head Q8_0.
@@ -52,6 +52,7 @@ class Config:
     rope_base: float = 100000.0
     eps: float = 1e-5
     page_size: int = 16
+    cache_bits: int = 16      # 16: bf16; 8: whole numbers with a scale for each token and kv head
     top: int = 5
 
 
@@ -89,8 +90,12 @@ class Decoder:
         floats = lambda *s: torch.empty(s, device=dev)
         width = -(-max_tokens // page)
         pages = n * width
-        self.k_cache = torch.zeros((cfg.layers, pages, page, kv, hd), dtype=torch.bfloat16, device=dev)
+        cache = torch.int8 if cfg.cache_bits == 8 else torch.bfloat16
+        self.k_cache = torch.zeros((cfg.layers, pages, page, kv, hd), dtype=cache, device=dev)
         self.v_cache = torch.zeros_like(self.k_cache)
+        self.scales = [{} for _ in range(cfg.layers)]
+        if cfg.cache_bits == 8:
+            self.scales = [dict(k_scales=floats(pages, page, kv), v_scales=floats(pages, page, kv)) for _ in range(cfg.layers)]
         self.table, self.ring = ints(n, width), torch.arange(pages, dtype=torch.int32, device=dev)
         # two sets in turn: lean_kv_pages writes its results beside its inputs
         self.lens, self.ring_state = [ints(n), ints(n)], [torch.tensor([0, pages], dtype=torch.int32, device=dev), ints(2)]
@@ -128,9 +133,9 @@ class Decoder:
             for name, y in (("q", self.q), ("k", self.k), ("v", self.v)):
                 self.linear((i, name), self.x, y)
             lean.lean_rope_append(self.q, self.k, self.v, self.positions, self.slots, self.turns, self.q_rot,
-                                  self.k_cache[i], self.v_cache[i], rot_dim=cfg.head_dim)
+                                  self.k_cache[i], self.v_cache[i], rot_dim=cfg.head_dim, **self.scales[i])
             lean.lean_paged_attention(self.q_rot, self.k_cache[i], self.v_cache[i], self.table, lens, self.att,
-                                      scale=cfg.head_dim ** -0.5, workspace=self.att_ws)
+                                      scale=cfg.head_dim ** -0.5, workspace=self.att_ws, **self.scales[i])
             self.linear((i, "o"), self.att, self.block)
             lean.lean_residual_norm(self.block, self.h, norms[2 * i + 1], self.h, self.x, eps=cfg.eps)
             gate, up = self.w.packed[(i, "gate")], self.w.packed[(i, "up")]
@@ -150,8 +155,9 @@ def main():
     ap.add_argument("--tokens", type=int, default=32)
     ap.add_argument("--sequences", type=int, default=1)
     ap.add_argument("--graph", action="store_true", help="two steps recorded into a CUDA graph")
+    ap.add_argument("--cache-bits", type=int, choices=(8, 16), default=16)
     args = ap.parse_args()
-    cfg = Config(layers=args.layers)
+    cfg = Config(layers=args.layers, cache_bits=args.cache_bits)
     dec = Decoder(cfg, Weights(cfg), args.sequences, args.tokens + 8)
     dec.ids.copy_(torch.arange(args.sequences) + 1)
     out = []
