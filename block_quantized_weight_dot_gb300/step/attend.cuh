@@ -71,18 +71,19 @@ struct Shared {  // an item that begins in a block and goes on in others (-1: no
 // Prefixes that sequences share (prefix.cuh): prefix i's tokens, its sequences starts[i]..starts[i + 1] - 1, whose query
 // heads that share a kv head are rows, and its part of the list of items, `rows` rows by tiles of 128 keys.
 constexpr int kTileRows = 128, kTileKeys = 128;
-// Tiles of a block's time that an item costs beside its own (q, the first scores, the last outputs).
-constexpr int kItemTiles = 2;
+// Tiles of a block's time that an item costs beside its own (q, the first scores, the last outputs): 5 to 8 us, which are
+// about four of 16-bit caches (96 sequences on 32768 tokens: 44.6 us, counted as two 47.8) and two in 8 bits.
+__host__ __device__ constexpr int item_tiles(bool in8) { return in8 ? 2 : 4; }
 struct PrefixList {
     const int32_t *starts, *lens;
-    int n, n_seqs, group, hkv, rows, most;  // most: tokens that a prefix's pages can hold
+    int n, n_seqs, group, hkv, rows, most, item_tiles;  // most: tokens that a prefix's pages can hold
     unsigned sms, own_most;                 // SMs, and the most blocks that sequences' own tokens can take
     float unit_ns, tile_ns;                 // what a unit of those and a tile of a prefix take of an SM's time
 };
 struct Prefix {
     int first, count, len, keys, tiles;  // keys: tiles of keys; tiles: of rows, for a kv head
-    __device__ __forceinline__ unsigned cost(int hkv) const {  // (the call refuses lists that 32 bits do not count)
-        return (unsigned)hkv * tiles * (keys + (keys > 0 ? kItemTiles : 0));
+    __device__ __forceinline__ unsigned cost(const PrefixList &p) const {  // (the call refuses lists that 32 bits do not count)
+        return (unsigned)p.hkv * tiles * (keys + (keys > 0 ? p.item_tiles : 0));
     }
 };
 __device__ __forceinline__ Prefix open_prefix(const PrefixList &p, int i, unsigned *err) {
@@ -98,12 +99,15 @@ __device__ __forceinline__ Prefix open_prefix(const PrefixList &p, int i, unsign
     return x;
 }
 // The two kernels of one call run beside one another: of the SMs, as many as this for `units` units of sequences' own
-// tokens where the prefixes have `tiles` tiles, by their times; the SMs that no tile needs at least.  Both kernels come to
-// the same number.
+// tokens where the prefixes have `tiles` tiles, so that both end together; the SMs that no tile needs at least.  With a and
+// b for all of their units and tiles on one of s SMs, and d that an item's beginning costs every block of the second:
+// a / n = b / (s - n) + d.  (In proportion to a and b, one rate for every type: 48 us where this takes 44, 96 sequences on
+// 32768 tokens, 16/2 heads of 128.)  Where they came to different numbers blocks would only wait for SMs.
 __device__ __forceinline__ unsigned own_blocks(const PrefixList &p, unsigned units, unsigned tiles) {
     if (tiles == 0) return p.own_most;
-    const float a = (float)units * p.unit_ns, b = (float)tiles * p.tile_ns;
-    const unsigned n = (unsigned)__float2int_rn(p.sms * __fdiv_rn(a, a + b));
+    const float s = p.sms, a = (float)units * p.unit_ns, d = p.item_tiles * p.tile_ns;
+    const float c = d * s + a + (float)tiles * p.tile_ns;
+    const unsigned n = (unsigned)__float2int_rn(2.f * a * s / (c + sqrtf(fmaxf(0.f, c * c - 4.f * d * a * s))));
     return min(p.own_most, min(p.sms - 1, max(max(1u, n), p.sms > tiles ? p.sms - tiles : 1)));
 }
 
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(AttShape<C, DP, WIDE>::kWarps * 32, 1) attend_
     most = __reduce_max_sync(0xffffffffu, most);
     if (p.list.n > 0) {
         unsigned tiles = 0;
-        for (int i = threadIdx.x; i < p.list.n; i += T) tiles += open_prefix(p.list, i, p.err).cost(p.hkv);
+        for (int i = threadIdx.x; i < p.list.n; i += T) tiles += open_prefix(p.list, i, p.err).cost(p.list);
         tiles = __reduce_add_sync(0xffffffffu, tiles);
         if (lane == 0) tile_scan[warp] = tiles;
     }

@@ -76,6 +76,11 @@ bool prefix_sizes_ok(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim, int64
            n_seqs <= (INT32_MAX - 512) / (hq / hkv);
 }
 
+// ns of an SM for 16 of a sequence's own tokens (16-bit and fp32 activations, caches of 16 and 8 bits, heads of up to 64
+// and 128), and for a tile of keys (one tile of rows, two, one with q and p in parts), where an SM has many of them; GB300.
+constexpr float kUnitNs[2][2][2] = {{{90, 165}, {80, 145}}, {{100, 190}, {103, 187}}};
+constexpr float kTileNs[3][2][2] = {{{1050, 1250}, {1800, 3100}}, {{1250, 1700}, {2400, 3400}}, {{1950, 4100}, {2750, 5800}}};
+
 // The workspace's parts: that of attend.cuh, rows' first parts, sequences' own results, maxima and sums, outputs.
 struct PrefixRoom {
     int64_t first, own_out, own_lse, ml, o, bytes, parts;
@@ -139,7 +144,7 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     if ((a->table_width * a->page_size / kUnit + 2 + kAttItemUnits) * a->n_seqs * a->n_kv_heads * tiles > UINT32_MAX)
         return LEAN_ERR_SHAPE;  // attend.cuh counts units of sequences' own tokens in 32 bits
     // as prefix.cuh its items' tiles: a prefix's sequences fill at least all but one of its tiles of rows
-    const int64_t columns = (a->prefix_width * a->page_size / kTileKeys + 1 + kItemTiles) * a->n_kv_heads;
+    const int64_t columns = (a->prefix_width * a->page_size / kTileKeys + 1 + item_tiles(in8)) * a->n_kv_heads;
     if (columns > UINT32_MAX / (a->n_seqs * group / kTileRows + a->n_prefixes)) return LEAN_ERR_SHAPE;
     const PrefixRoom room = prefix_room(a->n_seqs, a->n_q_heads, a->n_kv_heads, a->head_dim);
     if (a->workspace_bytes < room.bytes) return LEAN_ERR_SHAPE;
@@ -237,11 +242,9 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     p.err = err;
 
     // Two tiles of rows where a prefix has more than one of them on average (below that the second would be empty).
-    const bool two = a->act_dtype != LEAN_F32 && !(a->act_dtype == LEAN_F16 && a->cache_dtype == LEAN_BF16) &&
-                     a->n_seqs * group > a->n_prefixes * kTileRows;
     const bool bf16 = a->cache_dtype == LEAN_BF16;
-    // Both kernels run beside one another.  A unit of 16 tokens moves its keys and values at about 40 GB/s of an SM's, a
-    // tile takes 0.9 us for each of its tiles of rows.
+    const bool two = !splits(p.act, bf16) && a->n_seqs * group > a->n_prefixes * kTileRows;
+    // Both kernels run beside one another: by the times of their parts (own_blocks()).
     PrefixList list = {};
     list.starts = a->seq_starts;
     list.lens = a->prefix_lens;
@@ -253,8 +256,10 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     list.most = (int)(a->prefix_width * a->page_size);
     list.sms = (unsigned)std::min(step_sm_count(), kPrefixMaxCtas);
     list.own_most = (unsigned)att_grid(own, att_warps(in8, prefix_dim(a->head_dim), group > 8));
-    list.unit_ns = (float)(kUnit * 2 * a->head_dim * (in8 ? 1 : 2)) / 40.f;
-    list.tile_ns = two ? 1800.f : 900.f;
+    list.item_tiles = item_tiles(in8);
+    const int wide = prefix_dim(a->head_dim) == 128;
+    list.unit_ns = kUnitNs[a->act_dtype == LEAN_F32][in8][wide];
+    list.tile_ns = kTileNs[splits(p.act, bf16) ? 2 : two][in8][wide];
     p.list = own.list = list;
     p.own_lens = a->seq_lens;
     p.own_most = (int)(a->table_width * a->page_size);

@@ -44,12 +44,12 @@
 //     multiplied by the keys' scales, p by the values', relative to the largest of 32.
 //
 // Measured (GB300, in a graph, floors by bytes or tensor operations in brackets): 96
-// sequences on 32768 tokens, 16/2 heads of 128, bf16, 47.7 us (13.5); 256 on 16384,
-// 32/4 heads of 64, f16, 72 (18.0); 240 on 12 prompts in 8 bits, 96 (8.5); four on
-// 2000, fp32 q, 20.5 (0.4).  What bounds them is a group's time for 64 keys: 1500-1700
+// sequences on 32768 tokens, 16/2 heads of 128, bf16, 44.0 us (13.5); 256 on 16384,
+// 32/4 heads of 64, f16, 71 (18.0); 240 on 12 prompts in 8 bits, 96 (8.5); four on
+// 2000, fp32 q, 20.9 (0.4).  What bounds them is a group's time for 64 keys: 1500-1700
 // cycles (8 bits: 2400) in which two warps a scheduler wait for tensor memory, 64
 // exponentials and their sum, one after the other; issue slots are 45% busy, no pipe
-// is above 30%.  About 5 us pass before the first scores, and 10 in the last kernel.
+// is above 30%.  About 6 us pass before the first scores, 5 to 7 in the last kernel.
 #pragma once
 #include <cuda.h>
 
@@ -169,12 +169,12 @@ struct Walk {
     // false: no more
     __device__ __forceinline__ bool next(const PrefixArgs &p) {
         while (left > 0) {
-            while (off >= x.cost(p.hkv)) {
-                off -= x.cost(p.hkv);
+            while (off >= x.cost(p.list)) {
+                off -= x.cost(p.list);
                 if (++i >= p.n_prefixes) return false;
                 x = open_prefix(p.list, i, p.err);
             }
-            const int each = x.keys + kItemTiles;
+            const int each = x.keys + p.list.item_tiles;
             const int item = (int)(off / each);
             from = (int)(off - (unsigned)item * each);
             const int take = (int)min(left, (unsigned)(each - from));
@@ -258,9 +258,12 @@ __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The compiler lays what is behind such a condition away from the code around it.
+__device__ __forceinline__ bool seldom(bool b) { return __builtin_expect(b, 0); }
+
 // Wait for a phase; false: it, or another wait of the block, ran out.
 __device__ __forceinline__ bool phase_wait(PrefixBars &b, uint64_t *bar, uint32_t parity, unsigned *err) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (!seldom(!mbar_try_wait(bar, parity))) return true;
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(bar, parity)) {
         if (*reinterpret_cast<volatile int *>(&b.dead)) return false;
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
     const int per = (p.n_prefixes + THREADS - 1) / THREADS;
     const int lo = min(p.n_prefixes, (int)threadIdx.x * per), hi = min(p.n_prefixes, lo + per);
     unsigned mine = 0;
-    for (int i = lo; i < hi; ++i) mine += open_prefix(p.list, i, p.err).cost(p.hkv);
+    for (int i = lo; i < hi; ++i) mine += open_prefix(p.list, i, p.err).cost(p.list);
     unsigned incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
         unsigned off = run_lo - begins;
         int i = lo;
         for (;; ++i) {
-            const unsigned c = open_prefix(p.list, i, p.err).cost(p.hkv);
+            const unsigned c = open_prefix(p.list, i, p.err).cost(p.list);
             if (off < c) break;
             off -= c;
         }
@@ -539,15 +542,16 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
             float shift[2], back[2];
             auto refer_scales = [&](const int *exps) {
                 // values' scales lie in 0.5..1 times 2^(exponent of the largest of 32 - 126); sums are relative to
-                // 2^(v_ref - 126); what is below 2^-60 of the largest may count as 2^-60 of it
+                // 2^(v_ref - 126); what is below 2^-60 of the largest may count as 2^-60 of it.  Larger ones than the
+                // reference's make larger p, whose sums say whether they fit.
                 const float up = kLog2Lift - (m == -CUDART_INF_F ? 0.f : m);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int below = min(v_ref - exps[c], 60);
                     shift[c] = up - (float)below;
-                    back[c] = __uint_as_float((uint32_t)(127 + max(below, 0)) << 23);
+                    back[c] = __uint_as_float((uint32_t)(127 + max(below, -60)) << 23);
                 }
-                return exps[0] <= v_ref && exps[1] <= v_ref;
+                return max(exps[0], exps[1]) <= v_ref + 60;
             };
             // New references for a half whose largest score is `top`, and what is multiplied with the sums and the outputs
             // so far.
@@ -635,7 +639,7 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
                             z[3] = __float_as_uint(b.y);
                         }
                     }
-                    if (limit < kHalfKeys) {
+                    if (seldom(limit < kHalfKeys)) {
 #pragma unroll
                         for (int i = 0; i < kHalfKeys; ++i)
                             if (i >= limit) x[i / 32][i % 32] = 0xff800000u;
@@ -668,13 +672,13 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
                     // With the references of the half before, as long as no p is too large for its type; in the first half,
                     // and where they have to move, the largest score is looked for and p is computed again.
                     bool moves = in_run == 0;
-                    if (!moves) {
+                    if (!seldom(moves)) {
                         if (IN8) moves = !refer_scales(exps);
                         exponentials();
                         moves = moves || !(fmaxf(sums[0], sums[1]) <= kMostSum);
                     }
                     float fall = 1.f;
-                    if (__any_sync(0xffffffffu, moves)) {
+                    if (seldom(__any_sync(0xffffffffu, moves))) {
                         float tops[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
                         for (int i = 0; i < kHalfKeys; ++i) tops[i % 4] = fmaxf(tops[i % 4], __uint_as_float(x[i / 32][i % 32]));
@@ -702,7 +706,7 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
                     l = fmaf(l, fall, IN8 ? sums[0] * back[0] + sums[1] * back[1] : sums[0] + sums[1]);
                     ++in_run;
                     advance_half();
-                    if (++in_sum == kFoldHalves || t >= w.to) {
+                    if (seldom(++in_sum == kFoldHalves || t >= w.to)) {
                         ok = products_wait();
                         if (!ok) break;
                         const float f = ex2(m_part - (m == -CUDART_INF_F ? 0.f : m)), up = size();
@@ -1043,13 +1047,15 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
                             tm_after();
                             const uint32_t d = tmem + S::scores(g, u % NB);
                             const uint32_t b = k_lower + (j % KS * S::kTileBytes + half * kHalfKeys * 128 >> 4);
+                            // (the smallest parts first: a sum is cut off relative to what it has come to)
 #pragma unroll
-                            for (int part = 0; part < QP; ++part)
+                            for (int part = QP - 1; part >= 0; --part)
 #pragma unroll
                                 for (int s = 0; s < DP / 16; ++s) {
                                     const uint32_t in = (s / 4 * S::kChunkBytes + s % 4 * 32) >> 4;
                                     if (s < steps)
-                                        tm_mma_ss(d, q_lower + (part * S::kTileBytes >> 4) + in, b + in, kTileUpper, idesc, part + s > 0);
+                                        tm_mma_ss(d, q_lower + (part * S::kTileBytes >> 4) + in, b + in, kTileUpper, idesc,
+                                                  part < QP - 1 || s > 0);
                                 }
                             tm_commit(&bars.s_full[g][u % NB]);
                         }
@@ -1085,11 +1091,11 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
                             const uint32_t b = v_lower + (j % VS * S::kTileBytes + half * kHalfKeys * 128 >> 4);
                             const bool add = PP == 1 && in_sum % kFoldHalves > 0;
 #pragma unroll
-                            for (int s = 0; s < kHalfKeys / 16; ++s)
+                            for (int part = PP - 1; part >= 0; --part)
 #pragma unroll
-                                for (int part = 0; part < PP; ++part)
+                                for (int s = 0; s < kHalfKeys / 16; ++s)
                                     tm_mma_ts(d, a + S::part(s / 2, part) + s % 2 * 8, b + s * (2048 >> 4), kTileUpper, idesc,
-                                              part + s > 0 || add);
+                                              part < PP - 1 || s > 0 || add);
                             tm_commit(&bars.o_full[of][u % NB]);
                             if (ALL && of) ++u1;
                             else ++u0;
@@ -1366,12 +1372,13 @@ lean_status launch_prefix(const PrefixMaps &maps, const PrefixArgs &p, int64_t f
     if (!step_ensure_smem(kern, S::kSmemAsked, done)) return LEAN_ERR_CUDA;
     return step_launch(kern, std::min(step_sm_count(), kPrefixMaxCtas), prefix_threads(S::kIn8), S::kSmemAsked, flags, stream, maps, p);
 }
+// Whether q and p are split in parts.
+inline bool splits(int act, bool bf16_cache) { return act == LEAN_F32 || (act == LEAN_F16 && bf16_cache); }
 // 16-bit activations whose q is exact in one part (f16 on bf16 caches is not): one part each, two tiles of rows where
 // prefixes have more than one; else three parts of each.
 template <typename C, int DP>
 lean_status pick_prefix(const PrefixMaps &maps, const PrefixArgs &p, bool two, int64_t flags, void *stream) {
-    const bool split = p.act == LEAN_F32 || (p.act == LEAN_F16 && std::is_same<C, __nv_bfloat16>::value);
-    if (split) return launch_prefix<C, DP, 3, 3, 1>(maps, p, flags, stream);
+    if (splits(p.act, std::is_same<C, __nv_bfloat16>::value)) return launch_prefix<C, DP, 3, 3, 1>(maps, p, flags, stream);
     return two ? launch_prefix<C, DP, 1, 1, 2>(maps, p, flags, stream) : launch_prefix<C, DP, 1, 1, 1>(maps, p, flags, stream);
 }
 
