@@ -4,9 +4,11 @@
 // so HBM bounds the call.  A thread has one piece of a token's row, V elements,
 // which are 16 bytes of the output, for all tokens of its block: addresses then
 // only step by the tokens' places, which the block looks up once, in shared memory.
-// U tokens' keys and values of a thread are under way at once.  (Pieces numbered
-// through, each with its own divisions and its own slot: 292 us in place of 152 at
-// 131072 tokens of 8 heads of 128 in 8 bits to bf16.)
+// What is under way at once comes from the number of threads, not from a thread's
+// own loads: with one token's key and value each, 131072 tokens of 8 heads of 128
+// in 8 bits to bf16 take 132 us (92% of a copy's rate), with two tokens' 142, four
+// 152, eight 175.  (Pieces numbered through, each with its own divisions and its own
+// slot: 292.)
 #include "../../include/lean_cache.h"
 #include "step_common.cuh"
 
@@ -59,7 +61,6 @@ struct alignas(V) Cached<int8_t, V> {  // c * s: 2^23 + (c + 128) has c + 128 in
 // C: of the cache, A: of the output.
 template <typename C, typename A, int V>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs p) {
-    constexpr int U = 4;
     constexpr bool IN8 = sizeof(C) == 1;
     __shared__ int64_t place[kReadTokens], scale_place[kReadTokens];  // -1: zeros, -2: NaN
     step_begin();
@@ -86,43 +87,32 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs p)
     for (int j = p.row <= kReadThreads ? (int)threadIdx.x - first * p.row : threadIdx.x; j < p.row; j += kReadThreads) {
         const int head = j / p.pieces, d = (j - head * p.pieces) * V;
         const int64_t in_row = head * p.cache_hs + d, in_scales = head * p.scale_hs;
-        for (int t1 = first; t1 < nt; t1 += U * sub) {
-            Cached<C, V> x[2][U];
-            float s[2][U];
+        for (int t = first; t < nt; t += sub) {
+            const int64_t at = place[t], at_scale = scale_place[t] + in_scales;
+            Cached<C, V> x[2];
+            float s[2];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int t = t1 + u * sub;
-                const int64_t at = t < nt ? place[t] : -1;
-                const int64_t at_scale = IN8 && t < nt ? scale_place[t] + in_scales : 0;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const C *cache = static_cast<const C *>(i ? p.v : p.k);
-                    x[i][u] = Cached<C, V>{};
-                    s[i][u] = at == -2 ? CUDART_NAN_F : 1.f;
-                    if (cache && at >= 0) {
-                        if (LEAN_SPAN(at + in_row, V, p.cache_end, p.err))
-                            x[i][u] = *reinterpret_cast<const Cached<C, V> *>(cache + at + in_row);
-                        if (IN8 && LEAN_IN(at_scale, p.scale_end, p.err)) s[i][u] = (i ? p.v_scales : p.k_scales)[at_scale];
-                    }
+            for (int i = 0; i < 2; ++i) {
+                const C *cache = static_cast<const C *>(i ? p.v : p.k);
+                x[i] = Cached<C, V>{};
+                s[i] = at == -2 ? CUDART_NAN_F : 1.f;
+                if (cache && at >= 0) {
+                    if (LEAN_SPAN(at + in_row, V, p.cache_end, p.err)) x[i] = *reinterpret_cast<const Cached<C, V> *>(cache + at + in_row);
+                    if (IN8 && LEAN_IN(at_scale, p.scale_end, p.err)) s[i] = (i ? p.v_scales : p.k_scales)[at_scale];
                 }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int t = t1 + u * sub;
-                if (t >= nt) break;
+            for (int i = 0; i < 2; ++i) {
+                A *out = static_cast<A *>(i ? p.v_out : p.k_out);
+                if (!out) continue;
+                float f[V];
+                x[i].values(s[i], f);
+                if (!IN8 && at == -2) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    A *out = static_cast<A *>(i ? p.v_out : p.k_out);
-                    if (!out) continue;
-                    float f[V];
-                    x[i][u].values(s[i][u], f);
-                    if (!IN8 && place[t] == -2) {
-#pragma unroll
-                        for (int e = 0; e < V; ++e) f[e] = CUDART_NAN_F;
-                    }
-                    const int64_t to = (t0 + t) * (i ? p.vos : p.kos) + head * (i ? p.vohs : p.kohs) + d;
-                    if (LEAN_SPAN(to, V, i ? p.v_end : p.k_end, p.err)) store_vec<A, V>(out + to, f);
+                    for (int e = 0; e < V; ++e) f[e] = CUDART_NAN_F;
                 }
+                const int64_t to = (t0 + t) * (i ? p.vos : p.kos) + head * (i ? p.vohs : p.kohs) + d;
+                if (LEAN_SPAN(to, V, i ? p.v_end : p.k_end, p.err)) store_vec<A, V>(out + to, f);
             }
         }
     }
@@ -132,9 +122,9 @@ template <typename C, typename A, int V>
 lean_status launch_read(ReadArgs p, int64_t flags, void *stream) {
     p.pieces = p.dim / V;
     p.row = p.hkv * p.pieces;
-    // eight tokens a thread, but no fewer blocks than two for an SM while there are tokens for them
+    // eight tokens a thread, but no fewer blocks than four for an SM while there are tokens for them
     int64_t tokens = 8 * std::max(1, kReadThreads / p.row);
-    tokens = std::min(tokens, std::max<int64_t>(1, p.n_tokens / (2 * step_sm_count())));
+    tokens = std::min(tokens, std::max<int64_t>(1, p.n_tokens / (4 * step_sm_count())));
     p.tokens = (int)std::min<int64_t>(tokens, kReadTokens);
     return step_launch(kv_read_kernel<C, A, V>, (p.n_tokens + p.tokens - 1) / p.tokens, kReadThreads, 0, flags, stream, p);
 }

@@ -377,7 +377,7 @@ __device__ __forceinline__ void store_codes(int8_t *to, const uint32_t *w) {
 // A head belongs to p.lanes neighbouring lanes, a power of two, which have it for all of the block's tokens: each has up
 // to 16 of its elements, in pieces of two runs as above, so that a row's largest element is found by shuffles alone, and
 // U tokens' loads are under way.  Blocks have heads of q or of k and v (KV), which take three times the instructions.
-// (16384 tokens, 16/2 heads of 128, read back included: 39 us; both in one block 49, rows of all heads numbered through,
+// (16384 tokens, 16/2 heads of 128, read back included: 37.5 us; both in one block 49, rows of all heads numbered through,
 // each with its own divisions, 45.)
 template <typename A, int V, bool INTER, bool KV>
 __device__ __forceinline__ void rope8_block(const RopeArgs &p, float2 *cs, int64_t *place, int64_t *scale_at, int tokens) {
