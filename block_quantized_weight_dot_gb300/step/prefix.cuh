@@ -44,9 +44,9 @@
 //     multiplied by the keys' scales, p by the values', relative to the largest of 32.
 //
 // Measured (GB300, in a graph, floors by bytes or tensor operations in brackets): 96
-// sequences on 32768 tokens, 16/2 heads of 128, bf16, 44.0 us (13.5); 256 on 16384,
-// 32/4 heads of 64, f16, 71 (18.0); 240 on 12 prompts in 8 bits, 96 (8.5); four on
-// 2000, fp32 q, 20.9 (0.4).  What bounds them is a group's time for 64 keys: 1500-1700
+// sequences on 32768 tokens, 16/2 heads of 128, bf16, 43.6 us (13.5); 256 on 16384,
+// 32/4 heads of 64, f16, 71 (18.0); 240 on 12 prompts in 8 bits, 94.5 (8.5); four on
+// 2000, fp32 q, 19.6 (0.4).  What bounds them is a group's time for 64 keys: 1500-1700
 // cycles (8 bits: 2400) in which two warps a scheduler wait for tensor memory, 64
 // exponentials and their sum, one after the other; issue slots are 45% busy, no pipe
 // is above 30%.  About 6 us pass before the first scores, 5 to 7 in the last kernel.
@@ -394,6 +394,8 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
     unsigned *const before = reinterpret_cast<unsigned *>(smem);  // (the tiles' room, unused yet)
     constexpr int THREADS = prefix_threads(IN8);
     constexpr PrefixRegs REGS = prefix_regs(IN8, PP);
+    auto own_len = [&](int i) { return i < p.n_seqs && LEAN_IN(i, p.n_seqs, p.err) ? p.own_lens[i] : 0; };
+    const int len_ahead = own_len(threadIdx.x);
     const int per = (p.n_prefixes + THREADS - 1) / THREADS;
     const int lo = min(p.n_prefixes, (int)threadIdx.x * per), hi = min(p.n_prefixes, lo + per);
     unsigned mine = 0;
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
     if (lane == 31) before[warp] = incl;
     unsigned own = 0;  // units of sequences' own tokens, as attend.cuh counts them
     for (int i = threadIdx.x; i < p.n_seqs; i += THREADS) {
-        const int len = min(LEAN_IN(i, p.n_seqs, p.err) ? max(p.own_lens[i], 0) : 0, p.own_most);
+        const int len = min(max(i == (int)threadIdx.x ? len_ahead : own_len(i), 0), p.own_most);
         own += (unsigned)(max(1, len / kUnit + (len % kUnit != 0)) + kAttItemUnits) * p.own_groups;
     }
     own = __reduce_add_sync(0xffffffffu, own);
@@ -1241,11 +1243,29 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
 template <int DP, int NQ>
 __global__ void __launch_bounds__(256) prefix_sum_kernel(const PrefixArgs p) {
     constexpr int V = DP / 32, ROWS = NQ * kTileRows, HALVES = NQ == 2 ? 1 : 2, U = 16;
-    step_begin();
+    // (What the call is given is there: this kernel begins after blocks of the one before, and that after all that came
+    // before the call.  Every thread waits before it ends, so that this kernel's end implies the end of the ones before.)
+    pdl_launch_dependents();
     const int lane = threadIdx.x % 32;
     const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    if (row >= (int64_t)p.n_seqs * p.hq) return;
+    if (row >= (int64_t)p.n_seqs * p.hq) {
+        pdl_wait();
+        return;
+    }
     const int seq = (int)(row / p.hq), head = (int)(row % p.hq);
+    // its prefix: the last that begins at it or before
+    int lo = 0, hi = p.n_prefixes;  // how many begin so: lo..hi
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const bool so = at < hi && LEAN_IN(at, p.n_prefixes + 1, p.err) && p.list.starts[at] <= seq;
+        const int n = __popc(__ballot_sync(0xffffffffu, so));
+        if (n == 0) break;
+        hi = min(hi, lo + n * step);
+        lo += (n - 1) * step + 1;
+    }
+    Prefix x = {};
+    if (lo > 0) x = open_prefix(p.list, lo - 1, p.err);
+    pdl_wait();
     // asked for at once: the row's own result, and where its parts lie if it has a prefix
     const float own = p.own_lse[row] * 1.4426950408889634f;
     Vec<float, V> own_out = {};
@@ -1257,20 +1277,9 @@ __global__ void __launch_bounds__(256) prefix_sum_kernel(const PrefixArgs p) {
         const int b = 32 * i + lane;
         shared[i] = b < p.own_grid && LEAN_IN(b, kAttMaxCtas, p.err) ? p.shared[b] : Shared{-1, 0};
     }
-    // its prefix: the last that begins at it or before
-    int lo = 0, hi = p.n_prefixes;  // how many begin so: lo..hi
-    while (lo < hi) {
-        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const bool so = at < hi && LEAN_IN(at, p.n_prefixes + 1, p.err) && p.list.starts[at] <= seq;
-        const int n = __popc(__ballot_sync(0xffffffffu, so));
-        if (n == 0) break;
-        hi = min(hi, lo + n * step);
-        lo += (n - 1) * step + 1;
-    }
     int parts = 0;
     int64_t more = 0;  // the first part that goes on
     if (lo > 0) {
-        const Prefix x = open_prefix(p.list, lo - 1, p.err);
         if (seq >= x.first && seq < x.first + x.count && x.keys > 0) {
             const int r = ((seq - x.first) * p.group + head % p.group) % ROWS;
             // (bounds: where seq_starts does not ascend, another prefix's block may have written it, or none)
