@@ -34,8 +34,8 @@ SOURCES = ["lean_qmatmul.cu", "pack.cpp", "qmm_q4_0.cu", "qmm_q8_0.cu", "qmm_i8_
            "qmm_fixed_ws.cu"]
 # the operators of a serving step around the product (include/lean_step.h)
 STEP = os.path.join(HERE, "step")
-STEP_SOURCES = ["norm.cu", "rope.cu", "kv_pages.cu", "kv_read.cu", "attend.cu", "attend8.cu", "prefix.cu", "prefix8.cu",
-                "logprobs.cu"]
+STEP_SOURCES = ["norm.cu", "rope.cu", "kv_pages.cu", "kv_read.cu", "attend.cu", "attend8.cu", "beside.cu", "beside8.cu",
+                "prefix.cu", "prefix8.cu", "logprobs.cu"]
 # host-only helpers (no CUDA), compiled by the host C++ compiler
 HOST = os.path.join(HERE, "host")
 HOST_SOURCES = ["quant.cpp", "rope_table.cpp"]

@@ -1,6 +1,7 @@
 // attend.cuh -- lean_paged_attention's kernels: attention of one new token per
 // sequence over the paged cache (attend.cu: caches of 16 bits and the call;
-// attend8.cu: caches in 8 bits; prefix.cu uses both for sequences' own tokens).
+// attend8.cu: caches in 8 bits; beside.cu and beside8.cu: sequences' own tokens in
+// lean_prefix_attention).
 //
 //   z_j = scale q . k_j,  p_j = e^(z_j - m),  m = max z_j,
 //   out = sum p_j v_j / sum p_j,  lse = m + ln sum p_j
@@ -122,9 +123,7 @@ struct AttArgs {
     int64_t qs, qhs, os, ohs, page_stride, place_stride, cache_hs, table_stride, n_pages;
     int n_seqs, hq, hkv, group, tiles, dim, page, paged, whole, width, window;
     int act, out_act;
-    // beside a kernel for prefixes (list.n > 0), whose blocks may begin only when what came before this one is done (they
-    // do not wait for it themselves): blocks as own_blocks() says, parts of shared items left to the kernel after both
-    PrefixList list;
+    PrefixList list;  // (beside a kernel for prefixes)
     float scale_log2;
     const float *k_scales, *v_scales;  // of caches in 8 bits
     int64_t scale_page, scale_place, scale_hs;
@@ -136,6 +135,9 @@ struct AttArgs {
 // The kernels for a cache type; flags and stream as the calls have them (attend.cu, attend8.cu).
 lean_status attend_cache16(const AttArgs &p, bool bf16, int64_t flags, void *stream);
 lean_status attend_cache8(const AttArgs &p, int64_t flags, void *stream);
+// The same beside a kernel for prefixes, heads of 128 at most (beside.cu, beside8.cu).
+lean_status attend_beside16(const AttArgs &p, bool bf16, int64_t flags, void *stream);
+lean_status attend_beside8(const AttArgs &p, int64_t flags, void *stream);
 // What lean_paged_attention refuses, and its workspace, by sizes alone.
 bool att_sizes_ok(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim);
 // The workspace's parts, of att_workspace_bytes() bytes.
@@ -427,7 +429,10 @@ __device__ __forceinline__ void store_result(const AttArgs &p, const Head &f, in
 }
 
 // WIDE: 9 to 16 query heads in a group, one per row; else up to 8, two rows each.
-template <typename C, int DP, int PARTS, bool WIDE>
+// BESIDE: beside a kernel for prefixes, whose blocks may begin only when what came before this one is done (they do not wait
+// for it themselves); blocks as own_blocks() says, parts of shared items left to the kernel after both.  (Asked for in
+// p.list instead, at run time, it cost lean_paged_attention in 8 bits 7%.)
+template <typename C, int DP, int PARTS, bool WIDE, bool BESIDE>
 __global__ void __launch_bounds__(AttShape<C, DP, WIDE>::kWarps * 32, 1) attend_kernel(const AttArgs p) {
     using P = typename Operand<C>::type;
     constexpr bool IN8 = AttShape<C, DP, WIDE>::kIn8;
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(AttShape<C, DP, WIDE>::kWarps * 32, 1) attend_
     __shared__ unsigned units_before[T];
     __shared__ Record rec[2 * W];
 
-    if (p.list.n > 0) {
+    if (BESIDE) {
         pdl_wait();
         pdl_launch_dependents();
     } else {
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(AttShape<C, DP, WIDE>::kWarps * 32, 1) attend_
         if (lane >= o) incl += u;
     }
     most = __reduce_max_sync(0xffffffffu, most);
-    if (p.list.n > 0) {
+    if (BESIDE) {
         unsigned tiles = 0;
         for (int i = threadIdx.x; i < p.list.n; i += T) tiles += open_prefix(p.list, i, p.err).cost(p.list);
         tiles = __reduce_add_sync(0xffffffffu, tiles);
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(AttShape<C, DP, WIDE>::kWarps * 32, 1) attend_
     // Equal runs for all blocks (a unit a warp at least) have to be joined across blocks; where there are few
     // items and none is long, a block for each is done sooner.
     unsigned grid = gridDim.x;
-    if (p.list.n > 0) {
+    if (BESIDE) {
         unsigned tiles = 0;
 #pragma unroll
         for (int i = 0; i < W; ++i) tiles += tile_scan[i];
@@ -1194,10 +1199,10 @@ inline int64_t att_grid(const AttArgs &p, int W) {
     return std::min<int64_t>(std::min(step_sm_count(), kAttMaxCtas), std::max<int64_t>(1, units / W));
 }
 
-template <typename C, int DP, int PARTS, bool WIDE>
+template <typename C, int DP, int PARTS, bool WIDE, bool BESIDE>
 lean_status launch_attend(const AttArgs &p, int64_t flags, void *stream) {
     static std::atomic<uint64_t> done{0};
-    auto kern = attend_kernel<C, DP, PARTS, WIDE>;
+    auto kern = attend_kernel<C, DP, PARTS, WIDE, BESIDE>;
     if (!step_ensure_smem(kern, att_smem<C, DP, WIDE>(), done)) return LEAN_ERR_CUDA;
     constexpr int W = AttShape<C, DP, WIDE>::kWarps;
     const int64_t grid = att_grid(p, W);
@@ -1205,22 +1210,23 @@ lean_status launch_attend(const AttArgs &p, int64_t flags, void *stream) {
     // (no item can be shared by blocks where each gets its own whatever the lengths are)
     const int64_t most = ((int64_t)p.width * p.page + 2 * kUnit - 1) / kUnit;
     const bool by_item = (int64_t)p.n_seqs * p.hkv * p.tiles <= grid && (most + W - 1) / W <= kJoinUnits;
-    if (st != LEAN_OK || grid == 1 || by_item || p.list.n > 0) return st;
-    constexpr int H = WIDE ? 16 : 8;
-    return step_launch(attend_sum_kernel<H, DP>, grid, kSumWarps * 32, 0, LEAN_FLAG_EARLY_WEIGHTS, stream, p, (int)grid);
+    if (st != LEAN_OK || grid == 1 || by_item) return st;
+    if constexpr (!BESIDE)
+        return step_launch(attend_sum_kernel<WIDE ? 16 : 8, DP>, grid, kSumWarps * 32, 0, LEAN_FLAG_EARLY_WEIGHTS, stream, p, (int)grid);
+    else return st;
 }
-template <typename C, int DP>
+template <typename C, int DP, bool BESIDE>
 lean_status pick_attend(const AttArgs &p, int64_t flags, void *stream) {
     const bool wide = p.group > 8;
     if (p.act == LEAN_F32)
-        return wide ? launch_attend<C, DP, 3, true>(p, flags, stream) : launch_attend<C, DP, 3, false>(p, flags, stream);
-    return wide ? launch_attend<C, DP, 2, true>(p, flags, stream) : launch_attend<C, DP, 2, false>(p, flags, stream);
+        return wide ? launch_attend<C, DP, 3, true, BESIDE>(p, flags, stream) : launch_attend<C, DP, 3, false, BESIDE>(p, flags, stream);
+    return wide ? launch_attend<C, DP, 2, true, BESIDE>(p, flags, stream) : launch_attend<C, DP, 2, false, BESIDE>(p, flags, stream);
 }
 template <typename C>
 lean_status pick_dim(const AttArgs &p, int64_t flags, void *stream) {
-    if (p.dim <= 64) return pick_attend<C, 64>(p, flags, stream);
-    if (p.dim <= 128) return pick_attend<C, 128>(p, flags, stream);
-    return pick_attend<C, 256>(p, flags, stream);
+    if (p.dim <= 64) return pick_attend<C, 64, false>(p, flags, stream);
+    if (p.dim <= 128) return pick_attend<C, 128, false>(p, flags, stream);
+    return pick_attend<C, 256, false>(p, flags, stream);
 }
 
 }  // namespace

@@ -271,7 +271,7 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     p.cta_parts = own.cta_parts;
     p.part_extent = own.part_extent;
     // Sequences' own tokens first: blocks of the prefixes' kernel begin beside theirs.
-    lean_status st = in8 ? attend_cache8(own, a->flags, stream) : attend_cache16(own, bf16, a->flags, stream);
+    lean_status st = in8 ? attend_beside8(own, a->flags, stream) : attend_beside16(own, bf16, a->flags, stream);
     if (st != LEAN_OK) return st;
     constexpr int64_t early = LEAN_FLAG_EARLY_WEIGHTS;
     st = in8 ? prefix_cache8(p, two, early, stream) : prefix_cache16(p, bf16, two, early, stream);
