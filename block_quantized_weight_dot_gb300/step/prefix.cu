@@ -114,7 +114,8 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
         return LEAN_ERR_FORMAT;
     if (!prefix_sizes_ok(a->n_seqs, a->n_q_heads, a->n_kv_heads, a->head_dim, a->n_prefixes) || a->n_pages <= 0 ||
         a->n_pages > INT32_MAX || a->page_size <= 0 || a->table_width <= 0 || a->table_width > INT32_MAX / a->page_size ||
-        a->table_stride < a->table_width || a->prefix_width <= 0 || a->prefix_width > INT32_MAX / a->page_size ||
+        a->table_stride < a->table_width || a->prefix_width <= 0 ||
+        a->prefix_width > (INT32_MAX - kTileKeys) / a->page_size ||  // (a tile's end is counted in 32 bits)
         a->prefix_stride < a->prefix_width)
         return LEAN_ERR_SHAPE;
     if (in8 && (a->head_dim % 16 || a->scale_page_stride < 0 || a->scale_place_stride < 0 || a->scale_head_stride < 0))

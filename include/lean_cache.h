@@ -74,7 +74,8 @@ lean_status lean_kv_read(const lean_kv_read_args *args, void *stream);
  * Calls that may run at the same time must not share one.  Results do not depend
  * on timing.
  * LEAN_ERR_SHAPE: as for lean_paged_attention, of both tables, with head_dim at
- * most 128 (LEAN_I8: a multiple of 16), n_prefixes <= 0 or above n_seqs, query
+ * most 128 (LEAN_I8: a multiple of 16), prefixes whose pages can hold more than
+ * 2^31 - 129 tokens, n_prefixes <= 0 or above n_seqs, query
  * heads and prefixes x tokens that a prefix's pages can hold / 2^14 near 2^32 or
  * above, or a workspace too small. */
 typedef struct {

@@ -39,8 +39,8 @@ extern "C" {
 
 /* Element types of activations, residuals and caches.  LEAN_I8: of caches only
  * (lean_rope_append, lean_paged_attention and the calls of lean_cache.h), whole
- * numbers c in -127..127 with one fp32 scale s for each token and kv head, which
- * stand for c * s.  The scales lie in two arrays beside the caches, at page *
+ * numbers c in -127..127 with one fp32 scale s, 0 or above, for each token and kv
+ * head, which stand for c * s.  The scales lie in two arrays beside the caches, at page *
  * scale_page_stride + place * scale_place_stride + kv head * scale_head_stride
  * (a head's places beside one another are read fastest: scale_place_stride 1).
  * Their fields end the structs and are read for such caches only. */
