@@ -582,7 +582,9 @@ lean_status launch_rope8(RopeArgs p, bool inter, int64_t flags, void *stream) {
     p.pieces = p.dim / (2 * V);
     p.rot_pieces = p.rot / (2 * V);
     p.lanes = 2;
-    while (p.lanes < p.pieces && p.lanes < 32) p.lanes *= 2;
+    // as few lanes as hold a row, 32 at most (512 elements): 16384 tokens of 16/2 fp32 heads of 128 51.6 us, by twice as
+    // many 60.2; 20480 of 16/2 bf16 heads of 80, 40 of them rotated in halves, 44.2 and 59.8
+    while (p.lanes * (8 / V) < p.pieces) p.lanes *= 2;
     // as launch_rope, by lanes; blocks of q and of k and v have the same threads
     const int64_t items = (int64_t)std::max(p.hq, 2 * p.hkv) * p.lanes;
     const int64_t sub = std::max<int64_t>(1, 256 / items);
