@@ -44,10 +44,10 @@
 //     multiplied by the keys' scales, p by the values', relative to the largest of 32.
 //
 // Measured (GB300, in a graph, floors by bytes or tensor operations in brackets): 96
-// sequences on 32768 tokens, 16/2 heads of 128, bf16, 43.6 us (13.5); 256 on 16384,
+// sequences on 32768 tokens, 16/2 heads of 128, bf16, 42.6 us (13.5); 256 on 16384,
 // 32/4 heads of 64, f16, 71 (18.0); 240 on 12 prompts in 8 bits, 94.5 (8.5); four on
-// 2000, fp32 q, 19.6 (0.4).  What bounds them is a group's time for 64 keys: 1500-1700
-// cycles (8 bits: 2400) in which two warps a scheduler wait for tensor memory, 64
+// 2000, fp32 q, 19.6 (0.4).  What bounds them is a group's time for 64 keys: 1300-1700
+// cycles (8 bits: 2200) in which two warps a scheduler wait for tensor memory, 64
 // exponentials and their sum, one after the other; issue slots are 45% busy, no pipe
 // is above 30%.  About 6 us pass before the first scores, 5 to 7 in the last kernel.
 #pragma once
