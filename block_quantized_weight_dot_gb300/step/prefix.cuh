@@ -44,9 +44,9 @@
 //     multiplied by the keys' scales, p by the values', relative to the largest of 32.
 //
 // Measured (GB300, in a graph, floors by bytes or tensor operations in brackets): 96
-// sequences on 32768 tokens, 16/2 heads of 128, bf16, 42.6 us (13.5); 256 on 16384,
-// 32/4 heads of 64, f16, 71 (18.0); 240 on 12 prompts in 8 bits, 94.5 (8.5); four on
-// 2000, fp32 q, 19.6 (0.4).  What bounds them is a group's time for 64 keys: 1300-1700
+// sequences on 32768 tokens, 16/2 heads of 128, bf16, 44 us (13.5); 256 on 16384,
+// 32/4 heads of 64, f16, 67 (18.0); 240 on 12 prompts in 8 bits, 91 (8.5); four on
+// 2000, fp32 q, 19.3 (0.4).  What bounds them is a group's time for 64 keys: 1300-1700
 // cycles (8 bits: 2200) in which two warps a scheduler wait for tensor memory, 64
 // exponentials and their sum, one after the other; issue slots are 45% busy, no pipe
 // is above 30%.  About 6 us pass before the first scores, 5 to 7 in the last kernel.
@@ -1242,7 +1242,9 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
 // Parts of a row, and the sequence's own tokens, added up: a warp to a row.
 template <int DP, int NQ>
 __global__ void __launch_bounds__(256) prefix_sum_kernel(const PrefixArgs p) {
-    constexpr int V = DP / 32, ROWS = NQ * kTileRows, HALVES = NQ == 2 ? 1 : 2, U = 16;
+    // U parts' loads under way in a warp: registers are what limits the warps of an SM (256 sequences on 16384 tokens, heads
+    // of 64: six 66.9 us, eight 68.0, 16 71.3, 32 77; 96 on 32768, heads of 128: eight 46.1, 12 43.8, 16 44.3, 20 49)
+    constexpr int V = DP / 32, ROWS = NQ * kTileRows, HALVES = NQ == 2 ? 1 : 2, U = DP == 64 ? 6 : 12;
     // (What the call is given is there: this kernel begins after blocks of the one before, and that after all that came
     // before the call.  Every thread waits before it ends, so that this kernel's end implies the end of the ones before.)
     pdl_launch_dependents();
