@@ -29,9 +29,10 @@
 //   - S and O lie in tensor memory, S in buffers of 64 keys, as many as fit (three for
 //     heads of 64, two for heads of 128), so that products for the next keys run while a
 //     group works on these.  P replaces S and is read as an operand from there.
-//   - The reference of the exponentials only moves where a p would not fit its type:
-//     p is computed with the last one, the sums say whether it held, and no maximum is
-//     looked for (77.6 -> 72.3 us, 256 sequences on 16384 tokens, 32/4 heads of 64).
+//   - The reference of the exponentials only moves where p would become too large (for
+//     f16, or on average above the 2^8 of attend.cuh): p is computed with the last one,
+//     the sums say whether it held, and no maximum is looked for (77.6 -> 72.3 us, 256
+//     sequences on 16384 tokens, 32/4 heads of 64).
 //   - O is summed over 2048 keys in tensor memory, then added to the part in the
 //     workspace in fp32: the tensor cores cut off what is small next to their
 //     accumulator.  With p in three parts it is summed over 64 keys only and added in
@@ -531,13 +532,15 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.q_full);
             }
-            // What p is multiplied with, as a power of two, and the sum of 32 of them up to which none is too large for its
-            // type.  bf16 has fp32's range; f16 ends at 2^-25 (half its smallest step) and 65504: in one part p is lifted so
-            // that 32 equal ones stay below that and references seldom move (what is lost of one is 2^-34 of the largest),
-            // in more as in attend.cuh.
+            // What p is multiplied with, as a power of two, and the sum of 32 of them up to which the references hold.  bf16
+            // has fp32's range, but so do the sums of p v: as far as attend.cuh lets scores rise (up to a sum of 2^40 values
+            // above 2^80 came out infinite where scores rose by 24 nats).  f16 ends at 2^-25 (half its smallest step) and
+            // 65504: in one part p is lifted so that 32 equal ones stay below that and references seldom move (what is lost
+            // of one is 2^-34 of the largest), in more as in attend.cuh.
             constexpr float kLog2Lift = BF16 ? 0.f : PP == 1 ? 9.f : 13.f;
             constexpr float kDown = BF16 ? 1.f : PP == 1 ? 1.f / 512 : 1.f / 8192;
-            constexpr float kMostSum = BF16 ? 1099511627776.f : 65504.f;
+            constexpr float kMostSum = BF16 ? 8192.f : 65504.f;
+            static_assert(!BF16 || kMostSum == 32 << (int)PartRange<T>::kSlack, "as attend.cuh's");
             float m = -CUDART_INF_F, l = 0.f;
             int v_ref = 1;
             // The references m and v_ref: what they make of exponents and sums of 32 keys each.
@@ -671,8 +674,8 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
                             tm_st16(s_at + S::part(c, 0), part);  // (over the scores, which are in registers)
                         }
                     };
-                    // With the references of the half before, as long as no p is too large for its type; in the first half,
-                    // and where they have to move, the largest score is looked for and p is computed again.
+                    // With the references of the half before, as long as no p is too large; in the first half, and where
+                    // they have to move, the largest score is looked for and p is computed again.
                     bool moves = in_run == 0;
                     if (!seldom(moves)) {
                         if (IN8) moves = !refer_scales(exps);

@@ -66,8 +66,8 @@ lean_status lean_kv_read(const lean_kv_read_args *args, void *stream);
  * (that of the cache; f16 for LEAN_I8), which errs by 2^-8 of sum p |v| at most
  * (bf16; f16 2^-11 and, for each key, 2^-34 of the largest p), and is summed in
  * fp32; fp32 out, and f16 out of a bf16 cache, takes q and p in three parts, which
- * leave nothing of fp32's precision behind.  Sequences' own tokens are as for
- * lean_paged_attention.
+ * leave nothing of fp32's precision behind.  Sequences' own tokens, and how large
+ * values may be, are as for lean_paged_attention.
  * q, out: 16-byte aligned, strides multiples of 8 elements; caches: 16-byte
  * aligned, strides multiples of 16 bytes.  workspace:
  * lean_prefix_attention_workspace_bytes() bytes, 256-byte aligned, any contents.
