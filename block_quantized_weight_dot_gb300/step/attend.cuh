@@ -977,15 +977,21 @@ __global__ void __launch_bounds__(AttShape<C, DP, WIDE>::kWarps * 32, 1) attend_
                     const float2 ml = unpack2(folded[(2 * KS * NH + h) * 32]);
                     const float f = ex2(ml.x - (m[h] == -CUDART_INF_F ? 0.f : m[h]));
                     l[h] = fmaf(ml.y, f, l[h]);
-                    const float g = IN8 ? f * __uint_as_float((uint32_t)(253 - v_ref) << 23) : f;
+                    const float g = IN8 ? f * PartRange<P>::kLift : f;
                     f2[h] = pack2(g, g);
                 }
+                const float v_up = __uint_as_float((uint32_t)(253 - v_ref) << 23);
 #pragma unroll
                 for (int j = 0; j < 2 * KS; ++j)
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) acc[j][h] = fma2(folded[(j * NH + h) * 32], f2[h], acc[j][h]);
+                    for (int h = 0; h < NH; ++h) {
+                        const f32x2 then = folded[(j * NH + h) * 32];
+                        acc[j][h] = fma2(IN8 ? mul2(then, pack2(v_up, v_up)) : then, f2[h], acc[j][h]);
+                    }
             };
+            // (8 bits: what is folded is in the values' own size, without the lift, by which scales of 1e30 would not fit)
             const float v_size = IN8 ? __uint_as_float((uint32_t)(v_ref + 1) << 23) : 1.f;
+            const float v_fold = v_size * (1.f / PartRange<P>::kLift);
             if (++done % kFold == 0 && can_fold) {
                 if (done > kFold) unfold();
 #pragma unroll
@@ -997,7 +1003,7 @@ __global__ void __launch_bounds__(AttShape<C, DP, WIDE>::kWarps * 32, 1) attend_
                 for (int j = 0; j < 2 * KS; ++j)
 #pragma unroll
                     for (int h = 0; h < NH; ++h) {
-                        folded[(j * NH + h) * 32] = IN8 ? mul2(acc[j][h], pack2(v_size, v_size)) : acc[j][h];
+                        folded[(j * NH + h) * 32] = IN8 ? mul2(acc[j][h], pack2(v_fold, v_fold)) : acc[j][h];
                         acc[j][h] = 0;
                     }
             }

@@ -242,7 +242,8 @@ lean_status lean_kv_pages(const lean_kv_pages_args *args, void *stream);
  * f16 cache each p errs by up to 2^-38 of the sequence's largest one as well, and
  * each element of q by 2^-38 of its head's largest (f16 has no smaller steps);
  * with a LEAN_I8 cache p times its token's v_scales is so held, to 2^-38 of the
- * largest p times the largest of the v_scales.
+ * largest p times the largest of the v_scales.  Sums of p v are held in fp32, with p
+ * up to 2^8: values above 2^120 / keys in size may give infinities.
  * q, out and the caches: 16-byte aligned, strides multiples of 8 elements
  * (LEAN_I8 caches: of 16, and head_dim as well).
  * workspace: lean_paged_attention_workspace_bytes() bytes, 256-byte aligned,
