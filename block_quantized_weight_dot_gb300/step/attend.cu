@@ -16,21 +16,25 @@ bool att_sizes_ok(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim) {
            dim <= kAttMaxDim && n_seqs <= INT32_MAX / hq;
 }
 
-// What blocks share, a part per warp and two per block, and what a warp folds, of the largest grid.
+// What blocks share; in floats, parts of warps and of blocks and what warps fold, of the largest grid.
 int64_t att_workspace_bytes(int64_t hq, int64_t hkv, int64_t dim) {
     const int h = att_heads(hq, hkv), d = att_dim(dim);
-    return kSharedBytes + (int64_t)kAttMaxCtas * 4 * ((kAttMaxWarps + 2) * part_floats(h, d) + kAttMaxWarps * fold_floats(h, d));
+    return kSharedBytes + (int64_t)kAttMaxCtas * 4 * ((kAttRoomWarps + 2) * part_floats(h, d) + kAttRoomWarps * fold_floats(h, d));
 }
-void att_workspace(AttArgs &p, void *workspace) {
-    const int h = p.group > 8 ? 16 : 8, d = att_dim(p.dim), part = part_floats(h, d);
+void att_workspace(AttArgs &p, void *workspace, bool in8) {
+    const int h = p.group > 8 ? 16 : 8, d = att_dim(p.dim), part = part_floats(h, d), warps = att_warps(in8, d, p.group > 8);
+    const int64_t floats = (att_workspace_bytes(p.hq, p.hkv, p.dim) - kSharedBytes) / 4;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.shared = reinterpret_cast<Shared *>(ws);
     p.warp_parts = reinterpret_cast<float *>(ws + kSharedBytes);
-    p.warp_extent = (int64_t)kAttMaxCtas * kAttMaxWarps * part;
+    // (blocks of more warps have their parts in shared memory, and the folds of 16 warps, heads of 64, that room as well:
+    // for 155 blocks, where GB300 has 152 SMs)
+    p.warp_extent = warps > kAttRoomWarps ? 0 : (int64_t)kAttMaxCtas * kAttRoomWarps * part;
     p.cta_parts = p.warp_parts + p.warp_extent;
     p.part_extent = (int64_t)kAttMaxCtas * 2 * part;
     p.folds = reinterpret_cast<f32x2 *>(p.cta_parts + p.part_extent);
-    p.fold_extent = (int64_t)kAttMaxCtas * kAttMaxWarps * fold_floats(h, d);
+    p.fold_extent = floats - p.warp_extent - p.part_extent;
+    p.most_ctas = (int)std::min<int64_t>(kAttMaxCtas, p.fold_extent / (warps * fold_floats(h, d)));
 }
 
 lean_status attend_cache16(const AttArgs &p, bool bf16, int64_t flags, void *stream) {
@@ -108,7 +112,7 @@ extern "C" lean_status lean_paged_attention(const lean_attention_args *a, void *
     p.width = (int)a->table_width;
     p.window = (int)std::min<int64_t>(a->window, INT32_MAX);
     p.act = p.out_act = (int)a->act_dtype;
-    att_workspace(p, a->workspace);
+    att_workspace(p, a->workspace, in8);
     if (in8) {
         p.k_scales = a->k_scales;
         p.v_scales = a->v_scales;

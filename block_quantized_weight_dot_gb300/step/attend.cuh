@@ -67,6 +67,7 @@ namespace lean {
 constexpr int kAttMaxDim = 256;
 constexpr int kAttMaxCtas = 160;  // of a launch: at most one per SM
 constexpr int kAttMaxWarps = 16;  // of a block
+constexpr int kAttRoomWarps = 8;  // of a block, that the workspace has parts for
 constexpr int kUnit = 16;         // tokens
 constexpr int kAttItemUnits = 4;  // empty units counted to an item (below)
 constexpr int64_t kSharedBytes = 2048;  // a Shared for each block
@@ -135,6 +136,7 @@ struct AttArgs {
     int64_t scale_page, scale_place, scale_hs;
     int64_t cache_extent, q_extent, out_extent;  // elements, for the checked build
     int64_t warp_extent, part_extent, fold_extent, scale_extent;
+    int most_ctas;  // blocks that the workspace has room for
     unsigned *err;
 };
 
@@ -146,9 +148,9 @@ lean_status attend_beside16(const AttArgs &p, bool bf16, int64_t flags, void *st
 lean_status attend_beside8(const AttArgs &p, int64_t flags, void *stream);
 // What lean_paged_attention refuses, and its workspace, by sizes alone.
 bool att_sizes_ok(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim);
-// The workspace's parts, of att_workspace_bytes() bytes.
+// The workspace's parts, of att_workspace_bytes() bytes, as the kernel for caches in 8 bits or in 16 has them.
 int64_t att_workspace_bytes(int64_t hq, int64_t hkv, int64_t dim);
-void att_workspace(AttArgs &p, void *workspace);
+void att_workspace(AttArgs &p, void *workspace, bool in8);
 
 }  // namespace lean
 
@@ -455,7 +457,8 @@ __global__ void __launch_bounds__(AttShape<C, DP, WIDE>::kWarps * 32, 1) attend_
     // registers for q as it was read: beside the accumulators, and all through the item before
     constexpr bool EARLY_Q = !WIDE && DP <= 128, AHEAD_Q = !WIDE && DP == 64;
     static_assert(PF * 4 <= S * STAGE, "a part fits a queue");
-    static_assert(W <= kAttMaxWarps, "the workspace has parts for as many");
+    static_assert(W <= kAttMaxWarps, "a lane for each record");
+    static_assert(PSMEM || W <= kAttRoomWarps, "the workspace has parts for as many");
     static_assert(AttShape<C, DP, WIDE>::kSmem <= kMaxSmem, "shared memory");
     constexpr int AT = 2;  // steps of the values whose products are under way at once (more spill)
     extern __shared__ uint8_t queue_raw[];
@@ -1210,7 +1213,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) attend_sum_kernel(const AttArg
 // counted by 16, 1.25 by eight.)
 inline int64_t att_grid(const AttArgs &p, int W) {
     const int64_t units = ((int64_t)p.width * p.page + 2 * kUnit) / kUnit * p.n_seqs * p.hkv * p.tiles;
-    return std::min<int64_t>(std::min(step_sm_count(), kAttMaxCtas), std::max<int64_t>(1, units / std::min(W, 8)));
+    return std::min<int64_t>(std::min(step_sm_count(), p.most_ctas), std::max<int64_t>(1, units / std::min(W, 8)));
 }
 
 template <typename C, int DP, int PARTS, bool WIDE, bool BESIDE>

@@ -188,7 +188,7 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     own.q_extent = (a->n_seqs - 1) * a->q_stride + (a->n_q_heads - 1) * a->q_head_stride + a->head_dim;
     own.out_extent = a->n_seqs * a->n_q_heads * a->head_dim;
     own.err = err;
-    att_workspace(own, ws);
+    att_workspace(own, ws, in8);
     if (in8) {
         own.k_scales = a->k_scales;
         own.v_scales = a->v_scales;
