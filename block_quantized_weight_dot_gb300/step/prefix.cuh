@@ -65,8 +65,8 @@ namespace lean {
 constexpr int kHalfKeys = 64;  // of a tile
 constexpr int kPrefixMaxCtas = 160;
 // Threads of a block (in 8 bits a fifth group of four warps issues copies), and the registers that each of
-// its groups of 128 has after the start: together what the block is launched with, 128 (in 8 bits 96) for each thread.
-// setmaxnreg waits forever for more than that.
+// its groups of 128 has after the start: together no more than the block is launched with, as many for each thread as the
+// compiler gave the kernel (128, in 8 bits 96).  setmaxnreg waits forever for more than that, so that a launch asks first.
 constexpr int prefix_threads(bool in8) { return in8 ? 640 : 512; }
 struct PrefixRegs {
     int rows, loaders, mma, issuer;
@@ -75,12 +75,25 @@ constexpr PrefixRegs prefix_regs(bool in8, int pp) {
     return in8 ? (pp == 1 ? PrefixRegs{136, 72, 80, 56} : PrefixRegs{160, 56, 56, 48})
                : (pp == 1 ? PrefixRegs{152, 120, 88, 0} : PrefixRegs{192, 72, 56, 0});
 }
-constexpr bool prefix_regs_fit(bool in8, int pp) {
+constexpr bool prefix_regs_fit(int of_thread, bool in8, int pp) {
     const PrefixRegs r = prefix_regs(in8, pp);
-    return 2 * r.rows + r.loaders + r.mma + r.issuer <= (in8 ? 96 * 5 : 128 * 4);
+    return (2 * r.rows + r.loaders + r.mma + r.issuer) * 128 <= of_thread * prefix_threads(in8);
 }
-static_assert(prefix_regs_fit(false, 1) && prefix_regs_fit(false, 3) && prefix_regs_fit(true, 1) && prefix_regs_fit(true, 3),
+static_assert(prefix_regs_fit(128, false, 1) && prefix_regs_fit(128, false, 3) && prefix_regs_fit(96, true, 1) &&
+                  prefix_regs_fit(96, true, 3),
               "registers of a block");
+// The kernel as it was built, asked once per device.
+template <typename Kern>
+inline bool prefix_regs_there(Kern kern, bool in8, int pp, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    const uint64_t bit = 1ull << dev;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    cudaFuncAttributes built;
+    if (cudaFuncGetAttributes(&built, kern) != cudaSuccess || !prefix_regs_fit(built.numRegs, in8, pp)) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 // Halves of tiles whose products are summed in tensor memory before they are added in fp32 (one part of p): what is below
 // 2^-24 of a sum is cut off when it is added, 16 keys at a time, so that a row errs by 2^-16 of its largest sum at most.
 constexpr int kFoldHalves = 32;
@@ -1379,11 +1392,11 @@ __global__ void __launch_bounds__(256) prefix_sum_kernel(const PrefixArgs p) {
 
 template <typename C, int DP, int QP, int PP, int NQ>
 lean_status launch_prefix(const PrefixMaps &maps, const PrefixArgs &p, int64_t flags, void *stream) {
-    static std::atomic<uint64_t> done{0};
+    static std::atomic<uint64_t> smem_done{0}, regs_done{0};
     using S = PrefixShape<C, DP, QP, PP, NQ>;
     static_assert(S::kSmemAsked <= 232448, "shared memory");
     auto kern = prefix_kernel<C, DP, QP, PP, NQ>;
-    if (!step_ensure_smem(kern, S::kSmemAsked, done)) return LEAN_ERR_CUDA;
+    if (!step_ensure_smem(kern, S::kSmemAsked, smem_done) || !prefix_regs_there(kern, S::kIn8, PP, regs_done)) return LEAN_ERR_CUDA;
     return step_launch(kern, std::min(step_sm_count(), kPrefixMaxCtas), prefix_threads(S::kIn8), S::kSmemAsked, flags, stream, maps, p);
 }
 // Whether q and p are split in parts.
