@@ -80,6 +80,11 @@ bool prefix_sizes_ok(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim, int64
 // and 128), and for a tile of keys (one tile of rows, two, one with q and p in parts), where an SM has many of them; GB300.
 constexpr float kUnitNs[2][2][2] = {{{90, 165}, {80, 145}}, {{100, 190}, {103, 187}}};
 constexpr float kTileNs[3][2][2] = {{{1050, 1250}, {1800, 3100}}, {{1250, 1700}, {2400, 3400}}, {{1950, 4100}, {2750, 5800}}};
+// Of a unit of more than eight query heads a kv head, two for each thread (96 sequences with up to 500 tokens on prefixes of
+// up to 16384, 12 heads a kv head, counted like the others and by this: 4 kv heads of 64 bf16 47.8 and 49.1 us, in 8 bits
+// 87.0 and 71.3, fp32 q 103 and 88; 2 of 128 47.2 and 37.8, 65.4 and 66.0, 116 and 94; prefixes of up to 2000 12 to 25%
+// less; by 2 about the same).
+constexpr float kWideUnit = 1.5f;
 
 // The workspace's parts: that of attend.cuh, rows' first parts, sequences' own results, maxima and sums, outputs.
 struct PrefixRoom {
@@ -259,7 +264,7 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     list.own_most = (unsigned)att_grid(own, att_warps(in8, prefix_dim(a->head_dim), group > 8));
     list.item_tiles = item_tiles(in8);
     const int wide = prefix_dim(a->head_dim) == 128;
-    list.unit_ns = kUnitNs[a->act_dtype == LEAN_F32][in8][wide];
+    list.unit_ns = kUnitNs[a->act_dtype == LEAN_F32][in8][wide] * (group > 8 ? kWideUnit : 1.f);
     list.tile_ns = kTileNs[splits(p.act, bf16) ? 2 : two][in8][wide];
     p.list = own.list = list;
     p.own_lens = a->seq_lens;
