@@ -78,6 +78,7 @@ bool prefix_sizes_ok(int64_t n_seqs, int64_t hq, int64_t hkv, int64_t dim, int64
 
 // ns of an SM for 16 of a sequence's own tokens (16-bit and fp32 activations, caches of 16 and 8 bits, heads of up to 64
 // and 128), and for a tile of keys (one tile of rows, two, one with q and p in parts), where an SM has many of them; GB300.
+// Measured with up to eight query heads a kv head.
 constexpr float kUnitNs[2][2][2] = {{{90, 165}, {80, 145}}, {{100, 190}, {103, 187}}};
 constexpr float kTileNs[3][2][2] = {{{1050, 1250}, {1800, 3100}}, {{1250, 1700}, {2400, 3400}}, {{1950, 4100}, {2750, 5800}}};
 // Of a unit of more than eight query heads a kv head, two for each thread (96 sequences with up to 500 tokens on prefixes of
@@ -247,7 +248,8 @@ extern "C" lean_status lean_prefix_attention(const lean_prefix_args *a, void *st
     p.out_extent = (a->n_seqs - 1) * a->out_stride + (a->n_q_heads - 1) * a->out_head_stride + a->head_dim;
     p.err = err;
 
-    // Two tiles of rows where a prefix has more than one of them on average (below that the second would be empty).
+    // Two tiles of rows where a prefix has more than one of them on average (below that the second would mostly be empty);
+    // from what the host knows, so that a large prefix among many small ones has single tiles as well.
     const bool bf16 = a->cache_dtype == LEAN_BF16;
     const bool two = !splits(p.act, bf16) && a->n_seqs * group > a->n_prefixes * kTileRows;
     // Both kernels run beside one another: by the times of their parts (own_blocks()).

@@ -10,7 +10,8 @@
 // The query heads that share a kv head, of all sequences that share a prefix, are
 // rows of one matrix: S = Q K^T and O = P V are products that the fifth-generation
 // tensor cores take, 128 rows at a time, and a prefix's keys and values are read
-// once for 256 rows.  HBM would bound calls below about 290 rows a prefix, the
+// once for 256 rows (128 where q and p are in three parts or prefixes have no more
+// than 128 rows on average).  HBM would bound calls below about 290 rows a prefix, the
 // tensor cores those above it; what does is the softmax between the two products
 // (below).
 //
@@ -36,7 +37,8 @@
 //   - O is summed over 2048 keys in tensor memory, then added to the part in the
 //     workspace in fp32: the tensor cores cut off what is small next to their
 //     accumulator.  With p in three parts it is summed over 64 keys only and added in
-//     registers (those spill 340 bytes and more a thread in heads of 128).
+//     registers (heads of 128 spill 180 bytes a thread in f16, 344 in bf16, 668 in 8
+//     bits, of 64 84 to 124; with one part of p all spill 32 to 92).
 //   - q is copied where the operands' type holds it; else it is scaled by a power of
 //     two as in attend.cuh and split in three parts of that type, and p in three: fp32
 //     out, and f16 out of bf16 caches.  16-bit out has p in one part, which errs by
@@ -47,10 +49,12 @@
 // Measured (GB300, in a graph, floors by bytes or tensor operations in brackets): 96
 // sequences on 32768 tokens, 16/2 heads of 128, bf16, 44 us (13.5); 256 on 16384,
 // 32/4 heads of 64, f16, 67 (18.0); 240 on 12 prompts in 8 bits, 91 (8.5); four on
-// 2000, fp32 q, 19.3 (0.4).  What bounds them is a group's time for 64 keys: 1300-1700
+// 2000, fp32 q, 19.3 (0.4).  What bounds heads of 64 is a group's time for 64 keys: 1300
 // cycles (8 bits: 2200) in which two warps a scheduler wait for tensor memory, 64
-// exponentials and their sum, one after the other; issue slots are 45% busy, no pipe
-// is above 30%.  About 6 us pass before the first scores, 5 to 7 in the last kernel.
+// exponentials and their sum, one after the other; issue slots are 45% busy (8 bits
+// 51%), the tensor pipe 28% (15%).  Heads of 128 (1700 cycles, 35%) wait for that pipe's
+// operands from shared memory as well.  About 6 us pass before the first scores, 5 to 7
+// in the last kernel.
 #pragma once
 #include <cuda.h>
 
@@ -881,8 +885,8 @@ __global__ void __launch_bounds__(prefix_threads(sizeof(C) == 1), 1) prefix_kern
         if constexpr (IN8) {
             // Runs of rows as they lie in the cache, in the ring that the last four warps fill, become f16 (codes are
             // exact in it) in the operands' tiles; tiles that are not whole come row by row through registers.  (240
-            // sequences on 12 prompts 96 us; rows looked up and loaded by these threads 103, boxes issued between their
-            // conversions 126.)
+            // sequences on 12 prompts 96 us, with the sum as it is now 91; rows looked up and loaded by these threads 103,
+            // boxes issued between their conversions 126.)
             constexpr int PR = DP / 16, RUNS = S::kRuns, PIECES = S::kRawRows * PR / 128;  // 16-byte pieces: of a row, of a thread
             uint8_t *const raw = smem + S::kRawAt;
             auto convert = [&](uint8_t *tile, int row, int c, uint4 x) {  // piece c of a row

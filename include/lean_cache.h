@@ -53,8 +53,10 @@ lean_status lean_kv_read(const lean_kv_read_args *args, void *stream);
  * of their own in the pages of row s of block_table (the new token's k and v
  * among them, or among the prefix's):
  *   out[s][h] = sum_j p_j v_j,  p = softmax_j(scale * q[s][h] . k_j)
- * over both.  A prefix's keys and values are read once for up to 256 rows (query
- * heads that share a kv head, of its sequences), not once for each sequence.
+ * over both.  A prefix's keys and values are read once for up to 128 rows (query
+ * heads that share a kv head, of its sequences), not once for each sequence; once
+ * for 256 where q and p are in one part (below) and the sequences' rows, shared out
+ * evenly, come to more than 128 a prefix.
  * Sequences before seq_starts[0] or from seq_starts[n_prefixes] on have no
  * prefix.  seq_starts ascends, from 0 on, to n_seqs at most; where it does not,
  * what comes out for the sequences concerned is unspecified (numbers outside
@@ -64,9 +66,11 @@ lean_status lean_kv_read(const lean_kv_read_args *args, void *stream);
  * lean_paged_attention, a prefix's like a sequence's.
  * Precision: of the prefix, 16-bit out takes p in one part of the operands' type
  * (that of the cache; f16 for LEAN_I8), which errs by 2^-8 of sum p |v| at most
- * (bf16; f16 2^-11 and, for each key, 2^-34 of the largest p), and is summed in
- * fp32; fp32 out, and f16 out of a bf16 cache, takes q and p in three parts, which
- * leave nothing of fp32's precision behind.  Sequences' own tokens, and how large
+ * (bf16; f16 2^-11 and, for each key, 2^-34 of the largest p, LEAN_I8: of the largest
+ * p times the largest of the v_scales), and is summed in fp32: less exact than
+ * lean_paged_attention over a joined table, which takes two.  fp32 out, and f16 out
+ * of a bf16 cache, takes q and p in three parts, which leave nothing of fp32's
+ * precision behind but what f16 operands do there.  Sequences' own tokens, and how large
  * values may be, are as for lean_paged_attention.
  * q, out: 16-byte aligned, strides multiples of 8 elements; caches: 16-byte
  * aligned, strides multiples of 16 bytes.  workspace:
